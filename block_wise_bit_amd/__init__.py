@@ -1,7 +1,7 @@
 """MI355X (gfx950) nested block-wise 4-bit dequantization.
 
-Thin Python binding of the C ABI in include/dq4.h (libdq4.so, built in-tree
-by block_wise_bit_amd/build.py).  The functions keep the C names; they only
+Thin Python binding of the C ABI in include/dq4.h and include/dq4_linear.h
+(libdq4.so, built in-tree by block_wise_bit_amd/build.py).  The functions keep the C names; they only
 check and marshal arguments -- every step of the dequantization runs in the
 HIP kernels of the library.  torch provides device memory and the current
 stream, nothing else.  There is no fallback: if the library is missing or
@@ -25,6 +25,14 @@ cannot be loaded, every call raises.
     dq4_out_prod_fused_workspace_bytes(n_rows, n_cols, m, src1_transposed=False) -> int
     dq4_dequant_linear(..., n_out, n_in, blocksize, x, op) -> tensor
                                                    (Y = X W^T or G W, FP16/BF16 GEMM)
+    dq4_linear_fused(..., n_out, n_in, blocksize, x, bias, residual, activation) -> tensor
+                                                   (act(x W^T + bias) + residual in one product)
+    dq4_linear_fused_backward(..., n_out, n_in, blocksize, dy, pre) -> (dx, dz, dbias)
+    dq4_gated_fused(gate, up, n_ff, n_in, blocksize, x, activation) -> tensor
+                                                   (act(x Wg^T) * (x Wu^T) in one product)
+    dq4_gated_fused_backward(gate, up, n_ff, n_in, blocksize, dh, gate_pre, up_pre)
+                                                   -> (dx, dgate, dup)
+    dq4_{linear,gated}_fused[_backward]_workspace_bytes(...) -> int
     dq4_int8_prep(A, CB, SCB, cols) -> (subA, subB)  (LLM.int8 correction operands)
     dq4_memory_twin_f16(packed, n) -> tensor       (diagnostic: the FP16 call's memory
                                                    traffic without its arithmetic)
@@ -39,15 +47,29 @@ from typing import List, Optional, Tuple
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 LIBRARY_PATH = os.path.join(PKG_DIR, "libdq4.so")
 HEADER_PATH = os.path.join(os.path.dirname(PKG_DIR), "include", "dq4.h")
+LINEAR_HEADER_PATH = os.path.join(os.path.dirname(PKG_DIR), "include", "dq4_linear.h")
 
 DQ4_OK, DQ4_EINVAL, DQ4_EUNSUPPORTED, DQ4_EHIP, DQ4_EBLAS, DQ4_ESCRATCH = 0, 1, 2, 3, 4, 5
 DQ4_NOALLOC_MAX_BLOCKS = 1 << 23   # outer blocks the no-allocation call's static scratch holds
 DQ4_F32, DQ4_F16, DQ4_BF16 = 0, 1, 2
 DQ4_LINEAR_FORWARD, DQ4_LINEAR_GRAD_A = 0, 1
+DQ4_ACT_NONE, DQ4_ACT_RELU, DQ4_ACT_SILU, DQ4_ACT_GELU, DQ4_ACT_GELU_TANH = 0, 1, 2, 3, 4
+ACTIVATIONS = {"none": DQ4_ACT_NONE, "relu": DQ4_ACT_RELU, "silu": DQ4_ACT_SILU,
+               "gelu": DQ4_ACT_GELU, "gelu_tanh": DQ4_ACT_GELU_TANH}
 NESTED_BLOCKSIZE = 256
 ROW_BLOCK_BUDGET_BYTES = 256 << 20   # 256 MiB of F32 per transient row block
 
 _lib = None
+
+
+class Dq4Weight(ctypes.Structure):
+    """dq4_weight_t of include/dq4_linear.h: a nested 4-bit weight's device
+    pointers, offset and block sizes."""
+
+    _fields_ = [("packed", ctypes.c_void_p), ("scale_codes", ctypes.c_void_p),
+                ("nested_absmax", ctypes.c_void_p), ("scale_codebook", ctypes.c_void_p),
+                ("codebook4", ctypes.c_void_p), ("offset", ctypes.c_float),
+                ("blocksize", ctypes.c_int32), ("nested_blocksize", ctypes.c_int32)]
 
 
 class Dq4Error(RuntimeError):
@@ -96,6 +118,25 @@ def library() -> ctypes.CDLL:
     lib.dq4_dequant_linear.restype = i32
     lib.dq4_int8_prep.argtypes = [P, i64, i64, P, P, i64, P, i64, P, P, P]
     lib.dq4_int8_prep.restype = i32
+    W = ctypes.POINTER(Dq4Weight)
+    lib.dq4_linear_fused.argtypes = [W, i64, i64, i32, i32, P, i64, i64, P, P, i64, P, i64, P, i64,
+                                     P, i64, P]
+    lib.dq4_linear_fused_backward.argtypes = [W, i64, i64, i32, i32, P, i64, i64, P, i64, P, i64,
+                                              P, i64, P, P, i64, P]
+    lib.dq4_gated_fused.argtypes = [W, W, i64, i64, i32, i32, P, i64, i64, P, i64, P, P, i64, P,
+                                    i64, P]
+    lib.dq4_gated_fused_backward.argtypes = [W, W, i64, i64, i32, i32, P, i64, i64, P, P, i64, P,
+                                             i64, P, P, i64, P, i64, P]
+    for name in ("dq4_linear_fused", "dq4_linear_fused_backward", "dq4_gated_fused",
+                 "dq4_gated_fused_backward"):
+        getattr(lib, name).restype = i32
+    lib.dq4_linear_fused_workspace_bytes.argtypes = [i64, i64, i64, P, i64, i32]
+    lib.dq4_linear_fused_backward_workspace_bytes.argtypes = [i64, i64, i64, P, i64, i32]
+    lib.dq4_gated_fused_workspace_bytes.argtypes = [i64, i64, i64, P, i64, i32]
+    lib.dq4_gated_fused_backward_workspace_bytes.argtypes = [i64, i64, i64, P, P, i64, i32]
+    for name in ("dq4_linear_fused", "dq4_linear_fused_backward", "dq4_gated_fused",
+                 "dq4_gated_fused_backward"):
+        getattr(lib, name + "_workspace_bytes").restype = i64
     lib.dq4_last_blas_status.argtypes = []
     lib.dq4_last_blas_status.restype = i32
     lib.dq4_status_string.argtypes = [i32]
@@ -530,6 +571,360 @@ def dq4_dequant_linear(packed, scale_codes, nested_absmax, scale_codebook, codeb
             y.data_ptr(), w_workspace.data_ptr(), _stream_handle(device, stream))
     _raise_for(st, "dq4_dequant_linear")
     return y
+
+
+# ----------------------------------------------------------------------------
+# fused products over nested 4-bit weights (include/dq4_linear.h)
+# ----------------------------------------------------------------------------
+def _half_code(dtype, what: str) -> int:
+    torch = _torch()
+    if dtype is torch.bfloat16:
+        return DQ4_BF16
+    if dtype is torch.float16:
+        return DQ4_F16
+    raise ValueError(f"{what} must be float16 or bfloat16, got {dtype}")
+
+
+def _weight_of(packed, scale_codes, nested_absmax, scale_codebook, codebook4, offset, n: int,
+               blocksize: int, nested_blocksize: int):
+    """(device, Dq4Weight) of a checked weight of n elements."""
+    device = _check_inputs(packed, scale_codes, nested_absmax, scale_codebook, codebook4, n,
+                           blocksize, nested_blocksize)
+    return device, Dq4Weight(packed.data_ptr(), scale_codes.data_ptr(), nested_absmax.data_ptr(),
+                             scale_codebook.data_ptr(), codebook4.data_ptr(), offset, blocksize,
+                             nested_blocksize)
+
+
+def _gated_weights(gate, up, n: int, blocksize: int, nested_blocksize: int):
+    """The two weights of a gated call, each a mapping with the keys packed,
+    scale_codes, nested_absmax, scale_codebook, codebook4 and offset."""
+    device, g = _weight_of(**gate, n=n, blocksize=blocksize, nested_blocksize=nested_blocksize)
+    other, u = _weight_of(**up, n=n, blocksize=blocksize, nested_blocksize=nested_blocksize)
+    if other != device:
+        raise ValueError(f"the up weight is on {other}, the gate weight on {device}")
+    return device, g, u
+
+
+def _sizes(*values):
+    values = tuple(int(v) for v in values)
+    if min(values) < 0:
+        raise ValueError("sizes must not be negative")
+    return values
+
+
+def _activation_code(activation: str, gated: bool) -> int:
+    code = ACTIVATIONS.get(activation)
+    if code is None or (gated and code == DQ4_ACT_NONE):
+        raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)[(1 if gated else 0):]}, "
+                         f"got {activation!r}")
+    return code
+
+
+def _matrix(t, name: str, m: int, width: int, dtype, device) -> int:
+    """The row stride of an (m, width) matrix with unit stride along its rows."""
+    if t.dtype != dtype or t.device != device or t.dim() != 2 or tuple(t.shape) != (m, width):
+        raise ValueError(f"{name} must be a ({m}, {width}) {dtype} tensor on {device}")
+    row, col = t.stride()
+    if col != 1 and width > 1:
+        raise ValueError(f"{name} must have unit stride along its last dimension")
+    if m <= 1:
+        return width
+    if row < width:
+        raise ValueError(f"{name}'s rows overlap (row stride {row} below {width})")
+    return row
+
+
+def _overlap(a, b) -> bool:
+    """Whether two strided matrices share memory.  Column ranges of one row
+    stride (the halves of an (m, 2 n) buffer) do not, though their rows
+    interleave."""
+    if a is None or b is None or a.numel() == 0 or b.numel() == 0:
+        return False
+    a0, b0 = a.data_ptr(), b.data_ptr()
+
+    def last(t):
+        return sum((n - 1) * s for n, s in zip(t.shape, t.stride())) * t.element_size()
+    if a0 > b0 + last(b) or b0 > a0 + last(a):
+        return False
+    if a.dim() == b.dim() == 2 and a.stride(0) == b.stride(0) and a.dtype == b.dtype:
+        ld = a.stride(0) * a.element_size()
+        apart = (b0 - a0) % ld if ld > 0 else 0
+        return not (apart >= a.size(1) * a.element_size()
+                    and apart + b.size(1) * b.element_size() <= ld)
+    return True
+
+
+def _refuse_overlap(outputs, inputs):
+    """No output may share memory with another output or with an input."""
+    for i, (name, t) in enumerate(outputs):
+        for other, u in outputs[i + 1:] + inputs:
+            if _overlap(t, u):
+                raise ValueError(f"{name} overlaps {other}")
+
+
+def _bytes_workspace(workspace, preferred: int, least: int, device, stream):
+    """(address, bytes) of the caller's workspace, or of one of the preferred
+    size; the tensor itself is returned to keep it alive over the call."""
+    torch = _torch()
+    if workspace is None:
+        workspace = _used_on(torch.empty(preferred, dtype=torch.uint8, device=device), stream)
+    elif workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    nbytes = workspace.numel() * workspace.element_size()
+    if nbytes < least:
+        raise ValueError(f"workspace holds {nbytes} bytes, needs {least}")
+    return workspace, workspace.data_ptr(), nbytes
+
+
+def _address(t):
+    return t.data_ptr() if t is not None and t.numel() else None
+
+
+def dq4_linear_fused_workspace_bytes(n_out: int, n_in: int, m: int, x=None, least: bool = False) -> int:
+    """Workspace bytes of dq4_linear_fused for this x (None: 16-byte aligned
+    dense rows): the preferred size, or the smallest the call accepts."""
+    ld = int(n_in) if x is None or x.size(0) <= 1 else x.stride(0)
+    return int(library().dq4_linear_fused_workspace_bytes(int(n_out), int(n_in), int(m), _address(x)
+                                                          if x is not None else None, ld,
+                                                          1 if least else 0))
+
+
+def dq4_gated_fused_workspace_bytes(n_ff: int, n_in: int, m: int, x=None, least: bool = False) -> int:
+    """As dq4_linear_fused_workspace_bytes, for dq4_gated_fused."""
+    ld = int(n_in) if x is None or x.size(0) <= 1 else x.stride(0)
+    return int(library().dq4_gated_fused_workspace_bytes(int(n_ff), int(n_in), int(m), _address(x)
+                                                         if x is not None else None, ld,
+                                                         1 if least else 0))
+
+
+def dq4_linear_fused_backward_workspace_bytes(n_out: int, n_in: int, m: int, dz=None,
+                                              least: bool = False) -> int:
+    """Workspace bytes of dq4_linear_fused_backward; dz: the matrix its product
+    reads (dy where there is no activation; None: 16-byte aligned dense rows)."""
+    ld = int(n_out) if dz is None or dz.size(0) <= 1 else dz.stride(0)
+    return int(library().dq4_linear_fused_backward_workspace_bytes(
+        int(n_out), int(n_in), int(m), _address(dz), ld, 1 if least else 0))
+
+
+def dq4_gated_fused_backward_workspace_bytes(n_ff: int, n_in: int, m: int, dgate=None, dup=None,
+                                             least: bool = False) -> int:
+    """Workspace bytes of dq4_gated_fused_backward; dgate, dup: the matrices its
+    product reads (None: 16-byte aligned dense rows)."""
+    ld = int(n_ff) if dgate is None or dgate.size(0) <= 1 else dgate.stride(0)
+    return int(library().dq4_gated_fused_backward_workspace_bytes(
+        int(n_ff), int(n_in), int(m), _address(dgate), _address(dup), ld, 1 if least else 0))
+
+
+def dq4_linear_fused(packed, scale_codes, nested_absmax, scale_codebook, codebook4,
+                     offset: float, n_out: int, n_in: int, blocksize: int, x, bias=None,
+                     residual=None, activation: str = "none", y=None, pre=None, workspace=None,
+                     nested_blocksize: int = NESTED_BLOCKSIZE, stream=None):
+    """y = act(x W^T + bias) + residual for the nested 4-bit weight W
+    (n_out x n_in), without a pass of its own for bias, activation or residual.
+
+    x: (m, n_in) float16 or bfloat16, unit stride along its rows; bias:
+    (n_out,), residual: (m, n_out), both of x's dtype.  activation: "none",
+    "relu", "silu", "gelu" (erf) or "gelu_tanh".  W enters as the values
+    dq4_nested_dequant writes for x's dtype; sums are FP32, y is rounded once.
+    pre, where given, receives the pre-activation x W^T + bias, which
+    dq4_linear_fused_backward takes.  y may be residual itself.  Returns y
+    (m, n_out), allocated when None, as is the workspace."""
+    torch = _torch()
+    n_out, n_in, blocksize = _sizes(n_out, n_in, blocksize)
+    code = _half_code(x.dtype, "x")
+    act = _activation_code(activation, False)
+    device, w = _weight_of(packed, scale_codes, nested_absmax, scale_codebook, codebook4, offset,
+                           n_out * n_in, blocksize, int(nested_blocksize))
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D")
+    m = x.size(0)
+    ld_x = _matrix(x, "x", m, n_in, x.dtype, device)
+    if bias is not None and (bias.dtype != x.dtype or bias.device != device
+                             or tuple(bias.shape) != (n_out,) or (n_out > 1 and bias.stride(0) != 1)):
+        raise ValueError(f"bias must be a contiguous ({n_out},) {x.dtype} tensor on {device}")
+    ld_residual = 0 if residual is None else _matrix(residual, "residual", m, n_out, x.dtype, device)
+    given = y is not None
+    if not given:
+        y = _used_on(torch.empty((m, n_out), dtype=x.dtype, device=device), stream)
+    ld_y = _matrix(y, "y", m, n_out, x.dtype, device)
+    ld_pre = 0 if pre is None else _matrix(pre, "pre", m, n_out, x.dtype, device)
+    if given or pre is not None:
+        in_place = residual is not None and residual.data_ptr() == y.data_ptr() and ld_residual == ld_y
+        _refuse_overlap([("y", y), ("pre", pre)],
+                        [("x", x), ("bias", bias), ("residual", None if in_place else residual)])
+    address = x.data_ptr()
+    lib = library()
+    size = lib.dq4_linear_fused_workspace_bytes
+    keep, ws, nbytes = _bytes_workspace(
+        workspace, size(n_out, n_in, m, address, ld_x, 0) if workspace is None else 0,
+        size(n_out, n_in, m, address, ld_x, 1), device, stream)
+    with torch.cuda.device(device):
+        st = lib.dq4_linear_fused(
+            ctypes.byref(w), n_out, n_in, code, act, address, m, ld_x, _address(bias),
+            _address(residual), ld_residual, y.data_ptr(), ld_y, _address(pre), ld_pre, ws, nbytes,
+            _stream_handle(device, stream))
+    _raise_for(st, "dq4_linear_fused")
+    return y
+
+
+def dq4_linear_fused_backward(packed, scale_codes, nested_absmax, scale_codebook, codebook4,
+                              offset: float, n_out: int, n_in: int, blocksize: int, dy, pre=None,
+                              activation: str = "none", bias_grad: bool = False, dx=None, dz=None,
+                              dbias=None, workspace=None,
+                              nested_blocksize: int = NESTED_BLOCKSIZE, stream=None):
+    """Gradients of dq4_linear_fused: (dx, dz, dbias).
+
+    dy: (m, n_out), the gradient of y (it is also residual's).  pre: what the
+    forward call saved (unused with activation "none").  dz = dy * act'(pre),
+    in dy's dtype, is the gradient of the pre-activation, which a low-rank
+    adapter takes; with activation "none" it is dy itself.  dx = dz W.  dbias,
+    with bias_grad or a tensor given: the FP32 column sums of the unrounded
+    dy * act'(pre), else None.  The weight is frozen: it has no gradient."""
+    torch = _torch()
+    n_out, n_in, blocksize = _sizes(n_out, n_in, blocksize)
+    code = _half_code(dy.dtype, "dy")
+    act = _activation_code(activation, False)
+    device, w = _weight_of(packed, scale_codes, nested_absmax, scale_codebook, codebook4, offset,
+                           n_out * n_in, blocksize, int(nested_blocksize))
+    if dy.dim() != 2:
+        raise ValueError("dy must be 2-D")
+    m = dy.size(0)
+    ld_dy = _matrix(dy, "dy", m, n_out, dy.dtype, device)
+    ld_pre = ld_dz = 0
+    given = [("dx", dx), ("dz", dz), ("dbias", dbias)]
+    if act == DQ4_ACT_NONE:
+        if dz is not None:
+            raise ValueError("dz is dy itself when there is no activation: do not give one")
+        pre = None
+    else:
+        if pre is None:
+            raise ValueError("an activation's gradient needs pre")
+        ld_pre = _matrix(pre, "pre", m, n_out, dy.dtype, device)
+        if dz is None:
+            dz = _used_on(torch.empty((m, n_out), dtype=dy.dtype, device=device), stream)
+        ld_dz = _matrix(dz, "dz", m, n_out, dy.dtype, device)
+    if dx is None:
+        dx = _used_on(torch.empty((m, n_in), dtype=dy.dtype, device=device), stream)
+    ld_dx = _matrix(dx, "dx", m, n_in, dy.dtype, device)
+    if dbias is None:
+        if bias_grad:
+            dbias = _used_on(torch.empty((n_out,), dtype=torch.float32, device=device), stream)
+    elif (dbias.dtype != torch.float32 or dbias.device != device or tuple(dbias.shape) != (n_out,)
+          or (n_out > 1 and dbias.stride(0) != 1)):
+        raise ValueError(f"dbias must be a contiguous ({n_out},) float32 tensor on {device}")
+    if any(t is not None for _, t in given):
+        _refuse_overlap([("dx", dx), ("dz", dz), ("dbias", dbias)], [("dy", dy), ("pre", pre)])
+    lhs, ld_lhs = (dy, ld_dy) if act == DQ4_ACT_NONE else (dz, ld_dz)
+    lib = library()
+    size = lib.dq4_linear_fused_backward_workspace_bytes
+    keep, ws, nbytes = _bytes_workspace(
+        workspace, size(n_out, n_in, m, lhs.data_ptr(), ld_lhs, 0) if workspace is None else 0,
+        size(n_out, n_in, m, lhs.data_ptr(), ld_lhs, 1), device, stream)
+    with torch.cuda.device(device):
+        st = lib.dq4_linear_fused_backward(
+            ctypes.byref(w), n_out, n_in, code, act, dy.data_ptr(), m, ld_dy, _address(pre), ld_pre,
+            dx.data_ptr(), ld_dx, _address(dz), ld_dz, _address(dbias), ws, nbytes,
+            _stream_handle(device, stream))
+    _raise_for(st, "dq4_linear_fused_backward")
+    return dx, dy if act == DQ4_ACT_NONE else dz, dbias
+
+
+def dq4_gated_fused(gate, up, n_ff: int, n_in: int, blocksize: int, x,
+                    activation: str = "silu", h=None, gate_pre=None, up_pre=None, workspace=None,
+                    nested_blocksize: int = NESTED_BLOCKSIZE, stream=None):
+    """h = act(x Wg^T) * (x Wu^T), the gated half of a feed-forward block, in
+    one product over both nested 4-bit weights (n_ff x n_in each).
+
+    gate, up: mappings with the keys packed, scale_codes, nested_absmax,
+    scale_codebook, codebook4 (to_device's) and offset.  x: (m, n_in) float16
+    or bfloat16.  gate_pre and up_pre, where given (both or neither, one row
+    stride), receive the two products for dq4_gated_fused_backward.  The down
+    projection is dq4_linear_fused(x=h, residual=...).  Returns h (m, n_ff)."""
+    torch = _torch()
+    n_ff, n_in, blocksize = _sizes(n_ff, n_in, blocksize)
+    code = _half_code(x.dtype, "x")
+    act = _activation_code(activation, True)
+    device, wg, wu = _gated_weights(gate, up, n_ff * n_in, blocksize, int(nested_blocksize))
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D")
+    m = x.size(0)
+    ld_x = _matrix(x, "x", m, n_in, x.dtype, device)
+    if (gate_pre is None) != (up_pre is None):
+        raise ValueError("give both gate_pre and up_pre, or neither")
+    given = h is not None
+    if not given:
+        h = _used_on(torch.empty((m, n_ff), dtype=x.dtype, device=device), stream)
+    ld_h = _matrix(h, "h", m, n_ff, x.dtype, device)
+    ld_pre = 0
+    if gate_pre is not None:
+        ld_pre = _matrix(gate_pre, "gate_pre", m, n_ff, x.dtype, device)
+        if _matrix(up_pre, "up_pre", m, n_ff, x.dtype, device) != ld_pre:
+            raise ValueError("gate_pre and up_pre must have one row stride")
+    if given or gate_pre is not None:
+        _refuse_overlap([("h", h), ("gate_pre", gate_pre), ("up_pre", up_pre)], [("x", x)])
+    address = x.data_ptr()
+    lib = library()
+    size = lib.dq4_gated_fused_workspace_bytes
+    keep, ws, nbytes = _bytes_workspace(
+        workspace, size(n_ff, n_in, m, address, ld_x, 0) if workspace is None else 0,
+        size(n_ff, n_in, m, address, ld_x, 1), device, stream)
+    with torch.cuda.device(device):
+        st = lib.dq4_gated_fused(
+            ctypes.byref(wg), ctypes.byref(wu), n_ff, n_in, code, act, address, m, ld_x,
+            h.data_ptr(), ld_h, _address(gate_pre), _address(up_pre), ld_pre, ws, nbytes,
+            _stream_handle(device, stream))
+    _raise_for(st, "dq4_gated_fused")
+    return h
+
+
+def dq4_gated_fused_backward(gate, up, n_ff: int, n_in: int, blocksize: int, dh, gate_pre, up_pre,
+                             activation: str = "silu", dx=None, dgate=None, dup=None,
+                             workspace=None, nested_blocksize: int = NESTED_BLOCKSIZE,
+                             stream=None):
+    """Gradients of dq4_gated_fused: (dx, dgate, dup), with dgate = dh * up_pre *
+    act'(gate_pre) and dup = dh * act(gate_pre) in dh's dtype (a low-rank
+    adapter takes them) and dx = dgate Wg + dup Wu, one FP32 sum rounded once.
+    gate_pre, up_pre: what the forward call saved; dgate and dup, where given,
+    have one row stride.  The weights are frozen: they have no gradient."""
+    torch = _torch()
+    n_ff, n_in, blocksize = _sizes(n_ff, n_in, blocksize)
+    code = _half_code(dh.dtype, "dh")
+    act = _activation_code(activation, True)
+    device, wg, wu = _gated_weights(gate, up, n_ff * n_in, blocksize, int(nested_blocksize))
+    if dh.dim() != 2:
+        raise ValueError("dh must be 2-D")
+    m = dh.size(0)
+    ld_dh = _matrix(dh, "dh", m, n_ff, dh.dtype, device)
+    ld_pre = _matrix(gate_pre, "gate_pre", m, n_ff, dh.dtype, device)
+    if _matrix(up_pre, "up_pre", m, n_ff, dh.dtype, device) != ld_pre:
+        raise ValueError("gate_pre and up_pre must have one row stride")
+    given = dx is not None or dgate is not None or dup is not None
+    if dx is None:
+        dx = _used_on(torch.empty((m, n_in), dtype=dh.dtype, device=device), stream)
+    ld_dx = _matrix(dx, "dx", m, n_in, dh.dtype, device)
+    if dgate is None:
+        dgate = _used_on(torch.empty((m, n_ff), dtype=dh.dtype, device=device), stream)
+    if dup is None:
+        dup = _used_on(torch.empty((m, n_ff), dtype=dh.dtype, device=device), stream)
+    ld_dpre = _matrix(dgate, "dgate", m, n_ff, dh.dtype, device)
+    if _matrix(dup, "dup", m, n_ff, dh.dtype, device) != ld_dpre:
+        raise ValueError("dgate and dup must have one row stride")
+    if given:
+        _refuse_overlap([("dx", dx), ("dgate", dgate), ("dup", dup)],
+                        [("dh", dh), ("gate_pre", gate_pre), ("up_pre", up_pre)])
+    lib = library()
+    size = lib.dq4_gated_fused_backward_workspace_bytes
+    keep, ws, nbytes = _bytes_workspace(
+        workspace,
+        size(n_ff, n_in, m, dgate.data_ptr(), dup.data_ptr(), ld_dpre, 0) if workspace is None else 0,
+        size(n_ff, n_in, m, dgate.data_ptr(), dup.data_ptr(), ld_dpre, 1), device, stream)
+    with torch.cuda.device(device):
+        st = lib.dq4_gated_fused_backward(
+            ctypes.byref(wg), ctypes.byref(wu), n_ff, n_in, code, act, dh.data_ptr(), m, ld_dh,
+            gate_pre.data_ptr(), up_pre.data_ptr(), ld_pre, dx.data_ptr(), ld_dx, dgate.data_ptr(),
+            dup.data_ptr(), ld_dpre, ws, nbytes, _stream_handle(device, stream))
+    _raise_for(st, "dq4_gated_fused_backward")
+    return dx, dgate, dup
 
 
 def dq4_int8_prep(A, CB, SCB, cols, subA=None, subB=None, stream=None, validate=False):

@@ -1,0 +1,1184 @@
+// dq4_linear_fused.hip -- products over nested 4-bit weights with a fused
+// epilogue: the linear layer (bias, activation, residual), the gated half of a
+// feed-forward block, and the backward passes (include/dq4_linear.h).
+//
+// Route for any size: the weight is decoded once into 16-bit operand fragments
+// of the matrix instruction in the workspace (weight_fragments_kernel), then
+// one matrix kernel (fragment_product_kernel) multiplies and finishes each
+// output in its epilogue.  The decode moves 2.5 bytes per weight element, the
+// product 2 m operations per element: the decode is small against the
+// product once m is in the hundreds.
+//
+// Fragment layout.  The output columns n (weight rows forward, weight columns
+// backward) are taken in groups of 128, the summed index k in chunks of 64.
+// One (group, chunk) is 16 KiB: [2 k-steps of 32][8 fragments f][64 lanes][8
+// k], so that a fragment is 1 KiB in lane order: it moves from HBM to LDS and
+// from LDS to registers in straight lines, without bank conflicts, whatever
+// the weight's own layout.  Row r of fragment f is output column 8 r + f of
+// the group: a lane, which holds D rows 4 g + i of every fragment, then holds
+// 8 neighbouring columns per i and writes 16 bytes at once.  The gated
+// forward puts 64 gate columns (fragments 0-3, column 4 r + f) beside the same
+// 64 up columns (fragments 4-7) in one group, so that act(g) * u is formed in
+// registers.  The gated backward lays the chunks of Wg and Wu one after the
+// other: one sum over both.  Columns and k beyond the matrix are zeros.
+
+#include <hip/hip_runtime.h>
+
+#include <stdint.h>
+
+#include "dq4.h"
+#include "dq4_device.h"
+#include "dq4_linear.h"
+#include "dq4_linear_device.h"
+
+#pragma clang fp contract(off)
+
+namespace dq4 {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kGroup = 128;                  // output columns per fragment group
+constexpr int kChunk = 64;                   // k per chunk
+constexpr int kFrags = 8;                    // fragments per group and k-step
+constexpr int kFragBytes = 1024;
+constexpr int kUnitBytes = 2 * kFrags * kFragBytes;  // one (group, chunk): 16 KiB
+constexpr int kXcds = 8;
+constexpr int64_t kMaxDim = int64_t{1} << 21;  // m, n_out, n_in: every grid and 32-bit offset below fits
+
+// How the fragments of a call are laid out from its weight or weights.
+enum Layout {
+    kSingle = 0,   // one weight
+    kSideBySide = 1,  // gated forward: 64 gate and 64 up columns per group
+    kStacked = 2   // gated backward: the k-chunks of Wg, then those of Wu
+};
+
+struct Weight {
+    const uint8_t *packed;
+    const uint8_t *scale_codes;
+    const float *nested_absmax;
+    const float *scale_codebook;
+    const float *codebook4;
+    float offset;
+};
+
+struct FragmentArgs {
+    Weight w[2];
+    uint16_t *out;
+    int64_t n_out, n_in;  // the weight's shape (both weights)
+    int32_t log2_block;
+    int32_t group0;       // first fragment group of this launch
+    int32_t groups;
+    int32_t chunks;       // per weight
+    int32_t layout;
+};
+
+// One weight's lookup tables in LDS.
+struct Tables {
+    float scb[256];
+    float cb4[16];
+};
+
+__device__ __forceinline__ void load_tables(const Weight &w, Tables &t)
+{
+    const int i = threadIdx.x;
+    if (i < 256)
+        t.scb[i] = w.scale_codebook[i];
+    if (i < 16)
+        t.cb4[i] = w.codebook4[i];
+}
+
+__device__ __forceinline__ float scale_of(const Weight &w, const Tables &t, int64_t block)
+{
+    return block_scale(t.scb[w.scale_codes[block]], w.nested_absmax[block >> kNestedLog2],
+                       w.offset);
+}
+
+// The FP32 product of element `e` of the flat weight, before its rounding to T.
+__device__ __forceinline__ float element_of(const Weight &w, const Tables &t, int log2_block,
+                                            int64_t e)
+{
+    const uint32_t byte = w.packed[e >> 1];
+    const uint32_t code = (e & 1) ? byte >> 4 : byte & 15u;
+    return t.cb4[code] * scale_of(w, t, e >> log2_block);
+}
+
+// Decode into fragments.  kForward: k runs along the weight's rows (n_in), a
+// 16-byte unit is 8 neighbouring elements of one row, one packed dword.
+// Backward: k runs down the weight's columns; a thread takes the dwords of 8
+// rows (8 columns each) and writes 8 units, each pairing the same column of
+// the 8 rows.  kAligned: rows start on packed dwords (n_in % 8 == 0, 4-byte
+// aligned codes); otherwise every element finds its own byte and block.
+// Bound by memory: 0.5 B read and 2 B written per element.
+template <int OUT, bool kForward, bool kAligned>
+__global__ __launch_bounds__(kThreads) void weight_fragments_kernel(FragmentArgs a)
+{
+    __shared__ Tables tables[2];
+    const int n_weights = a.layout == kSingle ? 1 : 2;
+    load_tables(a.w[0], tables[0]);
+    if (n_weights == 2)
+        load_tables(a.w[1], tables[1]);
+    __syncthreads();
+
+    const int tid = threadIdx.x;
+    const int lb = a.log2_block;
+    const int all_chunks = a.layout == kStacked ? 2 * a.chunks : a.chunks;
+    if constexpr (kForward) {
+        // a workgroup decodes 4 chunks (256 k, 128 packed bytes a row) of a group
+        const int spans = (all_chunks + 3) / 4;
+        const int group = blockIdx.x / spans;
+        const int span = blockIdx.x - group * spans;
+        uint16_t *base = a.out + static_cast<int64_t>(group) * all_chunks * (kUnitBytes / 2);
+        for (int it = 0; it < 16; ++it) {
+            const int u = it * kThreads + tid;  // unit within the 4 chunks
+            const int lane = u & 63, f = (u >> 6) & 7, ks = (u >> 9) & 1;
+            const int chunk = span * 4 + (u >> 10);
+            if (chunk >= all_chunks)
+                break;
+            const int r = lane & 15;
+            int which = 0;
+            int64_t o;
+            if (a.layout == kSideBySide) {
+                which = f >> 2;
+                o = static_cast<int64_t>(a.group0 + group) * 64 + 4 * r + (f & 3);
+            } else {
+                o = static_cast<int64_t>(a.group0 + group) * kGroup + 8 * r + f;
+            }
+            const int64_t k = static_cast<int64_t>(chunk) * kChunk + ks * 32 + (lane >> 4) * 8;
+            u32x4 q = {0, 0, 0, 0};
+            if (o < a.n_out && k < a.n_in) {
+                const Weight &w = a.w[which];
+                const Tables &t = tables[which];
+                const int64_t e0 = o * a.n_in + k;
+                float v[8];
+                if constexpr (kAligned) {
+                    const uint32_t word = *reinterpret_cast<const uint32_t *>(w.packed + (e0 >> 1));
+                    const float s = scale_of(w, t, e0 >> lb);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        v[j] = t.cb4[(word >> (4 * j)) & 15u] * s;
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        v[j] = k + j < a.n_in ? element_of(w, t, lb, e0 + j) : 0.0f;
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    q[j] = Half<OUT>::pack2(v[2 * j], v[2 * j + 1]);
+            }
+            *reinterpret_cast<u32x4 *>(base + static_cast<int64_t>(chunk) * (kUnitBytes / 2) +
+                                       (u & 1023) * 8) = q;
+        }
+    } else {
+        // a workgroup decodes one chunk (64 weight rows) of two groups
+        const int pair = blockIdx.x / all_chunks;
+        const int chunk = blockIdx.x - pair * all_chunks;
+        const int lane = tid & 63, ks = (tid >> 6) & 1, group = pair * 2 + (tid >> 7);
+        if (group >= a.groups)
+            return;
+        const int which = chunk >= a.chunks ? 1 : 0;
+        const Weight &w = a.w[which];
+        const Tables &t = tables[which];
+        const int64_t o0 = static_cast<int64_t>(chunk - which * a.chunks) * kChunk + ks * 32 +
+                           (lane >> 4) * 8;
+        const int64_t j0 = static_cast<int64_t>(a.group0 + group) * kGroup + 8 * (lane & 15);
+        u32x4 q[8];
+#pragma unroll
+        for (int f = 0; f < 8; ++f)
+            q[f] = u32x4{0, 0, 0, 0};
+        if (j0 < a.n_in) {
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {  // two weight rows at a time
+                float v[2][8];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int64_t o = o0 + 2 * p + h;
+                    const int64_t e0 = o * a.n_in + j0;
+                    if (o >= a.n_out) {
+#pragma unroll
+                        for (int f = 0; f < 8; ++f)
+                            v[h][f] = 0.0f;
+                    } else if constexpr (kAligned) {
+                        const uint32_t word =
+                            *reinterpret_cast<const uint32_t *>(w.packed + (e0 >> 1));
+                        const float s = scale_of(w, t, e0 >> lb);
+#pragma unroll
+                        for (int f = 0; f < 8; ++f)
+                            v[h][f] = t.cb4[(word >> (4 * f)) & 15u] * s;
+                    } else {
+#pragma unroll
+                        for (int f = 0; f < 8; ++f)
+                            v[h][f] = j0 + f < a.n_in ? element_of(w, t, lb, e0 + f) : 0.0f;
+                    }
+                }
+#pragma unroll
+                for (int f = 0; f < 8; ++f)
+                    q[f][p] = Half<OUT>::pack2(v[0][f], v[1][f]);
+            }
+        }
+        uint16_t *base = a.out + (static_cast<int64_t>(group) * all_chunks + chunk) * (kUnitBytes / 2) +
+                         ks * (kFrags * kFragBytes / 2) + lane * 8;
+#pragma unroll
+        for (int f = 0; f < 8; ++f)
+            *reinterpret_cast<u32x4 *>(base + f * (kFragBytes / 2)) = q[f];
+    }
+}
+
+// ---------------------------------------------------------------------------
+// the product
+// ---------------------------------------------------------------------------
+struct ProductArgs {
+    const uint16_t *wfrag;      // group-major fragments of this launch's groups
+    const uint16_t *x[2];       // the second is read by chunks [chunks, 2 chunks)
+    int64_t ld_x;
+    int64_t k;                  // readable columns of an x matrix, a multiple of 8
+    int64_t m, n;               // rows; output columns in all (gated: h's columns)
+    int64_t n0;                 // first output column of this launch
+    int32_t groups;             // of this launch
+    int32_t chunks;             // per x matrix
+    int32_t n_x;
+    int32_t act;
+    int32_t vec;                // outputs and residual take whole vectors
+    int32_t tiles_t;
+    const uint16_t *bias;
+    const uint16_t *residual;
+    int64_t ld_residual;
+    uint16_t *y;
+    int64_t ld_y;
+    uint16_t *pre[2];
+    int64_t ld_pre;
+};
+
+__device__ __forceinline__ uint32_t lds_offset(const void *p)
+{
+    return static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
+        (__attribute__((address_space(3))) const void *)p));
+}
+
+// 16 bytes per lane from a buffer straight to LDS at `lds` + 16 lane; a lane
+// whose offset is out of the buffer's range gets zeros.  In asm (there is no
+// destination register): the compiler would make every LDS read wait for
+// these loads, also where they fill the other half of the double buffer; the
+// kernel's own wait and barrier order them.  (m0 needs one wait state before
+// the load reads it; the compiler never keeps a value in it across statements.)
+__device__ __forceinline__ void buffer_to_lds(u32x4 rsrc, uint32_t voffset, uint32_t soffset,
+                                              uint32_t lds)
+{
+    __asm__ volatile("s_mov_b32 m0, %0\n\t"
+                     "s_nop 0\n\t"
+                     "buffer_load_dwordx4 %1, %2, %3 offen lds"
+                     :
+                     : "s"(lds), "v"(voffset), "s"(rsrc), "s"(soffset)
+                     : "memory");
+}
+
+__device__ __forceinline__ u32x4 make_rsrc(const void *base, uint32_t bytes)
+{
+    const uint64_t b = reinterpret_cast<uint64_t>(base);
+    u32x4 r;
+    r[0] = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(b));
+    r[1] = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(b >> 32) & 0xFFFFu);
+    r[2] = __builtin_amdgcn_readfirstlane(bytes);
+    r[3] = kRawBufferWord3;
+    return r;
+}
+
+__device__ __forceinline__ void wait_all_and_barrier()
+{
+    __asm__ volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    __asm__ volatile("" ::: "memory");
+}
+
+template <int OUT, int N>
+__device__ __forceinline__ void load_values(const uint16_t *p, bool vec, int valid, float (&v)[N])
+{
+    if (vec) {
+        if constexpr (N == 8) {
+            const u32x4 q = *reinterpret_cast<const u32x4 *>(p);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[j] = Half<OUT>::widen((q[j / 2] >> (16 * (j & 1))) & 0xFFFFu);
+        } else {
+            const u32x2 q = *reinterpret_cast<const u32x2 *>(p);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                v[j] = Half<OUT>::widen((q[j / 2] >> (16 * (j & 1))) & 0xFFFFu);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            v[j] = j < valid ? Half<OUT>::widen(p[j]) : 0.0f;
+    }
+}
+
+template <int OUT, int N>
+__device__ __forceinline__ void store_values(uint16_t *p, bool vec, int valid, const float (&v)[N])
+{
+    if (vec) {
+        uint32_t q[N / 2];
+#pragma unroll
+        for (int j = 0; j < N / 2; ++j)
+            q[j] = Half<OUT>::pack2(v[2 * j], v[2 * j + 1]);
+        if constexpr (N == 8)
+            *reinterpret_cast<u32x4 *>(p) = u32x4{q[0], q[1], q[2], q[3]};
+        else
+            *reinterpret_cast<u32x2 *>(p) = u32x2{q[0], q[1]};
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            if (j < valid)
+                p[j] = static_cast<uint16_t>(Half<OUT>::pack2(v[j], 0.0f));
+    }
+}
+
+// Outputs of one row: columns n0 .. n0 + 7 of a linear call.
+template <int OUT>
+__device__ __forceinline__ void finish_linear(const ProductArgs &a, int64_t row, int64_t n0,
+                                              float (&z)[8])
+{
+    const int64_t left = a.n - n0;
+    if (row >= a.m || left <= 0)
+        return;
+    const int valid = left < 8 ? static_cast<int>(left) : 8;
+    const bool vec = a.vec && valid == 8;
+    if (a.bias) {
+        float b[8];
+        load_values<OUT, 8>(a.bias + n0, vec, valid, b);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            z[j] = z[j] + b[j];
+    }
+    if (a.pre[0])
+        store_values<OUT, 8>(a.pre[0] + row * a.ld_pre + n0, vec, valid, z);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        z[j] = act_f32(a.act, z[j]);
+    if (a.residual) {
+        float r[8];
+        load_values<OUT, 8>(a.residual + row * a.ld_residual + n0, vec, valid, r);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            z[j] = z[j] + r[j];
+    }
+    store_values<OUT, 8>(a.y + row * a.ld_y + n0, vec, valid, z);
+}
+
+// Columns n0 .. n0 + 3 of a gated call.
+template <int OUT>
+__device__ __forceinline__ void finish_gated(const ProductArgs &a, int64_t row, int64_t n0,
+                                             float (&g)[4], float (&u)[4])
+{
+    const int64_t left = a.n - n0;
+    if (row >= a.m || left <= 0)
+        return;
+    const int valid = left < 4 ? static_cast<int>(left) : 4;
+    const bool vec = a.vec && valid == 4;
+    if (a.pre[0]) {
+        store_values<OUT, 4>(a.pre[0] + row * a.ld_pre + n0, vec, valid, g);
+        store_values<OUT, 4>(a.pre[1] + row * a.ld_pre + n0, vec, valid, u);
+    }
+    float h[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        h[j] = act_f32(a.act, g[j]) * u[j];
+    store_values<OUT, 4>(a.y + row * a.ld_y + n0, vec, valid, h);
+}
+
+constexpr int kFinishLd = kGroup + 4;  // floats per row of a wave's epilogue slab
+
+// The epilogue of one wave's 128 columns x 16 TF rows.  16 rows at a time pass
+// through a slab of LDS that only this wave uses: a lane holds 8 neighbouring
+// columns of one row per D register, so the slab takes and gives whole
+// vectors, and the code after it is there once instead of once per register.
+template <int OUT, bool kGated, int TF>
+__device__ __forceinline__ void finish_wave(const ProductArgs &a, const f32x4 (&acc)[kFrags][TF],
+                                            float *slab, int64_t row0, int group, int lane)
+{
+    const int g = lane >> 4, c = lane & 15;
+#pragma unroll
+    for (int t = 0; t < TF; ++t) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float *to = slab + c * kFinishLd + 8 * (4 * g + i);
+            *reinterpret_cast<f32x4 *>(to) =
+                f32x4{acc[0][t][i], acc[1][t][i], acc[2][t][i], acc[3][t][i]};
+            *reinterpret_cast<f32x4 *>(to + 4) =
+                f32x4{acc[4][t][i], acc[5][t][i], acc[6][t][i], acc[7][t][i]};
+        }
+        // the wave's LDS operations complete in order; the compiler must not
+        // move the reads of other lanes' values above the writes
+        __asm__ volatile("" ::: "memory");
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll 1
+        for (int it = 0; it < 4; ++it) {
+            const float *from = slab + (it * 4 + g) * kFinishLd + 8 * c;
+            const f32x4 lo = *reinterpret_cast<const f32x4 *>(from);
+            const f32x4 hi = *reinterpret_cast<const f32x4 *>(from + 4);
+            const int64_t row = row0 + t * 16 + it * 4 + g;
+            if constexpr (kGated) {
+                float gv[4] = {lo[0], lo[1], lo[2], lo[3]}, uv[4] = {hi[0], hi[1], hi[2], hi[3]};
+                finish_gated<OUT>(a, row, a.n0 + static_cast<int64_t>(group) * 64 + 4 * c, gv, uv);
+            } else {
+                float z[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+                finish_linear<OUT>(a, row, a.n0 + static_cast<int64_t>(group) * kGroup + 8 * c, z);
+            }
+        }
+        __asm__ volatile("" ::: "memory");
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
+// Tile of 128 WN output columns x 16 TF WT rows; wave (wn, wt) takes group wn
+// of the tile and 16 TF rows.  Both operands go from HBM to LDS without
+// passing registers, double-buffered by chunks of 64 k.
+template <int OUT, bool kGated, int WN, int WT, int TF>
+__global__ __launch_bounds__(64 * WN * WT) void fragment_product_kernel(ProductArgs a)
+{
+    constexpr int kRows = 16 * TF * WT;
+    constexpr int kWBytes = WN * kUnitBytes;
+    constexpr int kXBytes = kRows * kChunk * 2;
+    constexpr int kStage = kWBytes + kXBytes;
+    constexpr int kWaves = WN * WT;
+    constexpr int kWLoads = WN * 16 / kWaves;          // 1 KiB loads per wave and chunk
+    constexpr int kXLoads = 2 * TF * WT / kWaves;
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kStage];
+    static_assert(kWaves * 16 * kFinishLd * 4 <= 2 * kStage, "the epilogue slabs fit the stages");
+
+    const int tid = threadIdx.x;
+    const int lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wn = wave % WN, wt = wave / WN;
+
+    // consecutive workgroups go to the XCDs in turn: give each XCD a
+    // contiguous run of tiles, so that its L2 serves their shared operands
+    const int tiles = gridDim.x;
+    const int per = tiles / kXcds, extra = tiles % kXcds;
+    const int xcd = blockIdx.x % kXcds, idx = blockIdx.x / kXcds;
+    const int tile = xcd * per + (xcd < extra ? xcd : extra) + idx;
+    const int tile_n = tile / a.tiles_t, tile_t = tile - tile_n * a.tiles_t;
+    const int group0 = tile_n * WN;
+    const int64_t row0 = static_cast<int64_t>(tile_t) * kRows;
+
+    const int all_chunks = a.chunks * a.n_x;
+    // loads: W fragments are straight 1 KiB runs; group wl of the tile
+    u32x4 rs_w[WN];
+#pragma unroll
+    for (int q = 0; q < WN; ++q) {
+        const int group = group0 + q < a.groups ? group0 + q : a.groups - 1;
+        rs_w[q] = make_rsrc(reinterpret_cast<const uint8_t *>(a.wfrag) +
+                                static_cast<int64_t>(group) * all_chunks * kUnitBytes,
+                            static_cast<uint32_t>(all_chunks) * kUnitBytes);
+    }
+    // x: 16 rows x 32 k per load; rows past the end lie past the buffer
+    const int64_t rows_left = a.m - row0;
+    const int64_t rows_here = rows_left < kRows ? rows_left : kRows;
+    const uint32_t x_bytes = static_cast<uint32_t>(((rows_here - 1) * a.ld_x + a.k) * 2);
+    u32x4 rs_x[2];
+    rs_x[0] = make_rsrc(a.x[0] + row0 * a.ld_x, x_bytes);
+    rs_x[1] = make_rsrc(a.x[a.n_x - 1] + row0 * a.ld_x, x_bytes);
+    uint32_t x_off[kXLoads], x_lds[kXLoads];
+    int32_t x_k[kXLoads];
+#pragma unroll
+    for (int q = 0; q < kXLoads; ++q) {
+        const int fr = wave * kXLoads + q;  // fragment: k-step fr & 1 of row block fr >> 1
+        const int row = (fr >> 1) * 16 + (lane & 15);
+        x_k[q] = (fr & 1) * 32 + (lane >> 4) * 8;
+        // a single row's stride is not looked at: rows past the end get an
+        // offset past any buffer
+        x_off[q] = row < rows_here
+                       ? static_cast<uint32_t>(row * static_cast<int32_t>(a.ld_x) + x_k[q]) * 2u
+                       : 0x80000000u;
+        x_lds[q] = kWBytes + fr * kFragBytes;
+    }
+    const uint32_t lds0 = lds_offset(lds);
+    const uint32_t w_voff = lane * 16;
+
+    auto issue = [&](int c, int buf) {
+        const uint32_t to = lds0 + buf * kStage;
+#pragma unroll
+        for (int q = 0; q < kWLoads; ++q) {
+            const int fr = wave * kWLoads + q;  // of WN * 16
+            buffer_to_lds(rs_w[fr / 16], w_voff,
+                          static_cast<uint32_t>(c) * kUnitBytes + (fr % 16) * kFragBytes,
+                          to + fr * kFragBytes);
+        }
+        const int second = c >= a.chunks ? 1 : 0;
+        const int ck = c - second * a.chunks;
+        const u32x4 rs = second ? rs_x[1] : rs_x[0];
+        const int32_t k_left = static_cast<int32_t>(a.k - static_cast<int64_t>(ck) * kChunk);
+#pragma unroll
+        for (int q = 0; q < kXLoads; ++q) {
+            const uint32_t off = x_off[q] + static_cast<uint32_t>(ck) * (kChunk * 2);
+            buffer_to_lds(rs, x_k[q] < k_left ? off : 0x80000000u, 0, to + x_lds[q]);
+        }
+    };
+
+    f32x4 acc[kFrags][TF];
+#pragma unroll
+    for (int f = 0; f < kFrags; ++f)
+#pragma unroll
+        for (int t = 0; t < TF; ++t)
+            acc[f][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+    if (all_chunks > 0) {
+        issue(0, 0);
+        wait_all_and_barrier();
+    }
+    for (int c = 0; c < all_chunks; ++c) {
+        const int buf = c & 1;
+        if (c + 1 < all_chunks)
+            issue(c + 1, buf ^ 1);
+        const uint8_t *w_lds = lds + buf * kStage + wn * kUnitBytes + lane * 16;
+        const uint8_t *x_l = lds + buf * kStage + kWBytes + wt * (TF * 2 * kFragBytes) + lane * 16;
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+            u32x4 wf[kFrags], xf[TF];
+#pragma unroll
+            for (int t = 0; t < TF; ++t)
+                xf[t] = *reinterpret_cast<const u32x4 *>(x_l + (2 * t + ks) * kFragBytes);
+#pragma unroll
+            for (int f = 0; f < kFrags; ++f)
+                wf[f] = *reinterpret_cast<const u32x4 *>(w_lds + (ks * kFrags + f) * kFragBytes);
+#pragma unroll
+            for (int f = 0; f < kFrags; ++f)
+#pragma unroll
+                for (int t = 0; t < TF; ++t)
+                    acc[f][t] = Half<OUT>::mfma(wf[f], xf[t], acc[f][t]);
+        }
+        wait_all_and_barrier();
+    }
+
+    if (group0 + wn >= a.groups)
+        return;
+    finish_wave<OUT, kGated, TF>(a, acc, reinterpret_cast<float *>(lds) + wave * (16 * kFinishLd),
+                                 row0 + wt * (TF * 16), group0 + wn, lane);
+}
+
+// ---------------------------------------------------------------------------
+// rows copied into a padded matrix, and the backward elementwise pass
+// ---------------------------------------------------------------------------
+// x rows (any alignment and stride) into rows of ld_out elements, zeros from
+// column k on: the form the product reads in 16-byte pieces.
+__global__ __launch_bounds__(kThreads) void rows_zero_fill_copy(const uint16_t *x, int64_t ld_x,
+                                                                int64_t m, int64_t k,
+                                                                uint16_t *out, int64_t ld_out)
+{
+    const int64_t c = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+    if (c >= ld_out)
+        return;
+    for (int64_t r = blockIdx.y; r < m; r += gridDim.y)
+        out[r * ld_out + c] = c < k ? x[r * ld_x + c] : static_cast<uint16_t>(0);
+}
+
+struct SlopeArgs {
+    const uint16_t *dy;
+    int64_t ld_dy;
+    const uint16_t *pre[2];     // z, or g and u
+    int64_t ld_pre;
+    uint16_t *dz[2];
+    int64_t ld_dz;
+    uint16_t *pad[2];           // padded copies for the product, or null
+    int64_t ld_pad;
+    float *partial;             // column sums, one row per row block, or null
+    int64_t m, n;
+    int32_t act;
+    int32_t rows_per_block;
+};
+
+// dz = T(dy act'(pre)), or dgate and dup; one thread per column, a block of
+// rows each, so that the column sums of the unrounded products (the bias
+// gradient) come from a fixed order of FP32 additions.
+template <int OUT, bool kGated>
+__global__ __launch_bounds__(kThreads) void activation_slope_kernel(SlopeArgs a)
+{
+    const int64_t c = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+    const int64_t width = a.pad[0] ? a.ld_pad : a.n;
+    if (c >= width)
+        return;
+    const int64_t r0 = static_cast<int64_t>(blockIdx.y) * a.rows_per_block;
+    const int64_t r1 = r0 + a.rows_per_block < a.m ? r0 + a.rows_per_block : a.m;
+    float sum = 0.0f;
+    for (int64_t r = r0; r < r1; ++r) {
+        uint16_t out[2] = {0, 0};
+        if (c < a.n) {
+            const float dy = Half<OUT>::widen(a.dy[r * a.ld_dy + c]);
+            float value, slope;
+            if constexpr (kGated) {
+                const float u = Half<OUT>::widen(a.pre[1][r * a.ld_pre + c]);
+                act_and_slope_f32(a.act, Half<OUT>::widen(a.pre[0][r * a.ld_pre + c]), &value,
+                                  &slope);
+                out[0] = static_cast<uint16_t>(Half<OUT>::pack2(dy * u * slope, 0.0f));
+                out[1] = static_cast<uint16_t>(Half<OUT>::pack2(dy * value, 0.0f));
+                a.dz[0][r * a.ld_dz + c] = out[0];
+                a.dz[1][r * a.ld_dz + c] = out[1];
+            } else {
+                float dz = dy;
+                if (a.act != DQ4_ACT_NONE) {
+                    act_and_slope_f32(a.act, Half<OUT>::widen(a.pre[0][r * a.ld_pre + c]), &value,
+                                      &slope);
+                    dz = dy * slope;
+                }
+                sum = sum + dz;
+                out[0] = static_cast<uint16_t>(Half<OUT>::pack2(dz, 0.0f));
+                if (a.dz[0])
+                    a.dz[0][r * a.ld_dz + c] = out[0];
+            }
+        }
+        if (a.pad[0]) {
+            a.pad[0][r * a.ld_pad + c] = out[0];
+            if constexpr (kGated)
+                a.pad[1][r * a.ld_pad + c] = out[1];
+        }
+    }
+    if constexpr (!kGated)
+        if (a.partial && c < a.n)
+            a.partial[static_cast<int64_t>(blockIdx.y) * a.n + c] = sum;
+}
+
+// dbias[c] = the row blocks' sums, added in order.
+__global__ __launch_bounds__(kThreads) void bias_grad_reduce_kernel(const float *partial,
+                                                                    int64_t n, int32_t blocks,
+                                                                    float *dbias)
+{
+    const int64_t c = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+    if (c >= n)
+        return;
+    float sum = 0.0f;
+    for (int32_t b = 0; b < blocks; ++b)
+        sum = sum + partial[b * n + c];
+    dbias[c] = sum;
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+int64_t ceil_div(int64_t a, int64_t b)
+{
+    return (a + b - 1) / b;
+}
+
+int64_t align256(int64_t b)
+{
+    return (b + 255) & ~int64_t{255};
+}
+
+dq4_status_t launch(const void *kernel, int64_t gx, int64_t gy, int threads, void **params,
+                    hipStream_t s)
+{
+    if (gx > 0x7FFFFFFF || gy > 65535)
+        return DQ4_EUNSUPPORTED;
+    const hipError_t e = hipLaunchKernel(kernel, dim3(static_cast<uint32_t>(gx), static_cast<uint32_t>(gy)),
+                                         dim3(threads), params, 0, s);
+    return e == hipSuccess ? DQ4_OK : hip_failed(e);
+}
+
+bool rows_aligned(const void *p, int64_t ld, int64_t rows, int64_t width)
+{
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (rows <= 1 || ld % 8 == 0) && width % 8 == 0;
+}
+
+// The product reads this matrix where it lies, or a padded copy of it.
+bool needs_copy(const void *x, int64_t ld, int64_t m, int64_t k)
+{
+    return !rows_aligned(x, ld, m, k) || (m > 1 && ld > (int64_t{1} << 22));
+}
+
+int64_t padded_ld(int64_t k)
+{
+    return ceil_div(k, kChunk) * kChunk;
+}
+
+// The sizes of one call's product.
+struct Shape {
+    int64_t m, n, k;   // rows, output columns, summed index per x matrix
+    int32_t layout;
+    int n_x() const { return layout == kStacked ? 2 : 1; }
+    int64_t per_group() const { return layout == kSideBySide ? 64 : kGroup; }
+    int64_t groups() const { return ceil_div(n, per_group()); }
+    int64_t chunks() const { return ceil_div(k, kChunk); }
+    int64_t group_bytes() const { return chunks() * n_x() * kUnitBytes; }
+};
+
+constexpr int64_t kRowBlock = 64;  // rows per block of column sums
+
+// Workspace: [padded x copies][column sums][fragments of a window of groups]
+int64_t copy_bytes(const Shape &s, bool copy)
+{
+    return copy ? align256(s.m * padded_ld(s.k) * 2) * s.n_x() : 0;
+}
+
+int64_t partial_bytes(int64_t m, int64_t n)
+{
+    return align256(ceil_div(m, kRowBlock) * n * 4);
+}
+
+int64_t workspace_need(const Shape &s, int64_t fixed, bool least)
+{
+    const int64_t groups = least ? (s.groups() < 2 ? s.groups() : 2) : s.groups();
+    return fixed + groups * s.group_bytes();
+}
+
+template <int OUT, bool kGated, int WN, int WT, int TF>
+dq4_status_t launch_product_tile(ProductArgs a, hipStream_t s)
+{
+    a.tiles_t = static_cast<int32_t>(ceil_div(a.m, 16 * TF * WT));
+    const int64_t tiles = ceil_div(a.groups, WN) * a.tiles_t;
+    void *params[] = {&a};
+    return launch(reinterpret_cast<const void *>(&fragment_product_kernel<OUT, kGated, WN, WT, TF>),
+                  tiles, 1, 64 * WN * WT, params, s);
+}
+
+template <int OUT, bool kGated>
+dq4_status_t launch_product(const ProductArgs &a, int cus, hipStream_t s)
+{
+    if (ceil_div(a.groups, 2) * ceil_div(a.m, 256) * 4 >= cus * int64_t{3})
+        return launch_product_tile<OUT, kGated, 2, 4, 4>(a, s);
+    if (a.groups * ceil_div(a.m, 128) >= cus)
+        return launch_product_tile<OUT, kGated, 1, 4, 2>(a, s);
+    return launch_product_tile<OUT, kGated, 1, 4, 1>(a, s);
+}
+
+template <int OUT, bool kForward>
+dq4_status_t launch_fragments(FragmentArgs a, bool aligned, hipStream_t s)
+{
+    const int64_t all_chunks = a.layout == kStacked ? 2 * a.chunks : a.chunks;
+    const int64_t grid = kForward ? a.groups * ceil_div(all_chunks, 4)
+                                  : ceil_div(a.groups, 2) * all_chunks;
+    void *params[] = {&a};
+    const void *kernel =
+        aligned ? reinterpret_cast<const void *>(&weight_fragments_kernel<OUT, kForward, true>)
+                : reinterpret_cast<const void *>(&weight_fragments_kernel<OUT, kForward, false>);
+    return launch(kernel, grid, 1, kThreads, params, s);
+}
+
+Weight device_weight(const dq4_weight_t &w)
+{
+    return Weight{w.packed, w.scale_codes, w.nested_absmax, w.scale_codebook, w.codebook4, w.offset};
+}
+
+// Decode and multiply, window by window of output columns.
+template <int OUT, bool kForward>
+dq4_status_t run_product(const Shape &sh, const dq4_weight_t *w0, const dq4_weight_t *w1,
+                         int64_t n_out, int64_t n_in, int log2_block, ProductArgs p,
+                         uint8_t *fragments, int64_t fragment_bytes, hipStream_t s)
+{
+    int device = 0;
+    const hipError_t e = hipGetDevice(&device);
+    if (e != hipSuccess)
+        return hip_failed(e);
+    const int cus = compute_units(device);
+    const int64_t groups = sh.groups();
+    const int64_t window =
+        sh.group_bytes() == 0 ? groups : (fragment_bytes / sh.group_bytes() < groups
+                                              ? fragment_bytes / sh.group_bytes()
+                                              : groups);
+    FragmentArgs f{};
+    f.w[0] = device_weight(*w0);
+    f.w[1] = device_weight(w1 ? *w1 : *w0);
+    f.out = reinterpret_cast<uint16_t *>(fragments);
+    f.n_out = n_out;
+    f.n_in = n_in;
+    f.log2_block = log2_block;
+    f.chunks = static_cast<int32_t>(sh.chunks());
+    f.layout = sh.layout;
+    const bool aligned = n_in % 8 == 0 && reinterpret_cast<uintptr_t>(w0->packed) % 4 == 0 &&
+                         (!w1 || reinterpret_cast<uintptr_t>(w1->packed) % 4 == 0);
+    p.wfrag = f.out;
+    p.m = sh.m;
+    p.n = sh.n;
+    p.chunks = f.chunks;
+    p.n_x = sh.n_x();
+    for (int64_t g0 = 0; g0 < groups; g0 += window) {
+        f.group0 = static_cast<int32_t>(g0);
+        f.groups = static_cast<int32_t>(groups - g0 < window ? groups - g0 : window);
+        if (f.chunks > 0) {
+            const dq4_status_t st = launch_fragments<OUT, kForward>(f, aligned, s);
+            if (st != DQ4_OK)
+                return st;
+        }
+        p.groups = f.groups;
+        p.n0 = g0 * sh.per_group();
+        dq4_status_t st;
+        if constexpr (kForward)
+            st = sh.layout == kSideBySide ? launch_product<OUT, true>(p, cus, s)
+                                          : launch_product<OUT, false>(p, cus, s);
+        else
+            st = launch_product<OUT, false>(p, cus, s);
+        if (st != DQ4_OK)
+            return st;
+    }
+    return DQ4_OK;
+}
+
+dq4_status_t copy_rows(const void *x, int64_t ld, int64_t m, int64_t k, void *out, hipStream_t s)
+{
+    const uint16_t *src = static_cast<const uint16_t *>(x);
+    uint16_t *dst = static_cast<uint16_t *>(out);
+    int64_t ld_out = padded_ld(k);
+    void *params[] = {&src, &ld, &m, &k, &dst, &ld_out};
+    return launch(reinterpret_cast<const void *>(&rows_zero_fill_copy), ceil_div(ld_out, kThreads),
+                  m < 4096 ? m : 4096, kThreads, params, s);
+}
+
+// Sizes, type, activation and layout of a call; *empty when there is nothing
+// to write.
+dq4_status_t check_call(const dq4_weight_t *w0, const dq4_weight_t *w1, int64_t n_out,
+                        int64_t n_in, int64_t m, int32_t dtype, int32_t act, bool gated,
+                        int *log2_block)
+{
+    if (!w0 || (gated && !w1))
+        return DQ4_EINVAL;
+    if (dtype != DQ4_F16 && dtype != DQ4_BF16)
+        return DQ4_EINVAL;
+    const dq4_status_t st = validate_layout(w0->blocksize, w0->nested_blocksize, dtype, log2_block);
+    if (st != DQ4_OK)
+        return st;
+    if (gated && (w1->blocksize != w0->blocksize || w1->nested_blocksize != w0->nested_blocksize))
+        return DQ4_EUNSUPPORTED;
+    if (n_out < 0 || n_in < 0 || m < 0)
+        return DQ4_EINVAL;
+    if (act < (gated ? DQ4_ACT_RELU : DQ4_ACT_NONE) || act > DQ4_ACT_GELU_TANH)
+        return DQ4_EINVAL;
+    if (n_out > kMaxDim || n_in > kMaxDim || m > kMaxDim)
+        return DQ4_EUNSUPPORTED;
+    return DQ4_OK;
+}
+
+bool weight_missing(const dq4_weight_t *w)
+{
+    return !w->packed || !w->scale_codes || !w->nested_absmax || !w->scale_codebook || !w->codebook4;
+}
+
+// A row stride that rows of this width cannot have.
+bool bad_ld(int64_t ld, int64_t m, int64_t width)
+{
+    return m > 1 && (ld < width || ld > INT64_MAX / 2 / m);
+}
+
+bool sizes_ok(int64_t n_out, int64_t n_in, int64_t m)
+{
+    return n_out > 0 && n_in >= 0 && m > 0 && n_out <= kMaxDim && n_in <= kMaxDim && m <= kMaxDim;
+}
+
+}  // namespace
+}  // namespace dq4
+
+using namespace dq4;
+
+extern "C" {
+
+int64_t dq4_linear_fused_workspace_bytes(int64_t n_out, int64_t n_in, int64_t m, const void *x,
+                                         int64_t ld_x, int32_t least)
+{
+    if (!sizes_ok(n_out, n_in, m))
+        return 0;
+    const Shape s{m, n_out, n_in, kSingle};
+    return workspace_need(s, copy_bytes(s, needs_copy(x, ld_x, m, n_in)), least != 0);
+}
+
+int64_t dq4_gated_fused_workspace_bytes(int64_t n_ff, int64_t n_in, int64_t m, const void *x,
+                                        int64_t ld_x, int32_t least)
+{
+    if (!sizes_ok(n_ff, n_in, m))
+        return 0;
+    const Shape s{m, n_ff, n_in, kSideBySide};
+    return workspace_need(s, copy_bytes(s, needs_copy(x, ld_x, m, n_in)), least != 0);
+}
+
+int64_t dq4_linear_fused_backward_workspace_bytes(int64_t n_out, int64_t n_in, int64_t m,
+                                                  const void *dz, int64_t ld_dz, int32_t least)
+{
+    if (!sizes_ok(n_out, n_in, m))
+        return 0;
+    const Shape s{m, n_in, n_out, kSingle};
+    return workspace_need(s, copy_bytes(s, needs_copy(dz, ld_dz, m, n_out)) + partial_bytes(m, n_out),
+                          least != 0);
+}
+
+int64_t dq4_gated_fused_backward_workspace_bytes(int64_t n_ff, int64_t n_in, int64_t m,
+                                                 const void *dgate, const void *dup,
+                                                 int64_t ld_dpre, int32_t least)
+{
+    if (!sizes_ok(n_ff, n_in, m))
+        return 0;
+    const Shape s{m, n_in, n_ff, kStacked};
+    const bool copy = needs_copy(dgate, ld_dpre, m, n_ff) || needs_copy(dup, ld_dpre, m, n_ff);
+    return workspace_need(s, copy_bytes(s, copy), least != 0);
+}
+
+dq4_status_t dq4_linear_fused(const dq4_weight_t *w, int64_t n_out, int64_t n_in, int32_t dtype,
+                              int32_t activation, const void *x, int64_t m, int64_t ld_x,
+                              const void *bias, const void *residual, int64_t ld_residual,
+                              void *y, int64_t ld_y, void *pre, int64_t ld_pre, void *workspace,
+                              int64_t workspace_bytes, void *stream)
+{
+    int log2_block = 0;
+    const dq4_status_t st = check_call(w, nullptr, n_out, n_in, m, dtype, activation, false, &log2_block);
+    if (st != DQ4_OK)
+        return st;
+    if (m == 0 || n_out == 0)
+        return DQ4_OK;
+    if (!y || (n_in > 0 && (!x || weight_missing(w))))
+        return DQ4_EINVAL;
+    if (bad_ld(ld_x, m, n_in) || bad_ld(ld_y, m, n_out) || (residual && bad_ld(ld_residual, m, n_out)) ||
+        (pre && bad_ld(ld_pre, m, n_out)))
+        return DQ4_EINVAL;
+    const Shape sh{m, n_out, n_in, kSingle};
+    const bool copy = needs_copy(x, ld_x, m, n_in);
+    const int64_t fixed = copy_bytes(sh, copy);
+    if (workspace_bytes < workspace_need(sh, fixed, true) || (workspace_bytes > 0 && !workspace))
+        return DQ4_EINVAL;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    ProductArgs p{};
+    p.x[0] = p.x[1] = static_cast<const uint16_t *>(x);
+    p.ld_x = m > 1 ? ld_x : n_in;
+    p.k = n_in;
+    if (copy && n_in > 0) {
+        const dq4_status_t cs = copy_rows(x, ld_x, m, n_in, ws, s);
+        if (cs != DQ4_OK)
+            return cs;
+        p.x[0] = p.x[1] = reinterpret_cast<uint16_t *>(ws);
+        p.ld_x = p.k = padded_ld(n_in);
+    }
+    p.act = activation;
+    p.bias = static_cast<const uint16_t *>(bias);
+    p.residual = static_cast<const uint16_t *>(residual);
+    p.ld_residual = ld_residual;
+    p.y = static_cast<uint16_t *>(y);
+    p.ld_y = ld_y;
+    p.pre[0] = static_cast<uint16_t *>(pre);
+    p.ld_pre = ld_pre;
+    p.vec = rows_aligned(y, ld_y, m, 8) && (!bias || reinterpret_cast<uintptr_t>(bias) % 16 == 0) &&
+            (!residual || rows_aligned(residual, ld_residual, m, 8)) &&
+            (!pre || rows_aligned(pre, ld_pre, m, 8));
+    if (dtype == DQ4_F16)
+        return run_product<DQ4_F16, true>(sh, w, nullptr, n_out, n_in, log2_block, p, ws + fixed,
+                                          workspace_bytes - fixed, s);
+    return run_product<DQ4_BF16, true>(sh, w, nullptr, n_out, n_in, log2_block, p, ws + fixed,
+                                       workspace_bytes - fixed, s);
+}
+
+dq4_status_t dq4_gated_fused(const dq4_weight_t *gate, const dq4_weight_t *up, int64_t n_ff,
+                             int64_t n_in, int32_t dtype, int32_t activation, const void *x,
+                             int64_t m, int64_t ld_x, void *h, int64_t ld_h, void *gate_pre,
+                             void *up_pre, int64_t ld_pre, void *workspace,
+                             int64_t workspace_bytes, void *stream)
+{
+    int log2_block = 0;
+    const dq4_status_t st = check_call(gate, up, n_ff, n_in, m, dtype, activation, true, &log2_block);
+    if (st != DQ4_OK)
+        return st;
+    if (m == 0 || n_ff == 0)
+        return DQ4_OK;
+    if (!h || (n_in > 0 && (!x || weight_missing(gate) || weight_missing(up))))
+        return DQ4_EINVAL;
+    if ((gate_pre == nullptr) != (up_pre == nullptr))
+        return DQ4_EINVAL;
+    if (bad_ld(ld_x, m, n_in) || bad_ld(ld_h, m, n_ff) || (gate_pre && bad_ld(ld_pre, m, n_ff)))
+        return DQ4_EINVAL;
+    const Shape sh{m, n_ff, n_in, kSideBySide};
+    const bool copy = needs_copy(x, ld_x, m, n_in);
+    const int64_t fixed = copy_bytes(sh, copy);
+    if (workspace_bytes < workspace_need(sh, fixed, true) || (workspace_bytes > 0 && !workspace))
+        return DQ4_EINVAL;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    ProductArgs p{};
+    p.x[0] = p.x[1] = static_cast<const uint16_t *>(x);
+    p.ld_x = m > 1 ? ld_x : n_in;
+    p.k = n_in;
+    if (copy && n_in > 0) {
+        const dq4_status_t cs = copy_rows(x, ld_x, m, n_in, ws, s);
+        if (cs != DQ4_OK)
+            return cs;
+        p.x[0] = p.x[1] = reinterpret_cast<uint16_t *>(ws);
+        p.ld_x = p.k = padded_ld(n_in);
+    }
+    p.act = activation;
+    p.y = static_cast<uint16_t *>(h);
+    p.ld_y = ld_h;
+    p.pre[0] = static_cast<uint16_t *>(gate_pre);
+    p.pre[1] = static_cast<uint16_t *>(up_pre);
+    p.ld_pre = ld_pre;
+    p.vec = rows_aligned(h, ld_h, m, 8) && (!gate_pre || (rows_aligned(gate_pre, ld_pre, m, 8) &&
+                                                          rows_aligned(up_pre, ld_pre, m, 8)));
+    if (dtype == DQ4_F16)
+        return run_product<DQ4_F16, true>(sh, gate, up, n_ff, n_in, log2_block, p, ws + fixed,
+                                          workspace_bytes - fixed, s);
+    return run_product<DQ4_BF16, true>(sh, gate, up, n_ff, n_in, log2_block, p, ws + fixed,
+                                       workspace_bytes - fixed, s);
+}
+
+dq4_status_t dq4_linear_fused_backward(const dq4_weight_t *w, int64_t n_out, int64_t n_in,
+                                       int32_t dtype, int32_t activation, const void *dy,
+                                       int64_t m, int64_t ld_dy, const void *pre, int64_t ld_pre,
+                                       void *dx, int64_t ld_dx, void *dz, int64_t ld_dz,
+                                       float *dbias, void *workspace, int64_t workspace_bytes,
+                                       void *stream)
+{
+    int log2_block = 0;
+    const dq4_status_t st = check_call(w, nullptr, n_out, n_in, m, dtype, activation, false, &log2_block);
+    if (st != DQ4_OK)
+        return st;
+    const bool act = activation != DQ4_ACT_NONE;
+    if (!act && dz)
+        return DQ4_EINVAL;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (m == 0) {  // empty sums
+        if (!dbias || n_out == 0)
+            return DQ4_OK;
+        const float *none = nullptr;
+        int64_t n = n_out;
+        int32_t blocks = 0;
+        void *params[] = {&none, &n, &blocks, &dbias};
+        return launch(reinterpret_cast<const void *>(&bias_grad_reduce_kernel), ceil_div(n, kThreads),
+                      1, kThreads, params, s);
+    }
+    if (n_out > 0 && (!dy || (act && (!pre || !dz)) || bad_ld(ld_dy, m, n_out) ||
+                      (act && (bad_ld(ld_pre, m, n_out) || bad_ld(ld_dz, m, n_out)))))
+        return DQ4_EINVAL;
+    if (n_in > 0 && (!dx || bad_ld(ld_dx, m, n_in) || (n_out > 0 && weight_missing(w))))
+        return DQ4_EINVAL;
+    const Shape sh{m, n_in, n_out, kSingle};
+    const void *lhs = act ? dz : dy;
+    const int64_t ld_lhs = act ? ld_dz : ld_dy;
+    const bool copy = n_in > 0 && needs_copy(lhs, ld_lhs, m, n_out);
+    const int64_t copied = copy_bytes(sh, copy);
+    const int64_t fixed = copied + partial_bytes(m, n_out);
+    if (n_out > 0 && (workspace_bytes < workspace_need(sh, fixed, true) || !workspace))
+        return DQ4_EINVAL;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    ProductArgs p{};
+    p.x[0] = p.x[1] = static_cast<const uint16_t *>(lhs);
+    p.ld_x = m > 1 ? ld_lhs : n_out;
+    p.k = n_out;
+    if (n_out > 0 && (act || dbias || copy)) {
+        SlopeArgs a{};
+        a.dy = static_cast<const uint16_t *>(dy);
+        a.ld_dy = ld_dy;
+        a.pre[0] = static_cast<const uint16_t *>(pre);
+        a.ld_pre = ld_pre;
+        a.dz[0] = static_cast<uint16_t *>(dz);
+        a.ld_dz = ld_dz;
+        if (copy) {
+            a.pad[0] = reinterpret_cast<uint16_t *>(ws);
+            a.ld_pad = padded_ld(n_out);
+            p.x[0] = p.x[1] = a.pad[0];
+            p.ld_x = p.k = a.ld_pad;
+        }
+        const int64_t blocks = ceil_div(m, kRowBlock);
+        a.partial = !dbias ? nullptr : blocks == 1 ? dbias : reinterpret_cast<float *>(ws + copied);
+        a.m = m;
+        a.n = n_out;
+        a.act = activation;
+        a.rows_per_block = static_cast<int32_t>(kRowBlock);
+        void *params[] = {&a};
+        const void *kernel = dtype == DQ4_F16
+                                 ? reinterpret_cast<const void *>(&activation_slope_kernel<DQ4_F16, false>)
+                                 : reinterpret_cast<const void *>(&activation_slope_kernel<DQ4_BF16, false>);
+        dq4_status_t ls = launch(kernel, ceil_div(copy ? a.ld_pad : n_out, kThreads), blocks, kThreads,
+                                 params, s);
+        if (ls != DQ4_OK)
+            return ls;
+        if (dbias && blocks > 1) {
+            const float *partial = a.partial;
+            int64_t n = n_out;
+            int32_t count = static_cast<int32_t>(blocks);
+            void *rp[] = {&partial, &n, &count, &dbias};
+            ls = launch(reinterpret_cast<const void *>(&bias_grad_reduce_kernel), ceil_div(n, kThreads), 1,
+                        kThreads, rp, s);
+            if (ls != DQ4_OK)
+                return ls;
+        }
+    }
+    if (n_in == 0)
+        return DQ4_OK;
+    p.act = DQ4_ACT_NONE;
+    p.y = static_cast<uint16_t *>(dx);
+    p.ld_y = ld_dx;
+    p.vec = rows_aligned(dx, ld_dx, m, 8);
+    if (dtype == DQ4_F16)
+        return run_product<DQ4_F16, false>(sh, w, nullptr, n_out, n_in, log2_block, p, ws + fixed,
+                                           workspace_bytes - fixed, s);
+    return run_product<DQ4_BF16, false>(sh, w, nullptr, n_out, n_in, log2_block, p, ws + fixed,
+                                        workspace_bytes - fixed, s);
+}
+
+dq4_status_t dq4_gated_fused_backward(const dq4_weight_t *gate, const dq4_weight_t *up,
+                                      int64_t n_ff, int64_t n_in, int32_t dtype,
+                                      int32_t activation, const void *dh, int64_t m,
+                                      int64_t ld_dh, const void *gate_pre, const void *up_pre,
+                                      int64_t ld_pre, void *dx, int64_t ld_dx, void *dgate,
+                                      void *dup, int64_t ld_dpre, void *workspace,
+                                      int64_t workspace_bytes, void *stream)
+{
+    int log2_block = 0;
+    const dq4_status_t st = check_call(gate, up, n_ff, n_in, m, dtype, activation, true, &log2_block);
+    if (st != DQ4_OK)
+        return st;
+    if (m == 0)
+        return DQ4_OK;
+    if (n_ff > 0 && (!dh || !gate_pre || !up_pre || !dgate || !dup || bad_ld(ld_dh, m, n_ff) ||
+                     bad_ld(ld_pre, m, n_ff) || bad_ld(ld_dpre, m, n_ff)))
+        return DQ4_EINVAL;
+    if (n_in > 0 && (!dx || bad_ld(ld_dx, m, n_in) ||
+                     (n_ff > 0 && (weight_missing(gate) || weight_missing(up)))))
+        return DQ4_EINVAL;
+    const Shape sh{m, n_in, n_ff, kStacked};
+    const bool copy = n_in > 0 && (needs_copy(dgate, ld_dpre, m, n_ff) || needs_copy(dup, ld_dpre, m, n_ff));
+    const int64_t fixed = copy_bytes(sh, copy);
+    if (n_ff > 0 && (workspace_bytes < workspace_need(sh, fixed, true) || (workspace_bytes > 0 && !workspace)))
+        return DQ4_EINVAL;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    ProductArgs p{};
+    p.x[0] = static_cast<const uint16_t *>(dgate);
+    p.x[1] = static_cast<const uint16_t *>(dup);
+    p.ld_x = m > 1 ? ld_dpre : n_ff;
+    p.k = n_ff;
+    if (n_ff > 0) {
+        SlopeArgs a{};
+        a.dy = static_cast<const uint16_t *>(dh);
+        a.ld_dy = ld_dh;
+        a.pre[0] = static_cast<const uint16_t *>(gate_pre);
+        a.pre[1] = static_cast<const uint16_t *>(up_pre);
+        a.ld_pre = ld_pre;
+        a.dz[0] = static_cast<uint16_t *>(dgate);
+        a.dz[1] = static_cast<uint16_t *>(dup);
+        a.ld_dz = ld_dpre;
+        if (copy) {
+            a.ld_pad = padded_ld(n_ff);
+            a.pad[0] = reinterpret_cast<uint16_t *>(ws);
+            a.pad[1] = reinterpret_cast<uint16_t *>(ws + fixed / 2);
+            p.x[0] = a.pad[0];
+            p.x[1] = a.pad[1];
+            p.ld_x = p.k = a.ld_pad;
+        }
+        a.m = m;
+        a.n = n_ff;
+        a.act = activation;
+        a.rows_per_block = static_cast<int32_t>(kRowBlock);
+        void *params[] = {&a};
+        const void *kernel = dtype == DQ4_F16
+                                 ? reinterpret_cast<const void *>(&activation_slope_kernel<DQ4_F16, true>)
+                                 : reinterpret_cast<const void *>(&activation_slope_kernel<DQ4_BF16, true>);
+        const dq4_status_t ls = launch(kernel, ceil_div(copy ? a.ld_pad : n_ff, kThreads),
+                                       ceil_div(m, kRowBlock), kThreads, params, s);
+        if (ls != DQ4_OK)
+            return ls;
+    }
+    if (n_in == 0)
+        return DQ4_OK;
+    p.act = DQ4_ACT_NONE;
+    p.y = static_cast<uint16_t *>(dx);
+    p.ld_y = ld_dx;
+    p.vec = rows_aligned(dx, ld_dx, m, 8);
+    if (dtype == DQ4_F16)
+        return run_product<DQ4_F16, false>(sh, gate, up, n_ff, n_in, log2_block, p, ws + fixed,
+                                           workspace_bytes - fixed, s);
+    return run_product<DQ4_BF16, false>(sh, gate, up, n_ff, n_in, log2_block, p, ws + fixed,
+                                        workspace_bytes - fixed, s);
+}
+
+}  // extern "C"
