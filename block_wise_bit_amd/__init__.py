@@ -130,10 +130,10 @@ def library() -> ctypes.CDLL:
     for name in ("dq4_linear_fused", "dq4_linear_fused_backward", "dq4_gated_fused",
                  "dq4_gated_fused_backward"):
         getattr(lib, name).restype = i32
-    lib.dq4_linear_fused_workspace_bytes.argtypes = [i64, i64, i64, P, i64, i32]
-    lib.dq4_linear_fused_backward_workspace_bytes.argtypes = [i64, i64, i64, P, i64, i32]
-    lib.dq4_gated_fused_workspace_bytes.argtypes = [i64, i64, i64, P, i64, i32]
-    lib.dq4_gated_fused_backward_workspace_bytes.argtypes = [i64, i64, i64, P, P, i64, i32]
+    lib.dq4_linear_fused_workspace_bytes.argtypes = [W, i64, i64, i64, P, i64, i32]
+    lib.dq4_linear_fused_backward_workspace_bytes.argtypes = [W, i64, i64, i64, P, i64, i32]
+    lib.dq4_gated_fused_workspace_bytes.argtypes = [W, W, i64, i64, i64, P, i64, i32]
+    lib.dq4_gated_fused_backward_workspace_bytes.argtypes = [W, W, i64, i64, i64, P, P, i64, i32]
     for name in ("dq4_linear_fused", "dq4_linear_fused_backward", "dq4_gated_fused",
                  "dq4_gated_fused_backward"):
         getattr(lib, name + "_workspace_bytes").restype = i64
@@ -662,57 +662,78 @@ def _refuse_overlap(outputs, inputs):
                 raise ValueError(f"{name} overlaps {other}")
 
 
-def _bytes_workspace(workspace, preferred: int, least: int, device, stream):
-    """(address, bytes) of the caller's workspace, or of one of the preferred
-    size; the tensor itself is returned to keep it alive over the call."""
+def _bytes_workspace(workspace, size, sizes, device, stream):
+    """(tensor, address, bytes) of the caller's workspace, checked against the
+    least that `size` asks for these sizes, or of one of the preferred size."""
     torch = _torch()
     if workspace is None:
-        workspace = _used_on(torch.empty(preferred, dtype=torch.uint8, device=device), stream)
-    elif workspace.device != device or not workspace.is_contiguous():
+        nbytes = size(*sizes, 0)
+        if nbytes == 0:
+            return None, None, 0
+        workspace = _used_on(torch.empty(nbytes, dtype=torch.uint8, device=device), stream)
+        return workspace, workspace.data_ptr(), nbytes
+    if workspace.device != device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {device}")
     nbytes = workspace.numel() * workspace.element_size()
+    least = size(*sizes, 1)
     if nbytes < least:
         raise ValueError(f"workspace holds {nbytes} bytes, needs {least}")
-    return workspace, workspace.data_ptr(), nbytes
+    return workspace, workspace.data_ptr() if nbytes else None, nbytes
 
 
 def _address(t):
     return t.data_ptr() if t is not None and t.numel() else None
 
 
-def dq4_linear_fused_workspace_bytes(n_out: int, n_in: int, m: int, x=None, least: bool = False) -> int:
-    """Workspace bytes of dq4_linear_fused for this x (None: 16-byte aligned
-    dense rows): the preferred size, or the smallest the call accepts."""
-    ld = int(n_in) if x is None or x.size(0) <= 1 else x.stride(0)
-    return int(library().dq4_linear_fused_workspace_bytes(int(n_out), int(n_in), int(m), _address(x)
-                                                          if x is not None else None, ld,
-                                                          1 if least else 0))
+def _query_weight(packed):
+    """A weight for a workspace query, which looks at the address of the packed
+    codes alone (None: 4-byte aligned)."""
+    return ctypes.byref(Dq4Weight(packed=None if packed is None else packed.data_ptr()))
 
 
-def dq4_gated_fused_workspace_bytes(n_ff: int, n_in: int, m: int, x=None, least: bool = False) -> int:
+def _query_matrix(t, width: int):
+    """(address, row stride) for a workspace query (None: 16-byte aligned, dense)."""
+    if t is None:
+        return None, width
+    return t.data_ptr(), width if t.size(0) <= 1 else t.stride(0)
+
+
+def dq4_linear_fused_workspace_bytes(n_out: int, n_in: int, m: int, x=None, packed=None,
+                                     least: bool = False) -> int:
+    """Workspace bytes of dq4_linear_fused for this x and these packed codes
+    (only their alignment matters; None: aligned): the preferred size, or the
+    smallest the call accepts."""
+    return int(library().dq4_linear_fused_workspace_bytes(
+        _query_weight(packed), int(n_out), int(n_in), int(m), *_query_matrix(x, int(n_in)),
+        1 if least else 0))
+
+
+def dq4_gated_fused_workspace_bytes(n_ff: int, n_in: int, m: int, x=None, gate_packed=None,
+                                    up_packed=None, least: bool = False) -> int:
     """As dq4_linear_fused_workspace_bytes, for dq4_gated_fused."""
-    ld = int(n_in) if x is None or x.size(0) <= 1 else x.stride(0)
-    return int(library().dq4_gated_fused_workspace_bytes(int(n_ff), int(n_in), int(m), _address(x)
-                                                         if x is not None else None, ld,
-                                                         1 if least else 0))
+    return int(library().dq4_gated_fused_workspace_bytes(
+        _query_weight(gate_packed), _query_weight(up_packed), int(n_ff), int(n_in), int(m),
+        *_query_matrix(x, int(n_in)), 1 if least else 0))
 
 
-def dq4_linear_fused_backward_workspace_bytes(n_out: int, n_in: int, m: int, dz=None,
+def dq4_linear_fused_backward_workspace_bytes(n_out: int, n_in: int, m: int, dz=None, packed=None,
                                               least: bool = False) -> int:
     """Workspace bytes of dq4_linear_fused_backward; dz: the matrix its product
-    reads (dy where there is no activation; None: 16-byte aligned dense rows)."""
-    ld = int(n_out) if dz is None or dz.size(0) <= 1 else dz.stride(0)
+    reads (dy where there is no activation)."""
     return int(library().dq4_linear_fused_backward_workspace_bytes(
-        int(n_out), int(n_in), int(m), _address(dz), ld, 1 if least else 0))
+        _query_weight(packed), int(n_out), int(n_in), int(m), *_query_matrix(dz, int(n_out)),
+        1 if least else 0))
 
 
 def dq4_gated_fused_backward_workspace_bytes(n_ff: int, n_in: int, m: int, dgate=None, dup=None,
+                                             gate_packed=None, up_packed=None,
                                              least: bool = False) -> int:
     """Workspace bytes of dq4_gated_fused_backward; dgate, dup: the matrices its
-    product reads (None: 16-byte aligned dense rows)."""
-    ld = int(n_ff) if dgate is None or dgate.size(0) <= 1 else dgate.stride(0)
+    product reads, of one row stride."""
+    address, ld = _query_matrix(dgate, int(n_ff))
     return int(library().dq4_gated_fused_backward_workspace_bytes(
-        int(n_ff), int(n_in), int(m), _address(dgate), _address(dup), ld, 1 if least else 0))
+        _query_weight(gate_packed), _query_weight(up_packed), int(n_ff), int(n_in), int(m),
+        address, _query_matrix(dup, int(n_ff))[0], ld, 1 if least else 0))
 
 
 def dq4_linear_fused(packed, scale_codes, nested_absmax, scale_codebook, codebook4,
@@ -754,10 +775,9 @@ def dq4_linear_fused(packed, scale_codes, nested_absmax, scale_codebook, codeboo
                         [("x", x), ("bias", bias), ("residual", None if in_place else residual)])
     address = x.data_ptr()
     lib = library()
+    sizes = (ctypes.byref(w), n_out, n_in, m, address, ld_x)
     size = lib.dq4_linear_fused_workspace_bytes
-    keep, ws, nbytes = _bytes_workspace(
-        workspace, size(n_out, n_in, m, address, ld_x, 0) if workspace is None else 0,
-        size(n_out, n_in, m, address, ld_x, 1), device, stream)
+    keep, ws, nbytes = _bytes_workspace(workspace, size, sizes, device, stream)
     with torch.cuda.device(device):
         st = lib.dq4_linear_fused(
             ctypes.byref(w), n_out, n_in, code, act, address, m, ld_x, _address(bias),
@@ -816,10 +836,9 @@ def dq4_linear_fused_backward(packed, scale_codes, nested_absmax, scale_codebook
         _refuse_overlap([("dx", dx), ("dz", dz), ("dbias", dbias)], [("dy", dy), ("pre", pre)])
     lhs, ld_lhs = (dy, ld_dy) if act == DQ4_ACT_NONE else (dz, ld_dz)
     lib = library()
+    sizes = (ctypes.byref(w), n_out, n_in, m, lhs.data_ptr(), ld_lhs)
     size = lib.dq4_linear_fused_backward_workspace_bytes
-    keep, ws, nbytes = _bytes_workspace(
-        workspace, size(n_out, n_in, m, lhs.data_ptr(), ld_lhs, 0) if workspace is None else 0,
-        size(n_out, n_in, m, lhs.data_ptr(), ld_lhs, 1), device, stream)
+    keep, ws, nbytes = _bytes_workspace(workspace, size, sizes, device, stream)
     with torch.cuda.device(device):
         st = lib.dq4_linear_fused_backward(
             ctypes.byref(w), n_out, n_in, code, act, dy.data_ptr(), m, ld_dy, _address(pre), ld_pre,
@@ -864,10 +883,9 @@ def dq4_gated_fused(gate, up, n_ff: int, n_in: int, blocksize: int, x,
         _refuse_overlap([("h", h), ("gate_pre", gate_pre), ("up_pre", up_pre)], [("x", x)])
     address = x.data_ptr()
     lib = library()
+    sizes = (ctypes.byref(wg), ctypes.byref(wu), n_ff, n_in, m, address, ld_x)
     size = lib.dq4_gated_fused_workspace_bytes
-    keep, ws, nbytes = _bytes_workspace(
-        workspace, size(n_ff, n_in, m, address, ld_x, 0) if workspace is None else 0,
-        size(n_ff, n_in, m, address, ld_x, 1), device, stream)
+    keep, ws, nbytes = _bytes_workspace(workspace, size, sizes, device, stream)
     with torch.cuda.device(device):
         st = lib.dq4_gated_fused(
             ctypes.byref(wg), ctypes.byref(wu), n_ff, n_in, code, act, address, m, ld_x,
@@ -913,11 +931,9 @@ def dq4_gated_fused_backward(gate, up, n_ff: int, n_in: int, blocksize: int, dh,
         _refuse_overlap([("dx", dx), ("dgate", dgate), ("dup", dup)],
                         [("dh", dh), ("gate_pre", gate_pre), ("up_pre", up_pre)])
     lib = library()
+    sizes = (ctypes.byref(wg), ctypes.byref(wu), n_ff, n_in, m, dgate.data_ptr(), dup.data_ptr(), ld_dpre)
     size = lib.dq4_gated_fused_backward_workspace_bytes
-    keep, ws, nbytes = _bytes_workspace(
-        workspace,
-        size(n_ff, n_in, m, dgate.data_ptr(), dup.data_ptr(), ld_dpre, 0) if workspace is None else 0,
-        size(n_ff, n_in, m, dgate.data_ptr(), dup.data_ptr(), ld_dpre, 1), device, stream)
+    keep, ws, nbytes = _bytes_workspace(workspace, size, sizes, device, stream)
     with torch.cuda.device(device):
         st = lib.dq4_gated_fused_backward(
             ctypes.byref(wg), ctypes.byref(wu), n_ff, n_in, code, act, dh.data_ptr(), m, ld_dh,

@@ -555,6 +555,278 @@ __global__ __launch_bounds__(64 * WN * WT) void fragment_product_kernel(ProductA
 }
 
 // ---------------------------------------------------------------------------
+// few rows: the weight decoded straight into operand registers
+// ---------------------------------------------------------------------------
+struct RowsArgs {
+    Weight w[2];
+    int64_t n_out, n_in;        // the weight's shape (both weights)
+    int64_t n_elems;            // n_out * n_in
+    int32_t log2_block;
+    int32_t row_blocks;
+    ProductArgs out;            // x and the epilogue's matrices
+};
+
+// The two values of a packed byte, low nibble first, in copies that the lanes
+// share out: entry b at byte 256 b, in it 32 copies of 8 bytes (one weight) or
+// 16 copies of both weights' pairs (gated).  The address of a lookup is one
+// byte permute, and lanes that are served together read different banks
+// whatever their codes: of a wave's 8-byte lookups 16 lanes are served at a
+// time (16 copies measured 2.7 ns per lookup and CU, 32 copies 2.4, 8 copies
+// 4.4, a single table 26).
+constexpr int kPairTableBytes = 256 * 32 * 8;
+
+template <int OUT>
+__device__ __forceinline__ u32x4 decode_dword(uint32_t word, float s, const uint8_t *table,
+                                              uint32_t lane_byte)
+{
+    u32x4 q;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        // bytes [lane_byte, word.byte[j], 0, 0]
+        const uint32_t at = __builtin_amdgcn_perm(word, lane_byte, 0x0C0C0000u | ((4u + j) << 8));
+        const f32x2 pair = *reinterpret_cast<const f32x2 *>(table + at);
+        q[j] = Half<OUT>::pack2(pair[0] * s, pair[1] * s);
+    }
+    return q;
+}
+
+// Output row r of the linear call's columns n0 .. n0 + 3.
+template <int OUT>
+__device__ __forceinline__ void finish_linear4(const ProductArgs &a, int64_t row, int64_t n0,
+                                               f32x4 acc)
+{
+    const int64_t left = a.n - n0;
+    if (row >= a.m || left <= 0)
+        return;
+    const int valid = left < 4 ? static_cast<int>(left) : 4;
+    const bool vec = a.vec && valid == 4;
+    float z[4] = {acc[0], acc[1], acc[2], acc[3]};
+    if (a.bias) {
+        float b[4];
+        load_values<OUT, 4>(a.bias + n0, vec, valid, b);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            z[j] = z[j] + b[j];
+    }
+    if (a.pre[0])
+        store_values<OUT, 4>(a.pre[0] + row * a.ld_pre + n0, vec, valid, z);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        z[j] = act_f32(a.act, z[j]);
+    if (a.residual) {
+        float r[4];
+        load_values<OUT, 4>(a.residual + row * a.ld_residual + n0, vec, valid, r);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            z[j] = z[j] + r[j];
+    }
+    store_values<OUT, 4>(a.y + row * a.ld_y + n0, vec, valid, z);
+}
+
+// m <= 16 TF rows of x against the 4-bit weight, which is read once and never
+// written out: a lane loads 16 packed bytes (32 k) of one weight row, decodes
+// each dword into the matrix instruction's operand registers, and multiplies
+// it with the x fragments of the same k.  A workgroup takes R fragments of 16
+// weight rows per row wave (gated: R / 2 of each weight, the same columns) at
+// a time; its waves split the chunks of 128 k, and the partial sums meet in
+// LDS.  Workgroups walk the row blocks; the next chunk's loads, also those of
+// the next row block, are issued before the current chunk is decoded.
+// kWhole: a lane's 32 k lie in one block (n_in % 32 == 0); otherwise they may
+// straddle two, and each dword (n_in % 8 == 0) picks one.
+template <int OUT, bool kGated, int R, int TF, int WAVES, int WR, bool kWhole>
+__global__ __launch_bounds__(64 * WAVES) void weight_rows_kernel(RowsArgs a)
+{
+    constexpr int kW = kGated ? 2 : 1;
+    constexpr int kPer = R / kW;                 // fragments per weight and row wave
+    constexpr int WK = WAVES / WR;
+    constexpr int kBlockRows = 16 * kPer * WR;   // weight rows per row block
+    constexpr int kSpan = 128;                   // k per chunk
+    constexpr int kBounds = kWhole ? 1 : 2;      // blocks a lane's 32 k may touch
+    __shared__ __attribute__((aligned(1024))) uint8_t table[kPairTableBytes];
+    __shared__ float scb[kW][256];
+    __shared__ __attribute__((aligned(16))) f32x4 partial[WAVES][R][64];
+
+    const int tid = threadIdx.x;
+    const int lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wk = wave % WK, wr = wave / WK;
+    const int r = lane & 15, g = lane >> 4;
+    const int lb = a.log2_block;
+    const uint32_t n_in = static_cast<uint32_t>(a.n_in);
+    const int chunks = static_cast<int>((n_in + kSpan - 1) / kSpan);
+
+    struct Loads {
+        u32x4 packed[R];
+        uint32_t code[R][kBounds];
+        float absmax[R][kBounds];
+    };
+    u32x4 x[4][TF];  // the current chunk's; each step's is reloaded once used
+    // buffers of the row block whose chunks are being loaded
+    u32x4 rs_packed[kW], rs_code[kW], rs_absmax[kW];
+    uint32_t block_phase = 0, group_phase = 0;  // of the row block's first element
+    auto enter = [&](int64_t rb) {
+        const int64_t e0 = rb * kBlockRows * a.n_in;
+        const int64_t b0 = e0 >> lb;
+        block_phase = static_cast<uint32_t>(e0 - (b0 << lb));
+        group_phase = static_cast<uint32_t>(b0 & 255);
+        const int64_t blocks = (a.n_elems + (int64_t{1} << lb) - 1) >> lb;
+        const int64_t most = 0x7FFFFFF0;
+        const int64_t pb = ((a.n_elems + 1) >> 1) - (e0 >> 1), cb = blocks - b0,
+                      gb = (((blocks + 255) >> 8) - (b0 >> 8)) * 4;
+#pragma unroll
+        for (int w = 0; w < kW; ++w) {
+            rs_packed[w] = make_rsrc(a.w[w].packed + (e0 >> 1), static_cast<uint32_t>(pb < most ? pb : most));
+            rs_code[w] = make_rsrc(a.w[w].scale_codes + b0, static_cast<uint32_t>(cb < most ? cb : most));
+            rs_absmax[w] = make_rsrc(a.w[w].nested_absmax + (b0 >> 8), static_cast<uint32_t>(gb < most ? gb : most));
+        }
+    };
+    auto rsrc = [](u32x4 q) {
+        return __builtin_amdgcn_make_buffer_rsrc(
+            reinterpret_cast<void *>((static_cast<uint64_t>(q[1]) << 32) | q[0]), 0,
+            static_cast<int32_t>(q[2]), kRawBufferWord3);
+    };
+    const u32x4 rs_x = make_rsrc(a.out.x[0],
+                                 static_cast<uint32_t>(((a.out.m - 1) * a.out.ld_x + a.out.k) * 2));
+    uint32_t x_row[TF];
+#pragma unroll
+    for (int t = 0; t < TF; ++t)
+        x_row[t] = t * 16 + r < a.out.m
+                       ? static_cast<uint32_t>((t * 16 + r) * a.out.ld_x * 2)
+                       : 0x80000000u;
+    auto load = [&](Loads &l, int c) {
+        const uint32_t k = c * kSpan + 32 * g;
+#pragma unroll
+        for (int f = 0; f < R; ++f) {
+            const int w = kGated ? f / kPer : 0;
+            const uint32_t row = wr * (16 * kPer) + (kGated ? f % kPer : f) * 16 + r;
+            const uint32_t e = row * n_in + k;
+            l.packed[f] = __builtin_amdgcn_raw_buffer_load_b128(rsrc(rs_packed[w]), e >> 1, 0, 0);
+#pragma unroll
+            for (int h = 0; h < kBounds; ++h) {
+                const uint32_t b = (block_phase + e + (h ? 31 : 0)) >> lb;
+                l.code[f][h] = __builtin_amdgcn_raw_buffer_load_b8(rsrc(rs_code[w]), b, 0, 0);
+                l.absmax[f][h] = __builtin_bit_cast(
+                    float, __builtin_amdgcn_raw_buffer_load_b32(rsrc(rs_absmax[w]),
+                                                                ((group_phase + b) >> 8) * 4, 0, 0));
+            }
+        }
+    };
+    auto load_x = [&](int c, int st) {
+        const uint32_t k = c * kSpan + 32 * g + 8 * st;
+#pragma unroll
+        for (int t = 0; t < TF; ++t)
+            x[st][t] = __builtin_amdgcn_raw_buffer_load_b128(
+                rsrc(rs_x), k < static_cast<uint32_t>(a.out.k) ? x_row[t] + k * 2 : 0x80000000u, 0, 0);
+    };
+
+    Loads cur;
+    int64_t load_rb = blockIdx.x;
+    int load_c = wk;
+    const bool any = wk < chunks;  // this wave has chunks at all
+    if (any) {
+        enter(load_rb);
+        load(cur, load_c);
+#pragma unroll
+        for (int st = 0; st < 4; ++st)
+            load_x(load_c, st);
+    }
+
+    // the lookup tables, while the first loads are in flight
+#pragma unroll
+    for (int w = 0; w < kW; ++w) {
+        if (tid < 256)
+            scb[w][tid] = a.w[w].scale_codebook[tid];
+    }
+    for (int i = tid; i < 256 * 32; i += 64 * WAVES) {
+        const int b = i >> 5;
+        const float *cb4 = a.w[kGated ? i & 1 : 0].codebook4;
+        *reinterpret_cast<f32x2 *>(&table[i * 8]) = f32x2{cb4[b & 15], cb4[b >> 4]};
+    }
+    __syncthreads();
+
+    const uint32_t lane_byte = kGated ? (lane & 15) * 16 : (lane & 31) * 8;
+    for (int64_t rb = blockIdx.x; rb < a.row_blocks; rb += gridDim.x) {
+        f32x4 acc[R][TF];
+#pragma unroll
+        for (int f = 0; f < R; ++f)
+#pragma unroll
+            for (int t = 0; t < TF; ++t)
+                acc[f][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        const uint32_t phase = static_cast<uint32_t>((rb * kBlockRows * a.n_in) & ((1 << lb) - 1));
+        for (int c = wk; c < chunks; c += WK) {
+            // the following chunk, of this row block or the next one
+            load_c += WK;
+            if (load_c >= chunks) {
+                load_c = wk;
+                load_rb += gridDim.x;
+                if (load_rb < a.row_blocks)
+                    enter(load_rb);
+            }
+            Loads next = cur;
+            if (load_rb < a.row_blocks)
+                load(next, load_c);
+            float s[R][kBounds];
+#pragma unroll
+            for (int f = 0; f < R; ++f)
+#pragma unroll
+                for (int h = 0; h < kBounds; ++h)
+                    s[f][h] = block_scale(scb[kGated ? f / kPer : 0][cur.code[f][h]], cur.absmax[f][h],
+                                          a.w[kGated ? f / kPer : 0].offset);
+            const uint32_t k = c * kSpan + 32 * g;
+            const bool tail = (c + 1) * kSpan > static_cast<int>(n_in);
+#pragma unroll
+            for (int st = 0; st < 4; ++st) {
+#pragma unroll
+                for (int f = 0; f < R; ++f) {
+                    float sc = s[f][0];
+                    if constexpr (!kWhole) {
+                        const uint32_t row = wr * (16 * kPer) + (kGated ? f % kPer : f) * 16 + r;
+                        const uint32_t e = phase + row * n_in + k;
+                        if (((e + 8 * st) >> lb) != (e >> lb))
+                            sc = s[f][kBounds - 1];
+                    }
+                    u32x4 wf = decode_dword<OUT>(cur.packed[f][st], sc,
+                                                 table + (kGated ? f / kPer : 0) * 8, lane_byte);
+                    if (tail && k + 8 * st >= n_in)  // beyond the row: no value at all
+                        wf = u32x4{0, 0, 0, 0};
+#pragma unroll
+                    for (int t = 0; t < TF; ++t)
+                        acc[f][t] = Half<OUT>::mfma(wf, x[st][t], acc[f][t]);
+                }
+                load_x(load_c, st);  // after the last row block: a chunk again, unused
+            }
+            cur = next;
+        }
+        // the k-waves' partial sums, 16 rows of x at a time
+#pragma unroll
+        for (int t = 0; t < TF; ++t) {
+            __syncthreads();
+#pragma unroll
+            for (int f = 0; f < R; ++f)
+                partial[wave][f][lane] = acc[f][t];
+            __syncthreads();
+            for (int i = tid; i < WR * kPer * 64; i += 64 * WAVES) {
+                const int ln = i & 63, f = (i >> 6) % kPer, row_wave = (i >> 6) / kPer;
+                f32x4 sum = partial[row_wave * WK][f][ln];
+                for (int q = 1; q < WK; ++q)
+                    sum = sum + partial[row_wave * WK + q][f][ln];
+                const int64_t n0 = rb * kBlockRows + row_wave * (16 * kPer) + f * 16 + (ln >> 4) * 4;
+                const int64_t row = t * 16 + (ln & 15);
+                if constexpr (kGated) {
+                    f32x4 up = partial[row_wave * WK][f + kPer][ln];
+                    for (int q = 1; q < WK; ++q)
+                        up = up + partial[row_wave * WK + q][f + kPer][ln];
+                    float gv[4] = {sum[0], sum[1], sum[2], sum[3]}, uv[4] = {up[0], up[1], up[2], up[3]};
+                    finish_gated<OUT>(a.out, row, n0, gv, uv);
+                } else {
+                    finish_linear4<OUT>(a.out, row, n0, sum);
+                }
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
 // rows copied into a padded matrix, and the backward elementwise pass
 // ---------------------------------------------------------------------------
 // x rows (any alignment and stride) into rows of ld_out elements, zeros from
@@ -718,6 +990,26 @@ int64_t workspace_need(const Shape &s, int64_t fixed, bool least)
     return fixed + groups * s.group_bytes();
 }
 
+constexpr int64_t kRowsMost = 64;  // rows of x that the decode-in-registers kernel takes
+
+// Whether that kernel takes the call: rows of whole packed dwords, and few
+// rows of x.
+bool rows_route(const dq4_weight_t *w0, const dq4_weight_t *w1, int64_t n_in, int64_t m)
+{
+    return m <= kRowsMost && n_in > 0 && n_in % 8 == 0 &&
+           reinterpret_cast<uintptr_t>(w0->packed) % 4 == 0 &&
+           (!w1 || reinterpret_cast<uintptr_t>(w1->packed) % 4 == 0);
+}
+
+// Workspace of a forward call: nothing but x's copy where the weight is
+// decoded in registers.
+int64_t forward_need(const Shape &s, const dq4_weight_t *w0, const dq4_weight_t *w1, int64_t n_in,
+                     bool copy, bool least)
+{
+    const int64_t fixed = copy_bytes(s, copy);
+    return rows_route(w0, w1, n_in, s.m) ? fixed : workspace_need(s, fixed, least);
+}
+
 template <int OUT, bool kGated, int WN, int WT, int TF>
 dq4_status_t launch_product_tile(ProductArgs a, hipStream_t s)
 {
@@ -736,6 +1028,38 @@ dq4_status_t launch_product(const ProductArgs &a, int cus, hipStream_t s)
     if (a.groups * ceil_div(a.m, 128) >= cus)
         return launch_product_tile<OUT, kGated, 1, 4, 2>(a, s);
     return launch_product_tile<OUT, kGated, 1, 4, 1>(a, s);
+}
+
+template <int OUT, bool kGated, int R, int TF, int WAVES, int WR, bool kWhole>
+dq4_status_t launch_rows_tile(RowsArgs a, int cus, hipStream_t s)
+{
+    const int64_t block_rows = 16 * (kGated ? R / 2 : R) * WR;
+    a.row_blocks = static_cast<int32_t>(ceil_div(a.n_out, block_rows));
+    void *params[] = {&a};
+    return launch(reinterpret_cast<const void *>(&weight_rows_kernel<OUT, kGated, R, TF, WAVES, WR, kWhole>),
+                  a.row_blocks < cus ? a.row_blocks : cus, 1, 64 * WAVES, params, s);
+}
+
+template <int OUT, bool kGated, bool kWhole>
+dq4_status_t launch_rows(const RowsArgs &a, int cus, hipStream_t s)
+{
+    const int64_t frags = ceil_div(a.n_out, 16);
+    if (a.out.m <= 16) {
+        if constexpr (kGated) {
+            if (frags <= 2 * cus)
+                return launch_rows_tile<OUT, true, 2, 1, 8, 1, kWhole>(a, cus, s);
+            return launch_rows_tile<OUT, true, 4, 1, 8, 1, kWhole>(a, cus, s);
+        } else {
+            if (frags <= cus)
+                return launch_rows_tile<OUT, false, 1, 1, 16, 1, kWhole>(a, cus, s);
+            if (frags <= 2 * cus || !kWhole)
+                return launch_rows_tile<OUT, false, 2, 1, 16, 1, kWhole>(a, cus, s);
+            return launch_rows_tile<OUT, false, kWhole ? 4 : 2, 1, 16, 1, kWhole>(a, cus, s);
+        }
+    }
+    if (a.out.m <= 32)
+        return launch_rows_tile<OUT, kGated, 4, 2, 8, 1, kWhole>(a, cus, s);
+    return launch_rows_tile<OUT, kGated, !kGated && kWhole ? 4 : 2, 4, 8, 1, kWhole>(a, cus, s);
 }
 
 template <int OUT, bool kForward>
@@ -767,6 +1091,25 @@ dq4_status_t run_product(const Shape &sh, const dq4_weight_t *w0, const dq4_weig
     if (e != hipSuccess)
         return hip_failed(e);
     const int cus = compute_units(device);
+    p.m = sh.m;
+    p.n = sh.n;
+    if constexpr (kForward) {
+        if (rows_route(w0, w1, n_in, sh.m)) {
+            RowsArgs r{};
+            r.w[0] = device_weight(*w0);
+            r.w[1] = device_weight(w1 ? *w1 : *w0);
+            r.n_out = n_out;
+            r.n_in = n_in;
+            r.n_elems = n_out * n_in;
+            r.log2_block = log2_block;
+            r.out = p;
+            if (n_in % 32 == 0)
+                return w1 ? launch_rows<OUT, true, true>(r, cus, s)
+                          : launch_rows<OUT, false, true>(r, cus, s);
+            return w1 ? launch_rows<OUT, true, false>(r, cus, s)
+                      : launch_rows<OUT, false, false>(r, cus, s);
+        }
+    }
     const int64_t groups = sh.groups();
     const int64_t window =
         sh.group_bytes() == 0 ? groups : (fragment_bytes / sh.group_bytes() < groups
@@ -784,8 +1127,6 @@ dq4_status_t run_product(const Shape &sh, const dq4_weight_t *w0, const dq4_weig
     const bool aligned = n_in % 8 == 0 && reinterpret_cast<uintptr_t>(w0->packed) % 4 == 0 &&
                          (!w1 || reinterpret_cast<uintptr_t>(w1->packed) % 4 == 0);
     p.wfrag = f.out;
-    p.m = sh.m;
-    p.n = sh.n;
     p.chunks = f.chunks;
     p.n_x = sh.n_x();
     for (int64_t g0 = 0; g0 < groups; g0 += window) {
@@ -867,39 +1208,43 @@ using namespace dq4;
 
 extern "C" {
 
-int64_t dq4_linear_fused_workspace_bytes(int64_t n_out, int64_t n_in, int64_t m, const void *x,
-                                         int64_t ld_x, int32_t least)
+int64_t dq4_linear_fused_workspace_bytes(const dq4_weight_t *w, int64_t n_out, int64_t n_in,
+                                         int64_t m, const void *x, int64_t ld_x, int32_t least)
 {
-    if (!sizes_ok(n_out, n_in, m))
+    if (!w || !sizes_ok(n_out, n_in, m))
         return 0;
     const Shape s{m, n_out, n_in, kSingle};
-    return workspace_need(s, copy_bytes(s, needs_copy(x, ld_x, m, n_in)), least != 0);
+    return forward_need(s, w, nullptr, n_in, needs_copy(x, ld_x, m, n_in), least != 0);
 }
 
-int64_t dq4_gated_fused_workspace_bytes(int64_t n_ff, int64_t n_in, int64_t m, const void *x,
+int64_t dq4_gated_fused_workspace_bytes(const dq4_weight_t *gate, const dq4_weight_t *up,
+                                        int64_t n_ff, int64_t n_in, int64_t m, const void *x,
                                         int64_t ld_x, int32_t least)
 {
-    if (!sizes_ok(n_ff, n_in, m))
+    if (!gate || !up || !sizes_ok(n_ff, n_in, m))
         return 0;
     const Shape s{m, n_ff, n_in, kSideBySide};
-    return workspace_need(s, copy_bytes(s, needs_copy(x, ld_x, m, n_in)), least != 0);
+    return forward_need(s, gate, up, n_in, needs_copy(x, ld_x, m, n_in), least != 0);
 }
 
-int64_t dq4_linear_fused_backward_workspace_bytes(int64_t n_out, int64_t n_in, int64_t m,
-                                                  const void *dz, int64_t ld_dz, int32_t least)
+int64_t dq4_linear_fused_backward_workspace_bytes(const dq4_weight_t *w, int64_t n_out,
+                                                  int64_t n_in, int64_t m, const void *dz,
+                                                  int64_t ld_dz, int32_t least)
 {
-    if (!sizes_ok(n_out, n_in, m))
+    if (!w || !sizes_ok(n_out, n_in, m))
         return 0;
     const Shape s{m, n_in, n_out, kSingle};
     return workspace_need(s, copy_bytes(s, needs_copy(dz, ld_dz, m, n_out)) + partial_bytes(m, n_out),
                           least != 0);
 }
 
-int64_t dq4_gated_fused_backward_workspace_bytes(int64_t n_ff, int64_t n_in, int64_t m,
-                                                 const void *dgate, const void *dup,
-                                                 int64_t ld_dpre, int32_t least)
+int64_t dq4_gated_fused_backward_workspace_bytes(const dq4_weight_t *gate,
+                                                 const dq4_weight_t *up, int64_t n_ff,
+                                                 int64_t n_in, int64_t m, const void *dgate,
+                                                 const void *dup, int64_t ld_dpre,
+                                                 int32_t least)
 {
-    if (!sizes_ok(n_ff, n_in, m))
+    if (!gate || !up || !sizes_ok(n_ff, n_in, m))
         return 0;
     const Shape s{m, n_in, n_ff, kStacked};
     const bool copy = needs_copy(dgate, ld_dpre, m, n_ff) || needs_copy(dup, ld_dpre, m, n_ff);
@@ -926,7 +1271,8 @@ dq4_status_t dq4_linear_fused(const dq4_weight_t *w, int64_t n_out, int64_t n_in
     const Shape sh{m, n_out, n_in, kSingle};
     const bool copy = needs_copy(x, ld_x, m, n_in);
     const int64_t fixed = copy_bytes(sh, copy);
-    if (workspace_bytes < workspace_need(sh, fixed, true) || (workspace_bytes > 0 && !workspace))
+    if (workspace_bytes < forward_need(sh, w, nullptr, n_in, copy, true) ||
+        (workspace_bytes > 0 && !workspace))
         return DQ4_EINVAL;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     hipStream_t s = static_cast<hipStream_t>(stream);
@@ -980,7 +1326,8 @@ dq4_status_t dq4_gated_fused(const dq4_weight_t *gate, const dq4_weight_t *up, i
     const Shape sh{m, n_ff, n_in, kSideBySide};
     const bool copy = needs_copy(x, ld_x, m, n_in);
     const int64_t fixed = copy_bytes(sh, copy);
-    if (workspace_bytes < workspace_need(sh, fixed, true) || (workspace_bytes > 0 && !workspace))
+    if (workspace_bytes < forward_need(sh, gate, up, n_in, copy, true) ||
+        (workspace_bytes > 0 && !workspace))
         return DQ4_EINVAL;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     hipStream_t s = static_cast<hipStream_t>(stream);

@@ -92,11 +92,12 @@ dq4_status_t dq4_linear_fused(const dq4_weight_t *w, int64_t n_out, int64_t n_in
                               void *y, int64_t ld_y, void *pre, int64_t ld_pre, void *workspace,
                               int64_t workspace_bytes, void *stream);
 
-/* Workspace bytes of dq4_linear_fused for x at this address and row stride
- * (only their alignment matters): the preferred size, or with least != 0 the
- * smallest the call accepts.  0 for sizes the call rejects.  Host only. */
-int64_t dq4_linear_fused_workspace_bytes(int64_t n_out, int64_t n_in, int64_t m, const void *x,
-                                         int64_t ld_x, int32_t least);
+/* Workspace bytes of dq4_linear_fused for this weight and x (only the
+ * alignment of w->packed, x and ld_x matters): the preferred size, or with
+ * least != 0 the smallest the call accepts.  0 when the call needs none, and
+ * for a missing weight or sizes the call rejects.  Host only. */
+int64_t dq4_linear_fused_workspace_bytes(const dq4_weight_t *w, int64_t n_out, int64_t n_in,
+                                         int64_t m, const void *x, int64_t ld_x, int32_t least);
 
 /*
  * dz = T(dy * act'(pre)), dx = T(dz W), dbias = column sums of the unrounded
@@ -114,8 +115,9 @@ dq4_status_t dq4_linear_fused_backward(const dq4_weight_t *w, int64_t n_out, int
                                        void *stream);
 
 /* dz, ld_dz: of the matrix the product reads (dy with DQ4_ACT_NONE). */
-int64_t dq4_linear_fused_backward_workspace_bytes(int64_t n_out, int64_t n_in, int64_t m,
-                                                  const void *dz, int64_t ld_dz, int32_t least);
+int64_t dq4_linear_fused_backward_workspace_bytes(const dq4_weight_t *w, int64_t n_out,
+                                                  int64_t n_in, int64_t m, const void *dz,
+                                                  int64_t ld_dz, int32_t least);
 
 /*
  * h = T(act(x Wg^T) * (x Wu^T)), both weights n_ff x n_in with one block size.
@@ -129,7 +131,8 @@ dq4_status_t dq4_gated_fused(const dq4_weight_t *gate, const dq4_weight_t *up, i
                              void *up_pre, int64_t ld_pre, void *workspace,
                              int64_t workspace_bytes, void *stream);
 
-int64_t dq4_gated_fused_workspace_bytes(int64_t n_ff, int64_t n_in, int64_t m, const void *x,
+int64_t dq4_gated_fused_workspace_bytes(const dq4_weight_t *gate, const dq4_weight_t *up,
+                                        int64_t n_ff, int64_t n_in, int64_t m, const void *x,
                                         int64_t ld_x, int32_t least);
 
 /*
@@ -147,9 +150,11 @@ dq4_status_t dq4_gated_fused_backward(const dq4_weight_t *gate, const dq4_weight
                                       int64_t workspace_bytes, void *stream);
 
 /* dgate, dup: of the matrices the product reads (their alignment matters). */
-int64_t dq4_gated_fused_backward_workspace_bytes(int64_t n_ff, int64_t n_in, int64_t m,
-                                                 const void *dgate, const void *dup,
-                                                 int64_t ld_dpre, int32_t least);
+int64_t dq4_gated_fused_backward_workspace_bytes(const dq4_weight_t *gate,
+                                                 const dq4_weight_t *up, int64_t n_ff,
+                                                 int64_t n_in, int64_t m, const void *dgate,
+                                                 const void *dup, int64_t ld_dpre,
+                                                 int32_t least);
 
 #ifdef __cplusplus
 }

@@ -48,7 +48,7 @@ def test_linear_validation(lib):
         return linear(lib, **k)
     assert call(m=0) == dq4.DQ4_OK
     assert call(n_out=0) == dq4.DQ4_OK
-    assert call() == dq4.DQ4_EINVAL                               # no workspace
+    assert call(m=300) == dq4.DQ4_EINVAL                          # no workspace
     assert call(ws=None, ws_bytes=BIG) == dq4.DQ4_EINVAL
     for k in (dict(null_w=True), dict(x=None), dict(y=None), dict(m=-1), dict(n_out=-1), dict(n_in=-1),
               dict(dtype=dq4.DQ4_F32), dict(dtype=7), dict(act=5), dict(act=-1), dict(ld_x=127),
@@ -102,21 +102,30 @@ def test_gated_backward_validation(lib):
 
 
 def test_workspace_sizes(lib):
-    for name in ("linear_fused", "gated_fused", "linear_fused_backward"):
+    w, odd = ctypes.byref(weight()), ctypes.byref(weight(packed=17))
+    for name, ws in (("linear_fused", (w,)), ("gated_fused", (w, w)), ("linear_fused_backward", (w,))):
         f = getattr(lib, f"dq4_{name}_workspace_bytes")
         for bad in ((0, 64, 4), (64, -1, 4), (64, 64, 0), (1 << 22, 64, 4), (64, 1 << 22, 4), (64, 64, 1 << 22)):
-            assert f(*bad, ONE, 64, 0) == 0
-        least, most = f(1000, 2048, 300, ONE, 2048, 1), f(1000, 2048, 300, ONE, 2048, 0)
+            assert f(*ws, *bad, ONE, 64, 0) == 0
+        assert f(*(None for _ in ws), 64, 64, 4, ONE, 64, 0) == 0
+        least, most = f(*ws, 1000, 2048, 300, ONE, 2048, 1), f(*ws, 1000, 2048, 300, ONE, 2048, 0)
         assert 0 < least <= most
         # a misaligned matrix takes a padded copy
-        assert f(1000, 2048, 300, P(2), 2048, 0) >= most + 300 * 1000 * 2
+        assert f(*ws, 1000, 2048, 300, P(2), 2048, 0) >= most + 300 * 1000 * 2
+    # one token: the weight is decoded in registers, unless its rows start off a dword
+    assert lib.dq4_linear_fused_workspace_bytes(w, 1000, 2048, 1, ONE, 2048, 0) == 0
+    assert lib.dq4_linear_fused_workspace_bytes(odd, 1000, 2048, 1, ONE, 2048, 1) > 0
+    assert lib.dq4_linear_fused_workspace_bytes(w, 1000, 2047, 1, ONE, 2047, 1) > 0
+    assert lib.dq4_gated_fused_workspace_bytes(w, w, 1000, 2048, 1, ONE, 2048, 0) == 0
+    assert lib.dq4_gated_fused_workspace_bytes(w, odd, 1000, 2048, 1, ONE, 2048, 1) > 0
     f = lib.dq4_gated_fused_backward_workspace_bytes
-    assert 0 < f(1000, 2048, 300, ONE, ONE, 1000, 1) <= f(1000, 2048, 300, ONE, ONE, 1000, 0)
-    assert f(1000, 2048, 300, ONE, P(2), 1000, 0) >= f(1000, 2048, 300, ONE, ONE, 1000, 0) + 2 * 300 * 1000 * 2
-    assert f(0, 64, 4, ONE, ONE, 64, 0) == 0
+    most = f(w, w, 1000, 2048, 300, ONE, ONE, 1000, 0)
+    assert 0 < f(w, w, 1000, 2048, 300, ONE, ONE, 1000, 1) <= most
+    assert f(w, w, 1000, 2048, 300, ONE, P(2), 1000, 0) >= most + 2 * 300 * 1000 * 2
+    assert f(w, w, 0, 64, 4, ONE, ONE, 64, 0) == 0
     # nothing overflows at the largest sizes
     big = 1 << 21
-    assert lib.dq4_linear_fused_workspace_bytes(big, big, big, P(2), big, 0) > 3 << 42
+    assert lib.dq4_linear_fused_workspace_bytes(w, big, big, big, P(2), big, 0) > 3 << 42
 
 
 def test_binding_rejects_host_tensors(lib):

@@ -237,6 +237,7 @@ def test_any_workspace_gives_the_same_bits(m, n_out, n_in):
 
     def buffers(size, *args):
         least, most = size(n_out, n_in, m, *args, least=True), size(n_out, n_in, m, *args)
+        assert least <= most
         for n in (least, (least + most) // 2, most, most + 1000):
             yield torch.full((n // 2 + 1,), float("nan"), dtype=torch.float16, device="cuda").view(torch.uint8)[:n]
     y = dq4.dq4_linear_fused(**w, **sizes, x=x)
@@ -490,7 +491,7 @@ def test_refusals():
     refused(f, **w, **s, x=x, y=y[:3])
     refused(f, **w, **s, x=x, y=x[:, :64])                          # y over x
     refused(f, **w, **s, x=x, y=y, pre=y)
-    refused(f, **w, **s, x=x, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    refused(f, **w, **s, x=x.repeat(100, 1), workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     refused(f, **w, **dict(s, blocksize=48), x=x)
     refused(f, **w, **dict(s, n_out=65), x=x)                       # more than the weight holds
     refused(f, **w, **dict(s, n_out=-1), x=x)
