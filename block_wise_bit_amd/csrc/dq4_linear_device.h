@@ -18,6 +18,7 @@ typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 // The 16-bit type T of a call (OUT = DQ4_F16 or DQ4_BF16): conversions from
@@ -57,7 +58,9 @@ struct Half<DQ4_BF16> {
     }
     static __device__ __forceinline__ uint32_t pack2(float lo, float hi)
     {
-        return pack_bf16x2(lo, hi);
+        // one v_cvt_pk_bf16_f32, round to nearest even
+        return __builtin_bit_cast(
+            uint32_t, __builtin_convertvector((f32x2{rounded_fp32(lo), rounded_fp32(hi)}), bf16x2));
     }
     static __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c)
     {

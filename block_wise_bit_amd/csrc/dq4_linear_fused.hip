@@ -582,8 +582,8 @@ __device__ __forceinline__ u32x4 decode_dword(uint32_t word, float s, const uint
     u32x4 q;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        // bytes [lane_byte, word.byte[j], 0, 0]
-        const uint32_t at = __builtin_amdgcn_perm(word, lane_byte, 0x0C0C0000u | ((4u + j) << 8));
+        // lane_byte with the word's byte j as its byte 1
+        const uint32_t at = __builtin_amdgcn_perm(word, lane_byte, 0x03020000u | ((4u + j) << 8));
         const f32x2 pair = *reinterpret_cast<const f32x2 *>(table + at);
         q[j] = Half<OUT>::pack2(pair[0] * s, pair[1] * s);
     }
@@ -623,33 +623,33 @@ __device__ __forceinline__ void finish_linear4(const ProductArgs &a, int64_t row
     store_values<OUT, 4>(a.y + row * a.ld_y + n0, vec, valid, z);
 }
 
-// m <= 16 TF rows of x against the 4-bit weight, which is read once and never
-// written out: a lane loads 16 packed bytes (32 k) of one weight row, decodes
-// each dword into the matrix instruction's operand registers, and multiplies
-// it with the x fragments of the same k.  A workgroup takes R fragments of 16
-// weight rows per row wave (gated: R / 2 of each weight, the same columns) at
-// a time; its waves split the chunks of 128 k, and the partial sums meet in
-// LDS.  Workgroups walk the row blocks; the next chunk's loads, also those of
-// the next row block, are issued before the current chunk is decoded.
-// kWhole: a lane's 32 k lie in one block (n_in % 32 == 0); otherwise they may
-// straddle two, and each dword (n_in % 8 == 0) picks one.
-template <int OUT, bool kGated, int R, int TF, int WAVES, int WR, bool kWhole>
-__global__ __launch_bounds__(64 * WAVES) void weight_rows_kernel(RowsArgs a)
+// Weight rows of whole dwords whose length is no multiple of 32: m <= 16 TF
+// rows of x against the 4-bit weight, which is read once and never written
+// out.  A lane loads 16 packed bytes (32 k) of one weight row, decodes each
+// dword into the matrix instruction's operand registers, and multiplies it
+// with the x fragments of the same k; its 32 k may straddle two blocks, and
+// each dword picks one.  A workgroup takes R fragments of 16 weight rows
+// (gated: R / 2 of each weight, the same columns) at a time; its waves split
+// the chunks of 128 k, and the partial sums meet in LDS.  Workgroups walk the
+// row blocks; the next chunk's loads, also those of the next row block, are
+// issued before the current chunk is decoded.
+template <int OUT, bool kGated, int R, int TF, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void ragged_rows_kernel(RowsArgs a)
 {
     constexpr int kW = kGated ? 2 : 1;
     constexpr int kPer = R / kW;                 // fragments per weight and row wave
-    constexpr int WK = WAVES / WR;
-    constexpr int kBlockRows = 16 * kPer * WR;   // weight rows per row block
+    constexpr int WK = WAVES;                    // waves along k
+    constexpr int kBlockRows = 16 * kPer;        // weight rows per row block
     constexpr int kSpan = 128;                   // k per chunk
-    constexpr int kBounds = kWhole ? 1 : 2;      // blocks a lane's 32 k may touch
-    __shared__ __attribute__((aligned(1024))) uint8_t table[kPairTableBytes];
+    constexpr int kBounds = 2;                   // blocks a lane's 32 k may touch
+    __shared__ __attribute__((aligned(1024))) uint8_t table[kPairTableBytes + 256];
     __shared__ float scb[kW][256];
     __shared__ __attribute__((aligned(16))) f32x4 partial[WAVES][R][64];
 
     const int tid = threadIdx.x;
     const int lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wk = wave % WK, wr = wave / WK;
+    const int wk = wave;
     const int r = lane & 15, g = lane >> 4;
     const int lb = a.log2_block;
     const uint32_t n_in = static_cast<uint32_t>(a.n_in);
@@ -698,9 +698,10 @@ __global__ __launch_bounds__(64 * WAVES) void weight_rows_kernel(RowsArgs a)
 #pragma unroll
         for (int f = 0; f < R; ++f) {
             const int w = kGated ? f / kPer : 0;
-            const uint32_t row = wr * (16 * kPer) + (kGated ? f % kPer : f) * 16 + r;
+            const uint32_t row = (kGated ? f % kPer : f) * 16 + r;
             const uint32_t e = row * n_in + k;
-            l.packed[f] = __builtin_amdgcn_raw_buffer_load_b128(rsrc(rs_packed[w]), e >> 1, 0, 0);
+            l.packed[f] = __builtin_amdgcn_raw_buffer_load_b128(
+                rsrc(rs_packed[w]), e >> 1, 0, 0);
 #pragma unroll
             for (int h = 0; h < kBounds; ++h) {
                 const uint32_t b = (block_phase + e + (h ? 31 : 0)) >> lb;
@@ -742,6 +743,8 @@ __global__ __launch_bounds__(64 * WAVES) void weight_rows_kernel(RowsArgs a)
         const float *cb4 = a.w[kGated ? i & 1 : 0].codebook4;
         *reinterpret_cast<f32x2 *>(&table[i * 8]) = f32x2{cb4[b & 15], cb4[b >> 4]};
     }
+    if (tid < 64)
+        *reinterpret_cast<uint32_t *>(&table[kPairTableBytes + tid * 4]) = 0;
     __syncthreads();
 
     const uint32_t lane_byte = kGated ? (lane & 15) * 16 : (lane & 31) * 8;
@@ -773,21 +776,18 @@ __global__ __launch_bounds__(64 * WAVES) void weight_rows_kernel(RowsArgs a)
                     s[f][h] = block_scale(scb[kGated ? f / kPer : 0][cur.code[f][h]], cur.absmax[f][h],
                                           a.w[kGated ? f / kPer : 0].offset);
             const uint32_t k = c * kSpan + 32 * g;
-            const bool tail = (c + 1) * kSpan > static_cast<int>(n_in);
 #pragma unroll
             for (int st = 0; st < 4; ++st) {
 #pragma unroll
                 for (int f = 0; f < R; ++f) {
                     float sc = s[f][0];
-                    if constexpr (!kWhole) {
-                        const uint32_t row = wr * (16 * kPer) + (kGated ? f % kPer : f) * 16 + r;
-                        const uint32_t e = phase + row * n_in + k;
-                        if (((e + 8 * st) >> lb) != (e >> lb))
-                            sc = s[f][kBounds - 1];
-                    }
+                    const uint32_t row = (kGated ? f % kPer : f) * 16 + r;
+                    const uint32_t e = phase + row * n_in + k;
+                    if (((e + 8 * st) >> lb) != (e >> lb))
+                        sc = s[f][kBounds - 1];
                     u32x4 wf = decode_dword<OUT>(cur.packed[f][st], sc,
                                                  table + (kGated ? f / kPer : 0) * 8, lane_byte);
-                    if (tail && k + 8 * st >= n_in)  // beyond the row: no value at all
+                    if (k + 8 * st >= n_in)  // beyond the row there is no value at all
                         wf = u32x4{0, 0, 0, 0};
 #pragma unroll
                     for (int t = 0; t < TF; ++t)
@@ -805,22 +805,513 @@ __global__ __launch_bounds__(64 * WAVES) void weight_rows_kernel(RowsArgs a)
             for (int f = 0; f < R; ++f)
                 partial[wave][f][lane] = acc[f][t];
             __syncthreads();
-            for (int i = tid; i < WR * kPer * 64; i += 64 * WAVES) {
-                const int ln = i & 63, f = (i >> 6) % kPer, row_wave = (i >> 6) / kPer;
-                f32x4 sum = partial[row_wave * WK][f][ln];
+            for (int i = tid; i < kPer * 64; i += 64 * WAVES) {
+                const int ln = i & 63, f = i >> 6;
+                f32x4 sum = partial[0][f][ln];
                 for (int q = 1; q < WK; ++q)
-                    sum = sum + partial[row_wave * WK + q][f][ln];
-                const int64_t n0 = rb * kBlockRows + row_wave * (16 * kPer) + f * 16 + (ln >> 4) * 4;
+                    sum = sum + partial[q][f][ln];
+                const int64_t n0 = rb * kBlockRows + f * 16 + (ln >> 4) * 4;
                 const int64_t row = t * 16 + (ln & 15);
                 if constexpr (kGated) {
-                    f32x4 up = partial[row_wave * WK][f + kPer][ln];
+                    f32x4 up = partial[0][f + kPer][ln];
                     for (int q = 1; q < WK; ++q)
-                        up = up + partial[row_wave * WK + q][f + kPer][ln];
+                        up = up + partial[q][f + kPer][ln];
                     float gv[4] = {sum[0], sum[1], sum[2], sum[3]}, uv[4] = {up[0], up[1], up[2], up[3]};
                     finish_gated<OUT>(a.out, row, n0, gv, uv);
                 } else {
                     finish_linear4<OUT>(a.out, row, n0, sum);
                 }
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// one to four rows of x: weight rows read in straight lines
+// ---------------------------------------------------------------------------
+// The products are dot products of whole weight rows, and the 4-bit weight is
+// all the memory traffic, so every load of it is 1 KiB of one row: lane l takes
+// the 16 bytes (32 k) l of a chunk of 2048 k.  The matrix instruction still
+// does the sum: with operand lane l holding the same 8 k of the weight row (A)
+// and of x (B), D[i][i] is the sum over the pieces i, 16 + i, 32 + i, 48 + i,
+// and the diagonal's 16 values add up to the chunk's dot product.  15 of 16
+// results are unused; the instruction is still cheaper than widening the
+// rounded weight for the vector unit (4 vector instructions per packed byte
+// against 10), and x stays in registers: a wave keeps one chunk of k and walks
+// rows.  The waves' partial sums meet in LDS, in a fixed order.
+struct TokenArgs {
+    Weight w[2];
+    int64_t n_in;
+    int64_t n_elems;
+    int32_t log2_block;
+    int32_t wk;                 // waves along k
+    int32_t batch;              // weight rows per pass through LDS
+    ProductArgs out;
+};
+
+constexpr int kTokenSpan = 2048;  // k per wave and chunk
+constexpr int kTokenDepth = 4;    // rows in flight per wave
+
+template <int OUT>
+__device__ __forceinline__ void finish_one(const ProductArgs &a, int64_t row, int64_t n, float z)
+{
+    if (a.bias)
+        z = z + Half<OUT>::widen(a.bias[n]);
+    if (a.pre[0])
+        a.pre[0][row * a.ld_pre + n] = static_cast<uint16_t>(Half<OUT>::pack2(z, 0.0f));
+    z = act_f32(a.act, z);
+    if (a.residual)
+        z = z + Half<OUT>::widen(a.residual[row * a.ld_residual + n]);
+    a.y[row * a.ld_y + n] = static_cast<uint16_t>(Half<OUT>::pack2(z, 0.0f));
+}
+
+// Floats of partial sums: what the tables leave of the LDS.
+template <bool kGated>
+constexpr int kTokenPartials = kGated ? 6144 : 8192;
+
+template <int OUT, bool kGated, int M, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void token_rows_kernel(TokenArgs a)
+{
+    constexpr int kW = kGated ? 2 : 1;
+    __shared__ __attribute__((aligned(1024))) uint8_t table[kW][kPairTableBytes + 256];
+    __shared__ float scb[kW][256];
+    __shared__ __attribute__((aligned(16))) float partial[2][kTokenPartials<kGated> / 2];
+
+    const int tid = threadIdx.x;
+    const int threads = blockDim.x;
+    const int lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int WK = a.wk, WR = (threads >> 6) / WK;
+    const int wk = wave % WK, wr = wave / WK;
+    const int lb = a.log2_block;
+    const uint32_t n_in = static_cast<uint32_t>(a.n_in);
+    const int chunks = static_cast<int>((n_in + kTokenSpan - 1) / kTokenSpan);
+    const int passes = (chunks + WK - 1) / WK;
+
+    // this workgroup's rows, in batches
+    const int64_t row_first = a.out.n * blockIdx.x / gridDim.x;
+    const int64_t row_last = a.out.n * (blockIdx.x + 1) / gridDim.x;
+    int64_t limit = row_last;
+
+    struct Row {
+        u32x4 packed;
+        uint32_t code;
+        float absmax;
+    };
+    Row ring[kTokenDepth][kW];
+    u32x4 x[M][4];
+    uint32_t k_lane = 0, packed_off = 0;
+    auto load = [&](Row (&to)[kW], int64_t row) {
+        row = row < limit ? row : limit - 1;  // loaded again, unused
+        const int64_t e0 = row * a.n_in;
+        const int64_t b0 = e0 >> lb;
+        const uint32_t phase = static_cast<uint32_t>(e0) & ((1u << lb) - 1);
+        const uint32_t b = (phase + k_lane) >> lb;
+        const uint32_t gr = ((static_cast<uint32_t>(b0) & 255) + b) >> 8;
+#pragma unroll
+        for (int w = 0; w < kW; ++w) {
+            const auto rsrc = [](const void *p) {
+                return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, 0x7FFFFFFF,
+                                                         kRawBufferWord3);
+            };
+            // lanes beyond the row: an offset past every buffer, zeros
+            const uint32_t past = packed_off & 0x80000000u;
+            to[w].packed = __builtin_amdgcn_raw_buffer_load_b128(rsrc(a.w[w].packed + (e0 >> 1)),
+                                                                 packed_off, 0, 0);
+            to[w].code = __builtin_amdgcn_raw_buffer_load_b8(rsrc(a.w[w].scale_codes + b0), b | past, 0, 0);
+            to[w].absmax = __builtin_bit_cast(
+                float, __builtin_amdgcn_raw_buffer_load_b32(rsrc(a.w[w].nested_absmax + (b0 >> 8)),
+                                                            (gr * 4) | past, 0, 0));
+        }
+    };
+    auto enter_chunk = [&](int chunk) {
+        k_lane = chunk * kTokenSpan + 32 * lane;
+        packed_off = k_lane < n_in ? k_lane / 2 : 0x80000000u;
+#pragma unroll
+        for (int t = 0; t < M; ++t)
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                x[t][s] = u32x4{0, 0, 0, 0};
+                if (k_lane < n_in && t < a.out.m)
+                    x[t][s] = *reinterpret_cast<const u32x4 *>(a.out.x[0] + t * a.out.ld_x + k_lane + 8 * s);
+            }
+    };
+
+    // the first rows' loads go out before the tables are built
+    int64_t b0 = row_first;
+    if (wk < chunks) {
+        enter_chunk(wk);
+#pragma unroll
+        for (int d = 0; d < kTokenDepth; ++d)
+            load(ring[d], b0 + wr + d * WR);
+    }
+#pragma unroll
+    for (int w = 0; w < kW; ++w) {
+        if (tid < 256)
+            scb[w][tid] = a.w[w].scale_codebook[tid];
+        for (int i = tid; i < 256 * 32; i += threads) {
+            const int b = i >> 5;
+            *reinterpret_cast<f32x2 *>(&table[w][i * 8]) =
+                f32x2{a.w[w].codebook4[b & 15], a.w[w].codebook4[b >> 4]};
+        }
+        if (tid < 64)
+            *reinterpret_cast<uint32_t *>(&table[w][kPairTableBytes + tid * 4]) = 0;
+    }
+    __syncthreads();
+
+    const uint32_t lane_byte = (lane & 31) * 8;
+    const int G = lane >> 4, c = lane & 15;
+    const bool diagonal = G == (c >> 2);
+    int parity = 0;
+    for (; b0 < row_last; b0 += a.batch, parity ^= 1) {
+        const int rows = static_cast<int>(row_last - b0 < a.batch ? row_last - b0 : a.batch);
+        float *part = partial[parity];
+        if (passes > 1)
+            limit = b0 + rows;
+        for (int pass = 0; pass < passes; ++pass) {
+            const int chunk = wk + pass * WK;
+            if (chunk >= chunks)
+                break;
+            if (pass > 0 || (passes > 1 && b0 != row_first)) {  // else the ring is filled
+                enter_chunk(chunk);
+#pragma unroll
+                for (int d = 0; d < kTokenDepth; ++d)
+                    load(ring[d], b0 + wr + d * WR);
+            }
+            // a lane beyond the row (its loads gave zeros) reads the row of
+            // zeros behind the table, times 0
+            const bool beyond = k_lane >= n_in;
+            const uint32_t from = beyond ? lane_byte | kPairTableBytes : lane_byte;
+            for (int r0 = wr; r0 < rows; r0 += kTokenDepth * WR) {
+#pragma unroll
+                for (int d = 0; d < kTokenDepth; ++d) {
+                    const int r = r0 + d * WR;
+                    if (r >= rows)
+                        break;
+#pragma unroll
+                    for (int w = 0; w < kW; ++w) {
+                        float s = block_scale(scb[w][ring[d][w].code], ring[d][w].absmax, a.w[w].offset);
+                        s = beyond ? 0.0f : s;
+                        f32x4 acc[M];
+#pragma unroll
+                        for (int st = 0; st < 4; ++st) {
+                            const u32x4 wf = decode_dword<OUT>(ring[d][w].packed[st], s, table[w], from);
+#pragma unroll
+                            for (int t = 0; t < M; ++t)
+                                acc[t] = Half<OUT>::mfma(wf, x[t][st],
+                                                         st == 0 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : acc[t]);
+                        }
+#pragma unroll
+                        for (int t = 0; t < M; ++t) {
+                            // the diagonal value of this lane's column, its quad's sum
+                            float v = (c & 2) ? ((c & 1) ? acc[t][3] : acc[t][2])
+                                              : ((c & 1) ? acc[t][1] : acc[t][0]);
+                            v = v + __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), 0xB1, 0xF, 0xF, true));
+                            v = v + __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), 0x4E, 0xF, 0xF, true));
+                            float *to = part + (((r * M + t) * kW + w) * WK + wk) * 4 + G;
+                            if (diagonal && (c & 3) == 0)
+                                *to = pass == 0 ? v : *to + v;
+                        }
+                    }
+                    // batches are whole rings long: with one pass the ring
+                    // runs on into the next batch
+                    load(ring[d], b0 + r + kTokenDepth * WR);
+                }
+            }
+        }
+        __syncthreads();
+        for (int i = tid; i < rows * M; i += threads) {
+            const int t = i / rows, r = i - t * rows;
+            if (t >= a.out.m)
+                break;
+            float z[kW];
+#pragma unroll
+            for (int w = 0; w < kW; ++w) {
+                const float *from = part + ((r * M + t) * kW + w) * WK * 4;
+                float sum = 0.0f;
+                for (int q = 0; q < WK; ++q) {
+                    const f32x4 v = *reinterpret_cast<const f32x4 *>(from + 4 * q);
+                    sum = sum + ((v[0] + v[1]) + (v[2] + v[3]));
+                }
+                z[w] = sum;
+            }
+            if constexpr (kGated) {
+                if (a.out.pre[0]) {
+                    a.out.pre[0][t * a.out.ld_pre + b0 + r] = static_cast<uint16_t>(Half<OUT>::pack2(z[0], 0.0f));
+                    a.out.pre[1][t * a.out.ld_pre + b0 + r] = static_cast<uint16_t>(Half<OUT>::pack2(z[1], 0.0f));
+                }
+                a.out.y[t * a.out.ld_y + b0 + r] =
+                    static_cast<uint16_t>(Half<OUT>::pack2(act_f32(a.out.act, z[0]) * z[1], 0.0f));
+            } else {
+                finish_one<OUT>(a.out, t, b0 + r, z[0]);
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// 5 to 64 rows of x: weight rows read 64 bytes at a time, transposed in registers
+// ---------------------------------------------------------------------------
+// x in operand fragments: fragment (chunk of 512 k, step, 16 rows of x) is 1
+// KiB in lane order; lane (r, g) of step 4 j + s holds row r's k 512 c + 128 g
+// + 32 j + 8 s .. + 7.  Rows and k beyond x are zeros.
+__global__ __launch_bounds__(kThreads) void x_fragments_zero_fill(const uint16_t *x, int64_t ld_x,
+                                                                  int64_t m, int64_t k, int32_t tf,
+                                                                  int32_t frags, bool aligned,
+                                                                  uint16_t *out)
+{
+    const int lane = threadIdx.x & 63;
+    const int fr = blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6);
+    if (fr >= frags)
+        return;
+    const int step = fr / tf, t = fr - step * tf;
+    const int64_t row = t * 16 + (lane & 15);
+    const int64_t k0 = static_cast<int64_t>(step >> 4) * 512 + 128 * (lane >> 4) + 8 * (step & 15);
+    u32x4 q = {0, 0, 0, 0};
+    if (row < m && k0 < k) {
+        const uint16_t *from = x + row * ld_x + k0;
+        if (aligned) {
+            q = *reinterpret_cast<const u32x4 *>(from);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (k0 + j < k)
+                    q[j / 2] |= static_cast<uint32_t>(from[j]) << (16 * (j & 1));
+        }
+    }
+    *reinterpret_cast<u32x4 *>(out + (static_cast<int64_t>(fr) * 64 + lane) * 8) = q;
+}
+
+// Lane l of each quad exchanges register j for lane j's register l.
+__device__ __forceinline__ void transpose_quads(uint32_t (&v)[4], bool odd, bool high)
+{
+    const auto xor1 = [](uint32_t a) {
+        return static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(a), 0xB1, 0xF, 0xF, true));
+    };
+    const auto xor2 = [](uint32_t a) {
+        return static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(a), 0x4E, 0xF, 0xF, true));
+    };
+    // every lane makes every exchange; only then does it choose
+    const uint32_t x0 = xor1(v[0]), x1 = xor1(v[1]), x2 = xor1(v[2]), x3 = xor1(v[3]);
+    const uint32_t a0 = odd ? x1 : v[0], a1 = odd ? v[1] : x0;
+    const uint32_t a2 = odd ? x3 : v[2], a3 = odd ? v[3] : x2;
+    const uint32_t y0 = xor2(a0), y1 = xor2(a1), y2 = xor2(a2), y3 = xor2(a3);
+    v[0] = high ? y2 : a0;
+    v[1] = high ? y3 : a1;
+    v[2] = high ? a2 : y0;
+    v[3] = high ? a3 : y1;
+}
+
+// m <= 16 TF rows of x against the 4-bit weight, which is read once and never
+// written out.  A wave takes two fragments of 16 weight rows (gated: one of
+// each weight, the same columns) and chunks of 512 k.  The matrix instruction
+// wants neighbouring lanes in different weight rows, memory wants them side by
+// side (a load whose neighbouring lanes lie in 16 rows took 64 accesses of the
+// vector cache, this one 16): so a load takes 256 bytes of 4 rows, a quad of
+// lanes on 64 of them, and 4 such loads are transposed between the lanes of
+// each quad.  Waves along k (wk of them) meet in LDS, in a fixed order.  The
+// next chunk's loads, also those of the next row block, are in flight while a
+// chunk is multiplied; each x fragment is reloaded 4 steps ahead.
+// S: blocks looked up per lane and 128 k (2: blocks of 64 k or more and n_in
+// % 64 == 0; else 4).
+template <int OUT, bool kGated, int TF, int S>
+__global__ __launch_bounds__(512) void batch_rows_kernel(RowsArgs a, const uint16_t *x_frags, int wk_waves)
+{
+    constexpr int R = 2, kW = kGated ? 2 : 1;
+    constexpr int kPer = R / kW;
+    constexpr int kSpan = 512;
+    __shared__ __attribute__((aligned(1024))) uint8_t table[kPairTableBytes + 256];
+    __shared__ float scb[kW][256];
+    __shared__ __attribute__((aligned(16))) f32x4 partial[8][R * TF][64];
+
+    const int tid = threadIdx.x;
+    const int lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int WK = wk_waves, WR = 8 / WK;
+    const int wk = wave % WK, wr = wave / WK;
+    const int g = lane >> 4;
+    const int block_rows = 16 * kPer * WR;
+    const int lb = a.log2_block;
+    const uint32_t n_in = static_cast<uint32_t>(a.n_in);
+    const int chunks = static_cast<int>((n_in + kSpan - 1) / kSpan);
+    const bool odd = lane & 1, high = lane & 2;
+
+    struct Loads {
+        u32x4 packed[R][4];
+        uint32_t code[R][S];
+        float absmax[R][S];
+    };
+    const auto rsrc_of = [](const void *p, int64_t bytes) {
+        return __builtin_amdgcn_make_buffer_rsrc(
+            const_cast<void *>(p), 0, static_cast<int32_t>(bytes < 0x7FFFFFF0 ? bytes : 0x7FFFFFF0),
+            kRawBufferWord3);
+    };
+    const uint32_t k_load = 32 * (((lane >> 4) << 2) | (lane & 3));  // of the loaded piece
+    const uint32_t row_load = 4 * ((lane >> 2) & 3);
+    const int64_t blocks = (a.n_elems + (int64_t{1} << lb) - 1) >> lb;
+    auto load = [&](Loads &l, int64_t rb, int c) {
+        const int64_t row0 = rb * block_rows + wr * (16 * kPer);
+        const int64_t e0 = row0 * a.n_in;
+        const int64_t b0 = e0 >> lb;
+        const uint32_t phase = static_cast<uint32_t>(e0) & ((1u << lb) - 1);
+        const uint32_t group_phase = static_cast<uint32_t>(b0) & 255;
+        const int64_t packed_left = ((a.n_elems + 1) >> 1) - (e0 >> 1);
+        if (packed_left <= 0) {  // row waves past the last row
+#pragma unroll
+            for (int f = 0; f < R; ++f) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    l.packed[f][q] = u32x4{0, 0, 0, 0};
+#pragma unroll
+                for (int h = 0; h < S; ++h) {
+                    l.code[f][h] = 0;
+                    l.absmax[f][h] = 0.0f;
+                }
+            }
+            return;
+        }
+        const uint32_t k = c * kSpan + k_load;
+        const uint32_t past = k < n_in ? 0u : 0x80000000u;
+#pragma unroll
+        for (int f = 0; f < R; ++f) {
+            const int w = kGated ? f : 0;
+            const uint32_t frag_row = kGated ? 0 : f * 16;
+            const auto rp = rsrc_of(a.w[w].packed + (e0 >> 1), packed_left);
+            const auto rc = rsrc_of(a.w[w].scale_codes + b0, blocks - b0);
+            const auto rm = rsrc_of(a.w[w].nested_absmax + (b0 >> 8), (((blocks + 255) >> 8) - (b0 >> 8)) * 4);
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                l.packed[f][q] = __builtin_amdgcn_raw_buffer_load_b128(
+                    rp, (((frag_row + row_load + q) * n_in + k) >> 1) | past, 0, 0);
+#pragma unroll
+            for (int h = 0; h < S; ++h) {
+                const uint32_t e = (frag_row + (lane & 15)) * n_in + c * kSpan + 128 * g + h * (128 / S);
+                const uint32_t b = (phase + e) >> lb;
+                l.code[f][h] = __builtin_amdgcn_raw_buffer_load_b8(rc, b, 0, 0);
+                l.absmax[f][h] = __builtin_bit_cast(
+                    float, __builtin_amdgcn_raw_buffer_load_b32(rm, ((group_phase + b) >> 8) * 4, 0, 0));
+            }
+        }
+    };
+    u32x4 x[4][TF];
+    auto load_x = [&](int c, int step) {  // step in 0 .. 15 of chunk c
+#pragma unroll
+        for (int t = 0; t < TF; ++t)
+            x[step & 3][t] = *reinterpret_cast<const u32x4 *>(
+                x_frags + ((static_cast<int64_t>(c) * 16 + step) * TF + t) * 512 + lane * 8);
+    };
+
+    Loads cur;
+    int64_t load_rb = blockIdx.x;
+    int load_c = wk;  // wk < chunks: the host takes no more waves along k than chunks
+    load(cur, load_rb, load_c);
+#pragma unroll
+    for (int st = 0; st < 4; ++st)
+        load_x(load_c, st);
+
+    // the lookup tables, while the first loads are in flight
+#pragma unroll
+    for (int w = 0; w < kW; ++w)
+        if (tid < 256)
+            scb[w][tid] = a.w[w].scale_codebook[tid];
+    for (int i = tid; i < 256 * 32; i += 512) {
+        const int b = i >> 5;
+        const float *cb4 = a.w[kGated ? i & 1 : 0].codebook4;
+        *reinterpret_cast<f32x2 *>(&table[i * 8]) = f32x2{cb4[b & 15], cb4[b >> 4]};
+    }
+    if (tid < 64)
+        *reinterpret_cast<uint32_t *>(&table[kPairTableBytes + tid * 4]) = 0;
+    __syncthreads();
+
+    const uint32_t lane_byte = kGated ? (lane & 15) * 16 : (lane & 31) * 8;
+    for (int64_t rb = blockIdx.x; rb < a.row_blocks; rb += gridDim.x) {
+        f32x4 acc[R][TF];
+#pragma unroll
+        for (int f = 0; f < R; ++f)
+#pragma unroll
+            for (int t = 0; t < TF; ++t)
+                acc[f][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int c = wk; c < chunks; c += WK) {
+            // the following chunk, of this row block or the next one
+            load_c += WK;
+            if (load_c >= chunks) {
+                load_c = wk;
+                load_rb += gridDim.x;
+            }
+            Loads next;
+            if (load_rb < a.row_blocks)
+                load(next, load_rb, load_c);
+            else
+                next = cur;
+            float s[R][S];
+#pragma unroll
+            for (int f = 0; f < R; ++f) {
+#pragma unroll
+                for (int h = 0; h < S; ++h)
+                    s[f][h] = block_scale(scb[kGated ? f : 0][cur.code[f][h]], cur.absmax[f][h],
+                                          a.w[kGated ? f : 0].offset);
+#pragma unroll
+                for (int d = 0; d < 4; ++d) {
+                    uint32_t v[4] = {cur.packed[f][0][d], cur.packed[f][1][d], cur.packed[f][2][d],
+                                     cur.packed[f][3][d]};
+                    transpose_quads(v, odd, high);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        cur.packed[f][j][d] = v[j];
+                }
+            }
+            const uint32_t k = c * kSpan + 128 * g;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                // a piece beyond the row (its load gave zeros) reads the row
+                // of zeros behind the table, times 0
+                const bool beyond = k + 32 * j >= n_in;
+                const uint32_t from = beyond ? lane_byte | kPairTableBytes : lane_byte;
+                float sj[R];
+#pragma unroll
+                for (int f = 0; f < R; ++f)
+                    sj[f] = beyond ? 0.0f : s[f][j * S / 4];
+#pragma unroll
+                for (int st = 0; st < 4; ++st) {
+#pragma unroll
+                    for (int f = 0; f < R; ++f) {
+                        const u32x4 wf = decode_dword<OUT>(cur.packed[f][j][st], sj[f],
+                                                           table + (kGated ? f : 0) * 8, from);
+#pragma unroll
+                        for (int t = 0; t < TF; ++t)
+                            acc[f][t] = Half<OUT>::mfma(wf, x[st][t], acc[f][t]);
+                    }
+                    if (j < 3)
+                        load_x(c, 4 * j + st + 4);
+                    else
+                        load_x(load_c, st);  // after the last row block: unused
+                }
+            }
+            cur = next;
+        }
+        __syncthreads();  // the last row block's sums are read
+#pragma unroll
+        for (int f = 0; f < R; ++f)
+#pragma unroll
+            for (int t = 0; t < TF; ++t)
+                partial[wave][f * TF + t][lane] = acc[f][t];
+        __syncthreads();
+        for (int i = tid; i < WR * kPer * TF * 64; i += 512) {
+            const int ln = i & 63, ft = (i >> 6) % (kPer * TF), row_wave = (i >> 6) / (kPer * TF);
+            const int f = ft / TF, t = ft - f * TF;
+            f32x4 sum = partial[row_wave * WK][f * TF + t][ln];
+            for (int q = 1; q < WK; ++q)
+                sum = sum + partial[row_wave * WK + q][f * TF + t][ln];
+            const int64_t n0 = rb * block_rows + row_wave * (16 * kPer) + f * 16 + (ln >> 4) * 4;
+            const int64_t row = t * 16 + (ln & 15);
+            if constexpr (kGated) {
+                f32x4 up = partial[row_wave * WK][TF + t][ln];
+                for (int q = 1; q < WK; ++q)
+                    up = up + partial[row_wave * WK + q][TF + t][ln];
+                float gv[4] = {sum[0], sum[1], sum[2], sum[3]}, uv[4] = {up[0], up[1], up[2], up[3]};
+                finish_gated<OUT>(a.out, row, n0, gv, uv);
+            } else {
+                finish_linear4<OUT>(a.out, row, n0, sum);
             }
         }
     }
@@ -990,24 +1481,53 @@ int64_t workspace_need(const Shape &s, int64_t fixed, bool least)
     return fixed + groups * s.group_bytes();
 }
 
-constexpr int64_t kRowsMost = 64;  // rows of x that the decode-in-registers kernel takes
+// Which kernel a forward call takes.
+enum Route {
+    kTokenRoute,    // up to 4 rows of x
+    kBatchRoute,    // up to 64
+    kRaggedRoute,   // up to 64, weight rows of whole dwords that are not 32 k apart
+    kProductRoute   // decode to fragments, then the product
+};
 
-// Whether that kernel takes the call: rows of whole packed dwords, and few
-// rows of x.
-bool rows_route(const dq4_weight_t *w0, const dq4_weight_t *w1, int64_t n_in, int64_t m)
+constexpr int64_t kTokenMost = 4, kBatchMost = 64;
+
+Route route_of(const dq4_weight_t *w0, const dq4_weight_t *w1, int64_t n_in, int64_t m)
 {
-    return m <= kRowsMost && n_in > 0 && n_in % 8 == 0 &&
-           reinterpret_cast<uintptr_t>(w0->packed) % 4 == 0 &&
-           (!w1 || reinterpret_cast<uintptr_t>(w1->packed) % 4 == 0);
+    if (m > kBatchMost || n_in == 0 || n_in % 8 != 0 ||
+        reinterpret_cast<uintptr_t>(w0->packed) % 4 != 0 ||
+        (w1 && reinterpret_cast<uintptr_t>(w1->packed) % 4 != 0))
+        return kProductRoute;
+    if (n_in % 32 != 0)
+        return kRaggedRoute;
+    return m <= kTokenMost ? kTokenRoute : kBatchRoute;
 }
 
-// Workspace of a forward call: nothing but x's copy where the weight is
-// decoded in registers.
-int64_t forward_need(const Shape &s, const dq4_weight_t *w0, const dq4_weight_t *w1, int64_t n_in,
-                     bool copy, bool least)
+int x_row_frags(int64_t m)
+{
+    return m <= 16 ? 1 : m <= 32 ? 2 : 4;
+}
+
+// Whether a forward call needs x in 16-byte aligned rows and x is not (the
+// batch route lays x out in fragments, from any rows).
+bool forward_copies(const dq4_weight_t *w0, const dq4_weight_t *w1, const void *x, int64_t ld_x,
+                    int64_t m, int64_t n_in)
+{
+    return route_of(w0, w1, n_in, m) != kBatchRoute && needs_copy(x, ld_x, m, n_in);
+}
+
+// Workspace of a forward call.
+int64_t forward_need(const Shape &s, const dq4_weight_t *w0, const dq4_weight_t *w1, bool copy,
+                     bool least)
 {
     const int64_t fixed = copy_bytes(s, copy);
-    return rows_route(w0, w1, n_in, s.m) ? fixed : workspace_need(s, fixed, least);
+    switch (route_of(w0, w1, s.k, s.m)) {
+    case kProductRoute:
+        return workspace_need(s, fixed, least);
+    case kBatchRoute:
+        return ceil_div(s.k, 512) * 16 * x_row_frags(s.m) * kFragBytes;
+    default:
+        return fixed;
+    }
 }
 
 template <int OUT, bool kGated, int WN, int WT, int TF>
@@ -1030,36 +1550,111 @@ dq4_status_t launch_product(const ProductArgs &a, int cus, hipStream_t s)
     return launch_product_tile<OUT, kGated, 1, 4, 1>(a, s);
 }
 
-template <int OUT, bool kGated, int R, int TF, int WAVES, int WR, bool kWhole>
-dq4_status_t launch_rows_tile(RowsArgs a, int cus, hipStream_t s)
+template <int OUT, bool kGated, int R, int TF, int WAVES>
+dq4_status_t launch_ragged_tile(RowsArgs a, int cus, hipStream_t s)
 {
-    const int64_t block_rows = 16 * (kGated ? R / 2 : R) * WR;
-    a.row_blocks = static_cast<int32_t>(ceil_div(a.n_out, block_rows));
+    a.row_blocks = static_cast<int32_t>(ceil_div(a.n_out, 16 * (kGated ? R / 2 : R)));
     void *params[] = {&a};
-    return launch(reinterpret_cast<const void *>(&weight_rows_kernel<OUT, kGated, R, TF, WAVES, WR, kWhole>),
+    return launch(reinterpret_cast<const void *>(&ragged_rows_kernel<OUT, kGated, R, TF, WAVES>),
                   a.row_blocks < cus ? a.row_blocks : cus, 1, 64 * WAVES, params, s);
 }
 
-template <int OUT, bool kGated, bool kWhole>
-dq4_status_t launch_rows(const RowsArgs &a, int cus, hipStream_t s)
+template <int OUT, bool kGated>
+dq4_status_t launch_ragged(const RowsArgs &a, int cus, hipStream_t s)
 {
-    const int64_t frags = ceil_div(a.n_out, 16);
-    if (a.out.m <= 16) {
-        if constexpr (kGated) {
-            if (frags <= 2 * cus)
-                return launch_rows_tile<OUT, true, 2, 1, 8, 1, kWhole>(a, cus, s);
-            return launch_rows_tile<OUT, true, 4, 1, 8, 1, kWhole>(a, cus, s);
-        } else {
-            if (frags <= cus)
-                return launch_rows_tile<OUT, false, 1, 1, 16, 1, kWhole>(a, cus, s);
-            if (frags <= 2 * cus || !kWhole)
-                return launch_rows_tile<OUT, false, 2, 1, 16, 1, kWhole>(a, cus, s);
-            return launch_rows_tile<OUT, false, kWhole ? 4 : 2, 1, 16, 1, kWhole>(a, cus, s);
+    if (a.out.m > 32)
+        return launch_ragged_tile<OUT, kGated, 2, 4, 8>(a, cus, s);
+    if (a.out.m > 16)
+        return launch_ragged_tile<OUT, kGated, kGated ? 4 : 2, 2, 8>(a, cus, s);
+    if constexpr (!kGated)
+        if (ceil_div(a.n_out, 16) <= cus)
+            return launch_ragged_tile<OUT, false, 1, 1, 16>(a, cus, s);
+    return launch_ragged_tile<OUT, kGated, 2, 1, kGated ? 8 : 16>(a, cus, s);
+}
+
+template <int OUT, bool kGated, int M>
+dq4_status_t launch_token_rows(const RowsArgs &r, int cus, hipStream_t s)
+{
+    // a wave's registers hold x's chunk and the rows in flight
+    constexpr int kWaves = M == 4 ? 8 : 16;
+    const int64_t chunks = ceil_div(r.n_in, kTokenSpan);
+    const int64_t passes = ceil_div(chunks, kWaves);
+    TokenArgs a{};
+    a.w[0] = r.w[0];
+    a.w[1] = r.w[1];
+    a.n_in = r.n_in;
+    a.n_elems = r.n_elems;
+    a.log2_block = r.log2_block;
+    a.wk = static_cast<int32_t>(ceil_div(chunks, passes));
+    const int wr = kWaves / a.wk;
+    const int ring = kTokenDepth * wr;  // rows of one turn of every wave's ring
+    const int fit = kTokenPartials<kGated> / 2 / (M * (kGated ? 2 : 1) * a.wk * 4);
+    a.batch = fit / ring * ring;
+    a.out = r.out;
+    void *params[] = {&a};
+    return launch(reinterpret_cast<const void *>(&token_rows_kernel<OUT, kGated, M, kWaves>),
+                  r.n_out < cus ? r.n_out : cus, 1, 64 * a.wk * wr, params, s);
+}
+
+template <int OUT, bool kGated, int TF>
+dq4_status_t launch_batch_rows(RowsArgs a, const uint16_t *x_frags, int cus, hipStream_t s)
+{
+    // waves along k: as many rounds of row blocks as fit the GPU, each as long
+    // as its chunks per wave plus about one for the sums' meeting
+    const int64_t tasks = ceil_div(a.n_out, kGated ? 16 : 32), chunks = ceil_div(a.n_in, 512);
+    int best = 1;
+    int64_t least = INT64_MAX;
+    for (int wk = 1; wk <= 8 && wk <= chunks; wk *= 2) {
+        const int64_t row_blocks = ceil_div(tasks, 8 / wk);
+        const int64_t cost = ceil_div(row_blocks, cus) * (ceil_div(chunks, wk) + 1);
+        if (cost < least) {
+            least = cost;
+            best = wk;
         }
     }
-    if (a.out.m <= 32)
-        return launch_rows_tile<OUT, kGated, 4, 2, 8, 1, kWhole>(a, cus, s);
-    return launch_rows_tile<OUT, kGated, !kGated && kWhole ? 4 : 2, 4, 8, 1, kWhole>(a, cus, s);
+    a.row_blocks = static_cast<int32_t>(ceil_div(tasks, 8 / best));
+    void *params[] = {&a, &x_frags, &best};
+    const void *kernel = a.log2_block >= 6 && a.n_in % 64 == 0
+                             ? reinterpret_cast<const void *>(&batch_rows_kernel<OUT, kGated, TF, 2>)
+                             : reinterpret_cast<const void *>(&batch_rows_kernel<OUT, kGated, TF, 4>);
+    return launch(kernel, a.row_blocks < cus ? a.row_blocks : cus, 1, 512, params, s);
+}
+
+template <int OUT, bool kGated>
+dq4_status_t launch_batch(const RowsArgs &a, uint8_t *workspace, int cus, hipStream_t s)
+{
+    const uint16_t *x = a.out.x[0];
+    int64_t ld = a.out.ld_x, m = a.out.m, k = a.n_in;
+    int32_t tf = x_row_frags(m);
+    int32_t frags = static_cast<int32_t>(ceil_div(k, 512) * 16 * tf);
+    bool aligned = rows_aligned(x, ld, m, k);
+    uint16_t *out = reinterpret_cast<uint16_t *>(workspace);
+    void *params[] = {&x, &ld, &m, &k, &tf, &frags, &aligned, &out};
+    const dq4_status_t st = launch(reinterpret_cast<const void *>(&x_fragments_zero_fill),
+                                   ceil_div(frags, kThreads / 64), 1, kThreads, params, s);
+    if (st != DQ4_OK)
+        return st;
+    if (tf == 1)
+        return launch_batch_rows<OUT, kGated, 1>(a, out, cus, s);
+    if (tf == 2)
+        return launch_batch_rows<OUT, kGated, 2>(a, out, cus, s);
+    return launch_batch_rows<OUT, kGated, 4>(a, out, cus, s);
+}
+
+// Up to 64 rows of x, by one of the kernels that read the 4-bit weight once.
+template <int OUT, bool kGated>
+dq4_status_t launch_few_rows(const RowsArgs &a, Route route, uint8_t *workspace, int cus,
+                             hipStream_t s)
+{
+    if (route == kRaggedRoute)
+        return launch_ragged<OUT, kGated>(a, cus, s);
+    if (route == kBatchRoute)
+        return launch_batch<OUT, kGated>(a, workspace, cus, s);
+    if (a.out.m == 1)
+        return launch_token_rows<OUT, kGated, 1>(a, cus, s);
+    if (a.out.m == 2)
+        return launch_token_rows<OUT, kGated, 2>(a, cus, s);
+    return launch_token_rows<OUT, kGated, 4>(a, cus, s);
 }
 
 template <int OUT, bool kForward>
@@ -1094,7 +1689,8 @@ dq4_status_t run_product(const Shape &sh, const dq4_weight_t *w0, const dq4_weig
     p.m = sh.m;
     p.n = sh.n;
     if constexpr (kForward) {
-        if (rows_route(w0, w1, n_in, sh.m)) {
+        const Route route = route_of(w0, w1, n_in, sh.m);
+        if (route != kProductRoute) {
             RowsArgs r{};
             r.w[0] = device_weight(*w0);
             r.w[1] = device_weight(w1 ? *w1 : *w0);
@@ -1103,11 +1699,8 @@ dq4_status_t run_product(const Shape &sh, const dq4_weight_t *w0, const dq4_weig
             r.n_elems = n_out * n_in;
             r.log2_block = log2_block;
             r.out = p;
-            if (n_in % 32 == 0)
-                return w1 ? launch_rows<OUT, true, true>(r, cus, s)
-                          : launch_rows<OUT, false, true>(r, cus, s);
-            return w1 ? launch_rows<OUT, true, false>(r, cus, s)
-                      : launch_rows<OUT, false, false>(r, cus, s);
+            return w1 ? launch_few_rows<OUT, true>(r, route, fragments, cus, s)
+                      : launch_few_rows<OUT, false>(r, route, fragments, cus, s);
         }
     }
     const int64_t groups = sh.groups();
@@ -1214,7 +1807,7 @@ int64_t dq4_linear_fused_workspace_bytes(const dq4_weight_t *w, int64_t n_out, i
     if (!w || !sizes_ok(n_out, n_in, m))
         return 0;
     const Shape s{m, n_out, n_in, kSingle};
-    return forward_need(s, w, nullptr, n_in, needs_copy(x, ld_x, m, n_in), least != 0);
+    return forward_need(s, w, nullptr, forward_copies(w, nullptr, x, ld_x, m, n_in), least != 0);
 }
 
 int64_t dq4_gated_fused_workspace_bytes(const dq4_weight_t *gate, const dq4_weight_t *up,
@@ -1224,7 +1817,7 @@ int64_t dq4_gated_fused_workspace_bytes(const dq4_weight_t *gate, const dq4_weig
     if (!gate || !up || !sizes_ok(n_ff, n_in, m))
         return 0;
     const Shape s{m, n_ff, n_in, kSideBySide};
-    return forward_need(s, gate, up, n_in, needs_copy(x, ld_x, m, n_in), least != 0);
+    return forward_need(s, gate, up, forward_copies(gate, up, x, ld_x, m, n_in), least != 0);
 }
 
 int64_t dq4_linear_fused_backward_workspace_bytes(const dq4_weight_t *w, int64_t n_out,
@@ -1269,9 +1862,9 @@ dq4_status_t dq4_linear_fused(const dq4_weight_t *w, int64_t n_out, int64_t n_in
         (pre && bad_ld(ld_pre, m, n_out)))
         return DQ4_EINVAL;
     const Shape sh{m, n_out, n_in, kSingle};
-    const bool copy = needs_copy(x, ld_x, m, n_in);
+    const bool copy = forward_copies(w, nullptr, x, ld_x, m, n_in);
     const int64_t fixed = copy_bytes(sh, copy);
-    if (workspace_bytes < forward_need(sh, w, nullptr, n_in, copy, true) ||
+    if (workspace_bytes < forward_need(sh, w, nullptr, copy, true) ||
         (workspace_bytes > 0 && !workspace))
         return DQ4_EINVAL;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
@@ -1324,9 +1917,9 @@ dq4_status_t dq4_gated_fused(const dq4_weight_t *gate, const dq4_weight_t *up, i
     if (bad_ld(ld_x, m, n_in) || bad_ld(ld_h, m, n_ff) || (gate_pre && bad_ld(ld_pre, m, n_ff)))
         return DQ4_EINVAL;
     const Shape sh{m, n_ff, n_in, kSideBySide};
-    const bool copy = needs_copy(x, ld_x, m, n_in);
+    const bool copy = forward_copies(gate, up, x, ld_x, m, n_in);
     const int64_t fixed = copy_bytes(sh, copy);
-    if (workspace_bytes < forward_need(sh, gate, up, n_in, copy, true) ||
+    if (workspace_bytes < forward_need(sh, gate, up, copy, true) ||
         (workspace_bytes > 0 && !workspace))
         return DQ4_EINVAL;
     uint8_t *ws = static_cast<uint8_t *>(workspace);

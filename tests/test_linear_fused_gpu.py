@@ -49,6 +49,18 @@ SHAPES = [
     (64, 256, 1024, 4096, "fp4"), (65, 257, 1025, 64, "nf4"), (150, 1001, 1377, 128, "nf4"),
     (256, 512, 512, 64, "nf4"), (257, 640, 520, 32, "fp4"), (300, 1536, 1000, 64, "nf4"),
     (1100, 2176, 352, 64, "nf4"),
+    # one to four rows: chunks of 2048 k met, missed and more than the waves;
+    # more weight rows than one pass through LDS
+    (1, 300, 2048, 64, "nf4"), (2, 70, 2080, 32, "nf4"), (3, 20, 34016, 4096, "fp4"),
+    (4, 530, 4128, 64, "nf4"), (1, 9000, 32, 32, "fp4"), (2, 20000, 96, 32, "nf4"),
+    (4, 6, 66560, 128, "nf4"), (1, 5, 66560, 64, "nf4"), (3, 257, 6176, 1024, "nf4"),
+    # five to 64: chunks of 512 k, rows and columns past the last fragment, more
+    # row blocks than workgroups
+    (5, 33, 512, 64, "nf4"), (16, 47, 544, 32, "fp4"), (17, 8200, 160, 64, "nf4"),
+    (31, 100, 1056, 4096, "nf4"), (33, 4100, 640, 128, "fp4"), (64, 31, 4608, 64, "nf4"),
+    (48, 17, 32, 32, "nf4"), (8, 300, 2080, 256, "nf4"),
+    # ... with rows of whole dwords only
+    (3, 50, 2056, 32, "nf4"), (40, 4200, 168, 64, "nf4"), (20, 90, 1000, 4096, "fp4"),
 ]
 
 
@@ -165,7 +177,8 @@ def untouched(big, view_shape, left, fill):
 
 
 @pytest.mark.parametrize("left,right", [(0, 8), (1, 0), (8, 16), (3, 4)])
-@pytest.mark.parametrize("m,n_out,n_in", [(1, 264, 512), (5, 264, 512), (33, 264, 520), (130, 200, 1001)])
+@pytest.mark.parametrize("m,n_out,n_in", [(1, 264, 512), (5, 264, 512), (3, 264, 2080), (33, 264, 520),
+                                          (64, 264, 544), (130, 200, 1001)])
 def test_strided_matrices(m, n_out, n_in, left, right):
     """Every matrix inside a larger buffer: NaN around the inputs, a mark around
     the outputs; the results equal the dense call's bit for bit."""
@@ -225,7 +238,7 @@ def test_strided_matrices(m, n_out, n_in, left, right):
     untouched(big_x, (m, n_in), left, mark)
 
 
-@pytest.mark.parametrize("m,n_out,n_in", [(3, 700, 515), (3, 768, 512), (200, 768, 512)])
+@pytest.mark.parametrize("m,n_out,n_in", [(3, 700, 515), (3, 768, 512), (20, 768, 512), (200, 768, 512)])
 def test_any_workspace_gives_the_same_bits(m, n_out, n_in):
     """The least workspace (windows of output columns), one in between, and
     one full of NaN."""
@@ -293,12 +306,35 @@ def test_unaligned_codes_and_single_row_strides():
                                                                 x=x[:1].contiguous())), "single row")
 
 
+@pytest.mark.parametrize("m,n_in", [(2, 2080), (4, 96), (20, 544), (20, 520), (90, 96)])
+def test_values_that_no_code_uses(m, n_in):
+    """Infinities and NaN in the codebooks reach the elements whose codes name
+    them, and nothing that lies beyond a row or in the padding."""
+    rng = np.random.Generator(np.random.PCG64(23))
+    host, w = make_weight(48, n_in, seed=20)
+    # code 0 (what a load beyond the weight gives) and scale code 0 are unused
+    packed = torch.where((w["packed"] & 15) == 0, w["packed"] | 1, w["packed"])
+    packed = torch.where((packed >> 4) == 0, packed | 16, packed)
+    codes = torch.clamp(w["scale_codes"], min=1)
+    plain = dict(w, packed=packed, scale_codes=codes)
+    bad = dict(plain, codebook4=w["codebook4"].clone(), scale_codebook=w["scale_codebook"].clone())
+    bad["codebook4"][0] = float("inf")
+    bad["scale_codebook"][0] = float("nan")
+    x = normal(rng, (m, n_in), "bf16")
+    dy = normal(rng, (m, 48), "bf16")
+    for a, b in ((dq4.dq4_linear_fused(**t, n_out=48, n_in=n_in, blocksize=64, x=x) for t in (plain, bad)),
+                 (dq4.dq4_gated_fused(t, t, 48, n_in, 64, x) for t in (plain, bad)),
+                 (dq4.dq4_linear_fused_backward(**t, n_out=48, n_in=n_in, blocksize=64, dy=dy)[0]
+                  for t in (plain, bad))):
+        assert_bits_equal(bits_of(b), bits_of(a), "unused codebook entries")
+
+
 def test_rows_do_not_mix():
     """A row of NaN or infinities reaches its own outputs only."""
     rng = np.random.Generator(np.random.PCG64(22))
     _, w = make_weight(300, 520, seed=15)
     _, up = make_weight(300, 520, seed=16)
-    for m in (6, 90):
+    for m in (6, 40, 90):
         x = normal(rng, (m, 520), "bf16")
         bad = x.clone()
         bad[2] = float("nan")
