@@ -575,19 +575,45 @@ struct RowsArgs {
 // 4.4, a single table 26).
 constexpr int kPairTableBytes = 256 * 32 * 8;
 
-template <int OUT>
-__device__ __forceinline__ u32x4 decode_dword(uint32_t word, float s, const uint8_t *table,
+struct Pairs {
+    f32x2 v[4];  // the eight codebook values of a packed dword
+};
+
+__device__ __forceinline__ Pairs lookup_dword(uint32_t word, const uint8_t *table,
                                               uint32_t lane_byte)
 {
-    u32x4 q;
+    Pairs p;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         // lane_byte with the word's byte j as its byte 1
         const uint32_t at = __builtin_amdgcn_perm(word, lane_byte, 0x03020000u | ((4u + j) << 8));
-        const f32x2 pair = *reinterpret_cast<const f32x2 *>(table + at);
-        q[j] = Half<OUT>::pack2(pair[0] * s, pair[1] * s);
+        p.v[j] = *reinterpret_cast<const f32x2 *>(table + at);
     }
+    return p;
+}
+
+template <int OUT>
+__device__ __forceinline__ u32x4 scaled_dword(const Pairs &p, float s)
+{
+    u32x4 q;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        q[j] = Half<OUT>::pack2(p.v[j][0] * s, p.v[j][1] * s);
     return q;
+}
+
+template <int OUT>
+__device__ __forceinline__ u32x4 decode_dword(uint32_t word, float s, const uint8_t *table,
+                                              uint32_t lane_byte)
+{
+    return scaled_dword<OUT>(lookup_dword(word, table, lane_byte), s);
+}
+
+// The lookups before this line are issued before what follows it: left to
+// itself the compiler waits for each lookup where it is used.
+__device__ __forceinline__ void keep_order()
+{
+    __builtin_amdgcn_sched_barrier(0);
 }
 
 // Output row r of the linear call's columns n0 .. n0 + 3.
@@ -842,15 +868,21 @@ __global__ __launch_bounds__(64 * WAVES) void ragged_rows_kernel(RowsArgs a)
 struct TokenArgs {
     Weight w[2];
     int64_t n_in;
-    int64_t n_elems;
     int32_t log2_block;
+    int32_t chunks;             // of 2048 k
     int32_t wk;                 // waves along k
+    int32_t rows_per, rows_extra;  // weight rows of a workgroup; the first ones take one more
     int32_t batch;              // weight rows per pass through LDS
     ProductArgs out;
 };
 
-constexpr int kTokenSpan = 2048;  // k per wave and chunk
-constexpr int kTokenDepth = 4;    // rows in flight per wave
+constexpr int kTokenSpan = 2048;   // k per wave and chunk
+constexpr int kTokenDepth = 3;     // pairs of row chunks in flight per wave
+constexpr int kTokenMaxChunks = 16;
+
+// Weight rows of one turn of a wave's ring.
+template <bool kGated>
+constexpr int kTokenRing = kTokenDepth * (kGated ? 1 : 2);
 
 template <int OUT>
 __device__ __forceinline__ void finish_one(const ProductArgs &a, int64_t row, int64_t n, float z)
@@ -867,15 +899,17 @@ __device__ __forceinline__ void finish_one(const ProductArgs &a, int64_t row, in
 
 // Floats of partial sums: what the tables leave of the LDS.
 template <bool kGated>
-constexpr int kTokenPartials = kGated ? 6144 : 8192;
+constexpr int kTokenPartials = kGated ? 6144 : 12288;
 
 template <int OUT, bool kGated, int M, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void token_rows_kernel(TokenArgs a)
 {
     constexpr int kW = kGated ? 2 : 1;
-    __shared__ __attribute__((aligned(1024))) uint8_t table[kW][kPairTableBytes + 256];
+    constexpr int kRows = kGated ? 1 : 2;  // weight rows of a pair of row chunks
+    __shared__ __attribute__((aligned(1024))) uint8_t table[kW * kPairTableBytes + 256];
     __shared__ float scb[kW][256];
     __shared__ __attribute__((aligned(16))) float partial[2][kTokenPartials<kGated> / 2];
+    __shared__ float unused[64];
 
     const int tid = threadIdx.x;
     const int threads = blockDim.x;
@@ -885,44 +919,47 @@ __global__ __launch_bounds__(64 * WAVES) void token_rows_kernel(TokenArgs a)
     const int wk = wave % WK, wr = wave / WK;
     const int lb = a.log2_block;
     const uint32_t n_in = static_cast<uint32_t>(a.n_in);
-    const int chunks = static_cast<int>((n_in + kTokenSpan - 1) / kTokenSpan);
+    const int chunks = a.chunks;
     const int passes = (chunks + WK - 1) / WK;
 
-    // this workgroup's rows, in batches
-    const int64_t row_first = a.out.n * blockIdx.x / gridDim.x;
-    const int64_t row_last = a.out.n * (blockIdx.x + 1) / gridDim.x;
-    int64_t limit = row_last;
+    // this workgroup's weight rows
+    const int block = blockIdx.x;
+    const int row_first = block * a.rows_per + (block < a.rows_extra ? block : a.rows_extra);
+    const int row_last = row_first + a.rows_per + (block < a.rows_extra ? 1 : 0);
 
     struct Row {
         u32x4 packed;
         uint32_t code;
         float absmax;
     };
-    Row ring[kTokenDepth][kW];
+    Row ring[kTokenDepth][2];  // gated: a row of each weight; else two rows
     u32x4 x[M][4];
     uint32_t k_lane = 0, packed_off = 0;
-    auto load = [&](Row (&to)[kW], int64_t row) {
-        row = row < limit ? row : limit - 1;  // loaded again, unused
+    auto load_one = [&](Row &to, int w, int row) {
+        row = row < row_last ? row : row_last - 1;  // loaded again, unused
         const int64_t e0 = row * a.n_in;
         const int64_t b0 = e0 >> lb;
         const uint32_t phase = static_cast<uint32_t>(e0) & ((1u << lb) - 1);
         const uint32_t b = (phase + k_lane) >> lb;
         const uint32_t gr = ((static_cast<uint32_t>(b0) & 255) + b) >> 8;
+        const auto rsrc = [](const void *p) {
+            return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, 0x7FFFFFFF,
+                                                     kRawBufferWord3);
+        };
+        // lanes beyond the row: an offset past every buffer, zeros
+        const uint32_t past = packed_off & 0x80000000u;
+        to.packed = __builtin_amdgcn_raw_buffer_load_b128(rsrc(a.w[w].packed + (e0 >> 1)), packed_off,
+                                                          0, 0);
+        to.code = __builtin_amdgcn_raw_buffer_load_b8(rsrc(a.w[w].scale_codes + b0), b | past, 0, 0);
+        to.absmax = __builtin_bit_cast(
+            float, __builtin_amdgcn_raw_buffer_load_b32(rsrc(a.w[w].nested_absmax + (b0 >> 8)),
+                                                        (gr * 4) | past, 0, 0));
+    };
+    // pair i of this wave's rows from `row0` on
+    auto load = [&](Row (&to)[2], int row0, int i) {
 #pragma unroll
-        for (int w = 0; w < kW; ++w) {
-            const auto rsrc = [](const void *p) {
-                return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, 0x7FFFFFFF,
-                                                         kRawBufferWord3);
-            };
-            // lanes beyond the row: an offset past every buffer, zeros
-            const uint32_t past = packed_off & 0x80000000u;
-            to[w].packed = __builtin_amdgcn_raw_buffer_load_b128(rsrc(a.w[w].packed + (e0 >> 1)),
-                                                                 packed_off, 0, 0);
-            to[w].code = __builtin_amdgcn_raw_buffer_load_b8(rsrc(a.w[w].scale_codes + b0), b | past, 0, 0);
-            to[w].absmax = __builtin_bit_cast(
-                float, __builtin_amdgcn_raw_buffer_load_b32(rsrc(a.w[w].nested_absmax + (b0 >> 8)),
-                                                            (gr * 4) | past, 0, 0));
-        }
+        for (int j = 0; j < 2; ++j)
+            load_one(to[j], kGated ? j : 0, row0 + (i * kRows + (kGated ? 0 : j)) * WR + wr);
     };
     auto enter_chunk = [&](int chunk) {
         k_lane = chunk * kTokenSpan + 32 * lane;
@@ -938,112 +975,135 @@ __global__ __launch_bounds__(64 * WAVES) void token_rows_kernel(TokenArgs a)
     };
 
     // the first rows' loads go out before the tables are built
-    int64_t b0 = row_first;
-    if (wk < chunks) {
-        enter_chunk(wk);
+    enter_chunk(wk);
 #pragma unroll
-        for (int d = 0; d < kTokenDepth; ++d)
-            load(ring[d], b0 + wr + d * WR);
-    }
+    for (int d = 0; d < kTokenDepth; ++d)
+        load(ring[d], row_first, d);
 #pragma unroll
     for (int w = 0; w < kW; ++w) {
         if (tid < 256)
             scb[w][tid] = a.w[w].scale_codebook[tid];
         for (int i = tid; i < 256 * 32; i += threads) {
             const int b = i >> 5;
-            *reinterpret_cast<f32x2 *>(&table[w][i * 8]) =
+            *reinterpret_cast<f32x2 *>(&table[w * kPairTableBytes + i * 8]) =
                 f32x2{a.w[w].codebook4[b & 15], a.w[w].codebook4[b >> 4]};
         }
-        if (tid < 64)
-            *reinterpret_cast<uint32_t *>(&table[w][kPairTableBytes + tid * 4]) = 0;
     }
+    if (tid < 64)
+        *reinterpret_cast<uint32_t *>(&table[kW * kPairTableBytes + tid * 4]) = 0;
     __syncthreads();
 
     const uint32_t lane_byte = (lane & 31) * 8;
     const int G = lane >> 4, c = lane & 15;
-    const bool diagonal = G == (c >> 2);
+    const bool writer = G == (c >> 2) && (c & 3) == 0;
     int parity = 0;
-    for (; b0 < row_last; b0 += a.batch, parity ^= 1) {
-        const int rows = static_cast<int>(row_last - b0 < a.batch ? row_last - b0 : a.batch);
+    for (int b0 = row_first; b0 < row_last; b0 += a.batch, parity ^= 1) {
+        const int rows = row_last - b0 < a.batch ? row_last - b0 : a.batch;
         float *part = partial[parity];
-        if (passes > 1)
-            limit = b0 + rows;
         for (int pass = 0; pass < passes; ++pass) {
             const int chunk = wk + pass * WK;
             if (chunk >= chunks)
                 break;
-            if (pass > 0 || (passes > 1 && b0 != row_first)) {  // else the ring is filled
+            if (passes > 1 && (pass > 0 || b0 != row_first)) {  // else the ring is filled
                 enter_chunk(chunk);
 #pragma unroll
                 for (int d = 0; d < kTokenDepth; ++d)
-                    load(ring[d], b0 + wr + d * WR);
+                    load(ring[d], b0, d);
             }
             // a lane beyond the row (its loads gave zeros) reads the row of
-            // zeros behind the table, times 0
+            // zeros behind the tables, times 0
             const bool beyond = k_lane >= n_in;
-            const uint32_t from = beyond ? lane_byte | kPairTableBytes : lane_byte;
-            for (int r0 = wr; r0 < rows; r0 += kTokenDepth * WR) {
+            uint32_t from[kW];
+#pragma unroll
+            for (int w = 0; w < kW; ++w)
+                from[w] = lane_byte + (beyond ? kW * kPairTableBytes : w * kPairTableBytes);
+            for (int i0 = 0; i0 * kRows * WR + wr < rows; i0 += kTokenDepth) {
 #pragma unroll
                 for (int d = 0; d < kTokenDepth; ++d) {
-                    const int r = r0 + d * WR;
-                    if (r >= rows)
-                        break;
+                    const int i = i0 + d;
+                    // a turn loads as often past the last row: were the number
+                    // of loads in flight not known, every turn would begin by
+                    // waiting for all of them
+                    if (i * kRows * WR + wr < rows) {
+                        float s[2];
+                        f32x4 acc[2][M];
+                        Pairs now[2], next[2];
 #pragma unroll
-                    for (int w = 0; w < kW; ++w) {
-                        float s = block_scale(scb[w][ring[d][w].code], ring[d][w].absmax, a.w[w].offset);
-                        s = beyond ? 0.0f : s;
-                        f32x4 acc[M];
-#pragma unroll
-                        for (int st = 0; st < 4; ++st) {
-                            const u32x4 wf = decode_dword<OUT>(ring[d][w].packed[st], s, table[w], from);
-#pragma unroll
-                            for (int t = 0; t < M; ++t)
-                                acc[t] = Half<OUT>::mfma(wf, x[t][st],
-                                                         st == 0 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f} : acc[t]);
+                        for (int j = 0; j < 2; ++j) {
+                            const int w = kGated ? j : 0;
+                            now[j] = lookup_dword(ring[d][j].packed[0], table, from[w]);
+                            s[j] = block_scale(scb[w][ring[d][j].code], ring[d][j].absmax, a.w[w].offset);
+                            s[j] = beyond ? 0.0f : s[j];
                         }
 #pragma unroll
-                        for (int t = 0; t < M; ++t) {
-                            // the diagonal value of this lane's column, its quad's sum
-                            float v = (c & 2) ? ((c & 1) ? acc[t][3] : acc[t][2])
-                                              : ((c & 1) ? acc[t][1] : acc[t][0]);
-                            v = v + __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), 0xB1, 0xF, 0xF, true));
-                            v = v + __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), 0x4E, 0xF, 0xF, true));
-                            float *to = part + (((r * M + t) * kW + w) * WK + wk) * 4 + G;
-                            if (diagonal && (c & 3) == 0)
-                                *to = pass == 0 ? v : *to + v;
+                        for (int st = 0; st < 4; ++st) {
+                            if (st < 3) {
+#pragma unroll
+                                for (int j = 0; j < 2; ++j)
+                                    next[j] = lookup_dword(ring[d][j].packed[st + 1], table, from[kGated ? j : 0]);
+                            }
+                            keep_order();
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                const u32x4 wf = scaled_dword<OUT>(now[j], s[j]);
+#pragma unroll
+                                for (int t = 0; t < M; ++t)
+                                    acc[j][t] = Half<OUT>::mfma(wf, x[t][st],
+                                                                st == 0 ? f32x4{0.0f, 0.0f, 0.0f, 0.0f}
+                                                                        : acc[j][t]);
+                                now[j] = next[j];
+                            }
+                        }
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const int r = (i * kRows + (kGated ? 0 : j)) * WR + wr;
+#pragma unroll
+                            for (int t = 0; t < M; ++t) {
+                                // the diagonal value of this lane's column, its quad's sum
+                                const f32x4 q = acc[j][t];
+                                const float lo = (c & 1) ? q[1] : q[0], hi = (c & 1) ? q[3] : q[2];
+                                float v = (c & 2) ? hi : lo;
+                                v = v + __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), 0xB1, 0xF, 0xF, true));
+                                v = v + __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), 0x4E, 0xF, 0xF, true));
+                                // no branch: other lanes and rows past the end
+                                // write where nothing is read
+                                float *to = part + (((r * M + t) * kW + (kGated ? j : 0)) * chunks + chunk) * 4 + G;
+                                *(writer && r < rows ? to : &unused[lane]) = v;
+                            }
                         }
                     }
                     // batches are whole rings long: with one pass the ring
                     // runs on into the next batch
-                    load(ring[d], b0 + r + kTokenDepth * WR);
+                    load(ring[d], b0, i + kTokenDepth);
                 }
             }
         }
         __syncthreads();
         for (int i = tid; i < rows * M; i += threads) {
-            const int t = i / rows, r = i - t * rows;
+            const int r = i / M, t = i % M;
             if (t >= a.out.m)
-                break;
+                continue;
             float z[kW];
 #pragma unroll
             for (int w = 0; w < kW; ++w) {
-                const float *from = part + ((r * M + t) * kW + w) * WK * 4;
+                const float *from = part + ((r * M + t) * kW + w) * chunks * 4;
                 float sum = 0.0f;
-                for (int q = 0; q < WK; ++q) {
+                for (int q = 0; q < chunks; ++q) {
                     const f32x4 v = *reinterpret_cast<const f32x4 *>(from + 4 * q);
                     sum = sum + ((v[0] + v[1]) + (v[2] + v[3]));
                 }
                 z[w] = sum;
             }
+            const int64_t n = b0 + r;
             if constexpr (kGated) {
                 if (a.out.pre[0]) {
-                    a.out.pre[0][t * a.out.ld_pre + b0 + r] = static_cast<uint16_t>(Half<OUT>::pack2(z[0], 0.0f));
-                    a.out.pre[1][t * a.out.ld_pre + b0 + r] = static_cast<uint16_t>(Half<OUT>::pack2(z[1], 0.0f));
+                    a.out.pre[0][t * a.out.ld_pre + n] = static_cast<uint16_t>(Half<OUT>::pack2(z[0], 0.0f));
+                    a.out.pre[1][t * a.out.ld_pre + n] = static_cast<uint16_t>(Half<OUT>::pack2(z[1], 0.0f));
                 }
-                a.out.y[t * a.out.ld_y + b0 + r] =
+                a.out.y[t * a.out.ld_y + n] =
                     static_cast<uint16_t>(Half<OUT>::pack2(act_f32(a.out.act, z[0]) * z[1], 0.0f));
             } else {
-                finish_one<OUT>(a.out, t, b0 + r, z[0]);
+                finish_one<OUT>(a.out, t, n, z[0]);
             }
         }
     }
@@ -1261,31 +1321,47 @@ __global__ __launch_bounds__(512) void batch_rows_kernel(RowsArgs a, const uint1
                 }
             }
             const uint32_t k = c * kSpan + 128 * g;
+            uint32_t from[4];
+            float sj[4][R];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 // a piece beyond the row (its load gave zeros) reads the row
                 // of zeros behind the table, times 0
                 const bool beyond = k + 32 * j >= n_in;
-                const uint32_t from = beyond ? lane_byte | kPairTableBytes : lane_byte;
-                float sj[R];
+                from[j] = beyond ? lane_byte | kPairTableBytes : lane_byte;
 #pragma unroll
                 for (int f = 0; f < R; ++f)
-                    sj[f] = beyond ? 0.0f : s[f][j * S / 4];
+                    sj[j][f] = beyond ? 0.0f : s[f][j * S / 4];
+            }
+            Pairs now[R], then[R];
 #pragma unroll
-                for (int st = 0; st < 4; ++st) {
+            for (int f = 0; f < R; ++f)
+                now[f] = lookup_dword(cur.packed[f][0][0], table + (kGated ? f : 0) * 8, from[0]);
 #pragma unroll
-                    for (int f = 0; f < R; ++f) {
-                        const u32x4 wf = decode_dword<OUT>(cur.packed[f][j][st], sj[f],
-                                                           table + (kGated ? f : 0) * 8, from);
+            for (int st = 0; st < 16; ++st) {
+                // with 64 rows of x the products cover the lookups, and there
+                // are no registers to spare
+                const int ahead = TF < 4 ? st + 1 : st;
+                if (ahead < 16) {
 #pragma unroll
-                        for (int t = 0; t < TF; ++t)
-                            acc[f][t] = Half<OUT>::mfma(wf, x[st][t], acc[f][t]);
-                    }
-                    if (j < 3)
-                        load_x(c, 4 * j + st + 4);
-                    else
-                        load_x(load_c, st);  // after the last row block: unused
+                    for (int f = 0; f < R; ++f)
+                        then[f] = lookup_dword(cur.packed[f][ahead / 4][ahead % 4],
+                                               table + (kGated ? f : 0) * 8, from[ahead / 4]);
                 }
+                if constexpr (TF < 4)
+                    keep_order();
+#pragma unroll
+                for (int f = 0; f < R; ++f) {
+                    const u32x4 wf = scaled_dword<OUT>(TF < 4 ? now[f] : then[f], sj[st / 4][f]);
+#pragma unroll
+                    for (int t = 0; t < TF; ++t)
+                        acc[f][t] = Half<OUT>::mfma(wf, x[st & 3][t], acc[f][t]);
+                    now[f] = then[f];
+                }
+                if (st < 12)
+                    load_x(c, st + 4);
+                else
+                    load_x(load_c, st - 12);  // after the last row block: unused
             }
             cur = next;
         }
@@ -1483,7 +1559,7 @@ int64_t workspace_need(const Shape &s, int64_t fixed, bool least)
 
 // Which kernel a forward call takes.
 enum Route {
-    kTokenRoute,    // up to 4 rows of x
+    kTokenRoute,    // up to 4 rows of x, weight rows of up to 32768
     kBatchRoute,    // up to 64
     kRaggedRoute,   // up to 64, weight rows of whole dwords that are not 32 k apart
     kProductRoute   // decode to fragments, then the product
@@ -1499,7 +1575,7 @@ Route route_of(const dq4_weight_t *w0, const dq4_weight_t *w1, int64_t n_in, int
         return kProductRoute;
     if (n_in % 32 != 0)
         return kRaggedRoute;
-    return m <= kTokenMost ? kTokenRoute : kBatchRoute;
+    return m <= kTokenMost && n_in <= kTokenMaxChunks * kTokenSpan ? kTokenRoute : kBatchRoute;
 }
 
 int x_row_frags(int64_t m)
@@ -1576,24 +1652,25 @@ template <int OUT, bool kGated, int M>
 dq4_status_t launch_token_rows(const RowsArgs &r, int cus, hipStream_t s)
 {
     // a wave's registers hold x's chunk and the rows in flight
-    constexpr int kWaves = M == 4 ? 8 : 16;
-    const int64_t chunks = ceil_div(r.n_in, kTokenSpan);
-    const int64_t passes = ceil_div(chunks, kWaves);
+    constexpr int kWaves = M == 1 ? 16 : 8;
     TokenArgs a{};
     a.w[0] = r.w[0];
     a.w[1] = r.w[1];
     a.n_in = r.n_in;
-    a.n_elems = r.n_elems;
     a.log2_block = r.log2_block;
-    a.wk = static_cast<int32_t>(ceil_div(chunks, passes));
+    a.chunks = static_cast<int32_t>(ceil_div(r.n_in, kTokenSpan));
+    a.wk = static_cast<int32_t>(ceil_div(a.chunks, ceil_div(a.chunks, kWaves)));
     const int wr = kWaves / a.wk;
-    const int ring = kTokenDepth * wr;  // rows of one turn of every wave's ring
-    const int fit = kTokenPartials<kGated> / 2 / (M * (kGated ? 2 : 1) * a.wk * 4);
+    const int64_t grid = r.n_out < cus ? r.n_out : cus;
+    a.rows_per = static_cast<int32_t>(r.n_out / grid);
+    a.rows_extra = static_cast<int32_t>(r.n_out % grid);
+    const int ring = kTokenRing<kGated> * wr;  // rows of one turn of every wave's ring
+    const int fit = kTokenPartials<kGated> / 2 / (M * (kGated ? 2 : 1) * a.chunks * 4);
     a.batch = fit / ring * ring;
     a.out = r.out;
     void *params[] = {&a};
-    return launch(reinterpret_cast<const void *>(&token_rows_kernel<OUT, kGated, M, kWaves>),
-                  r.n_out < cus ? r.n_out : cus, 1, 64 * a.wk * wr, params, s);
+    return launch(reinterpret_cast<const void *>(&token_rows_kernel<OUT, kGated, M, kWaves>), grid, 1,
+                  64 * a.wk * wr, params, s);
 }
 
 template <int OUT, bool kGated, int TF>
