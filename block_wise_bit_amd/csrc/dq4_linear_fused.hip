@@ -852,6 +852,119 @@ __global__ __launch_bounds__(64 * WAVES) void ragged_rows_kernel(RowsArgs a)
     }
 }
 
+// Forward decode of weights whose rows are whole 16-byte pieces (n_in % 32 ==
+// 0): a wave takes the 16 rows of one fragment f and 256 k.  A load takes 64
+// neighbouring bytes of each row (lane 4 r + p: 32 k of row r), the decoded 16
+// byte units change places in LDS, and every store is a whole fragment.  Each
+// scale is looked up once per 32 k.  Workgroups walk the (group, 256 k) items
+// with the next item's loads in flight.  Bound by memory: 0.5 B read, 2 B
+// written per element.
+constexpr int kDecodeWaves = 16;
+constexpr int kUnitLd = 1024 + 32;  // bytes between a wave's fragments in LDS: 8 neighbouring
+                                    // lanes' writes then meet 8 different bank groups
+
+template <int OUT, bool kTwo>
+__global__ __launch_bounds__(64 * kDecodeWaves) void weight_row_fragments_kernel(FragmentArgs a,
+                                                                                int32_t spans,
+                                                                                int32_t items)
+{
+    constexpr int kW = kTwo ? 2 : 1;
+    __shared__ __attribute__((aligned(1024))) uint8_t table[kPairTableBytes + 256];
+    __shared__ float scb[kW][256];
+    __shared__ __attribute__((aligned(16))) uint8_t units[kDecodeWaves][4 * kUnitLd];
+
+    const int tid = threadIdx.x;
+    const int lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int f = wave & 7, which = kTwo ? f >> 2 : 0;
+    const Weight w = a.w[which];
+    const int r = lane >> 2, p = lane & 3;
+    const int lb = a.log2_block;
+    const int64_t n_in = a.n_in;
+    const int row_of = kTwo ? 4 * r + (f & 3) : 8 * r + f;
+
+    struct Loads {
+        u32x4 packed[2];
+        uint32_t code[2];
+        float absmax[2];
+    };
+    // a workgroup's two halves of 8 waves take neighbouring items
+    auto load = [&](Loads &l, int item) {
+        const int group = item / spans, span = item - group * spans;
+        const int64_t o = static_cast<int64_t>(a.group0 + group) * (kTwo ? 64 : kGroup) + row_of;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int64_t k = static_cast<int64_t>(span) * 256 + h * 128 + 32 * p;
+            l.packed[h] = u32x4{0, 0, 0, 0};
+            l.code[h] = 0;
+            l.absmax[h] = 0.0f;
+            if (o < a.n_out && k < n_in) {
+                const int64_t e = o * n_in + k;
+                const int64_t b = e >> lb;
+                typedef uint32_t Dwords __attribute__((ext_vector_type(4), aligned(4)));
+                l.packed[h] = *reinterpret_cast<const Dwords *>(w.packed + (e >> 1));
+                l.code[h] = w.scale_codes[b];
+                l.absmax[h] = w.nested_absmax[b >> kNestedLog2];
+            }
+        }
+    };
+    int item = blockIdx.x * 2 + (wave >> 3);
+    const int step = gridDim.x * 2;
+    Loads cur;
+    if (item < items)
+        load(cur, item);
+#pragma unroll
+    for (int q = 0; q < kW; ++q)
+        if (tid < 256)
+            scb[q][tid] = a.w[q].scale_codebook[tid];
+    for (int i = tid; i < 256 * 32; i += 64 * kDecodeWaves) {
+        const int b = i >> 5;
+        const float *cb4 = a.w[kTwo ? i & 1 : 0].codebook4;
+        *reinterpret_cast<f32x2 *>(&table[i * 8]) = f32x2{cb4[b & 15], cb4[b >> 4]};
+    }
+    if (tid < 64)
+        *reinterpret_cast<uint32_t *>(&table[kPairTableBytes + tid * 4]) = 0;
+    __syncthreads();
+
+    const uint32_t lane_byte = kTwo ? (lane & 15) * 16 + which * 8 : (lane & 31) * 8;
+    const int chunks = a.chunks;
+    for (; item < items; item += step) {
+        Loads next = cur;
+        if (item + step < items)
+            load(next, item + step);
+        const int group = item / spans, span = item - group * spans;
+        const int64_t o = static_cast<int64_t>(a.group0 + group) * (kTwo ? 64 : kGroup) + row_of;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int64_t k = static_cast<int64_t>(span) * 256 + h * 128 + 32 * p;
+            const bool beyond = o >= a.n_out || k >= n_in;  // zeros, whatever the codebooks hold
+            const uint32_t from = beyond ? (lane_byte & 255) | kPairTableBytes : lane_byte;
+            float s = block_scale(scb[which][cur.code[h]], cur.absmax[h], w.offset);
+            s = beyond ? 0.0f : s;
+            uint8_t *to = units[wave] + p * kUnitLd + r * 16;
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+                *reinterpret_cast<u32x4 *>(to + g * 256) =
+                    decode_dword<OUT>(cur.packed[h][g], s, table, from);
+            // only this wave uses these units: its LDS operations are in order,
+            // the compiler must not move the reads above the writes
+            __asm__ volatile("" ::: "memory");
+            __builtin_amdgcn_wave_barrier();
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int chunk = span * 4 + h * 2 + (q >> 1);
+                const u32x4 v = *reinterpret_cast<const u32x4 *>(units[wave] + q * kUnitLd + lane * 16);
+                if (chunk < chunks)
+                    *reinterpret_cast<u32x4 *>(a.out + (static_cast<int64_t>(group) * chunks + chunk) * (kUnitBytes / 2) +
+                                               ((q & 1) * kFrags + f) * (kFragBytes / 2) + lane * 8) = v;
+            }
+            __asm__ volatile("" ::: "memory");
+            __builtin_amdgcn_wave_barrier();
+        }
+        cur = next;
+    }
+}
+
 // ---------------------------------------------------------------------------
 // one to four rows of x: weight rows read in straight lines
 // ---------------------------------------------------------------------------
@@ -1171,7 +1284,7 @@ __device__ __forceinline__ void transpose_quads(uint32_t (&v)[4], bool odd, bool
 // lanes on 64 of them, and 4 such loads are transposed between the lanes of
 // each quad.  Waves along k (wk of them) meet in LDS, in a fixed order.  The
 // next chunk's loads, also those of the next row block, are in flight while a
-// chunk is multiplied; each x fragment is reloaded 4 steps ahead.
+// chunk is multiplied; each x fragment is reloaded kAhead steps ahead.
 // S: blocks looked up per lane and 128 k (2: blocks of 64 k or more and n_in
 // % 64 == 0; else 4).
 template <int OUT, bool kGated, int TF, int S>
@@ -1253,11 +1366,12 @@ __global__ __launch_bounds__(512) void batch_rows_kernel(RowsArgs a, const uint1
             }
         }
     };
-    u32x4 x[4][TF];
+    constexpr int kAhead = TF == 4 && S == 4 ? 2 : 4;  // steps; what the registers hold
+    u32x4 x[kAhead][TF];
     auto load_x = [&](int c, int step) {  // step in 0 .. 15 of chunk c
 #pragma unroll
         for (int t = 0; t < TF; ++t)
-            x[step & 3][t] = *reinterpret_cast<const u32x4 *>(
+            x[step % kAhead][t] = *reinterpret_cast<const u32x4 *>(
                 x_frags + ((static_cast<int64_t>(c) * 16 + step) * TF + t) * 512 + lane * 8);
     };
 
@@ -1266,7 +1380,7 @@ __global__ __launch_bounds__(512) void batch_rows_kernel(RowsArgs a, const uint1
     int load_c = wk;  // wk < chunks: the host takes no more waves along k than chunks
     load(cur, load_rb, load_c);
 #pragma unroll
-    for (int st = 0; st < 4; ++st)
+    for (int st = 0; st < kAhead; ++st)
         load_x(load_c, st);
 
     // the lookup tables, while the first loads are in flight
@@ -1355,13 +1469,13 @@ __global__ __launch_bounds__(512) void batch_rows_kernel(RowsArgs a, const uint1
                     const u32x4 wf = scaled_dword<OUT>(TF < 4 ? now[f] : then[f], sj[st / 4][f]);
 #pragma unroll
                     for (int t = 0; t < TF; ++t)
-                        acc[f][t] = Half<OUT>::mfma(wf, x[st & 3][t], acc[f][t]);
+                        acc[f][t] = Half<OUT>::mfma(wf, x[st % kAhead][t], acc[f][t]);
                     now[f] = then[f];
                 }
-                if (st < 12)
-                    load_x(c, st + 4);
+                if (st + kAhead < 16)
+                    load_x(c, st + kAhead);
                 else
-                    load_x(load_c, st - 12);  // after the last row block: unused
+                    load_x(load_c, st + kAhead - 16);  // after the last row block: unused
             }
             cur = next;
         }
@@ -1735,9 +1849,23 @@ dq4_status_t launch_few_rows(const RowsArgs &a, Route route, uint8_t *workspace,
 }
 
 template <int OUT, bool kForward>
-dq4_status_t launch_fragments(FragmentArgs a, bool aligned, hipStream_t s)
+dq4_status_t launch_fragments(FragmentArgs a, bool aligned, int cus, hipStream_t s)
 {
     const int64_t all_chunks = a.layout == kStacked ? 2 * a.chunks : a.chunks;
+    if (kForward && aligned && a.n_in % 32 == 0) {
+        int32_t spans = static_cast<int32_t>(ceil_div(all_chunks, 4));
+        int64_t items64 = static_cast<int64_t>(a.groups) * spans;
+        if (items64 > INT32_MAX / 2)
+            return DQ4_EUNSUPPORTED;
+        int32_t items = static_cast<int32_t>(items64);
+        void *params[] = {&a, &spans, &items};
+        const void *kernel =
+            a.layout == kSideBySide
+                ? reinterpret_cast<const void *>(&weight_row_fragments_kernel<OUT, true>)
+                : reinterpret_cast<const void *>(&weight_row_fragments_kernel<OUT, false>);
+        const int64_t pairs = ceil_div(items, 2);
+        return launch(kernel, pairs < cus ? pairs : cus, 1, 64 * kDecodeWaves, params, s);
+    }
     const int64_t grid = kForward ? a.groups * ceil_div(all_chunks, 4)
                                   : ceil_div(a.groups, 2) * all_chunks;
     void *params[] = {&a};
@@ -1803,7 +1931,7 @@ dq4_status_t run_product(const Shape &sh, const dq4_weight_t *w0, const dq4_weig
         f.group0 = static_cast<int32_t>(g0);
         f.groups = static_cast<int32_t>(groups - g0 < window ? groups - g0 : window);
         if (f.chunks > 0) {
-            const dq4_status_t st = launch_fragments<OUT, kForward>(f, aligned, s);
+            const dq4_status_t st = launch_fragments<OUT, kForward>(f, aligned, cus, s);
             if (st != DQ4_OK)
                 return st;
         }
