@@ -239,6 +239,8 @@ struct ProductArgs {
     int32_t act;
     int32_t vec;                // outputs and residual take whole vectors
     int32_t tiles_t;
+    int32_t splits;             // of the chunks; above 1 the sums go to `partial`
+    f32x4 *partial;             // [split][tile][wave][f][16 rows][lane]
     const uint16_t *bias;
     const uint16_t *residual;
     int64_t ld_residual;
@@ -298,7 +300,7 @@ __device__ __forceinline__ void load_values(const uint16_t *p, bool vec, int val
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 v[j] = Half<OUT>::widen((q[j / 2] >> (16 * (j & 1))) & 0xFFFFu);
-        } else {
+        } else if constexpr (N == 4) {
             const u32x2 q = *reinterpret_cast<const u32x2 *>(p);
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -314,14 +316,14 @@ __device__ __forceinline__ void load_values(const uint16_t *p, bool vec, int val
 template <int OUT, int N>
 __device__ __forceinline__ void store_values(uint16_t *p, bool vec, int valid, const float (&v)[N])
 {
-    if (vec) {
-        uint32_t q[N / 2];
+    if (vec && N > 1) {
+        uint32_t q[N / 2 + 1];
 #pragma unroll
         for (int j = 0; j < N / 2; ++j)
             q[j] = Half<OUT>::pack2(v[2 * j], v[2 * j + 1]);
         if constexpr (N == 8)
             *reinterpret_cast<u32x4 *>(p) = u32x4{q[0], q[1], q[2], q[3]};
-        else
+        else if constexpr (N == 4)
             *reinterpret_cast<u32x2 *>(p) = u32x2{q[0], q[1]};
     } else {
 #pragma unroll
@@ -520,13 +522,17 @@ __global__ __launch_bounds__(64 * WN * WT) void fragment_product_kernel(ProductA
         for (int t = 0; t < TF; ++t)
             acc[f][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-    if (all_chunks > 0) {
-        issue(0, 0);
+    // this split's chunks
+    const int split = blockIdx.y;
+    const int c_first = static_cast<int>(static_cast<uint32_t>(all_chunks) * split / a.splits);
+    const int c_last = static_cast<int>(static_cast<uint32_t>(all_chunks) * (split + 1) / a.splits);
+    if (c_first < c_last) {
+        issue(c_first, c_first & 1);
         wait_all_and_barrier();
     }
-    for (int c = 0; c < all_chunks; ++c) {
+    for (int c = c_first; c < c_last; ++c) {
         const int buf = c & 1;
-        if (c + 1 < all_chunks)
+        if (c + 1 < c_last)
             issue(c + 1, buf ^ 1);
         const uint8_t *w_lds = lds + buf * kStage + wn * kUnitBytes + lane * 16;
         const uint8_t *x_l = lds + buf * kStage + kWBytes + wt * (TF * 2 * kFragBytes) + lane * 16;
@@ -550,8 +556,49 @@ __global__ __launch_bounds__(64 * WN * WT) void fragment_product_kernel(ProductA
 
     if (group0 + wn >= a.groups)
         return;
+    if (a.splits > 1) {
+        f32x4 *to = a.partial + ((static_cast<int64_t>(split) * tiles + tile) * kWaves + wave) *
+                                    (kFrags * TF * 64) + lane;
+#pragma unroll
+        for (int f = 0; f < kFrags; ++f)
+#pragma unroll
+            for (int t = 0; t < TF; ++t)
+                to[(f * TF + t) * 64] = acc[f][t];
+        return;
+    }
     finish_wave<OUT, kGated, TF>(a, acc, reinterpret_cast<float *>(lds) + wave * (16 * kFinishLd),
                                  row0 + wt * (TF * 16), group0 + wn, lane);
+}
+
+// The splits' sums of one wave's 128 columns x 16 rows, added in order, and
+// the epilogue.
+template <int OUT, bool kGated, int WN, int WT, int TF>
+__global__ __launch_bounds__(64) void product_reduce_kernel(ProductArgs a, int32_t tiles)
+{
+    __shared__ __attribute__((aligned(16))) float slab[16 * kFinishLd];
+    const int lane = threadIdx.x;
+    const int t = blockIdx.y;
+    const int tile = blockIdx.x / (WN * WT), wave = blockIdx.x % (WN * WT);
+    const int wn = wave % WN, wt = wave / WN;
+    const int tile_n = tile / a.tiles_t, tile_t = tile - tile_n * a.tiles_t;
+    const int group = tile_n * WN + wn;
+    const int64_t row0 = (static_cast<int64_t>(tile_t) * WT + wt) * (16 * TF) + 16 * t;
+    if (group >= a.groups || row0 >= a.m)
+        return;
+    const f32x4 *from = a.partial + (static_cast<int64_t>(tile) * (WN * WT) + wave) * (kFrags * TF * 64) +
+                        t * 64 + lane;
+    const int64_t split_step = static_cast<int64_t>(tiles) * (WN * WT) * (kFrags * TF * 64);
+    f32x4 acc[kFrags][1];
+#pragma unroll
+    for (int f = 0; f < kFrags; ++f)
+        acc[f][0] = from[f * TF * 64];
+    for (int s = 1; s < a.splits; ++s) {
+        from += split_step;
+#pragma unroll
+        for (int f = 0; f < kFrags; ++f)
+            acc[f][0] = acc[f][0] + from[f * TF * 64];
+    }
+    finish_wave<OUT, kGated, 1>(a, acc, slab, row0, group, lane);
 }
 
 // ---------------------------------------------------------------------------
@@ -1538,54 +1585,76 @@ struct SlopeArgs {
     int32_t rows_per_block;
 };
 
-// dz = T(dy act'(pre)), or dgate and dup; one thread per column, a block of
-// rows each, so that the column sums of the unrounded products (the bias
-// gradient) come from a fixed order of FP32 additions.
-template <int OUT, bool kGated>
+// dz = T(dy act'(pre)), or dgate and dup.  A thread takes N neighbouring columns
+// (8, a 16-byte load, where every matrix has 16-byte aligned rows; else 1) and
+// every eighth row of a block of rows; the column sums of the unrounded
+// products (the bias gradient) are FP32 additions in a fixed order: a thread's
+// rows, then the eight threads of a column.  Bound by memory.
+template <int OUT, bool kGated, int N>
 __global__ __launch_bounds__(kThreads) void activation_slope_kernel(SlopeArgs a)
 {
-    const int64_t c = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+    __shared__ float sums[8][32 * N];
+    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+    const int64_t c = (static_cast<int64_t>(blockIdx.x) * 32 + tx) * N;
     const int64_t width = a.pad[0] ? a.ld_pad : a.n;
-    if (c >= width)
-        return;
     const int64_t r0 = static_cast<int64_t>(blockIdx.y) * a.rows_per_block;
     const int64_t r1 = r0 + a.rows_per_block < a.m ? r0 + a.rows_per_block : a.m;
-    float sum = 0.0f;
-    for (int64_t r = r0; r < r1; ++r) {
-        uint16_t out[2] = {0, 0};
-        if (c < a.n) {
-            const float dy = Half<OUT>::widen(a.dy[r * a.ld_dy + c]);
-            float value, slope;
-            if constexpr (kGated) {
-                const float u = Half<OUT>::widen(a.pre[1][r * a.ld_pre + c]);
-                act_and_slope_f32(a.act, Half<OUT>::widen(a.pre[0][r * a.ld_pre + c]), &value,
-                                  &slope);
-                out[0] = static_cast<uint16_t>(Half<OUT>::pack2(dy * u * slope, 0.0f));
-                out[1] = static_cast<uint16_t>(Half<OUT>::pack2(dy * value, 0.0f));
-                a.dz[0][r * a.ld_dz + c] = out[0];
-                a.dz[1][r * a.ld_dz + c] = out[1];
-            } else {
-                float dz = dy;
-                if (a.act != DQ4_ACT_NONE) {
-                    act_and_slope_f32(a.act, Half<OUT>::widen(a.pre[0][r * a.ld_pre + c]), &value,
-                                      &slope);
-                    dz = dy * slope;
+    float sum[N] = {};
+    if (c < width) {
+        for (int64_t r = r0 + ty; r < r1; r += 8) {
+            float z0[N] = {}, z1[N] = {};
+            if (c < a.n) {
+                float dy[N], pre[N], up[N];
+                load_values<OUT, N>(a.dy + r * a.ld_dy + c, N > 1, N, dy);
+                if (a.act != DQ4_ACT_NONE)
+                    load_values<OUT, N>(a.pre[0] + r * a.ld_pre + c, N > 1, N, pre);
+                if constexpr (kGated)
+                    load_values<OUT, N>(a.pre[1] + r * a.ld_pre + c, N > 1, N, up);
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    float value, slope;
+                    if constexpr (kGated) {
+                        act_and_slope_f32(a.act, pre[j], &value, &slope);
+                        z0[j] = dy[j] * up[j] * slope;
+                        z1[j] = dy[j] * value;
+                    } else {
+                        z0[j] = dy[j];
+                        if (a.act != DQ4_ACT_NONE) {
+                            act_and_slope_f32(a.act, pre[j], &value, &slope);
+                            z0[j] = dy[j] * slope;
+                        }
+                        sum[j] = sum[j] + z0[j];
+                    }
                 }
-                sum = sum + dz;
-                out[0] = static_cast<uint16_t>(Half<OUT>::pack2(dz, 0.0f));
                 if (a.dz[0])
-                    a.dz[0][r * a.ld_dz + c] = out[0];
+                    store_values<OUT, N>(a.dz[0] + r * a.ld_dz + c, N > 1, N, z0);
+                if constexpr (kGated)
+                    store_values<OUT, N>(a.dz[1] + r * a.ld_dz + c, N > 1, N, z1);
+            }
+            if (a.pad[0]) {
+                store_values<OUT, N>(a.pad[0] + r * a.ld_pad + c, N > 1, N, z0);
+                if constexpr (kGated)
+                    store_values<OUT, N>(a.pad[1] + r * a.ld_pad + c, N > 1, N, z1);
             }
         }
-        if (a.pad[0]) {
-            a.pad[0][r * a.ld_pad + c] = out[0];
-            if constexpr (kGated)
-                a.pad[1][r * a.ld_pad + c] = out[1];
+    }
+    if constexpr (!kGated) {
+        if (a.partial) {
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                sums[ty][tx * N + j] = sum[j];
+            __syncthreads();
+            for (int i = threadIdx.x; i < 32 * N; i += kThreads) {
+                float total = sums[0][i];
+#pragma unroll
+                for (int q = 1; q < 8; ++q)
+                    total = total + sums[q][i];
+                const int64_t col = static_cast<int64_t>(blockIdx.x) * (32 * N) + i;
+                if (col < a.n)
+                    a.partial[static_cast<int64_t>(blockIdx.y) * a.n + col] = total;
+            }
         }
     }
-    if constexpr (!kGated)
-        if (a.partial && c < a.n)
-            a.partial[static_cast<int64_t>(blockIdx.y) * a.n + c] = sum;
 }
 
 // dbias[c] = the row blocks' sums, added in order.
@@ -1641,6 +1710,54 @@ int64_t padded_ld(int64_t k)
     return ceil_div(k, kChunk) * kChunk;
 }
 
+int current_compute_units()
+{
+    int device = 0;
+    if (hipGetDevice(&device) != hipSuccess) {
+        (void)hipGetLastError();
+        return 256;
+    }
+    return compute_units(device);
+}
+
+// How a product is cut: the tile (128 WN columns x 16 TF WT rows) and the
+// splits of the summed index.  It follows from the call's sizes and the GPU
+// alone, so that a smaller workspace changes nothing in the sums.
+struct Plan {
+    int tile;      // 0: 256 x 256, 1: 128 x 128, 2: 128 x 64
+    int splits;
+};
+
+constexpr int kTileCols[3] = {256, 128, 128}, kTileRows[3] = {256, 128, 64};
+constexpr int kTileResident[3] = {1, 2, 3};        // workgroups per CU (LDS)
+// Microseconds of one chunk of 64 k with every CU full, as measured: 1.2, 0.77
+// and 0.45 PFLOP/s over 256 CUs.
+constexpr double kTileChunk[3] = {1.78, 1.40, 1.80};
+
+Plan plan_of(int64_t m, int64_t groups, int64_t all_chunks, int cus)
+{
+    Plan best{2, 1};
+    double least = 1e300;
+    for (int tile = 0; tile < 3; ++tile) {
+        const int64_t tiles = ceil_div(groups * kGroup, kTileCols[tile]) * ceil_div(m, kTileRows[tile]);
+        for (int splits = 1; splits <= 16; ++splits) {
+            if (splits > 1 && splits * 2 > all_chunks)
+                break;
+            const int64_t rounds = ceil_div(tiles * splits, static_cast<int64_t>(cus) * kTileResident[tile]);
+            double cost = static_cast<double>(rounds) *
+                          (static_cast<double>(ceil_div(all_chunks, splits)) * kTileChunk[tile] + 2.0);
+            if (splits > 1)  // the partial sums, written and read at about 4 TB/s, and a launch
+                cost += 3.0 + static_cast<double>(splits) * static_cast<double>(m) *
+                                  static_cast<double>(groups * kGroup) * 8.0 / 4e6;
+            if (cost < least) {
+                least = cost;
+                best = Plan{tile, splits};
+            }
+        }
+    }
+    return best;
+}
+
 // The sizes of one call's product.
 struct Shape {
     int64_t m, n, k;   // rows, output columns, summed index per x matrix
@@ -1650,6 +1767,18 @@ struct Shape {
     int64_t groups() const { return ceil_div(n, per_group()); }
     int64_t chunks() const { return ceil_div(k, kChunk); }
     int64_t group_bytes() const { return chunks() * n_x() * kUnitBytes; }
+    Plan plan(int cus) const { return plan_of(m, groups(), chunks() * n_x(), cus); }
+    // partial sums of `g` groups
+    int64_t split_bytes(const Plan &p, int64_t g) const
+    {
+        return p.splits == 1 ? 0
+                             : p.splits * ceil_div(g * kGroup, kTileCols[p.tile]) * kTileCols[p.tile] *
+                                   ceil_div(m, kTileRows[p.tile]) * kTileRows[p.tile] * 4;
+    }
+    int64_t window_bytes(const Plan &p, int64_t g) const
+    {
+        return g * group_bytes() + split_bytes(p, g);
+    }
 };
 
 constexpr int64_t kRowBlock = 64;  // rows per block of column sums
@@ -1668,7 +1797,7 @@ int64_t partial_bytes(int64_t m, int64_t n)
 int64_t workspace_need(const Shape &s, int64_t fixed, bool least)
 {
     const int64_t groups = least ? (s.groups() < 2 ? s.groups() : 2) : s.groups();
-    return fixed + groups * s.group_bytes();
+    return fixed + s.window_bytes(s.plan(current_compute_units()), groups);
 }
 
 // Which kernel a forward call takes.
@@ -1726,16 +1855,23 @@ dq4_status_t launch_product_tile(ProductArgs a, hipStream_t s)
     a.tiles_t = static_cast<int32_t>(ceil_div(a.m, 16 * TF * WT));
     const int64_t tiles = ceil_div(a.groups, WN) * a.tiles_t;
     void *params[] = {&a};
-    return launch(reinterpret_cast<const void *>(&fragment_product_kernel<OUT, kGated, WN, WT, TF>),
-                  tiles, 1, 64 * WN * WT, params, s);
+    dq4_status_t st =
+        launch(reinterpret_cast<const void *>(&fragment_product_kernel<OUT, kGated, WN, WT, TF>), tiles,
+               a.splits, 64 * WN * WT, params, s);
+    if (st != DQ4_OK || a.splits == 1)
+        return st;
+    int32_t n_tiles = static_cast<int32_t>(tiles);
+    void *rp[] = {&a, &n_tiles};
+    return launch(reinterpret_cast<const void *>(&product_reduce_kernel<OUT, kGated, WN, WT, TF>),
+                  tiles * WN * WT, TF, 64, rp, s);
 }
 
 template <int OUT, bool kGated>
-dq4_status_t launch_product(const ProductArgs &a, int cus, hipStream_t s)
+dq4_status_t launch_product(const ProductArgs &a, const Plan &plan, hipStream_t s)
 {
-    if (ceil_div(a.groups, 2) * ceil_div(a.m, 256) * 4 >= cus * int64_t{3})
+    if (plan.tile == 0)
         return launch_product_tile<OUT, kGated, 2, 4, 4>(a, s);
-    if (a.groups * ceil_div(a.m, 128) >= cus)
+    if (plan.tile == 1)
         return launch_product_tile<OUT, kGated, 1, 4, 2>(a, s);
     return launch_product_tile<OUT, kGated, 1, 4, 1>(a, s);
 }
@@ -1909,14 +2045,16 @@ dq4_status_t run_product(const Shape &sh, const dq4_weight_t *w0, const dq4_weig
         }
     }
     const int64_t groups = sh.groups();
-    const int64_t window =
-        sh.group_bytes() == 0 ? groups : (fragment_bytes / sh.group_bytes() < groups
-                                              ? fragment_bytes / sh.group_bytes()
-                                              : groups);
+    const Plan plan = sh.plan(cus);
+    // the widest window that fits, in pairs of groups (a tile's columns)
+    int64_t window = groups;
+    while (window > 2 && sh.window_bytes(plan, window) > fragment_bytes)
+        window = window / 2 + (window / 2) % 2;
     FragmentArgs f{};
     f.w[0] = device_weight(*w0);
     f.w[1] = device_weight(w1 ? *w1 : *w0);
-    f.out = reinterpret_cast<uint16_t *>(fragments);
+    const int64_t split_bytes = sh.split_bytes(plan, window);
+    f.out = reinterpret_cast<uint16_t *>(fragments + split_bytes);
     f.n_out = n_out;
     f.n_in = n_in;
     f.log2_block = log2_block;
@@ -1925,6 +2063,8 @@ dq4_status_t run_product(const Shape &sh, const dq4_weight_t *w0, const dq4_weig
     const bool aligned = n_in % 8 == 0 && reinterpret_cast<uintptr_t>(w0->packed) % 4 == 0 &&
                          (!w1 || reinterpret_cast<uintptr_t>(w1->packed) % 4 == 0);
     p.wfrag = f.out;
+    p.splits = plan.splits;
+    p.partial = reinterpret_cast<f32x4 *>(fragments);
     p.chunks = f.chunks;
     p.n_x = sh.n_x();
     for (int64_t g0 = 0; g0 < groups; g0 += window) {
@@ -1939,14 +2079,35 @@ dq4_status_t run_product(const Shape &sh, const dq4_weight_t *w0, const dq4_weig
         p.n0 = g0 * sh.per_group();
         dq4_status_t st;
         if constexpr (kForward)
-            st = sh.layout == kSideBySide ? launch_product<OUT, true>(p, cus, s)
-                                          : launch_product<OUT, false>(p, cus, s);
+            st = sh.layout == kSideBySide ? launch_product<OUT, true>(p, plan, s)
+                                          : launch_product<OUT, false>(p, plan, s);
         else
-            st = launch_product<OUT, false>(p, cus, s);
+            st = launch_product<OUT, false>(p, plan, s);
         if (st != DQ4_OK)
             return st;
     }
     return DQ4_OK;
+}
+
+template <bool kGated>
+dq4_status_t launch_slope(const SlopeArgs &args, int32_t dtype, hipStream_t s)
+{
+    SlopeArgs a = args;
+    bool vec = rows_aligned(a.dy, a.ld_dy, a.m, a.n);
+    for (const void *p : {static_cast<const void *>(a.pre[0]), static_cast<const void *>(a.pre[1])})
+        vec = vec && (!p || rows_aligned(p, a.ld_pre, a.m, a.n));
+    for (const void *p : {static_cast<const void *>(a.dz[0]), static_cast<const void *>(a.dz[1])})
+        vec = vec && (!p || rows_aligned(p, a.ld_dz, a.m, a.n));
+    const void *kernel;
+    if (dtype == DQ4_F16)
+        kernel = vec ? reinterpret_cast<const void *>(&activation_slope_kernel<DQ4_F16, kGated, 8>)
+                     : reinterpret_cast<const void *>(&activation_slope_kernel<DQ4_F16, kGated, 1>);
+    else
+        kernel = vec ? reinterpret_cast<const void *>(&activation_slope_kernel<DQ4_BF16, kGated, 8>)
+                     : reinterpret_cast<const void *>(&activation_slope_kernel<DQ4_BF16, kGated, 1>);
+    void *params[] = {&a};
+    return launch(kernel, ceil_div(a.pad[0] ? a.ld_pad : a.n, vec ? 256 : 32), ceil_div(a.m, kRowBlock),
+                  kThreads, params, s);
 }
 
 dq4_status_t copy_rows(const void *x, int64_t ld, int64_t m, int64_t k, void *out, hipStream_t s)
@@ -2218,12 +2379,7 @@ dq4_status_t dq4_linear_fused_backward(const dq4_weight_t *w, int64_t n_out, int
         a.n = n_out;
         a.act = activation;
         a.rows_per_block = static_cast<int32_t>(kRowBlock);
-        void *params[] = {&a};
-        const void *kernel = dtype == DQ4_F16
-                                 ? reinterpret_cast<const void *>(&activation_slope_kernel<DQ4_F16, false>)
-                                 : reinterpret_cast<const void *>(&activation_slope_kernel<DQ4_BF16, false>);
-        dq4_status_t ls = launch(kernel, ceil_div(copy ? a.ld_pad : n_out, kThreads), blocks, kThreads,
-                                 params, s);
+        dq4_status_t ls = launch_slope<false>(a, dtype, s);
         if (ls != DQ4_OK)
             return ls;
         if (dbias && blocks > 1) {
@@ -2304,12 +2460,7 @@ dq4_status_t dq4_gated_fused_backward(const dq4_weight_t *gate, const dq4_weight
         a.n = n_ff;
         a.act = activation;
         a.rows_per_block = static_cast<int32_t>(kRowBlock);
-        void *params[] = {&a};
-        const void *kernel = dtype == DQ4_F16
-                                 ? reinterpret_cast<const void *>(&activation_slope_kernel<DQ4_F16, true>)
-                                 : reinterpret_cast<const void *>(&activation_slope_kernel<DQ4_BF16, true>);
-        const dq4_status_t ls = launch(kernel, ceil_div(copy ? a.ld_pad : n_ff, kThreads),
-                                       ceil_div(m, kRowBlock), kThreads, params, s);
+        const dq4_status_t ls = launch_slope<true>(a, dtype, s);
         if (ls != DQ4_OK)
             return ls;
     }
