@@ -570,6 +570,158 @@ __global__ __launch_bounds__(64 * WN * WT) void fragment_product_kernel(ProductA
                                  row0 + wt * (TF * 16), group0 + wn, lane);
 }
 
+// The 256 x 256 tile, for large products: 8 waves in two halves, one of each
+// half on every SIMD.  A wave alternates between a load phase (its operand
+// fragments of one k-step of 32 from LDS, and the loads from HBM to LDS of the
+// k-step three ahead) and a product phase (32 matrix instructions); every phase
+// ends on a barrier and the halves are one phase apart, so that while one
+// wave of a SIMD multiplies the other one loads.  Four buffers of one k-step
+// each: the step three ahead goes where step h - 1 lay, which both halves have
+// read by then, and it has four phases (about 2000 cycles) or more to arrive.
+template <int OUT, bool kGated>
+__global__ __launch_bounds__(512) void fragment_product_wide_kernel(ProductArgs a)
+{
+    constexpr int WN = 2, WT = 4, TF = 4;
+    constexpr int kRows = 16 * TF * WT;
+    constexpr int kStepW = kFrags * kFragBytes;      // one group's fragments of one k-step
+    constexpr int kStage = WN * kStepW + kRows * 64;  // 32 KiB
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * kStage];
+    static_assert(8 * 16 * kFinishLd * 4 <= 4 * kStage, "the epilogue slabs fit the stages");
+
+    const int tid = threadIdx.x;
+    const int lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wn = wave % WN, wt = wave / WN;
+
+    // each XCD takes a contiguous run of tiles, as in fragment_product_kernel
+    const int tiles = gridDim.x;
+    const int per = tiles / kXcds, extra = tiles % kXcds;
+    const int xcd = blockIdx.x % kXcds, idx = blockIdx.x / kXcds;
+    const int tile = xcd * per + (xcd < extra ? xcd : extra) + idx;
+    const int tile_n = tile / a.tiles_t, tile_t = tile - tile_n * a.tiles_t;
+    const int group0 = tile_n * WN;
+    const int64_t row0 = static_cast<int64_t>(tile_t) * kRows;
+    const int all_steps = a.chunks * a.n_x * 2;
+
+    // this wave's loads of a step: W fragments 2 wave, 2 wave + 1 (of 16), x
+    // fragments 2 wave, 2 wave + 1 (of 16)
+    const int w_group = group0 + wave / 4 < a.groups ? group0 + wave / 4 : a.groups - 1;
+    const u32x4 rs_w = make_rsrc(reinterpret_cast<const uint8_t *>(a.wfrag) +
+                                     static_cast<int64_t>(w_group) * all_steps * kStepW,
+                                 static_cast<uint32_t>(all_steps) * kStepW);
+    const int64_t rows_left = a.m - row0;
+    const int64_t rows_here = rows_left < kRows ? rows_left : kRows;
+    const uint32_t x_bytes = static_cast<uint32_t>(((rows_here - 1) * a.ld_x + a.k) * 2);
+    const u32x4 rs_x0 = make_rsrc(a.x[0] + row0 * a.ld_x, x_bytes);
+    const u32x4 rs_x1 = make_rsrc(a.x[a.n_x - 1] + row0 * a.ld_x, x_bytes);
+    uint32_t x_off[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const int row = (2 * wave + q) * 16 + (lane & 15);
+        x_off[q] = row < rows_here
+                       ? static_cast<uint32_t>(row * static_cast<int32_t>(a.ld_x) + (lane >> 4) * 8) * 2u
+                       : 0x80000000u;
+    }
+    const int32_t x_k = (lane >> 4) * 8;
+    const uint32_t lds0 = lds_offset(lds);
+    const uint32_t w_off = (wave % 4) * (2 * kFragBytes) + lane * 16;
+
+    // this split's steps
+    const int split = blockIdx.y;
+    const int h_first = 2 * static_cast<int>(static_cast<uint32_t>(all_steps / 2) * split / a.splits);
+    const int h_last = 2 * static_cast<int>(static_cast<uint32_t>(all_steps / 2) * (split + 1) / a.splits);
+
+    // always 4 loads: past the last step they fetch nothing and write zeros
+    // where nothing is read, so that the waits below count the same loads
+    auto issue = [&](int h) {
+        const uint32_t to = lds0 + (h & 3) * kStage;
+        const bool real = h < h_last;
+        const uint32_t w_at = real ? w_off : 0x80000000u;
+        const uint32_t soff = real ? static_cast<uint32_t>(h) * kStepW : 0u;
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+            buffer_to_lds(rs_w, w_at + q * kFragBytes, soff,
+                          to + (wave / 4) * kStepW + ((wave % 4) * 2 + q) * kFragBytes);
+        const int second = h >= 2 * a.chunks ? 1 : 0;
+        const int hk = h - second * 2 * a.chunks;
+        const u32x4 rs = second ? rs_x1 : rs_x0;
+        const int32_t k_left = static_cast<int32_t>(a.k) - hk * 32;
+        const bool in = real && x_k < k_left;
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+            buffer_to_lds(rs, in ? x_off[q] + static_cast<uint32_t>(hk) * 64u : 0x80000000u, 0,
+                          to + WN * kStepW + (2 * wave + q) * kFragBytes);
+    };
+
+    f32x4 acc[kFrags][TF];
+#pragma unroll
+    for (int f = 0; f < kFrags; ++f)
+#pragma unroll
+        for (int t = 0; t < TF; ++t)
+            acc[f][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+    issue(h_first);
+    issue(h_first + 1);
+    issue(h_first + 2);
+    __asm__ volatile("s_waitcnt vmcnt(8)" ::: "memory");
+    if (h_first == h_last)
+        __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    if (wave >= 4)
+        __builtin_amdgcn_s_barrier();  // the second half is one phase behind
+    for (int h = h_first; h < h_last; ++h) {
+        const uint8_t *stage = lds + (h & 3) * kStage;
+        const uint8_t *w_lds = stage + wn * kStepW + lane * 16;
+        const uint8_t *x_lds = stage + WN * kStepW + wt * (TF * kFragBytes) + lane * 16;
+        u32x4 wf[kFrags], xf[TF];
+#pragma unroll
+        for (int t = 0; t < TF; ++t)
+            xf[t] = *reinterpret_cast<const u32x4 *>(x_lds + t * kFragBytes);
+#pragma unroll
+        for (int f = 0; f < kFrags; ++f)
+            wf[f] = *reinterpret_cast<const u32x4 *>(w_lds + f * kFragBytes);
+        issue(h + 3);
+        // this wave's share of step h + 1 has arrived (steps h + 2 and h + 3
+        // are still under way), and its reads of step h are done
+        __asm__ volatile("s_waitcnt vmcnt(8) lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+        for (int f = 0; f < kFrags; ++f)
+#pragma unroll
+            for (int t = 0; t < TF; ++t)
+                acc[f][t] = Half<OUT>::mfma(wf[f], xf[t], acc[f][t]);
+        __builtin_amdgcn_s_setprio(0);
+        __builtin_amdgcn_sched_barrier(0);
+        // after the last barrier the buffers are the epilogue's: no load may
+        // still be on its way into them
+        if (h + 1 == h_last)
+            __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    if (wave < 4)
+        __builtin_amdgcn_s_barrier();
+    __asm__ volatile("" ::: "memory");
+
+    if (group0 + wn >= a.groups)
+        return;
+    if (a.splits > 1) {
+        f32x4 *to = a.partial + ((static_cast<int64_t>(split) * tiles + tile) * 8 + wave) *
+                                    (kFrags * TF * 64) + lane;
+#pragma unroll
+        for (int f = 0; f < kFrags; ++f)
+#pragma unroll
+            for (int t = 0; t < TF; ++t)
+                to[(f * TF + t) * 64] = acc[f][t];
+        return;
+    }
+    finish_wave<OUT, kGated, TF>(a, acc, reinterpret_cast<float *>(lds) + wave * (16 * kFinishLd),
+                                 row0 + wt * (TF * 16), group0 + wn, lane);
+}
+
 // The splits' sums of one wave's 128 columns x 16 rows, added in order, and
 // the epilogue.
 template <int OUT, bool kGated, int WN, int WT, int TF>
@@ -1855,9 +2007,12 @@ dq4_status_t launch_product_tile(ProductArgs a, hipStream_t s)
     a.tiles_t = static_cast<int32_t>(ceil_div(a.m, 16 * TF * WT));
     const int64_t tiles = ceil_div(a.groups, WN) * a.tiles_t;
     void *params[] = {&a};
-    dq4_status_t st =
-        launch(reinterpret_cast<const void *>(&fragment_product_kernel<OUT, kGated, WN, WT, TF>), tiles,
-               a.splits, 64 * WN * WT, params, s);
+    const void *kernel;
+    if constexpr (WN == 2)
+        kernel = reinterpret_cast<const void *>(&fragment_product_wide_kernel<OUT, kGated>);
+    else
+        kernel = reinterpret_cast<const void *>(&fragment_product_kernel<OUT, kGated, WN, WT, TF>);
+    dq4_status_t st = launch(kernel, tiles, a.splits, 64 * WN * WT, params, s);
     if (st != DQ4_OK || a.splits == 1)
         return st;
     int32_t n_tiles = static_cast<int32_t>(tiles);
