@@ -595,6 +595,37 @@ def _weight_of(packed, scale_codes, nested_absmax, scale_codebook, codebook4, of
                              nested_blocksize)
 
 
+def _launch(what: str, device, stream, workspace, sizes, *args) -> None:
+    """Call library function `what` on `device`: args, then the workspace (the
+    caller's, or one of the preferred size for `sizes`), then the stream.  A
+    single token's call takes the GPU about as long as Python, so nothing is
+    entered or asked that already holds."""
+    torch = _torch()
+    if torch.cuda.current_device() != device.index:
+        with torch.cuda.device(device):
+            return _launch(what, device, stream, workspace, sizes, *args)
+    lib = library()
+    size = getattr(lib, what + "_workspace_bytes")
+    if workspace is None:
+        nbytes, address = size(*sizes, 0), None
+        if nbytes:
+            workspace = _used_on(torch.empty(nbytes, dtype=torch.uint8, device=device), stream)
+            address = workspace.data_ptr()
+    else:
+        if workspace.device != device or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {device}")
+        nbytes = workspace.numel() * workspace.element_size()
+        least = size(*sizes, 1)
+        if nbytes < least:
+            raise ValueError(f"workspace holds {nbytes} bytes, needs {least}")
+        address = workspace.data_ptr() if nbytes else None
+    handle = (stream.cuda_stream if stream is not None
+              else torch._C._cuda_getCurrentRawStream(device.index))
+    st = getattr(lib, what)(*args, address, nbytes, handle)
+    if st != DQ4_OK:
+        _raise_for(st, what)
+
+
 def _gated_weights(gate, up, n: int, blocksize: int, nested_blocksize: int):
     """The two weights of a gated call, each a mapping with the keys packed,
     scale_codes, nested_absmax, scale_codebook, codebook4 and offset."""
@@ -605,11 +636,11 @@ def _gated_weights(gate, up, n: int, blocksize: int, nested_blocksize: int):
     return device, g, u
 
 
-def _sizes(*values):
-    values = tuple(int(v) for v in values)
-    if min(values) < 0:
+def _sizes(n_out, n_in, blocksize):
+    n_out, n_in, blocksize = int(n_out), int(n_in), int(blocksize)
+    if n_out < 0 or n_in < 0 or blocksize < 0:
         raise ValueError("sizes must not be negative")
-    return values
+    return n_out, n_in, blocksize
 
 
 def _activation_code(activation: str, gated: bool) -> int:
@@ -622,7 +653,7 @@ def _activation_code(activation: str, gated: bool) -> int:
 
 def _matrix(t, name: str, m: int, width: int, dtype, device) -> int:
     """The row stride of an (m, width) matrix with unit stride along its rows."""
-    if t.dtype != dtype or t.device != device or t.dim() != 2 or tuple(t.shape) != (m, width):
+    if t.dtype != dtype or t.device != device or t.shape != (m, width):
         raise ValueError(f"{name} must be a ({m}, {width}) {dtype} tensor on {device}")
     row, col = t.stride()
     if col != 1 and width > 1:
@@ -660,25 +691,6 @@ def _refuse_overlap(outputs, inputs):
         for other, u in outputs[i + 1:] + inputs:
             if _overlap(t, u):
                 raise ValueError(f"{name} overlaps {other}")
-
-
-def _bytes_workspace(workspace, size, sizes, device, stream):
-    """(tensor, address, bytes) of the caller's workspace, checked against the
-    least that `size` asks for these sizes, or of one of the preferred size."""
-    torch = _torch()
-    if workspace is None:
-        nbytes = size(*sizes, 0)
-        if nbytes == 0:
-            return None, None, 0
-        workspace = _used_on(torch.empty(nbytes, dtype=torch.uint8, device=device), stream)
-        return workspace, workspace.data_ptr(), nbytes
-    if workspace.device != device or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on {device}")
-    nbytes = workspace.numel() * workspace.element_size()
-    least = size(*sizes, 1)
-    if nbytes < least:
-        raise ValueError(f"workspace holds {nbytes} bytes, needs {least}")
-    return workspace, workspace.data_ptr() if nbytes else None, nbytes
 
 
 def _address(t):
@@ -774,16 +786,11 @@ def dq4_linear_fused(packed, scale_codes, nested_absmax, scale_codebook, codeboo
         _refuse_overlap([("y", y), ("pre", pre)],
                         [("x", x), ("bias", bias), ("residual", None if in_place else residual)])
     address = x.data_ptr()
-    lib = library()
     sizes = (ctypes.byref(w), n_out, n_in, m, address, ld_x)
-    size = lib.dq4_linear_fused_workspace_bytes
-    keep, ws, nbytes = _bytes_workspace(workspace, size, sizes, device, stream)
-    with torch.cuda.device(device):
-        st = lib.dq4_linear_fused(
-            ctypes.byref(w), n_out, n_in, code, act, address, m, ld_x, _address(bias),
-            _address(residual), ld_residual, y.data_ptr(), ld_y, _address(pre), ld_pre, ws, nbytes,
-            _stream_handle(device, stream))
-    _raise_for(st, "dq4_linear_fused")
+    _launch(
+        "dq4_linear_fused", device, stream, workspace, sizes,
+        ctypes.byref(w), n_out, n_in, code, act, address, m, ld_x, _address(bias),
+        _address(residual), ld_residual, y.data_ptr(), ld_y, _address(pre), ld_pre)
     return y
 
 
@@ -835,16 +842,11 @@ def dq4_linear_fused_backward(packed, scale_codes, nested_absmax, scale_codebook
     if any(t is not None for _, t in given):
         _refuse_overlap([("dx", dx), ("dz", dz), ("dbias", dbias)], [("dy", dy), ("pre", pre)])
     lhs, ld_lhs = (dy, ld_dy) if act == DQ4_ACT_NONE else (dz, ld_dz)
-    lib = library()
     sizes = (ctypes.byref(w), n_out, n_in, m, lhs.data_ptr(), ld_lhs)
-    size = lib.dq4_linear_fused_backward_workspace_bytes
-    keep, ws, nbytes = _bytes_workspace(workspace, size, sizes, device, stream)
-    with torch.cuda.device(device):
-        st = lib.dq4_linear_fused_backward(
-            ctypes.byref(w), n_out, n_in, code, act, dy.data_ptr(), m, ld_dy, _address(pre), ld_pre,
-            dx.data_ptr(), ld_dx, _address(dz), ld_dz, _address(dbias), ws, nbytes,
-            _stream_handle(device, stream))
-    _raise_for(st, "dq4_linear_fused_backward")
+    _launch(
+        "dq4_linear_fused_backward", device, stream, workspace, sizes,
+        ctypes.byref(w), n_out, n_in, code, act, dy.data_ptr(), m, ld_dy, _address(pre), ld_pre,
+        dx.data_ptr(), ld_dx, _address(dz), ld_dz, _address(dbias))
     return dx, dy if act == DQ4_ACT_NONE else dz, dbias
 
 
@@ -882,16 +884,11 @@ def dq4_gated_fused(gate, up, n_ff: int, n_in: int, blocksize: int, x,
     if given or gate_pre is not None:
         _refuse_overlap([("h", h), ("gate_pre", gate_pre), ("up_pre", up_pre)], [("x", x)])
     address = x.data_ptr()
-    lib = library()
     sizes = (ctypes.byref(wg), ctypes.byref(wu), n_ff, n_in, m, address, ld_x)
-    size = lib.dq4_gated_fused_workspace_bytes
-    keep, ws, nbytes = _bytes_workspace(workspace, size, sizes, device, stream)
-    with torch.cuda.device(device):
-        st = lib.dq4_gated_fused(
-            ctypes.byref(wg), ctypes.byref(wu), n_ff, n_in, code, act, address, m, ld_x,
-            h.data_ptr(), ld_h, _address(gate_pre), _address(up_pre), ld_pre, ws, nbytes,
-            _stream_handle(device, stream))
-    _raise_for(st, "dq4_gated_fused")
+    _launch(
+        "dq4_gated_fused", device, stream, workspace, sizes,
+        ctypes.byref(wg), ctypes.byref(wu), n_ff, n_in, code, act, address, m, ld_x,
+        h.data_ptr(), ld_h, _address(gate_pre), _address(up_pre), ld_pre)
     return h
 
 
@@ -930,16 +927,12 @@ def dq4_gated_fused_backward(gate, up, n_ff: int, n_in: int, blocksize: int, dh,
     if given:
         _refuse_overlap([("dx", dx), ("dgate", dgate), ("dup", dup)],
                         [("dh", dh), ("gate_pre", gate_pre), ("up_pre", up_pre)])
-    lib = library()
     sizes = (ctypes.byref(wg), ctypes.byref(wu), n_ff, n_in, m, dgate.data_ptr(), dup.data_ptr(), ld_dpre)
-    size = lib.dq4_gated_fused_backward_workspace_bytes
-    keep, ws, nbytes = _bytes_workspace(workspace, size, sizes, device, stream)
-    with torch.cuda.device(device):
-        st = lib.dq4_gated_fused_backward(
-            ctypes.byref(wg), ctypes.byref(wu), n_ff, n_in, code, act, dh.data_ptr(), m, ld_dh,
-            gate_pre.data_ptr(), up_pre.data_ptr(), ld_pre, dx.data_ptr(), ld_dx, dgate.data_ptr(),
-            dup.data_ptr(), ld_dpre, ws, nbytes, _stream_handle(device, stream))
-    _raise_for(st, "dq4_gated_fused_backward")
+    _launch(
+        "dq4_gated_fused_backward", device, stream, workspace, sizes,
+        ctypes.byref(wg), ctypes.byref(wu), n_ff, n_in, code, act, dh.data_ptr(), m, ld_dh,
+        gate_pre.data_ptr(), up_pre.data_ptr(), ld_pre, dx.data_ptr(), ld_dx, dgate.data_ptr(),
+        dup.data_ptr(), ld_dpre)
     return dx, dgate, dup
 
 
