@@ -673,9 +673,11 @@ def _overlap(a, b) -> bool:
         return False
     a0, b0 = a.data_ptr(), b.data_ptr()
 
-    def last(t):
-        return sum((n - 1) * s for n, s in zip(t.shape, t.stride())) * t.element_size()
-    if a0 > b0 + last(b) or b0 > a0 + last(a):
+    def span(t):
+        if t.is_contiguous():
+            return t.numel() * t.element_size()
+        return (sum((n - 1) * s for n, s in zip(t.shape, t.stride())) + 1) * t.element_size()
+    if a0 >= b0 + span(b) or b0 >= a0 + span(a):
         return False
     if a.dim() == b.dim() == 2 and a.stride(0) == b.stride(0) and a.dtype == b.dtype:
         ld = a.stride(0) * a.element_size()

@@ -93,13 +93,30 @@ __device__ __forceinline__ float scale_of(const Weight &w, const Tables &t, int6
                        w.offset);
 }
 
-// The FP32 product of element `e` of the flat weight, before its rounding to T.
-__device__ __forceinline__ float element_of(const Weight &w, const Tables &t, int log2_block,
-                                            int64_t e)
+// The FP32 products of elements e .. e + valid - 1 (valid in 1 .. 8) of the flat
+// weight, before their rounding to T, zeros after them; any alignment.  The
+// codes are 32 bits out of two neighbouring dwords (the dword with the last
+// byte is read whole, nothing beyond it), and since blocks are longer than 8
+// elements at most two of them meet.
+__device__ __forceinline__ void octet_of(const Weight &w, const Tables &t, int log2_block,
+                                         int64_t last_byte, int64_t e, int valid, float (&v)[8])
 {
-    const uint32_t byte = w.packed[e >> 1];
-    const uint32_t code = (e & 1) ? byte >> 4 : byte & 15u;
-    return t.cb4[code] * scale_of(w, t, e >> log2_block);
+    const uintptr_t address = reinterpret_cast<uintptr_t>(w.packed);
+    const uint32_t skew = static_cast<uint32_t>(address & 3);
+    const uint32_t *words = reinterpret_cast<const uint32_t *>(address - skew);
+    const int64_t bit = static_cast<int64_t>(skew) * 8 + 4 * e;
+    const int64_t at = bit >> 5, last = (last_byte + skew) >> 2;
+    const uint32_t lo = words[at], hi = words[at < last ? at + 1 : at];
+    const uint32_t word = __builtin_amdgcn_alignbit(hi, lo, static_cast<uint32_t>(bit) & 31);
+    const int64_t b = e >> log2_block;
+    const int64_t b_last = (e + valid - 1) >> log2_block;
+    const float s_lo = scale_of(w, t, b), s_hi = scale_of(w, t, b_last);
+    const int64_t meet = ((b + 1) << log2_block) - e;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float p = t.cb4[(word >> (4 * j)) & 15u] * (j < meet ? s_lo : s_hi);
+        v[j] = j < valid ? p : 0.0f;
+    }
 }
 
 // Decode into fragments.  kForward: k runs along the weight's rows (n_in), a
@@ -107,7 +124,7 @@ __device__ __forceinline__ float element_of(const Weight &w, const Tables &t, in
 // Backward: k runs down the weight's columns; a thread takes the dwords of 8
 // rows (8 columns each) and writes 8 units, each pairing the same column of
 // the 8 rows.  kAligned: rows start on packed dwords (n_in % 8 == 0, 4-byte
-// aligned codes); otherwise every element finds its own byte and block.
+// aligned codes); otherwise eight elements are cut out of two dwords.
 // Bound by memory: 0.5 B read and 2 B written per element.
 template <int OUT, bool kForward, bool kAligned>
 __global__ __launch_bounds__(kThreads) void weight_fragments_kernel(FragmentArgs a)
@@ -121,6 +138,7 @@ __global__ __launch_bounds__(kThreads) void weight_fragments_kernel(FragmentArgs
 
     const int tid = threadIdx.x;
     const int lb = a.log2_block;
+    const int64_t last_byte = (a.n_out * a.n_in - 1) >> 1;
     const int all_chunks = a.layout == kStacked ? 2 * a.chunks : a.chunks;
     if constexpr (kForward) {
         // a workgroup decodes 4 chunks (256 k, 128 packed bytes a row) of a group
@@ -157,9 +175,7 @@ __global__ __launch_bounds__(kThreads) void weight_fragments_kernel(FragmentArgs
                     for (int j = 0; j < 8; ++j)
                         v[j] = t.cb4[(word >> (4 * j)) & 15u] * s;
                 } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        v[j] = k + j < a.n_in ? element_of(w, t, lb, e0 + j) : 0.0f;
+                    octet_of(w, t, lb, last_byte, e0, static_cast<int>(a.n_in - k < 8 ? a.n_in - k : 8), v);
                 }
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
@@ -205,9 +221,8 @@ __global__ __launch_bounds__(kThreads) void weight_fragments_kernel(FragmentArgs
                         for (int f = 0; f < 8; ++f)
                             v[h][f] = t.cb4[(word >> (4 * f)) & 15u] * s;
                     } else {
-#pragma unroll
-                        for (int f = 0; f < 8; ++f)
-                            v[h][f] = j0 + f < a.n_in ? element_of(w, t, lb, e0 + f) : 0.0f;
+                        octet_of(w, t, lb, last_byte, e0,
+                                 static_cast<int>(a.n_in - j0 < 8 ? a.n_in - j0 : 8), v[h]);
                     }
                 }
 #pragma unroll
@@ -388,6 +403,25 @@ __device__ __forceinline__ void finish_gated(const ProductArgs &a, int64_t row, 
 
 constexpr int kFinishLd = kGroup + 4;  // floats per row of a wave's epilogue slab
 
+// Rows 4 it .. 4 it + 3 of a slab of 16 rows: a lane finishes 8 columns of one.
+template <int OUT, bool kGated>
+__device__ __forceinline__ void finish_slab_rows(const ProductArgs &a, const float *slab,
+                                                 int64_t row0, int group, int it, int lane)
+{
+    const int g = lane >> 4, c = lane & 15;
+    const float *from = slab + (it * 4 + g) * kFinishLd + 8 * c;
+    const f32x4 lo = *reinterpret_cast<const f32x4 *>(from);
+    const f32x4 hi = *reinterpret_cast<const f32x4 *>(from + 4);
+    const int64_t row = row0 + it * 4 + g;
+    if constexpr (kGated) {
+        float gv[4] = {lo[0], lo[1], lo[2], lo[3]}, uv[4] = {hi[0], hi[1], hi[2], hi[3]};
+        finish_gated<OUT>(a, row, a.n0 + static_cast<int64_t>(group) * 64 + 4 * c, gv, uv);
+    } else {
+        float z[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+        finish_linear<OUT>(a, row, a.n0 + static_cast<int64_t>(group) * kGroup + 8 * c, z);
+    }
+}
+
 // The epilogue of one wave's 128 columns x 16 TF rows.  16 rows at a time pass
 // through a slab of LDS that only this wave uses: a lane holds 8 neighbouring
 // columns of one row per D register, so the slab takes and gives whole
@@ -412,19 +446,8 @@ __device__ __forceinline__ void finish_wave(const ProductArgs &a, const f32x4 (&
         __asm__ volatile("" ::: "memory");
         __builtin_amdgcn_wave_barrier();
 #pragma unroll 1
-        for (int it = 0; it < 4; ++it) {
-            const float *from = slab + (it * 4 + g) * kFinishLd + 8 * c;
-            const f32x4 lo = *reinterpret_cast<const f32x4 *>(from);
-            const f32x4 hi = *reinterpret_cast<const f32x4 *>(from + 4);
-            const int64_t row = row0 + t * 16 + it * 4 + g;
-            if constexpr (kGated) {
-                float gv[4] = {lo[0], lo[1], lo[2], lo[3]}, uv[4] = {hi[0], hi[1], hi[2], hi[3]};
-                finish_gated<OUT>(a, row, a.n0 + static_cast<int64_t>(group) * 64 + 4 * c, gv, uv);
-            } else {
-                float z[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-                finish_linear<OUT>(a, row, a.n0 + static_cast<int64_t>(group) * kGroup + 8 * c, z);
-            }
-        }
+        for (int it = 0; it < 4; ++it)
+            finish_slab_rows<OUT, kGated>(a, slab, row0 + t * 16, group, it, lane);
         __asm__ volatile("" ::: "memory");
         __builtin_amdgcn_wave_barrier();
     }
@@ -723,12 +746,13 @@ __global__ __launch_bounds__(512) void fragment_product_wide_kernel(ProductArgs 
 }
 
 // The splits' sums of one wave's 128 columns x 16 rows, added in order, and
-// the epilogue.
+// the epilogue.  Four waves share the 8 fragments, so that a wave has the
+// loads of 8 splits in flight: the kernel is short and its time is latency.
 template <int OUT, bool kGated, int WN, int WT, int TF>
-__global__ __launch_bounds__(64) void product_reduce_kernel(ProductArgs a, int32_t tiles)
+__global__ __launch_bounds__(256) void product_reduce_kernel(ProductArgs a, int32_t tiles)
 {
     __shared__ __attribute__((aligned(16))) float slab[16 * kFinishLd];
-    const int lane = threadIdx.x;
+    const int lane = threadIdx.x & 63, q = threadIdx.x >> 6;
     const int t = blockIdx.y;
     const int tile = blockIdx.x / (WN * WT), wave = blockIdx.x % (WN * WT);
     const int wn = wave % WN, wt = wave / WN;
@@ -738,19 +762,33 @@ __global__ __launch_bounds__(64) void product_reduce_kernel(ProductArgs a, int32
     if (group >= a.groups || row0 >= a.m)
         return;
     const f32x4 *from = a.partial + (static_cast<int64_t>(tile) * (WN * WT) + wave) * (kFrags * TF * 64) +
-                        t * 64 + lane;
+                        (2 * q * TF + t) * 64 + lane;
     const int64_t split_step = static_cast<int64_t>(tiles) * (WN * WT) * (kFrags * TF * 64);
-    f32x4 acc[kFrags][1];
+    f32x4 acc[2];
 #pragma unroll
-    for (int f = 0; f < kFrags; ++f)
-        acc[f][0] = from[f * TF * 64];
-    for (int s = 1; s < a.splits; ++s) {
-        from += split_step;
+    for (int f = 0; f < 2; ++f)
+        acc[f] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int s = 0; s < a.splits; s += 8) {
+        f32x4 part[8][2];
 #pragma unroll
-        for (int f = 0; f < kFrags; ++f)
-            acc[f][0] = acc[f][0] + from[f * TF * 64];
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int f = 0; f < 2; ++f)  // past the last split: the first again, left out below
+                part[i][f] = from[(s + i < a.splits ? s + i : s) * split_step + f * TF * 64];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (s + i < a.splits)
+#pragma unroll
+                for (int f = 0; f < 2; ++f)
+                    acc[f] = acc[f] + part[i][f];
     }
-    finish_wave<OUT, kGated, 1>(a, acc, slab, row0, group, lane);
+    const int g = lane >> 4, c = lane & 15;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<f32x2 *>(slab + c * kFinishLd + 8 * (4 * g + i) + 2 * q) =
+            f32x2{acc[0][i], acc[1][i]};
+    __syncthreads();
+    finish_slab_rows<OUT, kGated>(a, slab, row0, group, q, lane);
 }
 
 // ---------------------------------------------------------------------------
@@ -1739,13 +1777,15 @@ struct SlopeArgs {
 
 // dz = T(dy act'(pre)), or dgate and dup.  A thread takes N neighbouring columns
 // (8, a 16-byte load, where every matrix has 16-byte aligned rows; else 1) and
-// every eighth row of a block of rows; the column sums of the unrounded
+// every 32nd row of a block of rows; the column sums of the unrounded
 // products (the bias gradient) are FP32 additions in a fixed order: a thread's
-// rows, then the eight threads of a column.  Bound by memory.
+// rows, then the 32 threads of a column.  Bound by memory.
+constexpr int kSlopeRows = 32;
+
 template <int OUT, bool kGated, int N>
-__global__ __launch_bounds__(kThreads) void activation_slope_kernel(SlopeArgs a)
+__global__ __launch_bounds__(32 * kSlopeRows) void activation_slope_kernel(SlopeArgs a)
 {
-    __shared__ float sums[8][32 * N];
+    __shared__ float sums[kSlopeRows][32 * N];
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
     const int64_t c = (static_cast<int64_t>(blockIdx.x) * 32 + tx) * N;
     const int64_t width = a.pad[0] ? a.ld_pad : a.n;
@@ -1753,7 +1793,7 @@ __global__ __launch_bounds__(kThreads) void activation_slope_kernel(SlopeArgs a)
     const int64_t r1 = r0 + a.rows_per_block < a.m ? r0 + a.rows_per_block : a.m;
     float sum[N] = {};
     if (c < width) {
-        for (int64_t r = r0 + ty; r < r1; r += 8) {
+        for (int64_t r = r0 + ty; r < r1; r += kSlopeRows) {
             float z0[N] = {}, z1[N] = {};
             if (c < a.n) {
                 float dy[N], pre[N], up[N];
@@ -1796,10 +1836,10 @@ __global__ __launch_bounds__(kThreads) void activation_slope_kernel(SlopeArgs a)
             for (int j = 0; j < N; ++j)
                 sums[ty][tx * N + j] = sum[j];
             __syncthreads();
-            for (int i = threadIdx.x; i < 32 * N; i += kThreads) {
+            for (int i = threadIdx.x; i < 32 * N; i += 32 * kSlopeRows) {
                 float total = sums[0][i];
 #pragma unroll
-                for (int q = 1; q < 8; ++q)
+                for (int q = 1; q < kSlopeRows; ++q)
                     total = total + sums[q][i];
                 const int64_t col = static_cast<int64_t>(blockIdx.x) * (32 * N) + i;
                 if (col < a.n)
@@ -1933,7 +1973,12 @@ struct Shape {
     }
 };
 
-constexpr int64_t kRowBlock = 64;  // rows per block of column sums
+// Rows per block of column sums: 64, and for small matrices enough that one
+// block takes them all and no second kernel has to add the blocks' sums.
+int64_t row_block(int64_t m, int64_t n)
+{
+    return m <= 256 && m * n <= (int64_t{1} << 19) ? 256 : 64;
+}
 
 // Workspace: [padded x copies][column sums][fragments of a window of groups]
 int64_t copy_bytes(const Shape &s, bool copy)
@@ -1943,7 +1988,7 @@ int64_t copy_bytes(const Shape &s, bool copy)
 
 int64_t partial_bytes(int64_t m, int64_t n)
 {
-    return align256(ceil_div(m, kRowBlock) * n * 4);
+    return align256(ceil_div(m, row_block(m, n)) * n * 4);
 }
 
 int64_t workspace_need(const Shape &s, int64_t fixed, bool least)
@@ -2018,7 +2063,7 @@ dq4_status_t launch_product_tile(ProductArgs a, hipStream_t s)
     int32_t n_tiles = static_cast<int32_t>(tiles);
     void *rp[] = {&a, &n_tiles};
     return launch(reinterpret_cast<const void *>(&product_reduce_kernel<OUT, kGated, WN, WT, TF>),
-                  tiles * WN * WT, TF, 64, rp, s);
+                  tiles * WN * WT, TF, 256, rp, s);
 }
 
 template <int OUT, bool kGated>
@@ -2261,8 +2306,8 @@ dq4_status_t launch_slope(const SlopeArgs &args, int32_t dtype, hipStream_t s)
         kernel = vec ? reinterpret_cast<const void *>(&activation_slope_kernel<DQ4_BF16, kGated, 8>)
                      : reinterpret_cast<const void *>(&activation_slope_kernel<DQ4_BF16, kGated, 1>);
     void *params[] = {&a};
-    return launch(kernel, ceil_div(a.pad[0] ? a.ld_pad : a.n, vec ? 256 : 32), ceil_div(a.m, kRowBlock),
-                  kThreads, params, s);
+    return launch(kernel, ceil_div(a.pad[0] ? a.ld_pad : a.n, vec ? 256 : 32), ceil_div(a.m, a.rows_per_block),
+                  32 * kSlopeRows, params, s);
 }
 
 dq4_status_t copy_rows(const void *x, int64_t ld, int64_t m, int64_t k, void *out, hipStream_t s)
@@ -2528,12 +2573,12 @@ dq4_status_t dq4_linear_fused_backward(const dq4_weight_t *w, int64_t n_out, int
             p.x[0] = p.x[1] = a.pad[0];
             p.ld_x = p.k = a.ld_pad;
         }
-        const int64_t blocks = ceil_div(m, kRowBlock);
+        a.rows_per_block = static_cast<int32_t>(row_block(m, n_out));
+        const int64_t blocks = ceil_div(m, a.rows_per_block);
         a.partial = !dbias ? nullptr : blocks == 1 ? dbias : reinterpret_cast<float *>(ws + copied);
         a.m = m;
         a.n = n_out;
         a.act = activation;
-        a.rows_per_block = static_cast<int32_t>(kRowBlock);
         dq4_status_t ls = launch_slope<false>(a, dtype, s);
         if (ls != DQ4_OK)
             return ls;
@@ -2614,7 +2659,7 @@ dq4_status_t dq4_gated_fused_backward(const dq4_weight_t *gate, const dq4_weight
         a.m = m;
         a.n = n_ff;
         a.act = activation;
-        a.rows_per_block = static_cast<int32_t>(kRowBlock);
+        a.rows_per_block = 64;
         const dq4_status_t ls = launch_slope<true>(a, dtype, s);
         if (ls != DQ4_OK)
             return ls;
