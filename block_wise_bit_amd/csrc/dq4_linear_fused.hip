@@ -812,6 +812,69 @@ struct RowsArgs {
 // 4.4, a single table 26).
 constexpr int kPairTableBytes = 256 * 32 * 8;
 
+// A barrier for LDS alone: it does not wait for the loads that the wave has
+// under way from memory, as __syncthreads() does.
+__device__ __forceinline__ void lds_barrier()
+{
+    __asm__ volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    __asm__ volatile("" ::: "memory");
+}
+
+// The codebooks' way into LDS, in two parts: `fetch_codebooks` goes before a
+// kernel's first weight loads (loads return in order: behind them the tables
+// would wait for the weight), `fill_tables` after them.  It fills kTables
+// tables (kTables == 1 and two weights: one table of both, 16 copies each),
+// the row of zeros behind them and the scale codebooks; every thread of the
+// workgroup (256 or more) calls it, and it ends on a barrier.  The 16 values
+// pass through LDS: taken from memory entry by entry they cost 5 us at the
+// start of every call.
+struct Codebooks {
+    float scb[2];
+    float cb4;
+};
+
+template <int kWeights>
+__device__ __forceinline__ Codebooks fetch_codebooks(const Weight (&w)[2])
+{
+    const int tid = threadIdx.x, threads = blockDim.x;
+    // without branches: a load that some threads skip makes the compiler lose
+    // count of the loads under way, and wait for all of them
+    Codebooks c;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const int i = (tid + q * threads) % (kWeights * 256);
+        c.scb[q] = w[kWeights == 2 ? i >> 8 : 0].scale_codebook[i & 255];
+    }
+    c.cb4 = w[kWeights == 2 ? (tid >> 4) & 1 : 0].codebook4[tid & 15];
+    return c;
+}
+
+template <int kWeights, int kTables>
+__device__ __forceinline__ void fill_tables(const Codebooks &c, uint8_t *table,
+                                            float (&scb)[kWeights][256], float (&cb4)[kWeights][16])
+{
+    const int tid = threadIdx.x, threads = blockDim.x;
+    // every thread stores (the rest over the table that is filled below), so
+    // that no load is moved behind a branch
+    float *rest = reinterpret_cast<float *>(table) + tid;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const int i = tid + q * threads;
+        *(i < kWeights * 256 ? &scb[i >> 8][i & 255] : rest) = c.scb[q];
+    }
+    *(tid < kWeights * 16 ? &cb4[tid >> 4][tid & 15] : rest) = c.cb4;
+    if (tid < 64)
+        *reinterpret_cast<uint32_t *>(&table[kTables * kPairTableBytes + tid * 4]) = 0;
+    lds_barrier();
+#pragma unroll 8
+    for (int i = tid; i < kTables * 256 * 32; i += threads) {
+        const int b = (i >> 5) & 255, which = kTables == 2 ? i >> 13 : kWeights == 2 ? i & 1 : 0;
+        *reinterpret_cast<f32x2 *>(&table[i * 8]) = f32x2{cb4[which][b & 15], cb4[which][b >> 4]};
+    }
+    lds_barrier();
+}
+
 struct Pairs {
     f32x2 v[4];  // the eight codebook values of a packed dword
 };
@@ -906,7 +969,7 @@ __global__ __launch_bounds__(64 * WAVES) void ragged_rows_kernel(RowsArgs a)
     constexpr int kSpan = 128;                   // k per chunk
     constexpr int kBounds = 2;                   // blocks a lane's 32 k may touch
     __shared__ __attribute__((aligned(1024))) uint8_t table[kPairTableBytes + 256];
-    __shared__ float scb[kW][256];
+    __shared__ float scb[kW][256], cb4[kW][16];
     __shared__ __attribute__((aligned(16))) f32x4 partial[WAVES][R][64];
 
     const int tid = threadIdx.x;
@@ -983,6 +1046,7 @@ __global__ __launch_bounds__(64 * WAVES) void ragged_rows_kernel(RowsArgs a)
                 rsrc(rs_x), k < static_cast<uint32_t>(a.out.k) ? x_row[t] + k * 2 : 0x80000000u, 0, 0);
     };
 
+    const Codebooks codebooks = fetch_codebooks<kW>(a.w);
     Loads cur;
     int64_t load_rb = blockIdx.x;
     int load_c = wk;
@@ -996,19 +1060,7 @@ __global__ __launch_bounds__(64 * WAVES) void ragged_rows_kernel(RowsArgs a)
     }
 
     // the lookup tables, while the first loads are in flight
-#pragma unroll
-    for (int w = 0; w < kW; ++w) {
-        if (tid < 256)
-            scb[w][tid] = a.w[w].scale_codebook[tid];
-    }
-    for (int i = tid; i < 256 * 32; i += 64 * WAVES) {
-        const int b = i >> 5;
-        const float *cb4 = a.w[kGated ? i & 1 : 0].codebook4;
-        *reinterpret_cast<f32x2 *>(&table[i * 8]) = f32x2{cb4[b & 15], cb4[b >> 4]};
-    }
-    if (tid < 64)
-        *reinterpret_cast<uint32_t *>(&table[kPairTableBytes + tid * 4]) = 0;
-    __syncthreads();
+    fill_tables<kW, 1>(codebooks, table, scb, cb4);
 
     const uint32_t lane_byte = kGated ? (lane & 15) * 16 : (lane & 31) * 8;
     for (int64_t rb = blockIdx.x; rb < a.row_blocks; rb += gridDim.x) {
@@ -1063,11 +1115,11 @@ __global__ __launch_bounds__(64 * WAVES) void ragged_rows_kernel(RowsArgs a)
         // the k-waves' partial sums, 16 rows of x at a time
 #pragma unroll
         for (int t = 0; t < TF; ++t) {
-            __syncthreads();
+            lds_barrier();
 #pragma unroll
             for (int f = 0; f < R; ++f)
                 partial[wave][f][lane] = acc[f][t];
-            __syncthreads();
+            lds_barrier();
             for (int i = tid; i < kPer * 64; i += 64 * WAVES) {
                 const int ln = i & 63, f = i >> 6;
                 f32x4 sum = partial[0][f][ln];
@@ -1107,7 +1159,7 @@ __global__ __launch_bounds__(64 * kDecodeWaves) void weight_row_fragments_kernel
 {
     constexpr int kW = kTwo ? 2 : 1;
     __shared__ __attribute__((aligned(1024))) uint8_t table[kPairTableBytes + 256];
-    __shared__ float scb[kW][256];
+    __shared__ float scb[kW][256], cb4[kW][16];
     __shared__ __attribute__((aligned(16))) uint8_t units[kDecodeWaves][4 * kUnitLd];
 
     const int tid = threadIdx.x;
@@ -1145,23 +1197,13 @@ __global__ __launch_bounds__(64 * kDecodeWaves) void weight_row_fragments_kernel
             }
         }
     };
+    const Codebooks codebooks = fetch_codebooks<kW>(a.w);
     int item = blockIdx.x * 2 + (wave >> 3);
     const int step = gridDim.x * 2;
     Loads cur;
     if (item < items)
         load(cur, item);
-#pragma unroll
-    for (int q = 0; q < kW; ++q)
-        if (tid < 256)
-            scb[q][tid] = a.w[q].scale_codebook[tid];
-    for (int i = tid; i < 256 * 32; i += 64 * kDecodeWaves) {
-        const int b = i >> 5;
-        const float *cb4 = a.w[kTwo ? i & 1 : 0].codebook4;
-        *reinterpret_cast<f32x2 *>(&table[i * 8]) = f32x2{cb4[b & 15], cb4[b >> 4]};
-    }
-    if (tid < 64)
-        *reinterpret_cast<uint32_t *>(&table[kPairTableBytes + tid * 4]) = 0;
-    __syncthreads();
+    fill_tables<kW, 1>(codebooks, table, scb, cb4);
 
     const uint32_t lane_byte = kTwo ? (lane & 15) * 16 + which * 8 : (lane & 31) * 8;
     const int chunks = a.chunks;
@@ -1230,10 +1272,6 @@ constexpr int kTokenSpan = 2048;   // k per wave and chunk
 constexpr int kTokenDepth = 3;     // pairs of row chunks in flight per wave
 constexpr int kTokenMaxChunks = 16;
 
-// Weight rows of one turn of a wave's ring.
-template <bool kGated>
-constexpr int kTokenRing = kTokenDepth * (kGated ? 1 : 2);
-
 template <int OUT>
 __device__ __forceinline__ void finish_one(const ProductArgs &a, int64_t row, int64_t n, float z)
 {
@@ -1251,13 +1289,13 @@ __device__ __forceinline__ void finish_one(const ProductArgs &a, int64_t row, in
 template <bool kGated>
 constexpr int kTokenPartials = kGated ? 6144 : 12288;
 
-template <int OUT, bool kGated, int M, int WAVES>
+template <int OUT, bool kGated, int M, int WAVES, int DEPTH>
 __global__ __launch_bounds__(64 * WAVES) void token_rows_kernel(TokenArgs a)
 {
     constexpr int kW = kGated ? 2 : 1;
     constexpr int kRows = kGated ? 1 : 2;  // weight rows of a pair of row chunks
     __shared__ __attribute__((aligned(1024))) uint8_t table[kW * kPairTableBytes + 256];
-    __shared__ float scb[kW][256];
+    __shared__ float scb[kW][256], cb4[kW][16];
     __shared__ __attribute__((aligned(16))) float partial[2][kTokenPartials<kGated> / 2];
     __shared__ float unused[64];
 
@@ -1282,7 +1320,7 @@ __global__ __launch_bounds__(64 * WAVES) void token_rows_kernel(TokenArgs a)
         uint32_t code;
         float absmax;
     };
-    Row ring[kTokenDepth][2];  // gated: a row of each weight; else two rows
+    Row ring[DEPTH][2];  // gated: a row of each weight; else two rows
     u32x4 x[M][4];
     uint32_t k_lane = 0, packed_off = 0;
     auto load_one = [&](Row &to, int w, int row) {
@@ -1311,6 +1349,9 @@ __global__ __launch_bounds__(64 * WAVES) void token_rows_kernel(TokenArgs a)
         for (int j = 0; j < 2; ++j)
             load_one(to[j], kGated ? j : 0, row0 + (i * kRows + (kGated ? 0 : j)) * WR + wr);
     };
+    const auto rs_x = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint16_t *>(a.out.x[0]), 0,
+        static_cast<int32_t>(((a.out.m - 1) * a.out.ld_x + a.out.k) * 2), kRawBufferWord3);
     auto enter_chunk = [&](int chunk) {
         k_lane = chunk * kTokenSpan + 32 * lane;
         packed_off = k_lane < n_in ? k_lane / 2 : 0x80000000u;
@@ -1318,30 +1359,20 @@ __global__ __launch_bounds__(64 * WAVES) void token_rows_kernel(TokenArgs a)
         for (int t = 0; t < M; ++t)
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
-                x[t][s] = u32x4{0, 0, 0, 0};
-                if (k_lane < n_in && t < a.out.m)
-                    x[t][s] = *reinterpret_cast<const u32x4 *>(a.out.x[0] + t * a.out.ld_x + k_lane + 8 * s);
+                // rows and k beyond x lie past the buffer: zeros
+                const uint32_t at = static_cast<uint32_t>(t * a.out.ld_x + k_lane + 8 * s) * 2;
+                x[t][s] = __builtin_amdgcn_raw_buffer_load_b128(
+                    rs_x, k_lane < n_in && t < a.out.m ? at : 0x80000000u, 0, 0);
             }
     };
 
+    const Codebooks codebooks = fetch_codebooks<kW>(a.w);
     // the first rows' loads go out before the tables are built
     enter_chunk(wk);
 #pragma unroll
-    for (int d = 0; d < kTokenDepth; ++d)
+    for (int d = 0; d < DEPTH; ++d)
         load(ring[d], row_first, d);
-#pragma unroll
-    for (int w = 0; w < kW; ++w) {
-        if (tid < 256)
-            scb[w][tid] = a.w[w].scale_codebook[tid];
-        for (int i = tid; i < 256 * 32; i += threads) {
-            const int b = i >> 5;
-            *reinterpret_cast<f32x2 *>(&table[w * kPairTableBytes + i * 8]) =
-                f32x2{a.w[w].codebook4[b & 15], a.w[w].codebook4[b >> 4]};
-        }
-    }
-    if (tid < 64)
-        *reinterpret_cast<uint32_t *>(&table[kW * kPairTableBytes + tid * 4]) = 0;
-    __syncthreads();
+    fill_tables<kW, kW>(codebooks, table, scb, cb4);
 
     const uint32_t lane_byte = (lane & 31) * 8;
     const int G = lane >> 4, c = lane & 15;
@@ -1357,7 +1388,7 @@ __global__ __launch_bounds__(64 * WAVES) void token_rows_kernel(TokenArgs a)
             if (passes > 1 && (pass > 0 || b0 != row_first)) {  // else the ring is filled
                 enter_chunk(chunk);
 #pragma unroll
-                for (int d = 0; d < kTokenDepth; ++d)
+                for (int d = 0; d < DEPTH; ++d)
                     load(ring[d], b0, d);
             }
             // a lane beyond the row (its loads gave zeros) reads the row of
@@ -1367,9 +1398,9 @@ __global__ __launch_bounds__(64 * WAVES) void token_rows_kernel(TokenArgs a)
 #pragma unroll
             for (int w = 0; w < kW; ++w)
                 from[w] = lane_byte + (beyond ? kW * kPairTableBytes : w * kPairTableBytes);
-            for (int i0 = 0; i0 * kRows * WR + wr < rows; i0 += kTokenDepth) {
+            for (int i0 = 0; i0 * kRows * WR + wr < rows; i0 += DEPTH) {
 #pragma unroll
-                for (int d = 0; d < kTokenDepth; ++d) {
+                for (int d = 0; d < DEPTH; ++d) {
                     const int i = i0 + d;
                     // a turn loads as often past the last row: were the number
                     // of loads in flight not known, every turn would begin by
@@ -1424,11 +1455,11 @@ __global__ __launch_bounds__(64 * WAVES) void token_rows_kernel(TokenArgs a)
                     }
                     // batches are whole rings long: with one pass the ring
                     // runs on into the next batch
-                    load(ring[d], b0, i + kTokenDepth);
+                    load(ring[d], b0, i + DEPTH);
                 }
             }
         }
-        __syncthreads();
+        lds_barrier();
         for (int i = tid; i < rows * M; i += threads) {
             const int r = i / M, t = i % M;
             if (t >= a.out.m)
@@ -1519,7 +1550,8 @@ __device__ __forceinline__ void transpose_quads(uint32_t (&v)[4], bool odd, bool
 // side (a load whose neighbouring lanes lie in 16 rows took 64 accesses of the
 // vector cache, this one 16): so a load takes 256 bytes of 4 rows, a quad of
 // lanes on 64 of them, and 4 such loads are transposed between the lanes of
-// each quad.  Waves along k (wk of them) meet in LDS, in a fixed order.  The
+// each quad; the scales are looked up four lanes to a row too, and handed over.
+// Waves along k (wk of them) meet in LDS, in a fixed order.  The
 // next chunk's loads, also those of the next row block, are in flight while a
 // chunk is multiplied; each x fragment is reloaded kAhead steps ahead.
 // S: blocks looked up per lane and 128 k (2: blocks of 64 k or more and n_in
@@ -1531,7 +1563,7 @@ __global__ __launch_bounds__(512) void batch_rows_kernel(RowsArgs a, const uint1
     constexpr int kPer = R / kW;
     constexpr int kSpan = 512;
     __shared__ __attribute__((aligned(1024))) uint8_t table[kPairTableBytes + 256];
-    __shared__ float scb[kW][256];
+    __shared__ float scb[kW][256], cb4[kW][16];
     __shared__ __attribute__((aligned(16))) f32x4 partial[8][R * TF][64];
 
     const int tid = threadIdx.x;
@@ -1595,7 +1627,8 @@ __global__ __launch_bounds__(512) void batch_rows_kernel(RowsArgs a, const uint1
                     rp, (((frag_row + row_load + q) * n_in + k) >> 1) | past, 0, 0);
 #pragma unroll
             for (int h = 0; h < S; ++h) {
-                const uint32_t e = (frag_row + (lane & 15)) * n_in + c * kSpan + 128 * g + h * (128 / S);
+                // of row lane / 4, the lane's quarter of the chunk
+                const uint32_t e = (frag_row + (lane >> 2)) * n_in + c * kSpan + 128 * (lane & 3) + h * (128 / S);
                 const uint32_t b = (phase + e) >> lb;
                 l.code[f][h] = __builtin_amdgcn_raw_buffer_load_b8(rc, b, 0, 0);
                 l.absmax[f][h] = __builtin_bit_cast(
@@ -1612,6 +1645,7 @@ __global__ __launch_bounds__(512) void batch_rows_kernel(RowsArgs a, const uint1
                 x_frags + ((static_cast<int64_t>(c) * 16 + step) * TF + t) * 512 + lane * 8);
     };
 
+    const Codebooks codebooks = fetch_codebooks<kW>(a.w);
     Loads cur;
     int64_t load_rb = blockIdx.x;
     int load_c = wk;  // wk < chunks: the host takes no more waves along k than chunks
@@ -1621,18 +1655,7 @@ __global__ __launch_bounds__(512) void batch_rows_kernel(RowsArgs a, const uint1
         load_x(load_c, st);
 
     // the lookup tables, while the first loads are in flight
-#pragma unroll
-    for (int w = 0; w < kW; ++w)
-        if (tid < 256)
-            scb[w][tid] = a.w[w].scale_codebook[tid];
-    for (int i = tid; i < 256 * 32; i += 512) {
-        const int b = i >> 5;
-        const float *cb4 = a.w[kGated ? i & 1 : 0].codebook4;
-        *reinterpret_cast<f32x2 *>(&table[i * 8]) = f32x2{cb4[b & 15], cb4[b >> 4]};
-    }
-    if (tid < 64)
-        *reinterpret_cast<uint32_t *>(&table[kPairTableBytes + tid * 4]) = 0;
-    __syncthreads();
+    fill_tables<kW, 1>(codebooks, table, scb, cb4);
 
     const uint32_t lane_byte = kGated ? (lane & 15) * 16 : (lane & 31) * 8;
     for (int64_t rb = blockIdx.x; rb < a.row_blocks; rb += gridDim.x) {
@@ -1658,9 +1681,13 @@ __global__ __launch_bounds__(512) void batch_rows_kernel(RowsArgs a, const uint1
 #pragma unroll
             for (int f = 0; f < R; ++f) {
 #pragma unroll
-                for (int h = 0; h < S; ++h)
-                    s[f][h] = block_scale(scb[kGated ? f : 0][cur.code[f][h]], cur.absmax[f][h],
-                                          a.w[kGated ? f : 0].offset);
+                for (int h = 0; h < S; ++h) {
+                    const float q = block_scale(scb[kGated ? f : 0][cur.code[f][h]], cur.absmax[f][h],
+                                                a.w[kGated ? f : 0].offset);
+                    // lane 16 g + r multiplies quarter g of row r
+                    s[f][h] = __builtin_bit_cast(
+                        float, __builtin_amdgcn_ds_bpermute((4 * (lane & 15) + g) * 4, __builtin_bit_cast(int, q)));
+                }
 #pragma unroll
                 for (int d = 0; d < 4; ++d) {
                     uint32_t v[4] = {cur.packed[f][0][d], cur.packed[f][1][d], cur.packed[f][2][d],
@@ -1716,13 +1743,13 @@ __global__ __launch_bounds__(512) void batch_rows_kernel(RowsArgs a, const uint1
             }
             cur = next;
         }
-        __syncthreads();  // the last row block's sums are read
+        lds_barrier();  // the last row block's sums are read
 #pragma unroll
         for (int f = 0; f < R; ++f)
 #pragma unroll
             for (int t = 0; t < TF; ++t)
                 partial[wave][f * TF + t][lane] = acc[f][t];
-        __syncthreads();
+        lds_barrier();
         for (int i = tid; i < WR * kPer * TF * 64; i += 512) {
             const int ln = i & 63, ft = (i >> 6) % (kPer * TF), row_wave = (i >> 6) / (kPer * TF);
             const int f = ft / TF, t = ft - f * TF;
@@ -2114,13 +2141,20 @@ dq4_status_t launch_token_rows(const RowsArgs &r, int cus, hipStream_t s)
     const int64_t grid = r.n_out < cus ? r.n_out : cus;
     a.rows_per = static_cast<int32_t>(r.n_out / grid);
     a.rows_extra = static_cast<int32_t>(r.n_out % grid);
-    const int ring = kTokenRing<kGated> * wr;  // rows of one turn of every wave's ring
+    const int pair = (kGated ? 1 : 2) * wr;  // rows of one pair of every wave
     const int fit = kTokenPartials<kGated> / 2 / (M * (kGated ? 2 : 1) * a.chunks * 4);
-    a.batch = fit / ring * ring;
     a.out = r.out;
     void *params[] = {&a};
-    return launch(reinterpret_cast<const void *>(&token_rows_kernel<OUT, kGated, M, kWaves>), grid, 1,
-                  64 * a.wk * wr, params, s);
+    // with a single pair for each wave there is nothing to load ahead: 4096 x
+    // 4096 at m = 1 10.6 us with a ring of three, TOKEN1 us with one
+    if (a.rows_per + (a.rows_extra ? 1 : 0) <= pair && pair <= fit) {
+        a.batch = pair;
+        return launch(reinterpret_cast<const void *>(&token_rows_kernel<OUT, kGated, M, kWaves, 1>), grid,
+                      1, 64 * a.wk * wr, params, s);
+    }
+    a.batch = fit / (kTokenDepth * pair) * (kTokenDepth * pair);
+    return launch(reinterpret_cast<const void *>(&token_rows_kernel<OUT, kGated, M, kWaves, kTokenDepth>),
+                  grid, 1, 64 * a.wk * wr, params, s);
 }
 
 template <int OUT, bool kGated, int TF>
