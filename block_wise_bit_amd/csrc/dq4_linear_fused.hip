@@ -43,7 +43,9 @@ constexpr int kFrags = 8;                    // fragments per group and k-step
 constexpr int kFragBytes = 1024;
 constexpr int kUnitBytes = 2 * kFrags * kFragBytes;  // one (group, chunk): 16 KiB
 constexpr int kXcds = 8;
-constexpr int64_t kMaxDim = int64_t{1} << 21;  // m, n_out, n_in: every grid and 32-bit offset below fits
+// m, n_out, n_in, and an m x n_out or m x n_in matrix: what keeps every grid and
+// 32-bit offset below in range.
+constexpr int64_t kMaxDim = int64_t{1} << 21, kMaxMatrix = int64_t{1} << 39;
 
 // How the fragments of a call are laid out from its weight or weights.
 enum Layout {
@@ -119,16 +121,210 @@ __device__ __forceinline__ void octet_of(const Weight &w, const Tables &t, int l
     }
 }
 
+template <int OUT, int N>
+__device__ __forceinline__ void load_values(const uint16_t *p, bool vec, int valid, float (&v)[N])
+{
+    if (vec) {
+        if constexpr (N == 8) {
+            const u32x4 q = *reinterpret_cast<const u32x4 *>(p);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                v[j] = Half<OUT>::widen((q[j / 2] >> (16 * (j & 1))) & 0xFFFFu);
+        } else if constexpr (N == 4) {
+            const u32x2 q = *reinterpret_cast<const u32x2 *>(p);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                v[j] = Half<OUT>::widen((q[j / 2] >> (16 * (j & 1))) & 0xFFFFu);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            v[j] = j < valid ? Half<OUT>::widen(p[j]) : 0.0f;
+    }
+}
+
+template <int OUT, int N>
+__device__ __forceinline__ void store_values(uint16_t *p, bool vec, int valid, const float (&v)[N])
+{
+    if (vec && N > 1) {
+        uint32_t q[N / 2 + 1];
+#pragma unroll
+        for (int j = 0; j < N / 2; ++j)
+            q[j] = Half<OUT>::pack2(v[2 * j], v[2 * j + 1]);
+        if constexpr (N == 8)
+            *reinterpret_cast<u32x4 *>(p) = u32x4{q[0], q[1], q[2], q[3]};
+        else if constexpr (N == 4)
+            *reinterpret_cast<u32x2 *>(p) = u32x2{q[0], q[1]};
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            if (j < valid)
+                p[j] = static_cast<uint16_t>(Half<OUT>::pack2(v[j], 0.0f));
+    }
+}
+
+// ---------------------------------------------------------------------------
+// what a call does beside the decode, before its product
+// ---------------------------------------------------------------------------
+// One row block of x rows (any alignment and stride) into rows of ld_out
+// elements, zeros from column k on: the form the product reads in 16-byte
+// pieces.
+struct CopyArgs {
+    const uint16_t *x;
+    int64_t ld_x, m, k;
+    uint16_t *out;
+    int64_t ld_out;
+};
+
+constexpr int kRowBlock = 32;  // rows of a block beside the decode
+
+__device__ __forceinline__ void copy_rows_zero_padded(const CopyArgs &a, int64_t bx, int64_t by)
+{
+    const int64_t c = bx * kThreads + threadIdx.x;
+    if (c >= a.ld_out)
+        return;
+    const int64_t r0 = by * kRowBlock, r1 = r0 + kRowBlock < a.m ? r0 + kRowBlock : a.m;
+#pragma unroll 8
+    for (int64_t r = r0; r < r1; ++r)
+        a.out[r * a.ld_out + c] = c < a.k ? a.x[r * a.ld_x + c] : static_cast<uint16_t>(0);
+}
+
+struct SlopeArgs {
+    const uint16_t *dy;
+    int64_t ld_dy;
+    const uint16_t *pre[2];     // z, or g and u
+    int64_t ld_pre;
+    uint16_t *dz[2];
+    int64_t ld_dz;
+    uint16_t *pad[2];           // padded copies for the product, or null
+    int64_t ld_pad;
+    float *partial;             // column sums, one row per row block, or null
+    int64_t m, n;
+    int32_t act;
+};
+
+// dz = T(dy act'(pre)), or dgate and dup, of one block of rows.  A thread takes
+// N neighbouring columns (8, a 16-byte load, where every matrix has 16-byte
+// aligned rows; else 1) and every eighth row; the column sums of the unrounded
+// products (the bias gradient) are FP32 additions in a fixed order: a thread's
+// rows, then the eight threads of a column.
+template <int OUT, bool kGated, int N>
+__device__ __forceinline__ void activation_slopes(const SlopeArgs &a, int64_t bx, int64_t by,
+                                                  float (&sums)[8][32 * N])
+{
+    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+    const int64_t c = (bx * 32 + tx) * N;
+    const int64_t width = a.pad[0] ? a.ld_pad : a.n;
+    const int64_t r0 = by * kRowBlock;
+    const int64_t r1 = r0 + kRowBlock < a.m ? r0 + kRowBlock : a.m;
+    float sum[N] = {};
+    if (c < width) {
+        for (int64_t r = r0 + ty; r < r1; r += 8) {
+            float z0[N] = {}, z1[N] = {};
+            if (c < a.n) {
+                float dy[N], pre[N], up[N];
+                load_values<OUT, N>(a.dy + r * a.ld_dy + c, N > 1, N, dy);
+                if (a.act != DQ4_ACT_NONE)
+                    load_values<OUT, N>(a.pre[0] + r * a.ld_pre + c, N > 1, N, pre);
+                if constexpr (kGated)
+                    load_values<OUT, N>(a.pre[1] + r * a.ld_pre + c, N > 1, N, up);
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    float value, slope;
+                    if constexpr (kGated) {
+                        act_and_slope_f32(a.act, pre[j], &value, &slope);
+                        z0[j] = dy[j] * up[j] * slope;
+                        z1[j] = dy[j] * value;
+                    } else {
+                        z0[j] = dy[j];
+                        if (a.act != DQ4_ACT_NONE) {
+                            act_and_slope_f32(a.act, pre[j], &value, &slope);
+                            z0[j] = dy[j] * slope;
+                        }
+                        sum[j] = sum[j] + z0[j];
+                    }
+                }
+                if (a.dz[0])
+                    store_values<OUT, N>(a.dz[0] + r * a.ld_dz + c, N > 1, N, z0);
+                if constexpr (kGated)
+                    store_values<OUT, N>(a.dz[1] + r * a.ld_dz + c, N > 1, N, z1);
+            }
+            if (a.pad[0]) {
+                store_values<OUT, N>(a.pad[0] + r * a.ld_pad + c, N > 1, N, z0);
+                if constexpr (kGated)
+                    store_values<OUT, N>(a.pad[1] + r * a.ld_pad + c, N > 1, N, z1);
+            }
+        }
+    }
+    if constexpr (!kGated) {
+        if (a.partial) {
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                sums[ty][tx * N + j] = sum[j];
+            __syncthreads();
+            for (int i = threadIdx.x; i < 32 * N; i += kThreads) {
+                float total = sums[0][i];
+#pragma unroll
+                for (int q = 1; q < 8; ++q)
+                    total = total + sums[q][i];
+                const int64_t col = bx * (32 * N) + i;
+                if (col < a.n)
+                    a.partial[by * a.n + col] = total;
+            }
+        }
+    }
+}
+
+// The work that goes with a decode launch.
+enum Beside {
+    kNothing = 0,
+    kCopy = 1,
+    kSlopes8 = 2,       // linear backward, 8 columns a thread
+    kSlopes1 = 3,
+    kGatedSlopes8 = 4,  // gated backward
+    kGatedSlopes1 = 5
+};
+
+struct BesideArgs {
+    int32_t blocks;     // workgroups of this work, after those of the decode
+    int32_t columns;    // of them, along the columns
+    CopyArgs copy;
+    SlopeArgs slope;
+};
+
+template <int OUT, int kBeside>
+__device__ __forceinline__ void work_beside(const BesideArgs &b, int block)
+{
+    const int by = block / b.columns, bx = block - by * b.columns;
+    if constexpr (kBeside == kCopy) {
+        copy_rows_zero_padded(b.copy, bx, by);
+    } else if constexpr (kBeside >= kSlopes8) {
+        constexpr bool kGated = kBeside >= kGatedSlopes8;
+        constexpr int N = kBeside == kSlopes8 || kBeside == kGatedSlopes8 ? 8 : 1;
+        __shared__ float sums[8][32 * N];
+        activation_slopes<OUT, kGated, N>(b.slope, bx, by, sums);
+    }
+}
+
 // Decode into fragments.  kForward: k runs along the weight's rows (n_in), a
 // 16-byte unit is 8 neighbouring elements of one row, one packed dword.
 // Backward: k runs down the weight's columns; a thread takes the dwords of 8
 // rows (8 columns each) and writes 8 units, each pairing the same column of
 // the 8 rows.  kAligned: rows start on packed dwords (n_in % 8 == 0, 4-byte
 // aligned codes); otherwise eight elements are cut out of two dwords.
-// Bound by memory: 0.5 B read and 2 B written per element.
-template <int OUT, bool kForward, bool kAligned>
-__global__ __launch_bounds__(kThreads) void weight_fragments_kernel(FragmentArgs a)
+// Bound by memory: 0.5 B read and 2 B written per element.  Workgroups behind
+// the decode's do the call's other work before the product (kBeside), which
+// does not depend on the weight: one launch, and neither waits for the other.
+template <int OUT, bool kForward, bool kAligned, int kBeside>
+__global__ __launch_bounds__(kThreads) void weight_fragments_kernel(FragmentArgs a, BesideArgs b)
 {
+    if constexpr (kBeside != kNothing) {
+        const int first = static_cast<int>(gridDim.x) - b.blocks;
+        if (static_cast<int>(blockIdx.x) >= first) {
+            work_beside<OUT, kBeside>(b, static_cast<int>(blockIdx.x) - first);
+            return;
+        }
+    }
     __shared__ Tables tables[2];
     const int n_weights = a.layout == kSingle ? 1 : 2;
     load_tables(a.w[0], tables[0]);
@@ -263,7 +459,25 @@ struct ProductArgs {
     int64_t ld_y;
     uint16_t *pre[2];
     int64_t ld_pre;
+    const float *bias_partial;  // column sums of row blocks, added up by workgroups
+    float *dbias;               // of their own (blockIdx.y == splits), or null
+    int64_t bias_n;
+    int32_t bias_blocks;
 };
+
+// dbias[c] = the row blocks' sums, added in order.
+__device__ __forceinline__ void add_bias_blocks(const float *partial, int64_t n, int32_t blocks,
+                                                float *dbias)
+{
+    for (int64_t c = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; c < n;
+         c += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+        float sum = 0.0f;
+#pragma unroll 8
+        for (int32_t b = 0; b < blocks; ++b)
+            sum = sum + partial[b * n + c];
+        dbias[c] = sum;
+    }
+}
 
 __device__ __forceinline__ uint32_t lds_offset(const void *p)
 {
@@ -304,48 +518,6 @@ __device__ __forceinline__ void wait_all_and_barrier()
     __asm__ volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
     __asm__ volatile("" ::: "memory");
-}
-
-template <int OUT, int N>
-__device__ __forceinline__ void load_values(const uint16_t *p, bool vec, int valid, float (&v)[N])
-{
-    if (vec) {
-        if constexpr (N == 8) {
-            const u32x4 q = *reinterpret_cast<const u32x4 *>(p);
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                v[j] = Half<OUT>::widen((q[j / 2] >> (16 * (j & 1))) & 0xFFFFu);
-        } else if constexpr (N == 4) {
-            const u32x2 q = *reinterpret_cast<const u32x2 *>(p);
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                v[j] = Half<OUT>::widen((q[j / 2] >> (16 * (j & 1))) & 0xFFFFu);
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < N; ++j)
-            v[j] = j < valid ? Half<OUT>::widen(p[j]) : 0.0f;
-    }
-}
-
-template <int OUT, int N>
-__device__ __forceinline__ void store_values(uint16_t *p, bool vec, int valid, const float (&v)[N])
-{
-    if (vec && N > 1) {
-        uint32_t q[N / 2 + 1];
-#pragma unroll
-        for (int j = 0; j < N / 2; ++j)
-            q[j] = Half<OUT>::pack2(v[2 * j], v[2 * j + 1]);
-        if constexpr (N == 8)
-            *reinterpret_cast<u32x4 *>(p) = u32x4{q[0], q[1], q[2], q[3]};
-        else if constexpr (N == 4)
-            *reinterpret_cast<u32x2 *>(p) = u32x2{q[0], q[1]};
-    } else {
-#pragma unroll
-        for (int j = 0; j < N; ++j)
-            if (j < valid)
-                p[j] = static_cast<uint16_t>(Half<OUT>::pack2(v[j], 0.0f));
-    }
 }
 
 // Outputs of one row: columns n0 .. n0 + 7 of a linear call.
@@ -466,6 +638,10 @@ __global__ __launch_bounds__(64 * WN * WT) void fragment_product_kernel(ProductA
     constexpr int kWaves = WN * WT;
     constexpr int kWLoads = WN * 16 / kWaves;          // 1 KiB loads per wave and chunk
     constexpr int kXLoads = 2 * TF * WT / kWaves;
+    if (static_cast<int>(blockIdx.y) == a.splits) {
+        add_bias_blocks(a.bias_partial, a.bias_n, a.bias_blocks, a.dbias);
+        return;
+    }
     __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kStage];
     static_assert(kWaves * 16 * kFinishLd * 4 <= 2 * kStage, "the epilogue slabs fit the stages");
 
@@ -608,6 +784,10 @@ __global__ __launch_bounds__(512) void fragment_product_wide_kernel(ProductArgs 
     constexpr int kRows = 16 * TF * WT;
     constexpr int kStepW = kFrags * kFragBytes;      // one group's fragments of one k-step
     constexpr int kStage = WN * kStepW + kRows * 64;  // 32 KiB
+    if (static_cast<int>(blockIdx.y) == a.splits) {
+        add_bias_blocks(a.bias_partial, a.bias_n, a.bias_blocks, a.dbias);
+        return;
+    }
     __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * kStage];
     static_assert(8 * 16 * kFinishLd * 4 <= 4 * kStage, "the epilogue slabs fit the stages");
 
@@ -1772,122 +1952,13 @@ __global__ __launch_bounds__(512) void batch_rows_kernel(RowsArgs a, const uint1
 }
 
 // ---------------------------------------------------------------------------
-// rows copied into a padded matrix, and the backward elementwise pass
+// the bias gradient on its own
 // ---------------------------------------------------------------------------
-// x rows (any alignment and stride) into rows of ld_out elements, zeros from
-// column k on: the form the product reads in 16-byte pieces.
-__global__ __launch_bounds__(kThreads) void rows_zero_fill_copy(const uint16_t *x, int64_t ld_x,
-                                                                int64_t m, int64_t k,
-                                                                uint16_t *out, int64_t ld_out)
-{
-    const int64_t c = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-    if (c >= ld_out)
-        return;
-    for (int64_t r = blockIdx.y; r < m; r += gridDim.y)
-        out[r * ld_out + c] = c < k ? x[r * ld_x + c] : static_cast<uint16_t>(0);
-}
-
-struct SlopeArgs {
-    const uint16_t *dy;
-    int64_t ld_dy;
-    const uint16_t *pre[2];     // z, or g and u
-    int64_t ld_pre;
-    uint16_t *dz[2];
-    int64_t ld_dz;
-    uint16_t *pad[2];           // padded copies for the product, or null
-    int64_t ld_pad;
-    float *partial;             // column sums, one row per row block, or null
-    int64_t m, n;
-    int32_t act;
-    int32_t rows_per_block;
-};
-
-// dz = T(dy act'(pre)), or dgate and dup.  A thread takes N neighbouring columns
-// (8, a 16-byte load, where every matrix has 16-byte aligned rows; else 1) and
-// every 32nd row of a block of rows; the column sums of the unrounded
-// products (the bias gradient) are FP32 additions in a fixed order: a thread's
-// rows, then the 32 threads of a column.  Bound by memory.
-constexpr int kSlopeRows = 32;
-
-template <int OUT, bool kGated, int N>
-__global__ __launch_bounds__(32 * kSlopeRows) void activation_slope_kernel(SlopeArgs a)
-{
-    __shared__ float sums[kSlopeRows][32 * N];
-    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-    const int64_t c = (static_cast<int64_t>(blockIdx.x) * 32 + tx) * N;
-    const int64_t width = a.pad[0] ? a.ld_pad : a.n;
-    const int64_t r0 = static_cast<int64_t>(blockIdx.y) * a.rows_per_block;
-    const int64_t r1 = r0 + a.rows_per_block < a.m ? r0 + a.rows_per_block : a.m;
-    float sum[N] = {};
-    if (c < width) {
-        for (int64_t r = r0 + ty; r < r1; r += kSlopeRows) {
-            float z0[N] = {}, z1[N] = {};
-            if (c < a.n) {
-                float dy[N], pre[N], up[N];
-                load_values<OUT, N>(a.dy + r * a.ld_dy + c, N > 1, N, dy);
-                if (a.act != DQ4_ACT_NONE)
-                    load_values<OUT, N>(a.pre[0] + r * a.ld_pre + c, N > 1, N, pre);
-                if constexpr (kGated)
-                    load_values<OUT, N>(a.pre[1] + r * a.ld_pre + c, N > 1, N, up);
-#pragma unroll
-                for (int j = 0; j < N; ++j) {
-                    float value, slope;
-                    if constexpr (kGated) {
-                        act_and_slope_f32(a.act, pre[j], &value, &slope);
-                        z0[j] = dy[j] * up[j] * slope;
-                        z1[j] = dy[j] * value;
-                    } else {
-                        z0[j] = dy[j];
-                        if (a.act != DQ4_ACT_NONE) {
-                            act_and_slope_f32(a.act, pre[j], &value, &slope);
-                            z0[j] = dy[j] * slope;
-                        }
-                        sum[j] = sum[j] + z0[j];
-                    }
-                }
-                if (a.dz[0])
-                    store_values<OUT, N>(a.dz[0] + r * a.ld_dz + c, N > 1, N, z0);
-                if constexpr (kGated)
-                    store_values<OUT, N>(a.dz[1] + r * a.ld_dz + c, N > 1, N, z1);
-            }
-            if (a.pad[0]) {
-                store_values<OUT, N>(a.pad[0] + r * a.ld_pad + c, N > 1, N, z0);
-                if constexpr (kGated)
-                    store_values<OUT, N>(a.pad[1] + r * a.ld_pad + c, N > 1, N, z1);
-            }
-        }
-    }
-    if constexpr (!kGated) {
-        if (a.partial) {
-#pragma unroll
-            for (int j = 0; j < N; ++j)
-                sums[ty][tx * N + j] = sum[j];
-            __syncthreads();
-            for (int i = threadIdx.x; i < 32 * N; i += 32 * kSlopeRows) {
-                float total = sums[0][i];
-#pragma unroll
-                for (int q = 1; q < kSlopeRows; ++q)
-                    total = total + sums[q][i];
-                const int64_t col = static_cast<int64_t>(blockIdx.x) * (32 * N) + i;
-                if (col < a.n)
-                    a.partial[static_cast<int64_t>(blockIdx.y) * a.n + col] = total;
-            }
-        }
-    }
-}
-
-// dbias[c] = the row blocks' sums, added in order.
 __global__ __launch_bounds__(kThreads) void bias_grad_reduce_kernel(const float *partial,
                                                                     int64_t n, int32_t blocks,
                                                                     float *dbias)
 {
-    const int64_t c = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-    if (c >= n)
-        return;
-    float sum = 0.0f;
-    for (int32_t b = 0; b < blocks; ++b)
-        sum = sum + partial[b * n + c];
-    dbias[c] = sum;
+    add_bias_blocks(partial, n, blocks, dbias);
 }
 
 // ---------------------------------------------------------------------------
@@ -2000,13 +2071,6 @@ struct Shape {
     }
 };
 
-// Rows per block of column sums: 64, and for small matrices enough that one
-// block takes them all and no second kernel has to add the blocks' sums.
-int64_t row_block(int64_t m, int64_t n)
-{
-    return m <= 256 && m * n <= (int64_t{1} << 19) ? 256 : 64;
-}
-
 // Workspace: [padded x copies][column sums][fragments of a window of groups]
 int64_t copy_bytes(const Shape &s, bool copy)
 {
@@ -2015,7 +2079,7 @@ int64_t copy_bytes(const Shape &s, bool copy)
 
 int64_t partial_bytes(int64_t m, int64_t n)
 {
-    return align256(ceil_div(m, row_block(m, n)) * n * 4);
+    return align256(ceil_div(m, kRowBlock) * n * 4);
 }
 
 int64_t workspace_need(const Shape &s, int64_t fixed, bool least)
@@ -2084,7 +2148,7 @@ dq4_status_t launch_product_tile(ProductArgs a, hipStream_t s)
         kernel = reinterpret_cast<const void *>(&fragment_product_wide_kernel<OUT, kGated>);
     else
         kernel = reinterpret_cast<const void *>(&fragment_product_kernel<OUT, kGated, WN, WT, TF>);
-    dq4_status_t st = launch(kernel, tiles, a.splits, 64 * WN * WT, params, s);
+    dq4_status_t st = launch(kernel, tiles, a.splits + (a.dbias ? 1 : 0), 64 * WN * WT, params, s);
     if (st != DQ4_OK || a.splits == 1)
         return st;
     int32_t n_tiles = static_cast<int32_t>(tiles);
@@ -2218,11 +2282,65 @@ dq4_status_t launch_few_rows(const RowsArgs &a, Route route, uint8_t *workspace,
     return launch_token_rows<OUT, kGated, 4>(a, cus, s);
 }
 
+// The work beside a decode: which, and in how many workgroups.
+struct BesideWork {
+    Beside kind;
+    BesideArgs args;
+};
+
+BesideWork copy_work(const void *x, int64_t ld, int64_t m, int64_t k, void *out)
+{
+    BesideWork w{kCopy, {}};
+    w.args.copy = CopyArgs{static_cast<const uint16_t *>(x), ld, m, k, static_cast<uint16_t *>(out),
+                           padded_ld(k)};
+    w.args.columns = static_cast<int32_t>(ceil_div(padded_ld(k), kThreads));
+    w.args.blocks = static_cast<int32_t>(ceil_div(m, kRowBlock)) * w.args.columns;
+    return w;
+}
+
+BesideWork slope_work(const SlopeArgs &a, bool gated)
+{
+    bool vec = rows_aligned(a.dy, a.ld_dy, a.m, a.n);
+    for (const void *p : {static_cast<const void *>(a.pre[0]), static_cast<const void *>(a.pre[1])})
+        vec = vec && (!p || rows_aligned(p, a.ld_pre, a.m, a.n));
+    for (const void *p : {static_cast<const void *>(a.dz[0]), static_cast<const void *>(a.dz[1])})
+        vec = vec && (!p || rows_aligned(p, a.ld_dz, a.m, a.n));
+    BesideWork w{gated ? (vec ? kGatedSlopes8 : kGatedSlopes1) : (vec ? kSlopes8 : kSlopes1), {}};
+    w.args.slope = a;
+    w.args.columns = static_cast<int32_t>(ceil_div(a.pad[0] ? a.ld_pad : a.n, vec ? 256 : 32));
+    w.args.blocks = static_cast<int32_t>(ceil_div(a.m, kRowBlock)) * w.args.columns;
+    return w;
+}
+
+template <int OUT, bool kForward, bool kAligned>
+const void *fragments_kernel(Beside kind)
+{
+    if constexpr (kForward) {
+        if (kind == kCopy)
+            return reinterpret_cast<const void *>(&weight_fragments_kernel<OUT, true, kAligned, kCopy>);
+        return reinterpret_cast<const void *>(&weight_fragments_kernel<OUT, true, kAligned, kNothing>);
+    } else {
+        switch (kind) {
+        case kSlopes8:
+            return reinterpret_cast<const void *>(&weight_fragments_kernel<OUT, false, kAligned, kSlopes8>);
+        case kSlopes1:
+            return reinterpret_cast<const void *>(&weight_fragments_kernel<OUT, false, kAligned, kSlopes1>);
+        case kGatedSlopes8:
+            return reinterpret_cast<const void *>(&weight_fragments_kernel<OUT, false, kAligned, kGatedSlopes8>);
+        case kGatedSlopes1:
+            return reinterpret_cast<const void *>(&weight_fragments_kernel<OUT, false, kAligned, kGatedSlopes1>);
+        default:
+            return reinterpret_cast<const void *>(&weight_fragments_kernel<OUT, false, kAligned, kNothing>);
+        }
+    }
+}
+
+// A decode of a.groups (none: 0) and the work beside it.
 template <int OUT, bool kForward>
-dq4_status_t launch_fragments(FragmentArgs a, bool aligned, int cus, hipStream_t s)
+dq4_status_t launch_fragments(FragmentArgs a, bool aligned, BesideWork beside, int cus, hipStream_t s)
 {
     const int64_t all_chunks = a.layout == kStacked ? 2 * a.chunks : a.chunks;
-    if (kForward && aligned && a.n_in % 32 == 0) {
+    if (kForward && aligned && a.n_in % 32 == 0 && beside.kind == kNothing) {
         int32_t spans = static_cast<int32_t>(ceil_div(all_chunks, 4));
         int64_t items64 = static_cast<int64_t>(a.groups) * spans;
         if (items64 > INT32_MAX / 2)
@@ -2236,13 +2354,12 @@ dq4_status_t launch_fragments(FragmentArgs a, bool aligned, int cus, hipStream_t
         const int64_t pairs = ceil_div(items, 2);
         return launch(kernel, pairs < cus ? pairs : cus, 1, 64 * kDecodeWaves, params, s);
     }
-    const int64_t grid = kForward ? a.groups * ceil_div(all_chunks, 4)
-                                  : ceil_div(a.groups, 2) * all_chunks;
-    void *params[] = {&a};
-    const void *kernel =
-        aligned ? reinterpret_cast<const void *>(&weight_fragments_kernel<OUT, kForward, true>)
-                : reinterpret_cast<const void *>(&weight_fragments_kernel<OUT, kForward, false>);
-    return launch(kernel, grid, 1, kThreads, params, s);
+    const int64_t grid = (kForward ? a.groups * ceil_div(all_chunks, 4)
+                                   : ceil_div(a.groups, 2) * all_chunks) + beside.args.blocks;
+    void *params[] = {&a, &beside.args};
+    return launch(aligned ? fragments_kernel<OUT, kForward, true>(beside.kind)
+                          : fragments_kernel<OUT, kForward, false>(beside.kind),
+                  grid, 1, kThreads, params, s);
 }
 
 Weight device_weight(const dq4_weight_t &w)
@@ -2254,7 +2371,8 @@ Weight device_weight(const dq4_weight_t &w)
 template <int OUT, bool kForward>
 dq4_status_t run_product(const Shape &sh, const dq4_weight_t *w0, const dq4_weight_t *w1,
                          int64_t n_out, int64_t n_in, int log2_block, ProductArgs p,
-                         uint8_t *fragments, int64_t fragment_bytes, hipStream_t s)
+                         BesideWork beside, uint8_t *fragments, int64_t fragment_bytes,
+                         hipStream_t s)
 {
     int device = 0;
     const hipError_t e = hipGetDevice(&device);
@@ -2266,6 +2384,11 @@ dq4_status_t run_product(const Shape &sh, const dq4_weight_t *w0, const dq4_weig
     if constexpr (kForward) {
         const Route route = route_of(w0, w1, n_in, sh.m);
         if (route != kProductRoute) {
+            if (beside.kind != kNothing) {
+                const dq4_status_t st = launch_fragments<OUT, true>(FragmentArgs{}, true, beside, cus, s);
+                if (st != DQ4_OK)
+                    return st;
+            }
             RowsArgs r{};
             r.w[0] = device_weight(*w0);
             r.w[1] = device_weight(w1 ? *w1 : *w0);
@@ -2305,9 +2428,10 @@ dq4_status_t run_product(const Shape &sh, const dq4_weight_t *w0, const dq4_weig
         f.group0 = static_cast<int32_t>(g0);
         f.groups = static_cast<int32_t>(groups - g0 < window ? groups - g0 : window);
         if (f.chunks > 0) {
-            const dq4_status_t st = launch_fragments<OUT, kForward>(f, aligned, cus, s);
+            const dq4_status_t st = launch_fragments<OUT, kForward>(f, aligned, beside, cus, s);
             if (st != DQ4_OK)
                 return st;
+            beside = BesideWork{kNothing, {}};  // it went with the first window
         }
         p.groups = f.groups;
         p.n0 = g0 * sh.per_group();
@@ -2319,39 +2443,9 @@ dq4_status_t run_product(const Shape &sh, const dq4_weight_t *w0, const dq4_weig
             st = launch_product<OUT, false>(p, plan, s);
         if (st != DQ4_OK)
             return st;
+        p.dbias = nullptr;
     }
     return DQ4_OK;
-}
-
-template <bool kGated>
-dq4_status_t launch_slope(const SlopeArgs &args, int32_t dtype, hipStream_t s)
-{
-    SlopeArgs a = args;
-    bool vec = rows_aligned(a.dy, a.ld_dy, a.m, a.n);
-    for (const void *p : {static_cast<const void *>(a.pre[0]), static_cast<const void *>(a.pre[1])})
-        vec = vec && (!p || rows_aligned(p, a.ld_pre, a.m, a.n));
-    for (const void *p : {static_cast<const void *>(a.dz[0]), static_cast<const void *>(a.dz[1])})
-        vec = vec && (!p || rows_aligned(p, a.ld_dz, a.m, a.n));
-    const void *kernel;
-    if (dtype == DQ4_F16)
-        kernel = vec ? reinterpret_cast<const void *>(&activation_slope_kernel<DQ4_F16, kGated, 8>)
-                     : reinterpret_cast<const void *>(&activation_slope_kernel<DQ4_F16, kGated, 1>);
-    else
-        kernel = vec ? reinterpret_cast<const void *>(&activation_slope_kernel<DQ4_BF16, kGated, 8>)
-                     : reinterpret_cast<const void *>(&activation_slope_kernel<DQ4_BF16, kGated, 1>);
-    void *params[] = {&a};
-    return launch(kernel, ceil_div(a.pad[0] ? a.ld_pad : a.n, vec ? 256 : 32), ceil_div(a.m, a.rows_per_block),
-                  32 * kSlopeRows, params, s);
-}
-
-dq4_status_t copy_rows(const void *x, int64_t ld, int64_t m, int64_t k, void *out, hipStream_t s)
-{
-    const uint16_t *src = static_cast<const uint16_t *>(x);
-    uint16_t *dst = static_cast<uint16_t *>(out);
-    int64_t ld_out = padded_ld(k);
-    void *params[] = {&src, &ld, &m, &k, &dst, &ld_out};
-    return launch(reinterpret_cast<const void *>(&rows_zero_fill_copy), ceil_div(ld_out, kThreads),
-                  m < 4096 ? m : 4096, kThreads, params, s);
 }
 
 // Sizes, type, activation and layout of a call; *empty when there is nothing
@@ -2373,7 +2467,8 @@ dq4_status_t check_call(const dq4_weight_t *w0, const dq4_weight_t *w1, int64_t 
         return DQ4_EINVAL;
     if (act < (gated ? DQ4_ACT_RELU : DQ4_ACT_NONE) || act > DQ4_ACT_GELU_TANH)
         return DQ4_EINVAL;
-    if (n_out > kMaxDim || n_in > kMaxDim || m > kMaxDim)
+    if (n_out > kMaxDim || n_in > kMaxDim || m > kMaxDim || m * n_out > kMaxMatrix ||
+        m * n_in > kMaxMatrix)
         return DQ4_EUNSUPPORTED;
     return DQ4_OK;
 }
@@ -2391,7 +2486,8 @@ bool bad_ld(int64_t ld, int64_t m, int64_t width)
 
 bool sizes_ok(int64_t n_out, int64_t n_in, int64_t m)
 {
-    return n_out > 0 && n_in >= 0 && m > 0 && n_out <= kMaxDim && n_in <= kMaxDim && m <= kMaxDim;
+    return n_out > 0 && n_in >= 0 && m > 0 && n_out <= kMaxDim && n_in <= kMaxDim && m <= kMaxDim &&
+           m * n_out <= kMaxMatrix && m * n_in <= kMaxMatrix;
 }
 
 }  // namespace
@@ -2473,10 +2569,9 @@ dq4_status_t dq4_linear_fused(const dq4_weight_t *w, int64_t n_out, int64_t n_in
     p.x[0] = p.x[1] = static_cast<const uint16_t *>(x);
     p.ld_x = m > 1 ? ld_x : n_in;
     p.k = n_in;
+    BesideWork beside{kNothing, {}};
     if (copy && n_in > 0) {
-        const dq4_status_t cs = copy_rows(x, ld_x, m, n_in, ws, s);
-        if (cs != DQ4_OK)
-            return cs;
+        beside = copy_work(x, ld_x, m, n_in, ws);
         p.x[0] = p.x[1] = reinterpret_cast<uint16_t *>(ws);
         p.ld_x = p.k = padded_ld(n_in);
     }
@@ -2492,9 +2587,9 @@ dq4_status_t dq4_linear_fused(const dq4_weight_t *w, int64_t n_out, int64_t n_in
             (!residual || rows_aligned(residual, ld_residual, m, 8)) &&
             (!pre || rows_aligned(pre, ld_pre, m, 8));
     if (dtype == DQ4_F16)
-        return run_product<DQ4_F16, true>(sh, w, nullptr, n_out, n_in, log2_block, p, ws + fixed,
+        return run_product<DQ4_F16, true>(sh, w, nullptr, n_out, n_in, log2_block, p, beside, ws + fixed,
                                           workspace_bytes - fixed, s);
-    return run_product<DQ4_BF16, true>(sh, w, nullptr, n_out, n_in, log2_block, p, ws + fixed,
+    return run_product<DQ4_BF16, true>(sh, w, nullptr, n_out, n_in, log2_block, p, beside, ws + fixed,
                                        workspace_bytes - fixed, s);
 }
 
@@ -2528,10 +2623,9 @@ dq4_status_t dq4_gated_fused(const dq4_weight_t *gate, const dq4_weight_t *up, i
     p.x[0] = p.x[1] = static_cast<const uint16_t *>(x);
     p.ld_x = m > 1 ? ld_x : n_in;
     p.k = n_in;
+    BesideWork beside{kNothing, {}};
     if (copy && n_in > 0) {
-        const dq4_status_t cs = copy_rows(x, ld_x, m, n_in, ws, s);
-        if (cs != DQ4_OK)
-            return cs;
+        beside = copy_work(x, ld_x, m, n_in, ws);
         p.x[0] = p.x[1] = reinterpret_cast<uint16_t *>(ws);
         p.ld_x = p.k = padded_ld(n_in);
     }
@@ -2544,9 +2638,9 @@ dq4_status_t dq4_gated_fused(const dq4_weight_t *gate, const dq4_weight_t *up, i
     p.vec = rows_aligned(h, ld_h, m, 8) && (!gate_pre || (rows_aligned(gate_pre, ld_pre, m, 8) &&
                                                           rows_aligned(up_pre, ld_pre, m, 8)));
     if (dtype == DQ4_F16)
-        return run_product<DQ4_F16, true>(sh, gate, up, n_ff, n_in, log2_block, p, ws + fixed,
+        return run_product<DQ4_F16, true>(sh, gate, up, n_ff, n_in, log2_block, p, beside, ws + fixed,
                                           workspace_bytes - fixed, s);
-    return run_product<DQ4_BF16, true>(sh, gate, up, n_ff, n_in, log2_block, p, ws + fixed,
+    return run_product<DQ4_BF16, true>(sh, gate, up, n_ff, n_in, log2_block, p, beside, ws + fixed,
                                        workspace_bytes - fixed, s);
 }
 
@@ -2593,6 +2687,8 @@ dq4_status_t dq4_linear_fused_backward(const dq4_weight_t *w, int64_t n_out, int
     p.x[0] = p.x[1] = static_cast<const uint16_t *>(lhs);
     p.ld_x = m > 1 ? ld_lhs : n_out;
     p.k = n_out;
+    BesideWork beside{kNothing, {}};
+    const int64_t blocks = ceil_div(m, kRowBlock);
     if (n_out > 0 && (act || dbias || copy)) {
         SlopeArgs a{};
         a.dy = static_cast<const uint16_t *>(dy);
@@ -2607,36 +2703,38 @@ dq4_status_t dq4_linear_fused_backward(const dq4_weight_t *w, int64_t n_out, int
             p.x[0] = p.x[1] = a.pad[0];
             p.ld_x = p.k = a.ld_pad;
         }
-        a.rows_per_block = static_cast<int32_t>(row_block(m, n_out));
-        const int64_t blocks = ceil_div(m, a.rows_per_block);
         a.partial = !dbias ? nullptr : blocks == 1 ? dbias : reinterpret_cast<float *>(ws + copied);
         a.m = m;
         a.n = n_out;
         a.act = activation;
-        dq4_status_t ls = launch_slope<false>(a, dtype, s);
-        if (ls != DQ4_OK)
-            return ls;
+        beside = slope_work(a, false);
         if (dbias && blocks > 1) {
-            const float *partial = a.partial;
-            int64_t n = n_out;
-            int32_t count = static_cast<int32_t>(blocks);
-            void *rp[] = {&partial, &n, &count, &dbias};
-            ls = launch(reinterpret_cast<const void *>(&bias_grad_reduce_kernel), ceil_div(n, kThreads), 1,
-                        kThreads, rp, s);
-            if (ls != DQ4_OK)
-                return ls;
+            p.bias_partial = a.partial;
+            p.bias_n = n_out;
+            p.bias_blocks = static_cast<int32_t>(blocks);
+            p.dbias = dbias;
         }
     }
-    if (n_in == 0)
-        return DQ4_OK;
+    if (n_in == 0) {  // no product: the slopes and the bias gradient alone
+        if (beside.kind == kNothing)
+            return DQ4_OK;
+        const dq4_status_t ls =
+            dtype == DQ4_F16 ? launch_fragments<DQ4_F16, false>(FragmentArgs{}, true, beside, 0, s)
+                             : launch_fragments<DQ4_BF16, false>(FragmentArgs{}, true, beside, 0, s);
+        if (ls != DQ4_OK || !p.dbias)
+            return ls;
+        void *rp[] = {&p.bias_partial, &p.bias_n, &p.bias_blocks, &p.dbias};
+        return launch(reinterpret_cast<const void *>(&bias_grad_reduce_kernel),
+                      ceil_div(n_out, kThreads), 1, kThreads, rp, s);
+    }
     p.act = DQ4_ACT_NONE;
     p.y = static_cast<uint16_t *>(dx);
     p.ld_y = ld_dx;
     p.vec = rows_aligned(dx, ld_dx, m, 8);
     if (dtype == DQ4_F16)
-        return run_product<DQ4_F16, false>(sh, w, nullptr, n_out, n_in, log2_block, p, ws + fixed,
+        return run_product<DQ4_F16, false>(sh, w, nullptr, n_out, n_in, log2_block, p, beside, ws + fixed,
                                            workspace_bytes - fixed, s);
-    return run_product<DQ4_BF16, false>(sh, w, nullptr, n_out, n_in, log2_block, p, ws + fixed,
+    return run_product<DQ4_BF16, false>(sh, w, nullptr, n_out, n_in, log2_block, p, beside, ws + fixed,
                                         workspace_bytes - fixed, s);
 }
 
@@ -2672,6 +2770,7 @@ dq4_status_t dq4_gated_fused_backward(const dq4_weight_t *gate, const dq4_weight
     p.x[1] = static_cast<const uint16_t *>(dup);
     p.ld_x = m > 1 ? ld_dpre : n_ff;
     p.k = n_ff;
+    BesideWork beside{kNothing, {}};
     if (n_ff > 0) {
         SlopeArgs a{};
         a.dy = static_cast<const uint16_t *>(dh);
@@ -2693,21 +2792,23 @@ dq4_status_t dq4_gated_fused_backward(const dq4_weight_t *gate, const dq4_weight
         a.m = m;
         a.n = n_ff;
         a.act = activation;
-        a.rows_per_block = 64;
-        const dq4_status_t ls = launch_slope<true>(a, dtype, s);
-        if (ls != DQ4_OK)
-            return ls;
+        beside = slope_work(a, true);
     }
-    if (n_in == 0)
-        return DQ4_OK;
+    if (n_in == 0) {  // no product: the slopes alone
+        if (beside.kind == kNothing)
+            return DQ4_OK;
+        return dtype == DQ4_F16
+                   ? launch_fragments<DQ4_F16, false>(FragmentArgs{}, true, beside, 0, s)
+                   : launch_fragments<DQ4_BF16, false>(FragmentArgs{}, true, beside, 0, s);
+    }
     p.act = DQ4_ACT_NONE;
     p.y = static_cast<uint16_t *>(dx);
     p.ld_y = ld_dx;
     p.vec = rows_aligned(dx, ld_dx, m, 8);
     if (dtype == DQ4_F16)
-        return run_product<DQ4_F16, false>(sh, gate, up, n_ff, n_in, log2_block, p, ws + fixed,
+        return run_product<DQ4_F16, false>(sh, gate, up, n_ff, n_in, log2_block, p, beside, ws + fixed,
                                            workspace_bytes - fixed, s);
-    return run_product<DQ4_BF16, false>(sh, gate, up, n_ff, n_in, log2_block, p, ws + fixed,
+    return run_product<DQ4_BF16, false>(sh, gate, up, n_ff, n_in, log2_block, p, beside, ws + fixed,
                                         workspace_bytes - fixed, s);
 }
 

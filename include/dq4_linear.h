@@ -46,7 +46,7 @@
  *                    pointer, unknown type or activation, workspace too small
  *   DQ4_EUNSUPPORTED block layout that dq4_nested_dequant rejects, two
  *                    weights with different block sizes, m, n_out or n_in
- *                    above 2^21
+ *                    above 2^21, m n_out or m n_in above 2^39
  *   DQ4_EHIP         a launch failed
  */
 #ifndef DQ4_LINEAR_H

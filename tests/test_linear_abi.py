@@ -56,7 +56,8 @@ def test_linear_validation(lib):
               dict(w=weight(scale_codes=None)), dict(w=weight(codebook4=None)), dict(ld_x=1 << 62)):
         assert call(**dict(dict(ws_bytes=BIG), **k)) == dq4.DQ4_EINVAL, k
     for k in (dict(w=weight(blocksize=48)), dict(w=weight(blocksize=16)), dict(w=weight(nested=128)),
-              dict(n_out=(1 << 21) + 1), dict(n_in=(1 << 21) + 1), dict(m=(1 << 21) + 1)):
+              dict(n_out=(1 << 21) + 1), dict(n_in=(1 << 21) + 1), dict(m=(1 << 21) + 1),
+              dict(m=1 << 19, n_out=1 << 21)):
         assert call(**dict(dict(ws_bytes=BIG), **k)) == dq4.DQ4_EUNSUPPORTED, k
 
 
@@ -125,7 +126,8 @@ def test_workspace_sizes(lib):
     assert f(w, w, 0, 64, 4, ONE, ONE, 64, 0) == 0
     # nothing overflows at the largest sizes
     big = 1 << 21
-    assert lib.dq4_linear_fused_workspace_bytes(w, big, big, big, P(2), big, 0) > 3 << 42
+    assert lib.dq4_linear_fused_workspace_bytes(w, big, big, big, P(2), big, 0) == 0
+    assert lib.dq4_linear_fused_workspace_bytes(w, big, big, 1 << 18, P(2), big, 0) > 8 << 40
 
 
 def test_binding_rejects_host_tensors(lib):
