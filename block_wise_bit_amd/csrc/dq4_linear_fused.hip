@@ -1671,11 +1671,12 @@ __global__ __launch_bounds__(64 * WAVES) void token_rows_kernel(TokenArgs a)
 }
 
 // ---------------------------------------------------------------------------
-// 5 to 64 rows of x: weight rows read 64 bytes at a time, transposed in registers
+// 5 to 192 rows of x: weight rows read 64 bytes at a time, transposed in registers
 // ---------------------------------------------------------------------------
 // x in operand fragments: fragment (chunk of 512 k, step, 16 rows of x) is 1
 // KiB in lane order; lane (r, g) of step 4 j + s holds row r's k 512 c + 128 g
-// + 32 j + 8 s .. + 7.  Rows and k beyond x are zeros.
+// + 32 j + 8 s .. + 7.  Rows and k beyond x are zeros.  More than 64 rows are
+// cut into slices of 64 (blockIdx.y), one after the other.
 __global__ __launch_bounds__(kThreads) void x_fragments_zero_fill(const uint16_t *x, int64_t ld_x,
                                                                   int64_t m, int64_t k, int32_t tf,
                                                                   int32_t frags, bool aligned,
@@ -1686,7 +1687,7 @@ __global__ __launch_bounds__(kThreads) void x_fragments_zero_fill(const uint16_t
     if (fr >= frags)
         return;
     const int step = fr / tf, t = fr - step * tf;
-    const int64_t row = t * 16 + (lane & 15);
+    const int64_t row = blockIdx.y * 64 + t * 16 + (lane & 15);
     const int64_t k0 = static_cast<int64_t>(step >> 4) * 512 + 128 * (lane >> 4) + 8 * (step & 15);
     u32x4 q = {0, 0, 0, 0};
     if (row < m && k0 < k) {
@@ -1700,7 +1701,8 @@ __global__ __launch_bounds__(kThreads) void x_fragments_zero_fill(const uint16_t
                     q[j / 2] |= static_cast<uint32_t>(from[j]) << (16 * (j & 1));
         }
     }
-    *reinterpret_cast<u32x4 *>(out + (static_cast<int64_t>(fr) * 64 + lane) * 8) = q;
+    const int64_t at = static_cast<int64_t>(blockIdx.y) * frags + fr;
+    *reinterpret_cast<u32x4 *>(out + (at * 64 + lane) * 8) = q;
 }
 
 // Lane l of each quad exchanges register j for lane j's register l.
@@ -1723,8 +1725,8 @@ __device__ __forceinline__ void transpose_quads(uint32_t (&v)[4], bool odd, bool
     v[3] = high ? a3 : y1;
 }
 
-// m <= 16 TF rows of x against the 4-bit weight, which is read once and never
-// written out.  A wave takes two fragments of 16 weight rows (gated: one of
+// 16 TF rows of x against the 4-bit weight, which is read once (for each 64
+// rows of x) and never written out.  A wave takes two fragments of 16 weight rows (gated: one of
 // each weight, the same columns) and chunks of 512 k.  The matrix instruction
 // wants neighbouring lanes in different weight rows, memory wants them side by
 // side (a load whose neighbouring lanes lie in 16 rows took 64 accesses of the
@@ -1746,6 +1748,9 @@ __global__ __launch_bounds__(512) void batch_rows_kernel(RowsArgs a, const uint1
     __shared__ float scb[kW][256], cb4[kW][16];
     __shared__ __attribute__((aligned(16))) f32x4 partial[8][R * TF][64];
 
+    // slice blockIdx.y of 64 rows of x; the weight is read again for each
+    const int64_t x_row0 = static_cast<int64_t>(blockIdx.y) * 64;
+    x_frags += static_cast<int64_t>(blockIdx.y) * ((a.n_in + 511) / 512) * (16 * TF * 512);
     const int tid = threadIdx.x;
     const int lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -1937,7 +1942,7 @@ __global__ __launch_bounds__(512) void batch_rows_kernel(RowsArgs a, const uint1
             for (int q = 1; q < WK; ++q)
                 sum = sum + partial[row_wave * WK + q][f * TF + t][ln];
             const int64_t n0 = rb * block_rows + row_wave * (16 * kPer) + f * 16 + (ln >> 4) * 4;
-            const int64_t row = t * 16 + (ln & 15);
+            const int64_t row = x_row0 + t * 16 + (ln & 15);
             if constexpr (kGated) {
                 f32x4 up = partial[row_wave * WK][TF + t][ln];
                 for (int q = 1; q < WK; ++q)
@@ -2091,12 +2096,13 @@ int64_t workspace_need(const Shape &s, int64_t fixed, bool least)
 // Which kernel a forward call takes.
 enum Route {
     kTokenRoute,    // up to 4 rows of x, weight rows of up to 32768
-    kBatchRoute,    // up to 64
+    kBatchRoute,    // up to 192: 64 rows a reading of the weight
     kRaggedRoute,   // up to 64, weight rows of whole dwords that are not 32 k apart
     kProductRoute   // decode to fragments, then the product
 };
 
-constexpr int64_t kTokenMost = 4, kBatchMost = 64;
+// Where the routes meet, measured: see the entry's comment.
+constexpr int64_t kTokenMost = 4, kBatchMost = 192, kRaggedMost = 64;
 
 Route route_of(const dq4_weight_t *w0, const dq4_weight_t *w1, int64_t n_in, int64_t m)
 {
@@ -2105,7 +2111,7 @@ Route route_of(const dq4_weight_t *w0, const dq4_weight_t *w1, int64_t n_in, int
         (w1 && reinterpret_cast<uintptr_t>(w1->packed) % 4 != 0))
         return kProductRoute;
     if (n_in % 32 != 0)
-        return kRaggedRoute;
+        return m <= kRaggedMost ? kRaggedRoute : kProductRoute;
     return m <= kTokenMost && n_in <= kTokenMaxChunks * kTokenSpan ? kTokenRoute : kBatchRoute;
 }
 
@@ -2131,7 +2137,7 @@ int64_t forward_need(const Shape &s, const dq4_weight_t *w0, const dq4_weight_t 
     case kProductRoute:
         return workspace_need(s, fixed, least);
     case kBatchRoute:
-        return ceil_div(s.k, 512) * 16 * x_row_frags(s.m) * kFragBytes;
+        return ceil_div(s.m, 64) * ceil_div(s.k, 512) * 16 * x_row_frags(s.m) * kFragBytes;
     default:
         return fixed;
     }
@@ -2242,7 +2248,7 @@ dq4_status_t launch_batch_rows(RowsArgs a, const uint16_t *x_frags, int cus, hip
     const void *kernel = a.log2_block >= 6 && a.n_in % 64 == 0
                              ? reinterpret_cast<const void *>(&batch_rows_kernel<OUT, kGated, TF, 2>)
                              : reinterpret_cast<const void *>(&batch_rows_kernel<OUT, kGated, TF, 4>);
-    return launch(kernel, a.row_blocks < cus ? a.row_blocks : cus, 1, 512, params, s);
+    return launch(kernel, a.row_blocks < cus ? a.row_blocks : cus, ceil_div(a.out.m, 64), 512, params, s);
 }
 
 template <int OUT, bool kGated>
@@ -2256,7 +2262,7 @@ dq4_status_t launch_batch(const RowsArgs &a, uint8_t *workspace, int cus, hipStr
     uint16_t *out = reinterpret_cast<uint16_t *>(workspace);
     void *params[] = {&x, &ld, &m, &k, &tf, &frags, &aligned, &out};
     const dq4_status_t st = launch(reinterpret_cast<const void *>(&x_fragments_zero_fill),
-                                   ceil_div(frags, kThreads / 64), 1, kThreads, params, s);
+                                   ceil_div(frags, kThreads / 64), ceil_div(m, 64), kThreads, params, s);
     if (st != DQ4_OK)
         return st;
     if (tf == 1)
@@ -2266,7 +2272,7 @@ dq4_status_t launch_batch(const RowsArgs &a, uint8_t *workspace, int cus, hipStr
     return launch_batch_rows<OUT, kGated, 4>(a, out, cus, s);
 }
 
-// Up to 64 rows of x, by one of the kernels that read the 4-bit weight once.
+// Few rows of x, by one of the kernels that read the 4-bit weight itself.
 template <int OUT, bool kGated>
 dq4_status_t launch_few_rows(const RowsArgs &a, Route route, uint8_t *workspace, int cus,
                              hipStream_t s)

@@ -41,7 +41,8 @@
  * Ownership, ordering and errors are as in dq4.h: everything is enqueued on
  * `stream` and can be captured into a graph, nothing is allocated, kept or
  * synchronized; arguments are checked before anything is enqueued.
- * Results are deterministic for a given device and shape.
+ * Results are deterministic for a given device, shape, and alignment of the
+ * packed codes; for another number of rows the sums may run in another order.
  *   DQ4_EINVAL       negative size, row stride below the row length, missing
  *                    pointer, unknown type or activation, workspace too small
  *   DQ4_EUNSUPPORTED block layout that dq4_nested_dequant rejects, two

@@ -58,7 +58,8 @@ SHAPES = [
     # row blocks than workgroups
     (5, 33, 512, 64, "nf4"), (16, 47, 544, 32, "fp4"), (17, 8200, 160, 64, "nf4"),
     (31, 100, 1056, 4096, "nf4"), (33, 4100, 640, 128, "fp4"), (64, 31, 4608, 64, "nf4"),
-    (48, 17, 32, 32, "nf4"), (8, 300, 2080, 256, "nf4"),
+    (48, 17, 32, 32, "nf4"), (8, 300, 2080, 256, "nf4"), (100, 90, 576, 64, "nf4"),
+    (128, 1030, 64, 64, "fp4"), (130, 40, 1056, 32, "nf4"), (192, 300, 512, 64, "nf4"),
     # ... with rows of whole dwords only
     (3, 50, 2056, 32, "nf4"), (40, 4200, 168, 64, "nf4"), (20, 90, 1000, 4096, "fp4"),
 ]
@@ -155,6 +156,40 @@ def test_gated_backward(shape, dt):
     s = np.abs(dg64) @ np.abs(wg) + np.abs(du64) @ np.abs(wu)
     dxe = dg64 @ wg + du64 @ wu
     lc.check(dx, dxe, lc.rounding(dt, dxe, gamma_deterministic(2 * n_ff) * s), "dx")
+
+
+# large tiles of the product, whole and split sums, rows and columns that end
+# inside a tile: references in float64 on the GPU
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("m,n_out,n_in", [(2000, 8200, 520), (2048, 4096, 11008), (700, 4104, 8200),
+                                          (1030, 16500, 136), (520, 2050, 16424)])
+def test_large_products(m, n_out, n_in, dt):
+    print(f"large {m} {n_out} {n_in} {dt}", flush=True)
+    rng = np.random.Generator(np.random.PCG64(m))
+    tdt, u, sub = lc.TYPES[dt]
+    host, w = make_weight(n_out, n_in, 64, "nf4", seed=m)
+    hu, up = make_weight(n_out, n_in, 64, "nf4", offset=-0.02, seed=m + 1)
+    w64, wu64 = (torch.from_numpy(lc.weight64(h, dt)).cuda() for h in (host, hu))
+
+    def close(got, exact, s, k, what):
+        gamma = gamma_deterministic(k)
+        err = (got.double() - exact).abs()
+        bound = gamma * s + u * (exact.abs() + gamma * s) + sub
+        print(f"{what}: worst err/bound {float((err / bound).max()):.3f}", flush=True)
+        assert bool(torch.isfinite(got).all()) and bool((err <= bound).all()), what
+    x, dy = normal(rng, (m, n_in), dt), normal(rng, (m, n_out), dt)
+    sizes = dict(n_out=n_out, n_in=n_in, blocksize=64)
+    y = dq4.dq4_linear_fused(**w, **sizes, x=x)
+    close(y, x.double() @ w64.t(), x.double().abs() @ w64.abs().t(), n_in, "forward")
+    dx, _, _ = dq4.dq4_linear_fused_backward(**w, **sizes, dy=dy)
+    close(dx, dy.double() @ w64, dy.double().abs() @ w64.abs(), n_out, "backward")
+    pre = torch.empty((2, m, n_out), dtype=tdt, device="cuda")
+    h = dq4.dq4_gated_fused(w, up, n_out, n_in, 64, x, activation="relu", gate_pre=pre[0], up_pre=pre[1])
+    close(pre[0], x.double() @ w64.t(), x.double().abs() @ w64.abs().t(), n_in, "gate_pre")
+    close(pre[1], x.double() @ wu64.t(), x.double().abs() @ wu64.abs().t(), n_in, "up_pre")
+    dx, dg, du = dq4.dq4_gated_fused_backward(w, up, n_out, n_in, 64, dy, pre[0], pre[1], activation="relu")
+    close(dx, dg.double() @ w64 + du.double() @ wu64, dg.double().abs() @ w64.abs() + du.double().abs() @ wu64.abs(),
+          2 * n_out, "gated backward")
 
 
 # ----------------------------------------------------------------------------
@@ -285,21 +320,22 @@ def test_residual_in_place(m):
 
 
 def test_unaligned_codes_and_single_row_strides():
-    """Packed codes that start on an odd byte; a single row whose stride is
-    nonsense (torch leaves it so)."""
+    """Packed codes that start on an odd byte (another kernel then, another
+    order of the sums); a single row whose stride is nonsense (torch leaves it
+    so)."""
     rng = np.random.Generator(np.random.PCG64(21))
     for m in (1, 70):
         host, w = make_weight(256, 512, seed=14)
-        x = normal(rng, (m, 512), "bf16")
-        y = dq4.dq4_linear_fused(**w, n_out=256, n_in=512, blocksize=64, x=x)
-        dx = dq4.dq4_linear_fused_backward(**w, n_out=256, n_in=512, blocksize=64, dy=y)[0]
+        w64 = lc.weight64(host, "bf16")
+        x, dy = normal(rng, (m, 512), "bf16"), normal(rng, (m, 256), "bf16")
         odd = torch.empty(w["packed"].numel() + 1, dtype=torch.uint8, device="cuda")
         odd[1:] = w["packed"]
         w1 = dict(w, packed=odd[1:])
-        assert_bits_equal(bits_of(dq4.dq4_linear_fused(**w1, n_out=256, n_in=512, blocksize=64, x=x)),
-                          bits_of(y), "odd codes, forward")
-        assert_bits_equal(bits_of(dq4.dq4_linear_fused_backward(**w1, n_out=256, n_in=512, blocksize=64, dy=y)[0]),
-                          bits_of(dx), "odd codes, backward")
+        y = dq4.dq4_linear_fused(**w1, n_out=256, n_in=512, blocksize=64, x=x)
+        (z, bz), _ = lc.linear_expected("bf16", "none", lc.to64(x), w64)
+        lc.check(y, z, bz, "odd codes, forward")
+        dx, dz, _ = dq4.dq4_linear_fused_backward(**w1, n_out=256, n_in=512, blocksize=64, dy=dy)
+        check_linear_backward("bf16", "none", dy, dy, dx, dz, None, w64)
     row = torch.as_strided(x[:1].contiguous(), (1, 512), (1, 1))
     y1 = dq4.dq4_linear_fused(**w, n_out=256, n_in=512, blocksize=64, x=row)
     assert_bits_equal(bits_of(y1), bits_of(dq4.dq4_linear_fused(**w, n_out=256, n_in=512, blocksize=64,
