@@ -197,7 +197,10 @@ struct SlopeArgs {
     uint16_t *dz[2];
     int64_t ld_dz;
     uint16_t *pad[2];           // padded copies for the product, or null
-    int64_t ld_pad;
+    int64_t ld_pad;             // their columns
+    int64_t pad_rows;           // their rows
+    int32_t frag_rows;          // 0: copies in rows; else in operand fragments, 16 frag_rows
+                                // rows a slice: [slice][32 columns][16 rows][lane][8]
     float *partial;             // column sums, one row per row block, or null
     int64_t m, n;
     int32_t act;
@@ -216,12 +219,13 @@ __device__ __forceinline__ void activation_slopes(const SlopeArgs &a, int64_t bx
     const int64_t c = (bx * 32 + tx) * N;
     const int64_t width = a.pad[0] ? a.ld_pad : a.n;
     const int64_t r0 = by * kRowBlock;
-    const int64_t r1 = r0 + kRowBlock < a.m ? r0 + kRowBlock : a.m;
+    const int64_t rows = a.pad[0] ? a.pad_rows : a.m;
+    const int64_t r1 = r0 + kRowBlock < rows ? r0 + kRowBlock : rows;
     float sum[N] = {};
     if (c < width) {
         for (int64_t r = r0 + ty; r < r1; r += 8) {
             float z0[N] = {}, z1[N] = {};
-            if (c < a.n) {
+            if (c < a.n && r < a.m) {
                 float dy[N], pre[N], up[N];
                 load_values<OUT, N>(a.dy + r * a.ld_dy + c, N > 1, N, dy);
                 if (a.act != DQ4_ACT_NONE)
@@ -250,9 +254,16 @@ __device__ __forceinline__ void activation_slopes(const SlopeArgs &a, int64_t bx
                     store_values<OUT, N>(a.dz[1] + r * a.ld_dz + c, N > 1, N, z1);
             }
             if (a.pad[0]) {
-                store_values<OUT, N>(a.pad[0] + r * a.ld_pad + c, N > 1, N, z0);
+                int64_t at = r * a.ld_pad + c;
+                if (a.frag_rows) {
+                    const uint32_t tf = a.frag_rows, block = static_cast<uint32_t>(r) >> 4;
+                    const int64_t slice = block / tf, t = block - slice * tf;
+                    at = ((slice * (a.ld_pad >> 5) + (c >> 5)) * tf + t) * 512 +
+                         (((c >> 3) & 3) * 16 + (r & 15)) * 8 + (c & 7);
+                }
+                store_values<OUT, N>(a.pad[0] + at, N > 1, N, z0);
                 if constexpr (kGated)
-                    store_values<OUT, N>(a.pad[1] + r * a.ld_pad + c, N > 1, N, z1);
+                    store_values<OUT, N>(a.pad[1] + at, N > 1, N, z1);
             }
         }
     }
@@ -1957,6 +1968,175 @@ __global__ __launch_bounds__(512) void batch_rows_kernel(RowsArgs a, const uint1
 }
 
 // ---------------------------------------------------------------------------
+// few rows of dz: dx = dz W with the weight decoded straight into operands
+// ---------------------------------------------------------------------------
+struct ColumnArgs {
+    Weight w[2];
+    int64_t n_out, n_in;
+    int32_t log2_block;
+    int32_t steps;              // of 32 weight rows, per weight
+    int32_t splits;             // of all steps
+    int32_t slices;             // of 16 TF rows of dz
+    const uint16_t *dz_frags[2];  // [slice][step][16 rows][lane][8], zeros beyond dz
+    ProductArgs out;            // partial, groups, bias sums
+};
+
+// 16 TF rows of dz (dgate and dup: kTwo, one sum over both) against 128 weight
+// columns: the sum runs down the weight's rows, so a lane takes the packed
+// dwords of 8 rows, 8 neighbouring columns each, looks up their values and
+// pairs the same column of two rows in one conversion: that transposes them
+// into operand fragments (column 8 r + f in row r of fragment f) for nothing.
+// A load takes 64 neighbouring bytes of 4 rows.  The 8 waves take steps of 32
+// rows in turn, their sums meet in LDS, and those of the workgroups that share
+// a column group in the workspace (product_reduce_kernel), in a fixed order.
+// Bound by the lookups in LDS and the decode's vector instructions: W is read
+// once for 16 TF rows of dz and never written out.
+template <int OUT, bool kTwo, int TF>
+__global__ __launch_bounds__(512) void weight_columns_kernel(ColumnArgs a)
+{
+    constexpr int kW = kTwo ? 2 : 1;
+    __shared__ __attribute__((aligned(1024))) uint8_t table[kPairTableBytes + 256];
+    __shared__ float scb[kW][256], cb4[kW][16];
+    __shared__ __attribute__((aligned(16))) f32x4 partial[8][kFrags][64];
+    if (static_cast<int>(blockIdx.y) == a.splits * a.slices) {
+        add_bias_blocks(a.out.bias_partial, a.out.bias_n, a.out.bias_blocks, a.out.dbias);
+        return;
+    }
+    const int tid = threadIdx.x;
+    const int lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int r = lane & 15, g = lane >> 4;
+    const int group = blockIdx.x;
+    const int slice = static_cast<int>(blockIdx.y) / a.splits;
+    const int split = static_cast<int>(blockIdx.y) - slice * a.splits;
+    const int lb = a.log2_block;
+    const uint32_t n_in = static_cast<uint32_t>(a.n_in);
+    const uint32_t j0 = group * kGroup + 8 * r;
+    // columns beyond the weight: nothing is loaded, and their sums are not kept
+    const uint32_t past = j0 < n_in ? 0u : 0x80000000u;
+    const int64_t n_elems = a.n_out * a.n_in;
+    const int64_t blocks = (n_elems + (int64_t{1} << lb) - 1) >> lb;
+    const int all_steps = a.steps * kW;
+    const int first = static_cast<int>(static_cast<uint32_t>(all_steps) * split / a.splits);
+    const int last = static_cast<int>(static_cast<uint32_t>(all_steps) * (split + 1) / a.splits);
+
+    struct Loads {
+        uint32_t packed[8], code[8];
+        float absmax[8];
+        u32x4 x[TF];
+    };
+    const auto rsrc_of = [](const void *p, int64_t bytes) {
+        return __builtin_amdgcn_make_buffer_rsrc(
+            const_cast<void *>(p), 0, static_cast<int32_t>(bytes < 0x7FFFFFF0 ? bytes : 0x7FFFFFF0),
+            kRawBufferWord3);
+    };
+    auto load = [&](Loads &l, int step) {
+        step = step < last ? step : last - 1;  // loaded again, unused
+        const int which = kTwo && step >= a.steps ? 1 : 0;
+        const int s = step - which * a.steps;
+        const Weight &w = a.w[which];
+        const int64_t e0 = static_cast<int64_t>(s) * 32 * a.n_in;
+        const int64_t b0 = e0 >> lb;
+        const uint32_t phase = static_cast<uint32_t>(e0) & ((1u << lb) - 1);
+        const uint32_t group_phase = static_cast<uint32_t>(b0) & 255;
+        const auto rp = rsrc_of(w.packed + (e0 >> 1), ((n_elems + 1) >> 1) - (e0 >> 1));
+        const auto rc = rsrc_of(w.scale_codes + b0, blocks - b0);
+        const auto rm = rsrc_of(w.nested_absmax + (b0 >> 8), (((blocks + 255) >> 8) - (b0 >> 8)) * 4);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const uint32_t e = (8 * g + q) * n_in + j0;
+            const uint32_t b = (phase + e) >> lb;
+            l.packed[q] = __builtin_amdgcn_raw_buffer_load_b32(rp, (e >> 1) | past, 0, 0);
+            l.code[q] = __builtin_amdgcn_raw_buffer_load_b8(rc, b | past, 0, 0);
+            l.absmax[q] = __builtin_bit_cast(
+                float, __builtin_amdgcn_raw_buffer_load_b32(rm, (((group_phase + b) >> 8) * 4) | past, 0, 0));
+        }
+#pragma unroll
+        for (int t = 0; t < TF; ++t)
+            l.x[t] = *reinterpret_cast<const u32x4 *>(
+                a.dz_frags[which] + ((static_cast<int64_t>(slice) * a.steps + s) * TF + t) * 512 + lane * 8);
+    };
+
+    const Codebooks codebooks = fetch_codebooks<kW>(a.w);
+    Loads cur;
+    load(cur, first + wave);
+    fill_tables<kW, 1>(codebooks, table, scb, cb4);
+
+    f32x4 acc[kFrags][TF];
+#pragma unroll
+    for (int f = 0; f < kFrags; ++f)
+#pragma unroll
+        for (int t = 0; t < TF; ++t)
+            acc[f][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int step = first + wave; step < last; step += 8) {
+        Loads next;
+        load(next, step + 8);
+        const int which = kTwo && step >= a.steps ? 1 : 0;
+        const uint32_t from = kTwo ? (lane & 15) * 16 + which * 8 : (lane & 31) * 8;
+        const float offset = a.w[which].offset;
+        float s[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            s[q] = block_scale(scb[which][cur.code[q]], cur.absmax[q], offset);
+        u32x4 wf[kFrags];
+        Pairs row[2];
+        row[0] = lookup_dword(cur.packed[0], table, from);
+        row[1] = lookup_dword(cur.packed[1], table, from);
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            Pairs then[2];
+            if (p < 3) {
+                then[0] = lookup_dword(cur.packed[2 * p + 2], table, from);
+                then[1] = lookup_dword(cur.packed[2 * p + 3], table, from);
+            }
+            keep_order();
+#pragma unroll
+            for (int f = 0; f < kFrags; ++f)
+                wf[f][p] = Half<OUT>::pack2(row[0].v[f / 2][f % 2] * s[2 * p],
+                                            row[1].v[f / 2][f % 2] * s[2 * p + 1]);
+            if (p < 3) {
+                row[0] = then[0];
+                row[1] = then[1];
+            }
+        }
+        // rows beyond the weight hold no value at all
+        const int left = static_cast<int>(a.n_out) - ((step - which * a.steps) * 32 + 8 * g);
+        if (__builtin_amdgcn_readfirstlane(static_cast<int>(a.n_out) - (step - which * a.steps) * 32) < 32) {
+#pragma unroll
+            for (int p = 0; p < 4; ++p) {
+                const uint32_t mask = left >= 2 * p + 2 ? 0xFFFFFFFFu : left == 2 * p + 1 ? 0xFFFFu : 0u;
+#pragma unroll
+                for (int f = 0; f < kFrags; ++f)
+                    wf[f][p] &= mask;
+            }
+        }
+#pragma unroll
+        for (int f = 0; f < kFrags; ++f)
+#pragma unroll
+            for (int t = 0; t < TF; ++t)
+                acc[f][t] = Half<OUT>::mfma(wf[f], cur.x[t], acc[f][t]);
+        cur = next;
+    }
+    // the waves' sums, 16 rows of dz at a time; wave f adds up fragment f
+    const int tile = group * a.slices + slice;
+    f32x4 *to = a.out.partial + (static_cast<int64_t>(split) * (gridDim.x * a.slices) + tile) * (kFrags * TF * 64);
+#pragma unroll
+    for (int t = 0; t < TF; ++t) {
+        if (t > 0)
+            lds_barrier();
+#pragma unroll
+        for (int f = 0; f < kFrags; ++f)
+            partial[wave][f][lane] = acc[f][t];
+        lds_barrier();
+        f32x4 sum = partial[0][wave][lane];
+#pragma unroll
+        for (int q = 1; q < 8; ++q)
+            sum = sum + partial[q][wave][lane];
+        to[(wave * TF + t) * 64 + lane] = sum;
+    }
+}
+
+// ---------------------------------------------------------------------------
 // the bias gradient on its own
 // ---------------------------------------------------------------------------
 __global__ __launch_bounds__(kThreads) void bias_grad_reduce_kernel(const float *partial,
@@ -2113,6 +2293,40 @@ Route route_of(const dq4_weight_t *w0, const dq4_weight_t *w1, int64_t n_in, int
     if (n_in % 32 != 0)
         return m <= kRaggedMost ? kRaggedRoute : kProductRoute;
     return m <= kTokenMost && n_in <= kTokenMaxChunks * kTokenSpan ? kTokenRoute : kBatchRoute;
+}
+
+// A backward call with few rows of dz whose weight rows are whole dwords
+// decodes in registers (weight_columns_kernel).
+constexpr int64_t kColumnsMost = 64;
+
+struct ColumnPlan {
+    bool use;
+    int tf, slices, splits;
+    int64_t steps, groups;  // steps per weight
+    int64_t frag_bytes() const { return slices * steps * tf * kFragBytes; }  // per matrix
+    int64_t partial_bytes() const { return splits * groups * slices * kFrags * tf * kFragBytes; }
+};
+
+ColumnPlan column_plan(const dq4_weight_t *w0, const dq4_weight_t *w1, int64_t n_out, int64_t n_in,
+                       int64_t m, int cus)
+{
+    ColumnPlan p{};
+    p.use = m <= kColumnsMost && n_out > 0 && n_in > 0 && n_in % 8 == 0 &&
+            reinterpret_cast<uintptr_t>(w0->packed) % 4 == 0 &&
+            (!w1 || reinterpret_cast<uintptr_t>(w1->packed) % 4 == 0);
+    if (!p.use)
+        return p;
+    p.tf = m <= 16 ? 1 : 2;
+    p.slices = static_cast<int>(ceil_div(m, 16 * p.tf));
+    p.steps = ceil_div(n_out, 32);
+    p.groups = ceil_div(n_in, kGroup);
+    // one workgroup per CU, each wave with a step at least
+    const int64_t all = p.steps * (w1 ? 2 : 1);
+    int64_t splits = cus / (p.groups * p.slices);
+    if (splits > ceil_div(all, 8))
+        splits = ceil_div(all, 8);
+    p.splits = static_cast<int>(splits < 1 ? 1 : splits);
+    return p;
 }
 
 int x_row_frags(int64_t m)
@@ -2314,7 +2528,7 @@ BesideWork slope_work(const SlopeArgs &a, bool gated)
     BesideWork w{gated ? (vec ? kGatedSlopes8 : kGatedSlopes1) : (vec ? kSlopes8 : kSlopes1), {}};
     w.args.slope = a;
     w.args.columns = static_cast<int32_t>(ceil_div(a.pad[0] ? a.ld_pad : a.n, vec ? 256 : 32));
-    w.args.blocks = static_cast<int32_t>(ceil_div(a.m, kRowBlock)) * w.args.columns;
+    w.args.blocks = static_cast<int32_t>(ceil_div(a.pad[0] ? a.pad_rows : a.m, kRowBlock)) * w.args.columns;
     return w;
 }
 
@@ -2454,6 +2668,54 @@ dq4_status_t run_product(const Shape &sh, const dq4_weight_t *w0, const dq4_weig
     return DQ4_OK;
 }
 
+template <int OUT, bool kTwo, int TF>
+dq4_status_t launch_columns_tile(ColumnArgs a, hipStream_t s)
+{
+    const int64_t tiles = static_cast<int64_t>(a.out.groups) * a.slices;
+    void *params[] = {&a};
+    const dq4_status_t st =
+        launch(reinterpret_cast<const void *>(&weight_columns_kernel<OUT, kTwo, TF>), a.out.groups,
+               static_cast<int64_t>(a.splits) * a.slices + (a.out.dbias ? 1 : 0), 512, params, s);
+    if (st != DQ4_OK)
+        return st;
+    ProductArgs p = a.out;
+    p.splits = a.splits;
+    p.tiles_t = a.slices;
+    int32_t n_tiles = static_cast<int32_t>(tiles);
+    void *rp[] = {&p, &n_tiles};
+    return launch(reinterpret_cast<const void *>(&product_reduce_kernel<OUT, false, 1, 1, TF>), tiles, TF,
+                  256, rp, s);
+}
+
+// dz's fragments and slopes, the product, the epilogue.
+template <int OUT>
+dq4_status_t run_columns(const ColumnPlan &plan, const dq4_weight_t *w0, const dq4_weight_t *w1,
+                         int64_t n_out, int64_t n_in, int64_t m, int log2_block, ProductArgs p,
+                         const BesideWork &beside, hipStream_t s)
+{
+    const dq4_status_t st = launch_fragments<OUT, false>(FragmentArgs{}, true, beside, 0, s);
+    if (st != DQ4_OK)
+        return st;
+    p.m = m;
+    p.n = n_in;
+    p.groups = static_cast<int32_t>(plan.groups);
+    ColumnArgs a{};
+    a.w[0] = device_weight(*w0);
+    a.w[1] = device_weight(w1 ? *w1 : *w0);
+    a.n_out = n_out;
+    a.n_in = n_in;
+    a.log2_block = log2_block;
+    a.steps = static_cast<int32_t>(plan.steps);
+    a.splits = plan.splits;
+    a.slices = plan.slices;
+    a.dz_frags[0] = beside.args.slope.pad[0];
+    a.dz_frags[1] = beside.args.slope.pad[1];
+    a.out = p;
+    if (plan.tf == 1)
+        return w1 ? launch_columns_tile<OUT, true, 1>(a, s) : launch_columns_tile<OUT, false, 1>(a, s);
+    return w1 ? launch_columns_tile<OUT, true, 2>(a, s) : launch_columns_tile<OUT, false, 2>(a, s);
+}
+
 // Sizes, type, activation and layout of a call; *empty when there is nothing
 // to write.
 dq4_status_t check_call(const dq4_weight_t *w0, const dq4_weight_t *w1, int64_t n_out,
@@ -2479,6 +2741,11 @@ dq4_status_t check_call(const dq4_weight_t *w0, const dq4_weight_t *w1, int64_t 
     return DQ4_OK;
 }
 
+bool bad_workspace(const void *workspace, int64_t bytes)
+{
+    return bytes > 0 && (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 != 0);
+}
+
 bool weight_missing(const dq4_weight_t *w)
 {
     return !w->packed || !w->scale_codes || !w->nested_absmax || !w->scale_codebook || !w->codebook4;
@@ -2494,6 +2761,29 @@ bool sizes_ok(int64_t n_out, int64_t n_in, int64_t m)
 {
     return n_out > 0 && n_in >= 0 && m > 0 && n_out <= kMaxDim && n_in <= kMaxDim && m <= kMaxDim &&
            m * n_out <= kMaxMatrix && m * n_in <= kMaxMatrix;
+}
+
+int64_t linear_backward_need(const dq4_weight_t *w, int64_t n_out, int64_t n_in, int64_t m,
+                             const void *lhs, int64_t ld_lhs, bool least)
+{
+    const ColumnPlan cp = column_plan(w, nullptr, n_out, n_in, m, current_compute_units());
+    if (cp.use)
+        return partial_bytes(m, n_out) + cp.frag_bytes() + cp.partial_bytes();
+    const Shape s{m, n_in, n_out, kSingle};
+    const bool copy = n_in > 0 && needs_copy(lhs, ld_lhs, m, n_out);
+    return workspace_need(s, copy_bytes(s, copy) + partial_bytes(m, n_out), least);
+}
+
+int64_t gated_backward_need(const dq4_weight_t *gate, const dq4_weight_t *up, int64_t n_ff,
+                            int64_t n_in, int64_t m, const void *dgate, const void *dup,
+                            int64_t ld_dpre, bool least)
+{
+    const ColumnPlan cp = column_plan(gate, up, n_ff, n_in, m, current_compute_units());
+    if (cp.use)
+        return 2 * cp.frag_bytes() + cp.partial_bytes();
+    const Shape s{m, n_in, n_ff, kStacked};
+    const bool copy = n_in > 0 && (needs_copy(dgate, ld_dpre, m, n_ff) || needs_copy(dup, ld_dpre, m, n_ff));
+    return workspace_need(s, copy_bytes(s, copy), least);
 }
 
 }  // namespace
@@ -2528,9 +2818,7 @@ int64_t dq4_linear_fused_backward_workspace_bytes(const dq4_weight_t *w, int64_t
 {
     if (!w || !sizes_ok(n_out, n_in, m))
         return 0;
-    const Shape s{m, n_in, n_out, kSingle};
-    return workspace_need(s, copy_bytes(s, needs_copy(dz, ld_dz, m, n_out)) + partial_bytes(m, n_out),
-                          least != 0);
+    return linear_backward_need(w, n_out, n_in, m, dz, ld_dz, least != 0);
 }
 
 int64_t dq4_gated_fused_backward_workspace_bytes(const dq4_weight_t *gate,
@@ -2541,9 +2829,7 @@ int64_t dq4_gated_fused_backward_workspace_bytes(const dq4_weight_t *gate,
 {
     if (!gate || !up || !sizes_ok(n_ff, n_in, m))
         return 0;
-    const Shape s{m, n_in, n_ff, kStacked};
-    const bool copy = needs_copy(dgate, ld_dpre, m, n_ff) || needs_copy(dup, ld_dpre, m, n_ff);
-    return workspace_need(s, copy_bytes(s, copy), least != 0);
+    return gated_backward_need(gate, up, n_ff, n_in, m, dgate, dup, ld_dpre, least != 0);
 }
 
 dq4_status_t dq4_linear_fused(const dq4_weight_t *w, int64_t n_out, int64_t n_in, int32_t dtype,
@@ -2567,7 +2853,7 @@ dq4_status_t dq4_linear_fused(const dq4_weight_t *w, int64_t n_out, int64_t n_in
     const bool copy = forward_copies(w, nullptr, x, ld_x, m, n_in);
     const int64_t fixed = copy_bytes(sh, copy);
     if (workspace_bytes < forward_need(sh, w, nullptr, copy, true) ||
-        (workspace_bytes > 0 && !workspace))
+        bad_workspace(workspace, workspace_bytes))
         return DQ4_EINVAL;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     hipStream_t s = static_cast<hipStream_t>(stream);
@@ -2621,7 +2907,7 @@ dq4_status_t dq4_gated_fused(const dq4_weight_t *gate, const dq4_weight_t *up, i
     const bool copy = forward_copies(gate, up, x, ld_x, m, n_in);
     const int64_t fixed = copy_bytes(sh, copy);
     if (workspace_bytes < forward_need(sh, gate, up, copy, true) ||
-        (workspace_bytes > 0 && !workspace))
+        bad_workspace(workspace, workspace_bytes))
         return DQ4_EINVAL;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     hipStream_t s = static_cast<hipStream_t>(stream);
@@ -2683,10 +2969,13 @@ dq4_status_t dq4_linear_fused_backward(const dq4_weight_t *w, int64_t n_out, int
     const Shape sh{m, n_in, n_out, kSingle};
     const void *lhs = act ? dz : dy;
     const int64_t ld_lhs = act ? ld_dz : ld_dy;
-    const bool copy = n_in > 0 && needs_copy(lhs, ld_lhs, m, n_out);
-    const int64_t copied = copy_bytes(sh, copy);
+    const ColumnPlan cp = column_plan(w, nullptr, n_out, n_in, m, current_compute_units());
+    const bool copy = cp.use || (n_in > 0 && needs_copy(lhs, ld_lhs, m, n_out));
+    const int64_t copied = cp.use ? cp.frag_bytes() : copy_bytes(sh, copy);
     const int64_t fixed = copied + partial_bytes(m, n_out);
-    if (n_out > 0 && (workspace_bytes < workspace_need(sh, fixed, true) || !workspace))
+    if (n_out > 0 &&
+        (workspace_bytes < linear_backward_need(w, n_out, n_in, m, lhs, ld_lhs, true) ||
+         bad_workspace(workspace, workspace_bytes)))
         return DQ4_EINVAL;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     ProductArgs p{};
@@ -2705,7 +2994,9 @@ dq4_status_t dq4_linear_fused_backward(const dq4_weight_t *w, int64_t n_out, int
         a.ld_dz = ld_dz;
         if (copy) {
             a.pad[0] = reinterpret_cast<uint16_t *>(ws);
-            a.ld_pad = padded_ld(n_out);
+            a.ld_pad = cp.use ? cp.steps * 32 : padded_ld(n_out);
+            a.pad_rows = cp.use ? cp.slices * 16 * cp.tf : m;
+            a.frag_rows = cp.use ? cp.tf : 0;
             p.x[0] = p.x[1] = a.pad[0];
             p.ld_x = p.k = a.ld_pad;
         }
@@ -2737,6 +3028,12 @@ dq4_status_t dq4_linear_fused_backward(const dq4_weight_t *w, int64_t n_out, int
     p.y = static_cast<uint16_t *>(dx);
     p.ld_y = ld_dx;
     p.vec = rows_aligned(dx, ld_dx, m, 8);
+    if (cp.use) {
+        p.partial = reinterpret_cast<f32x4 *>(ws + fixed);
+        return dtype == DQ4_F16
+                   ? run_columns<DQ4_F16>(cp, w, nullptr, n_out, n_in, m, log2_block, p, beside, s)
+                   : run_columns<DQ4_BF16>(cp, w, nullptr, n_out, n_in, m, log2_block, p, beside, s);
+    }
     if (dtype == DQ4_F16)
         return run_product<DQ4_F16, false>(sh, w, nullptr, n_out, n_in, log2_block, p, beside, ws + fixed,
                                            workspace_bytes - fixed, s);
@@ -2765,9 +3062,12 @@ dq4_status_t dq4_gated_fused_backward(const dq4_weight_t *gate, const dq4_weight
                      (n_ff > 0 && (weight_missing(gate) || weight_missing(up)))))
         return DQ4_EINVAL;
     const Shape sh{m, n_in, n_ff, kStacked};
-    const bool copy = n_in > 0 && (needs_copy(dgate, ld_dpre, m, n_ff) || needs_copy(dup, ld_dpre, m, n_ff));
-    const int64_t fixed = copy_bytes(sh, copy);
-    if (n_ff > 0 && (workspace_bytes < workspace_need(sh, fixed, true) || (workspace_bytes > 0 && !workspace)))
+    const ColumnPlan cp = column_plan(gate, up, n_ff, n_in, m, current_compute_units());
+    const bool copy = cp.use || (n_in > 0 && (needs_copy(dgate, ld_dpre, m, n_ff) ||
+                                              needs_copy(dup, ld_dpre, m, n_ff)));
+    const int64_t fixed = cp.use ? 2 * cp.frag_bytes() : copy_bytes(sh, copy);
+    if (n_ff > 0 && (workspace_bytes < gated_backward_need(gate, up, n_ff, n_in, m, dgate, dup, ld_dpre, true) ||
+                     bad_workspace(workspace, workspace_bytes)))
         return DQ4_EINVAL;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     hipStream_t s = static_cast<hipStream_t>(stream);
@@ -2788,7 +3088,9 @@ dq4_status_t dq4_gated_fused_backward(const dq4_weight_t *gate, const dq4_weight
         a.dz[1] = static_cast<uint16_t *>(dup);
         a.ld_dz = ld_dpre;
         if (copy) {
-            a.ld_pad = padded_ld(n_ff);
+            a.ld_pad = cp.use ? cp.steps * 32 : padded_ld(n_ff);
+            a.pad_rows = cp.use ? cp.slices * 16 * cp.tf : m;
+            a.frag_rows = cp.use ? cp.tf : 0;
             a.pad[0] = reinterpret_cast<uint16_t *>(ws);
             a.pad[1] = reinterpret_cast<uint16_t *>(ws + fixed / 2);
             p.x[0] = a.pad[0];
@@ -2811,6 +3113,12 @@ dq4_status_t dq4_gated_fused_backward(const dq4_weight_t *gate, const dq4_weight
     p.y = static_cast<uint16_t *>(dx);
     p.ld_y = ld_dx;
     p.vec = rows_aligned(dx, ld_dx, m, 8);
+    if (cp.use) {
+        p.partial = reinterpret_cast<f32x4 *>(ws + fixed);
+        return dtype == DQ4_F16
+                   ? run_columns<DQ4_F16>(cp, gate, up, n_ff, n_in, m, log2_block, p, beside, s)
+                   : run_columns<DQ4_BF16>(cp, gate, up, n_ff, n_in, m, log2_block, p, beside, s);
+    }
     if (dtype == DQ4_F16)
         return run_product<DQ4_F16, false>(sh, gate, up, n_ff, n_in, log2_block, p, beside, ws + fixed,
                                            workspace_bytes - fixed, s);

@@ -26,12 +26,12 @@
  * (in elements) given as ld_*; a single row's stride is not looked at.  Only
  * the m rows and their columns are read or written: what lies between the
  * rows of a strided matrix, and behind the last row, stays as it was.
- * No pointer has to be aligned beyond its element type; 16-byte aligned rows
- * take the fastest path.  `residual` may be `y` itself (same pointer and row
+ * No pointer but the workspace's has to be aligned beyond its element type;
+ * 16-byte aligned rows and 4-byte aligned packed codes take the fastest paths.  `residual` may be `y` itself (same pointer and row
  * stride); no other output may overlap an input or another output.
  *
- * workspace: caller-owned device memory of at least the bytes that the
- * call's *_workspace_bytes function returns with `least` = 1; with the bytes
+ * workspace: caller-owned device memory, 256-byte aligned, of at least the
+ * bytes that the call's *_workspace_bytes function returns with `least` = 1; with the bytes
  * of `least` = 0 the decoded weight of the large-m route fits whole, with
  * fewer it passes through in windows of output columns.  Its contents do not
  * matter before the call, and after it the workspace holds nothing of use.
@@ -45,6 +45,7 @@
  * packed codes; for another number of rows the sums may run in another order.
  *   DQ4_EINVAL       negative size, row stride below the row length, missing
  *                    pointer, unknown type or activation, workspace too small
+ *                    or not 256-byte aligned
  *   DQ4_EUNSUPPORTED block layout that dq4_nested_dequant rejects, two
  *                    weights with different block sizes, m, n_out or n_in
  *                    above 2^21, m n_out or m n_in above 2^39

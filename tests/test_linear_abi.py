@@ -9,7 +9,7 @@ import block_wise_bit_amd as dq4
 from libs import ensure_hip_library
 
 P = ctypes.c_void_p
-ONE = P(16)
+ONE = P(256)
 
 
 @pytest.fixture(scope="module")
@@ -50,6 +50,7 @@ def test_linear_validation(lib):
     assert call(n_out=0) == dq4.DQ4_OK
     assert call(m=300) == dq4.DQ4_EINVAL                          # no workspace
     assert call(ws=None, ws_bytes=BIG) == dq4.DQ4_EINVAL
+    assert call(ws=P(16), ws_bytes=BIG) == dq4.DQ4_EINVAL         # not 256-byte aligned
     for k in (dict(null_w=True), dict(x=None), dict(y=None), dict(m=-1), dict(n_out=-1), dict(n_in=-1),
               dict(dtype=dq4.DQ4_F32), dict(dtype=7), dict(act=5), dict(act=-1), dict(ld_x=127),
               dict(ld_y=63), dict(res=ONE, ld_res=63), dict(pre=ONE, ld_pre=63), dict(w=weight(ptr=None)),

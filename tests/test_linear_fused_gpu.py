@@ -60,6 +60,9 @@ SHAPES = [
     (31, 100, 1056, 4096, "nf4"), (33, 4100, 640, 128, "fp4"), (64, 31, 4608, 64, "nf4"),
     (48, 17, 32, 32, "nf4"), (8, 300, 2080, 256, "nf4"), (100, 90, 576, 64, "nf4"),
     (128, 1030, 64, 64, "fp4"), (130, 40, 1056, 32, "nf4"), (192, 300, 512, 64, "nf4"),
+    # gradients of few rows: steps of 32 weight rows over all splits, columns
+    # and rows that end inside a group or a step
+    (1, 3000, 136, 64, "nf4"), (16, 33, 4104, 32, "fp4"), (33, 1025, 264, 4096, "nf4"), (64, 2050, 520, 64, "nf4"),
     # ... with rows of whole dwords only
     (3, 50, 2056, 32, "nf4"), (40, 4200, 168, 64, "nf4"), (20, 90, 1000, 4096, "fp4"),
 ]
@@ -564,6 +567,7 @@ def test_refusals():
     refused(f, **w, **s, x=x, y=x[:, :64])                          # y over x
     refused(f, **w, **s, x=x, y=y, pre=y)
     refused(f, **w, **s, x=x.repeat(100, 1), workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    refused(f, **w, **s, x=x.repeat(100, 1), workspace=torch.empty(1 << 24, dtype=torch.uint8, device="cuda")[8:])
     refused(f, **w, **dict(s, blocksize=48), x=x)
     refused(f, **w, **dict(s, n_out=65), x=x)                       # more than the weight holds
     refused(f, **w, **dict(s, n_out=-1), x=x)
