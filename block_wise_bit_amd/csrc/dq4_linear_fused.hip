@@ -3,11 +3,18 @@
 // feed-forward block, and the backward passes (include/dq4_linear.h).
 //
 // Route for any size: the weight is decoded once into 16-bit operand fragments
-// of the matrix instruction in the workspace (weight_fragments_kernel), then
-// one matrix kernel (fragment_product_kernel) multiplies and finishes each
-// output in its epilogue.  The decode moves 2.5 bytes per weight element, the
-// product 2 m operations per element: the decode is small against the
-// product once m is in the hundreds.
+// of the matrix instruction in the workspace (weight_fragments_kernel,
+// weight_row_fragments_kernel), then one matrix kernel (fragment_product_kernel,
+// fragment_product_wide_kernel) multiplies and finishes each output in its
+// epilogue.  The decode moves 2.5 bytes per weight element, the product 2 m
+// operations per element: the decode is small against the product once m is
+// in the hundreds.
+//
+// Few rows: the call is bound by reading the 4-bit weight and by decoding it,
+// so the weight is decoded straight into operand registers and no copy is
+// written: token_rows_kernel (forward, m <= 2), batch_rows_kernel (forward, m <=
+// 192), ragged_rows_kernel (forward, m <= 64, rows of whole dwords only),
+// weight_columns_kernel (backward, m <= 128).
 //
 // Fragment layout.  The output columns n (weight rows forward, weight columns
 // backward) are taken in groups of 128, the summed index k in chunks of 64.
@@ -1436,7 +1443,7 @@ __global__ __launch_bounds__(64 * kDecodeWaves) void weight_row_fragments_kernel
 }
 
 // ---------------------------------------------------------------------------
-// one to four rows of x: weight rows read in straight lines
+// one or two rows of x: weight rows read in straight lines
 // ---------------------------------------------------------------------------
 // The products are dot products of whole weight rows, and the 4-bit weight is
 // all the memory traffic, so every load of it is 1 KiB of one row: lane l takes
@@ -1682,7 +1689,7 @@ __global__ __launch_bounds__(64 * WAVES) void token_rows_kernel(TokenArgs a)
 }
 
 // ---------------------------------------------------------------------------
-// 5 to 192 rows of x: weight rows read 64 bytes at a time, transposed in registers
+// 3 to 192 rows of x: weight rows read 64 bytes at a time, transposed in registers
 // ---------------------------------------------------------------------------
 // x in operand fragments: fragment (chunk of 512 k, step, 16 rows of x) is 1
 // KiB in lane order; lane (r, g) of step 4 j + s holds row r's k 512 c + 128 g
@@ -2275,14 +2282,20 @@ int64_t workspace_need(const Shape &s, int64_t fixed, bool least)
 
 // Which kernel a forward call takes.
 enum Route {
-    kTokenRoute,    // up to 4 rows of x, weight rows of up to 32768
+    kTokenRoute,    // one or two rows of x, weight rows of up to 32768
     kBatchRoute,    // up to 192: 64 rows a reading of the weight
     kRaggedRoute,   // up to 64, weight rows of whole dwords that are not 32 k apart
     kProductRoute   // decode to fragments, then the product
 };
 
-// Where the routes meet, measured: see the entry's comment.
-constexpr int64_t kTokenMost = 4, kBatchMost = 192, kRaggedMost = 64;
+// Where the routes meet, in whole calls (BF16 unless said otherwise, us):
+//   token | batch: gated 28672 x 8192 at m = 2 75 | 80, at m = 4 97 | 80; gated
+//     11008 x 4096 at m = 2 19 | 23, at m = 4 24 | 23
+//   batch | product: gated 11008 x 4096 at m = 192 92 | 118, at 256 about 122 |
+//     122; gated 28672 x 8192 at m = 192 338 | 477
+//   ragged | product: FP16 4096 x 11000 at m = 64 58 | 73; more rows would
+//     read the weight twice
+constexpr int64_t kTokenMost = 2, kBatchMost = 192, kRaggedMost = 64;
 
 Route route_of(const dq4_weight_t *w0, const dq4_weight_t *w1, int64_t n_in, int64_t m)
 {
@@ -2296,8 +2309,12 @@ Route route_of(const dq4_weight_t *w0, const dq4_weight_t *w1, int64_t n_in, int
 }
 
 // A backward call with few rows of dz whose weight rows are whole dwords
-// decodes in registers (weight_columns_kernel).
-constexpr int64_t kColumnsMost = 64;
+// decodes in registers (weight_columns_kernel), once for 32 rows.  Against the
+// product over a decoded copy, in whole calls (BF16, us): linear 4096 x 4096 at
+// m = 128 29 | 39, gated 11008 x 4096 at m = 128 74 | 118; from m = 129 on a
+// fifth reading of the weight brings them level (gated 28672 x 8192 at m = 192
+// 570 | about 600, linear 11008 x 4096 at m = 192 69 | 60).
+constexpr int64_t kColumnsMost = 128;
 
 struct ColumnPlan {
     bool use;
@@ -2430,7 +2447,7 @@ dq4_status_t launch_token_rows(const RowsArgs &r, int cus, hipStream_t s)
     a.out = r.out;
     void *params[] = {&a};
     // with a single pair for each wave there is nothing to load ahead: 4096 x
-    // 4096 at m = 1 10.6 us with a ring of three, TOKEN1 us with one
+    // 4096 at m = 1 takes 10.6 us with a ring of three, 7.6 us with one
     if (a.rows_per + (a.rows_extra ? 1 : 0) <= pair && pair <= fit) {
         a.batch = pair;
         return launch(reinterpret_cast<const void *>(&token_rows_kernel<OUT, kGated, M, kWaves, 1>), grid,
@@ -2497,9 +2514,7 @@ dq4_status_t launch_few_rows(const RowsArgs &a, Route route, uint8_t *workspace,
         return launch_batch<OUT, kGated>(a, workspace, cus, s);
     if (a.out.m == 1)
         return launch_token_rows<OUT, kGated, 1>(a, cus, s);
-    if (a.out.m == 2)
-        return launch_token_rows<OUT, kGated, 2>(a, cus, s);
-    return launch_token_rows<OUT, kGated, 4>(a, cus, s);
+    return launch_token_rows<OUT, kGated, 2>(a, cus, s);
 }
 
 // The work beside a decode: which, and in how many workgroups.
