@@ -8,13 +8,13 @@
 // fragment_product_wide_kernel) multiplies and finishes each output in its
 // epilogue.  The decode moves 2.5 bytes per weight element, the product 2 m
 // operations per element: the decode is small against the product once m is
-// in the hundreds.
+// above a thousand.
 //
-// Few rows: the call is bound by reading the 4-bit weight and by decoding it,
+// Fewer rows: the call is bound by reading the 4-bit weight and by decoding it,
 // so the weight is decoded straight into operand registers and no copy is
 // written: token_rows_kernel (forward, m <= 2), batch_rows_kernel (forward, m <=
-// 192), ragged_rows_kernel (forward, m <= 64, rows of whole dwords only),
-// weight_columns_kernel (backward, m <= 128).
+// 64), tile_rows_kernel (forward, m <= 1024), ragged_rows_kernel (forward, m <=
+// 64, rows of whole dwords only), weight_columns_kernel (backward, m <= 128).
 //
 // Fragment layout.  The output columns n (weight rows forward, weight columns
 // backward) are taken in groups of 128, the summed index k in chunks of 64.
@@ -1689,12 +1689,12 @@ __global__ __launch_bounds__(64 * WAVES) void token_rows_kernel(TokenArgs a)
 }
 
 // ---------------------------------------------------------------------------
-// 3 to 192 rows of x: weight rows read 64 bytes at a time, transposed in registers
+// 3 to 64 rows of x: weight rows read 64 bytes at a time, transposed in registers
 // ---------------------------------------------------------------------------
 // x in operand fragments: fragment (chunk of 512 k, step, 16 rows of x) is 1
 // KiB in lane order; lane (r, g) of step 4 j + s holds row r's k 512 c + 128 g
-// + 32 j + 8 s .. + 7.  Rows and k beyond x are zeros.  More than 64 rows are
-// cut into slices of 64 (blockIdx.y), one after the other.
+// + 32 j + 8 s .. + 7.  Rows and k beyond x are zeros.  More than 128 rows are
+// cut into slices of 128 (blockIdx.y), one after the other.
 __global__ __launch_bounds__(kThreads) void x_fragments_zero_fill(const uint16_t *x, int64_t ld_x,
                                                                   int64_t m, int64_t k, int32_t tf,
                                                                   int32_t frags, bool aligned,
@@ -1705,7 +1705,7 @@ __global__ __launch_bounds__(kThreads) void x_fragments_zero_fill(const uint16_t
     if (fr >= frags)
         return;
     const int step = fr / tf, t = fr - step * tf;
-    const int64_t row = blockIdx.y * 64 + t * 16 + (lane & 15);
+    const int64_t row = static_cast<int64_t>(blockIdx.y) * (16 * tf) + t * 16 + (lane & 15);
     const int64_t k0 = static_cast<int64_t>(step >> 4) * 512 + 128 * (lane >> 4) + 8 * (step & 15);
     u32x4 q = {0, 0, 0, 0};
     if (row < m && k0 < k) {
@@ -1743,8 +1743,8 @@ __device__ __forceinline__ void transpose_quads(uint32_t (&v)[4], bool odd, bool
     v[3] = high ? a3 : y1;
 }
 
-// 16 TF rows of x against the 4-bit weight, which is read once (for each 64
-// rows of x) and never written out.  A wave takes two fragments of 16 weight rows (gated: one of
+// 16 TF rows of x against the 4-bit weight, which is read once and never
+// written out.  A wave takes two fragments of 16 weight rows (gated: one of
 // each weight, the same columns) and chunks of 512 k.  The matrix instruction
 // wants neighbouring lanes in different weight rows, memory wants them side by
 // side (a load whose neighbouring lanes lie in 16 rows took 64 accesses of the
@@ -1766,9 +1766,6 @@ __global__ __launch_bounds__(512) void batch_rows_kernel(RowsArgs a, const uint1
     __shared__ float scb[kW][256], cb4[kW][16];
     __shared__ __attribute__((aligned(16))) f32x4 partial[8][R * TF][64];
 
-    // slice blockIdx.y of 64 rows of x; the weight is read again for each
-    const int64_t x_row0 = static_cast<int64_t>(blockIdx.y) * 64;
-    x_frags += static_cast<int64_t>(blockIdx.y) * ((a.n_in + 511) / 512) * (16 * TF * 512);
     const int tid = threadIdx.x;
     const int lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -1960,7 +1957,7 @@ __global__ __launch_bounds__(512) void batch_rows_kernel(RowsArgs a, const uint1
             for (int q = 1; q < WK; ++q)
                 sum = sum + partial[row_wave * WK + q][f * TF + t][ln];
             const int64_t n0 = rb * block_rows + row_wave * (16 * kPer) + f * 16 + (ln >> 4) * 4;
-            const int64_t row = x_row0 + t * 16 + (ln & 15);
+            const int64_t row = t * 16 + (ln & 15);
             if constexpr (kGated) {
                 f32x4 up = partial[row_wave * WK][TF + t][ln];
                 for (int q = 1; q < WK; ++q)
@@ -1971,6 +1968,293 @@ __global__ __launch_bounds__(512) void batch_rows_kernel(RowsArgs a, const uint1
                 finish_linear4<OUT>(a.out, row, n0, sum);
             }
         }
+    }
+}
+
+// 65 to 1024 rows of x: a tile of 128 rows of x and 256 weight rows (gated: 128
+// of each weight), over all of k or one of `splits` parts of it.  The weight
+// comes as in batch_rows_kernel, but a wave walks all the tile's k for 32
+// weight rows of its own, so that the 8 waves share x's fragments: four steps
+// of them at a time go straight to LDS, double buffered.  Per step of 32 k a
+// wave looks up 2 packed dwords per lane, reads 8 x fragments and issues 16
+// matrix instructions; the LDS bounds it (about 880 cycles per step of the
+// workgroup, 370 of them lookups, against 512 of the matrix pipe).  Measured:
+// 0.5 us per step, a tile of 8192 k in 130 us; gated 28672 x 8192 with 512 rows
+// 542 us, 0.89 PFLOP/s, where decode and product take 676.
+template <int OUT, bool kGated, int S>
+__global__ __launch_bounds__(512) void tile_rows_kernel(RowsArgs a, const uint16_t *x_frags)
+{
+    constexpr int R = 2, TF = 8, kW = kGated ? 2 : 1;
+    constexpr int kPer = R / kW;
+    constexpr int kSpan = 512;
+    constexpr int kStage = 4 * TF * kFragBytes;  // x's fragments of 4 steps: 32 KiB
+    __shared__ __attribute__((aligned(1024))) uint8_t table[kPairTableBytes + 256];
+    __shared__ float scb[kW][256], cb4[kW][16];
+    __shared__ __attribute__((aligned(1024))) uint8_t stage[2 * kStage];
+
+    // slice blockIdx.y of 128 rows of x; the weight is read again for each
+    const int64_t x_row0 = static_cast<int64_t>(blockIdx.y) * (16 * TF);
+    x_frags += static_cast<int64_t>(blockIdx.y) * ((a.n_in + 511) / 512) * (16 * TF * 512);
+    const int tid = threadIdx.x;
+    const int lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wr = wave;
+    const int g = lane >> 4;
+    constexpr int block_rows = 16 * kPer * 8;
+    const int split = blockIdx.x / a.row_blocks;
+    const int64_t rb = static_cast<int>(blockIdx.x) - split * a.row_blocks;
+    const int lb = a.log2_block;
+    const uint32_t n_in = static_cast<uint32_t>(a.n_in);
+    const int chunks = static_cast<int>((n_in + kSpan - 1) / kSpan);
+    const int begin = split * chunks / a.out.splits, end = (split + 1) * chunks / a.out.splits;
+    const bool odd = lane & 1, high = lane & 2;
+
+    struct Loads {
+        u32x4 packed[R][4];
+        uint32_t code[R][S];
+        float absmax[R][S];
+    };
+    const auto rsrc_of = [](const void *p, int64_t bytes) {
+        return __builtin_amdgcn_make_buffer_rsrc(
+            const_cast<void *>(p), 0,
+            static_cast<int32_t>(bytes < 0 ? 0 : bytes < 0x7FFFFFF0 ? bytes : 0x7FFFFFF0),
+            kRawBufferWord3);
+    };
+    const uint32_t k_load = 32 * (((lane >> 4) << 2) | (lane & 3));  // of the loaded piece
+    const uint32_t row_load = 4 * ((lane >> 2) & 3);
+    const int64_t blocks = (a.n_elems + (int64_t{1} << lb) - 1) >> lb;
+    auto load = [&](Loads &l, int c) {
+        const int64_t row0 = rb * block_rows + wr * (16 * kPer);
+        const int64_t e0 = row0 * a.n_in;
+        const int64_t b0 = e0 >> lb;
+        const uint32_t phase = static_cast<uint32_t>(e0) & ((1u << lb) - 1);
+        const uint32_t group_phase = static_cast<uint32_t>(b0) & 255;
+        const int64_t packed_left = ((a.n_elems + 1) >> 1) - (e0 >> 1);
+        const uint32_t k = c * kSpan + k_load;
+        const uint32_t past = k < n_in ? 0u : 0x80000000u;
+#pragma unroll
+        for (int f = 0; f < R; ++f) {
+            const int w = kGated ? f : 0;
+            const uint32_t frag_row = kGated ? 0 : f * 16;
+            const auto rp = rsrc_of(a.w[w].packed + (e0 >> 1), packed_left);
+            const auto rc = rsrc_of(a.w[w].scale_codes + b0, blocks - b0);
+            const auto rm = rsrc_of(a.w[w].nested_absmax + (b0 >> 8), (((blocks + 255) >> 8) - (b0 >> 8)) * 4);
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                l.packed[f][q] = __builtin_amdgcn_raw_buffer_load_b128(
+                    rp, (((frag_row + row_load + q) * n_in + k) >> 1) | past, 0, 0);
+#pragma unroll
+            for (int h = 0; h < S; ++h) {
+                // of row lane / 4, the lane's quarter of the chunk
+                const uint32_t e = (frag_row + (lane >> 2)) * n_in + c * kSpan + 128 * (lane & 3) + h * (128 / S);
+                const uint32_t b = (phase + e) >> lb;
+                l.code[f][h] = __builtin_amdgcn_raw_buffer_load_b8(rc, b, 0, 0);
+                l.absmax[f][h] = __builtin_bit_cast(
+                    float, __builtin_amdgcn_raw_buffer_load_b32(rm, ((group_phase + b) >> 8) * 4, 0, 0));
+            }
+        }
+    };
+    // four steps' x fragments, 32 KiB in a row, straight to LDS: 4 KiB a wave
+    const u32x4 rs_x = make_rsrc(x_frags, static_cast<uint32_t>(chunks) * (4 * kStage));
+    const uint32_t lds0 = lds_offset(stage);
+    auto issue_x = [&](int q) {  // stage q = 4 chunk + j
+        const uint32_t at = static_cast<uint32_t>(q) * kStage + wave * (4 * kFragBytes);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            buffer_to_lds(rs_x, lane * 16, at + i * kFragBytes,
+                          lds0 + (q & 1) * kStage + wave * (4 * kFragBytes) + i * kFragBytes);
+    };
+
+    // one register, hidden from the compiler, so that each read is it plus an
+    // immediate offset; without it every read's address took a register of its own
+    uint32_t x_at = lds0 + lane * 16;
+    __asm__("" : "+v"(x_at));
+    const auto *x_lane = reinterpret_cast<const __attribute__((address_space(3))) u32x4 *>(x_at);
+
+    const Codebooks codebooks = fetch_codebooks<kW>(a.w);
+    Loads cur;
+    issue_x(4 * begin);
+    load(cur, begin);
+
+    // the lookup tables, while the first loads are in flight
+    fill_tables<kW, 1>(codebooks, table, scb, cb4);
+
+    const uint32_t lane_byte = kGated ? (lane & 15) * 16 : (lane & 31) * 8;
+    wait_all_and_barrier();
+    f32x4 acc[R][TF];
+#pragma unroll
+    for (int f = 0; f < R; ++f)
+#pragma unroll
+        for (int t = 0; t < TF; ++t)
+            acc[f][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int c = begin; c < end; ++c) {
+        Loads next;
+        float s[R][S];
+#pragma unroll
+        for (int f = 0; f < R; ++f) {
+#pragma unroll
+            for (int h = 0; h < S; ++h) {
+                const float q = block_scale(scb[kGated ? f : 0][cur.code[f][h]], cur.absmax[f][h],
+                                            a.w[kGated ? f : 0].offset);
+                // lane 16 g + r multiplies quarter g of row r
+                s[f][h] = __builtin_bit_cast(
+                    float, __builtin_amdgcn_ds_bpermute((4 * (lane & 15) + g) * 4, __builtin_bit_cast(int, q)));
+            }
+#pragma unroll
+            for (int d = 0; d < 4; ++d) {
+                uint32_t v[4] = {cur.packed[f][0][d], cur.packed[f][1][d], cur.packed[f][2][d],
+                                 cur.packed[f][3][d]};
+                transpose_quads(v, odd, high);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    cur.packed[f][j][d] = v[j];
+            }
+        }
+        const uint32_t k = c * kSpan + 128 * g;
+        // a piece beyond the row (its load gave zeros) reads the row of
+        // zeros behind the table, times 0
+        const auto from = [&](int j) {
+            return k + 32 * j >= n_in ? lane_byte | kPairTableBytes : lane_byte;
+        };
+        Pairs now[R];
+#pragma unroll
+        for (int f = 0; f < R; ++f)
+            now[f] = lookup_dword(cur.packed[f][0][0], table + (kGated ? f : 0) * 8, from(0));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int q = 4 * c + j;
+            u32x4 x[2][TF / 2];  // the first half of a step's, the second
+            auto read_x = [&](int d, int half) {
+#pragma unroll
+                for (int t = 0; t < TF / 2; ++t)
+                    x[half][t] =
+                        x_lane[((j & 1) * kStage + (d * TF + half * (TF / 2) + t) * kFragBytes) / 16];
+            };
+            read_x(0, 0);
+            issue_x(q + 1 < 4 * end ? q + 1 : q - 1);  // at the end: a stage nobody reads
+            if (j == 1)
+                load(next, c + 1 < end ? c + 1 : c);
+#pragma unroll
+            for (int d = 0; d < 4; ++d) {
+                const int st = 4 * j + d;
+                u32x4 wf[R];
+                read_x(d, 1);
+#pragma unroll
+                for (int f = 0; f < R; ++f)
+                    wf[f] = scaled_dword<OUT>(now[f], k + 32 * j >= n_in ? 0.0f : s[f][j * S / 4]);
+                keep_order();
+                if (st < 15) {
+#pragma unroll
+                    for (int f = 0; f < R; ++f)
+                        now[f] = lookup_dword(cur.packed[f][(st + 1) / 4][(st + 1) % 4],
+                                              table + (kGated ? f : 0) * 8, from((st + 1) / 4));
+                }
+                keep_order();
+#pragma unroll
+                for (int f = 0; f < R; ++f)
+#pragma unroll
+                    for (int t = 0; t < TF / 2; ++t)
+                        acc[f][t] = Half<OUT>::mfma(wf[f], x[0][t], acc[f][t]);
+                keep_order();
+                if (d < 3)
+                    read_x(d + 1, 0);
+#pragma unroll
+                for (int f = 0; f < R; ++f)
+#pragma unroll
+                    for (int t = 0; t < TF / 2; ++t)
+                        acc[f][TF / 2 + t] = Half<OUT>::mfma(wf[f], x[1][t], acc[f][TF / 2 + t]);
+                keep_order();
+            }
+            // the next stage has arrived: behind its loads only the next
+            // chunk's weight loads (more than 8) may be under way
+            if (j == 1)
+                __asm__ volatile("s_waitcnt vmcnt(8) lgkmcnt(0)" ::: "memory");
+            else
+                __asm__ volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+            __builtin_amdgcn_s_barrier();
+            __asm__ volatile("" ::: "memory");
+        }
+        cur = next;
+    }
+    if (a.out.splits > 1) {
+        f32x4 *to = a.out.partial +
+                    (((static_cast<int64_t>(split) * gridDim.y + blockIdx.y) * a.row_blocks + rb) * 8 + wave) *
+                        (TF * R * 64) + lane;
+#pragma unroll
+        for (int t = 0; t < TF; ++t)
+#pragma unroll
+            for (int f = 0; f < R; ++f)
+                to[(t * R + f) * 64] = acc[f][t];
+        return;
+    }
+    // the epilogue, 4 x 16 rows of x at a time through this wave's part of
+    // the stages, so that its code is there once
+    f32x4 *mine = reinterpret_cast<f32x4 *>(stage + wave * (8 * kFragBytes));
+    const int64_t n0 = rb * block_rows + wr * (16 * kPer) + g * 4;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+#pragma unroll
+        for (int f = 0; f < R; ++f)
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+                mine[(t * R + f) * 64 + lane] = acc[f][half * 4 + t];
+#pragma unroll 1
+        for (int t = 0; t < 4; ++t) {
+            const int64_t row = x_row0 + (half * 4 + t) * 16 + (lane & 15);
+            const f32x4 u = mine[(t * R) * 64 + lane], v = mine[(t * R + 1) * 64 + lane];
+            if constexpr (kGated) {
+                float gv[4] = {u[0], u[1], u[2], u[3]}, uv[4] = {v[0], v[1], v[2], v[3]};
+                finish_gated<OUT>(a.out, row, n0, gv, uv);
+            } else {
+                finish_linear4<OUT>(a.out, row, n0, u);
+                finish_linear4<OUT>(a.out, row, n0 + 16, v);
+            }
+        }
+    }
+}
+
+// The splits' sums of 16 rows of x and one wave's 32 weight rows, added in
+// order, and the epilogue: a wave each, with the loads of 8 splits in flight.
+template <int OUT, bool kGated>
+__global__ __launch_bounds__(256) void tile_rows_reduce_kernel(RowsArgs a)
+{
+    constexpr int R = 2, TF = 8;
+    const int lane = threadIdx.x & 63;
+    const int t = blockIdx.x % 2 * 4 + (threadIdx.x >> 6);
+    const int64_t part = blockIdx.x / 2;  // wave of a row block
+    const int64_t row0 = (static_cast<int64_t>(blockIdx.y) * TF + t) * 16;
+    if (row0 >= a.out.m)
+        return;
+    const int64_t step = static_cast<int64_t>(gridDim.y) * a.row_blocks * (8 * TF * R * 64);
+    const f32x4 *from = a.out.partial +
+                        ((static_cast<int64_t>(blockIdx.y) * a.row_blocks * 8 + part) * TF + t) * (R * 64) + lane;
+    f32x4 sum[R];
+#pragma unroll
+    for (int f = 0; f < R; ++f)
+        sum[f] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int s = 0; s < a.out.splits; s += 8) {
+        f32x4 v[8][R];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int f = 0; f < R; ++f)  // past the last split: the first again, left out below
+                v[i][f] = from[(s + i < a.out.splits ? s + i : s) * step + f * 64];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (s + i < a.out.splits)
+#pragma unroll
+                for (int f = 0; f < R; ++f)
+                    sum[f] = sum[f] + v[i][f];
+    }
+    const int64_t row = row0 + (lane & 15);
+    const int64_t n0 = part * (16 * (kGated ? 1 : R)) + (lane >> 4) * 4;
+    if constexpr (kGated) {
+        float g[4] = {sum[0][0], sum[0][1], sum[0][2], sum[0][3]};
+        float u[4] = {sum[1][0], sum[1][1], sum[1][2], sum[1][3]};
+        finish_gated<OUT>(a.out, row, n0, g, u);
+    } else {
+        finish_linear4<OUT>(a.out, row, n0, sum[0]);
+        finish_linear4<OUT>(a.out, row, n0 + 16, sum[1]);
     }
 }
 
@@ -2208,6 +2492,7 @@ int current_compute_units()
 struct Plan {
     int tile;      // 0: 256 x 256, 1: 128 x 128, 2: 128 x 64
     int splits;
+    double cost;   // microseconds, roughly
 };
 
 constexpr int kTileCols[3] = {256, 128, 128}, kTileRows[3] = {256, 128, 64};
@@ -2218,8 +2503,7 @@ constexpr double kTileChunk[3] = {1.78, 1.40, 1.80};
 
 Plan plan_of(int64_t m, int64_t groups, int64_t all_chunks, int cus)
 {
-    Plan best{2, 1};
-    double least = 1e300;
+    Plan best{2, 1, 1e300};
     for (int tile = 0; tile < 3; ++tile) {
         const int64_t tiles = ceil_div(groups * kGroup, kTileCols[tile]) * ceil_div(m, kTileRows[tile]);
         for (int splits = 1; splits <= 16; ++splits) {
@@ -2231,10 +2515,8 @@ Plan plan_of(int64_t m, int64_t groups, int64_t all_chunks, int cus)
             if (splits > 1)  // the partial sums, written and read at about 4 TB/s, and a launch
                 cost += 3.0 + static_cast<double>(splits) * static_cast<double>(m) *
                                   static_cast<double>(groups * kGroup) * 8.0 / 4e6;
-            if (cost < least) {
-                least = cost;
-                best = Plan{tile, splits};
-            }
+            if (cost < best.cost)
+                best = Plan{tile, splits, cost};
         }
     }
     return best;
@@ -2280,10 +2562,40 @@ int64_t workspace_need(const Shape &s, int64_t fixed, bool least)
     return fixed + s.window_bytes(s.plan(current_compute_units()), groups);
 }
 
+// How the tile route is cut: its 128 x 256 tiles, each over one of `splits`
+// parts of k where the tiles alone leave CUs idle.
+struct TilePlan {
+    int64_t row_blocks, slices;
+    int splits;
+    double cost;  // microseconds, roughly
+    int64_t partial_bytes() const { return splits == 1 ? 0 : splits * row_blocks * slices * (128 * 256 * 4); }
+};
+
+TilePlan tile_plan(int64_t m, int64_t n_out, int64_t n_in, bool gated, int cus)
+{
+    TilePlan p{ceil_div(n_out, gated ? 128 : 256), ceil_div(m, 128), 1, 1e300};
+    const int64_t tiles = p.row_blocks * p.slices, chunks = ceil_div(n_in, 512);
+    for (int splits = 1; splits <= 16 && splits <= chunks; ++splits) {
+        // microseconds, as measured: 8 a chunk of 512 k, 9 until the tables
+        // are filled and the first loads have come; the partial sums, written
+        // and read at about 4 TB/s, and a launch
+        double cost = static_cast<double>(ceil_div(tiles * splits, cus)) *
+                      (static_cast<double>(ceil_div(chunks, splits)) * 8.0 + 9.0);
+        if (splits > 1)
+            cost += 3.0 + static_cast<double>(tiles * splits) * (128 * 256 * 8.0 / 4e6);
+        if (cost < p.cost) {
+            p.cost = cost;
+            p.splits = splits;
+        }
+    }
+    return p;
+}
+
 // Which kernel a forward call takes.
 enum Route {
     kTokenRoute,    // one or two rows of x, weight rows of up to 32768
-    kBatchRoute,    // up to 192: 64 rows a reading of the weight
+    kBatchRoute,    // up to 64 rows: x's fragments from memory, waves along k
+    kTileRoute,     // up to 1024: tiles of 128 rows of x, x's fragments through LDS
     kRaggedRoute,   // up to 64, weight rows of whole dwords that are not 32 k apart
     kProductRoute   // decode to fragments, then the product
 };
@@ -2291,21 +2603,33 @@ enum Route {
 // Where the routes meet, in whole calls (BF16 unless said otherwise, us):
 //   token | batch: gated 28672 x 8192 at m = 2 75 | 80, at m = 4 97 | 80; gated
 //     11008 x 4096 at m = 2 19 | 23, at m = 4 24 | 23
-//   batch | product: gated 11008 x 4096 at m = 192 92 | 118, at 256 about 122 |
-//     122; gated 28672 x 8192 at m = 192 338 | 477
+//   batch | tile, which costs the same for 1 to 128 rows: gated 28672 x 8192 at
+//     m = 64 119 | 151, two readings at m = 128 232 | 151; gated 11008 x 4096 at
+//     m = 64 33 | 48, at m = 128 63 | 49
+//   tile | product: the lesser of the two plans' costs, since both step with
+//     whole rounds of tiles: gated 28672 x 8192 at m = 512 542 | 676, at m =
+//     1024 994 | 1083 (beyond, the decode is a small part); linear 11008 x 4096
+//     at m = 512 77 | 80, at m = 700 141 | 110
 //   ragged | product: FP16 4096 x 11000 at m = 64 58 | 73; more rows would
 //     read the weight twice
-constexpr int64_t kTokenMost = 2, kBatchMost = 192, kRaggedMost = 64;
+constexpr int64_t kTokenMost = 2, kBatchMost = 64, kTileMost = 1024, kRaggedMost = 64;
 
-Route route_of(const dq4_weight_t *w0, const dq4_weight_t *w1, int64_t n_in, int64_t m)
+Route route_of(const dq4_weight_t *w0, const dq4_weight_t *w1, const Shape &s, int cus)
 {
-    if (m > kBatchMost || n_in == 0 || n_in % 8 != 0 ||
+    if (s.m > kTileMost || s.k == 0 || s.k % 8 != 0 ||
         reinterpret_cast<uintptr_t>(w0->packed) % 4 != 0 ||
         (w1 && reinterpret_cast<uintptr_t>(w1->packed) % 4 != 0))
         return kProductRoute;
-    if (n_in % 32 != 0)
-        return m <= kRaggedMost ? kRaggedRoute : kProductRoute;
-    return m <= kTokenMost && n_in <= kTokenMaxChunks * kTokenSpan ? kTokenRoute : kBatchRoute;
+    if (s.k % 32 != 0)
+        return s.m <= kRaggedMost ? kRaggedRoute : kProductRoute;
+    if (s.m <= kTokenMost && s.k <= kTokenMaxChunks * kTokenSpan)
+        return kTokenRoute;
+    if (s.m <= kBatchMost)
+        return kBatchRoute;
+    // the product's decode: 5.2 TB/s, and a launch
+    const double decode = 5.0 + static_cast<double>(s.n * s.k) * (w1 ? 2.0 : 1.0) * 4.8e-7;
+    return tile_plan(s.m, s.n, s.k, w1 != nullptr, cus).cost < s.plan(cus).cost + decode ? kTileRoute
+                                                                                        : kProductRoute;
 }
 
 // A backward call with few rows of dz whose weight rows are whole dwords
@@ -2348,15 +2672,23 @@ ColumnPlan column_plan(const dq4_weight_t *w0, const dq4_weight_t *w1, int64_t n
 
 int x_row_frags(int64_t m)
 {
-    return m <= 16 ? 1 : m <= 32 ? 2 : 4;
+    return m <= 16 ? 1 : m <= 32 ? 2 : m <= 64 ? 4 : 8;
+}
+
+// Bytes of x in operand fragments.
+int64_t x_fragment_bytes(int64_t m, int64_t k)
+{
+    const int64_t tf = x_row_frags(m);
+    return ceil_div(m, 16 * tf) * ceil_div(k, 512) * 16 * tf * kFragBytes;
 }
 
 // Whether a forward call needs x in 16-byte aligned rows and x is not (the
-// batch route lays x out in fragments, from any rows).
-bool forward_copies(const dq4_weight_t *w0, const dq4_weight_t *w1, const void *x, int64_t ld_x,
-                    int64_t m, int64_t n_in)
+// batch and tile routes lay x out in fragments, from any rows).
+bool forward_copies(const Shape &s, const dq4_weight_t *w0, const dq4_weight_t *w1, const void *x,
+                    int64_t ld_x)
 {
-    return route_of(w0, w1, n_in, m) != kBatchRoute && needs_copy(x, ld_x, m, n_in);
+    const Route route = route_of(w0, w1, s, current_compute_units());
+    return route != kBatchRoute && route != kTileRoute && needs_copy(x, ld_x, s.m, s.k);
 }
 
 // Workspace of a forward call.
@@ -2364,11 +2696,14 @@ int64_t forward_need(const Shape &s, const dq4_weight_t *w0, const dq4_weight_t 
                      bool least)
 {
     const int64_t fixed = copy_bytes(s, copy);
-    switch (route_of(w0, w1, s.k, s.m)) {
+    switch (route_of(w0, w1, s, current_compute_units())) {
     case kProductRoute:
         return workspace_need(s, fixed, least);
     case kBatchRoute:
-        return ceil_div(s.m, 64) * ceil_div(s.k, 512) * 16 * x_row_frags(s.m) * kFragBytes;
+        return x_fragment_bytes(s.m, s.k);
+    case kTileRoute:
+        return x_fragment_bytes(s.m, s.k) +
+               tile_plan(s.m, s.n, s.k, w1 != nullptr, current_compute_units()).partial_bytes();
     default:
         return fixed;
     }
@@ -2479,7 +2814,7 @@ dq4_status_t launch_batch_rows(RowsArgs a, const uint16_t *x_frags, int cus, hip
     const void *kernel = a.log2_block >= 6 && a.n_in % 64 == 0
                              ? reinterpret_cast<const void *>(&batch_rows_kernel<OUT, kGated, TF, 2>)
                              : reinterpret_cast<const void *>(&batch_rows_kernel<OUT, kGated, TF, 4>);
-    return launch(kernel, a.row_blocks < cus ? a.row_blocks : cus, ceil_div(a.out.m, 64), 512, params, s);
+    return launch(kernel, a.row_blocks < cus ? a.row_blocks : cus, 1, 512, params, s);
 }
 
 template <int OUT, bool kGated>
@@ -2493,14 +2828,30 @@ dq4_status_t launch_batch(const RowsArgs &a, uint8_t *workspace, int cus, hipStr
     uint16_t *out = reinterpret_cast<uint16_t *>(workspace);
     void *params[] = {&x, &ld, &m, &k, &tf, &frags, &aligned, &out};
     const dq4_status_t st = launch(reinterpret_cast<const void *>(&x_fragments_zero_fill),
-                                   ceil_div(frags, kThreads / 64), ceil_div(m, 64), kThreads, params, s);
+                                   ceil_div(frags, kThreads / 64), ceil_div(m, 16 * tf), kThreads, params, s);
     if (st != DQ4_OK)
         return st;
     if (tf == 1)
         return launch_batch_rows<OUT, kGated, 1>(a, out, cus, s);
     if (tf == 2)
         return launch_batch_rows<OUT, kGated, 2>(a, out, cus, s);
-    return launch_batch_rows<OUT, kGated, 4>(a, out, cus, s);
+    if (tf == 4)
+        return launch_batch_rows<OUT, kGated, 4>(a, out, cus, s);
+    const TilePlan p = tile_plan(m, a.n_out, k, kGated, cus);
+    RowsArgs b = a;
+    b.row_blocks = static_cast<int32_t>(p.row_blocks);
+    b.out.splits = p.splits;
+    b.out.partial = reinterpret_cast<f32x4 *>(workspace + x_fragment_bytes(m, k));
+    void *tile_params[] = {&b, &out};
+    const dq4_status_t tiles = launch(a.log2_block >= 6 && a.n_in % 64 == 0
+                                          ? reinterpret_cast<const void *>(&tile_rows_kernel<OUT, kGated, 2>)
+                                          : reinterpret_cast<const void *>(&tile_rows_kernel<OUT, kGated, 4>),
+                                      p.row_blocks * p.splits, p.slices, 512, tile_params, s);
+    if (tiles != DQ4_OK || p.splits == 1)
+        return tiles;
+    void *reduce_params[] = {&b};
+    return launch(reinterpret_cast<const void *>(&tile_rows_reduce_kernel<OUT, kGated>), p.row_blocks * 16,
+                  p.slices, 256, reduce_params, s);
 }
 
 // Few rows of x, by one of the kernels that read the 4-bit weight itself.
@@ -2510,7 +2861,7 @@ dq4_status_t launch_few_rows(const RowsArgs &a, Route route, uint8_t *workspace,
 {
     if (route == kRaggedRoute)
         return launch_ragged<OUT, kGated>(a, cus, s);
-    if (route == kBatchRoute)
+    if (route == kBatchRoute || route == kTileRoute)
         return launch_batch<OUT, kGated>(a, workspace, cus, s);
     if (a.out.m == 1)
         return launch_token_rows<OUT, kGated, 1>(a, cus, s);
@@ -2617,7 +2968,7 @@ dq4_status_t run_product(const Shape &sh, const dq4_weight_t *w0, const dq4_weig
     p.m = sh.m;
     p.n = sh.n;
     if constexpr (kForward) {
-        const Route route = route_of(w0, w1, n_in, sh.m);
+        const Route route = route_of(w0, w1, sh, cus);
         if (route != kProductRoute) {
             if (beside.kind != kNothing) {
                 const dq4_status_t st = launch_fragments<OUT, true>(FragmentArgs{}, true, beside, cus, s);
@@ -2814,7 +3165,7 @@ int64_t dq4_linear_fused_workspace_bytes(const dq4_weight_t *w, int64_t n_out, i
     if (!w || !sizes_ok(n_out, n_in, m))
         return 0;
     const Shape s{m, n_out, n_in, kSingle};
-    return forward_need(s, w, nullptr, forward_copies(w, nullptr, x, ld_x, m, n_in), least != 0);
+    return forward_need(s, w, nullptr, forward_copies(s, w, nullptr, x, ld_x), least != 0);
 }
 
 int64_t dq4_gated_fused_workspace_bytes(const dq4_weight_t *gate, const dq4_weight_t *up,
@@ -2824,7 +3175,7 @@ int64_t dq4_gated_fused_workspace_bytes(const dq4_weight_t *gate, const dq4_weig
     if (!gate || !up || !sizes_ok(n_ff, n_in, m))
         return 0;
     const Shape s{m, n_ff, n_in, kSideBySide};
-    return forward_need(s, gate, up, forward_copies(gate, up, x, ld_x, m, n_in), least != 0);
+    return forward_need(s, gate, up, forward_copies(s, gate, up, x, ld_x), least != 0);
 }
 
 int64_t dq4_linear_fused_backward_workspace_bytes(const dq4_weight_t *w, int64_t n_out,
@@ -2865,7 +3216,7 @@ dq4_status_t dq4_linear_fused(const dq4_weight_t *w, int64_t n_out, int64_t n_in
         (pre && bad_ld(ld_pre, m, n_out)))
         return DQ4_EINVAL;
     const Shape sh{m, n_out, n_in, kSingle};
-    const bool copy = forward_copies(w, nullptr, x, ld_x, m, n_in);
+    const bool copy = forward_copies(sh, w, nullptr, x, ld_x);
     const int64_t fixed = copy_bytes(sh, copy);
     if (workspace_bytes < forward_need(sh, w, nullptr, copy, true) ||
         bad_workspace(workspace, workspace_bytes))
@@ -2919,7 +3270,7 @@ dq4_status_t dq4_gated_fused(const dq4_weight_t *gate, const dq4_weight_t *up, i
     if (bad_ld(ld_x, m, n_in) || bad_ld(ld_h, m, n_ff) || (gate_pre && bad_ld(ld_pre, m, n_ff)))
         return DQ4_EINVAL;
     const Shape sh{m, n_ff, n_in, kSideBySide};
-    const bool copy = forward_copies(gate, up, x, ld_x, m, n_in);
+    const bool copy = forward_copies(sh, gate, up, x, ld_x);
     const int64_t fixed = copy_bytes(sh, copy);
     if (workspace_bytes < forward_need(sh, gate, up, copy, true) ||
         bad_workspace(workspace, workspace_bytes))

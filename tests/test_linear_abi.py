@@ -112,8 +112,13 @@ def test_workspace_sizes(lib):
         assert f(*(None for _ in ws), 64, 64, 4, ONE, 64, 0) == 0
         least, most = f(*ws, 1000, 2048, 300, ONE, 2048, 1), f(*ws, 1000, 2048, 300, ONE, 2048, 0)
         assert 0 < least <= most
-        # a misaligned matrix takes a padded copy
-        assert f(*ws, 1000, 2048, 300, P(2), 2048, 0) >= most + 300 * 1000 * 2
+        # a misaligned matrix takes a padded copy; the forward calls that read
+        # the 4-bit weight once for 128 rows lay x out anew from any rows
+        most = f(*ws, 1000, 2048, 1100, ONE, 2048, 0)
+        assert f(*ws, 1000, 2048, 1100, P(2), 2048, 0) >= most + 1100 * 1000 * 2
+        most = f(*ws, 4096, 4096, 512, ONE, 4096, 0)
+        copy = 512 * 4096 * 2 if name.endswith("backward") else 0
+        assert f(*ws, 4096, 4096, 512, P(2), 4096, 0) == most + copy
     # one token: the weight is decoded in registers, unless its rows start off a dword
     assert lib.dq4_linear_fused_workspace_bytes(w, 1000, 2048, 1, ONE, 2048, 0) == 0
     assert lib.dq4_linear_fused_workspace_bytes(odd, 1000, 2048, 1, ONE, 2048, 1) > 0

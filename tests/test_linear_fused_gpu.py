@@ -3,6 +3,8 @@ against float64 references (bounds: linear_cases.py), and of what the calls
 promise about strides, workspaces, streams, graphs and untouched memory."""
 from __future__ import annotations
 
+import threading
+
 import numpy as np
 import pytest
 
@@ -65,6 +67,10 @@ SHAPES = [
     (1, 3000, 136, 64, "nf4"), (16, 33, 4104, 32, "fp4"), (33, 1025, 264, 4096, "nf4"), (64, 2050, 520, 64, "nf4"),
     # ... with rows of whole dwords only
     (3, 50, 2056, 32, "nf4"), (40, 4200, 168, 64, "nf4"), (20, 90, 1000, 4096, "fp4"),
+    # tiles of 128 rows: rows, weight rows and chunks past the last tile, splits
+    # that divide the chunks unevenly, more tiles than workgroups
+    (65, 300, 1056, 32, "nf4"), (129, 2000, 4128, 64, "fp4"), (600, 33, 544, 64, "nf4"),
+    (1024, 700, 2048, 4096, "nf4"), (385, 257, 6176, 256, "nf4"), (900, 20000, 64, 32, "nf4"),
 ]
 
 
@@ -216,7 +222,7 @@ def untouched(big, view_shape, left, fill):
 
 @pytest.mark.parametrize("left,right", [(0, 8), (1, 0), (8, 16), (3, 4)])
 @pytest.mark.parametrize("m,n_out,n_in", [(1, 264, 512), (5, 264, 512), (3, 264, 2080), (33, 264, 520),
-                                          (64, 264, 544), (130, 200, 1001)])
+                                          (64, 264, 544), (130, 200, 1001), (200, 264, 1056)])
 def test_strided_matrices(m, n_out, n_in, left, right):
     """Every matrix inside a larger buffer: NaN around the inputs, a mark around
     the outputs; the results equal the dense call's bit for bit."""
@@ -541,6 +547,45 @@ def test_on_another_stream():
         assert_bits_equal(bits_of(got), bits_of(want), "forward")
         for a, b in zip(got_back, back):
             assert_bits_equal(bits_of(a), bits_of(b), "backward")
+
+
+def test_two_threads_at_once():
+    """Calls from two threads, each on a stream of its own, do not share
+    anything: every result has the bits of the call alone."""
+    rng = np.random.Generator(np.random.PCG64(72))
+    _, w = make_weight(1024, 2048, seed=62)
+    _, up = make_weight(1024, 2048, seed=63)
+    sizes = dict(n_out=1024, n_in=2048, blocksize=64)
+    xs = [normal(rng, (m, 2048), "bf16") for m in (1, 40, 200, 1100)]
+
+    def calls(x):
+        h = dq4.dq4_gated_fused(w, up, 1024, 2048, 64, x)
+        y = dq4.dq4_linear_fused(**w, **sizes, x=x, bias=h[0].contiguous())
+        dx, _, db = dq4.dq4_linear_fused_backward(**w, **sizes, dy=y, bias_grad=True)
+        return h, y, dx, db
+    want = [calls(x) for x in xs]
+    torch.cuda.synchronize()
+    got, failed = [{}, {}], []
+
+    def run(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for rep in range(5):
+                    for j in (range(4) if i == 0 else reversed(range(4))):
+                        got[i][j] = calls(xs[j])
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:  # reported by the test's own thread
+            failed.append(e)
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
+    for i in range(2):
+        for j in range(4):
+            for a, b in zip(got[i][j], want[j]):
+                assert_bits_equal(bits_of(a), bits_of(b), f"thread {i}")
 
 
 def test_refusals():
