@@ -645,7 +645,10 @@ __device__ __forceinline__ void finish_wave(const ProductArgs &a, const f32x4 (&
 
 // Tile of 128 WN output columns x 16 TF WT rows; wave (wn, wt) takes group wn
 // of the tile and 16 TF rows.  Both operands go from HBM to LDS without
-// passing registers, double-buffered by chunks of 64 k.
+// passing registers, double-buffered by chunks of 64 k.  Bound by the waits at
+// each chunk's barrier, which two or three workgroups per CU cover in part:
+// 0.77 PFLOP/s with 128 x 128, 0.45 with 128 x 64 (large products; the sizes
+// that take them have too few tiles of 256 x 256 to fill the GPU).
 template <int OUT, bool kGated, int WN, int WT, int TF>
 __global__ __launch_bounds__(64 * WN * WT) void fragment_product_kernel(ProductArgs a)
 {
@@ -795,6 +798,9 @@ __global__ __launch_bounds__(64 * WN * WT) void fragment_product_kernel(ProductA
 // wave of a SIMD multiplies the other one loads.  Four buffers of one k-step
 // each: the step three ahead goes where step h - 1 lay, which both halves have
 // read by then, and it has four phases (about 2000 cycles) or more to arrive.
+// Bound by the matrix pipe at the clock it runs at under this load, and by the
+// last round of tiles: 22016 x 4096 columns by 4096 rows in 630 us, 1.17 PFLOP/s;
+// 57344 x 8192 by 512 rows, 448 tiles on 256 CUs, 453 us, 1.06.
 template <int OUT, bool kGated>
 __global__ __launch_bounds__(512) void fragment_product_wide_kernel(ProductArgs a)
 {
@@ -945,7 +951,8 @@ __global__ __launch_bounds__(512) void fragment_product_wide_kernel(ProductArgs 
 
 // The splits' sums of one wave's 128 columns x 16 rows, added in order, and
 // the epilogue.  Four waves share the 8 fragments, so that a wave has the
-// loads of 8 splits in flight: the kernel is short and its time is latency.
+// loads of 8 splits in flight: the kernel is short and its time is latency (3 to
+// 5 us for 16 MB of sums).
 template <int OUT, bool kGated, int WN, int WT, int TF>
 __global__ __launch_bounds__(256) void product_reduce_kernel(ProductArgs a, int32_t tiles)
 {
@@ -998,6 +1005,7 @@ struct RowsArgs {
     int64_t n_elems;            // n_out * n_in
     int32_t log2_block;
     int32_t row_blocks;
+    int32_t whole, rest;        // tiles: those over all of k, those in out.splits parts
     ProductArgs out;            // x and the epilogue's matrices
 };
 
@@ -1156,7 +1164,10 @@ __device__ __forceinline__ void finish_linear4(const ProductArgs &a, int64_t row
 // (gated: R / 2 of each weight, the same columns) at a time; its waves split
 // the chunks of 128 k, and the partial sums meet in LDS.  Workgroups walk the
 // row blocks; the next chunk's loads, also those of the next row block, are
-// issued before the current chunk is decoded.
+// issued before the current chunk is decoded.  Bound by the latency of a few
+// chunks and of the sums' meeting at small sizes (1000 x 2376 with 37 rows: 15
+// us), by the decode's vector instructions at large ones (4096 x 11000 with 64
+// rows: 58 us a call).
 template <int OUT, bool kGated, int R, int TF, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void ragged_rows_kernel(RowsArgs a)
 {
@@ -1345,7 +1356,7 @@ __global__ __launch_bounds__(64 * WAVES) void ragged_rows_kernel(RowsArgs a)
 // byte units change places in LDS, and every store is a whole fragment.  Each
 // scale is looked up once per 32 k.  Workgroups walk the (group, 256 k) items
 // with the next item's loads in flight.  Bound by memory: 0.5 B read, 2 B
-// written per element.
+// written per element; 2 x 28672 x 8192 in 226 us, 5.2 TB/s.
 constexpr int kDecodeWaves = 16;
 constexpr int kUnitLd = 1024 + 32;  // bytes between a wave's fragments in LDS: 8 neighbouring
                                     // lanes' writes then meet 8 different bank groups
@@ -1454,7 +1465,10 @@ __global__ __launch_bounds__(64 * kDecodeWaves) void weight_row_fragments_kernel
 // results are unused; the instruction is still cheaper than widening the
 // rounded weight for the vector unit (4 vector instructions per packed byte
 // against 10), and x stays in registers: a wave keeps one chunk of k and walks
-// rows.  The waves' partial sums meet in LDS, in a fixed order.
+// rows.  The waves' partial sums meet in LDS, in a fixed order.  Bound by the
+// reading of the weight where it is long (gated 28672 x 8192, one token: 242 MB
+// in 60 us, 4.07 TB/s), by the lookup tables' filling and the launch where it is
+// short (4096 x 4096: 7.6 us).
 struct TokenArgs {
     Weight w[2];
     int64_t n_in;
@@ -1756,6 +1770,10 @@ __device__ __forceinline__ void transpose_quads(uint32_t (&v)[4], bool odd, bool
 // chunk is multiplied; each x fragment is reloaded kAhead steps ahead.
 // S: blocks looked up per lane and 128 k (2: blocks of 64 k or more and n_in
 // % 64 == 0; else 4).
+// Bound by the lookups, the decode's vector instructions and the x loads, which
+// two waves per SIMD overlap in part: about 9 us until the tables are filled and
+// the last sums have met, then per 33.5 M weight elements 4.8 us with 16 rows
+// of x and 6.9 with 64 (gated 28672 x 8192: 80 and 119 us).
 template <int OUT, bool kGated, int TF, int S>
 __global__ __launch_bounds__(512) void batch_rows_kernel(RowsArgs a, const uint16_t *x_frags, int wk_waves)
 {
@@ -1975,12 +1993,15 @@ __global__ __launch_bounds__(512) void batch_rows_kernel(RowsArgs a, const uint1
 // of each weight), over all of k or one of `splits` parts of it.  The weight
 // comes as in batch_rows_kernel, but a wave walks all the tile's k for 32
 // weight rows of its own, so that the 8 waves share x's fragments: four steps
-// of them at a time go straight to LDS, double buffered.  Per step of 32 k a
-// wave looks up 2 packed dwords per lane, reads 8 x fragments and issues 16
-// matrix instructions; the LDS bounds it (about 880 cycles per step of the
-// workgroup, 370 of them lookups, against 512 of the matrix pipe).  Measured:
-// 0.5 us per step, a tile of 8192 k in 130 us; gated 28672 x 8192 with 512 rows
-// 542 us, 0.89 PFLOP/s, where decode and product take 676.
+// of them at a time go straight to LDS, double buffered.  Lookups run one or
+// two steps ahead, the next chunk's scales and transposition are done within
+// this chunk's last steps, and a wave that multiplies goes first.  Per step of
+// 32 k a wave looks up 2 packed dwords per lane, reads 8 x fragments and issues
+// 16 matrix instructions; what bounds it is the LDS (about 880 cycles per step
+// of the workgroup, 370 of them lookups, against 512 of the matrix pipe), of
+// which about 0.7 is reached: 0.5 us per step, a tile of 8192 k in 130 us; gated
+// 28672 x 8192 with 512 rows 524 us, 0.92 PFLOP/s, where decode and product
+// take 676.
 template <int OUT, bool kGated, int S>
 __global__ __launch_bounds__(512) void tile_rows_kernel(RowsArgs a, const uint16_t *x_frags)
 {
@@ -1988,25 +2009,34 @@ __global__ __launch_bounds__(512) void tile_rows_kernel(RowsArgs a, const uint16
     constexpr int kPer = R / kW;
     constexpr int kSpan = 512;
     constexpr int kStage = 4 * TF * kFragBytes;  // x's fragments of 4 steps: 32 KiB
+    constexpr int kLook = S == 2 ? 2 : 1;        // steps that the lookups run ahead: what the registers hold
     __shared__ __attribute__((aligned(1024))) uint8_t table[kPairTableBytes + 256];
     __shared__ float scb[kW][256], cb4[kW][16];
     __shared__ __attribute__((aligned(1024))) uint8_t stage[2 * kStage];
 
-    // slice blockIdx.y of 128 rows of x; the weight is read again for each
-    const int64_t x_row0 = static_cast<int64_t>(blockIdx.y) * (16 * TF);
-    x_frags += static_cast<int64_t>(blockIdx.y) * ((a.n_in + 511) / 512) * (16 * TF * 512);
+    // this workgroup's tile, and its part of k
+    int tile = blockIdx.x, split = 0, splits = 1;
+    if (tile >= a.whole) {
+        splits = a.out.splits;
+        const int at = (tile - a.whole) / splits;
+        split = tile - a.whole - at * splits;
+        tile = a.whole + at;
+    }
+    // 128 rows of x; the weight is read again for each such slice
+    const int slice = tile / a.row_blocks;
+    const int64_t rb = tile - slice * a.row_blocks;
+    const int64_t x_row0 = static_cast<int64_t>(slice) * (16 * TF);
+    x_frags += static_cast<int64_t>(slice) * ((a.n_in + 511) / 512) * (16 * TF * 512);
     const int tid = threadIdx.x;
     const int lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wr = wave;
     const int g = lane >> 4;
     constexpr int block_rows = 16 * kPer * 8;
-    const int split = blockIdx.x / a.row_blocks;
-    const int64_t rb = static_cast<int>(blockIdx.x) - split * a.row_blocks;
     const int lb = a.log2_block;
     const uint32_t n_in = static_cast<uint32_t>(a.n_in);
     const int chunks = static_cast<int>((n_in + kSpan - 1) / kSpan);
-    const int begin = split * chunks / a.out.splits, end = (split + 1) * chunks / a.out.splits;
+    const int begin = split * chunks / splits, end = (split + 1) * chunks / splits;
     const bool odd = lane & 1, high = lane & 2;
 
     struct Loads {
@@ -2087,39 +2117,47 @@ __global__ __launch_bounds__(512) void tile_rows_kernel(RowsArgs a, const uint16
 #pragma unroll
         for (int t = 0; t < TF; ++t)
             acc[f][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int c = begin; c < end; ++c) {
-        Loads next;
-        float s[R][S];
+    // a fragment's scales, and its packed dwords into operand order
+    auto prepare = [&](Loads &l, float (&s)[R][S], int f) {
 #pragma unroll
-        for (int f = 0; f < R; ++f) {
-#pragma unroll
-            for (int h = 0; h < S; ++h) {
-                const float q = block_scale(scb[kGated ? f : 0][cur.code[f][h]], cur.absmax[f][h],
-                                            a.w[kGated ? f : 0].offset);
-                // lane 16 g + r multiplies quarter g of row r
-                s[f][h] = __builtin_bit_cast(
-                    float, __builtin_amdgcn_ds_bpermute((4 * (lane & 15) + g) * 4, __builtin_bit_cast(int, q)));
-            }
-#pragma unroll
-            for (int d = 0; d < 4; ++d) {
-                uint32_t v[4] = {cur.packed[f][0][d], cur.packed[f][1][d], cur.packed[f][2][d],
-                                 cur.packed[f][3][d]};
-                transpose_quads(v, odd, high);
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    cur.packed[f][j][d] = v[j];
-            }
+        for (int h = 0; h < S; ++h) {
+            const float q = block_scale(scb[kGated ? f : 0][l.code[f][h]], l.absmax[f][h],
+                                        a.w[kGated ? f : 0].offset);
+            // lane 16 g + r multiplies quarter g of row r
+            s[f][h] = __builtin_bit_cast(
+                float, __builtin_amdgcn_ds_bpermute((4 * (lane & 15) + g) * 4, __builtin_bit_cast(int, q)));
         }
-        const uint32_t k = c * kSpan + 128 * g;
-        // a piece beyond the row (its load gave zeros) reads the row of
-        // zeros behind the table, times 0
-        const auto from = [&](int j) {
-            return k + 32 * j >= n_in ? lane_byte | kPairTableBytes : lane_byte;
-        };
-        Pairs now[R];
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+            uint32_t v[4] = {l.packed[f][0][d], l.packed[f][1][d], l.packed[f][2][d], l.packed[f][3][d]};
+            transpose_quads(v, odd, high);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                l.packed[f][j][d] = v[j];
+        }
+    };
+    // step st's lookups; a piece beyond the row (its load gave zeros) reads the
+    // row of zeros behind the table, and is multiplied with 0
+    const uint32_t k_lane = 128 * g;
+    auto lookup = [&](Pairs (&to)[R], const Loads &l, int c, int st) {
+        const uint32_t from =
+            c * kSpan + k_lane + 32 * (st / 4) >= n_in ? lane_byte | kPairTableBytes : lane_byte;
 #pragma unroll
         for (int f = 0; f < R; ++f)
-            now[f] = lookup_dword(cur.packed[f][0][0], table + (kGated ? f : 0) * 8, from(0));
+            to[f] = lookup_dword(l.packed[f][st / 4][st % 4], table + (kGated ? f : 0) * 8, from);
+    };
+    float s[R][S];
+#pragma unroll
+    for (int f = 0; f < R; ++f)
+        prepare(cur, s, f);
+    Pairs now[kLook][R];
+#pragma unroll
+    for (int i = 0; i < kLook; ++i)
+        lookup(now[i], cur, begin, i);
+    for (int c = begin; c < end; ++c) {
+        Loads next;
+        float s_next[R][S];
+        const uint32_t k = c * kSpan + k_lane;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int q = 4 * c + j;
@@ -2141,15 +2179,14 @@ __global__ __launch_bounds__(512) void tile_rows_kernel(RowsArgs a, const uint16
                 read_x(d, 1);
 #pragma unroll
                 for (int f = 0; f < R; ++f)
-                    wf[f] = scaled_dword<OUT>(now[f], k + 32 * j >= n_in ? 0.0f : s[f][j * S / 4]);
+                    wf[f] = scaled_dword<OUT>(now[st % kLook][f], k + 32 * j >= n_in ? 0.0f : s[f][j * S / 4]);
                 keep_order();
-                if (st < 15) {
-#pragma unroll
-                    for (int f = 0; f < R; ++f)
-                        now[f] = lookup_dword(cur.packed[f][(st + 1) / 4][(st + 1) % 4],
-                                              table + (kGated ? f : 0) * 8, from((st + 1) / 4));
-                }
+                if (st + kLook < 16)
+                    lookup(now[st % kLook], cur, c, st + kLook);
+                else
+                    lookup(now[st % kLook], next, c + 1, st + kLook - 16);
                 keep_order();
+                __builtin_amdgcn_s_setprio(1);
 #pragma unroll
                 for (int f = 0; f < R; ++f)
 #pragma unroll
@@ -2158,11 +2195,14 @@ __global__ __launch_bounds__(512) void tile_rows_kernel(RowsArgs a, const uint16
                 keep_order();
                 if (d < 3)
                     read_x(d + 1, 0);
+                if (j == 3 && d < R)  // the next chunk has arrived
+                    prepare(next, s_next, d);
 #pragma unroll
                 for (int f = 0; f < R; ++f)
 #pragma unroll
                     for (int t = 0; t < TF / 2; ++t)
                         acc[f][TF / 2 + t] = Half<OUT>::mfma(wf[f], x[1][t], acc[f][TF / 2 + t]);
+                __builtin_amdgcn_s_setprio(0);
                 keep_order();
             }
             // the next stage has arrived: behind its loads only the next
@@ -2175,11 +2215,15 @@ __global__ __launch_bounds__(512) void tile_rows_kernel(RowsArgs a, const uint16
             __asm__ volatile("" ::: "memory");
         }
         cur = next;
+#pragma unroll
+        for (int f = 0; f < R; ++f)
+#pragma unroll
+            for (int h = 0; h < S; ++h)
+                s[f][h] = s_next[f][h];
     }
-    if (a.out.splits > 1) {
+    if (splits > 1) {
         f32x4 *to = a.out.partial +
-                    (((static_cast<int64_t>(split) * gridDim.y + blockIdx.y) * a.row_blocks + rb) * 8 + wave) *
-                        (TF * R * 64) + lane;
+                    ((static_cast<int64_t>(split) * a.rest + tile - a.whole) * 8 + wave) * (TF * R * 64) + lane;
 #pragma unroll
         for (int t = 0; t < TF; ++t)
 #pragma unroll
@@ -2221,13 +2265,14 @@ __global__ __launch_bounds__(256) void tile_rows_reduce_kernel(RowsArgs a)
     constexpr int R = 2, TF = 8;
     const int lane = threadIdx.x & 63;
     const int t = blockIdx.x % 2 * 4 + (threadIdx.x >> 6);
-    const int64_t part = blockIdx.x / 2;  // wave of a row block
-    const int64_t row0 = (static_cast<int64_t>(blockIdx.y) * TF + t) * 16;
+    const int wave = blockIdx.x / 2 % 8, at = blockIdx.x / 16;
+    const int tile = a.whole + at;
+    const int slice = tile / a.row_blocks, rb = tile - slice * a.row_blocks;
+    const int64_t row0 = (static_cast<int64_t>(slice) * TF + t) * 16;
     if (row0 >= a.out.m)
         return;
-    const int64_t step = static_cast<int64_t>(gridDim.y) * a.row_blocks * (8 * TF * R * 64);
-    const f32x4 *from = a.out.partial +
-                        ((static_cast<int64_t>(blockIdx.y) * a.row_blocks * 8 + part) * TF + t) * (R * 64) + lane;
+    const int64_t step = static_cast<int64_t>(a.rest) * (8 * TF * R * 64);
+    const f32x4 *from = a.out.partial + ((static_cast<int64_t>(at) * 8 + wave) * TF + t) * (R * 64) + lane;
     f32x4 sum[R];
 #pragma unroll
     for (int f = 0; f < R; ++f)
@@ -2247,7 +2292,7 @@ __global__ __launch_bounds__(256) void tile_rows_reduce_kernel(RowsArgs a)
                     sum[f] = sum[f] + v[i][f];
     }
     const int64_t row = row0 + (lane & 15);
-    const int64_t n0 = part * (16 * (kGated ? 1 : R)) + (lane >> 4) * 4;
+    const int64_t n0 = (static_cast<int64_t>(rb) * 8 + wave) * (16 * (kGated ? 1 : R)) + (lane >> 4) * 4;
     if constexpr (kGated) {
         float g[4] = {sum[0][0], sum[0][1], sum[0][2], sum[0][3]};
         float u[4] = {sum[1][0], sum[1][1], sum[1][2], sum[1][3]};
@@ -2281,7 +2326,9 @@ struct ColumnArgs {
 // rows in turn, their sums meet in LDS, and those of the workgroups that share
 // a column group in the workspace (product_reduce_kernel), in a fixed order.
 // Bound by the lookups in LDS and the decode's vector instructions: W is read
-// once for 16 TF rows of dz and never written out.
+// once for 16 TF rows of dz and never written out.  Whole calls: linear 11008 x
+// 4096 with up to 16 rows 27 us, with 64 33; gated 28672 x 8192 with 64 rows 183,
+// where decode and product take 547.
 template <int OUT, bool kTwo, int TF>
 __global__ __launch_bounds__(512) void weight_columns_kernel(ColumnArgs a)
 {
@@ -2562,31 +2609,35 @@ int64_t workspace_need(const Shape &s, int64_t fixed, bool least)
     return fixed + s.window_bytes(s.plan(current_compute_units()), groups);
 }
 
-// How the tile route is cut: its 128 x 256 tiles, each over one of `splits`
-// parts of k where the tiles alone leave CUs idle.
+// How the tile route is cut: whole rounds of 128 x 256 tiles, one per CU, and
+// the tiles of the last round, each over one of `splits` parts of k where they
+// alone leave CUs idle (gated 28672 x 8192 with 512 rows: 3.5 rounds take the
+// time of 3.5, not of 4).
 struct TilePlan {
-    int64_t row_blocks, slices;
+    int64_t row_blocks, whole, rest;
     int splits;
     double cost;  // microseconds, roughly
-    int64_t partial_bytes() const { return splits == 1 ? 0 : splits * row_blocks * slices * (128 * 256 * 4); }
+    int64_t partial_bytes() const { return splits == 1 ? 0 : splits * rest * (128 * 256 * 4); }
 };
 
 TilePlan tile_plan(int64_t m, int64_t n_out, int64_t n_in, bool gated, int cus)
 {
-    TilePlan p{ceil_div(n_out, gated ? 128 : 256), ceil_div(m, 128), 1, 1e300};
-    const int64_t tiles = p.row_blocks * p.slices, chunks = ceil_div(n_in, 512);
+    const int64_t row_blocks = ceil_div(n_out, gated ? 128 : 256);
+    const int64_t tiles = row_blocks * ceil_div(m, 128), chunks = ceil_div(n_in, 512);
+    const int64_t whole = tiles / cus * cus, rest = tiles - whole;
+    // microseconds, as measured: 8 a chunk of 512 k, 9 until the tables are
+    // filled and the first loads have come; the partial sums, written and read
+    // at about 4 TB/s, and a launch
+    const double rounds = static_cast<double>(whole / cus) * (static_cast<double>(chunks) * 8.0 + 9.0);
+    TilePlan p{row_blocks, tiles, 0, 1, 1e300};
     for (int splits = 1; splits <= 16 && splits <= chunks; ++splits) {
-        // microseconds, as measured: 8 a chunk of 512 k, 9 until the tables
-        // are filled and the first loads have come; the partial sums, written
-        // and read at about 4 TB/s, and a launch
-        double cost = static_cast<double>(ceil_div(tiles * splits, cus)) *
-                      (static_cast<double>(ceil_div(chunks, splits)) * 8.0 + 9.0);
+        double cost = rounds + static_cast<double>(ceil_div(rest * splits, cus)) *
+                                   (static_cast<double>(ceil_div(chunks, splits)) * 8.0 + 9.0);
         if (splits > 1)
-            cost += 3.0 + static_cast<double>(tiles * splits) * (128 * 256 * 8.0 / 4e6);
-        if (cost < p.cost) {
-            p.cost = cost;
-            p.splits = splits;
-        }
+            cost += 3.0 + static_cast<double>(rest * splits) * (128 * 256 * 8.0 / 4e6);
+        if (cost < p.cost)
+            p = splits == 1 ? TilePlan{row_blocks, tiles, 0, 1, cost}
+                            : TilePlan{row_blocks, whole, rest, splits, cost};
     }
     return p;
 }
@@ -2604,12 +2655,14 @@ enum Route {
 //   token | batch: gated 28672 x 8192 at m = 2 75 | 80, at m = 4 97 | 80; gated
 //     11008 x 4096 at m = 2 19 | 23, at m = 4 24 | 23
 //   batch | tile, which costs the same for 1 to 128 rows: gated 28672 x 8192 at
-//     m = 64 119 | 151, two readings at m = 128 232 | 151; gated 11008 x 4096 at
-//     m = 64 33 | 48, at m = 128 63 | 49
-//   tile | product: the lesser of the two plans' costs, since both step with
-//     whole rounds of tiles: gated 28672 x 8192 at m = 512 542 | 676, at m =
-//     1024 994 | 1083 (beyond, the decode is a small part); linear 11008 x 4096
-//     at m = 512 77 | 80, at m = 700 141 | 110
+//     m = 64 119 | 147, two readings at m = 128 232 | 147; gated 11008 x 4096 at
+//     m = 64 33 | 48, at m = 128 63 | 48
+//   tile | product: the lesser of the two plans' costs: gated 28672 x 8192 at
+//     m = 512 524 | 676, at m = 1024 999 | 1083; gated 11008 x 4096 at m = 320
+//     90 | 152, at m = 768 165 | 235; linear 11008 x 4096 at m = 700 95 | 110.
+//     Beyond 1024 rows the decode is a small part, and they lie within 8 % of
+//     each other either way (gated 11008 x 4096 at m = 1280 267 | 246, at m =
+//     1536 310 | 340; linear 4096 x 11008 at m = 2048 216 | 206)
 //   ragged | product: FP16 4096 x 11000 at m = 64 58 | 73; more rows would
 //     read the weight twice
 constexpr int64_t kTokenMost = 2, kBatchMost = 64, kTileMost = 1024, kRaggedMost = 64;
@@ -2840,18 +2893,20 @@ dq4_status_t launch_batch(const RowsArgs &a, uint8_t *workspace, int cus, hipStr
     const TilePlan p = tile_plan(m, a.n_out, k, kGated, cus);
     RowsArgs b = a;
     b.row_blocks = static_cast<int32_t>(p.row_blocks);
+    b.whole = static_cast<int32_t>(p.whole);
+    b.rest = static_cast<int32_t>(p.rest);
     b.out.splits = p.splits;
     b.out.partial = reinterpret_cast<f32x4 *>(workspace + x_fragment_bytes(m, k));
     void *tile_params[] = {&b, &out};
     const dq4_status_t tiles = launch(a.log2_block >= 6 && a.n_in % 64 == 0
                                           ? reinterpret_cast<const void *>(&tile_rows_kernel<OUT, kGated, 2>)
                                           : reinterpret_cast<const void *>(&tile_rows_kernel<OUT, kGated, 4>),
-                                      p.row_blocks * p.splits, p.slices, 512, tile_params, s);
+                                      p.whole + p.rest * p.splits, 1, 512, tile_params, s);
     if (tiles != DQ4_OK || p.splits == 1)
         return tiles;
     void *reduce_params[] = {&b};
-    return launch(reinterpret_cast<const void *>(&tile_rows_reduce_kernel<OUT, kGated>), p.row_blocks * 16,
-                  p.slices, 256, reduce_params, s);
+    return launch(reinterpret_cast<const void *>(&tile_rows_reduce_kernel<OUT, kGated>), p.rest * 16,
+                  1, 256, reduce_params, s);
 }
 
 // Few rows of x, by one of the kernels that read the 4-bit weight itself.

@@ -171,7 +171,9 @@ def test_gated_backward(shape, dt):
 # inside a tile: references in float64 on the GPU
 @pytest.mark.parametrize("dt", ["bf16", "f16"])
 @pytest.mark.parametrize("m,n_out,n_in", [(2000, 8200, 520), (2048, 4096, 11008), (700, 4104, 8200),
-                                          (1030, 16500, 136), (520, 2050, 16424)])
+                                          (1030, 16500, 136), (520, 2050, 16424),
+                                          # a round of whole tiles and one of split tiles
+                                          (1000, 8200, 1056), (513, 28672, 1600)])
 def test_large_products(m, n_out, n_in, dt):
     print(f"large {m} {n_out} {n_in} {dt}", flush=True)
     rng = np.random.Generator(np.random.PCG64(m))
