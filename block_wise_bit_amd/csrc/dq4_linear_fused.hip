@@ -799,7 +799,7 @@ __global__ __launch_bounds__(64 * WN * WT) void fragment_product_kernel(ProductA
 // each: the step three ahead goes where step h - 1 lay, which both halves have
 // read by then, and it has four phases (about 2000 cycles) or more to arrive.
 // Bound by the matrix pipe at the clock it runs at under this load, and by the
-// last round of tiles: 22016 x 4096 columns by 4096 rows in 630 us, 1.17 PFLOP/s;
+// last round of tiles: 22016 x 4096 columns by 4096 rows in 638 us, 1.16 PFLOP/s;
 // 57344 x 8192 by 512 rows, 448 tiles on 256 CUs, 453 us, 1.06.
 template <int OUT, bool kGated>
 __global__ __launch_bounds__(512) void fragment_product_wide_kernel(ProductArgs a)
@@ -951,8 +951,8 @@ __global__ __launch_bounds__(512) void fragment_product_wide_kernel(ProductArgs 
 
 // The splits' sums of one wave's 128 columns x 16 rows, added in order, and
 // the epilogue.  Four waves share the 8 fragments, so that a wave has the
-// loads of 8 splits in flight: the kernel is short and its time is latency (3 to
-// 5 us for 16 MB of sums).
+// loads of 8 splits in flight: the kernel is short and its time is latency
+// (about 4 us for up to a few MB of sums).
 template <int OUT, bool kGated, int WN, int WT, int TF>
 __global__ __launch_bounds__(256) void product_reduce_kernel(ProductArgs a, int32_t tiles)
 {
@@ -1773,7 +1773,7 @@ __device__ __forceinline__ void transpose_quads(uint32_t (&v)[4], bool odd, bool
 // Bound by the lookups, the decode's vector instructions and the x loads, which
 // two waves per SIMD overlap in part: about 9 us until the tables are filled and
 // the last sums have met, then per 33.5 M weight elements 4.8 us with 16 rows
-// of x and 6.9 with 64 (gated 28672 x 8192: 80 and 119 us).
+// of x and 7 to 9 with 64 (gated 28672 x 8192: 80 and 135 us).
 template <int OUT, bool kGated, int TF, int S>
 __global__ __launch_bounds__(512) void batch_rows_kernel(RowsArgs a, const uint16_t *x_frags, int wk_waves)
 {
@@ -2655,8 +2655,8 @@ enum Route {
 //   token | batch: gated 28672 x 8192 at m = 2 75 | 80, at m = 4 97 | 80; gated
 //     11008 x 4096 at m = 2 19 | 23, at m = 4 24 | 23
 //   batch | tile, which costs the same for 1 to 128 rows: gated 28672 x 8192 at
-//     m = 64 119 | 147, two readings at m = 128 232 | 147; gated 11008 x 4096 at
-//     m = 64 33 | 48, at m = 128 63 | 48
+//     m = 64 135 | 150, two readings at m = 128 232 | 150; gated 11008 x 4096 at
+//     m = 64 34 | 48, at m = 128 63 | 48
 //   tile | product: the lesser of the two plans' costs: gated 28672 x 8192 at
 //     m = 512 524 | 676, at m = 1024 999 | 1083; gated 11008 x 4096 at m = 320
 //     90 | 152, at m = 768 165 | 235; linear 11008 x 4096 at m = 700 95 | 110.
