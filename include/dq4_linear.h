@@ -27,16 +27,17 @@
  * the m rows and their columns are read or written: what lies between the
  * rows of a strided matrix, and behind the last row, stays as it was.
  * No pointer but the workspace's has to be aligned beyond its element type;
- * 16-byte aligned rows and 4-byte aligned packed codes take the fastest paths.  `residual` may be `y` itself (same pointer and row
- * stride); no other output may overlap an input or another output.
+ * 16-byte aligned rows and 4-byte aligned packed codes take the fastest paths.
+ * `residual` may be `y` itself (same pointer and row stride); no other output
+ * may overlap an input or another output.
  *
  * workspace: caller-owned device memory, 256-byte aligned, of at least the
- * bytes that the call's *_workspace_bytes function returns with `least` = 1; with the bytes
- * of `least` = 0 the decoded weight of the large-m route fits whole, with
- * fewer it passes through in windows of output columns.  Its contents do not
- * matter before the call, and after it the workspace holds nothing of use.
- * Calls that may overlap in time must not share one.  A workspace changes
- * speed only, never results.
+ * bytes that the call's *_workspace_bytes function returns with `least` = 1;
+ * with the bytes of `least` = 0 a decoded weight fits whole, with fewer it
+ * passes through in windows of output columns.  Its contents do not matter
+ * before the call, and after it the workspace holds nothing of use.  Calls
+ * that may overlap in time must not share one.  A workspace changes speed
+ * only, never results.
  *
  * Ownership, ordering and errors are as in dq4.h: everything is enqueued on
  * `stream` and can be captured into a graph, nothing is allocated, kept or
