@@ -284,7 +284,8 @@ def test_strided_matrices(m, n_out, n_in, left, right):
     untouched(big_x, (m, n_in), left, mark)
 
 
-@pytest.mark.parametrize("m,n_out,n_in", [(3, 700, 515), (3, 768, 512), (20, 768, 512), (200, 768, 512)])
+@pytest.mark.parametrize("m,n_out,n_in", [(3, 700, 515), (3, 768, 512), (20, 768, 512), (200, 768, 512),
+                                          (200, 4096, 2048)])
 def test_any_workspace_gives_the_same_bits(m, n_out, n_in):
     """The least workspace (windows of output columns), one in between, and
     one full of NaN."""
@@ -494,11 +495,12 @@ def test_feed_forward_block(dt, m):
         assert (np.abs(got - diff) <= bound).all(), (got, diff, bound)
 
 
-def test_graph_replays_follow_new_inputs():
+@pytest.mark.parametrize("m,n_ff,n_in", [(40, 512, 256), (300, 4096, 2048)])
+def test_graph_replays_follow_new_inputs(m, n_ff, n_in):
     """The whole block, forward and backward, captured once and replayed four
     times with new inputs and eager work in between; two graphs share one
     stream and one set of buffers."""
-    n_ff, n_in, bs, m = 512, 256, 64, 40
+    bs = 64
     rng = np.random.Generator(np.random.PCG64(61))
     gate, up, down = (make_weight(*s, seed=k)[1] for s, k in (((n_ff, n_in), 51), ((n_ff, n_in), 52), ((n_in, n_ff), 53)))
     x, dy = normal(rng, (m, n_in), "bf16"), normal(rng, (m, n_in), "bf16")
