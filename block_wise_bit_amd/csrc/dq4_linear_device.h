@@ -118,10 +118,17 @@ constexpr float kGeluCubic = 0.044715f;
 constexpr float kInvSqrt2Pi = 0.39894228040143268f;
 
 // The tanh form's 2 v, v = sqrt(2/pi) (z + 0.044715 z^3), with z held to [-64,
-// 64]: the sigmoid is 0 or 1 long before that, and z^3 cannot overflow.
+// 64]: the sigmoid is 0 or 1 long before that, and z^3 cannot overflow.  A NaN
+// gives -64: what is computed from it has to take the NaN from z itself.
 __device__ __forceinline__ float gelu_clamp(float z)
 {
     return __builtin_amdgcn_fmed3f(z, -64.0f, 64.0f);
+}
+
+// z held to [-bound, bound]; a NaN stays.
+__device__ __forceinline__ float held(float z, float bound)
+{
+    return z != z ? z : __builtin_amdgcn_fmed3f(z, -bound, bound);
 }
 
 // act(z); z/2 (1 + tanh v) is z sigmoid(2 v).
@@ -143,30 +150,35 @@ __device__ __forceinline__ float act_f32(int act, float z)
     }
 }
 
-// act(z) and its derivative.
+// act(z) and its derivative, for a saved z: a NaN gives NaN, and the
+// infinities, which a 16-bit z reaches by overflow, give the limits (the
+// formulas alone give 0 times infinity there).  `c` is z with the infinities
+// held to the largest finite number, whose products with a vanished sigmoid or
+// density are 0; z itself is multiplied only where it is not negative infinity.
 __device__ __forceinline__ void act_and_slope_f32(int act, float z, float *value, float *slope)
 {
+    constexpr float kMax = 3.402823466e+38f;
     switch (act) {
     case DQ4_ACT_RELU:
         *value = z < 0.0f ? 0.0f : z;
-        *slope = z > 0.0f ? 1.0f : 0.0f;
+        *slope = z > 0.0f ? 1.0f : z != z ? z : 0.0f;
         return;
     case DQ4_ACT_SILU: {
-        const float s = sigmoid_f32(z);
-        *value = z * s;
-        *slope = s * (1.0f + z * (1.0f - s));
+        const float s = sigmoid_f32(z), c = held(z, kMax);
+        *value = (z > 0.0f ? z : c) * s;
+        *slope = s * (1.0f + c * (1.0f - s));
         return;
     }
     case DQ4_ACT_GELU: {
-        const float c = normal_cdf_f32(z);
-        *value = z * c;
-        *slope = c + z * (kInvSqrt2Pi * exp_f32(-0.5f * (z * z)));
+        const float p = normal_cdf_f32(z), c = held(z, kMax);
+        *value = (z > 0.0f ? z : c) * p;
+        *slope = p + c * (kInvSqrt2Pi * exp_f32(-0.5f * (z * z)));
         return;
     }
     case DQ4_ACT_GELU_TANH: {
-        const float c = gelu_clamp(z);
+        const float c = held(z, 64.0f);
         const float s = sigmoid_f32(kGeluTwoC * (c + kGeluCubic * (c * c * c)));
-        *value = z * s;
+        *value = (z > 0.0f ? z : c) * s;
         *slope = s + c * s * (1.0f - s) * (kGeluTwoC * (1.0f + 3.0f * kGeluCubic * (c * c)));
         return;
     }

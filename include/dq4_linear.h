@@ -21,6 +21,10 @@
  * act and act' are evaluated in FP32 on the FP32 pre-activation (forward) or
  * on the saved one (backward).  A low-rank (LoRA) term enters as `residual`
  * of a call without activation; its gradients take dz, dgate and dup.
+ * A NaN pre-activation gives NaN with every activation, forward and backward.
+ * At a saved pre-activation of plus or minus infinity, which FP16 reaches by
+ * overflow, the backward calls take act' as 1 or 0 and act as infinity or 0,
+ * their limits.
  *
  * Matrices are row-major with unit stride along a row and the row stride
  * (in elements) given as ld_*; a single row's stride is not looked at.  Only
