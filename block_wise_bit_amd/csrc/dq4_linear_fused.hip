@@ -2156,6 +2156,7 @@ __global__ __launch_bounds__(512) void tile_rows_kernel(RowsArgs a, const uint16
         lookup(now[i], cur, begin, i);
     for (int c = begin; c < end; ++c) {
         Loads next;
+        const int c_next = c + 1 < end ? c + 1 : c;  // at the end: the chunk again, unused
         float s_next[R][S];
         const uint32_t k = c * kSpan + k_lane;
 #pragma unroll
@@ -2171,7 +2172,7 @@ __global__ __launch_bounds__(512) void tile_rows_kernel(RowsArgs a, const uint16
             read_x(0, 0);
             issue_x(q + 1 < 4 * end ? q + 1 : q - 1);  // at the end: a stage nobody reads
             if (j == 1)
-                load(next, c + 1 < end ? c + 1 : c);
+                load(next, c_next);
 #pragma unroll
             for (int d = 0; d < 4; ++d) {
                 const int st = 4 * j + d;
@@ -2184,7 +2185,7 @@ __global__ __launch_bounds__(512) void tile_rows_kernel(RowsArgs a, const uint16
                 if (st + kLook < 16)
                     lookup(now[st % kLook], cur, c, st + kLook);
                 else
-                    lookup(now[st % kLook], next, c + 1, st + kLook - 16);
+                    lookup(now[st % kLook], next, c_next, st + kLook - 16);
                 keep_order();
                 __builtin_amdgcn_s_setprio(1);
 #pragma unroll
