@@ -260,9 +260,8 @@ def _check_inputs(packed, scale_codes, nested_absmax, scale_codebook, codebook4,
 
 
 def _prepare_out(out, count: int, dtype, device, stream=None):
-    torch = _torch()
     if out is None:
-        return _used_on(torch.empty(count, dtype=dtype, device=device), stream)
+        return _output(count, dtype, device, stream)
     if out.device != device or out.dtype != dtype or not out.is_contiguous():
         raise ValueError("out must be a contiguous tensor of the output dtype on the inputs' device")
     if out.numel() < count:
@@ -270,14 +269,33 @@ def _prepare_out(out, count: int, dtype, device, stream=None):
     return out
 
 
+def _scratch(shape, dtype, device, stream):
+    """A new tensor for kernels on `stream` (None: the current stream), from
+    that stream's own memory.  torch's caching allocator hands a freed block to
+    the next allocation of the stream that it was allocated for, whose order
+    covers the block's earlier uses; on the current stream's memory the kernels
+    of another stream could run before those uses have ended."""
+    torch = _torch()
+    if stream is None or stream == torch.cuda.current_stream(device):
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _output(shape, dtype, device, stream):
+    """As _scratch, for a tensor that the caller gets: marked as used on the
+    caller's current stream too."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    return _used_on(_scratch(shape, dtype, device, stream), torch.cuda.current_stream(device))
+
+
 def _used_on(t, stream):
-    """Tell torch's caching allocator that the kernels enqueued on `stream`
-    use t, a tensor this module allocated on the current stream: when t is
-    freed, its memory is not handed to a new allocation until that stream's
-    work queued so far has finished.  Without it a temporary freed on return
-    could be reused by work on the current stream while a kernel on another
-    stream still reads or writes it.  (Nothing to do for the current stream,
-    whose order already covers it.)"""
+    """Tell torch's caching allocator that work on `stream` uses t, a tensor of
+    another stream's memory: when t is freed, its memory is not handed out
+    again until that stream's work queued so far has finished.  (Nothing to do
+    on the stream that t was allocated for, whose order already covers it.)"""
     if stream is not None and t.numel() > 0:
         t.record_stream(stream)
     return t
@@ -296,7 +314,9 @@ def dq4_nested_dequant(packed, scale_codes, nested_absmax, scale_codebook, codeb
     """Dequantize the first n elements; returns `out` (allocated when None).
 
     Enqueued on `stream` (default: torch's current stream on the inputs'
-    device); asynchronous like any kernel launch.
+    device); asynchronous like any kernel launch.  Here and in every call
+    below, what the call allocates is `stream`'s own memory; that the inputs
+    are ready in its order, and live until its work is done, is the caller's.
     """
     torch = _torch()
     out_dtype = torch.float16 if out_dtype is None else out_dtype
@@ -378,8 +398,7 @@ def dq4_nested_dequant_unfused(packed, scale_codes, nested_absmax, scale_codeboo
     out = _prepare_out(out, max(int(n), 0), out_dtype, device, stream)
     need = dq4_unfused_workspace_bytes(int(n), int(blocksize)) // 4
     if scale_workspace is None:
-        scale_workspace = _used_on(torch.empty(max(need, 1), dtype=torch.float32,
-                                               device=device), stream)
+        scale_workspace = _scratch(max(need, 1), torch.float32, device, stream)
     elif (scale_workspace.device != device or scale_workspace.dtype != torch.float32
           or not scale_workspace.is_contiguous() or scale_workspace.numel() < need):
         raise ValueError(f"scale_workspace must be a contiguous float32 tensor of >= {need} "
@@ -436,7 +455,7 @@ def _out_prod_operands(torch, packed, scale_codes, nested_absmax, scale_codebook
     # leading dimension is then the row length
     ld = max(int(src1.stride(0)) if src1.size(0) > 1 else int(src1.size(1)), 1)
     if dst is None:
-        dst = _used_on(torch.empty((m, n_cols), dtype=torch.float32, device=device), stream)
+        dst = _output((m, n_cols), torch.float32, device, stream)
     elif (dst.device != device or dst.dtype != torch.float32 or not dst.is_contiguous()
           or dst.numel() < m * n_cols):
         raise ValueError("dst must be a contiguous float32 tensor of m * n_cols values")
@@ -471,8 +490,7 @@ def dq4_out_prod_rows(packed, scale_codes, nested_absmax, scale_codebook, codebo
         blocksize, nested_blocksize, src1, src1_transposed, dst, stream)
     if workspace is None:
         rows = max(1, min(n_rows, int(workspace_bytes) // max(4 * n_cols, 1)))
-        workspace = _used_on(torch.empty(max(rows * n_cols, 1), dtype=torch.float32,
-                                         device=device), stream)
+        workspace = _scratch(max(rows * n_cols, 1), torch.float32, device, stream)
     workspace = _f32_workspace(torch, workspace, device)
     with torch.cuda.device(device):
         st = library().dq4_out_prod_rows(
@@ -515,8 +533,7 @@ def dq4_out_prod_fused(packed, scale_codes, nested_absmax, scale_codebook, codeb
     if workspace is None:
         nbytes = dq4_out_prod_fused_workspace_bytes(n_rows, n_cols, m, device,
                                                     src1_transposed=src1_transposed)
-        workspace = _used_on(torch.empty(max(nbytes // 4, 0), dtype=torch.float32,
-                                         device=device), stream)
+        workspace = _scratch(max(nbytes // 4, 0), torch.float32, device, stream)
     workspace = _f32_workspace(torch, workspace, device)
     with torch.cuda.device(device):
         st = library().dq4_out_prod_fused(
@@ -554,12 +571,11 @@ def dq4_dequant_linear(packed, scale_codes, nested_absmax, scale_codebook, codeb
         raise ValueError(f"x must be a contiguous (m, {k}) tensor on the inputs' device")
     m = int(x.size(0))
     if y is None:
-        y = _used_on(torch.empty((m, width), dtype=x.dtype, device=device), stream)
+        y = _output((m, width), x.dtype, device, stream)
     elif y.device != device or y.dtype != x.dtype or not y.is_contiguous() or y.numel() < m * width:
         raise ValueError(f"y must be a contiguous {x.dtype} tensor of {m} x {width} values")
     if w_workspace is None:
-        w_workspace = _used_on(torch.empty(max(n_out * n_in, 1), dtype=x.dtype, device=device),
-                               stream)
+        w_workspace = _scratch(max(n_out * n_in, 1), x.dtype, device, stream)
     elif (w_workspace.device != device or w_workspace.dtype != x.dtype
           or not w_workspace.is_contiguous() or w_workspace.numel() < n_out * n_in):
         raise ValueError("w_workspace must hold n_out * n_in values of x's dtype")
@@ -609,7 +625,7 @@ def _launch(what: str, device, stream, workspace, sizes, *args) -> None:
     if workspace is None:
         nbytes, address = size(*sizes, 0), None
         if nbytes:
-            workspace = _used_on(torch.empty(nbytes, dtype=torch.uint8, device=device), stream)
+            workspace = _scratch(nbytes, torch.uint8, device, stream)
             address = workspace.data_ptr()
     else:
         if workspace.device != device or not workspace.is_contiguous():
@@ -780,7 +796,7 @@ def dq4_linear_fused(packed, scale_codes, nested_absmax, scale_codebook, codeboo
     ld_residual = 0 if residual is None else _matrix(residual, "residual", m, n_out, x.dtype, device)
     given = y is not None
     if not given:
-        y = _used_on(torch.empty((m, n_out), dtype=x.dtype, device=device), stream)
+        y = _output((m, n_out), x.dtype, device, stream)
     ld_y = _matrix(y, "y", m, n_out, x.dtype, device)
     ld_pre = 0 if pre is None else _matrix(pre, "pre", m, n_out, x.dtype, device)
     if given or pre is not None:
@@ -830,14 +846,14 @@ def dq4_linear_fused_backward(packed, scale_codes, nested_absmax, scale_codebook
             raise ValueError("an activation's gradient needs pre")
         ld_pre = _matrix(pre, "pre", m, n_out, dy.dtype, device)
         if dz is None:
-            dz = _used_on(torch.empty((m, n_out), dtype=dy.dtype, device=device), stream)
+            dz = _output((m, n_out), dy.dtype, device, stream)
         ld_dz = _matrix(dz, "dz", m, n_out, dy.dtype, device)
     if dx is None:
-        dx = _used_on(torch.empty((m, n_in), dtype=dy.dtype, device=device), stream)
+        dx = _output((m, n_in), dy.dtype, device, stream)
     ld_dx = _matrix(dx, "dx", m, n_in, dy.dtype, device)
     if dbias is None:
         if bias_grad:
-            dbias = _used_on(torch.empty((n_out,), dtype=torch.float32, device=device), stream)
+            dbias = _output((n_out,), torch.float32, device, stream)
     elif (dbias.dtype != torch.float32 or dbias.device != device or tuple(dbias.shape) != (n_out,)
           or (n_out > 1 and dbias.stride(0) != 1)):
         raise ValueError(f"dbias must be a contiguous ({n_out},) float32 tensor on {device}")
@@ -876,7 +892,7 @@ def dq4_gated_fused(gate, up, n_ff: int, n_in: int, blocksize: int, x,
         raise ValueError("give both gate_pre and up_pre, or neither")
     given = h is not None
     if not given:
-        h = _used_on(torch.empty((m, n_ff), dtype=x.dtype, device=device), stream)
+        h = _output((m, n_ff), x.dtype, device, stream)
     ld_h = _matrix(h, "h", m, n_ff, x.dtype, device)
     ld_pre = 0
     if gate_pre is not None:
@@ -917,12 +933,12 @@ def dq4_gated_fused_backward(gate, up, n_ff: int, n_in: int, blocksize: int, dh,
         raise ValueError("gate_pre and up_pre must have one row stride")
     given = dx is not None or dgate is not None or dup is not None
     if dx is None:
-        dx = _used_on(torch.empty((m, n_in), dtype=dh.dtype, device=device), stream)
+        dx = _output((m, n_in), dh.dtype, device, stream)
     ld_dx = _matrix(dx, "dx", m, n_in, dh.dtype, device)
     if dgate is None:
-        dgate = _used_on(torch.empty((m, n_ff), dtype=dh.dtype, device=device), stream)
+        dgate = _output((m, n_ff), dh.dtype, device, stream)
     if dup is None:
-        dup = _used_on(torch.empty((m, n_ff), dtype=dh.dtype, device=device), stream)
+        dup = _output((m, n_ff), dh.dtype, device, stream)
     ld_dpre = _matrix(dgate, "dgate", m, n_ff, dh.dtype, device)
     if _matrix(dup, "dup", m, n_ff, dh.dtype, device) != ld_dpre:
         raise ValueError("dgate and dup must have one row stride")
@@ -971,9 +987,9 @@ def dq4_int8_prep(A, CB, SCB, cols, subA=None, subB=None, stream=None, validate=
     if validate and L and bool(((cols < 0) | (cols >= K)).any()):
         raise ValueError(f"column indices must lie in [0, {K})")
     if subA is None:
-        subA = _used_on(torch.empty((M, L), dtype=torch.float16, device=device), stream)
+        subA = _output((M, L), torch.float16, device, stream)
     if subB is None:
-        subB = _used_on(torch.empty((L, N), dtype=torch.float16, device=device), stream)
+        subB = _output((L, N), torch.float16, device, stream)
     for name, t, numel in (("subA", subA, M * L), ("subB", subB, L * N)):
         if (t.device != device or t.dtype != torch.float16 or not t.is_contiguous()
                 or t.numel() < numel):
