@@ -2519,6 +2519,15 @@ bool needs_copy(const void *x, int64_t ld, int64_t m, int64_t k)
     return !rows_aligned(x, ld, m, k) || (m > 1 && ld > (int64_t{1} << 22));
 }
 
+// The row stride of a matrix that the product reads where it lies, at most 2^22
+// (needs_copy): a tile's 256 rows then end below byte 2^31, the offset that the
+// kernels give to what must not be read.  One row's stride, and that of rows
+// without columns, may be anything and is not used.
+int64_t product_ld(int64_t ld, int64_t m, int64_t k)
+{
+    return m > 1 && k > 0 ? ld : k;
+}
+
 int64_t padded_ld(int64_t k)
 {
     return ceil_div(k, kChunk) * kChunk;
@@ -3281,7 +3290,7 @@ dq4_status_t dq4_linear_fused(const dq4_weight_t *w, int64_t n_out, int64_t n_in
     hipStream_t s = static_cast<hipStream_t>(stream);
     ProductArgs p{};
     p.x[0] = p.x[1] = static_cast<const uint16_t *>(x);
-    p.ld_x = m > 1 ? ld_x : n_in;
+    p.ld_x = product_ld(ld_x, m, n_in);
     p.k = n_in;
     BesideWork beside{kNothing, {}};
     if (copy && n_in > 0) {
@@ -3335,7 +3344,7 @@ dq4_status_t dq4_gated_fused(const dq4_weight_t *gate, const dq4_weight_t *up, i
     hipStream_t s = static_cast<hipStream_t>(stream);
     ProductArgs p{};
     p.x[0] = p.x[1] = static_cast<const uint16_t *>(x);
-    p.ld_x = m > 1 ? ld_x : n_in;
+    p.ld_x = product_ld(ld_x, m, n_in);
     p.k = n_in;
     BesideWork beside{kNothing, {}};
     if (copy && n_in > 0) {
@@ -3402,7 +3411,7 @@ dq4_status_t dq4_linear_fused_backward(const dq4_weight_t *w, int64_t n_out, int
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     ProductArgs p{};
     p.x[0] = p.x[1] = static_cast<const uint16_t *>(lhs);
-    p.ld_x = m > 1 ? ld_lhs : n_out;
+    p.ld_x = product_ld(ld_lhs, m, n_out);
     p.k = n_out;
     BesideWork beside{kNothing, {}};
     const int64_t blocks = ceil_div(m, kRowBlock);
@@ -3496,7 +3505,7 @@ dq4_status_t dq4_gated_fused_backward(const dq4_weight_t *gate, const dq4_weight
     ProductArgs p{};
     p.x[0] = static_cast<const uint16_t *>(dgate);
     p.x[1] = static_cast<const uint16_t *>(dup);
-    p.ld_x = m > 1 ? ld_dpre : n_ff;
+    p.ld_x = product_ld(ld_dpre, m, n_ff);
     p.k = n_ff;
     BesideWork beside{kNothing, {}};
     if (n_ff > 0) {
