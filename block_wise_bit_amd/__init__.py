@@ -681,6 +681,13 @@ def _matrix(t, name: str, m: int, width: int, dtype, device) -> int:
     return row
 
 
+def _end(t, start: int) -> int:
+    """The address behind the last byte of a tensor that starts at `start`."""
+    if t.is_contiguous():
+        return start + t.nbytes
+    return start + (sum((n - 1) * s for n, s in zip(t.shape, t.stride())) + 1) * t.element_size()
+
+
 def _overlap(a, b) -> bool:
     """Whether two strided matrices share memory.  Column ranges of one row
     stride (the halves of an (m, 2 n) buffer) do not, though their rows
@@ -688,12 +695,7 @@ def _overlap(a, b) -> bool:
     if a is None or b is None or a.numel() == 0 or b.numel() == 0:
         return False
     a0, b0 = a.data_ptr(), b.data_ptr()
-
-    def span(t):
-        if t.is_contiguous():
-            return t.numel() * t.element_size()
-        return (sum((n - 1) * s for n, s in zip(t.shape, t.stride())) + 1) * t.element_size()
-    if a0 >= b0 + span(b) or b0 >= a0 + span(a):
+    if a0 >= _end(b, b0) or b0 >= _end(a, a0):
         return False
     if a.dim() == b.dim() == 2 and a.stride(0) == b.stride(0) and a.dtype == b.dtype:
         ld = a.stride(0) * a.element_size()
@@ -703,12 +705,47 @@ def _overlap(a, b) -> bool:
     return True
 
 
-def _refuse_overlap(outputs, inputs):
-    """No output may share memory with another output or with an input."""
-    for i, (name, t) in enumerate(outputs):
-        for other, u in outputs[i + 1:] + inputs:
-            if _overlap(t, u):
-                raise ValueError(f"{name} overlaps {other}")
+WEIGHT_PARTS = ("packed", "scale_codes", "nested_absmax", "scale_codebook", "codebook4")
+
+
+def _refuse_overlap(outputs, inputs, weights, n: int, workspace=None, given: bool = True):
+    """No output may share memory with another output, an input or a weight, and
+    the caller's workspace with none of them.  Outputs that the call allocated
+    (`given` False) lie apart from all that lives.  `weights`: the Dq4Weight of n
+    elements, or the gate's and the up weight's.  One reading of each address: a
+    call of one token waits for this."""
+    placed = []   # what may not lie over anything else: (name, tensor, first byte, behind the last)
+    if given:
+        for name, t in outputs:
+            start = 0 if t is None else t.data_ptr()
+            if start:
+                placed.append((name, t, start, _end(t, start)))
+    if workspace is not None and workspace.numel():
+        start = workspace.data_ptr()
+        placed.append(("workspace", workspace, start, _end(workspace, start)))
+    for i, (name, t, first, last) in enumerate(placed):
+        for other, u, start, end in placed[i + 1:]:
+            if first < end and start < last and _overlap(t, u):
+                # the workspace, placed last, is the one to name
+                raise ValueError(f"{other} overlaps {name}" if u is workspace else f"{name} overlaps {other}")
+    for other, u in inputs:
+        start = 0 if u is None else u.data_ptr()
+        if start:
+            end = _end(u, start)
+            for name, t, first, last in placed:
+                if first < end and start < last and _overlap(t, u):
+                    raise ValueError(f"{name} overlaps {other}")
+    for w in weights:
+        blocksize, nested = w.blocksize, w.nested_blocksize
+        if n <= 0 or blocksize <= 0 or nested <= 0:
+            return
+        blocks = -(-n // blocksize)
+        parts = ((w.packed, (n + 1) // 2), (w.scale_codes, blocks), (w.nested_absmax, 4 * -(-blocks // nested)),
+                 (w.scale_codebook, 1024), (w.codebook4, 64))
+        for name, _, first, last in placed:
+            for i, (start, size) in enumerate(parts):
+                if first < start + size and start < last:
+                    raise ValueError(f"{name} overlaps a weight's {WEIGHT_PARTS[i]}")
 
 
 def _address(t):
@@ -799,10 +836,12 @@ def dq4_linear_fused(packed, scale_codes, nested_absmax, scale_codebook, codeboo
         y = _output((m, n_out), x.dtype, device, stream)
     ld_y = _matrix(y, "y", m, n_out, x.dtype, device)
     ld_pre = 0 if pre is None else _matrix(pre, "pre", m, n_out, x.dtype, device)
-    if given or pre is not None:
+    given = given or pre is not None
+    if given or workspace is not None:
         in_place = residual is not None and residual.data_ptr() == y.data_ptr() and ld_residual == ld_y
         _refuse_overlap([("y", y), ("pre", pre)],
-                        [("x", x), ("bias", bias), ("residual", None if in_place else residual)])
+                        [("x", x), ("bias", bias), ("residual", None if in_place else residual)],
+                        (w,), n_out * n_in, workspace, given)
     address = x.data_ptr()
     sizes = (ctypes.byref(w), n_out, n_in, m, address, ld_x)
     _launch(
@@ -836,7 +875,7 @@ def dq4_linear_fused_backward(packed, scale_codes, nested_absmax, scale_codebook
     m = dy.size(0)
     ld_dy = _matrix(dy, "dy", m, n_out, dy.dtype, device)
     ld_pre = ld_dz = 0
-    given = [("dx", dx), ("dz", dz), ("dbias", dbias)]
+    given = dx is not None or dz is not None or dbias is not None
     if act == DQ4_ACT_NONE:
         if dz is not None:
             raise ValueError("dz is dy itself when there is no activation: do not give one")
@@ -857,8 +896,9 @@ def dq4_linear_fused_backward(packed, scale_codes, nested_absmax, scale_codebook
     elif (dbias.dtype != torch.float32 or dbias.device != device or tuple(dbias.shape) != (n_out,)
           or (n_out > 1 and dbias.stride(0) != 1)):
         raise ValueError(f"dbias must be a contiguous ({n_out},) float32 tensor on {device}")
-    if any(t is not None for _, t in given):
-        _refuse_overlap([("dx", dx), ("dz", dz), ("dbias", dbias)], [("dy", dy), ("pre", pre)])
+    if given or workspace is not None:
+        _refuse_overlap([("dx", dx), ("dz", dz), ("dbias", dbias)], [("dy", dy), ("pre", pre)],
+                        (w,), n_out * n_in, workspace, given)
     lhs, ld_lhs = (dy, ld_dy) if act == DQ4_ACT_NONE else (dz, ld_dz)
     sizes = (ctypes.byref(w), n_out, n_in, m, lhs.data_ptr(), ld_lhs)
     _launch(
@@ -899,8 +939,10 @@ def dq4_gated_fused(gate, up, n_ff: int, n_in: int, blocksize: int, x,
         ld_pre = _matrix(gate_pre, "gate_pre", m, n_ff, x.dtype, device)
         if _matrix(up_pre, "up_pre", m, n_ff, x.dtype, device) != ld_pre:
             raise ValueError("gate_pre and up_pre must have one row stride")
-    if given or gate_pre is not None:
-        _refuse_overlap([("h", h), ("gate_pre", gate_pre), ("up_pre", up_pre)], [("x", x)])
+    given = given or gate_pre is not None
+    if given or workspace is not None:
+        _refuse_overlap([("h", h), ("gate_pre", gate_pre), ("up_pre", up_pre)], [("x", x)],
+                        (wg, wu), n_ff * n_in, workspace, given)
     address = x.data_ptr()
     sizes = (ctypes.byref(wg), ctypes.byref(wu), n_ff, n_in, m, address, ld_x)
     _launch(
@@ -942,9 +984,10 @@ def dq4_gated_fused_backward(gate, up, n_ff: int, n_in: int, blocksize: int, dh,
     ld_dpre = _matrix(dgate, "dgate", m, n_ff, dh.dtype, device)
     if _matrix(dup, "dup", m, n_ff, dh.dtype, device) != ld_dpre:
         raise ValueError("dgate and dup must have one row stride")
-    if given:
+    if given or workspace is not None:
         _refuse_overlap([("dx", dx), ("dgate", dgate), ("dup", dup)],
-                        [("dh", dh), ("gate_pre", gate_pre), ("up_pre", up_pre)])
+                        [("dh", dh), ("gate_pre", gate_pre), ("up_pre", up_pre)],
+                        (wg, wu), n_ff * n_in, workspace, given)
     sizes = (ctypes.byref(wg), ctypes.byref(wu), n_ff, n_in, m, dgate.data_ptr(), dup.data_ptr(), ld_dpre)
     _launch(
         "dq4_gated_fused_backward", device, stream, workspace, sizes,

@@ -33,7 +33,8 @@
  * No pointer but the workspace's has to be aligned beyond its element type;
  * 16-byte aligned rows and 4-byte aligned packed codes take the fastest paths.
  * `residual` may be `y` itself (same pointer and row stride); no other output
- * may overlap an input or another output.
+ * may overlap an input, a weight or another output, and the workspace none of
+ * them.  (Nothing is refused for it here; the Python binding does.)
  *
  * workspace: caller-owned device memory, 256-byte aligned, of at least the
  * bytes that the call's *_workspace_bytes function returns with `least` = 1;
