@@ -304,8 +304,9 @@ enum Beside {
 };
 
 struct BesideArgs {
-    int32_t blocks;     // workgroups of this work, after those of the decode
-    int32_t columns;    // of them, along the columns
+    int32_t blocks;     // workgroups of this work, after those of the decode: one a piece
+    int32_t first;      // their first piece
+    int32_t columns;    // pieces along the columns
     CopyArgs copy;
     SlopeArgs slope;
 };
@@ -313,7 +314,8 @@ struct BesideArgs {
 template <int OUT, int kBeside>
 __device__ __forceinline__ void work_beside(const BesideArgs &b, int block)
 {
-    const int by = block / b.columns, bx = block - by * b.columns;
+    const int item = b.first + block;
+    const int by = item / b.columns, bx = item - by * b.columns;
     if constexpr (kBeside == kCopy) {
         copy_rows_zero_padded(b.copy, bx, by);
     } else if constexpr (kBeside >= kSlopes8) {
@@ -2501,7 +2503,8 @@ int64_t align256(int64_t b)
 dq4_status_t launch(const void *kernel, int64_t gx, int64_t gy, int threads, void **params,
                     hipStream_t s)
 {
-    if (gx > 0x7FFFFFFF || gy > 65535)
+    // a launch of 2^32 threads or more along x runs a part of them, without an error
+    if (gx * threads > 0xFFFFFFFF || gy > 65535)
         return DQ4_EUNSUPPORTED;
     const hipError_t e = hipLaunchKernel(kernel, dim3(static_cast<uint32_t>(gx), static_cast<uint32_t>(gy)),
                                          dim3(threads), params, 0, s);
@@ -2939,6 +2942,10 @@ struct BesideWork {
     BesideArgs args;
 };
 
+// More pieces than these (matrices of 2^33 elements in odd rows), 2^31 threads,
+// take launches of their own.
+constexpr int32_t kMostBeside = 1 << 23;
+
 BesideWork copy_work(const void *x, int64_t ld, int64_t m, int64_t k, void *out)
 {
     BesideWork w{kCopy, {}};
@@ -3005,12 +3012,21 @@ dq4_status_t launch_fragments(FragmentArgs a, bool aligned, BesideWork beside, i
         const int64_t pairs = ceil_div(items, 2);
         return launch(kernel, pairs < cus ? pairs : cus, 1, 64 * kDecodeWaves, params, s);
     }
-    const int64_t grid = (kForward ? a.groups * ceil_div(all_chunks, 4)
-                                   : ceil_div(a.groups, 2) * all_chunks) + beside.args.blocks;
+    const int64_t grid = kForward ? a.groups * ceil_div(all_chunks, 4) : ceil_div(a.groups, 2) * all_chunks;
+    const void *kernel = aligned ? fragments_kernel<OUT, kForward, true>(beside.kind)
+                                 : fragments_kernel<OUT, kForward, false>(beside.kind);
+    while (beside.args.blocks > kMostBeside) {
+        BesideArgs part = beside.args;
+        part.blocks = kMostBeside;
+        void *params[] = {&a, &part};  // no decode: the grid has this work's workgroups alone
+        const dq4_status_t st = launch(kernel, kMostBeside, 1, kThreads, params, s);
+        if (st != DQ4_OK)
+            return st;
+        beside.args.first += kMostBeside;
+        beside.args.blocks -= kMostBeside;
+    }
     void *params[] = {&a, &beside.args};
-    return launch(aligned ? fragments_kernel<OUT, kForward, true>(beside.kind)
-                          : fragments_kernel<OUT, kForward, false>(beside.kind),
-                  grid, 1, kThreads, params, s);
+    return launch(kernel, grid + beside.args.blocks, 1, kThreads, params, s);
 }
 
 Weight device_weight(const dq4_weight_t &w)
