@@ -74,7 +74,8 @@ struct Half<DQ4_BF16> {
 // ---------------------------------------------------------------------------
 // exp(x) as 2^(x log2 e): the rounding of x log2 e leaves a relative error of
 // about |x| 2^-24, at most 6e-6 where the result is a normal FP32 number, far
-// below the half step of FP16 or BF16 that the results are rounded to.
+// below the half step of FP16 or BF16 that the results are rounded to (the
+// bias gradient, in FP32, keeps it).
 __device__ __forceinline__ float exp_f32(float x)
 {
     return __builtin_amdgcn_exp2f(x * 1.44269504088896341f);
@@ -87,8 +88,10 @@ __device__ __forceinline__ float sigmoid_f32(float x)
 }
 
 // erfc(|x|): the Chebyshev fit t exp(-x^2 + P(t)), t = 1 / (1 + |x| / 2), of
-// Press, Teukolsky, Vetterling and Flannery, "Numerical Recipes" (erfcc):
-// relative error below 1.2e-7 everywhere, the far tail included.
+// Press, Teukolsky, Vetterling and Flannery, "Numerical Recipes" (erfcc).  The
+// fit's own relative error is below 1.2e-7; here the exponent, about x^2 in
+// size, is rounded three times, which adds up to 1.5 x^2 2^-23 (1.5e-5 at x =
+// 9), and results below 2^-126, from |x| = 9.2 on, are flushed to 0.
 __device__ __forceinline__ float erfc_abs_f32(float x)
 {
     const float z = __builtin_fabsf(x);

@@ -218,6 +218,13 @@ struct SlopeArgs {
 // aligned rows; else 1) and every eighth row; the column sums of the unrounded
 // products (the bias gradient) are FP32 additions in a fixed order: a thread's
 // rows, then the eight threads of a column.
+// The product that follows takes dz in T, as it is written here and as an
+// adapter's gradient takes it: the matrix instruction's operands are 16 bits
+// wide, and dz as a sum of two of them would double its work (gated 11008 x
+// 4096 with 2048 rows: 330 us of 425 once more).  The rounding of dz and that
+// of dx are of one size, so dx's error is sqrt 2 times that of a product of the
+// unrounded dz (relative to dx, root mean square: BF16 2.3e-3 against 1.7e-3,
+// FP16 2.9e-4 against 2.1e-4).
 template <int OUT, bool kGated, int N>
 __device__ __forceinline__ void activation_slopes(const SlopeArgs &a, int64_t bx, int64_t by,
                                                   float (&sums)[8][32 * N])
@@ -2673,9 +2680,12 @@ enum Route {
 //   tile | product: the lesser of the two plans' costs: gated 28672 x 8192 at
 //     m = 512 524 | 676, at m = 1024 999 | 1083; gated 11008 x 4096 at m = 320
 //     90 | 152, at m = 768 165 | 235; linear 11008 x 4096 at m = 700 95 | 110.
-//     Beyond 1024 rows the decode is a small part, and they lie within 8 % of
-//     each other either way (gated 11008 x 4096 at m = 1280 267 | 246, at m =
-//     1536 310 | 340; linear 4096 x 11008 at m = 2048 216 | 206)
+//     Beyond 1024 rows the decode is a small part, and the plans' costs are
+//     too rough to choose.  They would take the tiles each time (tile | product
+//     as planned, then as measured): gated 11008 x 4096 at m = 1280 275 | 280,
+//     267 | 246; linear 4096 x 11008 at m = 2048 185 | 218, 216 | 206; gated
+//     11008 x 4096 at m = 1536 316 | 396, 310 | 340.  The limit is 8 and 5 % the
+//     better for the first two, 10 % the worse for the third.
 //   ragged | product: FP16 4096 x 11000 at m = 64 58 | 73; more rows would
 //     read the weight twice
 constexpr int64_t kTokenMost = 2, kBatchMost = 64, kTileMost = 1024, kRaggedMost = 64;
@@ -2701,9 +2711,9 @@ Route route_of(const dq4_weight_t *w0, const dq4_weight_t *w1, const Shape &s, i
 // A backward call with few rows of dz whose weight rows are whole dwords
 // decodes in registers (weight_columns_kernel), once for 32 rows.  Against the
 // product over a decoded copy, in whole calls (BF16, us): linear 4096 x 4096 at
-// m = 128 29 | 39, gated 11008 x 4096 at m = 128 74 | 118; from m = 129 on a
-// fifth reading of the weight brings them level (gated 28672 x 8192 at m = 192
-// 570 | about 600, linear 11008 x 4096 at m = 192 69 | 60).
+// m = 128 29 | 39, gated 11008 x 4096 at m = 128 74 | 118.  With the fifth
+// reading of the weight, from m = 129 on, one gains what the other loses: at m =
+// 192 gated 28672 x 8192 570 | about 600, linear 11008 x 4096 69 | 60.
 constexpr int64_t kColumnsMost = 128;
 
 struct ColumnPlan {

@@ -7,6 +7,7 @@
  * elements enter the products as exactly the values dq4_nested_dequant writes
  * for the call's 16-bit type T (DQ4_F16 or DQ4_BF16), for every number of
  * rows m; products are summed in FP32 and every result is rounded to T once.
+ * The backward products take dz, dgate and dup as rounded to T.
  *
  *     linear            z = x W^T + bias
  *                       pre = T(z),  y = T(act(z) + residual)
