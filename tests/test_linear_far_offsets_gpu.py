@@ -146,3 +146,32 @@ def test_parts_of_a_weight_at_any_address(m, n_out, n_in, skew):
     dq4.dq4_gated_fused(*off, n_out, n_in, 64, x, gate_pre=pre[0], up_pre=pre[1])
     close(pre[0], x, wv, "f16", "gate")
     close(pre[1], x, weight_values(up, n_out, n_in, 64, "f16"), "f16", "up")
+
+
+@pytest.mark.parametrize("m,n_out,n_in", [(2, 264, 512), (20, 264, 520), (40, 264, 544), (65, 100, 8192), (300, 264, 512),
+                                          (300, 201, 65)])
+def test_row_strides_above_2_to_22(m, n_out, n_in):
+    """Rows 2^22 + 8 elements apart: the dense call's bits."""
+    ld = (1 << 22) + 8
+    w, up = make_weight(n_out, n_in, 64, 170), make_weight(n_out, n_in, 64, 171)
+    sizes = dict(n_out=n_out, n_in=n_in, blocksize=64)
+
+    def far(t):
+        view = torch.empty((t.size(0) - 1) * ld + t.size(1), dtype=t.dtype, device="cuda").as_strided(t.shape, (ld, 1))
+        view.copy_(t)
+        return view
+    x, res, pre = normal(26, (m, n_in), "bf16"), normal(27, (m, n_out), "bf16"), normal(28, (m, n_out), "bf16")
+    y = far(torch.zeros_like(res))
+    dq4.dq4_linear_fused(**w, **sizes, x=far(x), residual=far(res), y=y)
+    assert_bits_equal(bits_of(y.contiguous()), bits_of(dq4.dq4_linear_fused(**w, **sizes, x=x, residual=res)), "linear")
+    h = dq4.dq4_gated_fused(w, up, n_out, n_in, 64, far(x))
+    assert_bits_equal(bits_of(h), bits_of(dq4.dq4_gated_fused(w, up, n_out, n_in, 64, x)), "gated")
+    kw = dict(activation="gelu", bias_grad=True)
+    got = dq4.dq4_linear_fused_backward(**w, **sizes, dy=far(res), pre=far(pre), dx=far(torch.zeros_like(x)),
+                                        dz=far(torch.zeros_like(res)), **kw)
+    for a, b in zip(got, dq4.dq4_linear_fused_backward(**w, **sizes, dy=res, pre=pre, **kw)):
+        assert_bits_equal(bits_of(a.contiguous()), bits_of(b), "linear backward")
+    got = dq4.dq4_gated_fused_backward(w, up, n_out, n_in, 64, far(res), far(pre), far(pre), dgate=far(torch.zeros_like(res)),
+                                       dup=far(torch.zeros_like(res)))
+    for a, b in zip(got, dq4.dq4_gated_fused_backward(w, up, n_out, n_in, 64, res, pre, pre)):
+        assert_bits_equal(bits_of(a.contiguous()), bits_of(b), "gated backward")
