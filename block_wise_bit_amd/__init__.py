@@ -276,7 +276,7 @@ def _scratch(shape, dtype, device, stream):
     covers the block's earlier uses; on the current stream's memory the kernels
     of another stream could run before those uses have ended."""
     torch = _torch()
-    if stream is None or stream == torch.cuda.current_stream(device):
+    if stream is None or _own_stream(device, stream) == torch.cuda.current_stream(device):
         return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=device)
@@ -301,9 +301,17 @@ def _used_on(t, stream):
     return t
 
 
+def _own_stream(device, stream):
+    """`stream`, which has to be one of the tensors' device: the kernels would
+    run on its own."""
+    if stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+    return stream
+
+
 def _stream_handle(device, stream) -> ctypes.c_void_p:
     torch = _torch()
-    s = stream if stream is not None else torch.cuda.current_stream(device)
+    s = _own_stream(device, stream) if stream is not None else torch.cuda.current_stream(device)
     return ctypes.c_void_p(s.cuda_stream)
 
 
@@ -635,7 +643,7 @@ def _launch(what: str, device, stream, workspace, sizes, *args) -> None:
         if nbytes < least:
             raise ValueError(f"workspace holds {nbytes} bytes, needs {least}")
         address = workspace.data_ptr() if nbytes else None
-    handle = (stream.cuda_stream if stream is not None
+    handle = (_own_stream(device, stream).cuda_stream if stream is not None
               else torch._C._cuda_getCurrentRawStream(device.index))
     st = getattr(lib, what)(*args, address, nbytes, handle)
     if st != DQ4_OK:

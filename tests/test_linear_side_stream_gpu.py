@@ -168,3 +168,29 @@ def test_captured_on_a_forked_stream(name):
         torch.cuda.synchronize()
         for a, b in zip(got, want):
             assert torch.equal(a, b)
+
+
+class OtherDevice:
+    """A stream of a device that is not the tensors'."""
+    device = torch.device("cuda", 1)
+    cuda_stream = 0
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_a_stream_of_another_device_is_refused(name):
+    call = calls()[name]
+    assert torch.cuda.current_device() == 0
+    with pytest.raises(ValueError, match="stream is on cuda:1"):
+        call(stream=OtherDevice())
+    torch.cuda.synchronize()
+
+
+def test_a_stream_of_another_device_is_refused_with_everything_given():
+    w = make_weight(33)
+    x = torch.ones((1, N_IN), dtype=torch.bfloat16, device="cuda")
+    y = torch.empty((1, N_OUT), dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError, match="stream is on cuda:1"):
+        dq4.dq4_linear_fused(**w, n_out=N_OUT, n_in=N_IN, blocksize=64, x=x, y=y, stream=OtherDevice())
+    out = torch.empty(N_OUT * N_IN, dtype=torch.float16, device="cuda")
+    with pytest.raises(ValueError, match="stream is on cuda:1"):
+        dq4.dq4_nested_dequant(**w, n=N_OUT * N_IN, blocksize=64, out=out, stream=OtherDevice())
