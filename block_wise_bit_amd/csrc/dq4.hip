@@ -418,7 +418,6 @@ __global__ __launch_bounds__(kThreads) void dq4_memory_twin_kernel(const uint32_
 // ---------------------------------------------------------------------------
 namespace {
 constexpr int kMaxDevices = 64;
-constexpr int64_t kMaxGrid = 0x7FFFFFFF;
 std::atomic<int> g_cu_count[kMaxDevices];
 thread_local int32_t t_last_hip_error = 0;
 
@@ -526,7 +525,7 @@ dq4_status_t launch_typed(const Args &a, hipStream_t stream)
     if (vec) {
         int64_t n_full = a.count / kTileElems;
         int64_t n_tiles = (a.count + kTileElems - 1) / kTileElems;
-        const int64_t grid = n_tiles < kMaxGrid ? n_tiles : kMaxGrid;
+        const int64_t grid = n_tiles < kMaxGroups ? n_tiles : kMaxGroups;
         void *params[] = {&args, &n_full, &n_tiles};
         e = hipLaunchKernel(reinterpret_cast<const void *>(&dq4_tile_kernel<OUT>),
                             dim3(static_cast<uint32_t>(grid)), dim3(kThreads), params, 0, stream);
@@ -537,7 +536,7 @@ dq4_status_t launch_typed(const Args &a, hipStream_t stream)
         int64_t n_full = (a.count - head) / kTileElems;
         const bool edge = head > 0 || head + n_full * kTileElems < a.count;
         int64_t n_tiles = n_full + (edge ? 1 : 0);  // slot 0 takes head and tail
-        const int64_t grid = n_tiles < kMaxGrid ? n_tiles : kMaxGrid;
+        const int64_t grid = n_tiles < kMaxGroups ? n_tiles : kMaxGroups;
         void *params[] = {&args, &head, &n_full, &n_tiles};
         // the first full tile decides for all (tiles are 4096 elements apart):
         // whole units when each lies in one packed dword and one block, else
@@ -653,7 +652,7 @@ dq4_status_t dq4_memory_twin_f16(const uint8_t *packed, int64_t n, void *out, vo
         return DQ4_EINVAL;
     const uint32_t *words = reinterpret_cast<const uint32_t *>(packed);
     int64_t n_tiles = n / kTileElemsPublic;
-    if (n_tiles > 0x7FFFFFFF)
+    if (n_tiles > dq4::kMaxGroups)
         return DQ4_EUNSUPPORTED;
     void *o = out;
     void *params[] = {&words, &o, &n_tiles};

@@ -1417,7 +1417,8 @@ dq4_status_t dq4_out_prod_fused(const uint8_t *packed, const uint8_t *scale_code
             return DQ4_EINVAL;
         for (int k = 0; k < n_ranges; ++k) {
             const int64_t tiles_i = dq4::ceil_div(ranges[k].m, ranges[k].plan.tile_i);
-            if (tiles_i > 0x7FFFFFFF || tiles_j > 0x7FFFFFFF || tiles_i * tiles_j > 0x7FFFFFFF)
+            if (tiles_i > dq4::kMaxGroups || tiles_j > dq4::kMaxGroups ||
+                tiles_i * tiles_j > dq4::kMaxGroups)
                 return DQ4_EUNSUPPORTED;
         }
     }
@@ -1457,7 +1458,7 @@ dq4_status_t dq4_out_prod_fused(const uint8_t *packed, const uint8_t *scale_code
                                                   copied, &c0, &c1);
         const int64_t tiles_r = dq4::ceil_div(n_rows, dq4::kTrTile);
         const int64_t tiles_c = dq4::ceil_div(c1 - c0, dq4::kTrTile);
-        if (copy_bytes > 0 && tiles_r <= 0x7FFFFFFF && tiles_c <= 65535 &&
+        if (copy_bytes > 0 && tiles_r <= dq4::kMaxGroups && tiles_c <= 65535 &&
             workspace_bytes >= copy_bytes + dq4::partial_bytes(planned, n_ranges, n_rows,
                                                                n_cols, device)) {
             const float *in = src1 + c0 * ld_src1;
@@ -1512,7 +1513,7 @@ dq4_status_t dq4_out_prod_fused(const uint8_t *packed, const uint8_t *scale_code
         const int64_t splits = dq4::ceil_div(n_rows, rps);
         const int64_t groups = splits * tiles_i * tiles_j;
         // the kernels count a split's stages (16 rows) or steps (4 rows) in 32 bits
-        if (groups > 0x7FFFFFFF || dq4::ceil_div(rps, dq4::kDirectK) > 0x7FFFFFFF)
+        if (groups > dq4::kMaxGroups || dq4::ceil_div(rps, dq4::kDirectK) > 0x7FFFFFFF)
             return DQ4_EUNSUPPORTED;
         const bool full = plan.direct && dq4::direct_split_fits(rps, n_cols, r_ld[k],
                                                                  plan.tile_i, r_tr[k]);

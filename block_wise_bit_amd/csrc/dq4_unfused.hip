@@ -157,7 +157,7 @@ hipError_t launch_value(const uint8_t *packed, const float *scale, const float *
     if (vec) {
         int64_t n_full = n / kTileElems;
         int64_t n_tiles = (n + kTileElems - 1) / kTileElems;
-        const int64_t grid = n_tiles < 0x7FFFFFFF ? n_tiles : 0x7FFFFFFF;
+        const int64_t grid = n_tiles < kMaxGroups ? n_tiles : kMaxGroups;
         int lb = log2_block;
         void *params[] = {&packed, &scale, &codebook4, &out, &n, &lb, &n_full, &n_tiles};
         return hipLaunchKernel(reinterpret_cast<const void *>(&dq4_value_tile_kernel<OUT>),
@@ -187,7 +187,7 @@ dq4_status_t launch_unfused(const uint8_t *packed, const uint8_t *scale_codes,
 {
     int64_t n_blocks = ((n - 1) >> log2_block) + 1;
     const int64_t grid = (n_blocks + kThreads - 1) / kThreads;
-    if (grid > 0x7FFFFFFF)
+    if (grid > kMaxGroups)
         return DQ4_EINVAL;
     {
         void *params[] = {&scale_codes, &nested_absmax, &scale_codebook, &scale_workspace,

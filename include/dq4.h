@@ -293,7 +293,7 @@ dq4_status_t dq4_out_prod_rows(const uint8_t *packed, const uint8_t *scale_codes
  * no-op.  Everything is enqueued on `stream`; nothing is allocated or
  * synchronized.  Errors: DQ4_EINVAL for bad sizes, a leading dimension that
  * is too small, a null pointer, or workspace_bytes > 0 with a null
- * workspace; DQ4_EUNSUPPORTED for a tile grid of more than 2^31 - 1
+ * workspace; DQ4_EUNSUPPORTED for a tile grid of 2^24 or more
  * workgroups or a split of more than 4 * (2^31 - 1) rows; layout errors as
  * for dq4_nested_dequant.
  */
