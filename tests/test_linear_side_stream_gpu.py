@@ -95,7 +95,7 @@ def test_allocations_come_from_the_given_stream(name, monkeypatch):
 
 @pytest.mark.parametrize("name", ["linear", "gated", "linear backward"])
 def test_workspace_is_not_one_still_read_on_the_current_stream(name, monkeypatch):
-    """The reported pattern: a call on the current stream drops its workspace
+    """A call on the current stream drops its workspace
     while its kernels are queued; a call on another stream must not get it."""
     call = calls()[name]
     side = torch.cuda.Stream()
