@@ -1,7 +1,7 @@
 """MI355X (gfx950) nested block-wise 4-bit dequantization.
 
-Thin Python binding of the C ABI in include/dq4.h and include/dq4_linear.h
-(libdq4.so, built in-tree by block_wise_bit_amd/build.py).  The functions keep the C names; they only
+Thin Python binding of the C ABI in include/dq4.h, include/dq4_linear.h and
+include/dq4_int8.h (libdq4.so, built in-tree by block_wise_bit_amd/build.py).  The functions keep the C names; they only
 check and marshal arguments -- every step of the dequantization runs in the
 HIP kernels of the library.  torch provides device memory and the current
 stream, nothing else.  There is no fallback: if the library is missing or
@@ -33,12 +33,18 @@ cannot be loaded, every call raises.
     dq4_gated_fused_backward(gate, up, n_ff, n_in, blocksize, dh, gate_pre, up_pre)
                                                    -> (dx, dgate, dup)
     dq4_{linear,gated}_fused[_backward]_workspace_bytes(...) -> int
+    dq4_int8_quant(x, threshold) -> (codes, scales, outliers)   (tokens to 8-bit codes)
+    dq4_int8_linear(codes, scales, CB, SCB, bias, residual, x, outliers) -> tensor
+                                                   (the LLM.int8 linear layer)
+    dq4_int8_linear_backward(dy, CB, SCB, bias_grad) -> (dx, dbias)
+    dq4_int8_{quant,linear,linear_backward}_workspace_bytes(...) -> int
     dq4_int8_prep(A, CB, SCB, cols) -> (subA, subB)  (LLM.int8 correction operands)
     dq4_memory_twin_f16(packed, n) -> tensor       (diagnostic: the FP16 call's memory
                                                    traffic without its arithmetic)
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
@@ -48,6 +54,7 @@ PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 LIBRARY_PATH = os.path.join(PKG_DIR, "libdq4.so")
 HEADER_PATH = os.path.join(os.path.dirname(PKG_DIR), "include", "dq4.h")
 LINEAR_HEADER_PATH = os.path.join(os.path.dirname(PKG_DIR), "include", "dq4_linear.h")
+INT8_HEADER_PATH = os.path.join(os.path.dirname(PKG_DIR), "include", "dq4_int8.h")
 
 DQ4_OK, DQ4_EINVAL, DQ4_EUNSUPPORTED, DQ4_EHIP, DQ4_EBLAS, DQ4_ESCRATCH = 0, 1, 2, 3, 4, 5
 DQ4_NOALLOC_MAX_BLOCKS = 1 << 23   # outer blocks the no-allocation call's static scratch holds
@@ -136,6 +143,17 @@ def library() -> ctypes.CDLL:
     lib.dq4_gated_fused_backward_workspace_bytes.argtypes = [W, W, i64, i64, i64, P, P, i64, i32]
     for name in ("dq4_linear_fused", "dq4_linear_fused_backward", "dq4_gated_fused",
                  "dq4_gated_fused_backward"):
+        getattr(lib, name + "_workspace_bytes").restype = i64
+    lib.dq4_int8_quant.argtypes = [P, i64, i64, i64, i32, f32, P, i64, P, P, P, i64, P]
+    lib.dq4_int8_linear.argtypes = [P, i64, i64, P, P, P, i64, i64, i32, P, i64, P, P, P, i64, P,
+                                    i64, P, i64, P]
+    lib.dq4_int8_linear_backward.argtypes = [P, P, i64, i64, i32, P, i64, i64, P, i64, P, P, i64, P]
+    for name in ("dq4_int8_quant", "dq4_int8_linear", "dq4_int8_linear_backward"):
+        getattr(lib, name).restype = i32
+    lib.dq4_int8_quant_workspace_bytes.argtypes = [i64, i64, f32]
+    lib.dq4_int8_linear_workspace_bytes.argtypes = [P, i64, i64, P, i64, i64, i32]
+    lib.dq4_int8_linear_backward_workspace_bytes.argtypes = [i64, i64, i64, P, i64]
+    for name in ("dq4_int8_quant", "dq4_int8_linear", "dq4_int8_linear_backward"):
         getattr(lib, name + "_workspace_bytes").restype = i64
     lib.dq4_last_blas_status.argtypes = []
     lib.dq4_last_blas_status.restype = i32
@@ -1003,6 +1021,212 @@ def dq4_gated_fused_backward(gate, up, n_ff: int, n_in: int, blocksize: int, dh,
         gate_pre.data_ptr(), up_pre.data_ptr(), ld_pre, dx.data_ptr(), ld_dx, dgate.data_ptr(),
         dup.data_ptr(), ld_dpre)
     return dx, dgate, dup
+
+
+# ----------------------------------------------------------------------------
+# the LLM.int8 linear layer (include/dq4_int8.h)
+# ----------------------------------------------------------------------------
+def _launch_sized(what: str, device, stream, workspace, nbytes: int, *args) -> None:
+    """Call library function `what` on `device`, which is the current one: args,
+    then a workspace of nbytes (the caller's, or a new one), then the stream."""
+    torch = _torch()
+    address = None
+    if workspace is None:
+        if nbytes:
+            workspace = _scratch(nbytes, torch.uint8, device, stream)
+            address = workspace.data_ptr()
+    else:
+        if workspace.device != device or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {device}")
+        held = workspace.numel() * workspace.element_size()
+        if held < nbytes:
+            raise ValueError(f"workspace holds {held} bytes, needs {nbytes}")
+        nbytes = held
+        address = workspace.data_ptr() if nbytes else None
+    handle = (_own_stream(device, stream).cuda_stream if stream is not None
+              else torch._C._cuda_getCurrentRawStream(device.index))
+    st = getattr(library(), what)(*args, address, nbytes, handle)
+    if st != DQ4_OK:
+        _raise_for(st, what)
+
+
+def _on_device(device):
+    """A context in which `device` is the current one; none where it is already (a
+    single token's call takes the GPU about as long as Python)."""
+    torch = _torch()
+    return contextlib.nullcontext() if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+
+def _vector(t, name: str, n: int, dtype, device):
+    if t.dtype != dtype or t.device != device or t.shape != (n,) or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be a contiguous ({n},) {dtype} tensor on {device}")
+
+
+def _int8_weight(CB, SCB):
+    """(device, n_out, n_in) of a checked LLM.int8 weight."""
+    torch = _torch()
+    device = CB.device
+    if device.type != "cuda":
+        raise ValueError("CB must be a GPU tensor")
+    if CB.dtype != torch.int8 or CB.dim() != 2 or not CB.is_contiguous():
+        raise ValueError("CB must be a contiguous 2-D int8 tensor")
+    n_out, n_in = CB.shape
+    _vector(SCB, "SCB", n_out, torch.float32, device)
+    return device, n_out, n_in
+
+
+def dq4_int8_quant_workspace_bytes(m: int, n_in: int, threshold: float = 0.0) -> int:
+    return int(library().dq4_int8_quant_workspace_bytes(int(m), int(n_in), float(threshold)))
+
+
+def dq4_int8_linear_workspace_bytes(n_out: int, n_in: int, m: int, outliers: bool = False, codes=None,
+                                    CB=None) -> int:
+    """Workspace bytes of dq4_int8_linear for these codes and this weight (only
+    their alignment and the codes' row stride matter; None: aligned, dense)."""
+    address, ld = _query_matrix(codes, int(n_in))
+    return int(library().dq4_int8_linear_workspace_bytes(
+        address, int(m), ld, None if CB is None else CB.data_ptr(), int(n_out), int(n_in),
+        1 if outliers else 0))
+
+
+def dq4_int8_linear_backward_workspace_bytes(n_out: int, n_in: int, m: int, dy=None) -> int:
+    return int(library().dq4_int8_linear_backward_workspace_bytes(
+        int(n_out), int(n_in), int(m), *_query_matrix(dy, int(n_out))))
+
+
+def dq4_int8_quant(x, threshold: float = 0.0, codes=None, scales=None, outliers=None, workspace=None,
+                   stream=None):
+    """Rows of x (m, n_in), float16 or bfloat16, to 8-bit codes: (codes, scales,
+    outliers).
+
+    scales: the rows' largest magnitudes, float32; codes: round(127 x / scale),
+    half to even, int8.  threshold > 0 (LLM.int8's 6.0): the columns in which an
+    element's magnitude reaches it are outliers; their codes are 0, and what
+    reaches it is left out of the scales.  outliers: int32, 1 + n_in values:
+    the number of those columns, the columns in ascending order, then -1.  It
+    stays on the device, so that nothing waits for it and the call can be
+    captured into a graph.  threshold 0: outliers is None, and a row with an
+    infinity or a NaN gets scale NaN and codes 0."""
+    torch = _torch()
+    code = _half_code(x.dtype, "x")
+    device = x.device
+    if device.type != "cuda" or x.dim() != 2:
+        raise ValueError("x must be a 2-D GPU tensor")
+    threshold = float(threshold)
+    if not threshold >= 0.0:
+        raise ValueError("threshold must not be negative")
+    m, n_in = x.shape
+    ld_x = _matrix(x, "x", m, n_in, x.dtype, device)
+    given = codes is not None or scales is not None or outliers is not None
+    if codes is None:
+        codes = _output((m, n_in), torch.int8, device, stream)
+    ld_codes = _matrix(codes, "codes", m, n_in, torch.int8, device)
+    if scales is None:
+        scales = _output((m,), torch.float32, device, stream)
+    _vector(scales, "scales", m, torch.float32, device)
+    if threshold == 0.0:
+        if outliers is not None:
+            raise ValueError("without a threshold there are no outliers: do not give them")
+    else:
+        if outliers is None:
+            outliers = _output((1 + n_in,), torch.int32, device, stream)
+        _vector(outliers, "outliers", 1 + n_in, torch.int32, device)
+    if given or workspace is not None:
+        _refuse_overlap([("codes", codes), ("scales", scales), ("outliers", outliers)], [("x", x)], (), 0,
+                        workspace, given)
+    with _on_device(device):
+        _launch_sized("dq4_int8_quant", device, stream, workspace,
+                      library().dq4_int8_quant_workspace_bytes(m, n_in, threshold),
+                      x.data_ptr(), m, n_in, ld_x, code, threshold, codes.data_ptr(), ld_codes,
+                      scales.data_ptr(), None if outliers is None else outliers.data_ptr())
+    return codes, scales, outliers
+
+
+def dq4_int8_linear(codes, scales, CB, SCB, bias=None, residual=None, x=None, outliers=None, dtype=None,
+                    y=None, workspace=None, stream=None):
+    """y = (codes CB^T) * scales * SCB / 127^2 + bias + residual, and with
+    outliers + x[:, outliers] W[:, outliers]^T, W = CB SCB / 127 rounded to y's
+    type: the LLM.int8 linear layer.
+
+    codes (m, n_in) int8, scales (m,), outliers: what dq4_int8_quant returns for
+    x.  CB (n_out, n_in) int8 and SCB (n_out,) float32: the weight.  bias
+    (n_out,), residual (m, n_out) and x (m, n_in): of y's dtype, float16 or
+    bfloat16 (default: x's, residual's, bias's or y's; else float16).  The sum
+    over the codes is exact, y is rounded once.  x and outliers go together; of
+    x only the outlier columns are read.  y may be residual itself.  Returns y
+    (m, n_out)."""
+    torch = _torch()
+    device, n_out, n_in = _int8_weight(CB, SCB)
+    if dtype is None:
+        dtype = next((t.dtype for t in (x, residual, bias, y) if t is not None), torch.float16)
+    code = _half_code(dtype, "dtype")
+    if codes.dim() != 2:
+        raise ValueError("codes must be 2-D")
+    m = codes.size(0)
+    ld_codes = _matrix(codes, "codes", m, n_in, torch.int8, device)
+    _vector(scales, "scales", m, torch.float32, device)
+    if (x is None) != (outliers is None):
+        raise ValueError("give both x and outliers, or neither")
+    ld_x = 0
+    if outliers is not None:
+        ld_x = _matrix(x, "x", m, n_in, dtype, device)
+        _vector(outliers, "outliers", 1 + n_in, torch.int32, device)
+    if bias is not None:
+        _vector(bias, "bias", n_out, dtype, device)
+    ld_residual = 0 if residual is None else _matrix(residual, "residual", m, n_out, dtype, device)
+    given = y is not None
+    if not given:
+        y = _output((m, n_out), dtype, device, stream)
+    ld_y = _matrix(y, "y", m, n_out, dtype, device)
+    if given or workspace is not None:
+        in_place = residual is not None and residual.data_ptr() == y.data_ptr() and ld_residual == ld_y
+        _refuse_overlap([("y", y)],
+                        [("codes", codes), ("scales", scales), ("CB", CB), ("SCB", SCB), ("bias", bias), ("x", x),
+                         ("outliers", outliers), ("residual", None if in_place else residual)],
+                        (), 0, workspace, given)
+    codes_at, CB_at = codes.data_ptr(), CB.data_ptr()
+    with _on_device(device):
+        _launch_sized("dq4_int8_linear", device, stream, workspace,
+                      library().dq4_int8_linear_workspace_bytes(codes_at, m, ld_codes, CB_at, n_out, n_in,
+                                                                0 if outliers is None else 1),
+                      codes_at, m, ld_codes, scales.data_ptr(), CB_at, SCB.data_ptr(), n_out, n_in, code,
+                      _address(x), ld_x, None if outliers is None or n_in == 0 else outliers.data_ptr(),
+                      _address(bias), _address(residual), ld_residual, y.data_ptr(), ld_y)
+    return y
+
+
+def dq4_int8_linear_backward(dy, CB, SCB, bias_grad: bool = False, dx=None, dbias=None, workspace=None,
+                             stream=None):
+    """Gradients of the LLM.int8 linear layer: (dx, dbias).
+
+    dy: (m, n_out) float16 or bfloat16, the gradient of y (it is also
+    residual's).  dx = dy W, W = CB SCB / 127 rounded to dy's type.  dbias, with
+    bias_grad or a tensor given: the FP32 column sums of dy, else None.  The
+    weight is frozen: it has no gradient."""
+    torch = _torch()
+    device, n_out, n_in = _int8_weight(CB, SCB)
+    code = _half_code(dy.dtype, "dy")
+    if dy.dim() != 2:
+        raise ValueError("dy must be 2-D")
+    m = dy.size(0)
+    ld_dy = _matrix(dy, "dy", m, n_out, dy.dtype, device)
+    given = dx is not None or dbias is not None
+    if dx is None:
+        dx = _output((m, n_in), dy.dtype, device, stream)
+    ld_dx = _matrix(dx, "dx", m, n_in, dy.dtype, device)
+    if dbias is None and bias_grad:
+        dbias = _output((n_out,), torch.float32, device, stream)
+    if dbias is not None:
+        _vector(dbias, "dbias", n_out, torch.float32, device)
+    if given or workspace is not None:
+        _refuse_overlap([("dx", dx), ("dbias", dbias)], [("dy", dy), ("CB", CB), ("SCB", SCB)], (), 0, workspace,
+                        given)
+    with _on_device(device):
+        _launch_sized("dq4_int8_linear_backward", device, stream, workspace,
+                      library().dq4_int8_linear_backward_workspace_bytes(n_out, n_in, m, dy.data_ptr(), ld_dy),
+                      CB.data_ptr(), SCB.data_ptr(), n_out, n_in, code, dy.data_ptr(), m, ld_dy, dx.data_ptr(),
+                      ld_dx, _address(dbias))
+    return dx, dbias
 
 
 def dq4_int8_prep(A, CB, SCB, cols, subA=None, subB=None, stream=None, validate=False):

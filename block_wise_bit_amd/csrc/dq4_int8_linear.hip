@@ -1,0 +1,1268 @@
+// dq4_int8_linear.hip -- the LLM.int8 linear layer (include/dq4_int8.h): tokens
+// quantized to 8-bit codes, and the product of the codes with a scale for each
+// token and channel, the outlier columns in 16 bits.  (Its gradient is a product
+// over a 16-bit copy of the weight, in dq4_linear_fused.hip.)
+//
+// The sum of a product is one of 8-bit integers in 32 bits, exact in any order,
+// on v_mfma_i32_16x16x64_i8: D (16 x 16) += A (16 x 64) B (64 x 16).  Lane l
+// holds A[l % 16][16 (l / 16) .. + 15] and the same of B's columns, one 16-byte
+// register quad each, and D[4 (l / 16) + i][l % 16] for i = 0 .. 3.  A is the
+// weight (16 output columns), B the codes (16 tokens).
+//
+// LDS layout of such a fragment: 1 KiB, 16 rows of 64 bytes, the 16-byte piece p
+// of row r in slot 4 r + (p ^ (r / 4)).  A load takes 64 neighbouring bytes of a
+// row with a quad of lanes straight to LDS, lane l to slot l; of a wave's 16-byte
+// LDS reads the 16 lanes that are served together, one piece of all 16 rows, then
+// lie in 16 different slots of a 256-byte line: no bank conflicts.
+//
+// Up to 64 tokens: int8_rows_kernel, the weight read once.  More:
+// int8_product_kernel, tiles of both operands in LDS.
+
+#include <hip/hip_runtime.h>
+
+#include <stdint.h>
+
+#include "dq4.h"
+#include "dq4_device.h"
+#include "dq4_int8.h"
+#include "dq4_linear_device.h"
+
+#pragma clang fp contract(off)
+
+namespace dq4 {
+namespace {
+
+typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kFragBytes = 1024;
+constexpr int kStep = 64;                     // k per matrix instruction
+constexpr int kXcds = 8;
+constexpr int64_t kMaxDim = int64_t{1} << 21, kMaxMatrix = int64_t{1} << 38;
+// 128 * 128 * kMaxSum stays below 2^31.
+constexpr int64_t kMaxSum = (int64_t{1} << 17) - 1;
+constexpr float kR127 = 0x1.020408p-7f;       // the FP32 value nearest 1/127
+constexpr float kR16129 = 1.0f / 16129.0f;    // 1 / 127^2
+constexpr uint32_t kPast = 0x80000000u;       // an offset past every buffer
+
+// ---------------------------------------------------------------------------
+// quantization
+// ---------------------------------------------------------------------------
+struct QuantArgs {
+    const uint16_t *x;
+    int64_t m, k, ld_x;
+    uint32_t limit;       // the least 15-bit pattern of a magnitude at the threshold
+    uint32_t non_finite;  // T's infinity
+    int8_t *codes;
+    int64_t ld_codes;
+    float *scales;
+    int32_t *outliers;    // null: no threshold
+    uint8_t *flags;       // one byte a column, 0 before the rows are read
+    int32_t vec_in, vec_out;
+};
+
+// The code of x in a row of scale s: round(127 x / s), half to even.  x and s are
+// multiplied by `up`, a power of two that keeps what follows inside FP32's normal
+// range.  The quotient is at most 127 and its FP32 value within 3e-5, so only the
+// whole numbers next to it come into question, and the remainder 127 x - q s,
+// exact in FP32 (127 x has 18 bits, q s 19, and both are multiples of x's last
+// place where q is not 0), decides.
+__device__ __forceinline__ int code_of(float x, float up, float s, float inv)
+{
+    const float xs = x * up;
+    float q = __builtin_rintf(xs * inv);
+    const float r = 127.0f * xs - q * s;
+    const float twice = 2.0f * __builtin_fabsf(r);
+    const int odd = static_cast<int>(q) & 1;
+    const bool move = twice > s || (twice == s && odd);
+    q = q + (move ? __builtin_copysignf(1.0f, r) : 0.0f);
+    return static_cast<int>(q);
+}
+
+// Inclusive prefix sum over a wave.
+__device__ __forceinline__ int wave_prefix(int v, int lane)
+{
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const int other = __shfl_up(v, d);
+        v += lane >= d ? other : 0;
+    }
+    return v;
+}
+
+// The positions of `count` entries of each of the workgroup's threads in a list:
+// the number before this thread's, and all of them in *total.
+template <int THREADS>
+__device__ __forceinline__ int list_position(int count, int *total, int (&sums)[THREADS / 64])
+{
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int upto = wave_prefix(count, lane);
+    __syncthreads();  // sums may still be read
+    if (lane == 63)
+        sums[wave] = upto;
+    __syncthreads();
+    int before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 64; ++w) {
+        before += w < wave ? sums[w] : 0;
+        all += sums[w];
+    }
+    *total = all;
+    return before + upto - count;
+}
+
+// A row of x per workgroup and turn: its scale, then its codes.  A thread holds up
+// to kHeld pieces of 8 elements between the two, the rest is read again.  Bound by
+// memory: 2 bytes read and 1 written per element.
+// kOne: the only row, by one workgroup, which also makes the list of outliers.
+constexpr int kHeld = 4;
+
+template <int OUT, bool kOne>
+__global__ __launch_bounds__(kOne ? 1024 : 256) void int8_quant_rows_kernel(QuantArgs a)
+{
+    constexpr int THREADS = kOne ? 1024 : 256;
+    constexpr int kWords = kOne ? (kMaxSum + 31) / 32 : 1;
+    __shared__ uint32_t peaks[2][THREADS / 64];
+    __shared__ uint32_t flagged[kWords];
+    __shared__ int sums[THREADS / 64];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int k = static_cast<int>(a.k);
+    if constexpr (kOne) {
+        for (int i = tid; i < kWords; i += THREADS)
+            flagged[i] = 0;
+        __syncthreads();
+    }
+    int turn = 0;
+    for (int64_t row = blockIdx.x; row < a.m; row += gridDim.x, turn ^= 1) {
+        const uint16_t *x = a.x + row * a.ld_x;
+        auto load = [&](int c) {
+            u32x4 q = {0, 0, 0, 0};
+            if (a.vec_in) {
+                q = *reinterpret_cast<const u32x4 *>(x + c);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (c + j < k)
+                        q[j / 2] |= static_cast<uint32_t>(x[c + j]) << (16 * (j & 1));
+            }
+            return q;
+        };
+        uint32_t peak = 0;
+        auto look = [&](const u32x4 &q, int c) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t b = (q[j / 2] >> (16 * (j & 1))) & 0x7FFFu;
+                if (b >= a.limit) {  // not below the threshold (a NaN is not)
+                    if constexpr (kOne)
+                        atomicOr(&flagged[(c + j) >> 5], 1u << ((c + j) & 31));
+                    else
+                        a.flags[c + j] = 1;
+                } else {
+                    peak = b > peak ? b : peak;
+                }
+            }
+        };
+        u32x4 held[kHeld];
+#pragma unroll
+        for (int h = 0; h < kHeld; ++h) {
+            const int c = (h * THREADS + tid) * 8;
+            held[h] = u32x4{0, 0, 0, 0};
+            if (c < k)
+                held[h] = load(c);
+        }
+#pragma unroll
+        for (int h = 0; h < kHeld; ++h) {
+            const int c = (h * THREADS + tid) * 8;
+            if (c < k)
+                look(held[h], c);
+        }
+        for (int c = (kHeld * THREADS + tid) * 8; c < k; c += THREADS * 8)
+            look(load(c), c);
+#pragma unroll
+        for (int d = 32; d > 0; d /= 2) {
+            const uint32_t other = __shfl_xor(peak, d);
+            peak = other > peak ? other : peak;
+        }
+        if (lane == 0)
+            peaks[turn][wave] = peak;
+        __syncthreads();  // the next row's peaks go to the other half
+#pragma unroll
+        for (int w = 0; w < THREADS / 64; ++w)
+            peak = peaks[turn][w] > peak ? peaks[turn][w] : peak;
+        float scale = Half<OUT>::widen(peak);
+        if (peak >= a.non_finite)
+            scale = __builtin_nanf("");
+        if (tid == 0)
+            a.scales[row] = scale;
+        const bool none = peak == 0 || peak >= a.non_finite;
+        const float up = scale < 0x1p-100f ? 0x1p64f : scale > 0x1p100f ? 0x1p-64f : 1.0f;
+        const float s = scale * up;
+        const float inv = 127.0f * __builtin_amdgcn_rcpf(s);
+        int8_t *codes = a.codes + row * a.ld_codes;
+        auto write = [&](const u32x4 &q, int c) {
+            uint32_t out[2] = {0, 0};
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t b = (q[j / 2] >> (16 * (j & 1))) & 0xFFFFu;
+                const bool zero = none || (b & 0x7FFFu) >= a.limit;
+                const int code = zero ? 0 : code_of(Half<OUT>::widen(b), up, s, inv);
+                out[j / 4] |= (static_cast<uint32_t>(code) & 0xFFu) << (8 * (j & 3));
+            }
+            if (a.vec_out) {
+                *reinterpret_cast<u32x2 *>(codes + c) = u32x2{out[0], out[1]};
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (c + j < k)
+                        codes[c + j] = static_cast<int8_t>(out[j / 4] >> (8 * (j & 3)));
+            }
+        };
+#pragma unroll
+        for (int h = 0; h < kHeld; ++h) {
+            const int c = (h * THREADS + tid) * 8;
+            if (c < k)
+                write(held[h], c);
+        }
+        for (int c = (kHeld * THREADS + tid) * 8; c < k; c += THREADS * 8)
+            write(load(c), c);
+    }
+    if constexpr (kOne) {
+        if (!a.outliers)
+            return;
+        // (the flags are complete: every thread passed the row's barrier)
+        int count = 0;
+        uint32_t word[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            word[q] = 4 * tid + q < kWords ? flagged[4 * tid + q] : 0;
+            count += __builtin_popcount(word[q]);
+        }
+        int total;
+        int at = list_position<THREADS>(count, &total, sums);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            for (uint32_t w = word[q]; w; w &= w - 1)
+                a.outliers[1 + at++] = (4 * tid + q) * 32 + __builtin_ctz(w);
+        for (int i = total + tid; i < k; i += THREADS)
+            a.outliers[1 + i] = -1;
+        if (tid == 0)
+            a.outliers[0] = total;
+    }
+}
+
+__global__ __launch_bounds__(256) void int8_flags_zero_fill(uint32_t *flags, int32_t words)
+{
+    const int i = blockIdx.x * 256 + threadIdx.x;
+    if (i < words)
+        flags[i] = 0;
+}
+
+// The flagged columns: workgroup 0 lists them, the others set their codes to zero
+// in the rows blockIdx.x - 1, ... .
+constexpr int kListed = 4096;  // columns looked at in one go
+
+__global__ __launch_bounds__(1024) void int8_outliers_zero_fill(QuantArgs a)
+{
+    __shared__ int sums[16];
+    __shared__ int list[kListed];
+    const int tid = threadIdx.x;
+    const int k = static_cast<int>(a.k);
+    int before = 0;
+    for (int c0 = 0; c0 < k; c0 += kListed) {
+        // the flags behind column k - 1 are zero
+        const int c = c0 + 4 * tid;
+        const uint32_t word = c < k ? *reinterpret_cast<const uint32_t *>(a.flags + c) : 0;
+        int total;
+        int at = list_position<1024>(__builtin_popcount(word), &total, sums);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if ((word >> (8 * j)) & 1)
+                list[at++] = c + j;
+        __syncthreads();
+        if (blockIdx.x == 0) {
+            for (int i = tid; i < total; i += 1024)
+                a.outliers[1 + before + i] = list[i];
+        } else if (total > 0) {
+            // 32 threads a row
+            const int64_t step = gridDim.x - 1;
+            for (int64_t row = blockIdx.x - 1 + (tid >> 5) * step; row < a.m; row += 32 * step)
+                for (int i = tid & 31; i < total; i += 32)
+                    a.codes[row * a.ld_codes + list[i]] = 0;
+        }
+        before += total;
+        __syncthreads();
+    }
+    if (blockIdx.x == 0) {
+        for (int i = before + tid; i < k; i += 1024)
+            a.outliers[1 + i] = -1;
+        if (tid == 0)
+            a.outliers[0] = before;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// the product
+// ---------------------------------------------------------------------------
+struct Int8Args {
+    const int8_t *codes;
+    int64_t ld_codes;
+    const float *scales;
+    const int8_t *w;
+    int64_t ld_w;
+    const float *w_scales;
+    int64_t m, n;
+    int32_t k;                  // bytes of a row to read, zeros behind column n_in included
+    int32_t n_in;
+    const uint16_t *x;          // of the outlier columns
+    int64_t ld_x;
+    const int32_t *outliers;    // null: none
+    const uint16_t *w_outliers, *x_outliers;  // fragments of the first kOutlierChunks * 32 of them
+    const uint16_t *bias, *residual;
+    int64_t ld_residual;
+    uint16_t *y;
+    int64_t ld_y;
+    int32_t vec;                // bias, residual and y take whole vectors
+    int32_t row_blocks;
+    int32_t tiles_t;
+    int32_t splits;             // of the steps of k; above 1 the sums go to `partial`
+    i32x4 *partial;             // [split][tile][wave][fragment][16 tokens][lane]
+};
+
+__device__ __forceinline__ i32x4 mfma_i8(u32x4 a, u32x4 b, i32x4 c)
+{
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a),
+                                                 __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
+}
+
+// Byte of piece `g` of row `r` in a fragment in LDS.
+__device__ __forceinline__ uint32_t piece_at(int r, int g)
+{
+    return static_cast<uint32_t>(4 * r + (g ^ (r >> 2))) * 16;
+}
+
+// --- outlier columns ---------------------------------------------------------
+// They enter through the 16-bit matrix instruction, on the FP32 value of the
+// integer sum: 32 of them a chunk.  Their operands are gathered once per call
+// into fragments (int8_outlier_fragments_kernel) for the first 128 columns;
+// columns beyond are gathered where they are used, which is slow but needs no
+// memory: at a threshold of 6, models have a few dozen.
+constexpr int kOutlierChunks = 4;
+
+__device__ __forceinline__ int outlier_count(const Int8Args &a)
+{
+    if (!a.outliers)
+        return 0;
+    const int c = a.outliers[0];
+    return c < 0 ? 0 : c > a.n_in ? a.n_in : c;
+}
+
+template <int OUT>
+constexpr uint32_t kNan = OUT == DQ4_F16 ? 0x7E00u : 0x7FC0u;
+
+// W[n][c_l] for l = l0 .. l0 + 7, zeros past the last column and row.
+template <int OUT>
+__device__ __forceinline__ u32x4 gather_weight(const Int8Args &a, int64_t n, int l0, int count)
+{
+    u32x4 q = {0, 0, 0, 0};
+    if (n >= a.n)
+        return q;
+    const float s = a.w_scales[n];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        if (l0 + j >= count)
+            break;
+        const int c = a.outliers[1 + l0 + j];
+        uint32_t v = kNan<OUT>;
+        if (c >= 0 && c < a.n_in) {
+            const float scaled = static_cast<float>(a.w[n * a.ld_w + c]) * s;
+            v = Half<OUT>::pack2(scaled * kR127, 0.0f) & 0xFFFFu;
+        }
+        q[j / 2] |= v << (16 * (j & 1));
+    }
+    return q;
+}
+
+template <int OUT>
+__device__ __forceinline__ u32x4 gather_x(const Int8Args &a, int64_t t, int l0, int count)
+{
+    u32x4 q = {0, 0, 0, 0};
+    if (t >= a.m)
+        return q;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        if (l0 + j >= count)
+            break;
+        const int c = a.outliers[1 + l0 + j];
+        const uint32_t v = c >= 0 && c < a.n_in ? a.x[t * a.ld_x + c] : kNan<OUT>;
+        q[j / 2] |= v << (16 * (j & 1));
+    }
+    return q;
+}
+
+// Row (output column) of lane row r of weight fragment f: kWide as the product's
+// tiles take them, 8 r + f of 128; else 16 in a row.
+template <bool kWide>
+__device__ __forceinline__ int64_t fragment_row(int64_t f, int r)
+{
+    return kWide ? (f >> 3) * 128 + 8 * r + (f & 7) : f * 16 + r;
+}
+
+// A wave gathers one fragment of 16 rows: of the weight, or of x.
+template <int OUT, bool kWide>
+__global__ __launch_bounds__(256) void int8_outlier_fragments_kernel(Int8Args a, int64_t w_frags,
+                                                                     int64_t x_frags, uint16_t *out)
+{
+    const int lane = threadIdx.x & 63;
+    const int count = outlier_count(a);
+    for (int64_t f = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6); f < w_frags + x_frags;
+         f += static_cast<int64_t>(gridDim.x) * 4) {
+        for (int c = 0; c < kOutlierChunks && 32 * c < count; ++c) {
+            const int l0 = 32 * c + 8 * (lane >> 4);
+            const u32x4 q = f < w_frags
+                                ? gather_weight<OUT>(a, fragment_row<kWide>(f, lane & 15), l0, count)
+                                : gather_x<OUT>(a, (f - w_frags) * 16 + (lane & 15), l0, count);
+            *reinterpret_cast<u32x4 *>(out + ((f * kOutlierChunks + c) * 64 + lane) * 8) = q;
+        }
+    }
+}
+
+// Chunk c of weight fragment f, or of the x fragment t.
+template <int OUT, bool kWide>
+__device__ __forceinline__ u32x4 weight_outliers(const Int8Args &a, int64_t f, int c, int count, int lane)
+{
+    if (c < kOutlierChunks)
+        return *reinterpret_cast<const u32x4 *>(a.w_outliers + ((f * kOutlierChunks + c) * 64 + lane) * 8);
+    return gather_weight<OUT>(a, fragment_row<kWide>(f, lane & 15), 32 * c + 8 * (lane >> 4), count);
+}
+
+template <int OUT>
+__device__ __forceinline__ u32x4 x_outliers(const Int8Args &a, int64_t t, int c, int count, int lane)
+{
+    if (c < kOutlierChunks)
+        return *reinterpret_cast<const u32x4 *>(a.x_outliers + ((t * kOutlierChunks + c) * 64 + lane) * 8);
+    return gather_x<OUT>(a, t * 16 + (lane & 15), 32 * c + 8 * (lane >> 4), count);
+}
+
+// --- the epilogue --------------------------------------------------------------
+// The sum's value.  In this order no intermediate result leaves FP32's range where
+// the value itself does not: sum / 127^2 is at most k.
+__device__ __forceinline__ float scaled_sum(int sum, float w_scale, float scale)
+{
+    return static_cast<float>(sum) * kR16129 * w_scale * scale;
+}
+
+// Bias, residual and the rounding of N neighbouring outputs.
+template <int OUT, int N>
+__device__ __forceinline__ void finish(const Int8Args &a, int64_t row, int64_t n0, float (&z)[N])
+{
+    const int64_t left = a.n - n0;
+    if (row >= a.m || left <= 0)
+        return;
+    const int valid = left < N ? static_cast<int>(left) : N;
+    const bool vec = a.vec && valid == N;
+    float v[N];
+    if (a.bias) {
+        load_values<OUT, N>(a.bias + n0, vec, valid, v);
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            z[j] = z[j] + v[j];
+    }
+    if (a.residual) {
+        load_values<OUT, N>(a.residual + row * a.ld_residual + n0, vec, valid, v);
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            z[j] = z[j] + v[j];
+    }
+    store_values<OUT, N>(a.y + row * a.ld_y + n0, vec, valid, z);
+}
+
+// --- up to 64 tokens -------------------------------------------------------------
+// 16 TF tokens against row blocks of 16 R weight rows.  The 8 waves split k, steps
+// of 64 in turn; each has a ring of DEPTH steps of both operands in LDS that only
+// it fills and reads, so nothing but the meeting of the sums, integer additions in
+// LDS, needs a barrier, and the next row block's loads are under way across it.
+// Rows that are no multiple of 16 bytes, or not aligned so, take kAligned ==
+// false: dwords into registers, shifted to bytes, and no ring.
+template <int OUT, int TF, int R, int DEPTH, bool kAligned>
+__global__ __launch_bounds__(512) void int8_rows_kernel(Int8Args a)
+{
+    constexpr int kFrags = R + TF;
+    __shared__ __attribute__((aligned(1024))) uint8_t ring[kAligned ? 8 * DEPTH * kFrags * kFragBytes : 16];
+    __shared__ __attribute__((aligned(16))) int32_t sums[2][R * TF * 256];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int r = lane & 15, g = lane >> 4;
+    const int steps = (a.k + kStep - 1) / kStep;
+    const int mine = wave < steps ? (steps - wave + 7) / 8 : 0;
+    const int count = outlier_count(a);
+
+    // codes: one buffer; rows past the last one lie past it
+    const uint32_t x_bytes = static_cast<uint32_t>((a.m - 1) * a.ld_codes + a.k);
+    // a row block's weight, from its first row to the weight's end
+    const auto bytes_of = [&](int64_t rb) {
+        const int64_t left = (a.n - rb * (16 * R) - 1) * a.ld_w + a.k;
+        return static_cast<uint32_t>(left < 0x7FFFFFF0 ? left : 0x7FFFFFF0);
+    };
+
+    for (int i = tid; i < 2 * R * TF * 256; i += 512)
+        (&sums[0][0])[i] = 0;
+    __syncthreads();
+
+    // the loads run ahead of the products, by steps and then by row blocks
+    int64_t l_rb = blockIdx.x;
+    int l_i = 0;
+    [[maybe_unused]] u32x4 rs_w = {}, rs_x = {};
+    [[maybe_unused]] uint32_t w_off[R], x_off[TF];
+    [[maybe_unused]] const int piece = (lane & 3) ^ ((lane >> 4) & 3);
+    [[maybe_unused]] const uint32_t ring0 = lds_offset(ring) + wave * (DEPTH * kFrags * kFragBytes);
+    if constexpr (kAligned) {
+        rs_x = make_rsrc(a.codes, x_bytes);
+        rs_w = make_rsrc(a.w + l_rb * (16 * R) * a.ld_w, bytes_of(l_rb));
+#pragma unroll
+        for (int f = 0; f < R; ++f)
+            w_off[f] = static_cast<uint32_t>((16 * f + (lane >> 2)) * a.ld_w) + 16 * piece;
+#pragma unroll
+        for (int t = 0; t < TF; ++t) {
+            const int row = 16 * t + (lane >> 2);
+            x_off[t] = row < a.m ? static_cast<uint32_t>(row * a.ld_codes) + 16 * piece : kPast;
+        }
+    }
+    // always kFrags loads: past the last step they fetch zeros that nobody reads
+    auto issue = [&](int slot) {
+        const uint32_t k0 = static_cast<uint32_t>(wave + 8 * l_i) * kStep;
+        const bool in = l_rb < a.row_blocks && k0 + 16 * piece < static_cast<uint32_t>(a.k);
+        const uint32_t to = ring0 + slot * (kFrags * kFragBytes);
+#pragma unroll
+        for (int f = 0; f < R; ++f)
+            buffer_to_lds(rs_w, in ? w_off[f] + k0 : kPast, 0, to + f * kFragBytes);
+#pragma unroll
+        for (int t = 0; t < TF; ++t)
+            buffer_to_lds(rs_x, in ? x_off[t] + k0 : kPast, 0, to + (R + t) * kFragBytes);
+        if (++l_i == mine) {
+            l_i = 0;
+            l_rb += gridDim.x;
+            if (l_rb < a.row_blocks)
+                rs_w = make_rsrc(a.w + l_rb * (16 * R) * a.ld_w, bytes_of(l_rb));
+        }
+    };
+    // 16 bytes at any address: 5 dwords, those past the buffer are zeros
+    [[maybe_unused]] auto load_bytes = [&](__amdgpu_buffer_rsrc_t rsrc, uint32_t at, int left) {
+        const u32x4 lo = __builtin_amdgcn_raw_buffer_load_b128(rsrc, at & ~3u, 0, 0);
+        const uint32_t hi = __builtin_amdgcn_raw_buffer_load_b32(rsrc, (at & ~3u) + 16, 0, 0);
+        u32x4 q;
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+            const uint32_t v = __builtin_amdgcn_alignbyte(d < 3 ? lo[d + 1] : hi, lo[d], at & 3);
+            const int valid = left - 4 * d;  // bytes of the row
+            q[d] = valid >= 4 ? v : valid <= 0 ? 0u : v & ((1u << (8 * valid)) - 1);
+        }
+        return q;
+    };
+
+    int slot = 0, parity = 0;
+    if constexpr (kAligned) {
+        if (mine > 0)
+#pragma unroll
+            for (int d = 0; d < DEPTH; ++d)
+                issue(d);
+    }
+    for (int64_t rb = blockIdx.x; rb < a.row_blocks; rb += gridDim.x, parity ^= 1) {
+        i32x4 acc[R][TF];
+#pragma unroll
+        for (int f = 0; f < R; ++f)
+#pragma unroll
+            for (int t = 0; t < TF; ++t)
+                acc[f][t] = i32x4{0, 0, 0, 0};
+        if constexpr (kAligned) {
+            for (int i = 0; i < mine; ++i) {
+                __asm__ volatile("s_waitcnt vmcnt(%0)" ::"n"((DEPTH - 1) * kFrags) : "memory");
+                const uint8_t *from = ring + (wave * DEPTH + slot) * (kFrags * kFragBytes) + piece_at(r, g);
+                u32x4 q[kFrags];
+#pragma unroll
+                for (int f = 0; f < kFrags; ++f)
+                    q[f] = *reinterpret_cast<const u32x4 *>(from + f * kFragBytes);
+                // the slot is read: it may be filled again
+                __asm__ volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                __builtin_amdgcn_sched_barrier(0);
+                issue(slot);
+                slot = slot + 1 == DEPTH ? 0 : slot + 1;
+#pragma unroll
+                for (int f = 0; f < R; ++f)
+#pragma unroll
+                    for (int t = 0; t < TF; ++t)
+                        acc[f][t] = mfma_i8(q[f], q[R + t], acc[f][t]);
+            }
+        } else {
+            const uintptr_t w_at = reinterpret_cast<uintptr_t>(a.w + rb * (16 * R) * a.ld_w);
+            const uintptr_t x_at = reinterpret_cast<uintptr_t>(a.codes);
+            const uint32_t w_skew = w_at & 3, x_skew = x_at & 3;
+            // whole dwords, up to the one with the last byte
+            const auto rw = __builtin_amdgcn_make_buffer_rsrc(
+                reinterpret_cast<void *>(w_at - w_skew), 0, (bytes_of(rb) + w_skew + 3) & ~3u, kRawBufferWord3);
+            const auto rx = __builtin_amdgcn_make_buffer_rsrc(
+                reinterpret_cast<void *>(x_at - x_skew), 0, (x_bytes + x_skew + 3) & ~3u, kRawBufferWord3);
+            const int64_t rows_left = a.n - rb * (16 * R);
+            auto load = [&](u32x4 (&q)[kFrags], int i) {
+                const int k0 = (wave + 8 * i) * kStep + 16 * g;
+                const int left = i < mine ? a.k - k0 : 0;  // bytes of the row from here on
+#pragma unroll
+                for (int f = 0; f < R; ++f) {
+                    const int row = 16 * f + r;
+                    q[f] = load_bytes(rw, left > 0 && row < rows_left
+                                              ? static_cast<uint32_t>(row * a.ld_w) + k0 + w_skew : kPast, left);
+                }
+#pragma unroll
+                for (int t = 0; t < TF; ++t) {
+                    const int row = 16 * t + r;
+                    q[R + t] = load_bytes(rx, left > 0 && row < a.m
+                                                  ? static_cast<uint32_t>(row * a.ld_codes) + k0 + x_skew : kPast, left);
+                }
+            };
+            u32x4 now[kFrags], next[kFrags];
+            load(now, 0);
+            for (int i = 0; i < mine; ++i) {
+                load(next, i + 1);
+#pragma unroll
+                for (int f = 0; f < R; ++f)
+#pragma unroll
+                    for (int t = 0; t < TF; ++t)
+                        acc[f][t] = mfma_i8(now[f], now[R + t], acc[f][t]);
+#pragma unroll
+                for (int f = 0; f < kFrags; ++f)
+                    now[f] = next[f];
+            }
+        }
+        int32_t *sum = sums[parity];
+        if (mine > 0) {
+#pragma unroll
+            for (int f = 0; f < R; ++f)
+#pragma unroll
+                for (int t = 0; t < TF; ++t)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        atomicAdd(&sum[(f * TF + t) * 256 + r * 16 + 4 * g + i], acc[f][t][i]);
+        }
+        lds_barrier();
+        // a wave each finishes 16 rows x 16 tokens, and clears their sums for the
+        // row block after the next
+#pragma unroll
+        for (int p0 = 0; p0 < R * TF; p0 += 8) {
+            const int p = p0 + wave;
+            if (p >= R * TF)
+                break;
+            const int f = p / TF, t = p - f * TF;
+            i32x4 *at = reinterpret_cast<i32x4 *>(&sum[p * 256 + r * 16 + 4 * g]);
+            const i32x4 q = *at;
+            *at = i32x4{0, 0, 0, 0};
+            const int64_t n0 = rb * (16 * R) + f * 16 + 4 * g, row = t * 16 + r;
+            const float scale = row < a.m ? a.scales[row] : 0.0f;
+            f32x4 z;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                z[i] = scaled_sum(q[i], n0 + i < a.n ? a.w_scales[n0 + i] : 0.0f, scale);
+            for (int c = 0; 32 * c < count; ++c)
+                z = Half<OUT>::mfma(weight_outliers<OUT, false>(a, rb * R + f, c, count, lane),
+                                    x_outliers<OUT>(a, t, c, count, lane), z);
+            float out[4] = {z[0], z[1], z[2], z[3]};
+            finish<OUT, 4>(a, row, n0, out);
+        }
+    }
+}
+
+// --- more tokens ------------------------------------------------------------------
+constexpr int kGroup = 128, kGroupFrags = 8;
+constexpr int kFinishLd = kGroup + 4;  // floats per row of a wave's epilogue slab
+
+// 16 tokens x 128 columns of sums to outputs, through a slab of LDS that only this
+// wave uses: a lane holds 8 neighbouring columns of one token per D register, so
+// the slab takes and gives whole vectors.
+template <int OUT>
+__device__ __forceinline__ void finish_slab_rows(const Int8Args &a, const float *slab, int64_t row0,
+                                                 int64_t group, int it, int lane)
+{
+    const int g = lane >> 4, c = lane & 15;
+    const float *from = slab + (it * 4 + g) * kFinishLd + 8 * c;
+    const f32x4 lo = *reinterpret_cast<const f32x4 *>(from);
+    const f32x4 hi = *reinterpret_cast<const f32x4 *>(from + 4);
+    float z[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+    finish<OUT, 8>(a, row0 + it * 4 + g, group * kGroup + 8 * c, z);
+}
+
+// FP32 values of fragments F0 .. F0 + N - 1 of a group and 16 tokens, outliers
+// included.
+template <int OUT, int N>
+__device__ __forceinline__ void tile_values(const Int8Args &a, const i32x4 *sum, int stride, int f0,
+                                            int64_t group, int64_t row0, int count, int lane,
+                                            f32x4 (&z)[N])
+{
+    const int g = lane >> 4;
+    const int64_t row = row0 + (lane & 15);
+    const float scale = row < a.m ? a.scales[row] : 0.0f;
+#pragma unroll
+    for (int f = 0; f < N; ++f)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t n = group * kGroup + 8 * (4 * g + i) + f0 + f;
+            z[f][i] = scaled_sum(sum[f * stride][i], n < a.n ? a.w_scales[n] : 0.0f, scale);
+        }
+    for (int c = 0; 32 * c < count; ++c) {
+        const u32x4 xf = x_outliers<OUT>(a, row0 >> 4, c, count, lane);
+#pragma unroll
+        for (int f = 0; f < N; ++f)
+            z[f] = Half<OUT>::mfma(weight_outliers<OUT, true>(a, group * kGroupFrags + f0 + f, c, count, lane), xf,
+                                   z[f]);
+    }
+}
+
+// Tile of 128 WN output columns x 16 TF WT tokens; wave (wn, wt) takes group wn of
+// the tile and 16 TF tokens.  Both operands go from memory straight to LDS, four
+// steps of 64 k in a ring, the step three ahead under way while one is multiplied;
+// one barrier a step.
+template <int OUT, int WN, int WT, int TF>
+__global__ __launch_bounds__(64 * WN * WT) void int8_product_kernel(Int8Args a)
+{
+    constexpr int kWaves = WN * WT;
+    constexpr int kRows = 16 * TF * WT;
+    constexpr int kStageFrags = WN * kGroupFrags + TF * WT;
+    constexpr int kStage = kStageFrags * kFragBytes;
+    constexpr int kLoads = kStageFrags / kWaves;
+    static_assert(kLoads * kWaves == kStageFrags, "the waves share the loads evenly");
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * kStage];
+    static_assert(kWaves * 16 * kFinishLd * 4 <= 4 * kStage, "the epilogue slabs fit the stages");
+
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wn = wave % WN, wt = wave / WN;
+
+    // consecutive workgroups go to the XCDs in turn: give each XCD a contiguous
+    // run of tiles, so that its L2 serves their shared operands
+    const int tiles = gridDim.x;
+    const int per = tiles / kXcds, extra = tiles % kXcds;
+    const int xcd = blockIdx.x % kXcds, idx = blockIdx.x / kXcds;
+    const int tile = xcd * per + (xcd < extra ? xcd : extra) + idx;
+    const int tile_n = tile / a.tiles_t, tile_t = tile - tile_n * a.tiles_t;
+    const int64_t col0 = static_cast<int64_t>(tile_n) * (WN * kGroup);
+    const int64_t row0 = static_cast<int64_t>(tile_t) * kRows;
+
+    // this wave's loads of a step: fragments wave * kLoads .. of the weight's, then
+    // the codes'; rows past the end get an offset past any buffer
+    const int64_t cols_left = a.n - col0, rows_left = a.m - row0;
+    const int cols_here = static_cast<int>(cols_left < WN * kGroup ? cols_left : WN * kGroup);
+    const int rows_here = static_cast<int>(rows_left < kRows ? rows_left : kRows);
+    const u32x4 rs_w = make_rsrc(a.w + col0 * a.ld_w, static_cast<uint32_t>((cols_here - 1) * a.ld_w + a.k));
+    const u32x4 rs_x = make_rsrc(a.codes + row0 * a.ld_codes,
+                                 static_cast<uint32_t>((rows_here - 1) * a.ld_codes + a.k));
+    const int piece = (lane & 3) ^ ((lane >> 4) & 3), lr = lane >> 2;
+    uint32_t off[kLoads];
+#pragma unroll
+    for (int q = 0; q < kLoads; ++q) {
+        const int fr = wave * kLoads + q;
+        if (fr < WN * kGroupFrags) {
+            const int row = (fr >> 3) * kGroup + 8 * lr + (fr & 7);
+            off[q] = row < cols_here ? static_cast<uint32_t>(row * a.ld_w) + 16 * piece : kPast;
+        } else {
+            const int row = (fr - WN * kGroupFrags) * 16 + lr;
+            off[q] = row < rows_here ? static_cast<uint32_t>(row * a.ld_codes) + 16 * piece : kPast;
+        }
+    }
+    const uint32_t to0 = lds_offset(lds) + wave * (kLoads * kFragBytes);
+
+    const int steps = (a.k + kStep - 1) / kStep;
+    const int split = blockIdx.y;
+    const int h_first = static_cast<int>(static_cast<uint32_t>(steps * split) / static_cast<uint32_t>(a.splits));
+    const int h_last = static_cast<int>(static_cast<uint32_t>(steps * (split + 1)) / static_cast<uint32_t>(a.splits));
+
+    // always kLoads: past the last step they fetch zeros that nobody reads
+    auto issue = [&](int h) {
+        const uint32_t k0 = static_cast<uint32_t>(h) * kStep;
+        const bool in = h < h_last && k0 + 16 * piece < static_cast<uint32_t>(a.k);
+        const uint32_t to = to0 + (h & 3) * kStage;
+#pragma unroll
+        for (int q = 0; q < kLoads; ++q)
+            buffer_to_lds(wave * kLoads + q < WN * kGroupFrags ? rs_w : rs_x, in ? off[q] + k0 : kPast, 0,
+                          to + q * kFragBytes);
+    };
+
+    i32x4 acc[kGroupFrags][TF];
+#pragma unroll
+    for (int f = 0; f < kGroupFrags; ++f)
+#pragma unroll
+        for (int t = 0; t < TF; ++t)
+            acc[f][t] = i32x4{0, 0, 0, 0};
+
+    issue(h_first);
+    issue(h_first + 1);
+    issue(h_first + 2);
+    const uint32_t from = piece_at(lane & 15, lane >> 4);
+    for (int h = h_first; h < h_last; ++h) {
+        // step h has arrived (h + 1 and h + 2 are under way), and this wave's reads
+        // of step h - 1 are done: its place is filled next
+        __asm__ volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(2 * kLoads) : "memory");
+        __builtin_amdgcn_s_barrier();
+        __asm__ volatile("" ::: "memory");
+        const uint8_t *stage = lds + (h & 3) * kStage + from;
+        u32x4 wf[kGroupFrags], xf[TF];
+#pragma unroll
+        for (int t = 0; t < TF; ++t)
+            xf[t] = *reinterpret_cast<const u32x4 *>(stage + (WN * kGroupFrags + wt * TF + t) * kFragBytes);
+#pragma unroll
+        for (int f = 0; f < kGroupFrags; ++f)
+            wf[f] = *reinterpret_cast<const u32x4 *>(stage + (wn * kGroupFrags + f) * kFragBytes);
+        issue(h + 3);
+#pragma unroll
+        for (int f = 0; f < kGroupFrags; ++f)
+#pragma unroll
+            for (int t = 0; t < TF; ++t)
+                acc[f][t] = mfma_i8(wf[f], xf[t], acc[f][t]);
+    }
+    // the epilogue takes the buffers: no load may still be on its way into them
+    __asm__ volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    __asm__ volatile("" ::: "memory");
+
+    if (a.splits > 1) {
+        i32x4 *to = a.partial +
+                    ((static_cast<int64_t>(split) * tiles + tile) * kWaves + wave) * (kGroupFrags * TF * 64) + lane;
+#pragma unroll
+        for (int f = 0; f < kGroupFrags; ++f)
+#pragma unroll
+            for (int t = 0; t < TF; ++t)
+                to[(f * TF + t) * 64] = acc[f][t];
+        return;
+    }
+    const int count = outlier_count(a);
+    float *slab = reinterpret_cast<float *>(lds) + wave * (16 * kFinishLd);
+    const int64_t group = static_cast<int64_t>(tile_n) * WN + wn;
+    const int64_t wave_row0 = row0 + wt * (16 * TF);
+    const int g = lane >> 4, c = lane & 15;
+    if (group * kGroup >= a.n)
+        return;
+#pragma unroll
+    for (int t = 0; t < TF; ++t) {
+        if (wave_row0 + t * 16 >= a.m)
+            return;
+        f32x4 z[kGroupFrags];
+        tile_values<OUT, kGroupFrags>(a, &acc[0][t], TF, 0, group, wave_row0 + t * 16, count, lane, z);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float *to = slab + c * kFinishLd + 8 * (4 * g + i);
+            *reinterpret_cast<f32x4 *>(to) = f32x4{z[0][i], z[1][i], z[2][i], z[3][i]};
+            *reinterpret_cast<f32x4 *>(to + 4) = f32x4{z[4][i], z[5][i], z[6][i], z[7][i]};
+        }
+        // the wave's LDS operations complete in order; the compiler must not move
+        // the reads of other lanes' values above the writes
+        __asm__ volatile("" ::: "memory");
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll 1
+        for (int it = 0; it < 4; ++it)
+            finish_slab_rows<OUT>(a, slab, wave_row0 + t * 16, group, it, lane);
+        __asm__ volatile("" ::: "memory");
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
+// The splits' sums of one wave's 128 columns x 16 tokens, and the epilogue.  Four
+// waves share the 8 fragments.
+template <int OUT, int WN, int WT, int TF>
+__global__ __launch_bounds__(256) void int8_product_reduce_kernel(Int8Args a, int32_t tiles)
+{
+    __shared__ __attribute__((aligned(16))) float slab[16 * kFinishLd];
+    const int lane = threadIdx.x & 63, q = threadIdx.x >> 6;
+    const int t = blockIdx.y;
+    const int tile = blockIdx.x / (WN * WT), wave = blockIdx.x % (WN * WT);
+    const int wn = wave % WN, wt = wave / WN;
+    const int tile_n = tile / a.tiles_t, tile_t = tile - tile_n * a.tiles_t;
+    const int64_t group = static_cast<int64_t>(tile_n) * WN + wn;
+    const int64_t row0 = (static_cast<int64_t>(tile_t) * WT + wt) * (16 * TF) + 16 * t;
+    if (group * kGroup >= a.n || row0 >= a.m)
+        return;
+    const i32x4 *from = a.partial + (static_cast<int64_t>(tile) * (WN * WT) + wave) * (kGroupFrags * TF * 64) +
+                        (2 * q * TF + t) * 64 + lane;
+    const int64_t split_step = static_cast<int64_t>(tiles) * (WN * WT) * (kGroupFrags * TF * 64);
+    i32x4 sum[2] = {};
+    for (int s = 0; s < a.splits; s += 8) {
+        i32x4 part[8][2];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int f = 0; f < 2; ++f)  // past the last split: the first again, left out below
+                part[i][f] = from[(s + i < a.splits ? s + i : s) * split_step + f * TF * 64];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (s + i < a.splits)
+#pragma unroll
+                for (int f = 0; f < 2; ++f)
+                    sum[f] = sum[f] + part[i][f];
+    }
+    f32x4 z[2];
+    tile_values<OUT, 2>(a, sum, 1, 2 * q, group, row0, outlier_count(a), lane, z);
+    const int g = lane >> 4, c = lane & 15;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<f32x2 *>(slab + c * kFinishLd + 8 * (4 * g + i) + 2 * q) = f32x2{z[0][i], z[1][i]};
+    __syncthreads();
+    finish_slab_rows<OUT>(a, slab, row0, group, q, lane);
+}
+
+// Rows of bytes, any alignment and stride, into rows of ld_out bytes (a multiple of
+// 16) with zeros behind column k.
+__global__ __launch_bounds__(256) void int8_rows_zero_fill(const int8_t *in, int64_t ld_in, int64_t rows,
+                                                           int32_t k, int8_t *out, int32_t ld_out)
+{
+    const int words = ld_out / 4;
+    for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+        const int8_t *from = in + row * ld_in;
+        uint32_t *to = reinterpret_cast<uint32_t *>(out + row * ld_out);
+        for (int c = threadIdx.x; c < words; c += 256) {
+            uint32_t q = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (4 * c + j < k)
+                    q |= static_cast<uint32_t>(static_cast<uint8_t>(from[4 * c + j])) << (8 * j);
+            to[c] = q;
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+// The least 15-bit pattern of T whose value is not below the threshold; T's
+// infinity where every finite value is.
+uint32_t threshold_pattern(float threshold, int32_t dtype)
+{
+    const auto value = [&](uint32_t bits) {
+        if (dtype == DQ4_BF16) {
+            const uint32_t wide = bits << 16;
+            float f;
+            __builtin_memcpy(&f, &wide, 4);
+            return static_cast<double>(f);
+        }
+        const int e = static_cast<int>(bits >> 10);
+        const double f = static_cast<double>(bits & 1023);
+        return e == 0 ? f * 0x1p-24 : __builtin_ldexp(1024.0 + f, e - 25);
+    };
+    uint32_t low = 1, high = dtype == DQ4_F16 ? 0x7C00u : 0x7F80u;
+    while (low < high) {
+        const uint32_t mid = (low + high) / 2;
+        if (value(mid) >= static_cast<double>(threshold))
+            high = mid;
+        else
+            low = mid + 1;
+    }
+    return low;
+}
+
+bool sizes_fit(int64_t m, int64_t n_out, int64_t n_in)
+{
+    return m <= kMaxDim && n_out <= kMaxDim && n_in <= kMaxSum && m * n_out <= kMaxMatrix;
+}
+
+// Row strides up to this keep a tile's 256 rows below the offset 2^31.
+constexpr int64_t kMaxStride = int64_t{1} << 22;
+
+// Whether rows of bytes can be loaded 16 at a time.
+bool byte_rows_aligned(const void *p, int64_t ld, int64_t rows, int64_t k)
+{
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && k % 16 == 0 &&
+           (rows <= 1 || (ld % 16 == 0 && ld <= kMaxStride));
+}
+
+constexpr int64_t kRowsMost = 64;  // tokens of int8_rows_kernel
+
+constexpr int kTileCols[3] = {256, 128, 128}, kTileRows[3] = {256, 128, 64};
+constexpr int kTileResident[3] = {1, 2, 3};  // workgroups per CU (LDS)
+// Microseconds of one step of 64 k with every CU full.
+constexpr double kTileStep[3] = {0.9, 0.7, 0.6};
+
+struct Plan {
+    int tile, splits;
+    double cost;
+};
+
+Plan plan_of(int64_t m, int64_t n, int64_t k, int cus)
+{
+    Plan best{2, 1, 1e300};
+    const int64_t steps = ceil_div(k, kStep);
+    for (int tile = 0; tile < 3; ++tile) {
+        const int64_t tiles = ceil_div(n, kTileCols[tile]) * ceil_div(m, kTileRows[tile]);
+        for (int splits = 1; splits <= 16; ++splits) {
+            if (splits > 1 && splits * 4 > steps)
+                break;
+            const int64_t rounds = ceil_div(tiles * splits, static_cast<int64_t>(cus) * kTileResident[tile]);
+            double cost = static_cast<double>(rounds) *
+                          (static_cast<double>(ceil_div(steps, splits)) * kTileStep[tile] + 3.0);
+            if (splits > 1)  // the partial sums, written and read at about 4 TB/s, and a launch
+                cost += 3.0 + static_cast<double>(splits) * static_cast<double>(m) * static_cast<double>(n) * 8.0 / 4e6;
+            if (cost < best.cost)
+                best = Plan{tile, splits, cost};
+        }
+    }
+    return best;
+}
+
+int64_t partial_bytes(const Plan &p, int64_t m, int64_t n)
+{
+    return p.splits == 1 ? 0
+                         : p.splits * ceil_div(n, kTileCols[p.tile]) * kTileCols[p.tile] *
+                               ceil_div(m, kTileRows[p.tile]) * kTileRows[p.tile] * 4;
+}
+
+// What a product's workspace holds, in this order.
+struct Layout {
+    bool rows;                       // int8_rows_kernel
+    bool copy_codes, copy_weight;    // in rows of ld_copy bytes
+    int64_t ld_copy;
+    int64_t codes_bytes, weight_bytes;
+    int64_t w_frags, x_frags;        // outlier fragments
+    Plan plan;
+    int64_t partial;
+    int64_t frag_bytes() const { return (w_frags + x_frags) * kOutlierChunks * kFragBytes; }
+    int64_t bytes() const { return codes_bytes + weight_bytes + frag_bytes() + partial; }
+};
+
+Layout layout_of(const void *codes, int64_t m, int64_t ld_codes, const void *w, int64_t n, int64_t k,
+                 bool outliers, int cus)
+{
+    Layout l{};
+    l.rows = m <= kRowsMost;
+    l.copy_codes = l.rows ? m > 1 && ld_codes > kMaxStride : !byte_rows_aligned(codes, ld_codes, m, k);
+    l.copy_weight = !l.rows && !byte_rows_aligned(w, k, n, k);
+    l.ld_copy = ceil_div(k, kStep) * kStep;
+    l.codes_bytes = l.copy_codes ? align256(m * l.ld_copy) : 0;
+    l.weight_bytes = l.copy_weight ? align256(n * l.ld_copy) : 0;
+    if (!l.rows) {
+        l.plan = plan_of(m, n, k, cus);
+        l.partial = partial_bytes(l.plan, m, n);
+    }
+    if (outliers && k > 0) {
+        l.w_frags = l.rows ? ceil_div(n, 16) : ceil_div(n, kGroup) * kGroupFrags;
+        l.x_frags = ceil_div(m, 16);
+    }
+    return l;
+}
+
+template <int OUT, int TF, int R, int DEPTH>
+dq4_status_t launch_rows_tile(Int8Args a, bool aligned, int cus, hipStream_t s)
+{
+    a.row_blocks = static_cast<int32_t>(ceil_div(a.n, 16 * R));
+    void *params[] = {&a};
+    const void *kernel = aligned ? reinterpret_cast<const void *>(&int8_rows_kernel<OUT, TF, R, DEPTH, true>)
+                                 : reinterpret_cast<const void *>(&int8_rows_kernel<OUT, TF, R, DEPTH, false>);
+    return launch(kernel, a.row_blocks < cus ? a.row_blocks : cus, 1, 512, params, s);
+}
+
+template <int OUT>
+dq4_status_t launch_rows(const Int8Args &a, int cus, hipStream_t s)
+{
+    const bool aligned = byte_rows_aligned(a.codes, a.ld_codes, a.m, a.k) && byte_rows_aligned(a.w, a.ld_w, a.n, a.k);
+    const bool two = ceil_div(a.n, 32) >= cus;
+    if (a.m <= 16)
+        return two ? launch_rows_tile<OUT, 1, 2, 6>(a, aligned, cus, s) : launch_rows_tile<OUT, 1, 1, 8>(a, aligned, cus, s);
+    if (a.m <= 32)
+        return two ? launch_rows_tile<OUT, 2, 2, 4>(a, aligned, cus, s) : launch_rows_tile<OUT, 2, 1, 6>(a, aligned, cus, s);
+    return two ? launch_rows_tile<OUT, 4, 2, 3>(a, aligned, cus, s) : launch_rows_tile<OUT, 4, 1, 3>(a, aligned, cus, s);
+}
+
+template <int OUT, int WN, int WT, int TF>
+dq4_status_t launch_tile(Int8Args a, hipStream_t s)
+{
+    a.tiles_t = static_cast<int32_t>(ceil_div(a.m, 16 * TF * WT));
+    const int64_t tiles = ceil_div(a.n, WN * kGroup) * a.tiles_t;
+    void *params[] = {&a};
+    const dq4_status_t st = launch(reinterpret_cast<const void *>(&int8_product_kernel<OUT, WN, WT, TF>), tiles,
+                                   a.splits, 64 * WN * WT, params, s);
+    if (st != DQ4_OK || a.splits == 1)
+        return st;
+    int32_t n_tiles = static_cast<int32_t>(tiles);
+    void *rp[] = {&a, &n_tiles};
+    return launch(reinterpret_cast<const void *>(&int8_product_reduce_kernel<OUT, WN, WT, TF>), tiles * WN * WT, TF,
+                  256, rp, s);
+}
+
+dq4_status_t copy_rows(const int8_t *in, int64_t ld_in, int64_t rows, int64_t k, uint8_t *out, int64_t ld_out,
+                       int cus, hipStream_t s)
+{
+    int32_t k32 = static_cast<int32_t>(k), ld32 = static_cast<int32_t>(ld_out);
+    void *params[] = {&in, &ld_in, &rows, &k32, &out, &ld32};
+    const int64_t grid = rows < cus * 8 ? rows : cus * 8;
+    return launch(reinterpret_cast<const void *>(&int8_rows_zero_fill), grid, 1, 256, params, s);
+}
+
+template <int OUT>
+dq4_status_t run_linear(Int8Args a, const Layout &l, uint8_t *ws, int cus, hipStream_t s)
+{
+    dq4_status_t st = DQ4_OK;
+    if (l.copy_codes && a.k > 0) {
+        st = copy_rows(a.codes, a.ld_codes, a.m, a.k, ws, l.ld_copy, cus, s);
+        if (st != DQ4_OK)
+            return st;
+        a.codes = reinterpret_cast<const int8_t *>(ws);
+        a.ld_codes = l.ld_copy;
+    }
+    if (l.copy_weight && a.k > 0) {
+        uint8_t *to = ws + l.codes_bytes;
+        st = copy_rows(a.w, a.ld_w, a.n, a.k, to, l.ld_copy, cus, s);
+        if (st != DQ4_OK)
+            return st;
+        a.w = reinterpret_cast<const int8_t *>(to);
+        a.ld_w = l.ld_copy;
+    }
+    uint16_t *frags = reinterpret_cast<uint16_t *>(ws + l.codes_bytes + l.weight_bytes);
+    if (l.w_frags > 0) {
+        int64_t w_frags = l.w_frags, x_frags = l.x_frags;
+        void *params[] = {&a, &w_frags, &x_frags, &frags};
+        const int64_t groups = ceil_div(w_frags + x_frags, 4);
+        const void *kernel = l.rows ? reinterpret_cast<const void *>(&int8_outlier_fragments_kernel<OUT, false>)
+                                    : reinterpret_cast<const void *>(&int8_outlier_fragments_kernel<OUT, true>);
+        st = launch(kernel, groups < cus * 8 ? groups : cus * 8, 1, 256, params, s);
+        if (st != DQ4_OK)
+            return st;
+        a.w_outliers = frags;
+        a.x_outliers = frags + w_frags * kOutlierChunks * (kFragBytes / 2);
+    } else {
+        a.outliers = nullptr;
+    }
+    if (l.rows)
+        return launch_rows<OUT>(a, cus, s);
+    // copies end in zeros: the tiles read whole pieces of 16
+    a.k = static_cast<int32_t>(l.copy_codes || l.copy_weight ? ceil_div(a.k, 16) * 16 : a.k);
+    a.splits = l.plan.splits;
+    a.partial = reinterpret_cast<i32x4 *>(ws + l.codes_bytes + l.weight_bytes + l.frag_bytes());
+    if (l.plan.tile == 0)
+        return launch_tile<OUT, 2, 4, 4>(a, s);
+    if (l.plan.tile == 1)
+        return launch_tile<OUT, 1, 4, 2>(a, s);
+    return launch_tile<OUT, 1, 4, 1>(a, s);
+}
+
+}  // namespace
+}  // namespace dq4
+
+using namespace dq4;
+
+extern "C" {
+
+int64_t dq4_int8_quant_workspace_bytes(int64_t m, int64_t n_in, float threshold)
+{
+    if (!(threshold > 0.0f) || m <= 1 || n_in <= 0 || n_in > kMaxSum)
+        return 0;
+    return align256(n_in);
+}
+
+dq4_status_t dq4_int8_quant(const void *x, int64_t m, int64_t n_in, int64_t ld_x, int32_t dtype,
+                            float threshold, int8_t *codes, int64_t ld_codes, float *scales,
+                            int32_t *outliers, void *workspace, int64_t workspace_bytes, void *stream)
+{
+    if (m < 0 || n_in < 0 || (dtype != DQ4_F16 && dtype != DQ4_BF16) || !(threshold >= 0.0f))
+        return DQ4_EINVAL;
+    if (!sizes_fit(m, 0, n_in) || m * n_in > kMaxMatrix)
+        return DQ4_EUNSUPPORTED;
+    const bool mixed = threshold > 0.0f;
+    if (mixed != (outliers != nullptr))
+        return DQ4_EINVAL;
+    if (m > 0 && (!scales || (n_in > 0 && (!x || !codes || bad_ld(ld_x, m, n_in) || bad_ld(ld_codes, m, n_in)))))
+        return DQ4_EINVAL;
+    if (workspace_bytes < dq4_int8_quant_workspace_bytes(m, n_in, threshold) ||
+        bad_workspace(workspace, workspace_bytes))
+        return DQ4_EINVAL;
+    if (m == 0 && !mixed)
+        return DQ4_OK;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    const int cus = current_compute_units();
+    QuantArgs a{};
+    a.x = static_cast<const uint16_t *>(x);
+    a.m = m;
+    a.k = n_in;
+    a.ld_x = ld_x;
+    a.non_finite = dtype == DQ4_F16 ? 0x7C00u : 0x7F80u;
+    a.limit = mixed ? threshold_pattern(threshold, dtype) : 0x8000u;
+    a.codes = codes;
+    a.ld_codes = ld_codes;
+    a.scales = scales;
+    a.outliers = outliers;
+    a.flags = static_cast<uint8_t *>(workspace);
+    a.vec_in = rows_aligned(x, ld_x, m, n_in);
+    a.vec_out = reinterpret_cast<uintptr_t>(codes) % 8 == 0 && n_in % 8 == 0 && (m <= 1 || ld_codes % 8 == 0);
+    void *params[] = {&a};
+    if (m <= 1) {
+        const void *kernel = dtype == DQ4_F16
+                                 ? reinterpret_cast<const void *>(&int8_quant_rows_kernel<DQ4_F16, true>)
+                                 : reinterpret_cast<const void *>(&int8_quant_rows_kernel<DQ4_BF16, true>);
+        return launch(kernel, 1, 1, 1024, params, s);
+    }
+    if (mixed && n_in > 0) {
+        uint32_t *words = static_cast<uint32_t *>(workspace);
+        int32_t n = static_cast<int32_t>(align256(n_in) / 4);
+        void *fill[] = {&words, &n};
+        const dq4_status_t st =
+            launch(reinterpret_cast<const void *>(&int8_flags_zero_fill), ceil_div(n, 256), 1, 256, fill, s);
+        if (st != DQ4_OK)
+            return st;
+    }
+    const int64_t grid = m < cus * 8 ? m : cus * 8;
+    const void *kernel = dtype == DQ4_F16
+                             ? reinterpret_cast<const void *>(&int8_quant_rows_kernel<DQ4_F16, false>)
+                             : reinterpret_cast<const void *>(&int8_quant_rows_kernel<DQ4_BF16, false>);
+    const dq4_status_t st = launch(kernel, grid, 1, 256, params, s);
+    if (st != DQ4_OK || !mixed)
+        return st;
+    const int64_t zero = ceil_div(m, 16) < cus ? ceil_div(m, 16) : cus;
+    return launch(reinterpret_cast<const void *>(&int8_outliers_zero_fill), 1 + zero, 1, 1024, params, s);
+}
+
+int64_t dq4_int8_linear_workspace_bytes(const int8_t *codes, int64_t m, int64_t ld_codes, const int8_t *CB,
+                                        int64_t n_out, int64_t n_in, int32_t outliers)
+{
+    if (m <= 0 || n_out <= 0 || n_in < 0 || !sizes_fit(m, n_out, n_in))
+        return 0;
+    return layout_of(codes, m, ld_codes, CB, n_out, n_in, outliers != 0, current_compute_units()).bytes();
+}
+
+dq4_status_t dq4_int8_linear(const int8_t *codes, int64_t m, int64_t ld_codes, const float *scales,
+                             const int8_t *CB, const float *SCB, int64_t n_out, int64_t n_in, int32_t dtype,
+                             const void *x, int64_t ld_x, const int32_t *outliers, const void *bias,
+                             const void *residual, int64_t ld_residual, void *y, int64_t ld_y,
+                             void *workspace, int64_t workspace_bytes, void *stream)
+{
+    if (m < 0 || n_out < 0 || n_in < 0 || (dtype != DQ4_F16 && dtype != DQ4_BF16))
+        return DQ4_EINVAL;
+    if (!sizes_fit(m, n_out, n_in))
+        return DQ4_EUNSUPPORTED;
+    if (m == 0 || n_out == 0)
+        return DQ4_OK;
+    if (!scales || !SCB || !y || (n_in > 0 && (!codes || !CB)) || ((x != nullptr) != (outliers != nullptr) && n_in > 0))
+        return DQ4_EINVAL;
+    if (bad_ld(ld_codes, m, n_in) || bad_ld(ld_y, m, n_out) || (residual && bad_ld(ld_residual, m, n_out)) ||
+        (outliers && bad_ld(ld_x, m, n_in)))
+        return DQ4_EINVAL;
+    const int cus = current_compute_units();
+    const Layout l = layout_of(codes, m, ld_codes, CB, n_out, n_in, outliers != nullptr, cus);
+    if (workspace_bytes < l.bytes() || bad_workspace(workspace, workspace_bytes))
+        return DQ4_EINVAL;
+    Int8Args a{};
+    a.codes = codes;
+    a.ld_codes = m > 1 ? ld_codes : n_in;
+    a.scales = scales;
+    a.w = CB;
+    a.ld_w = n_in;
+    a.w_scales = SCB;
+    a.m = m;
+    a.n = n_out;
+    a.k = a.n_in = static_cast<int32_t>(n_in);
+    a.x = static_cast<const uint16_t *>(x);
+    a.ld_x = ld_x;
+    a.outliers = outliers;
+    a.bias = static_cast<const uint16_t *>(bias);
+    a.residual = static_cast<const uint16_t *>(residual);
+    a.ld_residual = ld_residual;
+    a.y = static_cast<uint16_t *>(y);
+    a.ld_y = ld_y;
+    a.vec = rows_aligned(y, ld_y, m, 8) && (!bias || reinterpret_cast<uintptr_t>(bias) % 16 == 0) &&
+            (!residual || rows_aligned(residual, ld_residual, m, 8));
+    a.splits = 1;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    return dtype == DQ4_F16 ? run_linear<DQ4_F16>(a, l, ws, cus, s) : run_linear<DQ4_BF16>(a, l, ws, cus, s);
+}
+
+}  // extern "C"

@@ -35,6 +35,7 @@
 
 #include "dq4.h"
 #include "dq4_device.h"
+#include "dq4_int8.h"
 #include "dq4_linear.h"
 #include "dq4_linear_device.h"
 
@@ -408,6 +409,83 @@ __global__ __launch_bounds__(kThreads) void weight_fragments_kernel(FragmentArgs
         for (int f = 0; f < 8; ++f)
             *reinterpret_cast<u32x4 *>(base + f * (kFragBytes / 2)) = q[f];
     }
+}
+
+// The columns of an LLM.int8 weight (include/dq4_int8.h) as fragments of 16-bit
+// values, laid out as in the backward decode above.  kAligned: 8 codes of a row are
+// an aligned 8-byte load; otherwise they are cut out of three dwords (the dword
+// with the weight's last byte is read whole, nothing beyond it).  Bound by memory:
+// 1 byte read and 2 written per element.
+struct Int8FragmentArgs {
+    const int8_t *codes;
+    const float *scales;
+    uint16_t *out;
+    int64_t n_out, n_in;
+    int32_t groups, chunks;
+};
+
+template <int OUT, bool kAligned>
+__global__ __launch_bounds__(kThreads) void int8_column_fragments_kernel(Int8FragmentArgs a)
+{
+    constexpr float kR127 = 0x1.020408p-7f;  // the FP32 value nearest 1/127
+    const int tid = threadIdx.x;
+    const int pair = blockIdx.x / a.chunks, chunk = blockIdx.x - pair * a.chunks;
+    const int lane = tid & 63, ks = (tid >> 6) & 1, group = pair * 2 + (tid >> 7);
+    if (group >= a.groups)
+        return;
+    const int64_t o0 = static_cast<int64_t>(chunk) * kChunk + ks * 32 + (lane >> 4) * 8;
+    const int64_t j0 = static_cast<int64_t>(group) * kGroup + 8 * (lane & 15);
+    const uintptr_t base = reinterpret_cast<uintptr_t>(a.codes);
+    const uintptr_t last = (base + a.n_out * a.n_in - 1) & ~uintptr_t{3};
+    u32x4 q[8];
+#pragma unroll
+    for (int f = 0; f < 8; ++f)
+        q[f] = u32x4{0, 0, 0, 0};
+    if (j0 < a.n_in) {
+        u32x2 code[8];
+        float scale[8];
+#pragma unroll
+        for (int h = 0; h < 8; ++h) {
+            const int64_t o = o0 + h;
+            code[h] = u32x2{0, 0};
+            scale[h] = 0.0f;
+            if (o < a.n_out) {
+                scale[h] = a.scales[o];
+                const uintptr_t at = base + o * a.n_in + j0;
+                if constexpr (kAligned) {
+                    code[h] = *reinterpret_cast<const u32x2 *>(at);
+                } else {
+                    uint32_t d[3];
+#pragma unroll
+                    for (int i = 0; i < 3; ++i) {
+                        const uintptr_t w = (at & ~uintptr_t{3}) + 4 * i;
+                        d[i] = *reinterpret_cast<const uint32_t *>(w < last ? w : last);
+                    }
+                    code[h] = u32x2{__builtin_amdgcn_alignbyte(d[1], d[0], static_cast<uint32_t>(at) & 3),
+                                    __builtin_amdgcn_alignbyte(d[2], d[1], static_cast<uint32_t>(at) & 3)};
+                }
+            }
+        }
+#pragma unroll
+        for (int p = 0; p < 4; ++p)
+#pragma unroll
+            for (int f = 0; f < 8; ++f) {
+                float v[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int8_t c = static_cast<int8_t>(code[2 * p + h][f / 4] >> (8 * (f & 3)));
+                    const float scaled = static_cast<float>(c) * scale[2 * p + h];
+                    // columns past the last one: products that nobody takes
+                    v[h] = scaled * kR127;
+                }
+                q[f][p] = Half<OUT>::pack2(v[0], v[1]);
+            }
+    }
+    uint16_t *to = a.out + (static_cast<int64_t>(group) * a.chunks + chunk) * (kUnitBytes / 2) +
+                   ks * (kFrags * kFragBytes / 2) + lane * 8;
+#pragma unroll
+    for (int f = 0; f < 8; ++f)
+        *reinterpret_cast<u32x4 *>(to + f * (kFragBytes / 2)) = q[f];
 }
 
 // ---------------------------------------------------------------------------
@@ -2879,6 +2957,52 @@ dq4_status_t run_product(const Shape &sh, const dq4_weight_t *w0, const dq4_weig
     return DQ4_OK;
 }
 
+// dx = dy W for an LLM.int8 weight: its columns to 16-bit fragments, then the
+// product.
+template <int OUT>
+dq4_status_t run_int8_columns(const Shape &sh, const int8_t *codes, const float *scales, ProductArgs p,
+                              const BesideWork &beside, uint8_t *ws, hipStream_t s)
+{
+    int device = 0;
+    const hipError_t e = hipGetDevice(&device);
+    if (e != hipSuccess)
+        return hip_failed(e);
+    const int cus = compute_units(device);
+    const Plan plan = sh.plan(cus);
+    if (beside.kind != kNothing) {
+        const dq4_status_t st = launch_fragments<OUT, false>(FragmentArgs{}, true, beside, cus, s);
+        if (st != DQ4_OK)
+            return st;
+    }
+    p.m = sh.m;
+    p.n = sh.n;
+    p.splits = plan.splits;
+    p.partial = reinterpret_cast<f32x4 *>(ws);
+    p.n_x = 1;
+    p.groups = static_cast<int32_t>(sh.groups());
+    p.chunks = static_cast<int32_t>(sh.chunks());
+    Int8FragmentArgs f{};
+    f.codes = codes;
+    f.scales = scales;
+    f.out = reinterpret_cast<uint16_t *>(ws + sh.split_bytes(plan, sh.groups()));
+    f.n_out = sh.k;
+    f.n_in = sh.n;
+    f.groups = p.groups;
+    f.chunks = p.chunks;
+    p.wfrag = f.out;
+    if (f.chunks > 0) {
+        const bool aligned = sh.n % 8 == 0 && reinterpret_cast<uintptr_t>(codes) % 8 == 0;
+        void *params[] = {&f};
+        const dq4_status_t st =
+            launch(aligned ? reinterpret_cast<const void *>(&int8_column_fragments_kernel<OUT, true>)
+                           : reinterpret_cast<const void *>(&int8_column_fragments_kernel<OUT, false>),
+                   ceil_div(sh.groups(), 2) * f.chunks, 1, kThreads, params, s);
+        if (st != DQ4_OK)
+            return st;
+    }
+    return launch_product<OUT, false>(p, plan, s);
+}
+
 template <int OUT, bool kTwo, int TF>
 dq4_status_t launch_columns_tile(ColumnArgs a, hipStream_t s)
 {
@@ -2950,6 +3074,13 @@ dq4_status_t check_call(const dq4_weight_t *w0, const dq4_weight_t *w1, int64_t 
         m * n_in > kMaxMatrix)
         return DQ4_EUNSUPPORTED;
     return DQ4_OK;
+}
+
+int64_t int8_backward_need(int64_t n_out, int64_t n_in, int64_t m, const void *dy, int64_t ld_dy)
+{
+    const Shape s{m, n_in, n_out, kSingle};
+    const bool copy = n_in > 0 && needs_copy(dy, ld_dy, m, n_out);
+    return workspace_need(s, copy_bytes(s, copy) + partial_bytes(m, n_out), false);
 }
 
 bool sizes_ok(int64_t n_out, int64_t n_in, int64_t m)
@@ -3319,6 +3450,95 @@ dq4_status_t dq4_gated_fused_backward(const dq4_weight_t *gate, const dq4_weight
                                            workspace_bytes - fixed, s);
     return run_product<DQ4_BF16, false>(sh, gate, up, n_ff, n_in, log2_block, p, beside, ws + fixed,
                                         workspace_bytes - fixed, s);
+}
+
+int64_t dq4_int8_linear_backward_workspace_bytes(int64_t n_out, int64_t n_in, int64_t m, const void *dy,
+                                                 int64_t ld_dy)
+{
+    if (!sizes_ok(n_out, n_in, m))
+        return 0;
+    return int8_backward_need(n_out, n_in, m, dy, ld_dy);
+}
+
+dq4_status_t dq4_int8_linear_backward(const int8_t *CB, const float *SCB, int64_t n_out, int64_t n_in,
+                                      int32_t dtype, const void *dy, int64_t m, int64_t ld_dy, void *dx,
+                                      int64_t ld_dx, float *dbias, void *workspace, int64_t workspace_bytes,
+                                      void *stream)
+{
+    if (n_out < 0 || n_in < 0 || m < 0 || (dtype != DQ4_F16 && dtype != DQ4_BF16))
+        return DQ4_EINVAL;
+    if (n_out > kMaxDim || n_in > kMaxDim || m > kMaxDim || m * n_out > kMaxMatrix / 2 ||
+        m * n_in > kMaxMatrix / 2)
+        return DQ4_EUNSUPPORTED;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    if (m == 0) {  // empty sums
+        if (!dbias || n_out == 0)
+            return DQ4_OK;
+        const float *none = nullptr;
+        int64_t n = n_out;
+        int32_t blocks = 0;
+        void *params[] = {&none, &n, &blocks, &dbias};
+        return launch(reinterpret_cast<const void *>(&bias_grad_reduce_kernel), ceil_div(n, kThreads), 1,
+                      kThreads, params, s);
+    }
+    if (n_out > 0 && (!dy || bad_ld(ld_dy, m, n_out)))
+        return DQ4_EINVAL;
+    if (n_in > 0 && (!dx || bad_ld(ld_dx, m, n_in) || (n_out > 0 && (!CB || !SCB))))
+        return DQ4_EINVAL;
+    if (n_out > 0 && (workspace_bytes < int8_backward_need(n_out, n_in, m, dy, ld_dy) ||
+                      bad_workspace(workspace, workspace_bytes)))
+        return DQ4_EINVAL;
+    const Shape sh{m, n_in, n_out, kSingle};
+    const bool copy = n_in > 0 && needs_copy(dy, ld_dy, m, n_out);
+    const int64_t copied = copy_bytes(sh, copy), fixed = copied + partial_bytes(m, n_out);
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    ProductArgs p{};
+    p.x[0] = p.x[1] = static_cast<const uint16_t *>(dy);
+    p.ld_x = product_ld(ld_dy, m, n_out);
+    p.k = n_out;
+    BesideWork beside{kNothing, {}};
+    const int64_t blocks = ceil_div(m, kRowBlock);
+    if (n_out > 0 && (dbias || copy)) {
+        SlopeArgs a{};
+        a.dy = static_cast<const uint16_t *>(dy);
+        a.ld_dy = ld_dy;
+        if (copy) {
+            a.pad[0] = reinterpret_cast<uint16_t *>(ws);
+            a.ld_pad = padded_ld(n_out);
+            a.pad_rows = m;
+            p.x[0] = p.x[1] = a.pad[0];
+            p.ld_x = p.k = a.ld_pad;
+        }
+        a.partial = !dbias ? nullptr : blocks == 1 ? dbias : reinterpret_cast<float *>(ws + copied);
+        a.m = m;
+        a.n = n_out;
+        a.act = DQ4_ACT_NONE;
+        beside = slope_work(a, false);
+        if (dbias && blocks > 1) {
+            p.bias_partial = a.partial;
+            p.bias_n = n_out;
+            p.bias_blocks = static_cast<int32_t>(blocks);
+            p.dbias = dbias;
+        }
+    }
+    if (n_in == 0) {  // no product: the bias gradient alone
+        if (beside.kind == kNothing)
+            return DQ4_OK;
+        const dq4_status_t st =
+            dtype == DQ4_F16 ? launch_fragments<DQ4_F16, false>(FragmentArgs{}, true, beside, 0, s)
+                             : launch_fragments<DQ4_BF16, false>(FragmentArgs{}, true, beside, 0, s);
+        if (st != DQ4_OK || !p.dbias)
+            return st;
+        void *rp[] = {&p.bias_partial, &p.bias_n, &p.bias_blocks, &p.dbias};
+        return launch(reinterpret_cast<const void *>(&bias_grad_reduce_kernel), ceil_div(n_out, kThreads), 1,
+                      kThreads, rp, s);
+    }
+    p.act = DQ4_ACT_NONE;
+    p.y = static_cast<uint16_t *>(dx);
+    p.ld_y = ld_dx;
+    p.vec = rows_aligned(dx, ld_dx, m, 8);
+    return dtype == DQ4_F16 ? run_int8_columns<DQ4_F16>(sh, CB, SCB, p, beside, ws + fixed, s)
+                            : run_int8_columns<DQ4_BF16>(sh, CB, SCB, p, beside, ws + fixed, s);
 }
 
 }  // extern "C"
