@@ -1,7 +1,7 @@
 """MI355X (gfx950) nested block-wise 4-bit dequantization.
 
-Thin Python binding of the C ABI in include/dq4.h, include/dq4_linear.h and
-include/dq4_int8.h (libdq4.so, built in-tree by block_wise_bit_amd/build.py).  The functions keep the C names; they only
+Thin Python binding of the C ABI in include/dq4.h, include/dq4_linear.h,
+include/dq4_int8.h and include/dq4_moe.h (libdq4.so, built in-tree by block_wise_bit_amd/build.py).  The functions keep the C names; they only
 check and marshal arguments -- every step of the dequantization runs in the
 HIP kernels of the library.  torch provides device memory and the current
 stream, nothing else.  There is no fallback: if the library is missing or
@@ -38,6 +38,10 @@ cannot be loaded, every call raises.
                                                    (the LLM.int8 linear layer)
     dq4_int8_linear_backward(dy, CB, SCB, bias_grad) -> (dx, dbias)
     dq4_int8_{quant,linear,linear_backward}_workspace_bytes(...) -> int
+    dq4_moe_route(x, router, top_k) -> (ids, weights)           (a token's experts)
+    dq4_moe_fused(gate, up, down, ..., x, ids, weights) -> tensor
+                                                   (a mixture-of-experts layer, few tokens)
+    dq4_moe_fused_workspace_bytes(n_experts, n_ff, n_in, m, top_k) -> int
     dq4_int8_prep(A, CB, SCB, cols) -> (subA, subB)  (LLM.int8 correction operands)
     dq4_memory_twin_f16(packed, n) -> tensor       (diagnostic: the FP16 call's memory
                                                    traffic without its arithmetic)
@@ -55,6 +59,7 @@ LIBRARY_PATH = os.path.join(PKG_DIR, "libdq4.so")
 HEADER_PATH = os.path.join(os.path.dirname(PKG_DIR), "include", "dq4.h")
 LINEAR_HEADER_PATH = os.path.join(os.path.dirname(PKG_DIR), "include", "dq4_linear.h")
 INT8_HEADER_PATH = os.path.join(os.path.dirname(PKG_DIR), "include", "dq4_int8.h")
+MOE_HEADER_PATH = os.path.join(os.path.dirname(PKG_DIR), "include", "dq4_moe.h")
 
 DQ4_OK, DQ4_EINVAL, DQ4_EUNSUPPORTED, DQ4_EHIP, DQ4_EBLAS, DQ4_ESCRATCH = 0, 1, 2, 3, 4, 5
 DQ4_NOALLOC_MAX_BLOCKS = 1 << 23   # outer blocks the no-allocation call's static scratch holds
@@ -155,6 +160,13 @@ def library() -> ctypes.CDLL:
     lib.dq4_int8_linear_backward_workspace_bytes.argtypes = [i64, i64, i64, P, i64]
     for name in ("dq4_int8_quant", "dq4_int8_linear", "dq4_int8_linear_backward"):
         getattr(lib, name + "_workspace_bytes").restype = i64
+    lib.dq4_moe_route.argtypes = [P, i64, i64, i64, i32, P, P, i32, i32, i32, P, P, P]
+    lib.dq4_moe_fused.argtypes = [W, W, W, i32, i64, i64, i32, i32, P, i64, i64, P, P, i32, P, i64, P,
+                                  i64, P, i64, P]
+    for name in ("dq4_moe_route", "dq4_moe_fused"):
+        getattr(lib, name).restype = i32
+    lib.dq4_moe_fused_workspace_bytes.argtypes = [i32, i64, i64, i64, i32]
+    lib.dq4_moe_fused_workspace_bytes.restype = i64
     lib.dq4_last_blas_status.argtypes = []
     lib.dq4_last_blas_status.restype = i32
     lib.dq4_status_string.argtypes = [i32]
@@ -1227,6 +1239,119 @@ def dq4_int8_linear_backward(dy, CB, SCB, bias_grad: bool = False, dx=None, dbia
                       CB.data_ptr(), SCB.data_ptr(), n_out, n_in, code, dy.data_ptr(), m, ld_dy, dx.data_ptr(),
                       ld_dx, _address(dbias))
     return dx, dbias
+
+
+# ----------------------------------------------------------------------------
+# a mixture-of-experts layer for a few tokens (include/dq4_moe.h)
+# ----------------------------------------------------------------------------
+def dq4_moe_fused_workspace_bytes(n_experts: int, n_ff: int, n_in: int, m: int, top_k: int) -> int:
+    return int(library().dq4_moe_fused_workspace_bytes(int(n_experts), int(n_ff), int(n_in), int(m),
+                                                       int(top_k)))
+
+
+def _dense(t, name: str, shape, dtype, device):
+    if t.dtype != dtype or t.device != device or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {tuple(shape)} {dtype} tensor on {device}")
+
+
+def dq4_moe_route(x, router, top_k: int, bias=None, renormalize: bool = True, ids=None, weights=None,
+                  stream=None):
+    """The top_k experts of each row of x and their weights: (ids, weights).
+
+    x: (m, n_in), router: (n_experts, n_in), one of float16 and bfloat16; bias:
+    (n_experts,) float32.  Logits are x router^T + bias, summed in 64 bits; ids
+    (m, top_k) int32 are those of the largest, in falling order, ties to the
+    lower index; weights (m, top_k) float32 are their softmax, over the chosen
+    experts or, with renormalize False, over all.  An expert with a bias of minus
+    infinity is not chosen: where fewer than top_k are left, the id is -1 and
+    the weight 0."""
+    torch = _torch()
+    code = _half_code(x.dtype, "x")
+    device = x.device
+    if device.type != "cuda" or x.dim() != 2:
+        raise ValueError("x must be a 2-D GPU tensor")
+    m, n_in = x.shape
+    ld_x = _matrix(x, "x", m, n_in, x.dtype, device)
+    if router.dim() != 2:
+        raise ValueError("router must be 2-D")
+    n_experts, top_k = router.size(0), int(top_k)
+    _dense(router, "router", (n_experts, n_in), x.dtype, device)
+    if not 1 <= top_k <= n_experts:
+        raise ValueError(f"top_k must lie in 1 .. {n_experts}, got {top_k}")
+    if bias is not None:
+        _vector(bias, "bias", n_experts, torch.float32, device)
+    given = ids is not None or weights is not None
+    if ids is None:
+        ids = _output((m, top_k), torch.int32, device, stream)
+    if weights is None:
+        weights = _output((m, top_k), torch.float32, device, stream)
+    _dense(ids, "ids", (m, top_k), torch.int32, device)
+    _dense(weights, "weights", (m, top_k), torch.float32, device)
+    if given:
+        _refuse_overlap([("ids", ids), ("weights", weights)], [("x", x), ("router", router), ("bias", bias)], (), 0)
+    with _on_device(device):
+        handle = (_own_stream(device, stream).cuda_stream if stream is not None
+                  else torch._C._cuda_getCurrentRawStream(device.index))
+        st = library().dq4_moe_route(x.data_ptr(), m, n_in, ld_x, code, router.data_ptr(), _address(bias), n_experts,
+                                     top_k, 1 if renormalize else 0, ids.data_ptr(), weights.data_ptr(), handle)
+    if st != DQ4_OK:
+        _raise_for(st, "dq4_moe_route")
+    return ids, weights
+
+
+def dq4_moe_fused(gate, up, down, n_experts: int, n_ff: int, n_in: int, blocksize: int, x, ids, weights,
+                  activation: str = "silu", residual=None, y=None, workspace=None,
+                  nested_blocksize: int = NESTED_BLOCKSIZE, stream=None):
+    """y = sum over the chosen experts e of w_e (act(x Wg_e^T) * (x Wu_e^T)) Wd_e^T
+    + residual: a mixture-of-experts feed-forward layer for up to 64 tokens, each
+    chosen expert's 4-bit matrices read once.
+
+    gate, up: the experts' matrices stacked by rows, one nested 4-bit weight of
+    (n_experts n_ff, n_in) each, down: (n_experts n_in, n_ff), as mappings with the
+    keys packed, scale_codes, nested_absmax, scale_codebook, codebook4
+    (to_device's) and offset.  x: (m, n_in) float16 or bfloat16; ids (m, top_k)
+    int32 and weights (m, top_k) float32: dq4_moe_route's, or another router's.
+    An id outside 0 .. n_experts - 1 stands for no expert; a row of those gives
+    residual, or zeros.  Longer prompts: dq4_gated_fused and dq4_linear_fused,
+    expert by expert.  y may be residual itself.  Returns y (m, n_in)."""
+    torch = _torch()
+    n_ff, n_in, blocksize = _sizes(n_ff, n_in, blocksize)
+    n_experts = int(n_experts)
+    if n_experts < 1:
+        raise ValueError("n_experts must be at least 1")
+    code = _half_code(x.dtype, "x")
+    act = _activation_code(activation, True)
+    n = n_experts * n_ff * n_in
+    device, wg, wu = _gated_weights(gate, up, n, blocksize, int(nested_blocksize))
+    other, wd = _weight_of(**down, n=n, blocksize=blocksize, nested_blocksize=int(nested_blocksize))
+    if other != device:
+        raise ValueError(f"the down weight is on {other}, the gate weight on {device}")
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D")
+    m = x.size(0)
+    ld_x = _matrix(x, "x", m, n_in, x.dtype, device)
+    if ids.dim() != 2 or ids.size(1) < 1:
+        raise ValueError("ids must be (m, top_k)")
+    top_k = ids.size(1)
+    _dense(ids, "ids", (m, top_k), torch.int32, device)
+    _dense(weights, "weights", (m, top_k), torch.float32, device)
+    ld_residual = 0 if residual is None else _matrix(residual, "residual", m, n_in, x.dtype, device)
+    given = y is not None
+    if not given:
+        y = _output((m, n_in), x.dtype, device, stream)
+    ld_y = _matrix(y, "y", m, n_in, x.dtype, device)
+    if given or workspace is not None:
+        in_place = residual is not None and residual.data_ptr() == y.data_ptr() and ld_residual == ld_y
+        _refuse_overlap([("y", y)], [("x", x), ("ids", ids), ("weights", weights),
+                                     ("residual", None if in_place else residual)],
+                        (wg, wu, wd), n, workspace, given)
+    with _on_device(device):
+        _launch_sized("dq4_moe_fused", device, stream, workspace,
+                      library().dq4_moe_fused_workspace_bytes(n_experts, n_ff, n_in, m, top_k),
+                      ctypes.byref(wg), ctypes.byref(wu), ctypes.byref(wd), n_experts, n_ff, n_in, code, act,
+                      x.data_ptr(), m, ld_x, ids.data_ptr(), weights.data_ptr(), top_k, _address(residual),
+                      ld_residual, y.data_ptr(), ld_y)
+    return y
 
 
 def dq4_int8_prep(A, CB, SCB, cols, subA=None, subB=None, stream=None, validate=False):

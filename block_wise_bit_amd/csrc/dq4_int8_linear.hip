@@ -78,38 +78,6 @@ __device__ __forceinline__ int code_of(float x, float up, float s, float inv)
     return static_cast<int>(q);
 }
 
-// Inclusive prefix sum over a wave.
-__device__ __forceinline__ int wave_prefix(int v, int lane)
-{
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-        const int other = __shfl_up(v, d);
-        v += lane >= d ? other : 0;
-    }
-    return v;
-}
-
-// The positions of `count` entries of each of the workgroup's threads in a list:
-// the number before this thread's, and all of them in *total.
-template <int THREADS>
-__device__ __forceinline__ int list_position(int count, int *total, int (&sums)[THREADS / 64])
-{
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int upto = wave_prefix(count, lane);
-    __syncthreads();  // sums may still be read
-    if (lane == 63)
-        sums[wave] = upto;
-    __syncthreads();
-    int before = 0, all = 0;
-#pragma unroll
-    for (int w = 0; w < THREADS / 64; ++w) {
-        before += w < wave ? sums[w] : 0;
-        all += sums[w];
-    }
-    *total = all;
-    return before + upto - count;
-}
-
 // A row of x per workgroup and turn: its scale, then its codes.  A thread holds up
 // to kHeld pieces of 8 elements between the two, the rest is read again.  Bound by
 // memory: 2 bytes read and 1 written per element.

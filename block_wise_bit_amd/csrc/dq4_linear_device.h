@@ -405,6 +405,61 @@ __device__ __forceinline__ void keep_order()
     __builtin_amdgcn_sched_barrier(0);
 }
 
+// Lane l of each quad exchanges register j for lane j's register l.
+__device__ __forceinline__ void transpose_quads(uint32_t (&v)[4], bool odd, bool high)
+{
+    const auto xor1 = [](uint32_t a) {
+        return static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(a), 0xB1, 0xF, 0xF, true));
+    };
+    const auto xor2 = [](uint32_t a) {
+        return static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(a), 0x4E, 0xF, 0xF, true));
+    };
+    // every lane makes every exchange; only then does it choose
+    const uint32_t x0 = xor1(v[0]), x1 = xor1(v[1]), x2 = xor1(v[2]), x3 = xor1(v[3]);
+    const uint32_t a0 = odd ? x1 : v[0], a1 = odd ? v[1] : x0;
+    const uint32_t a2 = odd ? x3 : v[2], a3 = odd ? v[3] : x2;
+    const uint32_t y0 = xor2(a0), y1 = xor2(a1), y2 = xor2(a2), y3 = xor2(a3);
+    v[0] = high ? y2 : a0;
+    v[1] = high ? y3 : a1;
+    v[2] = high ? a2 : y0;
+    v[3] = high ? a3 : y1;
+}
+
+// ---------------------------------------------------------------------------
+// lists
+// ---------------------------------------------------------------------------
+// Inclusive prefix sum over a wave.
+__device__ __forceinline__ int wave_prefix(int v, int lane)
+{
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const int other = __shfl_up(v, d);
+        v += lane >= d ? other : 0;
+    }
+    return v;
+}
+
+// The positions of `count` entries of each of the workgroup's threads in a list:
+// the number before this thread's, and all of them in *total.
+template <int THREADS>
+__device__ __forceinline__ int list_position(int count, int *total, int (&sums)[THREADS / 64])
+{
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int upto = wave_prefix(count, lane);
+    __syncthreads();  // sums may still be read
+    if (lane == 63)
+        sums[wave] = upto;
+    __syncthreads();
+    int before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 64; ++w) {
+        before += w < wave ? sums[w] : 0;
+        all += sums[w];
+    }
+    *total = all;
+    return before + upto - count;
+}
+
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------

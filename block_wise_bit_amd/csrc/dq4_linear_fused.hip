@@ -1619,26 +1619,6 @@ __global__ __launch_bounds__(kThreads) void x_fragments_zero_fill(const uint16_t
     *reinterpret_cast<u32x4 *>(out + (at * 64 + lane) * 8) = q;
 }
 
-// Lane l of each quad exchanges register j for lane j's register l.
-__device__ __forceinline__ void transpose_quads(uint32_t (&v)[4], bool odd, bool high)
-{
-    const auto xor1 = [](uint32_t a) {
-        return static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(a), 0xB1, 0xF, 0xF, true));
-    };
-    const auto xor2 = [](uint32_t a) {
-        return static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(a), 0x4E, 0xF, 0xF, true));
-    };
-    // every lane makes every exchange; only then does it choose
-    const uint32_t x0 = xor1(v[0]), x1 = xor1(v[1]), x2 = xor1(v[2]), x3 = xor1(v[3]);
-    const uint32_t a0 = odd ? x1 : v[0], a1 = odd ? v[1] : x0;
-    const uint32_t a2 = odd ? x3 : v[2], a3 = odd ? v[3] : x2;
-    const uint32_t y0 = xor2(a0), y1 = xor2(a1), y2 = xor2(a2), y3 = xor2(a3);
-    v[0] = high ? y2 : a0;
-    v[1] = high ? y3 : a1;
-    v[2] = high ? a2 : y0;
-    v[3] = high ? a3 : y1;
-}
-
 // 16 TF rows of x against the 4-bit weight, which is read once and never
 // written out.  A wave takes two fragments of 16 weight rows (gated: one of
 // each weight, the same columns) and chunks of 512 k.  The matrix instruction
