@@ -10,10 +10,12 @@
 // weight (16 output columns), B the codes (16 tokens).
 //
 // LDS layout of such a fragment: 1 KiB, 16 rows of 64 bytes, the 16-byte piece p
-// of row r in slot 4 r + (p ^ (r / 4)).  A load takes 64 neighbouring bytes of a
-// row with a quad of lanes straight to LDS, lane l to slot l; of a wave's 16-byte
-// LDS reads the 16 lanes that are served together, one piece of all 16 rows, then
-// lie in 16 different slots of a 256-byte line: no bank conflicts.
+// of row r in slot 4 r + (p ^ turn(r / 4)), turn = 0, 2, 3, 1.  A load takes 64
+// neighbouring bytes of a row with a quad of lanes straight to LDS, lane l to slot
+// l.  Of a wave's 16-byte LDS reads 16 lanes are served together, and they have to
+// lie in 16 different slots of a 256-byte line.  With this turn they do, whether
+// those are 16 lanes in a row or quads of two pieces (with turn(q) = q a product
+// lost 17 % of its cycles to bank conflicts).
 //
 // Up to 64 tokens: int8_rows_kernel, the weight read once.  More:
 // int8_product_kernel, tiles of both operands in LDS.
@@ -290,7 +292,7 @@ struct Int8Args {
     int64_t ld_y;
     int32_t vec;                // bias, residual and y take whole vectors
     int32_t row_blocks;
-    int32_t tiles_t;
+    int32_t tiles_n, tiles_t;
     int32_t splits;             // of the steps of k; above 1 the sums go to `partial`
     i32x4 *partial;             // [split][tile][wave][fragment][16 tokens][lane]
 };
@@ -301,10 +303,21 @@ __device__ __forceinline__ i32x4 mfma_i8(u32x4 a, u32x4 b, i32x4 c)
                                                  __builtin_bit_cast(i32x4, b), c, 0, 0, 0);
 }
 
+__device__ __forceinline__ int turn(int q)
+{
+    return (0x78 >> (2 * q)) & 3;
+}
+
 // Byte of piece `g` of row `r` in a fragment in LDS.
 __device__ __forceinline__ uint32_t piece_at(int r, int g)
 {
-    return static_cast<uint32_t>(4 * r + (g ^ (r >> 2))) * 16;
+    return static_cast<uint32_t>(4 * r + (g ^ turn(r >> 2))) * 16;
+}
+
+// The piece that lane l loads, of row l / 4.
+__device__ __forceinline__ int piece_of(int lane)
+{
+    return (lane & 3) ^ turn(lane >> 4);
 }
 
 // --- outlier columns ---------------------------------------------------------
@@ -480,7 +493,7 @@ __global__ __launch_bounds__(512) void int8_rows_kernel(Int8Args a)
     int l_i = 0;
     [[maybe_unused]] u32x4 rs_w = {}, rs_x = {};
     [[maybe_unused]] uint32_t w_off[R], x_off[TF];
-    [[maybe_unused]] const int piece = (lane & 3) ^ ((lane >> 4) & 3);
+    [[maybe_unused]] const int piece = piece_of(lane);
     [[maybe_unused]] const uint32_t ring0 = lds_offset(ring) + wave * (DEPTH * kFrags * kFragBytes);
     if constexpr (kAligned) {
         rs_x = make_rsrc(a.codes, x_bytes);
@@ -681,21 +694,79 @@ __device__ __forceinline__ void tile_values(const Int8Args &a, const i32x4 *sum,
     }
 }
 
+// The epilogue of one wave's 128 columns x 16 TF tokens.
+template <int OUT, int TF>
+__device__ __forceinline__ void finish_wave(const Int8Args &a, const i32x4 (&acc)[kGroupFrags][TF], float *slab,
+                                            int64_t group, int64_t row0, int lane)
+{
+    const int count = outlier_count(a);
+    const int g = lane >> 4, c = lane & 15;
+    if (group * kGroup >= a.n)
+        return;
+#pragma unroll
+    for (int t = 0; t < TF; ++t) {
+        if (row0 + t * 16 >= a.m)
+            return;
+        f32x4 z[kGroupFrags];
+        tile_values<OUT, kGroupFrags>(a, &acc[0][t], TF, 0, group, row0 + t * 16, count, lane, z);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float *to = slab + c * kFinishLd + 8 * (4 * g + i);
+            *reinterpret_cast<f32x4 *>(to) = f32x4{z[0][i], z[1][i], z[2][i], z[3][i]};
+            *reinterpret_cast<f32x4 *>(to + 4) = f32x4{z[4][i], z[5][i], z[6][i], z[7][i]};
+        }
+        // the wave's LDS operations complete in order; the compiler must not move
+        // the reads of other lanes' values above the writes
+        __asm__ volatile("" ::: "memory");
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll 1
+        for (int it = 0; it < 4; ++it)
+            finish_slab_rows<OUT>(a, slab, row0 + t * 16, group, it, lane);
+        __asm__ volatile("" ::: "memory");
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
 // Tile of 128 WN output columns x 16 TF WT tokens; wave (wn, wt) takes group wn of
-// the tile and 16 TF tokens.  Both operands go from memory straight to LDS, four
-// steps of 64 k in a ring, the step three ahead under way while one is multiplied;
-// one barrier a step.
+// the tile and 16 TF tokens.  Both operands go from memory straight to LDS, 128 k
+// at a time: a load takes whole 128-byte lines of 8 rows, lane l the 16 bytes l % 8
+// of row l / 8 (with 64 bytes of 16 rows each line was fetched twice, and an 8192^3
+// product took 18 % longer).  A chunk is 8 rows of every fragment of the tile; two
+// chunks make 128 k, two steps of matrix instructions, and a ring of five lets each
+// chunk be under way for two steps.  In it the piece p of row r lies in place p ^ (r
+// / 2) of its 128 bytes, for reads without bank conflicts as above.
+//
+// The 256 x 256 tile (WN = 2), 8 waves, has two halves of waves, one of each half
+// on every SIMD, one phase apart: while one multiplies, the other reads its operands
+// of the next step from LDS and issues its loads.  The other tiles have several
+// workgroups per CU instead, and one barrier for 128 k.
+constexpr int kRing = 5;
+
+// Tiles go in bands of kBand columns, row by row: the 32 that an XCD works on at a
+// time are then about as many rows as columns, and its L2 fetches the least (8192^3:
+// see below).
+constexpr int kBand = 4;
+
+__device__ __forceinline__ void place_of(const Int8Args &a, int tile, int *tile_n, int *tile_t)
+{
+    const int band = tile / (kBand * a.tiles_t);
+    const int left = a.tiles_n - band * kBand, width = left < kBand ? left : kBand;
+    const int in = tile - band * (kBand * a.tiles_t);
+    *tile_t = in / width;
+    *tile_n = band * kBand + in - *tile_t * width;
+}
+
 template <int OUT, int WN, int WT, int TF>
 __global__ __launch_bounds__(64 * WN * WT) void int8_product_kernel(Int8Args a)
 {
     constexpr int kWaves = WN * WT;
     constexpr int kRows = 16 * TF * WT;
-    constexpr int kStageFrags = WN * kGroupFrags + TF * WT;
-    constexpr int kStage = kStageFrags * kFragBytes;
-    constexpr int kLoads = kStageFrags / kWaves;
-    static_assert(kLoads * kWaves == kStageFrags, "the waves share the loads evenly");
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * kStage];
-    static_assert(kWaves * 16 * kFinishLd * 4 <= 4 * kStage, "the epilogue slabs fit the stages");
+    constexpr int kTileFrags = WN * kGroupFrags + TF * WT;
+    constexpr int kChunk = kTileFrags * kFragBytes;
+    constexpr int kLoads = kTileFrags / kWaves;
+    static_assert(kLoads * kWaves == kTileFrags, "the waves share the loads evenly");
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[kRing * kChunk];
+    static_assert(kWaves * 16 * kFinishLd * 4 <= kRing * kChunk, "the epilogue slabs fit the ring");
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -707,11 +778,12 @@ __global__ __launch_bounds__(64 * WN * WT) void int8_product_kernel(Int8Args a)
     const int per = tiles / kXcds, extra = tiles % kXcds;
     const int xcd = blockIdx.x % kXcds, idx = blockIdx.x / kXcds;
     const int tile = xcd * per + (xcd < extra ? xcd : extra) + idx;
-    const int tile_n = tile / a.tiles_t, tile_t = tile - tile_n * a.tiles_t;
+    int tile_n, tile_t;
+    place_of(a, tile, &tile_n, &tile_t);
     const int64_t col0 = static_cast<int64_t>(tile_n) * (WN * kGroup);
     const int64_t row0 = static_cast<int64_t>(tile_t) * kRows;
 
-    // this wave's loads of a step: fragments wave * kLoads .. of the weight's, then
+    // this wave's loads of a chunk: fragments wave * kLoads .. of the weight's, then
     // the codes'; rows past the end get an offset past any buffer
     const int64_t cols_left = a.n - col0, rows_left = a.m - row0;
     const int cols_here = static_cast<int>(cols_left < WN * kGroup ? cols_left : WN * kGroup);
@@ -719,35 +791,42 @@ __global__ __launch_bounds__(64 * WN * WT) void int8_product_kernel(Int8Args a)
     const u32x4 rs_w = make_rsrc(a.w + col0 * a.ld_w, static_cast<uint32_t>((cols_here - 1) * a.ld_w + a.k));
     const u32x4 rs_x = make_rsrc(a.codes + row0 * a.ld_codes,
                                  static_cast<uint32_t>((rows_here - 1) * a.ld_codes + a.k));
-    const int piece = (lane & 3) ^ ((lane >> 4) & 3), lr = lane >> 2;
-    uint32_t off[kLoads];
+    uint32_t off[2][kLoads];
+    int from_k[2];
 #pragma unroll
-    for (int q = 0; q < kLoads; ++q) {
-        const int fr = wave * kLoads + q;
-        if (fr < WN * kGroupFrags) {
-            const int row = (fr >> 3) * kGroup + 8 * lr + (fr & 7);
-            off[q] = row < cols_here ? static_cast<uint32_t>(row * a.ld_w) + 16 * piece : kPast;
-        } else {
-            const int row = (fr - WN * kGroupFrags) * 16 + lr;
-            off[q] = row < rows_here ? static_cast<uint32_t>(row * a.ld_codes) + 16 * piece : kPast;
+    for (int h = 0; h < 2; ++h) {
+        const int r = (lane >> 3) + 8 * h;
+        from_k[h] = 16 * ((lane & 7) ^ (r >> 1));
+#pragma unroll
+        for (int q = 0; q < kLoads; ++q) {
+            const int fr = wave * kLoads + q;
+            if (fr < WN * kGroupFrags) {
+                const int row = (fr >> 3) * kGroup + 8 * r + (fr & 7);
+                off[h][q] = row < cols_here ? static_cast<uint32_t>(row * a.ld_w) + from_k[h] : kPast;
+            } else {
+                const int row = (fr - WN * kGroupFrags) * 16 + r;
+                off[h][q] = row < rows_here ? static_cast<uint32_t>(row * a.ld_codes) + from_k[h] : kPast;
+            }
         }
     }
     const uint32_t to0 = lds_offset(lds) + wave * (kLoads * kFragBytes);
 
-    const int steps = (a.k + kStep - 1) / kStep;
+    const int pairs = (a.k + 2 * kStep - 1) / (2 * kStep);
     const int split = blockIdx.y;
-    const int h_first = static_cast<int>(static_cast<uint32_t>(steps * split) / static_cast<uint32_t>(a.splits));
-    const int h_last = static_cast<int>(static_cast<uint32_t>(steps * (split + 1)) / static_cast<uint32_t>(a.splits));
+    const int p_first = static_cast<int>(static_cast<uint32_t>(pairs * split) / static_cast<uint32_t>(a.splits));
+    const int p_last = static_cast<int>(static_cast<uint32_t>(pairs * (split + 1)) / static_cast<uint32_t>(a.splits));
 
-    // always kLoads: past the last step they fetch zeros that nobody reads
-    auto issue = [&](int h) {
-        const uint32_t k0 = static_cast<uint32_t>(h) * kStep;
-        const bool in = h < h_last && k0 + 16 * piece < static_cast<uint32_t>(a.k);
-        const uint32_t to = to0 + (h & 3) * kStage;
+    // always kLoads: past the last chunk they fetch zeros that nobody reads
+    int slot = 0;  // of the next chunk
+    auto issue = [&](int p, int h) {
+        const int k0 = p * (2 * kStep);
+        const bool in = p < p_last && k0 + from_k[h] < a.k;
+        const uint32_t to = to0 + slot * kChunk;
 #pragma unroll
         for (int q = 0; q < kLoads; ++q)
-            buffer_to_lds(wave * kLoads + q < WN * kGroupFrags ? rs_w : rs_x, in ? off[q] + k0 : kPast, 0,
+            buffer_to_lds(wave * kLoads + q < WN * kGroupFrags ? rs_w : rs_x, in ? off[h][q] + k0 : kPast, 0,
                           to + q * kFragBytes);
+        slot = slot + 1 == kRing ? 0 : slot + 1;
     };
 
     i32x4 acc[kGroupFrags][TF];
@@ -757,32 +836,84 @@ __global__ __launch_bounds__(64 * WN * WT) void int8_product_kernel(Int8Args a)
         for (int t = 0; t < TF; ++t)
             acc[f][t] = i32x4{0, 0, 0, 0};
 
-    issue(h_first);
-    issue(h_first + 1);
-    issue(h_first + 2);
-    const uint32_t from = piece_at(lane & 15, lane >> 4);
-    for (int h = h_first; h < h_last; ++h) {
-        // step h has arrived (h + 1 and h + 2 are under way), and this wave's reads
-        // of step h - 1 are done: its place is filled next
-        __asm__ volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(2 * kLoads) : "memory");
-        __builtin_amdgcn_s_barrier();
-        __asm__ volatile("" ::: "memory");
-        const uint8_t *stage = lds + (h & 3) * kStage + from;
-        u32x4 wf[kGroupFrags], xf[TF];
+    // lane 16 g + r reads piece 4 s + g of row r for step s
+    const int r = lane & 15, g = lane >> 4;
+    const uint32_t in_row = (r & 7) * 128;
+    const uint32_t at[2] = {in_row + 16 * (g ^ (r >> 1)), in_row + 16 * ((4 + g) ^ (r >> 1))};
+    int first = 0;  // slot of the pair's first chunk
+    u32x4 wf[kGroupFrags], xf[TF];
+    auto read = [&](int s) {
+        const int second = first + 1 == kRing ? 0 : first + 1;
+        const uint8_t *from = lds + (r < 8 ? first : second) * kChunk + at[s];
 #pragma unroll
         for (int t = 0; t < TF; ++t)
-            xf[t] = *reinterpret_cast<const u32x4 *>(stage + (WN * kGroupFrags + wt * TF + t) * kFragBytes);
+            xf[t] = *reinterpret_cast<const u32x4 *>(from + (WN * kGroupFrags + wt * TF + t) * kFragBytes);
 #pragma unroll
         for (int f = 0; f < kGroupFrags; ++f)
-            wf[f] = *reinterpret_cast<const u32x4 *>(stage + (wn * kGroupFrags + f) * kFragBytes);
-        issue(h + 3);
+            wf[f] = *reinterpret_cast<const u32x4 *>(from + (wn * kGroupFrags + f) * kFragBytes);
+    };
+    auto multiply = [&]() {
 #pragma unroll
         for (int f = 0; f < kGroupFrags; ++f)
 #pragma unroll
             for (int t = 0; t < TF; ++t)
                 acc[f][t] = mfma_i8(wf[f], xf[t], acc[f][t]);
+    };
+
+    issue(p_first, 0);
+    issue(p_first, 1);
+    issue(p_first + 1, 0);
+    if constexpr (WN == 2) {
+        __asm__ volatile("s_waitcnt vmcnt(%0)" ::"n"(kLoads) : "memory");
+        __builtin_amdgcn_s_barrier();
+        if (wave >= kWaves / 2)
+            __builtin_amdgcn_s_barrier();  // the second half is one phase behind
+        for (int p = p_first; p < p_last; ++p) {
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                read(s);
+                // into the places of pair p - 1, which both halves have read
+                if (s == 0)
+                    issue(p + 1, 1);
+                else
+                    issue(p + 2, 0);
+                // this wave's reads are done, and before the next pair its share of
+                // that has arrived (the chunk after it is under way)
+                if (s == 0)
+                    __asm__ volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                else
+                    __asm__ volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(kLoads) : "memory");
+                __builtin_amdgcn_sched_barrier(0);
+                __builtin_amdgcn_s_barrier();
+                __builtin_amdgcn_sched_barrier(0);
+                __builtin_amdgcn_s_setprio(1);
+                multiply();
+                __builtin_amdgcn_s_setprio(0);
+                __builtin_amdgcn_sched_barrier(0);
+                __builtin_amdgcn_s_barrier();
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            first = first + 2 >= kRing ? first + 2 - kRing : first + 2;
+        }
+        if (wave < kWaves / 2)
+            __builtin_amdgcn_s_barrier();
+    } else {
+        for (int p = p_first; p < p_last; ++p) {
+            // the pair has arrived (the chunk after it is under way), and this wave's
+            // reads of the last pair are done: its places are filled next
+            __asm__ volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(kLoads) : "memory");
+            __builtin_amdgcn_s_barrier();
+            __asm__ volatile("" ::: "memory");
+            read(0);
+            issue(p + 1, 1);
+            multiply();
+            read(1);
+            issue(p + 2, 0);
+            multiply();
+            first = first + 2 >= kRing ? first + 2 - kRing : first + 2;
+        }
     }
-    // the epilogue takes the buffers: no load may still be on its way into them
+    // the epilogue takes the ring: no load may still be on its way into it
     __asm__ volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
     __asm__ volatile("" ::: "memory");
@@ -797,35 +928,8 @@ __global__ __launch_bounds__(64 * WN * WT) void int8_product_kernel(Int8Args a)
                 to[(f * TF + t) * 64] = acc[f][t];
         return;
     }
-    const int count = outlier_count(a);
-    float *slab = reinterpret_cast<float *>(lds) + wave * (16 * kFinishLd);
-    const int64_t group = static_cast<int64_t>(tile_n) * WN + wn;
-    const int64_t wave_row0 = row0 + wt * (16 * TF);
-    const int g = lane >> 4, c = lane & 15;
-    if (group * kGroup >= a.n)
-        return;
-#pragma unroll
-    for (int t = 0; t < TF; ++t) {
-        if (wave_row0 + t * 16 >= a.m)
-            return;
-        f32x4 z[kGroupFrags];
-        tile_values<OUT, kGroupFrags>(a, &acc[0][t], TF, 0, group, wave_row0 + t * 16, count, lane, z);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float *to = slab + c * kFinishLd + 8 * (4 * g + i);
-            *reinterpret_cast<f32x4 *>(to) = f32x4{z[0][i], z[1][i], z[2][i], z[3][i]};
-            *reinterpret_cast<f32x4 *>(to + 4) = f32x4{z[4][i], z[5][i], z[6][i], z[7][i]};
-        }
-        // the wave's LDS operations complete in order; the compiler must not move
-        // the reads of other lanes' values above the writes
-        __asm__ volatile("" ::: "memory");
-        __builtin_amdgcn_wave_barrier();
-#pragma unroll 1
-        for (int it = 0; it < 4; ++it)
-            finish_slab_rows<OUT>(a, slab, wave_row0 + t * 16, group, it, lane);
-        __asm__ volatile("" ::: "memory");
-        __builtin_amdgcn_wave_barrier();
-    }
+    finish_wave<OUT, TF>(a, acc, reinterpret_cast<float *>(lds) + wave * (16 * kFinishLd),
+                         static_cast<int64_t>(tile_n) * WN + wn, row0 + wt * (16 * TF), lane);
 }
 
 // The splits' sums of one wave's 128 columns x 16 tokens, and the epilogue.  Four
@@ -838,7 +942,8 @@ __global__ __launch_bounds__(256) void int8_product_reduce_kernel(Int8Args a, in
     const int t = blockIdx.y;
     const int tile = blockIdx.x / (WN * WT), wave = blockIdx.x % (WN * WT);
     const int wn = wave % WN, wt = wave / WN;
-    const int tile_n = tile / a.tiles_t, tile_t = tile - tile_n * a.tiles_t;
+    int tile_n, tile_t;
+    place_of(a, tile, &tile_n, &tile_t);
     const int64_t group = static_cast<int64_t>(tile_n) * WN + wn;
     const int64_t row0 = (static_cast<int64_t>(tile_t) * WT + wt) * (16 * TF) + 16 * t;
     if (group * kGroup >= a.n || row0 >= a.m)
@@ -938,7 +1043,7 @@ bool byte_rows_aligned(const void *p, int64_t ld, int64_t rows, int64_t k)
 constexpr int64_t kRowsMost = 64;  // tokens of int8_rows_kernel
 
 constexpr int kTileCols[3] = {256, 128, 128}, kTileRows[3] = {256, 128, 64};
-constexpr int kTileResident[3] = {1, 2, 3};  // workgroups per CU (LDS)
+constexpr int kTileResident[3] = {1, 2, 2};  // workgroups per CU (LDS)
 // Microseconds of one step of 64 k with every CU full.
 constexpr double kTileStep[3] = {0.9, 0.7, 0.6};
 
@@ -1035,7 +1140,8 @@ template <int OUT, int WN, int WT, int TF>
 dq4_status_t launch_tile(Int8Args a, hipStream_t s)
 {
     a.tiles_t = static_cast<int32_t>(ceil_div(a.m, 16 * TF * WT));
-    const int64_t tiles = ceil_div(a.n, WN * kGroup) * a.tiles_t;
+    a.tiles_n = static_cast<int32_t>(ceil_div(a.n, WN * kGroup));
+    const int64_t tiles = static_cast<int64_t>(a.tiles_n) * a.tiles_t;
     void *params[] = {&a};
     const dq4_status_t st = launch(reinterpret_cast<const void *>(&int8_product_kernel<OUT, WN, WT, TF>), tiles,
                                    a.splits, 64 * WN * WT, params, s);
