@@ -17,7 +17,7 @@
 // those are 16 lanes in a row or quads of two pieces (with turn(q) = q a product
 // lost 17 % of its cycles to bank conflicts).
 //
-// Up to 64 tokens: int8_rows_kernel, the weight read once.  More:
+// Few tokens (up to 32 or 64): int8_rows_kernel, the weight read once.  More:
 // int8_product_kernel, tiles of both operands in LDS.
 
 #include <hip/hip_runtime.h>
@@ -291,7 +291,7 @@ struct Int8Args {
     uint16_t *y;
     int64_t ld_y;
     int32_t vec;                // bias, residual and y take whole vectors
-    int32_t row_blocks;
+    int32_t rows_per, rows_extra;  // weight rows of a workgroup; the first ones take one more
     int32_t tiles_n, tiles_t;
     int32_t splits;             // of the steps of k; above 1 the sums go to `partial`
     i32x4 *partial;             // [split][tile][wave][fragment][16 tokens][lane]
@@ -322,10 +322,12 @@ __device__ __forceinline__ int piece_of(int lane)
 
 // --- outlier columns ---------------------------------------------------------
 // They enter through the 16-bit matrix instruction, on the FP32 value of the
-// integer sum: 32 of them a chunk.  Their operands are gathered once per call
-// into fragments (int8_outlier_fragments_kernel) for the first 128 columns;
-// columns beyond are gathered where they are used, which is slow but needs no
-// memory: at a threshold of 6, models have a few dozen.
+// integer sum: 32 of them a chunk.  With more than 16 tokens their operands are
+// gathered once per call into fragments (int8_outlier_fragments_kernel) for the
+// first 128 columns; with up to 16 the row kernel gathers two chunks itself while
+// it multiplies, and saves the launch.  Columns beyond are gathered where they are
+// used, which is slow but needs no memory: at a threshold of 6, models have a few
+// dozen.
 constexpr int kOutlierChunks = 4;
 
 __device__ __forceinline__ int outlier_count(const Int8Args &a)
@@ -339,44 +341,67 @@ __device__ __forceinline__ int outlier_count(const Int8Args &a)
 template <int OUT>
 constexpr uint32_t kNan = OUT == DQ4_F16 ? 0x7E00u : 0x7FC0u;
 
-// W[n][c_l] for l = l0 .. l0 + 7, zeros past the last column and row.
-template <int OUT>
-__device__ __forceinline__ u32x4 gather_weight(const Int8Args &a, int64_t n, int l0, int count)
+// A lane's 8 columns of a chunk: kNone past the last one, kBad for an index that is
+// no column.  (All loads without branches, so that they are under way together.)
+constexpr int kNone = -1, kBad = -2;
+
+struct Columns {
+    int c[8];
+};
+
+__device__ __forceinline__ Columns load_columns(const Int8Args &a, int l0, int count)
 {
-    u32x4 q = {0, 0, 0, 0};
-    if (n >= a.n)
-        return q;
-    const float s = a.w_scales[n];
+    Columns q;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        if (l0 + j >= count)
-            break;
-        const int c = a.outliers[1 + l0 + j];
-        uint32_t v = kNan<OUT>;
-        if (c >= 0 && c < a.n_in) {
-            const float scaled = static_cast<float>(a.w[n * a.ld_w + c]) * s;
-            v = Half<OUT>::pack2(scaled * kR127, 0.0f) & 0xFFFFu;
-        }
-        q[j / 2] |= v << (16 * (j & 1));
+        const int c = a.outliers[1 + (l0 + j < a.n_in ? l0 + j : a.n_in - 1)];
+        q.c[j] = l0 + j >= count ? kNone : c < 0 || c >= a.n_in ? kBad : c;
     }
     return q;
 }
 
-template <int OUT>
-__device__ __forceinline__ u32x4 gather_x(const Int8Args &a, int64_t t, int l0, int count)
+// The codes W[n][c] is made of, and it; zeros past the last row.
+struct Codes {
+    int8_t b[8];
+    float s;
+};
+
+__device__ __forceinline__ Codes load_codes(const Int8Args &a, int64_t n, const Columns &q)
 {
-    u32x4 q = {0, 0, 0, 0};
-    if (t >= a.m)
-        return q;
+    Codes w;
+    const int64_t row = n < a.n ? n : 0;
+    w.s = a.w_scales[row];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        w.b[j] = a.w[row * a.ld_w + (q.c[j] < 0 ? 0 : q.c[j])];
+    return w;
+}
+
+template <int OUT>
+__device__ __forceinline__ u32x4 weight_fragment(const Int8Args &a, int64_t n, const Columns &q, const Codes &w)
+{
+    uint32_t v[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        if (l0 + j >= count)
-            break;
-        const int c = a.outliers[1 + l0 + j];
-        const uint32_t v = c >= 0 && c < a.n_in ? a.x[t * a.ld_x + c] : kNan<OUT>;
-        q[j / 2] |= v << (16 * (j & 1));
+        const float scaled = static_cast<float>(w.b[j]) * w.s;
+        v[j] = Half<OUT>::pack2(scaled * kR127, 0.0f) & 0xFFFFu;
+        v[j] = q.c[j] == kNone || n >= a.n ? 0u : q.c[j] == kBad ? kNan<OUT> : v[j];
     }
-    return q;
+    return u32x4{v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16};
+}
+
+template <int OUT>
+__device__ __forceinline__ u32x4 x_fragment(const Int8Args &a, int64_t t, const Columns &q)
+{
+    const int64_t row = t < a.m ? t : 0;
+    uint32_t v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        v[j] = a.x[row * a.ld_x + (q.c[j] < 0 ? 0 : q.c[j])];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        v[j] = q.c[j] == kNone || t >= a.m ? 0u : q.c[j] == kBad ? kNan<OUT> : v[j];
+    return u32x4{v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16};
 }
 
 // Row (output column) of lane row r of weight fragment f: kWide as the product's
@@ -387,40 +412,68 @@ __device__ __forceinline__ int64_t fragment_row(int64_t f, int r)
     return kWide ? (f >> 3) * 128 + 8 * r + (f & 7) : f * 16 + r;
 }
 
-// A wave gathers one fragment of 16 rows: of the weight, or of x.
+// A wave gathers one chunk of one fragment of 16 rows: of the weight, or of x.
 template <int OUT, bool kWide>
 __global__ __launch_bounds__(256) void int8_outlier_fragments_kernel(Int8Args a, int64_t w_frags,
                                                                      int64_t x_frags, uint16_t *out)
 {
     const int lane = threadIdx.x & 63;
     const int count = outlier_count(a);
-    for (int64_t f = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6); f < w_frags + x_frags;
-         f += static_cast<int64_t>(gridDim.x) * 4) {
-        for (int c = 0; c < kOutlierChunks && 32 * c < count; ++c) {
-            const int l0 = 32 * c + 8 * (lane >> 4);
-            const u32x4 q = f < w_frags
-                                ? gather_weight<OUT>(a, fragment_row<kWide>(f, lane & 15), l0, count)
-                                : gather_x<OUT>(a, (f - w_frags) * 16 + (lane & 15), l0, count);
-            *reinterpret_cast<u32x4 *>(out + ((f * kOutlierChunks + c) * 64 + lane) * 8) = q;
+    const int chunks = (count + 31) / 32 < kOutlierChunks ? (count + 31) / 32 : kOutlierChunks;
+    const int64_t items = (w_frags + x_frags) * kOutlierChunks;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6); i < items;
+         i += static_cast<int64_t>(gridDim.x) * 4) {
+        const int64_t f = i / kOutlierChunks;
+        const int c = static_cast<int>(i % kOutlierChunks);
+        if (c >= chunks)
+            continue;
+        const Columns q = load_columns(a, 32 * c + 8 * (lane >> 4), count);
+        u32x4 v;
+        if (f < w_frags) {
+            const int64_t n = fragment_row<kWide>(f, lane & 15);
+            v = weight_fragment<OUT>(a, n, q, load_codes(a, n, q));
+        } else {
+            v = x_fragment<OUT>(a, (f - w_frags) * 16 + (lane & 15), q);
         }
+        *reinterpret_cast<u32x4 *>(out + (i * 64 + lane) * 8) = v;
     }
 }
 
-// Chunk c of weight fragment f, or of the x fragment t.
-template <int OUT, bool kWide>
-__device__ __forceinline__ u32x4 weight_outliers(const Int8Args &a, int64_t f, int c, int count, int lane)
+// One column after the other: the tiles' epilogue has no registers for more.
+template <int OUT>
+__device__ __forceinline__ uint32_t weight_value(const Int8Args &a, int64_t n, int c)
 {
-    if (c < kOutlierChunks)
-        return *reinterpret_cast<const u32x4 *>(a.w_outliers + ((f * kOutlierChunks + c) * 64 + lane) * 8);
-    return gather_weight<OUT>(a, fragment_row<kWide>(f, lane & 15), 32 * c + 8 * (lane >> 4), count);
+    if (n >= a.n)
+        return 0;
+    const float scaled = static_cast<float>(a.w[n * a.ld_w + c]) * a.w_scales[n];
+    return Half<OUT>::pack2(scaled * kR127, 0.0f) & 0xFFFFu;
 }
 
 template <int OUT>
-__device__ __forceinline__ u32x4 x_outliers(const Int8Args &a, int64_t t, int c, int count, int lane)
+__device__ __forceinline__ uint32_t x_value(const Int8Args &a, int64_t t, int c)
 {
-    if (c < kOutlierChunks)
-        return *reinterpret_cast<const u32x4 *>(a.x_outliers + ((t * kOutlierChunks + c) * 64 + lane) * 8);
-    return gather_x<OUT>(a, t * 16 + (lane & 15), 32 * c + 8 * (lane >> 4), count);
+    return t < a.m ? a.x[t * a.ld_x + c] : 0u;
+}
+
+template <int OUT, class Value>
+__device__ __forceinline__ u32x4 gather_slowly(const Int8Args &a, int l0, int count, Value value)
+{
+    uint64_t q[2] = {0, 0};
+#pragma unroll 1
+    for (int j = 0; j < 8 && l0 + j < count; ++j) {
+        const int c = a.outliers[1 + l0 + j];
+        const uint64_t v = c < 0 || c >= a.n_in ? kNan<OUT> : value(c);
+        q[0] |= j < 4 ? v << (16 * j) : 0;
+        q[1] |= j < 4 ? 0 : v << (16 * (j - 4));
+    }
+    return u32x4{static_cast<uint32_t>(q[0]), static_cast<uint32_t>(q[0] >> 32), static_cast<uint32_t>(q[1]),
+                 static_cast<uint32_t>(q[1] >> 32)};
+}
+
+// Chunk c of fragment f that int8_outlier_fragments_kernel wrote.
+__device__ __forceinline__ u32x4 held_fragment(const uint16_t *frags, int64_t f, int c, int lane)
+{
+    return *reinterpret_cast<const u32x4 *>(frags + ((f * kOutlierChunks + c) * 64 + lane) * 8);
 }
 
 // --- the epilogue --------------------------------------------------------------
@@ -431,15 +484,15 @@ __device__ __forceinline__ float scaled_sum(int sum, float w_scale, float scale)
     return static_cast<float>(sum) * kR16129 * w_scale * scale;
 }
 
-// Bias, residual and the rounding of N neighbouring outputs.
+// Bias, residual and the rounding of N neighbouring outputs, up to column last - 1.
 template <int OUT, int N>
-__device__ __forceinline__ void finish(const Int8Args &a, int64_t row, int64_t n0, float (&z)[N])
+__device__ __forceinline__ void finish(const Int8Args &a, int64_t row, int64_t n0, int64_t last, float (&z)[N])
 {
-    const int64_t left = a.n - n0;
+    const int64_t left = last - n0;
     if (row >= a.m || left <= 0)
         return;
     const int valid = left < N ? static_cast<int>(left) : N;
-    const bool vec = a.vec && valid == N;
+    const bool vec = a.vec && valid == N && n0 % N == 0;
     float v[N];
     if (a.bias) {
         load_values<OUT, N>(a.bias + n0, vec, valid, v);
@@ -456,18 +509,288 @@ __device__ __forceinline__ void finish(const Int8Args &a, int64_t row, int64_t n
     store_values<OUT, N>(a.y + row * a.ld_y + n0, vec, valid, z);
 }
 
-// --- up to 64 tokens -------------------------------------------------------------
-// 16 TF tokens against row blocks of 16 R weight rows.  The 8 waves split k, steps
-// of 64 in turn; each has a ring of DEPTH steps of both operands in LDS that only
-// it fills and reads, so nothing but the meeting of the sums, integer additions in
-// LDS, needs a barrier, and the next row block's loads are under way across it.
-// Rows that are no multiple of 16 bytes, or not aligned so, take kAligned ==
-// false: dwords into registers, shifted to bytes, and no ring.
-template <int OUT, int TF, int R, int DEPTH, bool kAligned>
+// --- few tokens ----------------------------------------------------------------
+// 16 TF tokens against a workgroup's share of the weight's rows, which is the same
+// for all up to one row, 16 R at a time.  The 8 waves split k, steps
+// of 64 in turn, and each keeps the codes of its steps in registers over all its row
+// blocks (up to XF steps; a memory pipeline that also carried the codes again for
+// every row block took 60 us instead of 42 for 28672 x 8192 with 16 tokens).  A wave
+// has a ring of kUnits fragments in LDS that only it fills and reads, first with
+// codes, then with weight rows, so nothing but the meeting of the sums, integer
+// additions in LDS, needs a barrier, and the next row block's loads are under way
+// across it.
+// XF = 0: k is too long for that, and each step brings its codes along.
+constexpr int kUnits = 16;  // fragments of a wave's ring
+
+// The weight rows of this workgroup.
+struct RowRange {
+    int64_t first, last;
+};
+
+__device__ __forceinline__ RowRange row_range(const Int8Args &a)
+{
+    const int b = blockIdx.x;
+    const int64_t first = static_cast<int64_t>(b) * a.rows_per + (b < a.rows_extra ? b : a.rows_extra);
+    return RowRange{first, first + a.rows_per + (b < a.rows_extra ? 1 : 0)};
+}
+
+// A wave each finishes 16 rows x 16 tokens of the row block from `row0` to `last`,
+// and clears their sums for the row block after the next.
+template <int OUT, int TF, int R, class Gathered>
+__device__ __forceinline__ void finish_rows(const Int8Args &a, int32_t *sum, int64_t row0, int64_t last, int wave,
+                                            int lane, int count, const Gathered &gathered)
+{
+    const int r = lane & 15, g = lane >> 4;
+    if (wave >= R * TF)
+        return;
+    const int f = wave / TF, t = wave - f * TF;
+    i32x4 *at = reinterpret_cast<i32x4 *>(&sum[wave * 256 + r * 16 + 4 * g]);
+    const i32x4 q = *at;
+    *at = i32x4{0, 0, 0, 0};
+    const int64_t n0 = row0 + f * 16 + 4 * g, row = t * 16 + r;
+    const int64_t n = row0 + f * 16 + r;  // the lane's row of the weight's operand
+    const float scale = row < a.m ? a.scales[row] : 0.0f;
+    f32x4 z;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        z[i] = scaled_sum(q[i], n0 + i < last ? a.w_scales[n0 + i] : 0.0f, scale);
+    constexpr int kFirst = Gathered::kChunks;
+    if constexpr (kFirst > 0)
+#pragma unroll
+        for (int c = 0; c < kFirst; ++c)
+            if (32 * c < count)
+                z = Half<OUT>::mfma(weight_fragment<OUT>(a, n, gathered.columns[c], gathered.codes[c]), gathered.x[c], z);
+    for (int c = kFirst; 32 * c < count; ++c) {
+        if (kFirst == 0 && c < kOutlierChunks) {
+            // (rows of any fragment: the workgroup's first row is no multiple of 16)
+            const int64_t held = n < a.n ? n : a.n - 1;
+            z = Half<OUT>::mfma(held_fragment(a.w_outliers, held >> 4, c, 16 * g + static_cast<int>(held & 15)),
+                                held_fragment(a.x_outliers, t, c, lane), z);
+            continue;
+        }
+        const Columns q2 = load_columns(a, 32 * c + 8 * g, count);
+        z = Half<OUT>::mfma(weight_fragment<OUT>(a, n, q2, load_codes(a, n, q2)), x_fragment<OUT>(a, row, q2), z);
+    }
+    float out[4] = {z[0], z[1], z[2], z[3]};
+    finish<OUT, 4>(a, row, n0, last, out);
+}
+
+// Up to 16 tokens: the columns of the first two chunks of outliers and x's operands,
+// by the waves that finish; the weight's codes at the start of a row block.
+template <int OUT, int TF, int R>
+struct Gathered {
+    static constexpr int kChunks = TF == 1 ? 2 : 0;
+    Columns columns[2];
+    u32x4 x[2];
+    Codes codes[2];
+
+    __device__ __forceinline__ void begin(const Int8Args &a, int wave, int lane, int count)
+    {
+        if constexpr (kChunks > 0) {
+            if (wave < R)
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c)
+                    if (32 * c < count) {
+                        columns[c] = load_columns(a, 32 * c + 8 * (lane >> 4), count);
+                        x[c] = x_fragment<OUT>(a, lane & 15, columns[c]);
+                    }
+        }
+    }
+    __device__ __forceinline__ void row_block(const Int8Args &a, int64_t row0, int wave, int lane, int count)
+    {
+        if constexpr (kChunks > 0) {
+            if (wave < R)
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c)
+                    if (32 * c < count)
+                        codes[c] = load_codes(a, row0 + wave * 16 + (lane & 15), columns[c]);
+        }
+    }
+};
+
+// Bytes of rows row0 .. last - 1.
+__device__ __forceinline__ uint32_t weight_bytes(const Int8Args &a, int64_t row0, int64_t last)
+{
+    const int64_t left = (last - row0 - 1) * a.ld_w + a.k;
+    return static_cast<uint32_t>(left < 0x7FFFFFF0 ? left : 0x7FFFFFF0);
+}
+
+template <int R, int TF>
+__device__ __forceinline__ void add_sums(int32_t *sum, const i32x4 (&acc)[R][TF], int lane)
+{
+#pragma unroll
+    for (int f = 0; f < R; ++f)
+#pragma unroll
+        for (int t = 0; t < TF; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                atomicAdd(&sum[(f * TF + t) * 256 + (lane & 15) * 16 + 4 * (lane >> 4) + i], acc[f][t][i]);
+}
+
+template <int OUT, int TF, int R, int XF>
 __global__ __launch_bounds__(512) void int8_rows_kernel(Int8Args a)
 {
+    constexpr int kStepUnits = XF > 0 ? R : R + TF;                    // of the ring
+    constexpr int kSteps = kUnits / kStepUnits;                        // steps that fit it
+    constexpr int kSlots = kSteps * kStepUnits;
+    __shared__ __attribute__((aligned(1024))) uint8_t ring[8 * kSlots * kFragBytes];
+    __shared__ __attribute__((aligned(16))) int32_t sums[2][R * TF * 256];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int steps = (a.k + kStep - 1) / kStep;
+    const int mine = wave < steps ? (steps - wave + 7) / 8 : 0;
+    const int count = outlier_count(a);
+
+    for (int i = tid; i < 2 * R * TF * 256; i += 512)
+        (&sums[0][0])[i] = 0;
+    __syncthreads();
+    Gathered<OUT, TF, R> gathered;
+    gathered.begin(a, wave, lane, count);
+
+    // the loads run ahead of the products: the codes' (XF > 0), then by steps, then by
+    // row blocks; rows past the last one lie past the buffers
+    const int piece = piece_of(lane);
+    const uint32_t ring0 = lds_offset(ring) + wave * (kSlots * kFragBytes);
+    const u32x4 rs_x = make_rsrc(a.codes, static_cast<uint32_t>((a.m - 1) * a.ld_codes + a.k));
+    const RowRange rows = row_range(a);
+    u32x4 rs_w = make_rsrc(a.w + rows.first * a.ld_w, weight_bytes(a, rows.first, rows.last));
+    const uint32_t w_off = static_cast<uint32_t>((lane >> 2) * a.ld_w) + 16 * piece;
+    const auto load_x = [&](int t, int i, int slot) {
+        const int row = 16 * t + (lane >> 2);
+        const uint32_t k0 = static_cast<uint32_t>(wave + 8 * i) * kStep;
+        const bool in = row < a.m && i < mine && k0 + 16 * piece < static_cast<uint32_t>(a.k);
+        buffer_to_lds(rs_x, in ? static_cast<uint32_t>(row * a.ld_codes) + k0 + 16 * piece : kPast, 0,
+                      ring0 + slot * kFragBytes);
+    };
+    int64_t l_row = rows.first;
+    int l_i = 0;
+    // past the last step the loads fetch zeros that nobody reads
+    const auto load_w = [&](int f, int slot) {
+        const uint32_t k0 = static_cast<uint32_t>(wave + 8 * l_i) * kStep;
+        const bool in = l_row < rows.last && k0 + 16 * piece < static_cast<uint32_t>(a.k);
+        u32x4 rs;
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+            rs[d] = __builtin_amdgcn_readfirstlane(rs_w[d]);
+        buffer_to_lds(rs, in ? w_off + f * 16 * static_cast<uint32_t>(a.ld_w) + k0 : kPast, 0,
+                      ring0 + slot * kFragBytes);
+    };
+    const auto next_step = [&]() {
+        if (++l_i == mine) {
+            l_i = 0;
+            l_row += 16 * R;
+            if (l_row < rows.last)
+                rs_w = make_rsrc(a.w + l_row * a.ld_w, weight_bytes(a, l_row, rows.last));
+        }
+    };
+    const auto load_step = [&](int slot) {
+#pragma unroll
+        for (int f = 0; f < R; ++f)
+            load_w(f, slot + f);
+        if constexpr (XF == 0)
+#pragma unroll
+            for (int t = 0; t < TF; ++t)
+                load_x(t, l_row < rows.last ? l_i : mine, slot + R + t);
+        next_step();
+    };
+    const auto at = [&](int slot) {
+        return ring + (wave * kSlots + slot) * kFragBytes + piece_at(lane & 15, lane >> 4);
+    };
+
+    u32x4 x[XF > 0 ? XF : 1][TF];
+    int slot = 0;
+    if (mine > 0) {
+        if constexpr (XF > 0) {
+            // one row of fragments through the ring: the codes' (an even number of
+            // steps, so that the weight's steps lie whole behind them), then the weight's
+            static_assert(kSlots == kUnits && kSlots % R == 0, "a step of the weight is not cut");
+            const int code_steps = (mine + 1) & ~1, codes = code_steps * TF;
+            const auto load_unit = [&](int u) {
+                if (u < codes) {
+                    load_x(u % TF, u / TF, u % kSlots);
+                } else {
+                    const int f = (u - codes) % R;
+                    load_w(f, u % kSlots);
+                    if (f == R - 1)
+                        next_step();
+                }
+            };
+#pragma unroll
+            for (int u = 0; u < kSlots; ++u)
+                load_unit(u);
+#pragma unroll
+            for (int i = 0; i < XF; ++i)
+                if (i < code_steps)
+#pragma unroll
+                    for (int t = 0; t < TF; ++t) {
+                        const int u = i * TF + t;
+                        __asm__ volatile("s_waitcnt vmcnt(%0)" ::"n"(kSlots - 1) : "memory");
+                        x[i][t] = *reinterpret_cast<const u32x4 *>(at(u % kSlots));
+                        __asm__ volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                        __builtin_amdgcn_sched_barrier(0);
+                        load_unit(u + kSlots);
+                    }
+            slot = codes % kSlots;
+        } else {
+#pragma unroll
+            for (int d = 0; d < kSteps; ++d)
+                load_step(d * kStepUnits);
+        }
+    }
+    int parity = 0;
+    for (int64_t row0 = rows.first; row0 < rows.last; row0 += 16 * R, parity ^= 1) {
+        i32x4 acc[R][TF];
+#pragma unroll
+        for (int f = 0; f < R; ++f)
+#pragma unroll
+            for (int t = 0; t < TF; ++t)
+                acc[f][t] = i32x4{0, 0, 0, 0};
+        gathered.row_block(a, row0, wave, lane, count);
+        const auto step = [&](const u32x4 (&held)[TF]) {
+            __asm__ volatile("s_waitcnt vmcnt(%0)" ::"n"((kSteps - 1) * kStepUnits) : "memory");
+            u32x4 wf[R], xf[TF];
+#pragma unroll
+            for (int f = 0; f < R; ++f)
+                wf[f] = *reinterpret_cast<const u32x4 *>(at(slot + f));
+#pragma unroll
+            for (int t = 0; t < TF; ++t)
+                if constexpr (XF > 0)
+                    xf[t] = held[t];
+                else
+                    xf[t] = *reinterpret_cast<const u32x4 *>(at(slot + R + t));
+            // the step's places are read: they may be filled again
+            __asm__ volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            __builtin_amdgcn_sched_barrier(0);
+            load_step(slot);
+            slot = slot + kStepUnits == kSlots ? 0 : slot + kStepUnits;
+#pragma unroll
+            for (int f = 0; f < R; ++f)
+#pragma unroll
+                for (int t = 0; t < TF; ++t)
+                    acc[f][t] = mfma_i8(wf[f], xf[t], acc[f][t]);
+        };
+        if constexpr (XF > 0) {
+#pragma unroll
+            for (int i = 0; i < XF; ++i)
+                if (i < mine)
+                    step(x[i]);
+        } else {
+            for (int i = 0; i < mine; ++i)
+                step(x[0]);
+        }
+        if (mine > 0)
+            add_sums<R, TF>(sums[parity], acc, lane);
+        lds_barrier();
+        finish_rows<OUT, TF, R>(a, sums[parity], row0, rows.last, wave, lane, count, gathered);
+    }
+}
+
+// The same for rows that are no multiple of 16 bytes, or not aligned so: dwords into
+// registers, shifted to bytes, and no ring.
+template <int OUT, int TF, int R>
+__global__ __launch_bounds__(512) void int8_any_rows_kernel(Int8Args a)
+{
     constexpr int kFrags = R + TF;
-    __shared__ __attribute__((aligned(1024))) uint8_t ring[kAligned ? 8 * DEPTH * kFrags * kFragBytes : 16];
     __shared__ __attribute__((aligned(16))) int32_t sums[2][R * TF * 256];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -475,58 +798,17 @@ __global__ __launch_bounds__(512) void int8_rows_kernel(Int8Args a)
     const int steps = (a.k + kStep - 1) / kStep;
     const int mine = wave < steps ? (steps - wave + 7) / 8 : 0;
     const int count = outlier_count(a);
-
-    // codes: one buffer; rows past the last one lie past it
     const uint32_t x_bytes = static_cast<uint32_t>((a.m - 1) * a.ld_codes + a.k);
-    // a row block's weight, from its first row to the weight's end
-    const auto bytes_of = [&](int64_t rb) {
-        const int64_t left = (a.n - rb * (16 * R) - 1) * a.ld_w + a.k;
-        return static_cast<uint32_t>(left < 0x7FFFFFF0 ? left : 0x7FFFFFF0);
-    };
-
     for (int i = tid; i < 2 * R * TF * 256; i += 512)
         (&sums[0][0])[i] = 0;
     __syncthreads();
+    Gathered<OUT, TF, R> gathered;
+    gathered.begin(a, wave, lane, count);
 
-    // the loads run ahead of the products, by steps and then by row blocks
-    int64_t l_rb = blockIdx.x;
-    int l_i = 0;
-    [[maybe_unused]] u32x4 rs_w = {}, rs_x = {};
-    [[maybe_unused]] uint32_t w_off[R], x_off[TF];
-    [[maybe_unused]] const int piece = piece_of(lane);
-    [[maybe_unused]] const uint32_t ring0 = lds_offset(ring) + wave * (DEPTH * kFrags * kFragBytes);
-    if constexpr (kAligned) {
-        rs_x = make_rsrc(a.codes, x_bytes);
-        rs_w = make_rsrc(a.w + l_rb * (16 * R) * a.ld_w, bytes_of(l_rb));
-#pragma unroll
-        for (int f = 0; f < R; ++f)
-            w_off[f] = static_cast<uint32_t>((16 * f + (lane >> 2)) * a.ld_w) + 16 * piece;
-#pragma unroll
-        for (int t = 0; t < TF; ++t) {
-            const int row = 16 * t + (lane >> 2);
-            x_off[t] = row < a.m ? static_cast<uint32_t>(row * a.ld_codes) + 16 * piece : kPast;
-        }
-    }
-    // always kFrags loads: past the last step they fetch zeros that nobody reads
-    auto issue = [&](int slot) {
-        const uint32_t k0 = static_cast<uint32_t>(wave + 8 * l_i) * kStep;
-        const bool in = l_rb < a.row_blocks && k0 + 16 * piece < static_cast<uint32_t>(a.k);
-        const uint32_t to = ring0 + slot * (kFrags * kFragBytes);
-#pragma unroll
-        for (int f = 0; f < R; ++f)
-            buffer_to_lds(rs_w, in ? w_off[f] + k0 : kPast, 0, to + f * kFragBytes);
-#pragma unroll
-        for (int t = 0; t < TF; ++t)
-            buffer_to_lds(rs_x, in ? x_off[t] + k0 : kPast, 0, to + (R + t) * kFragBytes);
-        if (++l_i == mine) {
-            l_i = 0;
-            l_rb += gridDim.x;
-            if (l_rb < a.row_blocks)
-                rs_w = make_rsrc(a.w + l_rb * (16 * R) * a.ld_w, bytes_of(l_rb));
-        }
-    };
+    const RowRange rows = row_range(a);
+
     // 16 bytes at any address: 5 dwords, those past the buffer are zeros
-    [[maybe_unused]] auto load_bytes = [&](__amdgpu_buffer_rsrc_t rsrc, uint32_t at, int left) {
+    const auto load_bytes = [&](__amdgpu_buffer_rsrc_t rsrc, uint32_t at, int left) {
         const u32x4 lo = __builtin_amdgcn_raw_buffer_load_b128(rsrc, at & ~3u, 0, 0);
         const uint32_t hi = __builtin_amdgcn_raw_buffer_load_b32(rsrc, (at & ~3u) + 16, 0, 0);
         u32x4 q;
@@ -538,114 +820,57 @@ __global__ __launch_bounds__(512) void int8_rows_kernel(Int8Args a)
         }
         return q;
     };
-
-    int slot = 0, parity = 0;
-    if constexpr (kAligned) {
-        if (mine > 0)
-#pragma unroll
-            for (int d = 0; d < DEPTH; ++d)
-                issue(d);
-    }
-    for (int64_t rb = blockIdx.x; rb < a.row_blocks; rb += gridDim.x, parity ^= 1) {
+    int parity = 0;
+    for (int64_t row0 = rows.first; row0 < rows.last; row0 += 16 * R, parity ^= 1) {
         i32x4 acc[R][TF];
 #pragma unroll
         for (int f = 0; f < R; ++f)
 #pragma unroll
             for (int t = 0; t < TF; ++t)
                 acc[f][t] = i32x4{0, 0, 0, 0};
-        if constexpr (kAligned) {
-            for (int i = 0; i < mine; ++i) {
-                __asm__ volatile("s_waitcnt vmcnt(%0)" ::"n"((DEPTH - 1) * kFrags) : "memory");
-                const uint8_t *from = ring + (wave * DEPTH + slot) * (kFrags * kFragBytes) + piece_at(r, g);
-                u32x4 q[kFrags];
+        gathered.row_block(a, row0, wave, lane, count);
+        const uintptr_t w_at = reinterpret_cast<uintptr_t>(a.w + row0 * a.ld_w);
+        const uintptr_t x_at = reinterpret_cast<uintptr_t>(a.codes);
+        const uint32_t w_skew = w_at & 3, x_skew = x_at & 3;
+        // whole dwords, up to the one with the last byte
+        const auto rw = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void *>(w_at - w_skew), 0,
+                                                          (weight_bytes(a, row0, rows.last) + w_skew + 3) & ~3u, kRawBufferWord3);
+        const auto rx = __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void *>(x_at - x_skew), 0,
+                                                          (x_bytes + x_skew + 3) & ~3u, kRawBufferWord3);
+        const int64_t rows_left = rows.last - row0;
+        const auto load = [&](u32x4 (&q)[kFrags], int i) {
+            const int k0 = (wave + 8 * i) * kStep + 16 * g;
+            const int left = i < mine ? a.k - k0 : 0;  // bytes of the row from here on
 #pragma unroll
-                for (int f = 0; f < kFrags; ++f)
-                    q[f] = *reinterpret_cast<const u32x4 *>(from + f * kFragBytes);
-                // the slot is read: it may be filled again
-                __asm__ volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-                __builtin_amdgcn_sched_barrier(0);
-                issue(slot);
-                slot = slot + 1 == DEPTH ? 0 : slot + 1;
-#pragma unroll
-                for (int f = 0; f < R; ++f)
-#pragma unroll
-                    for (int t = 0; t < TF; ++t)
-                        acc[f][t] = mfma_i8(q[f], q[R + t], acc[f][t]);
+            for (int f = 0; f < R; ++f) {
+                const int row = 16 * f + r;
+                q[f] = load_bytes(rw, left > 0 && row < rows_left
+                                          ? static_cast<uint32_t>(row * a.ld_w) + k0 + w_skew : kPast, left);
             }
-        } else {
-            const uintptr_t w_at = reinterpret_cast<uintptr_t>(a.w + rb * (16 * R) * a.ld_w);
-            const uintptr_t x_at = reinterpret_cast<uintptr_t>(a.codes);
-            const uint32_t w_skew = w_at & 3, x_skew = x_at & 3;
-            // whole dwords, up to the one with the last byte
-            const auto rw = __builtin_amdgcn_make_buffer_rsrc(
-                reinterpret_cast<void *>(w_at - w_skew), 0, (bytes_of(rb) + w_skew + 3) & ~3u, kRawBufferWord3);
-            const auto rx = __builtin_amdgcn_make_buffer_rsrc(
-                reinterpret_cast<void *>(x_at - x_skew), 0, (x_bytes + x_skew + 3) & ~3u, kRawBufferWord3);
-            const int64_t rows_left = a.n - rb * (16 * R);
-            auto load = [&](u32x4 (&q)[kFrags], int i) {
-                const int k0 = (wave + 8 * i) * kStep + 16 * g;
-                const int left = i < mine ? a.k - k0 : 0;  // bytes of the row from here on
 #pragma unroll
-                for (int f = 0; f < R; ++f) {
-                    const int row = 16 * f + r;
-                    q[f] = load_bytes(rw, left > 0 && row < rows_left
-                                              ? static_cast<uint32_t>(row * a.ld_w) + k0 + w_skew : kPast, left);
-                }
-#pragma unroll
-                for (int t = 0; t < TF; ++t) {
-                    const int row = 16 * t + r;
-                    q[R + t] = load_bytes(rx, left > 0 && row < a.m
-                                                  ? static_cast<uint32_t>(row * a.ld_codes) + k0 + x_skew : kPast, left);
-                }
-            };
-            u32x4 now[kFrags], next[kFrags];
-            load(now, 0);
-            for (int i = 0; i < mine; ++i) {
-                load(next, i + 1);
-#pragma unroll
-                for (int f = 0; f < R; ++f)
-#pragma unroll
-                    for (int t = 0; t < TF; ++t)
-                        acc[f][t] = mfma_i8(now[f], now[R + t], acc[f][t]);
-#pragma unroll
-                for (int f = 0; f < kFrags; ++f)
-                    now[f] = next[f];
+            for (int t = 0; t < TF; ++t) {
+                const int row = 16 * t + r;
+                q[R + t] = load_bytes(rx, left > 0 && row < a.m
+                                              ? static_cast<uint32_t>(row * a.ld_codes) + k0 + x_skew : kPast, left);
             }
-        }
-        int32_t *sum = sums[parity];
-        if (mine > 0) {
+        };
+        u32x4 now[kFrags], next[kFrags];
+        load(now, 0);
+        for (int i = 0; i < mine; ++i) {
+            load(next, i + 1);
 #pragma unroll
             for (int f = 0; f < R; ++f)
 #pragma unroll
                 for (int t = 0; t < TF; ++t)
+                    acc[f][t] = mfma_i8(now[f], now[R + t], acc[f][t]);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        atomicAdd(&sum[(f * TF + t) * 256 + r * 16 + 4 * g + i], acc[f][t][i]);
+            for (int f = 0; f < kFrags; ++f)
+                now[f] = next[f];
         }
+        if (mine > 0)
+            add_sums<R, TF>(sums[parity], acc, lane);
         lds_barrier();
-        // a wave each finishes 16 rows x 16 tokens, and clears their sums for the
-        // row block after the next
-#pragma unroll
-        for (int p0 = 0; p0 < R * TF; p0 += 8) {
-            const int p = p0 + wave;
-            if (p >= R * TF)
-                break;
-            const int f = p / TF, t = p - f * TF;
-            i32x4 *at = reinterpret_cast<i32x4 *>(&sum[p * 256 + r * 16 + 4 * g]);
-            const i32x4 q = *at;
-            *at = i32x4{0, 0, 0, 0};
-            const int64_t n0 = rb * (16 * R) + f * 16 + 4 * g, row = t * 16 + r;
-            const float scale = row < a.m ? a.scales[row] : 0.0f;
-            f32x4 z;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                z[i] = scaled_sum(q[i], n0 + i < a.n ? a.w_scales[n0 + i] : 0.0f, scale);
-            for (int c = 0; 32 * c < count; ++c)
-                z = Half<OUT>::mfma(weight_outliers<OUT, false>(a, rb * R + f, c, count, lane),
-                                    x_outliers<OUT>(a, t, c, count, lane), z);
-            float out[4] = {z[0], z[1], z[2], z[3]};
-            finish<OUT, 4>(a, row, n0, out);
-        }
+        finish_rows<OUT, TF, R>(a, sums[parity], row0, rows.last, wave, lane, count, gathered);
     }
 }
 
@@ -665,7 +890,7 @@ __device__ __forceinline__ void finish_slab_rows(const Int8Args &a, const float 
     const f32x4 lo = *reinterpret_cast<const f32x4 *>(from);
     const f32x4 hi = *reinterpret_cast<const f32x4 *>(from + 4);
     float z[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-    finish<OUT, 8>(a, row0 + it * 4 + g, group * kGroup + 8 * c, z);
+    finish<OUT, 8>(a, row0 + it * 4 + g, group * kGroup + 8 * c, a.n, z);
 }
 
 // FP32 values of fragments F0 .. F0 + N - 1 of a group and 16 tokens, outliers
@@ -685,12 +910,22 @@ __device__ __forceinline__ void tile_values(const Int8Args &a, const i32x4 *sum,
             const int64_t n = group * kGroup + 8 * (4 * g + i) + f0 + f;
             z[f][i] = scaled_sum(sum[f * stride][i], n < a.n ? a.w_scales[n] : 0.0f, scale);
         }
-    for (int c = 0; 32 * c < count; ++c) {
-        const u32x4 xf = x_outliers<OUT>(a, row0 >> 4, c, count, lane);
+    for (int c = 0; c < kOutlierChunks && 32 * c < count; ++c) {
+        const u32x4 xf = held_fragment(a.x_outliers, row0 >> 4, c, lane);
 #pragma unroll
         for (int f = 0; f < N; ++f)
-            z[f] = Half<OUT>::mfma(weight_outliers<OUT, true>(a, group * kGroupFrags + f0 + f, c, count, lane), xf,
-                                   z[f]);
+            z[f] = Half<OUT>::mfma(held_fragment(a.w_outliers, group * kGroupFrags + f0 + f, c, lane), xf, z[f]);
+    }
+#pragma unroll 1
+    for (int c = kOutlierChunks; 32 * c < count; ++c) {
+        const int l0 = 32 * c + 8 * g;
+        const u32x4 xf = gather_slowly<OUT>(a, l0, count, [&](int column) { return x_value<OUT>(a, row, column); });
+#pragma unroll
+        for (int f = 0; f < N; ++f) {
+            const int64_t n = fragment_row<true>(group * kGroupFrags + f0 + f, lane & 15);
+            const u32x4 wf = gather_slowly<OUT>(a, l0, count, [&](int column) { return weight_value<OUT>(a, n, column); });
+            z[f] = Half<OUT>::mfma(wf, xf, z[f]);
+        }
     }
 }
 
@@ -978,13 +1213,20 @@ __global__ __launch_bounds__(256) void int8_product_reduce_kernel(Int8Args a, in
 
 // Rows of bytes, any alignment and stride, into rows of ld_out bytes (a multiple of
 // 16) with zeros behind column k.
-__global__ __launch_bounds__(256) void int8_rows_zero_fill(const int8_t *in, int64_t ld_in, int64_t rows,
-                                                           int32_t k, int8_t *out, int32_t ld_out)
+struct CopyArgs {
+    const int8_t *in;
+    int64_t ld_in, rows;
+    int8_t *out;
+};
+
+__global__ __launch_bounds__(256) void int8_rows_zero_fill(CopyArgs a, CopyArgs b, int32_t k, int32_t ld_out)
 {
     const int words = ld_out / 4;
-    for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
-        const int8_t *from = in + row * ld_in;
-        uint32_t *to = reinterpret_cast<uint32_t *>(out + row * ld_out);
+    for (int64_t item = blockIdx.x; item < a.rows + b.rows; item += gridDim.x) {
+        const bool first = item < a.rows;
+        const int64_t row = first ? item : item - a.rows;
+        const int8_t *from = first ? a.in + row * a.ld_in : b.in + row * b.ld_in;
+        uint32_t *to = reinterpret_cast<uint32_t *>((first ? a.out : b.out) + row * ld_out);
         for (int c = threadIdx.x; c < words; c += 256) {
             uint32_t q = 0;
 #pragma unroll
@@ -1040,12 +1282,23 @@ bool byte_rows_aligned(const void *p, int64_t ld, int64_t rows, int64_t k)
            (rows <= 1 || (ld % 16 == 0 && ld <= kMaxStride));
 }
 
-constexpr int64_t kRowsMost = 64;  // tokens of int8_rows_kernel
+// Tokens of the row kernels, and of their form that gathers outliers itself.
+constexpr int64_t kRowsMost = 64, kGatheredMost = 16;
+
+// Whether a call takes a row kernel.  With more than 32 tokens and more than 4096 k
+// a wave's codes do not fit its registers, and the tiles are faster (64 tokens, us,
+// rows | tiles: 28672 x 8192 83 | 69, 4096 x 14336 23.1 | 19.8; 4096 x 4096 11.3 |
+// 14.6; 32 tokens, 28672 x 8192: 53 | 67), unless they had to copy the weight first.
+bool takes_rows(int64_t m, int64_t k, bool aligned)
+{
+    return m <= kRowsMost && (m <= 32 || k <= 4096 || !aligned);
+}
 
 constexpr int kTileCols[3] = {256, 128, 128}, kTileRows[3] = {256, 128, 64};
 constexpr int kTileResident[3] = {1, 2, 2};  // workgroups per CU (LDS)
-// Microseconds of one step of 64 k with every CU full.
-constexpr double kTileStep[3] = {0.9, 0.7, 0.6};
+// Microseconds of one step of 64 k with every CU full, as measured at 8192^3 (438,
+// 565 and 755 us).
+constexpr double kTileStep[3] = {0.86, 0.55, 0.37};
 
 struct Plan {
     int tile, splits;
@@ -1064,8 +1317,8 @@ Plan plan_of(int64_t m, int64_t n, int64_t k, int cus)
             const int64_t rounds = ceil_div(tiles * splits, static_cast<int64_t>(cus) * kTileResident[tile]);
             double cost = static_cast<double>(rounds) *
                           (static_cast<double>(ceil_div(steps, splits)) * kTileStep[tile] + 3.0);
-            if (splits > 1)  // the partial sums, written and read at about 4 TB/s, and a launch
-                cost += 3.0 + static_cast<double>(splits) * static_cast<double>(m) * static_cast<double>(n) * 8.0 / 4e6;
+            if (splits > 1)  // the partial sums, written and read at about 8 TB/s (cache), and a launch
+                cost += 3.0 + static_cast<double>(splits) * static_cast<double>(m) * static_cast<double>(n) * 8.0 / 8e6;
             if (cost < best.cost)
                 best = Plan{tile, splits, cost};
         }
@@ -1097,7 +1350,7 @@ Layout layout_of(const void *codes, int64_t m, int64_t ld_codes, const void *w, 
                  bool outliers, int cus)
 {
     Layout l{};
-    l.rows = m <= kRowsMost;
+    l.rows = takes_rows(m, k, byte_rows_aligned(codes, ld_codes, m, k) && byte_rows_aligned(w, k, n, k));
     l.copy_codes = l.rows ? m > 1 && ld_codes > kMaxStride : !byte_rows_aligned(codes, ld_codes, m, k);
     l.copy_weight = !l.rows && !byte_rows_aligned(w, k, n, k);
     l.ld_copy = ceil_div(k, kStep) * kStep;
@@ -1107,33 +1360,46 @@ Layout layout_of(const void *codes, int64_t m, int64_t ld_codes, const void *w, 
         l.plan = plan_of(m, n, k, cus);
         l.partial = partial_bytes(l.plan, m, n);
     }
-    if (outliers && k > 0) {
+    if (outliers && k > 0 && m > kGatheredMost) {
         l.w_frags = l.rows ? ceil_div(n, 16) : ceil_div(n, kGroup) * kGroupFrags;
         l.x_frags = ceil_div(m, 16);
     }
     return l;
 }
 
-template <int OUT, int TF, int R, int DEPTH>
+template <int OUT, int TF, int R>
 dq4_status_t launch_rows_tile(Int8Args a, bool aligned, int cus, hipStream_t s)
 {
-    a.row_blocks = static_cast<int32_t>(ceil_div(a.n, 16 * R));
+    const int64_t grid = ceil_div(a.n, 16) < cus ? ceil_div(a.n, 16) : cus;
+    a.rows_per = static_cast<int32_t>(a.n / grid);
+    a.rows_extra = static_cast<int32_t>(a.n % grid);
+    // codes are kept where there is more than one row block to keep them for (16
+    // tokens, 4096 x 14336, one row block: 16.4 us kept, 13.3 not)
+    const bool keep = a.n > grid * (16 * R);
+    const int64_t steps = ceil_div(ceil_div(a.k, kStep), 8);  // of a wave
+    const void *kernel = reinterpret_cast<const void *>(&int8_rows_kernel<OUT, TF, R, 0>);
+    if (!aligned)
+        kernel = reinterpret_cast<const void *>(&int8_any_rows_kernel<OUT, TF, R>);
+    else if (keep && steps <= 8)
+        kernel = reinterpret_cast<const void *>(&int8_rows_kernel<OUT, TF, R, 8>);
+    else if (keep && steps <= 16 && TF <= 2)
+        kernel = reinterpret_cast<const void *>(&int8_rows_kernel<OUT, TF, R, TF <= 2 ? 16 : 8>);
+    else if (keep && steps <= 32 && TF == 1)
+        kernel = reinterpret_cast<const void *>(&int8_rows_kernel<OUT, TF, R, TF == 1 ? 32 : 8>);
     void *params[] = {&a};
-    const void *kernel = aligned ? reinterpret_cast<const void *>(&int8_rows_kernel<OUT, TF, R, DEPTH, true>)
-                                 : reinterpret_cast<const void *>(&int8_rows_kernel<OUT, TF, R, DEPTH, false>);
-    return launch(kernel, a.row_blocks < cus ? a.row_blocks : cus, 1, 512, params, s);
+    return launch(kernel, grid, 1, 512, params, s);
 }
 
 template <int OUT>
 dq4_status_t launch_rows(const Int8Args &a, int cus, hipStream_t s)
 {
     const bool aligned = byte_rows_aligned(a.codes, a.ld_codes, a.m, a.k) && byte_rows_aligned(a.w, a.ld_w, a.n, a.k);
-    const bool two = ceil_div(a.n, 32) >= cus;
+    const bool two = a.n > static_cast<int64_t>(16) * cus;  // more than 16 rows a workgroup
     if (a.m <= 16)
-        return two ? launch_rows_tile<OUT, 1, 2, 6>(a, aligned, cus, s) : launch_rows_tile<OUT, 1, 1, 8>(a, aligned, cus, s);
+        return two ? launch_rows_tile<OUT, 1, 2>(a, aligned, cus, s) : launch_rows_tile<OUT, 1, 1>(a, aligned, cus, s);
     if (a.m <= 32)
-        return two ? launch_rows_tile<OUT, 2, 2, 4>(a, aligned, cus, s) : launch_rows_tile<OUT, 2, 1, 6>(a, aligned, cus, s);
-    return two ? launch_rows_tile<OUT, 4, 2, 3>(a, aligned, cus, s) : launch_rows_tile<OUT, 4, 1, 3>(a, aligned, cus, s);
+        return two ? launch_rows_tile<OUT, 2, 2>(a, aligned, cus, s) : launch_rows_tile<OUT, 2, 1>(a, aligned, cus, s);
+    return two ? launch_rows_tile<OUT, 4, 2>(a, aligned, cus, s) : launch_rows_tile<OUT, 4, 1>(a, aligned, cus, s);
 }
 
 template <int OUT, int WN, int WT, int TF>
@@ -1153,39 +1419,35 @@ dq4_status_t launch_tile(Int8Args a, hipStream_t s)
                   256, rp, s);
 }
 
-dq4_status_t copy_rows(const int8_t *in, int64_t ld_in, int64_t rows, int64_t k, uint8_t *out, int64_t ld_out,
-                       int cus, hipStream_t s)
-{
-    int32_t k32 = static_cast<int32_t>(k), ld32 = static_cast<int32_t>(ld_out);
-    void *params[] = {&in, &ld_in, &rows, &k32, &out, &ld32};
-    const int64_t grid = rows < cus * 8 ? rows : cus * 8;
-    return launch(reinterpret_cast<const void *>(&int8_rows_zero_fill), grid, 1, 256, params, s);
-}
-
 template <int OUT>
 dq4_status_t run_linear(Int8Args a, const Layout &l, uint8_t *ws, int cus, hipStream_t s)
 {
     dq4_status_t st = DQ4_OK;
-    if (l.copy_codes && a.k > 0) {
-        st = copy_rows(a.codes, a.ld_codes, a.m, a.k, ws, l.ld_copy, cus, s);
+    if ((l.copy_codes || l.copy_weight) && a.k > 0) {
+        CopyArgs codes{}, weight{};
+        if (l.copy_codes) {
+            codes = CopyArgs{a.codes, a.ld_codes, a.m, reinterpret_cast<int8_t *>(ws)};
+            a.codes = codes.out;
+            a.ld_codes = l.ld_copy;
+        }
+        if (l.copy_weight) {
+            weight = CopyArgs{a.w, a.ld_w, a.n, reinterpret_cast<int8_t *>(ws + l.codes_bytes)};
+            a.w = weight.out;
+            a.ld_w = l.ld_copy;
+        }
+        int32_t k = a.k, ld = static_cast<int32_t>(l.ld_copy);
+        void *params[] = {&codes, &weight, &k, &ld};
+        const int64_t rows = codes.rows + weight.rows;
+        st = launch(reinterpret_cast<const void *>(&int8_rows_zero_fill), rows < cus * 8 ? rows : cus * 8, 1, 256,
+                    params, s);
         if (st != DQ4_OK)
             return st;
-        a.codes = reinterpret_cast<const int8_t *>(ws);
-        a.ld_codes = l.ld_copy;
-    }
-    if (l.copy_weight && a.k > 0) {
-        uint8_t *to = ws + l.codes_bytes;
-        st = copy_rows(a.w, a.ld_w, a.n, a.k, to, l.ld_copy, cus, s);
-        if (st != DQ4_OK)
-            return st;
-        a.w = reinterpret_cast<const int8_t *>(to);
-        a.ld_w = l.ld_copy;
     }
     uint16_t *frags = reinterpret_cast<uint16_t *>(ws + l.codes_bytes + l.weight_bytes);
     if (l.w_frags > 0) {
         int64_t w_frags = l.w_frags, x_frags = l.x_frags;
         void *params[] = {&a, &w_frags, &x_frags, &frags};
-        const int64_t groups = ceil_div(w_frags + x_frags, 4);
+        const int64_t groups = w_frags + x_frags;  // (four chunks each)
         const void *kernel = l.rows ? reinterpret_cast<const void *>(&int8_outlier_fragments_kernel<OUT, false>)
                                     : reinterpret_cast<const void *>(&int8_outlier_fragments_kernel<OUT, true>);
         st = launch(kernel, groups < cus * 8 ? groups : cus * 8, 1, 256, params, s);
@@ -1193,8 +1455,6 @@ dq4_status_t run_linear(Int8Args a, const Layout &l, uint8_t *ws, int cus, hipSt
             return st;
         a.w_outliers = frags;
         a.x_outliers = frags + w_frags * kOutlierChunks * (kFragBytes / 2);
-    } else {
-        a.outliers = nullptr;
     }
     if (l.rows)
         return launch_rows<OUT>(a, cus, s);
@@ -1325,7 +1585,7 @@ dq4_status_t dq4_int8_linear(const int8_t *codes, int64_t m, int64_t ld_codes, c
     a.k = a.n_in = static_cast<int32_t>(n_in);
     a.x = static_cast<const uint16_t *>(x);
     a.ld_x = ld_x;
-    a.outliers = outliers;
+    a.outliers = n_in > 0 ? outliers : nullptr;
     a.bias = static_cast<const uint16_t *>(bias);
     a.residual = static_cast<const uint16_t *>(residual);
     a.ld_residual = ld_residual;

@@ -50,7 +50,7 @@ def test_linear_validation(lib):
     for k in (dict(m=-1), dict(n=-1), dict(k=-1), dict(dtype=0), dict(dtype=9), dict(codes=None), dict(scales=None),
               dict(CB=None), dict(SCB=None), dict(y=None), dict(x=ONE), dict(outliers=ONE), dict(ld_codes=63),
               dict(ld_y=31), dict(residual=ONE, ld_r=31), dict(x=ONE, outliers=ONE, ld_x=63), dict(ws=P(16)),
-              dict(ws=None), dict(x=ONE, outliers=ONE, ws_bytes=0), dict(ws_bytes=-1), dict(ld_y=1 << 62)):
+              dict(ws=None), dict(m=20, x=ONE, outliers=ONE, ws_bytes=0), dict(ws_bytes=-1), dict(ld_y=1 << 62)):
         assert call(**k) == dq4.DQ4_EINVAL, k
     for k in (dict(k=1 << 17, ld_codes=1 << 17), dict(n=(1 << 21) + 1, ld_y=1 << 22), dict(m=(1 << 21) + 1),
               dict(m=1 << 20, n=1 << 20, ld_y=1 << 20)):
@@ -79,7 +79,9 @@ def test_workspace_sizes(lib):
     # a few tokens: the weight is read where it lies, whatever its alignment
     assert linear(ONE, 64, 4096, ONE, 4096, 4096, 0) == 0
     assert linear(P(1), 64, 4095, P(3), 4095, 4095, 0) == 0
-    # outlier operands of 128 columns
+    assert linear(P(1), 64, 8000, P(3), 4095, 8000, 0) == 0
+    # outlier operands of 128 columns; up to 16 tokens are gathered in the product
+    assert linear(ONE, 16, 4096, ONE, 4096, 4096, 1) == 0
     assert linear(ONE, 64, 4096, ONE, 4096, 4096, 1) == (4096 + 64) * 256
     # tiles: rows that are no multiple of 16 bytes take padded copies
     dense = linear(ONE, 2048, 4096, ONE, 4096, 4096, 0)
