@@ -161,7 +161,8 @@ struct Pass {
 };
 
 struct MoeArgs {
-    Weight w[3];             // gate, up, down
+    Weight w[2];             // gate, up
+    Weight down;
     int32_t log2_block, log2_down;
     int32_t n_experts, top_k;
     int64_t n_ff, n_in, m;
@@ -315,6 +316,25 @@ struct RowBlock {
     int rows;
 };
 
+// One weight matrix and where a chunk of its rows begins.
+struct Source {
+    Weight w;
+    int log2_block;
+    int64_t n_elems;
+    uint32_t n;  // row length
+};
+
+// (field by field: an array or a choice of structs would pass through memory)
+__device__ __forceinline__ Weight either(const Weight &a, const Weight &b, int second)
+{
+    return Weight{second ? b.packed : a.packed,
+                  second ? b.scale_codes : a.scale_codes,
+                  second ? b.nested_absmax : a.nested_absmax,
+                  second ? b.scale_codebook : a.scale_codebook,
+                  second ? b.codebook4 : a.codebook4,
+                  second ? b.offset : a.offset};
+}
+
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_from(const void *p, int64_t bytes)
 {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0,
@@ -322,60 +342,91 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_from(const void *p, int
                                              kRawBufferWord3);
 }
 
+// The buffers of a row block, and the place of its first element in them.
+struct Buffers {
+    __amdgpu_buffer_rsrc_t packed, codes, absmax;
+    uint32_t nibble0;      // of the first element in `packed`, which starts at a dword
+    uint32_t phase;        // elements of the first block before it
+    uint32_t group_phase;  // blocks of the first group before that block
+};
+
+__device__ __forceinline__ Buffers buffers_of(const Source &s, const RowBlock &b)
+{
+    const int64_t e0 = b.row0 * s.n, b0 = e0 >> s.log2_block;
+    const int64_t blocks = (s.n_elems + (int64_t{1} << s.log2_block) - 1) >> s.log2_block;
+    const uintptr_t at = reinterpret_cast<uintptr_t>(s.w.packed) + (e0 >> 1);
+    const uint32_t skew = static_cast<uint32_t>(at & 3);
+    Buffers q;
+    // whole dwords, up to the one with the last byte
+    q.packed = buffer_from(reinterpret_cast<const void *>(at - skew),
+                           (((s.n_elems + 1) >> 1) - (e0 >> 1) + skew + 3) & ~int64_t{3});
+    q.codes = buffer_from(s.w.scale_codes + b0, blocks - b0);
+    q.absmax = buffer_from(s.w.nested_absmax + (b0 >> kNestedLog2),
+                           (((blocks + 255) >> kNestedLog2) - (b0 >> kNestedLog2)) * 4);
+    q.nibble0 = 2 * skew + (static_cast<uint32_t>(e0) & 1);
+    q.phase = static_cast<uint32_t>(e0) & ((1u << s.log2_block) - 1);
+    q.group_phase = static_cast<uint32_t>(b0) & 255;
+    return q;
+}
+
+__device__ __forceinline__ void load_scale(const Buffers &q, uint32_t block, bool in, uint32_t *code, float *absmax)
+{
+    *code = __builtin_amdgcn_raw_buffer_load_b8(q.codes, in ? block : 0x80000000u, 0, 0);
+    *absmax = __builtin_bit_cast(
+        float, __builtin_amdgcn_raw_buffer_load_b32(
+                   q.absmax, in ? ((q.group_phase + block) >> kNestedLog2) * 4 : 0x80000000u, 0, 0));
+}
+
 // Row lengths that are multiples of 32, packed codes at 4-byte boundaries.  A load
 // takes 256 bytes of 4 rows, a quad of lanes on 64 of them; 4 such loads are
 // transposed between the lanes of each quad; the scales, S blocks per 128 k, are
 // looked up four lanes to a row and handed over.  S = 2: blocks of 64 k or more and
-// row lengths that are multiples of 64; else S = 4.
+// row lengths that are multiples of 64; else S = 4.  The next chunk's loads are
+// issued as this one's registers come free.
 template <int OUT, int S>
 struct EvenRows {
-    static constexpr bool kAhead = true;  // the registers hold the next chunk's loads
+    static constexpr bool kEven = true;
     u32x4 packed[4];
     uint32_t code[S];
     float absmax[S];
-    uint32_t from[4];
-    float s[4];
+    float s[S];
 
-    __device__ __forceinline__ void load(const Weight &w, int lb, int64_t n_elems, const RowBlock &b,
-                                         uint32_t n, int c, int lane)
+    __device__ __forceinline__ void load_scales(const Source &w, const RowBlock &b, int c, int lane)
     {
-        const int64_t e0 = b.row0 * n, b0 = e0 >> lb;
-        const uint32_t phase = static_cast<uint32_t>(e0) & ((1u << lb) - 1);
-        const uint32_t group_phase = static_cast<uint32_t>(b0) & 255;
-        const int64_t blocks = (n_elems + (int64_t{1} << lb) - 1) >> lb;
-        const auto rp = buffer_from(w.packed + (e0 >> 1), ((n_elems + 1) >> 1) - (e0 >> 1));
-        const auto rc = buffer_from(w.scale_codes + b0, blocks - b0);
-        const auto rm = buffer_from(w.nested_absmax + (b0 >> kNestedLog2),
-                                    (((blocks + 255) >> kNestedLog2) - (b0 >> kNestedLog2)) * 4);
-        const uint32_t k = c * kSpan + 32 * (((lane >> 4) << 2) | (lane & 3));
-        const int row = 4 * ((lane >> 2) & 3);
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-            packed[q] = __builtin_amdgcn_raw_buffer_load_b128(
-                rp, k < n && row + q < b.rows ? ((row + q) * n + k) >> 1 : 0x80000000u, 0, 0);
+        const Buffers q = buffers_of(w, b);
 #pragma unroll
         for (int h = 0; h < S; ++h) {
-            const uint32_t e = (lane >> 2) * n + c * kSpan + 128 * (lane & 3) + h * (128 / S);
-            const uint32_t blk = (phase + e) >> lb;
-            code[h] = __builtin_amdgcn_raw_buffer_load_b8(rc, blk, 0, 0);
-            absmax[h] = __builtin_bit_cast(
-                float, __builtin_amdgcn_raw_buffer_load_b32(rm, ((group_phase + blk) >> kNestedLog2) * 4, 0, 0));
+            const uint32_t e = (lane >> 2) * w.n + c * kSpan + 128 * (lane & 3) + h * (128 / S);
+            load_scale(q, (q.phase + e) >> w.log2_block, true, &code[h], &absmax[h]);
         }
     }
 
-    // `zeros`: the table's row of zeros, which a piece beyond the row or the last
-    // row (its load gave zeros) reads, times 0.
-    __device__ __forceinline__ void prepare(const float *scb, float offset, const RowBlock &b, uint32_t n, int c,
-                                            uint32_t lane_byte, int lane)
+    __device__ __forceinline__ void load_packed(int i, const Source &w, const RowBlock &b, int c, int lane)
+    {
+        const Buffers q = buffers_of(w, b);
+        const uint32_t k = c * kSpan + 32 * (((lane >> 4) << 2) | (lane & 3));
+        const int row = 4 * ((lane >> 2) & 3) + i;
+        packed[i] = __builtin_amdgcn_raw_buffer_load_b128(
+            q.packed, k < w.n && row < b.rows ? ((row * w.n + k) >> 1) + (q.nibble0 >> 1) : 0x80000000u, 0, 0);
+    }
+
+    __device__ __forceinline__ void load(const Source &w, const RowBlock &b, int c, int lane)
+    {
+        load_scales(w, b, c, lane);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            load_packed(i, w, b, c, lane);
+    }
+
+    __device__ __forceinline__ void prepare(const float *scb, float offset, int lane)
     {
         const int g = lane >> 4, r = lane & 15;
-        float given[S];
 #pragma unroll
         for (int h = 0; h < S; ++h) {
             const float q = block_scale(scb[code[h]], absmax[h], offset);
             // lane 16 g + r multiplies quarter g of row r
-            given[h] = __builtin_bit_cast(float, __builtin_amdgcn_ds_bpermute((4 * r + g) * 4,
-                                                                              __builtin_bit_cast(int, q)));
+            s[h] = __builtin_bit_cast(float, __builtin_amdgcn_ds_bpermute((4 * r + g) * 4,
+                                                                          __builtin_bit_cast(int, q)));
         }
 #pragma unroll
         for (int d = 0; d < 4; ++d) {
@@ -385,100 +436,73 @@ struct EvenRows {
             for (int j = 0; j < 4; ++j)
                 packed[j][d] = v[j];
         }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const bool beyond = c * kSpan + 128 * g + 32 * j >= n || r >= b.rows;
-            from[j] = beyond ? lane_byte | kPairTableBytes : lane_byte;
-            s[j] = beyond ? 0.0f : given[j * S / 4];
-        }
     }
 
-    __device__ __forceinline__ Pairs look(const uint8_t *table, int step) const
+    // A piece beyond the row or the last row: its load gave zeros; it reads the
+    // table's row of zeros, times 0.
+    static __device__ __forceinline__ bool beyond(const Source &w, const RowBlock &b, int c, int j, int lane)
     {
-        return lookup_dword(packed[step / 4][step % 4], table, from[step / 4]);
+        return c * kSpan + 128 * (lane >> 4) + 32 * j >= static_cast<int>(w.n) || (lane & 15) >= b.rows;
     }
 
-    __device__ __forceinline__ u32x4 operand(const Pairs &p, int step) const
+    __device__ __forceinline__ Pairs look(const uint8_t *table, uint32_t lane_byte, bool beyond, int step) const
     {
-        return scaled_dword<OUT>(p, s[step / 4]);
+        return lookup_dword(packed[step / 4][step % 4], table, beyond ? lane_byte | kPairTableBytes : lane_byte);
+    }
+
+    __device__ __forceinline__ u32x4 operand(const Pairs &p, bool beyond, int step) const
+    {
+        return scaled_dword<OUT>(p, beyond ? 0.0f : s[step / 4 * S / 4]);
     }
 };
 
-// Any row length and alignment: a lane takes its own row's 32 k, five dwords that
-// are shifted to its first nibble.  Blocks are at least 32 elements long, so a
-// piece meets at most two; each element picks its scale.  Dwords are read up to the
-// one with the last byte.
+// Any row length and alignment: a lane takes its own row's 32 k at a time, five
+// dwords that are shifted to their first nibble.  Blocks are at least 32 elements
+// long, so a piece meets at most two; each element picks its scale.
 template <int OUT>
 struct AnyRows {
-    static constexpr bool kAhead = false;
-    u32x4 lo[4];
-    uint32_t hi[4];
-    uint32_t code[4][2];
-    float absmax[4][2];
+    static constexpr bool kEven = false;
+    u32x4 lo;
+    uint32_t hi;
+    uint32_t code[2];
+    float absmax[2];
     uint32_t shift;
-    int meet[4], valid[4];
-    float s[4][2];
-    uint32_t from;
+    int meet, valid;
+    float s[2];
 
-    __device__ __forceinline__ void load(const Weight &w, int lb, int64_t n_elems, const RowBlock &b, uint32_t n,
-                                         int c, int lane)
+    __device__ __forceinline__ void load(const Source &w, const RowBlock &b, int c, int j, int lane)
     {
-        const int64_t e0 = b.row0 * n, b0 = e0 >> lb;
-        const uint32_t phase = static_cast<uint32_t>(e0) & ((1u << lb) - 1);
-        const uint32_t group_phase = static_cast<uint32_t>(b0) & 255;
-        const int64_t blocks = (n_elems + (int64_t{1} << lb) - 1) >> lb;
-        const uintptr_t at = reinterpret_cast<uintptr_t>(w.packed) + (e0 >> 1);
-        const uint32_t skew = static_cast<uint32_t>(at & 3);
-        const auto rp = buffer_from(reinterpret_cast<const void *>(at - skew),
-                                    (((n_elems + 1) >> 1) - (e0 >> 1) + skew + 3) & ~int64_t{3});
-        const auto rc = buffer_from(w.scale_codes + b0, blocks - b0);
-        const auto rm = buffer_from(w.nested_absmax + (b0 >> kNestedLog2),
-                                    (((blocks + 255) >> kNestedLog2) - (b0 >> kNestedLog2)) * 4);
+        const Buffers q = buffers_of(w, b);
         const int r = lane & 15;
-        const uint32_t nibble0 = 2 * skew + (static_cast<uint32_t>(e0) & 1);
+        const uint32_t k = c * kSpan + 128 * (lane >> 4) + 32 * j;
+        const int left = r < b.rows ? static_cast<int>(w.n) - static_cast<int>(k) : 0;
+        valid = left < 0 ? 0 : left > 32 ? 32 : left;
+        const uint32_t e = r * w.n + k, nibble = q.nibble0 + e;
+        shift = 4 * (nibble & 7);
+        const uint32_t word = valid > 0 ? (nibble >> 3) * 4 : 0x80000000u;
+        lo = __builtin_amdgcn_raw_buffer_load_b128(q.packed, word, 0, 0);
+        hi = __builtin_amdgcn_raw_buffer_load_b32(q.packed, word + 16, 0, 0);
+        const uint32_t block = (q.phase + e) >> w.log2_block;
+        meet = static_cast<int>(((block + 1) << w.log2_block) - q.phase - e);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint32_t k = c * kSpan + 128 * (lane >> 4) + 32 * j;
-            const int left = r < b.rows ? static_cast<int>(n) - static_cast<int>(k) : 0;
-            valid[j] = left < 0 ? 0 : left > 32 ? 32 : left;
-            const uint32_t e = r * n + k;
-            const uint32_t nibble = nibble0 + e;
-            shift = 4 * (nibble & 7);  // the same for all j
-            const uint32_t word = valid[j] > 0 ? (nibble >> 3) * 4 : 0x80000000u;
-            lo[j] = __builtin_amdgcn_raw_buffer_load_b128(rp, word, 0, 0);
-            hi[j] = __builtin_amdgcn_raw_buffer_load_b32(rp, word + 16, 0, 0);
-            const uint32_t blk = (phase + e) >> lb;
-            meet[j] = static_cast<int>(((blk + 1) << lb) - phase - e);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                code[j][h] = __builtin_amdgcn_raw_buffer_load_b8(rc, valid[j] > 0 ? blk + h : 0x80000000u, 0, 0);
-                absmax[j][h] = __builtin_bit_cast(
-                    float, __builtin_amdgcn_raw_buffer_load_b32(
-                               rm, valid[j] > 0 ? ((group_phase + blk + h) >> kNestedLog2) * 4 : 0x80000000u, 0, 0));
-            }
-        }
+        for (int h = 0; h < 2; ++h)
+            load_scale(q, block + h, valid > 0, &code[h], &absmax[h]);
     }
 
-    __device__ __forceinline__ void prepare(const float *scb, float offset, const RowBlock &, uint32_t, int,
-                                            uint32_t lane_byte, int)
+    __device__ __forceinline__ void prepare(const float *scb, float offset)
     {
-        from = lane_byte;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                s[j][h] = block_scale(scb[code[j][h]], absmax[j][h], offset);
+        for (int h = 0; h < 2; ++h)
+            s[h] = block_scale(scb[code[h]], absmax[h], offset);
     }
 
-    __device__ __forceinline__ Pairs look(const uint8_t *table, int step) const
+    __device__ __forceinline__ Pairs look(const uint8_t *table, uint32_t lane_byte, int d) const
     {
-        const int j = step / 4, d = step % 4;
-        return lookup_dword(__builtin_amdgcn_alignbit(d < 3 ? lo[j][d + 1] : hi[j], lo[j][d], shift), table, from);
+        return lookup_dword(__builtin_amdgcn_alignbit(d < 3 ? lo[d + 1] : hi, lo[d], shift), table, lane_byte);
     }
 
-    __device__ __forceinline__ u32x4 operand(const Pairs &p, int step) const
+    __device__ __forceinline__ u32x4 operand(const Pairs &p, int d) const
     {
-        const int j = step / 4, d = step % 4;
         u32x4 q;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -486,8 +510,8 @@ struct AnyRows {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int at = 8 * d + 2 * i + h;
-                const float z = p.v[i][h] * (at < meet[j] ? s[j][0] : s[j][1]);
-                v[h] = at < valid[j] ? z : 0.0f;
+                const float z = p.v[i][h] * (at < meet ? s[0] : s[1]);
+                v[h] = at < valid ? z : 0.0f;
             }
             q[i] = Half<OUT>::pack2(v[0], v[1]);
         }
@@ -495,154 +519,259 @@ struct AnyRows {
     }
 };
 
+// The other operand: fragments of TF tiles, in operand order; or (kOne) the one
+// token's row, in the lanes of column 0.
+template <int TF, bool kOne>
+struct Columns {
+    const uint16_t *at[TF];
+    __amdgpu_buffer_rsrc_t row;
+    uint32_t k_lane;
+
+    __device__ __forceinline__ u32x4 load(int t, int step) const
+    {
+        if constexpr (kOne)
+            return __builtin_amdgcn_raw_buffer_load_b128(row, k_lane + 16 * step, 0, 0);
+        else
+            return *reinterpret_cast<const u32x4 *>(at[t] + step * 512);
+    }
+};
+
+// What a wave holds of a row block: an even one's chunk, or two pieces in turn.
+template <class Rows>
+struct Held {
+    Rows r[Rows::kEven ? 1 : 2];
+
+    __device__ __forceinline__ void load_first(const Source &src, const RowBlock &rows, int c, int lane)
+    {
+        if constexpr (Rows::kEven)
+            r[0].load(src, rows, c, lane);
+        else
+            r[0].load(src, rows, c, 0, lane);
+    }
+};
+
+// acc[t] += 16 weight rows x a chunk of 512 k x TF tiles.  `next`: where the wave's
+// next chunk lies (the same again after the last one: unused).  Lookups run one step
+// ahead.
+template <int OUT, class Rows, int TF, bool kOne>
+__device__ __forceinline__ void multiply_chunk(Held<Rows> &held, const Source &src, const RowBlock &rows, int c,
+                                               const RowBlock &next, int next_c, const float *scb,
+                                               const uint8_t *table, uint32_t lane_byte,
+                                               const Columns<TF, kOne> &x, f32x4 (&acc)[TF], int lane)
+{
+    constexpr int kAhead = 4;
+    u32x4 xf[kAhead][TF];
+#pragma unroll
+    for (int st = 0; st < kAhead; ++st)
+#pragma unroll
+        for (int t = 0; t < TF; ++t)
+            xf[st][t] = x.load(t, st);
+    Rows ahead;
+    if constexpr (Rows::kEven)
+        held.r[0].prepare(scb, src.w.offset, lane);
+    Pairs now{}, then{};
+#pragma unroll
+    for (int st = 0; st < 16; ++st) {
+        u32x4 wf;
+        if constexpr (Rows::kEven) {
+            const bool beyond = Rows::beyond(src, rows, c, st / 4, lane);
+            if (st == 0)
+                now = held.r[0].look(table, lane_byte, beyond, 0);
+            if (st < 15)
+                then = held.r[0].look(table, lane_byte, Rows::beyond(src, rows, c, (st + 1) / 4, lane), st + 1);
+            keep_order();
+            wf = held.r[0].operand(now, beyond, st);
+            // the next chunk's loads, as registers come free
+            if (st == 0)
+                ahead.load_scales(src, next, next_c, lane);
+            if (st == 1 || st == 3 || st == 7)
+                ahead.load_packed(st == 1 ? 0 : st == 3 ? 1 : 2, src, next, next_c, lane);
+            if (st == 7)
+                ahead.load_packed(3, src, next, next_c, lane);
+        } else {
+            const int j = st / 4, d = st % 4;
+            if (d == 0) {
+                held.r[j & 1].prepare(scb, src.w.offset);
+                if (j < 3)
+                    held.r[(j + 1) & 1].load(src, rows, c, j + 1, lane);
+                else
+                    held.r[0].load(src, next, next_c, 0, lane);
+                now = held.r[j & 1].look(table, lane_byte, 0);
+            }
+            if (d < 3)
+                then = held.r[j & 1].look(table, lane_byte, d + 1);
+            keep_order();
+            wf = held.r[j & 1].operand(now, d);
+        }
+#pragma unroll
+        for (int t = 0; t < TF; ++t)
+            acc[t] = Half<OUT>::mfma(wf, xf[st % kAhead][t], acc[t]);
+        now = then;
+        if (st + kAhead < 16)
+#pragma unroll
+            for (int t = 0; t < TF; ++t)
+                xf[st % kAhead][t] = x.load(t, st + kAhead);
+    }
+    if constexpr (Rows::kEven)
+        held.r[0] = ahead;
+}
+
+// A single token's plan: its valid experts, each once, in the order of its row.
+struct OnePlan {
+    int n;
+    int expert[kMaxTopK];
+    float share[kMaxTopK];
+};
+
+__device__ __forceinline__ void plan_one(const MoeArgs &a, OnePlan &p)
+{
+    const int lane = threadIdx.x;
+    if (lane >= 64)
+        return;
+    const bool in = lane < a.top_k;
+    const int e = in ? a.ids[lane] : -1;
+    const float w = in ? a.weights[lane] : 0.0f;
+    bool first = e >= 0 && e < a.n_experts;
+    float share = w;
+#pragma unroll
+    for (int j = 0; j < kMaxTopK; ++j) {
+        const int other = __shfl(e, j);
+        const float more = __shfl(w, j);
+        first = first && !(j < lane && other == e);
+        share = j > lane && other == e ? share + more : share;
+    }
+    const uint64_t mask = __ballot(first);
+    if (first) {
+        const int at = __builtin_popcountll(mask & ((uint64_t{1} << lane) - 1));
+        p.expert[at] = e;
+        p.share[at] = share;
+    }
+    if (lane == 0)
+        p.n = __builtin_popcountll(mask);
+}
+
 // ---------------------------------------------------------------------------
 // gate and up
 // ---------------------------------------------------------------------------
-// An item is a unit's row block: 16 rows of the expert's gate and the same of its
-// up matrix.  The 8 waves take its chunks in turn, their sums meet in LDS in a
-// fixed order, and h goes out in the down product's operand order.  The next
-// chunk's weight, also that of the next item, is in flight while one is
-// multiplied.
-template <int OUT, class Rows, int TF>
-__global__ __launch_bounds__(512) void moe_gate_up_kernel(MoeArgs a)
+// An item is a pass's row block: 16 rows of the expert's gate and the same of its up
+// matrix.  `wk` waves for each of both take its chunks in turn, and a workgroup takes
+// as many items at a time as it has such groups of waves; a group's sums meet in LDS
+// in a fixed order, and h goes out in the down product's operand order.  The next
+// chunk's weight, also that of the next item, is in flight while one is multiplied.
+// (A wave for each matrix: 16 waves hold one matrix's chunk and the next, and with
+// four waves a SIMD lookups, vector instructions and loads overlap; a wave for both
+// left room for 8 waves.)
+template <int OUT, class Rows, int TF, bool kOne, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void moe_gate_up_kernel(MoeArgs a, int32_t wk_waves)
 {
     __shared__ __attribute__((aligned(1024))) uint8_t table[kPairTableBytes + 256];
     __shared__ float scb[2][256], cb4[2][16];
-    __shared__ __attribute__((aligned(16))) f32x4 partial[8][2 * TF][64];
+    __shared__ __attribute__((aligned(16))) f32x4 partial[WAVES][TF][64];
+    __shared__ OnePlan one;
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const uint32_t n = static_cast<uint32_t>(a.n_in);
+    const int WK = wk_waves, WR = WAVES / (2 * WK);
+    const int which = wave & 1, wk = (wave >> 1) % WK, wr = wave / (2 * WK);
     const int n_ff = static_cast<int>(a.n_ff);
     const int chunks = chunks_of(a.n_in), h_chunks = chunks_of(a.n_ff);
     const int row_blocks = (n_ff + 15) >> 4;
     const int64_t n_elems = static_cast<int64_t>(a.n_experts) * a.n_ff * a.n_in;
-    const Weight pair[2] = {a.w[0], a.w[1]};
+    const Source src = {either(a.w[0], a.w[1], which), a.log2_block, n_elems, static_cast<uint32_t>(a.n_in)};
 
-    const Codebooks codebooks = fetch_codebooks<2>(pair);
-    const int items = *a.n_units * row_blocks;
-    int next_item = blockIdx.x, next_c = wave;
-    Pass unit{}, next_unit{};
+    const Codebooks codebooks = fetch_codebooks<2>(a.w);
+    int n_passes;
+    if constexpr (kOne) {
+        plan_one(a, one);
+        __syncthreads();
+        n_passes = one.n;
+    } else {
+        n_passes = *a.n_units;
+    }
+    const int items = n_passes * row_blocks;
+    const int step = gridDim.x * WR;
+    int next_item = blockIdx.x * WR + wr, next_c = wk;
+    Pass pass{}, next_pass{};
     RowBlock rows{}, next_rows{};
     const auto enter = [&](int item) {
         const int u = item / row_blocks;
-        next_unit = a.units[u];
+        if constexpr (kOne)
+            next_pass = Pass{one.expert[u], 0, u, 1};
+        else
+            next_pass = a.units[u];
         const int row = (item - u * row_blocks) * 16;
-        next_rows = RowBlock{static_cast<int64_t>(next_unit.expert) * n_ff + row, n_ff - row < 16 ? n_ff - row : 16};
+        next_rows = RowBlock{static_cast<int64_t>(next_pass.expert) * n_ff + row, n_ff - row < 16 ? n_ff - row : 16};
     };
-    Rows cur[2], next[2];
-    const bool some = wave < chunks;
+    Held<Rows> held;
     if (next_item < items) {
         enter(next_item);
-        if (some && Rows::kAhead)
-#pragma unroll
-            for (int f = 0; f < 2; ++f)
-                next[f].load(a.w[f], a.log2_block, n_elems, next_rows, n, next_c, lane);
+        held.load_first(src, next_rows, next_c, lane);
     }
     fill_tables<2, 1>(codebooks, table, scb, cb4);
-    const uint32_t lane_byte = (lane & 15) * 16;
+    const uint32_t lane_byte = (lane & 15) * 16 + which * 8;
 
-    for (int item = blockIdx.x; item < items; item += gridDim.x) {
-        unit = next_unit;
+    for (int item0 = blockIdx.x * WR; item0 < items; item0 += step) {
+        const int item = item0 + wr;
+        pass = next_pass;
         rows = next_rows;
-        f32x4 acc[2][TF];
+        f32x4 acc[TF];
 #pragma unroll
-        for (int f = 0; f < 2; ++f)
+        for (int t = 0; t < TF; ++t)
+            acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        if (item < items)
+            for (int c = wk; c < chunks; c += WK) {  // wk < chunks
+                next_c += WK;
+                if (next_c >= chunks) {
+                    next_c = wk;
+                    next_item += step;
+                    if (next_item < items)
+                        enter(next_item);
+                }
+                Columns<TF, kOne> x;
+                if constexpr (kOne) {
+                    x.row = buffer_from(a.x, a.n_in * 2);
+                    x.k_lane = (lane & 15) == 0 ? (c * kSpan + 128 * (lane >> 4)) * 2 : 0x80000000u;
+                } else {
+#pragma unroll
+                    for (int t = 0; t < TF; ++t)  // past the pass's last tile: that again, unused
+                        x.at[t] = a.x_frags +
+                                  (static_cast<int64_t>(pass.x_tile + (t < pass.tiles ? t : pass.tiles - 1)) * chunks +
+                                   c) * kTileChunk + lane * 8;
+                }
+                multiply_chunk<OUT, Rows, TF, kOne>(held, src, rows, c, next_rows, next_c, scb[which], table, lane_byte,
+                                                    x, acc, lane);
+            }
+        lds_barrier();  // the last items' sums are read
+        if (item < items)
 #pragma unroll
             for (int t = 0; t < TF; ++t)
-                acc[f][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        for (int c = wave; c < chunks; c += 8) {
-#pragma unroll
-            for (int f = 0; f < 2; ++f) {
-                if constexpr (Rows::kAhead)
-                    cur[f] = next[f];
-                else
-                    cur[f].load(a.w[f], a.log2_block, n_elems, rows, n, c, lane);
-            }
-            next_c += 8;
-            if (next_c >= chunks) {
-                next_c = wave;
-                next_item += gridDim.x;
-                if (next_item < items)
-                    enter(next_item);
-            }
-            // past the last item: the last one's again, unused
-            if constexpr (Rows::kAhead)
-#pragma unroll
-                for (int f = 0; f < 2; ++f)
-                    next[f].load(a.w[f], a.log2_block, n_elems, next_rows, n, next_c, lane);
-#pragma unroll
-            for (int f = 0; f < 2; ++f)
-                cur[f].prepare(scb[f], a.w[f].offset, rows, n, c, lane_byte, lane);
-            const uint16_t *x[TF];
-#pragma unroll
-            for (int t = 0; t < TF; ++t)  // past the unit's last tile: that again, unused
-                x[t] = a.x_frags +
-                       (static_cast<int64_t>(unit.x_tile + (t < unit.tiles ? t : unit.tiles - 1)) * chunks + c) *
-                           kTileChunk + lane * 8;
-            constexpr int kAhead = 4;
-            u32x4 xf[kAhead][TF];
-#pragma unroll
-            for (int st = 0; st < kAhead; ++st)
-#pragma unroll
-                for (int t = 0; t < TF; ++t)
-                    xf[st][t] = *reinterpret_cast<const u32x4 *>(x[t] + st * 512);
-            Pairs now[2], then[2];
-#pragma unroll
-            for (int f = 0; f < 2; ++f)
-                now[f] = cur[f].look(table + f * 8, 0);
-#pragma unroll
-            for (int st = 0; st < 16; ++st) {
-                if (st < 15)
-#pragma unroll
-                    for (int f = 0; f < 2; ++f)
-                        then[f] = cur[f].look(table + f * 8, st + 1);
-                keep_order();
-#pragma unroll
-                for (int f = 0; f < 2; ++f) {
-                    const u32x4 wf = cur[f].operand(now[f], st);
-#pragma unroll
-                    for (int t = 0; t < TF; ++t)
-                        acc[f][t] = Half<OUT>::mfma(wf, xf[st % kAhead][t], acc[f][t]);
-                    now[f] = then[f];
-                }
-                if (st + kAhead < 16)
-#pragma unroll
-                    for (int t = 0; t < TF; ++t)
-                        xf[st % kAhead][t] = *reinterpret_cast<const u32x4 *>(x[t] + (st + kAhead) * 512);
-            }
-        }
-        if (!some) {  // this wave has no chunk: it follows the items all the same
-            next_item += gridDim.x;
-            if (next_item < items)
-                enter(next_item);
-        }
-        lds_barrier();  // the last item's sums are read
-        if (some)
-#pragma unroll
-            for (int f = 0; f < 2; ++f)
-#pragma unroll
-                for (int t = 0; t < TF; ++t)
-                    partial[wave][f * TF + t][lane] = acc[f][t];
+                partial[wave][t][lane] = acc[t];
         lds_barrier();
-        const int live = chunks < 8 ? chunks : 8;
-        if (wave < unit.tiles) {  // a wave finishes one tile
-            const int t = wave;
-            f32x4 gate = {0.0f, 0.0f, 0.0f, 0.0f}, up = {0.0f, 0.0f, 0.0f, 0.0f};
-            for (int q = 0; q < live; ++q) {
-                gate = gate + partial[q][t][lane];
-                up = up + partial[q][TF + t][lane];
-            }
-            // the lane's four neighbouring k of h, column lane % 16
-            const int k = (item - item / row_blocks * row_blocks) * 16 + 4 * (lane >> 4);
-            float h[4];
+        if (item < items) {  // a wave of the group finishes a tile
+            for (int t = wave - wr * (2 * WK); t < pass.tiles; t += 2 * WK) {
+                f32x4 gate = {0.0f, 0.0f, 0.0f, 0.0f}, up = {0.0f, 0.0f, 0.0f, 0.0f};
+                for (int q = wr * (2 * WK); q < (wr + 1) * (2 * WK); q += 2) {
+                    gate = gate + partial[q][t][lane];
+                    up = up + partial[q + 1][t][lane];
+                }
+                // the lane's four neighbouring k of h, column lane % 16
+                const int k = (item - item / row_blocks * row_blocks) * 16 + 4 * (lane >> 4);
+                float h[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                h[i] = k + i < n_ff ? act_f32(a.act, gate[i]) * up[i] : 0.0f;
-            const int ch = k / kSpan, in = k % kSpan;
-            uint16_t *to = a.h_frags + (static_cast<int64_t>(unit.h_tile + t) * h_chunks + ch) * kTileChunk +
-                           (((in & 127) >> 3) * 64 + (in >> 7) * 16 + (lane & 15)) * 8 + (in & 7);
-            *reinterpret_cast<u32x2 *>(to) = u32x2{Half<OUT>::pack2(h[0], h[1]), Half<OUT>::pack2(h[2], h[3])};
+                for (int i = 0; i < 4; ++i)
+                    h[i] = k + i < n_ff ? act_f32(a.act, gate[i]) * up[i] : 0.0f;
+                const u32x2 out = {Half<OUT>::pack2(h[0], h[1]), Half<OUT>::pack2(h[2], h[3])};
+                if constexpr (kOne) {  // a row of its own
+                    if ((lane & 15) == 0)
+                        *reinterpret_cast<u32x2 *>(a.h_frags + static_cast<int64_t>(pass.h_tile) * h_chunks * kSpan + k) =
+                            out;
+                } else {
+                    const int ch = k / kSpan, in = k % kSpan;
+                    uint16_t *to = a.h_frags + (static_cast<int64_t>(pass.h_tile + t) * h_chunks + ch) * kTileChunk +
+                                   (((in & 127) >> 3) * 64 + (in >> 7) * 16 + (lane & 15)) * 8 + (in & 7);
+                    *reinterpret_cast<u32x2 *>(to) = out;
+                }
+            }
         }
     }
 }
@@ -650,111 +779,100 @@ __global__ __launch_bounds__(512) void moe_gate_up_kernel(MoeArgs a)
 // ---------------------------------------------------------------------------
 // down, and the sum over a token's experts
 // ---------------------------------------------------------------------------
-// A workgroup takes 16 output columns and walks all units: its waves take the
-// (unit, chunk) pairs in turn, multiply a unit's sums by its tokens' weights and
-// add them to their own sums for every token, in a fixed order; the waves' sums
-// meet at the end.  So a token's experts are added up without a pass of their own.
-template <int OUT, class Rows, int TF>
-__global__ __launch_bounds__(512) void moe_down_kernel(MoeArgs a)
+// A workgroup takes 16 output columns and walks all passes: its waves take the
+// (pass, chunk) pairs in turn, multiply a pass's sums by its tokens' weights and add
+// them to their own sums for every token, in a fixed order; the waves' sums meet at
+// the end.  So a token's experts are added up without a pass of their own.
+template <int OUT, class Rows, int TF, bool kOne, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void moe_down_kernel(MoeArgs a)
 {
+    constexpr int kTokens = kOne ? 1 : kMaxTokens;
     __shared__ __attribute__((aligned(1024))) uint8_t table[kPairTableBytes + 256];
     __shared__ float scb[1][256], cb4[1][16];
-    __shared__ __attribute__((aligned(16))) float sums[8][kMaxTokens][16];
+    __shared__ __attribute__((aligned(16))) float sums[WAVES][kTokens][16];
+    __shared__ OnePlan one;
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const uint32_t n = static_cast<uint32_t>(a.n_ff);
     const int n_out = static_cast<int>(a.n_in);
     const int chunks = chunks_of(a.n_ff);
     const int64_t n_elems = static_cast<int64_t>(a.n_experts) * a.n_ff * a.n_in;
-    const Weight one[2] = {a.w[2], a.w[2]};
+    const Weight both[2] = {a.down, a.down};
+    const Source src = {a.down, a.log2_down, n_elems, static_cast<uint32_t>(a.n_ff)};
 
-    const Codebooks codebooks = fetch_codebooks<1>(one);
-    const int items = *a.n_units * chunks;
+    const Codebooks codebooks = fetch_codebooks<1>(both);
+    int n_passes;
+    if constexpr (kOne) {
+        plan_one(a, one);
+        __syncthreads();
+        n_passes = one.n;
+    } else {
+        n_passes = *a.n_units;
+    }
+    const int items = n_passes * chunks;
     const int row_blocks = (n_out + 15) >> 4;
-    Pass next_unit{};
+    Pass next_pass{};
     RowBlock next_rows{};
     int next_c = 0;
     const auto enter = [&](int row_block, int item) {
         const int u = item / chunks;
-        next_unit = a.units[u];
+        if constexpr (kOne)
+            next_pass = Pass{one.expert[u], 0, u, 1};
+        else
+            next_pass = a.units[u];
         next_c = item - u * chunks;
         const int row = row_block * 16;
-        next_rows = RowBlock{static_cast<int64_t>(next_unit.expert) * n_out + row,
+        next_rows = RowBlock{static_cast<int64_t>(next_pass.expert) * n_out + row,
                              n_out - row < 16 ? n_out - row : 16};
     };
-    Rows cur, next;
-    const bool some = wave < items;
-    if (some) {
+    Held<Rows> held;
+    if (wave < items) {
         enter(blockIdx.x, wave);
-        if constexpr (Rows::kAhead)
-            next.load(a.w[2], a.log2_down, n_elems, next_rows, n, next_c, lane);
+        held.load_first(src, next_rows, next_c, lane);
     }
     fill_tables<1, 1>(codebooks, table, scb, cb4);
     const uint32_t lane_byte = (lane & 31) * 8;
 
     for (int row_block = blockIdx.x; row_block < row_blocks; row_block += gridDim.x) {
-        for (int i = lane; i < kMaxTokens * 4; i += 64)
+        for (int i = lane; i < (kOne ? 1 : static_cast<int>(a.m)) * 4; i += 64)
             reinterpret_cast<f32x4 *>(&sums[wave][0][0])[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         f32x4 acc[TF];
 #pragma unroll
         for (int t = 0; t < TF; ++t)
             acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        for (int item = wave; item < items; item += 8) {
-            if constexpr (Rows::kAhead)
-                cur = next;
-            else
-                cur.load(a.w[2], a.log2_down, n_elems, next_rows, n, next_c, lane);
-            const Pass unit = next_unit;
+        for (int item = wave; item < items; item += WAVES) {
+            const Pass pass = next_pass;
             const RowBlock rows = next_rows;
             const int c = next_c;
-            const bool last = item + 8 >= items;
+            const bool last = item + WAVES >= items;
             if (!last)
-                enter(row_block, item + 8);
+                enter(row_block, item + WAVES);
             else if (row_block + static_cast<int>(gridDim.x) < row_blocks)
                 enter(row_block + gridDim.x, wave);
-            // past the last item: the same again, unused
-            if constexpr (Rows::kAhead)
-                next.load(a.w[2], a.log2_down, n_elems, next_rows, n, next_c, lane);
-            cur.prepare(scb[0], a.w[2].offset, rows, n, c, lane_byte, lane);
-            const uint16_t *h[TF];
-#pragma unroll
-            for (int t = 0; t < TF; ++t)
-                h[t] = a.h_frags +
-                       (static_cast<int64_t>(unit.h_tile + (t < unit.tiles ? t : unit.tiles - 1)) * chunks + c) *
-                           kTileChunk + lane * 8;
-            constexpr int kAhead = 4;
-            u32x4 hf[kAhead][TF];
-#pragma unroll
-            for (int st = 0; st < kAhead; ++st)
+            Columns<TF, kOne> h;
+            if constexpr (kOne) {
+                // (zeros behind the row's last k: the products left them out)
+                h.row = buffer_from(a.h_frags + static_cast<int64_t>(pass.h_tile) * chunks * kSpan,
+                                    (a.n_ff + 15) / 16 * 32);
+                h.k_lane = (lane & 15) == 0 ? (c * kSpan + 128 * (lane >> 4)) * 2 : 0x80000000u;
+            } else {
 #pragma unroll
                 for (int t = 0; t < TF; ++t)
-                    hf[st][t] = *reinterpret_cast<const u32x4 *>(h[t] + st * 512);
-            Pairs now = cur.look(table, 0), then{};
-#pragma unroll
-            for (int st = 0; st < 16; ++st) {
-                if (st < 15)
-                    then = cur.look(table, st + 1);
-                keep_order();
-                const u32x4 wf = cur.operand(now, st);
-#pragma unroll
-                for (int t = 0; t < TF; ++t)
-                    acc[t] = Half<OUT>::mfma(wf, hf[st % kAhead][t], acc[t]);
-                now = then;
-                if (st + kAhead < 16)
-#pragma unroll
-                    for (int t = 0; t < TF; ++t)
-                        hf[st % kAhead][t] = *reinterpret_cast<const u32x4 *>(h[t] + (st + kAhead) * 512);
+                    h.at[t] = a.h_frags +
+                              (static_cast<int64_t>(pass.h_tile + (t < pass.tiles ? t : pass.tiles - 1)) * chunks + c) *
+                                  kTileChunk + lane * 8;
             }
-            // the wave's next pair is of another unit: this one's sums to its tokens
-            if (last || next_unit.h_tile != unit.h_tile) {
+            multiply_chunk<OUT, Rows, TF, kOne>(held, src, rows, c, next_rows, next_c, scb[0], table, lane_byte, h, acc,
+                                                lane);
+            // the wave's next pair is of another pass: this one's sums to its tokens
+            if (last || next_pass.h_tile != pass.h_tile) {
 #pragma unroll
                 for (int t = 0; t < TF; ++t) {
-                    if (t < unit.tiles) {
-                        const int at = (unit.h_tile + t) * 16 + (lane & 15);
-                        const int token = a.token_of[at];
+                    if (t < pass.tiles) {
+                        const int at = (pass.h_tile + t) * 16 + (lane & 15);
+                        const int token = kOne ? ((lane & 15) == 0 ? 0 : -1) : a.token_of[at];
                         if (token >= 0) {
-                            const float w = a.share_of[at];
+                            const float w = kOne ? one.share[pass.h_tile] : a.share_of[at];
                             f32x4 *to = reinterpret_cast<f32x4 *>(&sums[wave][token][4 * (lane >> 4)]);
                             f32x4 v = *to;
 #pragma unroll
@@ -772,7 +890,7 @@ __global__ __launch_bounds__(512) void moe_down_kernel(MoeArgs a)
             const int token = tid >> 2, i0 = 4 * (tid & 3);
             f32x4 z = *reinterpret_cast<const f32x4 *>(&sums[0][token][i0]);
 #pragma unroll
-            for (int q = 1; q < 8; ++q)
+            for (int q = 1; q < WAVES; ++q)
                 z = z + *reinterpret_cast<const f32x4 *>(&sums[q][token][i0]);
             const int n0 = row_block * 16 + i0;
             const int valid = n_out - n0 < 4 ? n_out - n0 : 4;
@@ -831,50 +949,77 @@ bool sizes_fit(int64_t n_experts, int64_t n_ff, int64_t n_in, int64_t m, int64_t
            n_in <= kMaxWidth && n_experts * n_ff * n_in <= kMaxWeight;
 }
 
+// A single token's kernels read x and h as they lie, and plan for themselves.
+bool one_token(const MoeArgs &a)
+{
+    return a.m == 1 && a.vec_x;
+}
+
 bool four_aligned(const void *p)
 {
     return reinterpret_cast<uintptr_t>(p) % 4 == 0;
 }
 
+// One token, up to a tile a pass, more.
 template <int OUT, class Rows>
-const void *gate_up_kernel(int tf)
-{
-    return tf == 1 ? reinterpret_cast<const void *>(&moe_gate_up_kernel<OUT, Rows, 1>)
-                   : reinterpret_cast<const void *>(&moe_gate_up_kernel<OUT, Rows, 2>);
-}
+struct Kernels {
+    // (two tiles' sums and operands do not leave registers for 16 waves)
+    static constexpr int kWaves = 16, kWavesOfTwo = 8;
 
-template <int OUT, class Rows>
-const void *down_kernel(int tf)
-{
-    return tf == 1 ? reinterpret_cast<const void *>(&moe_down_kernel<OUT, Rows, 1>)
-                   : reinterpret_cast<const void *>(&moe_down_kernel<OUT, Rows, 2>);
-}
+    static dq4_status_t gate_up(const MoeArgs &a, int cus, hipStream_t s)
+    {
+        const void *kernel = one_token(a)
+                                 ? reinterpret_cast<const void *>(&moe_gate_up_kernel<OUT, Rows, 1, true, kWaves>)
+                             : a.tf == 1
+                                 ? reinterpret_cast<const void *>(&moe_gate_up_kernel<OUT, Rows, 1, false, kWaves>)
+                                 : reinterpret_cast<const void *>(&moe_gate_up_kernel<OUT, Rows, 2, false, kWavesOfTwo>);
+        // waves along k for each matrix: no more than chunks
+        const int waves = a.tf == 1 ? kWaves : kWavesOfTwo;
+        int32_t wk = waves / 2;
+        while (wk > ceil_div(a.n_in, kSpan))
+            wk /= 2;
+        MoeArgs args = a;
+        void *params[] = {&args, &wk};
+        const int64_t most = ceil_div(a.max_tiles * ceil_div(a.n_ff, 16), waves / (2 * wk));
+        return launch(kernel, most < cus ? most : cus, 1, 64 * waves, params, s);
+    }
+
+    static dq4_status_t down(const MoeArgs &a, int cus, hipStream_t s)
+    {
+        const void *kernel = one_token(a) ? reinterpret_cast<const void *>(&moe_down_kernel<OUT, Rows, 1, true, kWaves>)
+                             : a.tf == 1
+                                 ? reinterpret_cast<const void *>(&moe_down_kernel<OUT, Rows, 1, false, kWaves>)
+                                 : reinterpret_cast<const void *>(&moe_down_kernel<OUT, Rows, 2, false, kWavesOfTwo>);
+        MoeArgs args = a;
+        void *params[] = {&args};
+        const int64_t row_blocks = ceil_div(a.n_in, 16);
+        return launch(kernel, row_blocks < cus ? row_blocks : cus, 1, 64 * (a.tf == 1 ? kWaves : kWavesOfTwo), params, s);
+    }
+};
 
 template <int OUT>
 dq4_status_t run_moe(MoeArgs a, int cus, hipStream_t s)
 {
-    void *params[] = {&a};
-    const int64_t pieces = a.max_tiles * ceil_div(a.n_in, kSpan);
-    dq4_status_t st = launch(reinterpret_cast<const void *>(&moe_plan_zero_fill), pieces < cus ? pieces : cus, 1, 512,
-                             params, s);
-    if (st != DQ4_OK)
-        return st;
-    if (a.n_ff > 0) {
-        const bool even = a.n_in % 32 == 0 && four_aligned(a.w[0].packed) && four_aligned(a.w[1].packed);
-        const void *kernel = !even ? gate_up_kernel<OUT, AnyRows<OUT>>(a.tf)
-                             : a.log2_block >= 6 && a.n_in % 64 == 0 ? gate_up_kernel<OUT, EvenRows<OUT, 2>>(a.tf)
-                                                                     : gate_up_kernel<OUT, EvenRows<OUT, 4>>(a.tf);
-        const int64_t most = a.max_tiles * ceil_div(a.n_ff, 16);
-        st = launch(kernel, most < cus ? most : cus, 1, 512, params, s);
+    dq4_status_t st;
+    if (!one_token(a)) {  // (a single token's kernels plan for themselves)
+        void *params[] = {&a};
+        const int64_t pieces = a.max_tiles * ceil_div(a.n_in, kSpan);
+        st = launch(reinterpret_cast<const void *>(&moe_plan_zero_fill), pieces < cus ? pieces : cus, 1, 512, params, s);
         if (st != DQ4_OK)
             return st;
     }
-    const bool even = a.n_ff % 32 == 0 && four_aligned(a.w[2].packed);
-    const void *kernel = !even ? down_kernel<OUT, AnyRows<OUT>>(a.tf)
-                         : a.log2_down >= 6 && a.n_ff % 64 == 0 ? down_kernel<OUT, EvenRows<OUT, 2>>(a.tf)
-                                                                : down_kernel<OUT, EvenRows<OUT, 4>>(a.tf);
-    const int64_t row_blocks = ceil_div(a.n_in, 16);
-    return launch(kernel, row_blocks < cus ? row_blocks : cus, 1, 512, params, s);
+    if (a.n_ff > 0) {
+        const bool even = a.n_in % 32 == 0 && four_aligned(a.w[0].packed) && four_aligned(a.w[1].packed);
+        st = !even ? Kernels<OUT, AnyRows<OUT>>::gate_up(a, cus, s)
+             : a.log2_block >= 6 && a.n_in % 64 == 0 ? Kernels<OUT, EvenRows<OUT, 2>>::gate_up(a, cus, s)
+                                                     : Kernels<OUT, EvenRows<OUT, 4>>::gate_up(a, cus, s);
+        if (st != DQ4_OK)
+            return st;
+    }
+    const bool even = a.n_ff % 32 == 0 && four_aligned(a.down.packed);
+    return !even ? Kernels<OUT, AnyRows<OUT>>::down(a, cus, s)
+           : a.log2_down >= 6 && a.n_ff % 64 == 0 ? Kernels<OUT, EvenRows<OUT, 2>>::down(a, cus, s)
+                                                  : Kernels<OUT, EvenRows<OUT, 4>>::down(a, cus, s);
 }
 
 }  // namespace
@@ -961,7 +1106,7 @@ dq4_status_t dq4_moe_fused(const dq4_weight_t *gate, const dq4_weight_t *up, con
     MoeArgs a{};
     a.w[0] = device_weight(*gate);
     a.w[1] = device_weight(*up);
-    a.w[2] = device_weight(*down);
+    a.down = device_weight(*down);
     a.log2_block = log2_block;
     a.log2_down = log2_down;
     a.n_experts = n_experts;
