@@ -381,8 +381,7 @@ __device__ __forceinline__ void load_scale(const Buffers &q, uint32_t block, boo
 // takes 256 bytes of 4 rows, a quad of lanes on 64 of them; 4 such loads are
 // transposed between the lanes of each quad; the scales, S blocks per 128 k, are
 // looked up four lanes to a row and handed over.  S = 2: blocks of 64 k or more and
-// row lengths that are multiples of 64; else S = 4.  The next chunk's loads are
-// issued as this one's registers come free.
+// row lengths that are multiples of 64; else S = 4.
 template <int OUT, int S>
 struct EvenRows {
     static constexpr bool kEven = true;
@@ -445,9 +444,9 @@ struct EvenRows {
         return c * kSpan + 128 * (lane >> 4) + 32 * j >= static_cast<int>(w.n) || (lane & 15) >= b.rows;
     }
 
-    __device__ __forceinline__ Pairs look(const uint8_t *table, uint32_t lane_byte, bool beyond, int step) const
+    __device__ __forceinline__ Pairs look(const uint8_t *table, uint32_t lane_byte, int step) const
     {
-        return lookup_dword(packed[step / 4][step % 4], table, beyond ? lane_byte | kPairTableBytes : lane_byte);
+        return lookup_dword(packed[step / 4][step % 4], table, lane_byte);
     }
 
     __device__ __forceinline__ u32x4 operand(const Pairs &p, bool beyond, int step) const
@@ -524,96 +523,127 @@ struct AnyRows {
 template <int TF, bool kOne>
 struct Columns {
     const uint16_t *at[TF];
-    __amdgpu_buffer_rsrc_t row;
-    uint32_t k_lane;
+    const uint16_t *row;
+    uint32_t row_bytes, k_lane;
 
     __device__ __forceinline__ u32x4 load(int t, int step) const
     {
         if constexpr (kOne)
-            return __builtin_amdgcn_raw_buffer_load_b128(row, k_lane + 16 * step, 0, 0);
+            return __builtin_amdgcn_raw_buffer_load_b128(buffer_from(row, row_bytes), k_lane + 16 * step, 0, 0);
         else
             return *reinterpret_cast<const u32x4 *>(at[t] + step * 512);
     }
 };
 
-// What a wave holds of a row block: an even one's chunk, or two pieces in turn.
-template <class Rows>
-struct Held {
-    Rows r[Rows::kEven ? 1 : 2];
+// Steps that the other operand is loaded ahead; what the registers hold.
+template <int W>
+constexpr int kAheadOf = W == 2 ? 2 : 4;
 
-    __device__ __forceinline__ void load_first(const Source &src, const RowBlock &rows, int c, int lane)
+// What a wave holds: of a row block an even one's chunk, or two pieces in turn; and
+// the other operand's next steps.
+template <class Rows, int W, int TF>
+struct Held {
+    Rows r[W][Rows::kEven ? 1 : 2];
+    static constexpr int kAhead = kAheadOf<W>;
+    u32x4 x[kAhead][TF];
+
+    template <bool kOne>
+    __device__ __forceinline__ void load_first(const Source (&src)[W], const RowBlock &rows, int c,
+                                               const Columns<TF, kOne> &columns, int lane)
     {
-        if constexpr (Rows::kEven)
-            r[0].load(src, rows, c, lane);
-        else
-            r[0].load(src, rows, c, 0, lane);
+#pragma unroll
+        for (int f = 0; f < W; ++f) {
+            if constexpr (Rows::kEven)
+                r[f][0].load(src[f], rows, c, lane);
+            else
+                r[f][0].load(src[f], rows, c, 0, lane);
+        }
+#pragma unroll
+        for (int st = 0; st < kAhead; ++st)
+#pragma unroll
+            for (int t = 0; t < TF; ++t)
+                x[st][t] = columns.load(t, st);
     }
 };
 
-// acc[t] += 16 weight rows x a chunk of 512 k x TF tiles.  `next`: where the wave's
-// next chunk lies (the same again after the last one: unused).  Lookups run one step
-// ahead.
-template <int OUT, class Rows, int TF, bool kOne>
-__device__ __forceinline__ void multiply_chunk(Held<Rows> &held, const Source &src, const RowBlock &rows, int c,
-                                               const RowBlock &next, int next_c, const float *scb,
-                                               const uint8_t *table, uint32_t lane_byte,
-                                               const Columns<TF, kOne> &x, f32x4 (&acc)[TF], int lane)
+// Where the wave's next chunk lies (the same again after the last one: unused).
+template <int TF, bool kOne>
+struct Place {
+    RowBlock rows;
+    int c;
+    Columns<TF, kOne> x;
+};
+
+// acc[f][t] += 16 rows of each of W weights x a chunk of 512 k x TF tiles.  Lookups
+// run one weight's step ahead (weight f's table lies f * 8 bytes behind the first's).
+// Loads return in the order of their issue: the next chunk's weight, which comes from
+// memory, goes out behind this chunk's last load from cache.
+template <int OUT, class Rows, int W, int TF, bool kOne>
+__device__ __forceinline__ void multiply_chunk(Held<Rows, W, TF> &held, const Source (&src)[W],
+                                               const Place<TF, kOne> &at, const Place<TF, kOne> &next,
+                                               const float *scb, const uint8_t *table, uint32_t lane_byte,
+                                               uint32_t zero_byte, f32x4 (&acc)[W][TF], int lane)
 {
-    constexpr int kAhead = 4;
-    u32x4 xf[kAhead][TF];
-#pragma unroll
-    for (int st = 0; st < kAhead; ++st)
-#pragma unroll
-        for (int t = 0; t < TF; ++t)
-            xf[st][t] = x.load(t, st);
-    Rows ahead;
+    constexpr int kAhead = kAheadOf<W>;
+    Rows ahead[W];
     if constexpr (Rows::kEven)
-        held.r[0].prepare(scb, src.w.offset, lane);
+#pragma unroll
+        for (int f = 0; f < W; ++f)
+            held.r[f][0].prepare(scb + 256 * f, src[f].w.offset, lane);
     Pairs now{}, then{};
 #pragma unroll
     for (int st = 0; st < 16; ++st) {
-        u32x4 wf;
-        if constexpr (Rows::kEven) {
-            const bool beyond = Rows::beyond(src, rows, c, st / 4, lane);
-            if (st == 0)
-                now = held.r[0].look(table, lane_byte, beyond, 0);
-            if (st < 15)
-                then = held.r[0].look(table, lane_byte, Rows::beyond(src, rows, c, (st + 1) / 4, lane), st + 1);
-            keep_order();
-            wf = held.r[0].operand(now, beyond, st);
-            // the next chunk's loads, as registers come free
-            if (st == 0)
-                ahead.load_scales(src, next, next_c, lane);
-            if (st == 1 || st == 3 || st == 7)
-                ahead.load_packed(st == 1 ? 0 : st == 3 ? 1 : 2, src, next, next_c, lane);
-            if (st == 7)
-                ahead.load_packed(3, src, next, next_c, lane);
-        } else {
-            const int j = st / 4, d = st % 4;
-            if (d == 0) {
-                held.r[j & 1].prepare(scb, src.w.offset);
-                if (j < 3)
-                    held.r[(j + 1) & 1].load(src, rows, c, j + 1, lane);
-                else
-                    held.r[0].load(src, next, next_c, 0, lane);
-                now = held.r[j & 1].look(table, lane_byte, 0);
-            }
-            if (d < 3)
-                then = held.r[j & 1].look(table, lane_byte, d + 1);
-            keep_order();
-            wf = held.r[j & 1].operand(now, d);
-        }
+        const int j = st / 4, d = st % 4;
+        if constexpr (!Rows::kEven)
+            if (d == 0)
 #pragma unroll
-        for (int t = 0; t < TF; ++t)
-            acc[t] = Half<OUT>::mfma(wf, xf[st % kAhead][t], acc[t]);
-        now = then;
-        if (st + kAhead < 16)
+                for (int f = 0; f < W; ++f) {
+                    held.r[f][j & 1].prepare(scb + 256 * f, src[f].w.offset);
+                    if (j < 3)
+                        held.r[f][(j + 1) & 1].load(src[f], at.rows, at.c, j + 1, lane);
+                    else
+                        held.r[f][0].load(src[f], next.rows, next.c, 0, lane);
+                }
+#pragma unroll
+        for (int f = 0; f < W; ++f) {
+            const int nf = f + 1 < W ? f + 1 : 0, ns = f + 1 < W ? st : st + 1;
+            u32x4 wf;
+            if constexpr (Rows::kEven) {
+                const bool beyond = Rows::beyond(src[f], at.rows, at.c, j, lane);
+                if (st == 0 && f == 0)
+                    now = held.r[0][0].look(table, beyond ? zero_byte : lane_byte, 0);
+                if (ns < 16)
+                    then = held.r[nf][0].look(
+                        table + nf * 8, Rows::beyond(src[nf], at.rows, at.c, ns / 4, lane) ? zero_byte : lane_byte, ns);
+                keep_order();
+                wf = held.r[f][0].operand(now, beyond, st);
+            } else {
+                if (d == 0 && f == 0)
+                    now = held.r[0][j & 1].look(table, lane_byte, 0);
+                if (ns / 4 == j)
+                    then = held.r[nf][j & 1].look(table + nf * 8, lane_byte, ns % 4);
+                keep_order();
+                wf = held.r[f][j & 1].operand(now, d);
+            }
 #pragma unroll
             for (int t = 0; t < TF; ++t)
-                xf[st % kAhead][t] = x.load(t, st + kAhead);
+                acc[f][t] = Half<OUT>::mfma(wf, held.x[st % kAhead][t], acc[f][t]);
+            now = then;
+        }
+        if constexpr (Rows::kEven)
+            if (st == 16 - kAhead)
+#pragma unroll
+                for (int f = 0; f < W; ++f)
+                    ahead[f].load(src[f], next.rows, next.c, lane);
+#pragma unroll
+        for (int t = 0; t < TF; ++t)
+            held.x[st % kAhead][t] =
+                st + kAhead < 16 ? at.x.load(t, st + kAhead) : next.x.load(t, st + kAhead - 16);
     }
     if constexpr (Rows::kEven)
-        held.r[0] = ahead;
+#pragma unroll
+        for (int f = 0; f < W; ++f)
+            held.r[f][0] = ahead[f];
 }
 
 // A single token's plan: its valid experts, each once, in the order of its row.
@@ -661,23 +691,28 @@ __device__ __forceinline__ void plan_one(const MoeArgs &a, OnePlan &p)
 // (A wave for each matrix: 16 waves hold one matrix's chunk and the next, and with
 // four waves a SIMD lookups, vector instructions and loads overlap; a wave for both
 // left room for 8 waves.)
-template <int OUT, class Rows, int TF, bool kOne, int WAVES>
+template <int OUT, class Rows, int W, int TF, bool kOne, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void moe_gate_up_kernel(MoeArgs a, int32_t wk_waves)
 {
-    __shared__ __attribute__((aligned(1024))) uint8_t table[kPairTableBytes + 256];
+    constexpr int kTables = 3 - W;  // W == 2: one table of both weights
+    __shared__ __attribute__((aligned(1024))) uint8_t table[kTables * kPairTableBytes + 256];
     __shared__ float scb[2][256], cb4[2][16];
-    __shared__ __attribute__((aligned(16))) f32x4 partial[WAVES][TF][64];
+    __shared__ __attribute__((aligned(16))) f32x4 partial[WAVES][W * TF][64];
     __shared__ OnePlan one;
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int WK = wk_waves, WR = WAVES / (2 * WK);
-    const int which = wave & 1, wk = (wave >> 1) % WK, wr = wave / (2 * WK);
+    constexpr int kShare = 3 - W;  // waves that share a chunk
+    const int WK = wk_waves, WR = WAVES / (kShare * WK);
+    const int which = W == 2 ? 0 : wave & 1, wk = wave / kShare % WK, wr = wave / (kShare * WK);
     const int n_ff = static_cast<int>(a.n_ff);
     const int chunks = chunks_of(a.n_in), h_chunks = chunks_of(a.n_ff);
     const int row_blocks = (n_ff + 15) >> 4;
     const int64_t n_elems = static_cast<int64_t>(a.n_experts) * a.n_ff * a.n_in;
-    const Source src = {either(a.w[0], a.w[1], which), a.log2_block, n_elems, static_cast<uint32_t>(a.n_in)};
+    Source src[W];
+#pragma unroll
+    for (int f = 0; f < W; ++f)
+        src[f] = Source{either(a.w[0], a.w[1], which + f), a.log2_block, n_elems, static_cast<uint32_t>(a.n_in)};
 
     const Codebooks codebooks = fetch_codebooks<2>(a.w);
     int n_passes;
@@ -690,9 +725,24 @@ __global__ __launch_bounds__(64 * WAVES) void moe_gate_up_kernel(MoeArgs a, int3
     }
     const int items = n_passes * row_blocks;
     const int step = gridDim.x * WR;
-    int next_item = blockIdx.x * WR + wr, next_c = wk;
+    int next_item = blockIdx.x * WR + wr;
     Pass pass{}, next_pass{};
-    RowBlock rows{}, next_rows{};
+    Place<TF, kOne> at{}, next{};
+    // chunk c of the pass
+    const auto columns = [&](const Pass &p, int c) {
+        Columns<TF, kOne> x{};
+        if constexpr (kOne) {
+            x.row = a.x;
+            x.row_bytes = static_cast<uint32_t>(a.n_in * 2);
+            x.k_lane = (lane & 15) == 0 ? (c * kSpan + 128 * (lane >> 4)) * 2 : 0x80000000u;
+        } else {
+#pragma unroll
+            for (int t = 0; t < TF; ++t)  // past the pass's last tile: that again, unused
+                x.at[t] = a.x_frags + (static_cast<int64_t>(p.x_tile + (t < p.tiles ? t : p.tiles - 1)) * chunks + c) *
+                                          kTileChunk + lane * 8;
+        }
+        return x;
+    };
     const auto enter = [&](int item) {
         const int u = item / row_blocks;
         if constexpr (kOne)
@@ -700,59 +750,56 @@ __global__ __launch_bounds__(64 * WAVES) void moe_gate_up_kernel(MoeArgs a, int3
         else
             next_pass = a.units[u];
         const int row = (item - u * row_blocks) * 16;
-        next_rows = RowBlock{static_cast<int64_t>(next_pass.expert) * n_ff + row, n_ff - row < 16 ? n_ff - row : 16};
+        next.rows = RowBlock{static_cast<int64_t>(next_pass.expert) * n_ff + row, n_ff - row < 16 ? n_ff - row : 16};
+        next.c = wk;
+        next.x = columns(next_pass, wk);
     };
-    Held<Rows> held;
+    Held<Rows, W, TF> held;
     if (next_item < items) {
         enter(next_item);
-        held.load_first(src, next_rows, next_c, lane);
+        held.load_first(src, next.rows, next.c, next.x, lane);
     }
-    fill_tables<2, 1>(codebooks, table, scb, cb4);
-    const uint32_t lane_byte = (lane & 15) * 16 + which * 8;
+    fill_tables<2, kTables>(codebooks, table, scb, cb4);
+    const uint32_t copy = W == 2 ? (lane & 15) * 16 : (lane & 31) * 8;
+    const uint32_t lane_byte = copy + which * kPairTableBytes, zero_byte = copy % 248 + kTables * kPairTableBytes;
 
     for (int item0 = blockIdx.x * WR; item0 < items; item0 += step) {
         const int item = item0 + wr;
         pass = next_pass;
-        rows = next_rows;
-        f32x4 acc[TF];
+        f32x4 acc[W][TF];
 #pragma unroll
-        for (int t = 0; t < TF; ++t)
-            acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int f = 0; f < W; ++f)
+#pragma unroll
+            for (int t = 0; t < TF; ++t)
+                acc[f][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         if (item < items)
             for (int c = wk; c < chunks; c += WK) {  // wk < chunks
-                next_c += WK;
-                if (next_c >= chunks) {
-                    next_c = wk;
+                at = next;
+                if (c + WK < chunks) {
+                    next.c = c + WK;
+                    next.x = columns(pass, c + WK);
+                } else {
                     next_item += step;
                     if (next_item < items)
                         enter(next_item);
                 }
-                Columns<TF, kOne> x;
-                if constexpr (kOne) {
-                    x.row = buffer_from(a.x, a.n_in * 2);
-                    x.k_lane = (lane & 15) == 0 ? (c * kSpan + 128 * (lane >> 4)) * 2 : 0x80000000u;
-                } else {
-#pragma unroll
-                    for (int t = 0; t < TF; ++t)  // past the pass's last tile: that again, unused
-                        x.at[t] = a.x_frags +
-                                  (static_cast<int64_t>(pass.x_tile + (t < pass.tiles ? t : pass.tiles - 1)) * chunks +
-                                   c) * kTileChunk + lane * 8;
-                }
-                multiply_chunk<OUT, Rows, TF, kOne>(held, src, rows, c, next_rows, next_c, scb[which], table, lane_byte,
-                                                    x, acc, lane);
+                multiply_chunk<OUT, Rows, W, TF, kOne>(held, src, at, next, scb[which], table, lane_byte, zero_byte,
+                                                       acc, lane);
             }
         lds_barrier();  // the last items' sums are read
         if (item < items)
 #pragma unroll
-            for (int t = 0; t < TF; ++t)
-                partial[wave][t][lane] = acc[t];
+            for (int f = 0; f < W; ++f)
+#pragma unroll
+                for (int t = 0; t < TF; ++t)
+                    partial[wave][f * TF + t][lane] = acc[f][t];
         lds_barrier();
         if (item < items) {  // a wave of the group finishes a tile
-            for (int t = wave - wr * (2 * WK); t < pass.tiles; t += 2 * WK) {
+            for (int t = wave - wr * (kShare * WK); t < pass.tiles; t += kShare * WK) {
                 f32x4 gate = {0.0f, 0.0f, 0.0f, 0.0f}, up = {0.0f, 0.0f, 0.0f, 0.0f};
-                for (int q = wr * (2 * WK); q < (wr + 1) * (2 * WK); q += 2) {
+                for (int q = wr * (kShare * WK); q < (wr + 1) * (kShare * WK); q += kShare) {
                     gate = gate + partial[q][t][lane];
-                    up = up + partial[q + 1][t][lane];
+                    up = up + (W == 2 ? partial[q][(W - 1) * TF + t][lane] : partial[q + kShare - 1][t][lane]);
                 }
                 // the lane's four neighbouring k of h, column lane % 16
                 const int k = (item - item / row_blocks * row_blocks) * 16 + 4 * (lane >> 4);
@@ -798,7 +845,7 @@ __global__ __launch_bounds__(64 * WAVES) void moe_down_kernel(MoeArgs a)
     const int chunks = chunks_of(a.n_ff);
     const int64_t n_elems = static_cast<int64_t>(a.n_experts) * a.n_ff * a.n_in;
     const Weight both[2] = {a.down, a.down};
-    const Source src = {a.down, a.log2_down, n_elems, static_cast<uint32_t>(a.n_ff)};
+    const Source src[1] = {{a.down, a.log2_down, n_elems, static_cast<uint32_t>(a.n_ff)}};
 
     const Codebooks codebooks = fetch_codebooks<1>(both);
     int n_passes;
@@ -812,58 +859,55 @@ __global__ __launch_bounds__(64 * WAVES) void moe_down_kernel(MoeArgs a)
     const int items = n_passes * chunks;
     const int row_blocks = (n_out + 15) >> 4;
     Pass next_pass{};
-    RowBlock next_rows{};
-    int next_c = 0;
+    Place<TF, kOne> at{}, next{};
     const auto enter = [&](int row_block, int item) {
         const int u = item / chunks;
         if constexpr (kOne)
             next_pass = Pass{one.expert[u], 0, u, 1};
         else
             next_pass = a.units[u];
-        next_c = item - u * chunks;
+        next.c = item - u * chunks;
         const int row = row_block * 16;
-        next_rows = RowBlock{static_cast<int64_t>(next_pass.expert) * n_out + row,
+        next.rows = RowBlock{static_cast<int64_t>(next_pass.expert) * n_out + row,
                              n_out - row < 16 ? n_out - row : 16};
+        if constexpr (kOne) {
+            // (zeros behind the row's last k: the products left them out)
+            next.x.row = a.h_frags + static_cast<int64_t>(u) * chunks * kSpan;
+            next.x.row_bytes = static_cast<uint32_t>((a.n_ff + 15) / 16 * 32);
+            next.x.k_lane = (lane & 15) == 0 ? (next.c * kSpan + 128 * (lane >> 4)) * 2 : 0x80000000u;
+        } else {
+#pragma unroll
+            for (int t = 0; t < TF; ++t)
+                next.x.at[t] =
+                    a.h_frags +
+                    (static_cast<int64_t>(next_pass.h_tile + (t < next_pass.tiles ? t : next_pass.tiles - 1)) * chunks +
+                     next.c) * kTileChunk + lane * 8;
+        }
     };
-    Held<Rows> held;
+    Held<Rows, 1, TF> held;
     if (wave < items) {
         enter(blockIdx.x, wave);
-        held.load_first(src, next_rows, next_c, lane);
+        held.load_first(src, next.rows, next.c, next.x, lane);
     }
     fill_tables<1, 1>(codebooks, table, scb, cb4);
-    const uint32_t lane_byte = (lane & 31) * 8;
+    const uint32_t lane_byte = (lane & 31) * 8, zero_byte = lane_byte + kPairTableBytes;
 
     for (int row_block = blockIdx.x; row_block < row_blocks; row_block += gridDim.x) {
         for (int i = lane; i < (kOne ? 1 : static_cast<int>(a.m)) * 4; i += 64)
             reinterpret_cast<f32x4 *>(&sums[wave][0][0])[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        f32x4 acc[TF];
+        f32x4 acc[1][TF];
 #pragma unroll
         for (int t = 0; t < TF; ++t)
-            acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            acc[0][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         for (int item = wave; item < items; item += WAVES) {
             const Pass pass = next_pass;
-            const RowBlock rows = next_rows;
-            const int c = next_c;
+            at = next;
             const bool last = item + WAVES >= items;
             if (!last)
                 enter(row_block, item + WAVES);
             else if (row_block + static_cast<int>(gridDim.x) < row_blocks)
                 enter(row_block + gridDim.x, wave);
-            Columns<TF, kOne> h;
-            if constexpr (kOne) {
-                // (zeros behind the row's last k: the products left them out)
-                h.row = buffer_from(a.h_frags + static_cast<int64_t>(pass.h_tile) * chunks * kSpan,
-                                    (a.n_ff + 15) / 16 * 32);
-                h.k_lane = (lane & 15) == 0 ? (c * kSpan + 128 * (lane >> 4)) * 2 : 0x80000000u;
-            } else {
-#pragma unroll
-                for (int t = 0; t < TF; ++t)
-                    h.at[t] = a.h_frags +
-                              (static_cast<int64_t>(pass.h_tile + (t < pass.tiles ? t : pass.tiles - 1)) * chunks + c) *
-                                  kTileChunk + lane * 8;
-            }
-            multiply_chunk<OUT, Rows, TF, kOne>(held, src, rows, c, next_rows, next_c, scb[0], table, lane_byte, h, acc,
-                                                lane);
+            multiply_chunk<OUT, Rows, 1, TF, kOne>(held, src, at, next, scb[0], table, lane_byte, zero_byte, acc, lane);
             // the wave's next pair is of another pass: this one's sums to its tokens
             if (last || next_pass.h_tile != pass.h_tile) {
 #pragma unroll
@@ -877,11 +921,11 @@ __global__ __launch_bounds__(64 * WAVES) void moe_down_kernel(MoeArgs a)
                             f32x4 v = *to;
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
-                                v[i] = v[i] + w * acc[t][i];
+                                v[i] = v[i] + w * acc[0][t][i];
                             *to = v;
                         }
                     }
-                    acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                    acc[0][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
                 }
             }
         }
@@ -969,18 +1013,19 @@ struct Kernels {
     static dq4_status_t gate_up(const MoeArgs &a, int cus, hipStream_t s)
     {
         const void *kernel = one_token(a)
-                                 ? reinterpret_cast<const void *>(&moe_gate_up_kernel<OUT, Rows, 1, true, kWaves>)
+                                 ? reinterpret_cast<const void *>(&moe_gate_up_kernel<OUT, Rows, 1, 1, true, kWaves>)
                              : a.tf == 1
-                                 ? reinterpret_cast<const void *>(&moe_gate_up_kernel<OUT, Rows, 1, false, kWaves>)
-                                 : reinterpret_cast<const void *>(&moe_gate_up_kernel<OUT, Rows, 2, false, kWavesOfTwo>);
+                                 ? reinterpret_cast<const void *>(&moe_gate_up_kernel<OUT, Rows, 2, 1, false, kWaves>)
+                                 : reinterpret_cast<const void *>(&moe_gate_up_kernel<OUT, Rows, 2, 2, false, kWavesOfTwo>);
         // waves along k for each matrix: no more than chunks
         const int waves = a.tf == 1 ? kWaves : kWavesOfTwo;
-        int32_t wk = waves / 2;
+        const int share = one_token(a) ? 2 : 1;  // waves of a chunk
+        int32_t wk = waves / share;
         while (wk > ceil_div(a.n_in, kSpan))
             wk /= 2;
         MoeArgs args = a;
         void *params[] = {&args, &wk};
-        const int64_t most = ceil_div(a.max_tiles * ceil_div(a.n_ff, 16), waves / (2 * wk));
+        const int64_t most = ceil_div(a.max_tiles * ceil_div(a.n_ff, 16), waves / (share * wk));
         return launch(kernel, most < cus ? most : cus, 1, 64 * waves, params, s);
     }
 
