@@ -11,9 +11,8 @@
 // The weight is decoded in operand registers as in dq4_linear_fused.hip's few-row
 // kernels, through one lookup table of byte pairs in LDS, and multiplied on
 // v_mfma_f32_16x16x32_{f16,bf16}: 16 weight rows by a tile of 16 tokens.  An
-// expert's tokens are gathered into tiles (with up to 16 tokens in all, the one
-// tile of all tokens serves every expert), so that an expert costs its own
-// tokens, not everybody's.
+// expert's tokens are gathered into tiles, so that an expert costs its own tokens,
+// not everybody's.
 //
 // Operand order of x and h: chunks of 512 k, [tile][chunk][16 steps][64 lanes][8],
 // lane 16 g + c of step 4 j + s holding column c's k 512 chunk + 128 g + 32 j + 8
@@ -157,7 +156,8 @@ __global__ __launch_bounds__(64 * kRouteWaves) void moe_route_kernel(RouteArgs a
 // ---------------------------------------------------------------------------
 // A pass goes over one expert's matrices with up to `tf` tiles of its tokens.
 struct Pass {
-    int32_t expert, x_tile, h_tile, tiles;
+    int32_t expert, tile, tiles;  // the first of its tiles
+    int32_t columns;              // of them all: 16 in each but the last
 };
 
 struct MoeArgs {
@@ -173,10 +173,10 @@ struct MoeArgs {
     const float *weights;
     int32_t vec_x, vec_y;
     int32_t max_tiles;
-    int32_t *n_units;
-    Pass *units;
-    int32_t *token_of;       // [h tile][16]: the column's token, or -1
-    float *share_of;         // [h tile][16]: its weight for the tile's expert
+    int32_t *n_passes;
+    Pass *passes;
+    int32_t *token_of;       // [tile][16]: the column's token
+    float *share_of;         // [tile][16]: its weight for the tile's expert
     uint16_t *x_frags, *h_frags;
     const uint16_t *residual;
     int64_t ld_residual;
@@ -191,8 +191,8 @@ __device__ __forceinline__ int chunks_of(int64_t k)
 
 // Every workgroup works the plan out for itself (up to 1024 choices, a mask of
 // tokens for each expert); workgroup 0 writes it, and all write x tiles in operand
-// order, with zeros where there is no token or no k, and zeros for the k of h that
-// the products leave out.
+// order, with zeros where there is no k, and zeros for the k of h that the products
+// leave out.  Columns without a token are not written and never read.
 __global__ __launch_bounds__(512) void moe_plan_zero_fill(MoeArgs a)
 {
     __shared__ uint32_t mask[kMaxExperts][2];
@@ -209,33 +209,27 @@ __global__ __launch_bounds__(512) void moe_plan_zero_fill(MoeArgs a)
             atomicOr(&mask[e][t >> 5], 1u << (t & 31));
     }
     __syncthreads();
-    const bool one_tile = m <= 16;  // the tile of all tokens
     const int count = __builtin_popcount(mask[tid][0]) + __builtin_popcount(mask[tid][1]);
-    const int tiles = count == 0 ? 0 : one_tile ? 1 : (count + 15) / 16;
+    const int tiles = (count + 15) / 16;
     const int passes = (tiles + a.tf - 1) / a.tf;
-    int n_tiles, n_units;
+    int n_tiles, n_passes;
     const int my_tile = list_position<512>(tiles, &n_tiles, sums);
     tile0[tid] = my_tile;
-    const int my_unit = list_position<512>(passes, &n_units, sums);
+    const int my_pass = list_position<512>(passes, &n_passes, sums);
     // where a choice's token lies among its expert's
     const auto tile_column = [&](int e, int t) {
         const uint32_t below = (1u << (t & 31)) - 1;
-        const int slot = one_tile ? t
-                         : t < 32 ? __builtin_popcount(mask[e][0] & below)
-                                  : __builtin_popcount(mask[e][0]) + __builtin_popcount(mask[e][1] & below);
-        return tile0[e] * 16 + slot;
+        return tile0[e] * 16 + (t < 32 ? __builtin_popcount(mask[e][0] & below)
+                                       : __builtin_popcount(mask[e][0]) + __builtin_popcount(mask[e][1] & below));
     };
     if (blockIdx.x == 0) {
         if (tid == 0)
-            *a.n_units = n_units;
+            *a.n_passes = n_passes;
         for (int q = 0; q < passes; ++q) {
-            const int left = tiles - q * a.tf;
-            a.units[my_unit + q] = Pass{tid, one_tile ? 0 : my_tile + q * a.tf, my_tile + q * a.tf,
-                                        left < a.tf ? left : a.tf};
+            const int left = tiles - q * a.tf, columns = count - q * a.tf * 16;
+            a.passes[my_pass + q] = Pass{tid, my_tile + q * a.tf, left < a.tf ? left : a.tf,
+                                         columns < a.tf * 16 ? columns : a.tf * 16};
         }
-        for (int i = tid; i < n_tiles * 16; i += 512)
-            a.token_of[i] = -1;
-        __syncthreads();  // (and tile0 is complete)
         for (int p = tid; p < pairs; p += 512) {
             const int e = a.ids[p], t = p / a.top_k, j = p - t * a.top_k;
             if (e < 0 || e >= a.n_experts)
@@ -255,53 +249,51 @@ __global__ __launch_bounds__(512) void moe_plan_zero_fill(MoeArgs a)
             a.share_of[at] = w;
         }
     }
-    const int x_tiles = one_tile ? (n_tiles > 0 ? 1 : 0) : n_tiles;
     const int chunks = chunks_of(a.n_in), h_chunks = chunks_of(a.n_ff);
     const int h_from = static_cast<int>((a.n_ff + 15) / 16 * 16);
-    // pieces of a tile's x: one chunk each
+    // pieces of a tile's x: one chunk each, the columns that have a token
     for (int item = blockIdx.x; item < n_tiles * chunks; item += gridDim.x) {
         const int tile = item / chunks, ch = item - tile * chunks;
         __syncthreads();  // the last item's tokens are read
         if (tid < 16)
-            token[tid] = one_tile && tid < m ? tid : -1;
+            token[tid] = -1;
         __syncthreads();
-        if (!one_tile)
-            for (int p = tid; p < pairs; p += 512) {
-                const int e = a.ids[p], t = p / a.top_k;
-                if (e < 0 || e >= a.n_experts)
-                    continue;
-                const int at = tile_column(e, t);
-                if (at >> 4 == tile)
-                    token[at & 15] = t;
-            }
+        for (int p = tid; p < pairs; p += 512) {
+            const int e = a.ids[p], t = p / a.top_k;
+            if (e < 0 || e >= a.n_experts)
+                continue;
+            const int at = tile_column(e, t);
+            if (at >> 4 == tile)
+                token[at & 15] = t;
+        }
         __syncthreads();
-        if (tile < x_tiles) {
-            uint16_t *to = a.x_frags + (static_cast<int64_t>(tile) * chunks + ch) * kTileChunk;
-            for (int u = tid; u < 1024; u += 512) {
-                const int lane = u & 63, step = u >> 6;
-                const int t = token[lane & 15];
-                const int k0 = ch * kSpan + 128 * (lane >> 4) + 8 * step;
-                u32x4 q = {0, 0, 0, 0};
-                if (t >= 0 && k0 < a.n_in) {
-                    const uint16_t *from = a.x + t * a.ld_x + k0;
-                    if (a.vec_x) {
-                        q = *reinterpret_cast<const u32x4 *>(from);
-                    } else {
+        uint16_t *to = a.x_frags + (static_cast<int64_t>(tile) * chunks + ch) * kTileChunk;
+        for (int u = tid; u < 1024; u += 512) {
+            const int lane = u & 63, step = u >> 6;
+            const int t = token[lane & 15];
+            if (t < 0)
+                continue;
+            const int k0 = ch * kSpan + 128 * (lane >> 4) + 8 * step;
+            u32x4 q = {0, 0, 0, 0};
+            if (k0 < a.n_in) {
+                const uint16_t *from = a.x + t * a.ld_x + k0;
+                if (a.vec_x) {
+                    q = *reinterpret_cast<const u32x4 *>(from);
+                } else {
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            if (k0 + j < a.n_in)
-                                q[j / 2] |= static_cast<uint32_t>(from[j]) << (16 * (j & 1));
-                    }
+                    for (int j = 0; j < 8; ++j)
+                        if (k0 + j < a.n_in)
+                            q[j / 2] |= static_cast<uint32_t>(from[j]) << (16 * (j & 1));
                 }
-                *reinterpret_cast<u32x4 *>(to + u * 8) = q;
             }
+            *reinterpret_cast<u32x4 *>(to + u * 8) = q;
         }
         if (ch == 0 && h_chunks > 0) {
-            uint16_t *to = a.h_frags + (static_cast<int64_t>(tile) * h_chunks + h_chunks - 1) * kTileChunk;
+            uint16_t *to_h = a.h_frags + (static_cast<int64_t>(tile) * h_chunks + h_chunks - 1) * kTileChunk;
             for (int u = tid; u < 1024; u += 512) {
                 const int k0 = (h_chunks - 1) * kSpan + 128 * ((u & 63) >> 4) + 8 * (u >> 6);
                 if (k0 >= h_from)
-                    *reinterpret_cast<u32x4 *>(to + u * 8) = u32x4{0, 0, 0, 0};
+                    *reinterpret_cast<u32x4 *>(to_h + u * 8) = u32x4{0, 0, 0, 0};
             }
         }
     }
@@ -519,21 +511,47 @@ struct AnyRows {
 };
 
 // The other operand: fragments of TF tiles, in operand order; or (kOne) the one
-// token's row, in the lanes of column 0.
+// token's row, in the lanes of column 0.  Columns without a token lie past the buffer:
+// their lanes get zeros and move nothing (with 16 columns always, an expert that 4 of
+// 16 tokens chose moved 16 KiB of h for 4 KiB of weight).
 template <int TF, bool kOne>
 struct Columns {
-    const uint16_t *at[TF];
-    const uint16_t *row;
-    uint32_t row_bytes, k_lane;
+    const uint16_t *at;
+    uint32_t bytes;
+    uint32_t offset[TF];
 
     __device__ __forceinline__ u32x4 load(int t, int step) const
     {
-        if constexpr (kOne)
-            return __builtin_amdgcn_raw_buffer_load_b128(buffer_from(row, row_bytes), k_lane + 16 * step, 0, 0);
-        else
-            return *reinterpret_cast<const u32x4 *>(at[t] + step * 512);
+        return __builtin_amdgcn_raw_buffer_load_b128(buffer_from(at, bytes), offset[t] + (kOne ? 16 : 1024) * step, 0,
+                                                     0);
     }
 };
+
+// Chunk c of a pass over tiles of `chunks` chunks.
+template <int TF>
+__device__ __forceinline__ Columns<TF, false> tile_columns(const uint16_t *frags, const Pass &p, int chunks, int c,
+                                                           int lane)
+{
+    Columns<TF, false> x;
+    x.at = frags + (static_cast<int64_t>(p.tile) * chunks + c) * kTileChunk;
+    x.bytes = 0x7FFFFFF0;
+#pragma unroll
+    for (int t = 0; t < TF; ++t)
+        x.offset[t] = 16 * t + (lane & 15) < p.columns
+                          ? static_cast<uint32_t>(t) * chunks * (kTileChunk * 2) + lane * 16
+                          : 0x80000000u;
+    return x;
+}
+
+// Chunk c of one row of k values; zeros behind it.
+__device__ __forceinline__ Columns<1, true> row_columns(const uint16_t *row, int64_t k, int c, int lane)
+{
+    Columns<1, true> x;
+    x.at = row;
+    x.bytes = static_cast<uint32_t>(k * 2);
+    x.offset[0] = (lane & 15) == 0 ? (c * kSpan + 128 * (lane >> 4)) * 2 : 0x80000000u;
+    return x;
+}
 
 // Steps that the other operand is loaded ahead; what the registers hold.
 template <int W>
@@ -721,34 +739,25 @@ __global__ __launch_bounds__(64 * WAVES) void moe_gate_up_kernel(MoeArgs a, int3
         __syncthreads();
         n_passes = one.n;
     } else {
-        n_passes = *a.n_units;
+        n_passes = *a.n_passes;
     }
     const int items = n_passes * row_blocks;
     const int step = gridDim.x * WR;
     int next_item = blockIdx.x * WR + wr;
     Pass pass{}, next_pass{};
     Place<TF, kOne> at{}, next{};
-    // chunk c of the pass
     const auto columns = [&](const Pass &p, int c) {
-        Columns<TF, kOne> x{};
-        if constexpr (kOne) {
-            x.row = a.x;
-            x.row_bytes = static_cast<uint32_t>(a.n_in * 2);
-            x.k_lane = (lane & 15) == 0 ? (c * kSpan + 128 * (lane >> 4)) * 2 : 0x80000000u;
-        } else {
-#pragma unroll
-            for (int t = 0; t < TF; ++t)  // past the pass's last tile: that again, unused
-                x.at[t] = a.x_frags + (static_cast<int64_t>(p.x_tile + (t < p.tiles ? t : p.tiles - 1)) * chunks + c) *
-                                          kTileChunk + lane * 8;
-        }
-        return x;
+        if constexpr (kOne)
+            return row_columns(a.x, a.n_in, c, lane);
+        else
+            return tile_columns<TF>(a.x_frags, p, chunks, c, lane);
     };
     const auto enter = [&](int item) {
         const int u = item / row_blocks;
         if constexpr (kOne)
-            next_pass = Pass{one.expert[u], 0, u, 1};
+            next_pass = Pass{one.expert[u], u, 1, 1};
         else
-            next_pass = a.units[u];
+            next_pass = a.passes[u];
         const int row = (item - u * row_blocks) * 16;
         next.rows = RowBlock{static_cast<int64_t>(next_pass.expert) * n_ff + row, n_ff - row < 16 ? n_ff - row : 16};
         next.c = wk;
@@ -810,11 +819,10 @@ __global__ __launch_bounds__(64 * WAVES) void moe_gate_up_kernel(MoeArgs a, int3
                 const u32x2 out = {Half<OUT>::pack2(h[0], h[1]), Half<OUT>::pack2(h[2], h[3])};
                 if constexpr (kOne) {  // a row of its own
                     if ((lane & 15) == 0)
-                        *reinterpret_cast<u32x2 *>(a.h_frags + static_cast<int64_t>(pass.h_tile) * h_chunks * kSpan + k) =
-                            out;
-                } else {
+                        *reinterpret_cast<u32x2 *>(a.h_frags + static_cast<int64_t>(pass.tile) * h_chunks * kSpan + k) = out;
+                } else if (16 * t + (lane & 15) < pass.columns) {
                     const int ch = k / kSpan, in = k % kSpan;
-                    uint16_t *to = a.h_frags + (static_cast<int64_t>(pass.h_tile + t) * h_chunks + ch) * kTileChunk +
+                    uint16_t *to = a.h_frags + (static_cast<int64_t>(pass.tile + t) * h_chunks + ch) * kTileChunk +
                                    (((in & 127) >> 3) * 64 + (in >> 7) * 16 + (lane & 15)) * 8 + (in & 7);
                     *reinterpret_cast<u32x2 *>(to) = out;
                 }
@@ -854,7 +862,7 @@ __global__ __launch_bounds__(64 * WAVES) void moe_down_kernel(MoeArgs a)
         __syncthreads();
         n_passes = one.n;
     } else {
-        n_passes = *a.n_units;
+        n_passes = *a.n_passes;
     }
     const int items = n_passes * chunks;
     const int row_blocks = (n_out + 15) >> 4;
@@ -863,26 +871,18 @@ __global__ __launch_bounds__(64 * WAVES) void moe_down_kernel(MoeArgs a)
     const auto enter = [&](int row_block, int item) {
         const int u = item / chunks;
         if constexpr (kOne)
-            next_pass = Pass{one.expert[u], 0, u, 1};
+            next_pass = Pass{one.expert[u], u, 1, 1};
         else
-            next_pass = a.units[u];
+            next_pass = a.passes[u];
         next.c = item - u * chunks;
         const int row = row_block * 16;
         next.rows = RowBlock{static_cast<int64_t>(next_pass.expert) * n_out + row,
                              n_out - row < 16 ? n_out - row : 16};
-        if constexpr (kOne) {
-            // (zeros behind the row's last k: the products left them out)
-            next.x.row = a.h_frags + static_cast<int64_t>(u) * chunks * kSpan;
-            next.x.row_bytes = static_cast<uint32_t>((a.n_ff + 15) / 16 * 32);
-            next.x.k_lane = (lane & 15) == 0 ? (next.c * kSpan + 128 * (lane >> 4)) * 2 : 0x80000000u;
-        } else {
-#pragma unroll
-            for (int t = 0; t < TF; ++t)
-                next.x.at[t] =
-                    a.h_frags +
-                    (static_cast<int64_t>(next_pass.h_tile + (t < next_pass.tiles ? t : next_pass.tiles - 1)) * chunks +
-                     next.c) * kTileChunk + lane * 8;
-        }
+        if constexpr (kOne)  // (up to the last k that the products wrote)
+            next.x = row_columns(a.h_frags + static_cast<int64_t>(u) * chunks * kSpan, (a.n_ff + 15) / 16 * 16, next.c,
+                                 lane);
+        else
+            next.x = tile_columns<TF>(a.h_frags, next_pass, chunks, next.c, lane);
     };
     Held<Rows, 1, TF> held;
     if (wave < items) {
@@ -909,21 +909,19 @@ __global__ __launch_bounds__(64 * WAVES) void moe_down_kernel(MoeArgs a)
                 enter(row_block + gridDim.x, wave);
             multiply_chunk<OUT, Rows, 1, TF, kOne>(held, src, at, next, scb[0], table, lane_byte, zero_byte, acc, lane);
             // the wave's next pair is of another pass: this one's sums to its tokens
-            if (last || next_pass.h_tile != pass.h_tile) {
+            if (last || next_pass.tile != pass.tile) {
 #pragma unroll
                 for (int t = 0; t < TF; ++t) {
-                    if (t < pass.tiles) {
-                        const int at = (pass.h_tile + t) * 16 + (lane & 15);
-                        const int token = kOne ? ((lane & 15) == 0 ? 0 : -1) : a.token_of[at];
-                        if (token >= 0) {
-                            const float w = kOne ? one.share[pass.h_tile] : a.share_of[at];
-                            f32x4 *to = reinterpret_cast<f32x4 *>(&sums[wave][token][4 * (lane >> 4)]);
-                            f32x4 v = *to;
+                    if (16 * t + (lane & 15) < pass.columns) {
+                        const int place = (pass.tile + t) * 16 + (lane & 15);
+                        const int token = kOne ? 0 : a.token_of[place];
+                        const float w = kOne ? one.share[pass.tile] : a.share_of[place];
+                        f32x4 *to = reinterpret_cast<f32x4 *>(&sums[wave][token][4 * (lane >> 4)]);
+                        f32x4 v = *to;
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                v[i] = v[i] + w * acc[0][t][i];
-                            *to = v;
-                        }
+                        for (int i = 0; i < 4; ++i)
+                            v[i] = v[i] + w * acc[0][t][i];
+                        *to = v;
                     }
                     acc[0][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
                 }
@@ -960,7 +958,7 @@ __global__ __launch_bounds__(64 * WAVES) void moe_down_kernel(MoeArgs a)
 // ---------------------------------------------------------------------------
 // Tiles of a pass over an expert: as many as its share of the tokens is likely to
 // fill, if they spread evenly, up to two (registers); an expert with more takes
-// more passes.  (Up to 16 tokens there is one tile.)
+// more passes.
 int tiles_per_pass(int64_t m, int64_t top_k, int64_t n_experts)
 {
     return m <= 16 || m * top_k <= 8 * n_experts ? 1 : 2;
@@ -969,7 +967,7 @@ int tiles_per_pass(int64_t m, int64_t top_k, int64_t n_experts)
 // What the workspace holds, in this order.
 struct Layout {
     int64_t max_tiles;  // at most this many tiles, and units
-    int64_t units, tokens, shares, x, h, all;
+    int64_t passes, tokens, shares, x, h, all;
 };
 
 Layout layout_of(int64_t n_experts, int64_t n_ff, int64_t n_in, int64_t m, int64_t top_k)
@@ -978,11 +976,11 @@ Layout layout_of(int64_t n_experts, int64_t n_ff, int64_t n_in, int64_t m, int64
     const int64_t pairs = m * top_k;
     // an expert's last tile may hold one token alone
     l.max_tiles = (pairs < n_experts ? pairs : n_experts) + pairs / 16;
-    l.units = 256;
-    l.tokens = l.units + align256(l.max_tiles * static_cast<int64_t>(sizeof(Pass)));
+    l.passes = 256;
+    l.tokens = l.passes + align256(l.max_tiles * static_cast<int64_t>(sizeof(Pass)));
     l.shares = l.tokens + align256(l.max_tiles * 64);
     l.x = l.shares + align256(l.max_tiles * 64);
-    l.h = l.x + (m <= 16 ? 1 : l.max_tiles) * ceil_div(n_in, kSpan) * kTileChunk * 2;
+    l.h = l.x + l.max_tiles * ceil_div(n_in, kSpan) * kTileChunk * 2;
     l.all = l.h + l.max_tiles * ceil_div(n_ff, kSpan) * kTileChunk * 2;
     return l;
 }
@@ -1168,8 +1166,8 @@ dq4_status_t dq4_moe_fused(const dq4_weight_t *gate, const dq4_weight_t *up, con
     a.vec_x = rows_aligned(x, ld_x, m, n_in);
     a.vec_y = rows_aligned(y, ld_y, m, 8) && (!residual || rows_aligned(residual, ld_residual, m, 8));
     a.max_tiles = static_cast<int32_t>(l.max_tiles);
-    a.n_units = reinterpret_cast<int32_t *>(ws);
-    a.units = reinterpret_cast<Pass *>(ws + l.units);
+    a.n_passes = reinterpret_cast<int32_t *>(ws);
+    a.passes = reinterpret_cast<Pass *>(ws + l.passes);
     a.token_of = reinterpret_cast<int32_t *>(ws + l.tokens);
     a.share_of = reinterpret_cast<float *>(ws + l.shares);
     a.x_frags = reinterpret_cast<uint16_t *>(ws + l.x);

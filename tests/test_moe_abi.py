@@ -64,8 +64,8 @@ def test_workspace_sizes(lib):
     for bad in ((0, 32, 64, 4, 2), (4, -1, 64, 4, 2), (4, 32, 0, 4, 2), (4, 32, 64, 0, 2), (4, 32, 64, 4, 0),
                 (513, 32, 64, 4, 2), (4, 32, 64, 65, 2), (4, 32, 64, 4, 17)):
         assert f(*bad) == 0, bad
-    # one tile of x (512 k a chunk, 16 KiB) and a tile of h per expert
-    assert f(64, 1024, 2048, 1, 8) == 256 + 256 + 512 + 512 + 4 * 16384 + 8 * 2 * 16384
+    # a tile of x (512 k a chunk, 16 KiB) and one of h for each expert
+    assert f(64, 1024, 2048, 1, 8) == 256 + 256 + 512 + 512 + 8 * 4 * 16384 + 8 * 2 * 16384
     # 64 tokens: a tile per expert and one more for every 16 choices
     assert f(8, 512, 512, 64, 2) == 256 + 256 + 2 * 1024 + 16 * 16384 + 16 * 16384
     assert f(512, 1 << 10, 1 << 10, 64, 16) > 0
