@@ -41,7 +41,7 @@ cannot be loaded, every call raises.
     dq4_moe_route(x, router, top_k) -> (ids, weights)           (a token's experts)
     dq4_moe_fused(gate, up, down, ..., x, ids, weights) -> tensor
                                                    (a mixture-of-experts layer, few tokens)
-    dq4_moe_fused_workspace_bytes(n_experts, n_ff, n_in, m, top_k) -> int
+    dq4_moe_{route,fused}_workspace_bytes(...) -> int
     dq4_int8_prep(A, CB, SCB, cols) -> (subA, subB)  (LLM.int8 correction operands)
     dq4_memory_twin_f16(packed, n) -> tensor       (diagnostic: the FP16 call's memory
                                                    traffic without its arithmetic)
@@ -160,7 +160,9 @@ def library() -> ctypes.CDLL:
     lib.dq4_int8_linear_backward_workspace_bytes.argtypes = [i64, i64, i64, P, i64]
     for name in ("dq4_int8_quant", "dq4_int8_linear", "dq4_int8_linear_backward"):
         getattr(lib, name + "_workspace_bytes").restype = i64
-    lib.dq4_moe_route.argtypes = [P, i64, i64, i64, i32, P, P, i32, i32, i32, P, P, P]
+    lib.dq4_moe_route.argtypes = [P, i64, i64, i64, i32, P, P, i32, i32, i32, P, P, P, i64, P]
+    lib.dq4_moe_route_workspace_bytes.argtypes = [i64, i32]
+    lib.dq4_moe_route_workspace_bytes.restype = i64
     lib.dq4_moe_fused.argtypes = [W, W, W, i32, i64, i64, i32, i32, P, i64, i64, P, P, i32, P, i64, P,
                                   i64, P, i64, P]
     for name in ("dq4_moe_route", "dq4_moe_fused"):
@@ -1244,6 +1246,10 @@ def dq4_int8_linear_backward(dy, CB, SCB, bias_grad: bool = False, dx=None, dbia
 # ----------------------------------------------------------------------------
 # a mixture-of-experts layer for a few tokens (include/dq4_moe.h)
 # ----------------------------------------------------------------------------
+def dq4_moe_route_workspace_bytes(m: int, n_experts: int) -> int:
+    return int(library().dq4_moe_route_workspace_bytes(int(m), int(n_experts)))
+
+
 def dq4_moe_fused_workspace_bytes(n_experts: int, n_ff: int, n_in: int, m: int, top_k: int) -> int:
     return int(library().dq4_moe_fused_workspace_bytes(int(n_experts), int(n_ff), int(n_in), int(m),
                                                        int(top_k)))
@@ -1255,7 +1261,7 @@ def _dense(t, name: str, shape, dtype, device):
 
 
 def dq4_moe_route(x, router, top_k: int, bias=None, renormalize: bool = True, ids=None, weights=None,
-                  stream=None):
+                  workspace=None, stream=None):
     """The top_k experts of each row of x and their weights: (ids, weights).
 
     x: (m, n_in), router: (n_experts, n_in), one of float16 and bfloat16; bias:
@@ -1287,15 +1293,14 @@ def dq4_moe_route(x, router, top_k: int, bias=None, renormalize: bool = True, id
         weights = _output((m, top_k), torch.float32, device, stream)
     _dense(ids, "ids", (m, top_k), torch.int32, device)
     _dense(weights, "weights", (m, top_k), torch.float32, device)
-    if given:
-        _refuse_overlap([("ids", ids), ("weights", weights)], [("x", x), ("router", router), ("bias", bias)], (), 0)
+    if given or workspace is not None:
+        _refuse_overlap([("ids", ids), ("weights", weights)], [("x", x), ("router", router), ("bias", bias)], (), 0,
+                        workspace, given)
     with _on_device(device):
-        handle = (_own_stream(device, stream).cuda_stream if stream is not None
-                  else torch._C._cuda_getCurrentRawStream(device.index))
-        st = library().dq4_moe_route(x.data_ptr(), m, n_in, ld_x, code, router.data_ptr(), _address(bias), n_experts,
-                                     top_k, 1 if renormalize else 0, ids.data_ptr(), weights.data_ptr(), handle)
-    if st != DQ4_OK:
-        _raise_for(st, "dq4_moe_route")
+        _launch_sized("dq4_moe_route", device, stream, workspace,
+                      library().dq4_moe_route_workspace_bytes(m, n_experts),
+                      x.data_ptr(), m, n_in, ld_x, code, router.data_ptr(), _address(bias), n_experts, top_k,
+                      1 if renormalize else 0, ids.data_ptr(), weights.data_ptr())
     return ids, weights
 
 

@@ -51,84 +51,103 @@ struct RouteArgs {
     const float *bias;
     int32_t n_experts, top_k, renormalize;
     int32_t vec;
+    double *logits;  // m x n_experts
     int32_t *ids;
     float *weights;
 };
 
-// A token per workgroup.  A wave takes every 16th expert, four at a time; the
-// products are exact in FP32 and their sums run in 64 bits, since the choice
-// between two experts hangs on the last place.  An expert's rank is the number of
-// experts before it.  Bound by the reading of the router's matrix from cache by
-// one CU (64 experts x 2048: 256 KiB).
-constexpr int kRouteWaves = 16, kRouteExperts = 4;
-
-template <int OUT>
-__global__ __launch_bounds__(64 * kRouteWaves) void moe_route_kernel(RouteArgs a)
+// Logits.  kExperts = 1: a workgroup for one token and expert, its waves share k.
+// kExperts = 4: a wave for one token and four experts, so that x is read less often.
+// The products are exact in FP32 and their sums run in 64 bits, since the choice
+// between two experts hangs on the last place.  (One workgroup per token for
+// everything took 16.6 us for 64 experts x 2048: the conversions to 64 bits on one CU.)
+template <int OUT, int kExperts>
+__global__ __launch_bounds__(256) void moe_logits_kernel(RouteArgs a)
 {
-    __shared__ double logit[kMaxExperts];
+    __shared__ double part[4];
+    constexpr int kWaves = kExperts == 1 ? 4 : 1;  // that share an item
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int k = static_cast<int>(a.n_in), E = a.n_experts;
+    const int groups = (E + kExperts - 1) / kExperts;
+    const int64_t items = a.m * groups;
+    for (int64_t item = static_cast<int64_t>(blockIdx.x) * (4 / kWaves) + wave / kWaves; item < items;
+         item += static_cast<int64_t>(gridDim.x) * (4 / kWaves)) {
+        const int64_t t = static_cast<uint32_t>(item) / static_cast<uint32_t>(groups);
+        const int e0 = static_cast<int>(item - t * groups) * kExperts;
+        const uint16_t *x = a.x + t * a.ld_x;
+        double sum[kExperts] = {};
+#pragma unroll 4
+        for (int c = (wave % kWaves * 64 + lane) * 8; c < k; c += kWaves * 512) {
+            const int valid = k - c < 8 ? k - c : 8;
+            float xv[8];
+            load_values<OUT, 8>(x + c, a.vec, valid, xv);
+#pragma unroll
+            for (int q = 0; q < kExperts; ++q) {
+                const int e = e0 + q < E ? e0 + q : E - 1;
+                float r[8];
+                load_values<OUT, 8>(a.router + static_cast<int64_t>(e) * k + c, a.vec, valid, r);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    sum[q] = sum[q] + static_cast<double>(xv[j] * r[j]);
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < kExperts; ++q) {
+#pragma unroll
+            for (int d = 32; d > 0; d /= 2)
+                sum[q] = sum[q] + __shfl_xor(sum[q], d);
+            if constexpr (kWaves == 4) {
+                if (lane == 0)
+                    part[wave] = sum[q];
+                __syncthreads();
+                sum[q] = part[0] + part[1] + part[2] + part[3];
+                __syncthreads();
+            }
+            if (lane == 0 && wave % kWaves == 0 && e0 + q < E)
+                a.logits[t * E + e0 + q] = a.bias ? sum[q] + static_cast<double>(a.bias[e0 + q]) : sum[q];
+        }
+    }
+}
+
+// A token per workgroup, a thread per expert: an expert's rank is the number of
+// experts before it.
+__global__ __launch_bounds__(kMaxExperts) void moe_select_kernel(RouteArgs a)
+{
+    __shared__ __attribute__((aligned(16))) double logit[kMaxExperts];
     __shared__ double best[kMaxTopK];
     __shared__ float share[kMaxExperts];
-    __shared__ int any_nan;
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int E = a.n_experts;
-    const int k = static_cast<int>(a.n_in);
+    __shared__ int masked, any_nan;
+    const int tid = threadIdx.x;
+    const int E = a.n_experts, padded = (E + 63) & ~63;  // the workgroup's threads
+    const double minus_infinity = -__builtin_inf();
     for (int64_t t = blockIdx.x; t < a.m; t += gridDim.x) {
-        const uint16_t *x = a.x + t * a.ld_x;
-        for (int e0 = wave * kRouteExperts; e0 < E; e0 += kRouteWaves * kRouteExperts) {
-            double sum[kRouteExperts] = {};
-            for (int c = lane * 8; c < k; c += 512) {
-                const int valid = k - c < 8 ? k - c : 8;
-                float xv[8];
-                load_values<OUT, 8>(x + c, a.vec, valid, xv);
-#pragma unroll
-                for (int q = 0; q < kRouteExperts; ++q) {
-                    const int e = e0 + q < E ? e0 + q : E - 1;
-                    float r[8];
-                    load_values<OUT, 8>(a.router + static_cast<int64_t>(e) * k + c, a.vec, valid, r);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        sum[q] = sum[q] + static_cast<double>(xv[j] * r[j]);
-                }
-            }
-#pragma unroll
-            for (int q = 0; q < kRouteExperts; ++q) {
-#pragma unroll
-                for (int d = 32; d > 0; d /= 2)
-                    sum[q] = sum[q] + __shfl_xor(sum[q], d);
-                if (lane == 0 && e0 + q < E)
-                    logit[e0 + q] = a.bias ? sum[q] + static_cast<double>(a.bias[e0 + q]) : sum[q];
-            }
-        }
+        const double mine = tid < E ? a.logits[t * E + tid] : minus_infinity;
+        logit[tid] = mine;
         if (tid == 0)
-            any_nan = 0;
+            masked = any_nan = 0;
         __syncthreads();
-        const double minus_infinity = -__builtin_inf();
-        if (tid < E) {
-            const double mine = logit[tid];
-            const bool nan = mine != mine;
-            if (nan)
-                any_nan = 1;
-            int rank = 0;
-            for (int e = 0; e < E; ++e) {
-                const double other = logit[e];
-                const bool before = nan ? other == other ? other != minus_infinity : e < tid
-                                        : other > mine || (other == mine && e < tid);
-                rank += before ? 1 : 0;
-            }
-            if (mine != minus_infinity && rank < a.top_k) {
-                a.ids[t * a.top_k + rank] = tid;
-                best[rank] = mine;
-            }
+        const bool nan = mine != mine;
+        int rank = 0;
+#pragma unroll 8
+        for (int e = 0; e < padded; ++e) {
+            const double other = logit[e];
+            const bool before = nan ? (other == other ? other != minus_infinity : e < tid)
+                                    : other > mine || (other == mine && e < tid);
+            rank += before ? 1 : 0;
         }
-        // places that no expert is left for: as many experts as are not masked
-        int chosen = 0;
-        for (int e = 0; e < E && chosen < a.top_k; ++e)
-            chosen += logit[e] != minus_infinity ? 1 : 0;
+        if (nan)
+            any_nan = 1;
+        if (mine == minus_infinity && tid < E)
+            atomicAdd(&masked, 1);
+        if (mine != minus_infinity && rank < a.top_k) {
+            a.ids[t * a.top_k + rank] = tid;
+            best[rank] = mine;
+        }
         __syncthreads();
+        // as many places as there are experts left
+        const int chosen = E - masked < a.top_k ? E - masked : a.top_k;
         const double top = chosen > 0 ? best[0] : 0.0;
-        if (tid < E)
-            share[tid] = exp_f32(static_cast<float>(logit[tid] - top));
+        share[tid] = exp_f32(static_cast<float>(mine - top));
         __syncthreads();
         if (tid < a.top_k) {
             float total = 0.0f;
@@ -136,7 +155,8 @@ __global__ __launch_bounds__(64 * kRouteWaves) void moe_route_kernel(RouteArgs a
                 for (int j = 0; j < chosen; ++j)
                     total = total + exp_f32(static_cast<float>(best[j] - top));
             } else {
-                for (int e = 0; e < E; ++e)
+#pragma unroll 8
+                for (int e = 0; e < padded; ++e)
                     total = total + share[e];
             }
             float w = 0.0f;
@@ -1072,9 +1092,17 @@ using namespace dq4;
 
 extern "C" {
 
+int64_t dq4_moe_route_workspace_bytes(int64_t m, int32_t n_experts)
+{
+    if (m <= 0 || n_experts <= 0 || m > kMaxRows || n_experts > kMaxExperts)
+        return 0;
+    return align256(m * n_experts * 8);
+}
+
 dq4_status_t dq4_moe_route(const void *x, int64_t m, int64_t n_in, int64_t ld_x, int32_t dtype,
                            const void *router, const float *bias, int32_t n_experts, int32_t top_k,
-                           int32_t renormalize, int32_t *ids, float *weights, void *stream)
+                           int32_t renormalize, int32_t *ids, float *weights, void *workspace,
+                           int64_t workspace_bytes, void *stream)
 {
     if (m < 0 || n_in < 0 || n_experts < 0 || (dtype != DQ4_F16 && dtype != DQ4_BF16) || top_k < 1 ||
         top_k > n_experts)
@@ -1083,7 +1111,8 @@ dq4_status_t dq4_moe_route(const void *x, int64_t m, int64_t n_in, int64_t ld_x,
         return DQ4_EUNSUPPORTED;
     if (m == 0)
         return DQ4_OK;
-    if (!ids || !weights || (n_in > 0 && (!x || !router)) || bad_ld(ld_x, m, n_in))
+    if (!ids || !weights || (n_in > 0 && (!x || !router)) || bad_ld(ld_x, m, n_in) ||
+        workspace_bytes < dq4_moe_route_workspace_bytes(m, n_experts) || bad_workspace(workspace, workspace_bytes))
         return DQ4_EINVAL;
     RouteArgs a{};
     a.x = static_cast<const uint16_t *>(x);
@@ -1096,13 +1125,23 @@ dq4_status_t dq4_moe_route(const void *x, int64_t m, int64_t n_in, int64_t ld_x,
     a.top_k = top_k;
     a.renormalize = renormalize != 0;
     a.vec = rows_aligned(x, ld_x, m, n_in) && reinterpret_cast<uintptr_t>(router) % 16 == 0;
+    a.logits = static_cast<double *>(workspace);
     a.ids = ids;
     a.weights = weights;
     void *params[] = {&a};
-    const int64_t most = current_compute_units() * int64_t{8};
-    return launch(dtype == DQ4_F16 ? reinterpret_cast<const void *>(&moe_route_kernel<DQ4_F16>)
-                                   : reinterpret_cast<const void *>(&moe_route_kernel<DQ4_BF16>),
-                  m < most ? m : most, 1, 64 * kRouteWaves, params, static_cast<hipStream_t>(stream));
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    const int64_t cus = current_compute_units();
+    const bool four = m * n_experts > cus * 16;
+    const int64_t groups = four ? ceil_div(m * ceil_div(n_experts, 4), 4) : m * n_experts;
+    const void *kernel = dtype == DQ4_F16 ? (four ? reinterpret_cast<const void *>(&moe_logits_kernel<DQ4_F16, 4>)
+                                                  : reinterpret_cast<const void *>(&moe_logits_kernel<DQ4_F16, 1>))
+                                          : (four ? reinterpret_cast<const void *>(&moe_logits_kernel<DQ4_BF16, 4>)
+                                                  : reinterpret_cast<const void *>(&moe_logits_kernel<DQ4_BF16, 1>));
+    const dq4_status_t st = launch(kernel, groups < cus * 8 ? groups : cus * 8, 1, 256, params, s);
+    if (st != DQ4_OK)
+        return st;
+    return launch(reinterpret_cast<const void *>(&moe_select_kernel), m < cus * 8 ? m : cus * 8, 1,
+                  static_cast<int>(ceil_div(n_experts, 64)) * 64, params, s);
 }
 
 int64_t dq4_moe_fused_workspace_bytes(int32_t n_experts, int64_t n_ff, int64_t n_in, int64_t m, int32_t top_k)

@@ -26,7 +26,7 @@
  * is refused for it here; the Python binding does.)
  *
  * workspace: caller-owned device memory, 256-byte aligned, of at least the
- * bytes that dq4_moe_fused_workspace_bytes returns.  Its contents do not matter
+ * bytes that the call's *_workspace_bytes function returns.  Its contents do not matter
  * before the call, and after it the workspace holds nothing of use.  Calls that
  * may overlap in time must not share one.
  *
@@ -70,7 +70,11 @@ extern "C" {
  */
 dq4_status_t dq4_moe_route(const void *x, int64_t m, int64_t n_in, int64_t ld_x, int32_t dtype,
                            const void *router, const float *bias, int32_t n_experts, int32_t top_k,
-                           int32_t renormalize, int32_t *ids, float *weights, void *stream);
+                           int32_t renormalize, int32_t *ids, float *weights, void *workspace,
+                           int64_t workspace_bytes, void *stream);
+
+/* 0 for sizes the call rejects.  Host only. */
+int64_t dq4_moe_route_workspace_bytes(int64_t m, int32_t n_experts);
 
 /*
  * x: m x n_in.  ids, weights: m x top_k, dense, as dq4_moe_route writes them or

@@ -21,18 +21,21 @@ def lib():
 
 def test_exports_every_declared_function(lib):
     names = dq4.header_functions(dq4.MOE_HEADER_PATH)
-    assert set(names) == {"dq4_moe_route", "dq4_moe_fused", "dq4_moe_fused_workspace_bytes"}
+    assert set(names) == {"dq4_moe_route", "dq4_moe_fused", "dq4_moe_route_workspace_bytes",
+                          "dq4_moe_fused_workspace_bytes"}
     for name in names:
         assert hasattr(lib, name), name
         assert callable(getattr(dq4, name)), name
 
 
 def test_route_validation(lib):
-    def call(x=ONE, m=4, n=64, ld=64, dtype=dq4.DQ4_F16, router=ONE, bias=None, E=8, k=2, ids=ONE, weights=ONE):
-        return lib.dq4_moe_route(x, m, n, ld, dtype, router, bias, E, k, 1, ids, weights, None)
+    def call(x=ONE, m=4, n=64, ld=64, dtype=dq4.DQ4_F16, router=ONE, bias=None, E=8, k=2, ids=ONE, weights=ONE,
+             ws=ONE, ws_bytes=BIG):
+        return lib.dq4_moe_route(x, m, n, ld, dtype, router, bias, E, k, 1, ids, weights, ws, ws_bytes, None)
     assert call(m=0) == dq4.DQ4_OK
     for k in (dict(m=-1), dict(n=-1), dict(E=-1), dict(E=0), dict(k=0), dict(k=9), dict(dtype=0), dict(dtype=3),
-              dict(x=None), dict(router=None), dict(ids=None), dict(weights=None), dict(ld=63), dict(ld=1 << 62)):
+              dict(x=None), dict(router=None), dict(ids=None), dict(weights=None), dict(ld=63), dict(ld=1 << 62), dict(ws=None),
+              dict(ws=P(16)), dict(ws_bytes=255)):
         assert call(**k) == dq4.DQ4_EINVAL, k
     for k in (dict(E=513), dict(E=20, k=17), dict(m=(1 << 21) + 1), dict(n=(1 << 17) + 1, ld=1 << 18)):
         assert call(**k) == dq4.DQ4_EUNSUPPORTED, k
@@ -69,6 +72,8 @@ def test_workspace_sizes(lib):
     # 64 tokens: a tile per expert and one more for every 16 choices
     assert f(8, 512, 512, 64, 2) == 256 + 256 + 2 * 1024 + 16 * 16384 + 16 * 16384
     assert f(512, 1 << 10, 1 << 10, 64, 16) > 0
+    g = lib.dq4_moe_route_workspace_bytes
+    assert g(1, 8) == 256 and g(100, 64) == 51200 and g(0, 8) == 0 and g(4, 513) == 0 and g((1 << 21) + 1, 8) == 0
 
 
 def test_binding_rejects_host_tensors(lib):
