@@ -415,7 +415,8 @@ __global__ __launch_bounds__(kThreads) void weight_fragments_kernel(FragmentArgs
 // values, laid out as in the backward decode above.  kAligned: 8 codes of a row are
 // an aligned 8-byte load; otherwise they are cut out of three dwords (the dword
 // with the weight's last byte is read whole, nothing beyond it).  Bound by memory:
-// 1 byte read and 2 written per element.
+// 1 byte read and 2 written per element (11008 x 4096: 33 us, 4.1 TB/s).  Workgroups
+// behind these do the call's work beside the decode, as above.
 struct Int8FragmentArgs {
     const int8_t *codes;
     const float *scales;
@@ -424,9 +425,16 @@ struct Int8FragmentArgs {
     int32_t groups, chunks;
 };
 
-template <int OUT, bool kAligned>
-__global__ __launch_bounds__(kThreads) void int8_column_fragments_kernel(Int8FragmentArgs a)
+template <int OUT, bool kAligned, int kBeside>
+__global__ __launch_bounds__(kThreads) void int8_column_fragments_kernel(Int8FragmentArgs a, BesideArgs b)
 {
+    if constexpr (kBeside != kNothing) {
+        const int first = static_cast<int>(gridDim.x) - b.blocks;
+        if (static_cast<int>(blockIdx.x) >= first) {
+            work_beside<OUT, kBeside>(b, static_cast<int>(blockIdx.x) - first);
+            return;
+        }
+    }
     constexpr float kR127 = 0x1.020408p-7f;  // the FP32 value nearest 1/127
     const int tid = threadIdx.x;
     const int pair = blockIdx.x / a.chunks, chunk = blockIdx.x - pair * a.chunks;
@@ -2937,11 +2945,24 @@ dq4_status_t run_product(const Shape &sh, const dq4_weight_t *w0, const dq4_weig
     return DQ4_OK;
 }
 
+template <int OUT>
+const void *int8_fragments_kernel(bool aligned, Beside kind)
+{
+    if (kind == kSlopes8)
+        return aligned ? reinterpret_cast<const void *>(&int8_column_fragments_kernel<OUT, true, kSlopes8>)
+                       : reinterpret_cast<const void *>(&int8_column_fragments_kernel<OUT, false, kSlopes8>);
+    if (kind == kSlopes1)
+        return aligned ? reinterpret_cast<const void *>(&int8_column_fragments_kernel<OUT, true, kSlopes1>)
+                       : reinterpret_cast<const void *>(&int8_column_fragments_kernel<OUT, false, kSlopes1>);
+    return aligned ? reinterpret_cast<const void *>(&int8_column_fragments_kernel<OUT, true, kNothing>)
+                   : reinterpret_cast<const void *>(&int8_column_fragments_kernel<OUT, false, kNothing>);
+}
+
 // dx = dy W for an LLM.int8 weight: its columns to 16-bit fragments, then the
 // product.
 template <int OUT>
 dq4_status_t run_int8_columns(const Shape &sh, const int8_t *codes, const float *scales, ProductArgs p,
-                              const BesideWork &beside, uint8_t *ws, hipStream_t s)
+                              BesideWork beside, uint8_t *ws, hipStream_t s)
 {
     int device = 0;
     const hipError_t e = hipGetDevice(&device);
@@ -2949,10 +2970,11 @@ dq4_status_t run_int8_columns(const Shape &sh, const int8_t *codes, const float 
         return hip_failed(e);
     const int cus = compute_units(device);
     const Plan plan = sh.plan(cus);
-    if (beside.kind != kNothing) {
+    if (beside.args.blocks > kMostBeside) {
         const dq4_status_t st = launch_fragments<OUT, false>(FragmentArgs{}, true, beside, cus, s);
         if (st != DQ4_OK)
             return st;
+        beside = BesideWork{kNothing, {}};
     }
     p.m = sh.m;
     p.n = sh.n;
@@ -2972,11 +2994,9 @@ dq4_status_t run_int8_columns(const Shape &sh, const int8_t *codes, const float 
     p.wfrag = f.out;
     if (f.chunks > 0) {
         const bool aligned = sh.n % 8 == 0 && reinterpret_cast<uintptr_t>(codes) % 8 == 0;
-        void *params[] = {&f};
-        const dq4_status_t st =
-            launch(aligned ? reinterpret_cast<const void *>(&int8_column_fragments_kernel<OUT, true>)
-                           : reinterpret_cast<const void *>(&int8_column_fragments_kernel<OUT, false>),
-                   ceil_div(sh.groups(), 2) * f.chunks, 1, kThreads, params, s);
+        void *params[] = {&f, &beside.args};
+        const dq4_status_t st = launch(int8_fragments_kernel<OUT>(aligned, beside.kind),
+                                       ceil_div(sh.groups(), 2) * f.chunks + beside.args.blocks, 1, kThreads, params, s);
         if (st != DQ4_OK)
             return st;
     }
