@@ -730,6 +730,47 @@ __device__ __forceinline__ void plan_one(const MoeArgs &a, OnePlan &p)
         p.n = __builtin_popcountll(mask);
 }
 
+// The tables in two parts.  A workgroup's first loads of weight go out between them:
+// behind those, what waits for the codebooks would wait for the weight too (one token,
+// 8 of 64 experts of 1024 x 2048: 7.5 of the gate and up kernel's 14 us).
+template <int kWeights, int kTables>
+__device__ __forceinline__ void store_codebooks(const Codebooks &c, uint8_t *table, float (&scb)[kWeights][256],
+                                                float (&cb4)[kWeights][16])
+{
+    const int tid = threadIdx.x, threads = blockDim.x;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const int i = tid + q * threads;
+        if (i < kWeights * 256)
+            scb[i >> 8][i & 255] = c.scb[q];
+    }
+    if (tid < kWeights * 16)
+        cb4[tid >> 4][tid & 15] = c.cb4;
+    if (tid < 64)
+        *reinterpret_cast<uint32_t *>(&table[kTables * kPairTableBytes + tid * 4]) = 0;
+}
+
+// A thread writes two neighbours of a pair's 32 places, one of each weight where two
+// share a table; its first value is always the same.
+template <int THREADS, int kWeights, int kTables>
+__device__ __forceinline__ void fill_pairs(uint8_t *table, const float (&cb4)[kWeights][16])
+{
+    static_assert(THREADS % 256 == 0 && 4096 % THREADS == 0, "a thread keeps its first value");
+    const int tid = threadIdx.x;
+    constexpr bool kShared = kWeights == 2 && kTables == 1;
+    float first[kWeights];
+#pragma unroll
+    for (int w = 0; w < kWeights; ++w)
+        first[w] = cb4[w][(tid >> 4) & 15];
+#pragma unroll
+    for (int q = 0; q < kTables * 4096 / THREADS; ++q) {
+        const int which = q * THREADS / 4096, second = (tid >> 8) + q * THREADS % 4096 / 256;
+        *reinterpret_cast<f32x4 *>(&table[(tid + q * THREADS) * 16]) =
+            f32x4{first[which], cb4[which][second], first[kShared ? 1 : which], cb4[kShared ? 1 : which][second]};
+    }
+    lds_barrier();
+}
+
 // ---------------------------------------------------------------------------
 // gate and up
 // ---------------------------------------------------------------------------
@@ -766,13 +807,14 @@ __global__ __launch_bounds__(64 * WAVES) void moe_gate_up_kernel(MoeArgs a, int3
 
     const Codebooks codebooks = fetch_codebooks<2>(a.w);
     int n_passes;
-    if constexpr (kOne) {
+    if constexpr (kOne)
         plan_one(a, one);
-        __syncthreads();
-        n_passes = one.n;
-    } else {
+    else
         n_passes = *a.n_passes;
-    }
+    store_codebooks<2, kTables>(codebooks, table, scb, cb4);
+    __syncthreads();
+    if constexpr (kOne)
+        n_passes = one.n;
     const int items = n_passes * row_blocks;
     const int step = gridDim.x * WR;
     int next_item = blockIdx.x * WR + wr;
@@ -796,11 +838,13 @@ __global__ __launch_bounds__(64 * WAVES) void moe_gate_up_kernel(MoeArgs a, int3
         next.x = columns(next_pass, wk);
     };
     Held<Rows, W, TF> held;
-    if (next_item < items) {
+    // (without a branch around the loads: what waits for some where branches meet waits
+    // for them all; no rows, no columns: nothing is moved)
+    next.x = columns(Pass{0, 0, 0, 0}, 0);
+    if (next_item < items)
         enter(next_item);
-        held.load_first(src, next.rows, next.c, next.x, lane);
-    }
-    fill_tables<2, kTables>(codebooks, table, scb, cb4);
+    held.load_first(src, next.rows, next.c, next.x, lane);
+    fill_pairs<64 * WAVES, 2, kTables>(table, cb4);
     const uint32_t copy = W == 2 ? (lane & 15) * 16 : (lane & 31) * 8;
     const uint32_t lane_byte = copy + which * kPairTableBytes, zero_byte = copy % 248 + kTables * kPairTableBytes;
 
@@ -889,17 +933,24 @@ __global__ __launch_bounds__(64 * WAVES) void moe_down_kernel(MoeArgs a)
 
     const Codebooks codebooks = fetch_codebooks<1>(both);
     int n_passes;
-    if constexpr (kOne) {
+    if constexpr (kOne)
         plan_one(a, one);
-        __syncthreads();
-        n_passes = one.n;
-    } else {
+    else
         n_passes = *a.n_passes;
-    }
+    store_codebooks<1, 1>(codebooks, table, scb, cb4);
+    __syncthreads();
+    if constexpr (kOne)
+        n_passes = one.n;
     const int items = n_passes * chunks;
     const int row_blocks = (n_out + 15) >> 4;
     Pass next_pass{};
     Place<TF, kOne> at{}, next{};
+    const auto columns = [&](const Pass &p, int c) {
+        if constexpr (kOne)  // (up to the last k that the products wrote)
+            return row_columns(a.h_frags + static_cast<int64_t>(p.tile) * chunks * kSpan, (a.n_ff + 15) / 16 * 16, c, lane);
+        else
+            return tile_columns<TF>(a.h_frags, p, chunks, c, lane);
+    };
     const auto enter = [&](int row_block, int item) {
         const int u = item / chunks;
         if constexpr (kOne)
@@ -910,18 +961,14 @@ __global__ __launch_bounds__(64 * WAVES) void moe_down_kernel(MoeArgs a)
         const int row = row_block * 16;
         next.rows = RowBlock{static_cast<int64_t>(next_pass.expert) * n_out + row,
                              n_out - row < 16 ? n_out - row : 16};
-        if constexpr (kOne)  // (up to the last k that the products wrote)
-            next.x = row_columns(a.h_frags + static_cast<int64_t>(u) * chunks * kSpan, (a.n_ff + 15) / 16 * 16, next.c,
-                                 lane);
-        else
-            next.x = tile_columns<TF>(a.h_frags, next_pass, chunks, next.c, lane);
+        next.x = columns(next_pass, next.c);
     };
     Held<Rows, 1, TF> held;
-    if (wave < items) {
+    next.x = columns(Pass{0, 0, 0, 0}, 0);
+    if (wave < items)
         enter(blockIdx.x, wave);
-        held.load_first(src, next.rows, next.c, next.x, lane);
-    }
-    fill_tables<1, 1>(codebooks, table, scb, cb4);
+    held.load_first(src, next.rows, next.c, next.x, lane);
+    fill_pairs<64 * WAVES, 1, 1>(table, cb4);
     const uint32_t lane_byte = (lane & 31) * 8, zero_byte = lane_byte + kPairTableBytes;
 
     for (int row_block = blockIdx.x; row_block < row_blocks; row_block += gridDim.x) {
