@@ -110,11 +110,21 @@ __global__ __launch_bounds__(256) void moe_logits_kernel(RouteArgs a)
     }
 }
 
+// A logit as a whole number in the same order: -infinity, NaN, the values upwards.
+constexpr uint64_t kMasked = 0x000FFFFFFFFFFFFFull;
+
+__device__ __forceinline__ uint64_t key_of(double logit)
+{
+    const uint64_t bits = __builtin_bit_cast(uint64_t, logit + 0.0);  // -0 is 0
+    const uint64_t key = bits >> 63 ? ~bits : bits | 0x8000000000000000ull;
+    return logit != logit ? kMasked + 1 : key;
+}
+
 // A token per workgroup, a thread per expert: an expert's rank is the number of
 // experts before it.
 __global__ __launch_bounds__(kMaxExperts) void moe_select_kernel(RouteArgs a)
 {
-    __shared__ __attribute__((aligned(16))) double logit[kMaxExperts];
+    __shared__ __attribute__((aligned(16))) uint64_t keys[kMaxExperts];
     __shared__ double best[kMaxTopK];
     __shared__ float share[kMaxExperts];
     __shared__ int masked, any_nan;
@@ -123,24 +133,21 @@ __global__ __launch_bounds__(kMaxExperts) void moe_select_kernel(RouteArgs a)
     const double minus_infinity = -__builtin_inf();
     for (int64_t t = blockIdx.x; t < a.m; t += gridDim.x) {
         const double mine = tid < E ? a.logits[t * E + tid] : minus_infinity;
-        logit[tid] = mine;
+        const uint64_t key = tid < E ? key_of(mine) : 0;
+        keys[tid] = key;
         if (tid == 0)
             masked = any_nan = 0;
         __syncthreads();
         const bool nan = mine != mine;
         int rank = 0;
-#pragma unroll 8
-        for (int e = 0; e < padded; ++e) {
-            const double other = logit[e];
-            const bool before = nan ? (other == other ? other != minus_infinity : e < tid)
-                                    : other > mine || (other == mine && e < tid);
-            rank += before ? 1 : 0;
-        }
+#pragma unroll 16
+        for (int e = 0; e < padded; ++e)
+            rank += keys[e] >= (e < tid ? key : key + 1) ? 1 : 0;
         if (nan)
             any_nan = 1;
-        if (mine == minus_infinity && tid < E)
+        if (key == kMasked)
             atomicAdd(&masked, 1);
-        if (mine != minus_infinity && rank < a.top_k) {
+        if (key > kMasked && rank < a.top_k) {
             a.ids[t * a.top_k + rank] = tid;
             best[rank] = mine;
         }
