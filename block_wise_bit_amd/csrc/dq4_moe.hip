@@ -3,10 +3,18 @@
 // weights.
 //
 // Few tokens choose few experts, and each chosen expert's matrices are read once:
-// the layer is bound by that and by the decode.  Four launches: the router, a
-// plan (which experts, which tokens each, and x in operand fragments), the gate
-// and up products of every chosen expert in one kernel, and the down products of
-// all of them with the weighted sum over a token's experts in another.
+// the layer is bound by that and by the decode.  Two launches route (the logits, the
+// choice), three multiply: a plan (which experts, which tokens each, and x in operand
+// fragments; a single token's kernels plan for themselves), the gate and up products
+// of every chosen expert, and the down products of all of them with the weighted sum
+// over a token's experts.
+//
+// Measured on one MI355X (gate and up | down, us): one token, 8 of 64 experts of 1024
+// x 2048, 26.7 MB of weight, 11.9 | 8.4, a wave has one chunk, and launch, plan, tables
+// and the memory's latency are most of it; 16 tokens, all of 8 experts of 14336 x 4096,
+// 748 MB, 144 | 79 (3.5 | 3.2 TB/s; vector instructions and lookups fill half of the
+// time, the wait for the next chunk the rest); 64 tokens, 4 of 16 experts of 1000 x
+// 2376, 60 MB, 25.6 | 19.4.
 //
 // The weight is decoded in operand registers as in dq4_linear_fused.hip's few-row
 // kernels, through one lookup table of byte pairs in LDS, and multiplied on
@@ -58,7 +66,10 @@ struct RouteArgs {
 };
 
 // Logits.  kExperts = 1: a workgroup for one token and expert, its waves share k.
-// kExperts = 4: a wave for one token and four experts, so that x is read less often.
+// kExperts = 4: a wave for one token and four experts, so that x is read less often
+// (with router and choice, from Python, us, one expert | four: 64 tokens, 64 experts x
+// 2048 13.9 | 13.7, 128 tokens 16.5 | 13.4, 2048 tokens 157 | 101; up to 16 tokens and
+// 8 experts x 4096 14.0 | 14.9).
 // The products are exact in FP32 and their sums run in 64 bits, since the choice
 // between two experts hangs on the last place.  (One workgroup per token for
 // everything took 16.6 us for 64 experts x 2048: the conversions to 64 bits on one CU.)
@@ -1044,7 +1055,9 @@ __global__ __launch_bounds__(64 * WAVES) void moe_down_kernel(MoeArgs a)
 // ---------------------------------------------------------------------------
 // Tiles of a pass over an expert: as many as its share of the tokens is likely to
 // fill, if they spread evenly, up to two (registers); an expert with more takes
-// more passes.
+// more passes.  (The whole call, us, with one | two: 64 tokens, 8 of 64 experts of 1024
+// x 2048, 8 tokens each, 94 | 121; 40 and 64 tokens, 4 of 16 experts of 1000 x 2376, 10
+// and 16 tokens each, 50.7 | 48.6 and 69 | 50.)
 int tiles_per_pass(int64_t m, int64_t top_k, int64_t n_experts)
 {
     return m <= 16 || m * top_k <= 8 * n_experts ? 1 : 2;
@@ -1052,7 +1065,7 @@ int tiles_per_pass(int64_t m, int64_t top_k, int64_t n_experts)
 
 // What the workspace holds, in this order.
 struct Layout {
-    int64_t max_tiles;  // at most this many tiles, and units
+    int64_t max_tiles;  // at most this many tiles, and passes
     int64_t passes, tokens, shares, x, h, all;
 };
 
@@ -1099,14 +1112,17 @@ struct Kernels {
         const int waves = a.tf == 1 ? kWaves : kWavesOfTwo;
         const int share = one_token(a) ? 2 : 1;  // waves of a chunk
         // Waves along k for each matrix, no more than chunks: what leaves a wave the
-        // fewest chunks if the tokens spread over the experts.
+        // fewest chunks if the tokens spread over the experts, the fewer waves of two
+        // (the whole call, us, with 1, 2, 4, 8: 16 tokens, 8 of 64 experts of 1024 x
+        // 2048 80, 83, 85; 64 tokens, 2 of 8 experts of 2048 x 4096 61, 48, 49, 51; 64
+        // tokens, 4 of 16 experts of 1000 x 2376 61, 50, 55).
         const int64_t chunks = ceil_div(a.n_in, kSpan), pairs = a.m * a.top_k;
         const int64_t items = (pairs < a.n_experts ? pairs : a.n_experts) * ceil_div(a.n_ff, 16);
         int32_t wk = 0;
         int64_t least = 0;
         for (int w = waves / share; w > 0; w /= 2) {
             const int64_t each = ceil_div(items, static_cast<int64_t>(cus) * (waves / share / w)) * ceil_div(chunks, w);
-            if (w <= chunks && (wk == 0 || each < least)) {
+            if (w <= chunks && (wk == 0 || each <= least)) {
                 wk = w;
                 least = each;
             }

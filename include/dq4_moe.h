@@ -20,21 +20,22 @@
  * elements) given as ld_*; a single row's stride is not looked at.  Only the m
  * rows and their columns are read or written.  No pointer but the workspace's
  * has to be aligned beyond its element type; 4-byte aligned packed codes and
- * row lengths that are multiples of 32 take the fastest path.  `residual` may be
- * `y` itself (same pointer and row stride); no other output may overlap an
- * input, a weight or another output, and the workspace none of them.  (Nothing
- * is refused for it here; the Python binding does.)
+ * row lengths that are multiples of 32 take the fastest path, multiples of 8
+ * the next.  `residual` may be `y` itself (same pointer and row stride); no
+ * other output may overlap an input, a weight or another output, and the
+ * workspace none of them.  (Nothing is refused for it here; the Python binding
+ * does.)
  *
  * workspace: caller-owned device memory, 256-byte aligned, of at least the
- * bytes that the call's *_workspace_bytes function returns.  Its contents do not matter
- * before the call, and after it the workspace holds nothing of use.  Calls that
- * may overlap in time must not share one.
+ * bytes that the call's *_workspace_bytes function returns.  Its contents do
+ * not matter before the call, and after it the workspace holds nothing of use.
+ * Calls that may overlap in time must not share one.
  *
  * Ownership, ordering and errors are as in dq4.h: everything is enqueued on
  * `stream` and can be captured into a graph, nothing is allocated, kept or
  * synchronized; arguments are checked before anything is enqueued.  Results
- * are deterministic for a given device, shape, and alignment of the packed
- * codes; for another number of tokens the sums may run in another order.
+ * are deterministic for a given device, shape, and alignment of x and the
+ * packed codes; for another number of tokens the sums may run in another order.
  *   DQ4_EINVAL       negative size, row stride below the row length, missing
  *                    pointer, unknown type or activation, top_k below 1 or
  *                    above n_experts, workspace too small or not 256-byte
