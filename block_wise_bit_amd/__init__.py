@@ -1289,10 +1289,12 @@ def dq4_moe_route(x, router, top_k: int, bias=None, renormalize: bool = True, id
     given = ids is not None or weights is not None
     if ids is None:
         ids = _output((m, top_k), torch.int32, device, stream)
+    else:
+        _dense(ids, "ids", (m, top_k), torch.int32, device)
     if weights is None:
         weights = _output((m, top_k), torch.float32, device, stream)
-    _dense(ids, "ids", (m, top_k), torch.int32, device)
-    _dense(weights, "weights", (m, top_k), torch.float32, device)
+    else:
+        _dense(weights, "weights", (m, top_k), torch.float32, device)
     if given or workspace is not None:
         _refuse_overlap([("ids", ids), ("weights", weights)], [("x", x), ("router", router), ("bias", bias)], (), 0,
                         workspace, given)

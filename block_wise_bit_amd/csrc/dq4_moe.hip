@@ -10,9 +10,9 @@
 // over a token's experts.
 //
 // Measured on one MI355X (gate and up | down, us): one token, 8 of 64 experts of 1024
-// x 2048, 26.7 MB of weight, 11.9 | 8.4, a wave has one chunk, and launch, plan, tables
+// x 2048, 26 MB of weight, 11.9 | 8.4, a wave has one chunk, and launch, plan, tables
 // and the memory's latency are most of it; 16 tokens, all of 8 experts of 14336 x 4096,
-// 748 MB, 144 | 79 (3.5 | 3.2 TB/s; vector instructions and lookups fill half of the
+// 727 MB, 145 | 76 (3.3 | 3.2 TB/s; vector instructions and lookups fill half of the
 // time, the wait for the next chunk the rest); 64 tokens, 4 of 16 experts of 1000 x
 // 2376, 60 MB, 25.6 | 19.4.
 //
