@@ -411,6 +411,46 @@ __global__ __launch_bounds__(kThreads) void weight_fragments_kernel(FragmentArgs
     }
 }
 
+// 8 codes of a row at byte address `at`; kAligned: one load.  Else dwords, none past
+// the one that holds the weight's last byte.
+template <bool kAligned>
+__device__ __forceinline__ u32x2 load_codes8(uintptr_t at, uintptr_t last)
+{
+    if constexpr (kAligned) {
+        return *reinterpret_cast<const u32x2 *>(at);
+    } else {
+        uint32_t d[3];
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            const uintptr_t w = (at & ~uintptr_t{3}) + 4 * i;
+            d[i] = *reinterpret_cast<const uint32_t *>(w < last ? w : last);
+        }
+        return u32x2{__builtin_amdgcn_alignbyte(d[1], d[0], static_cast<uint32_t>(at) & 3),
+                     __builtin_amdgcn_alignbyte(d[2], d[1], static_cast<uint32_t>(at) & 3)};
+    }
+}
+
+// 8 rows of 8 columns to the 8 columns' pieces of 8 rows, as dq4_int8_prep rounds.
+template <int OUT>
+__device__ __forceinline__ void decode_codes(const u32x2 (&code)[8], const float (&scale)[8], u32x4 (&q)[8])
+{
+    constexpr float kR127 = 0x1.020408p-7f;  // the FP32 value nearest 1/127
+#pragma unroll
+    for (int p = 0; p < 4; ++p)
+#pragma unroll
+        for (int f = 0; f < 8; ++f) {
+            float v[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int8_t c = static_cast<int8_t>(code[2 * p + h][f / 4] >> (8 * (f & 3)));
+                const float scaled = static_cast<float>(c) * scale[2 * p + h];
+                // columns past the last one: products that nobody takes
+                v[h] = scaled * kR127;
+            }
+            q[f][p] = Half<OUT>::pack2(v[0], v[1]);
+        }
+}
+
 // The columns of an LLM.int8 weight (include/dq4_int8.h) as fragments of 16-bit
 // values, laid out as in the backward decode above.  kAligned: 8 codes of a row are
 // an aligned 8-byte load; otherwise they are cut out of three dwords (the dword
@@ -435,7 +475,6 @@ __global__ __launch_bounds__(kThreads) void int8_column_fragments_kernel(Int8Fra
             return;
         }
     }
-    constexpr float kR127 = 0x1.020408p-7f;  // the FP32 value nearest 1/127
     const int tid = threadIdx.x;
     const int pair = blockIdx.x / a.chunks, chunk = blockIdx.x - pair * a.chunks;
     const int lane = tid & 63, ks = (tid >> 6) & 1, group = pair * 2 + (tid >> 7);
@@ -459,35 +498,10 @@ __global__ __launch_bounds__(kThreads) void int8_column_fragments_kernel(Int8Fra
             scale[h] = 0.0f;
             if (o < a.n_out) {
                 scale[h] = a.scales[o];
-                const uintptr_t at = base + o * a.n_in + j0;
-                if constexpr (kAligned) {
-                    code[h] = *reinterpret_cast<const u32x2 *>(at);
-                } else {
-                    uint32_t d[3];
-#pragma unroll
-                    for (int i = 0; i < 3; ++i) {
-                        const uintptr_t w = (at & ~uintptr_t{3}) + 4 * i;
-                        d[i] = *reinterpret_cast<const uint32_t *>(w < last ? w : last);
-                    }
-                    code[h] = u32x2{__builtin_amdgcn_alignbyte(d[1], d[0], static_cast<uint32_t>(at) & 3),
-                                    __builtin_amdgcn_alignbyte(d[2], d[1], static_cast<uint32_t>(at) & 3)};
-                }
+                code[h] = load_codes8<kAligned>(base + o * a.n_in + j0, last);
             }
         }
-#pragma unroll
-        for (int p = 0; p < 4; ++p)
-#pragma unroll
-            for (int f = 0; f < 8; ++f) {
-                float v[2];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int8_t c = static_cast<int8_t>(code[2 * p + h][f / 4] >> (8 * (f & 3)));
-                    const float scaled = static_cast<float>(c) * scale[2 * p + h];
-                    // columns past the last one: products that nobody takes
-                    v[h] = scaled * kR127;
-                }
-                q[f][p] = Half<OUT>::pack2(v[0], v[1]);
-            }
+        decode_codes<OUT>(code, scale, q);
     }
     uint16_t *to = a.out + (static_cast<int64_t>(group) * a.chunks + chunk) * (kUnitBytes / 2) +
                    ks * (kFrags * kFragBytes / 2) + lane * 8;
@@ -997,6 +1011,124 @@ __global__ __launch_bounds__(256) void product_reduce_kernel(ProductArgs a, int3
             f32x2{acc[0][i], acc[1][i]};
     __syncthreads();
     finish_slab_rows<OUT, kGated>(a, slab, row0, group, q, lane);
+}
+
+// ---------------------------------------------------------------------------
+// few rows of an LLM.int8 layer's gradient: no fragments in memory
+// ---------------------------------------------------------------------------
+// A workgroup takes 128 columns and a share of the weight's rows for 16 TF tokens, its
+// waves every eighth step of 32 rows: a wave loads 8 codes of 8 rows a lane, decodes
+// them to operands in registers and multiplies; the next step is in flight meanwhile.
+// The waves' sums meet in LDS, the workgroups' in product_reduce_kernel, both in a fixed
+// order.  The last `bias_rows` rows of workgroups add up the bias gradient.  Bound by reading the
+// weight: 28672 x 8192, 16 tokens, 3.7 TB/s, from 33 tokens on by reading it for each 32.
+struct Int8ColumnArgs {
+    const int8_t *codes;
+    const float *scales;
+    const uint16_t *dy;
+    int64_t ld_dy;
+    int64_t n_out, n_in, m;
+    int32_t steps, slices, splits, bias_rows;
+    f32x4 *partial;
+    float *dbias;  // or null
+};
+
+template <int OUT, int TF, bool kAligned, bool kVec>
+__global__ __launch_bounds__(512) void int8_columns_kernel(Int8ColumnArgs a)
+{
+    __shared__ __attribute__((aligned(16))) f32x4 part[8][kFrags * TF][64];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    if (static_cast<int>(blockIdx.y) >= a.splits * a.slices) {
+        const int64_t block = (static_cast<int64_t>(blockIdx.y) - a.splits * a.slices) * gridDim.x + blockIdx.x;
+        const int64_t stride = static_cast<int64_t>(a.bias_rows) * gridDim.x * 512;
+        for (int64_t c = block * 512 + tid; c < a.n_out; c += stride) {
+            float sum = 0.0f;
+#pragma unroll 8
+            for (int64_t r = 0; r < a.m; ++r)
+                sum = sum + Half<OUT>::widen(a.dy[r * a.ld_dy + c]);
+            a.dbias[c] = sum;
+        }
+        return;
+    }
+    const int split = static_cast<uint32_t>(blockIdx.y) / static_cast<uint32_t>(a.slices);
+    const int slice = blockIdx.y - split * a.slices, group = blockIdx.x;
+    const int first = static_cast<int>(static_cast<uint32_t>(a.steps) * split / static_cast<uint32_t>(a.splits));
+    const int last = static_cast<int>(static_cast<uint32_t>(a.steps) * (split + 1) / static_cast<uint32_t>(a.splits));
+    const uintptr_t base = reinterpret_cast<uintptr_t>(a.codes);
+    const uintptr_t last_dword = (base + a.n_out * a.n_in - 1) & ~uintptr_t{3};
+    int64_t j0 = static_cast<int64_t>(group) * kGroup + 8 * (lane & 15);
+    j0 = j0 < a.n_in ? j0 : 0;  // sums that nobody takes
+    struct Step {
+        u32x2 code[8];
+        float scale[8];
+        u32x4 x[TF];
+    };
+    // (without branches: rows past the end load the last one's, times 0)
+    const auto load = [&](Step &s, int step) {
+        const int64_t o0 = static_cast<int64_t>(step < last ? step : last - 1) * 32 + 8 * (lane >> 4);
+#pragma unroll
+        for (int h = 0; h < 8; ++h) {
+            const int64_t o = o0 + h < a.n_out ? o0 + h : a.n_out - 1;
+            s.code[h] = load_codes8<kAligned>(base + o * a.n_in + j0, last_dword);
+            const float scale = a.scales[o];
+            s.scale[h] = o0 + h < a.n_out ? scale : 0.0f;
+        }
+#pragma unroll
+        for (int t = 0; t < TF; ++t) {
+            const int64_t token = (static_cast<int64_t>(slice) * TF + t) * 16 + (lane & 15);
+            const bool in = token < a.m;
+            const uint16_t *row = a.dy + (in ? token : 0) * a.ld_dy;
+            if constexpr (kVec) {
+                const u32x4 v = *reinterpret_cast<const u32x4 *>(row + (o0 < a.n_out ? o0 : 0));
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    s.x[t][i] = in && o0 < a.n_out ? v[i] : 0;
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int64_t k = o0 + 2 * i;
+                    const uint32_t lo = row[k < a.n_out ? k : 0], hi = row[k + 1 < a.n_out ? k + 1 : 0];
+                    s.x[t][i] = !in ? 0u : (k < a.n_out ? lo : 0u) | (k + 1 < a.n_out ? hi << 16 : 0u);
+                }
+            }
+        }
+    };
+    f32x4 acc[kFrags][TF];
+#pragma unroll
+    for (int f = 0; f < kFrags; ++f)
+#pragma unroll
+        for (int t = 0; t < TF; ++t)
+            acc[f][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    Step now, next;
+    if (first + wave < last)
+        load(now, first + wave);
+    for (int step = first + wave; step < last; step += 8) {
+        load(next, step + 8);
+        u32x4 q[8];
+        decode_codes<OUT>(now.code, now.scale, q);
+#pragma unroll
+        for (int f = 0; f < kFrags; ++f)
+#pragma unroll
+            for (int t = 0; t < TF; ++t)
+                acc[f][t] = Half<OUT>::mfma(q[f], now.x[t], acc[f][t]);
+        now = next;
+    }
+#pragma unroll
+    for (int f = 0; f < kFrags; ++f)
+#pragma unroll
+        for (int t = 0; t < TF; ++t)
+            part[wave][f * TF + t][lane] = acc[f][t];
+    __syncthreads();
+    f32x4 *to = a.partial + (static_cast<int64_t>(split) * gridDim.x * a.slices +
+                             static_cast<int64_t>(group) * a.slices + slice) * (kFrags * TF * 64);
+    for (int i = tid; i < kFrags * TF * 64; i += 512) {
+        f32x4 z = part[0][i >> 6][i & 63];
+#pragma unroll
+        for (int w = 1; w < 8; ++w)
+            z = z + part[w][i >> 6][i & 63];
+        to[i] = z;
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -2958,6 +3090,60 @@ const void *int8_fragments_kernel(bool aligned, Beside kind)
                    : reinterpret_cast<const void *>(&int8_column_fragments_kernel<OUT, false, kNothing>);
 }
 
+// Tokens up to which the columns are multiplied as they are decoded (whole calls, us, decode
+// and product | this: 16 tokens, 11008 x 4096 56 | 17, 28672 x 8192 288 | 63; 64 tokens 60 |
+// 27, 289 | 100; 128 tokens 63 | 46, 300 | 187, 1001 x 1377 17.4 | 17.0).
+constexpr int64_t kInt8ColumnsMost = 128;
+
+struct Int8ColumnPlan {
+    int tf;
+    int64_t slices, groups, steps, splits;
+    int64_t bytes() const { return splits * groups * slices * kFrags * tf * kFragBytes; }
+};
+
+Int8ColumnPlan int8_column_plan(int64_t n_out, int64_t n_in, int64_t m, int cus)
+{
+    Int8ColumnPlan p{};
+    p.tf = m <= 16 ? 1 : 2;
+    p.slices = ceil_div(m, 16 * p.tf);
+    p.groups = ceil_div(n_in, kGroup);
+    p.steps = ceil_div(n_out, 32);
+    // one workgroup per CU, each wave with a step at least
+    p.splits = cus / (p.groups * p.slices);
+    if (p.splits > ceil_div(p.steps, 8))
+        p.splits = ceil_div(p.steps, 8);
+    if (p.splits < 1)
+        p.splits = 1;
+    return p;
+}
+
+template <int OUT, int TF>
+dq4_status_t run_int8_few(const Int8ColumnPlan &plan, Int8ColumnArgs a, ProductArgs p, hipStream_t s)
+{
+    const bool aligned = a.n_in % 8 == 0 && reinterpret_cast<uintptr_t>(a.codes) % 8 == 0;
+    const bool vec = rows_aligned(a.dy, a.ld_dy, a.m, a.n_out);
+    const void *kernel = aligned ? (vec ? reinterpret_cast<const void *>(&int8_columns_kernel<OUT, TF, true, true>)
+                                        : reinterpret_cast<const void *>(&int8_columns_kernel<OUT, TF, true, false>))
+                                 : (vec ? reinterpret_cast<const void *>(&int8_columns_kernel<OUT, TF, false, true>)
+                                        : reinterpret_cast<const void *>(&int8_columns_kernel<OUT, TF, false, false>));
+    a.steps = static_cast<int32_t>(plan.steps);
+    a.slices = static_cast<int32_t>(plan.slices);
+    a.splits = static_cast<int32_t>(plan.splits);
+    const int64_t bias_rows = !a.dbias ? 0 : ceil_div(a.n_out, 512 * plan.groups);
+    a.bias_rows = static_cast<int32_t>(bias_rows < 256 ? bias_rows : 256);
+    void *params[] = {&a};
+    const dq4_status_t st = launch(kernel, plan.groups, plan.splits * plan.slices + a.bias_rows, 512, params, s);
+    if (st != DQ4_OK)
+        return st;
+    p.partial = a.partial;
+    p.splits = a.splits;
+    p.tiles_t = a.slices;
+    p.groups = static_cast<int32_t>(plan.groups);
+    int32_t tiles = static_cast<int32_t>(plan.groups * plan.slices);
+    void *rp[] = {&p, &tiles};
+    return launch(reinterpret_cast<const void *>(&product_reduce_kernel<OUT, false, 1, 1, TF>), tiles, TF, 256, rp, s);
+}
+
 // dx = dy W for an LLM.int8 weight: its columns to 16-bit fragments, then the
 // product.
 template <int OUT>
@@ -3078,6 +3264,8 @@ dq4_status_t check_call(const dq4_weight_t *w0, const dq4_weight_t *w1, int64_t 
 
 int64_t int8_backward_need(int64_t n_out, int64_t n_in, int64_t m, const void *dy, int64_t ld_dy)
 {
+    if (m <= kInt8ColumnsMost && n_in > 0)
+        return int8_column_plan(n_out, n_in, m, current_compute_units()).bytes();
     const Shape s{m, n_in, n_out, kSingle};
     const bool copy = n_in > 0 && needs_copy(dy, ld_dy, m, n_out);
     return workspace_need(s, copy_bytes(s, copy) + partial_bytes(m, n_out), false);
@@ -3493,6 +3681,20 @@ dq4_status_t dq4_int8_linear_backward(const int8_t *CB, const float *SCB, int64_
     const int64_t copied = copy_bytes(sh, copy), fixed = copied + partial_bytes(m, n_out);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     ProductArgs p{};
+    if (m <= kInt8ColumnsMost && n_in > 0 && n_out > 0) {
+        const Int8ColumnPlan plan = int8_column_plan(n_out, n_in, m, current_compute_units());
+        p.m = m;
+        p.n = n_in;
+        p.act = DQ4_ACT_NONE;
+        p.y = static_cast<uint16_t *>(dx);
+        p.ld_y = ld_dx;
+        p.vec = rows_aligned(dx, ld_dx, m, 8);
+        Int8ColumnArgs a{CB, SCB, static_cast<const uint16_t *>(dy), ld_dy, n_out, n_in, m, 0, 0, 0, 0,
+                         reinterpret_cast<f32x4 *>(ws), dbias};
+        if (plan.tf == 1)
+            return dtype == DQ4_F16 ? run_int8_few<DQ4_F16, 1>(plan, a, p, s) : run_int8_few<DQ4_BF16, 1>(plan, a, p, s);
+        return dtype == DQ4_F16 ? run_int8_few<DQ4_F16, 2>(plan, a, p, s) : run_int8_few<DQ4_BF16, 2>(plan, a, p, s);
+    }
     p.x[0] = p.x[1] = static_cast<const uint16_t *>(dy);
     p.ld_x = product_ld(ld_dy, m, n_out);
     p.k = n_out;

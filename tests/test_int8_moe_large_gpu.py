@@ -104,6 +104,39 @@ def test_int8_backward_of_a_far_weight():
         check(dx, want, bound, "far weight")
 
 
+@pytest.mark.parametrize("m,n,k", [(3, 70000, 40), (1, 131072, 8), (128, 5000, 24), (129, 640, 264), (65, 33, 700),
+                                   (33, 1000, 2376), (96, 24, 4099), (128, 4096, 1024), (16, 2048, 16384), (2, 17, 1)])
+def test_int8_backward_few_tokens(m, n, k):
+    rng = np.random.default_rng(m + n)
+    CB, SCB = weight(rng, n, k)
+    dy = normal(rng, (m, n), "f16")
+    # what lies beside a row is not read, or has no part in the result
+    for pad, skew in ((0, 0), (8, 0), (3, 1)):
+        wide = torch.full((m, n + pad + skew), float("nan"), dtype=torch.float16, device="cuda")
+        wide[:, skew:skew + n] = dy.cuda()
+        buf = torch.full((n * k + skew,), 77, dtype=torch.int8, device="cuda")
+        CBd = buf[skew:].view(n, k)
+        CBd.copy_(CB)
+        dx, db = dq4.dq4_int8_linear_backward(wide[:, skew:skew + n], CBd, SCB.cuda(), bias_grad=True)
+        (want, bound), (wb, bb) = backward64("f16", dy, CB, SCB)
+        check(dx, want, bound, f"dx {m} {n} {k} {pad}")
+        check(db, wb, bb, "dbias")
+
+
+@pytest.mark.parametrize("m", [4, 40, 130])
+def test_int8_backward_rows_do_not_mix(m):
+    rng = np.random.default_rng(m)
+    CB, SCB = weight(rng, 70, 90)
+    dy = normal(rng, (m, 70), "bf16")
+    clean, _ = dq4.dq4_int8_linear_backward(dy.cuda(), CB.cuda(), SCB.cuda())
+    dy[2, 69] = float("nan")
+    dy[3, 0] = float("inf")
+    dx, _ = dq4.dq4_int8_linear_backward(dy.cuda(), CB.cuda(), SCB.cuda())
+    keep = [i for i in range(m) if i not in (2, 3)]
+    assert torch.equal(dx[keep], clean[keep]) and bool(torch.isnan(dx[2]).all())
+    assert not bool(torch.isfinite(dx[3]).any())
+
+
 # rows of multiples of 8 that are no multiples of 32, and larger layers
 @pytest.mark.parametrize("dt", ["f16", "bf16"])
 @pytest.mark.parametrize("m,E,k,n_ff,n_in,bs", [
