@@ -1021,7 +1021,8 @@ __global__ __launch_bounds__(256) void product_reduce_kernel(ProductArgs a, int3
 // them to operands in registers and multiplies; the next step is in flight meanwhile.
 // The waves' sums meet in LDS, the workgroups' in product_reduce_kernel, both in a fixed
 // order.  The last `bias_rows` rows of workgroups add up the bias gradient.  Bound by reading the
-// weight: 28672 x 8192, 16 tokens, 3.7 TB/s, from 33 tokens on by reading it for each 32.
+// weight: 28672 x 8192, 16 tokens, 3.7 TB/s, from 33 tokens on by reading it for each 32
+// (sums of 64 do not fit the registers beside two steps).
 struct Int8ColumnArgs {
     const int8_t *codes;
     const float *scales;
