@@ -151,6 +151,41 @@ def test_moe_larger(dt, m, E, k, n_ff, n_in, bs):
                 what=f"{dt} {m} {E} {k} {n_ff}x{n_in}")
 
 
+@pytest.mark.parametrize("n_ff,n_in", [(64, 96), (24, 40), (33, 47)])
+@pytest.mark.parametrize("m", [1, 5, 20, 64])
+def test_moe_padded_rows_are_not_read(m, n_ff, n_in):
+    """Rows without a valid expert hold NaN, as do the weights of ids that are none."""
+    rng = np.random.default_rng(m)
+    layer = Layer(5, n_ff, n_in, 32, seed=9)
+    ids, weights = choose(rng, m, 5, 3)
+    x, residual = normal(rng, (m, n_in), "f16"), normal(rng, (m, n_in), "f16")
+    padded = np.arange(m) % 3 == (0 if m == 1 else 1)
+    ids[padded] = -1
+    ids[~padded, 1] = 5
+    want, bound = moe64("f16", "silu", layer, x, ids, weights, residual)
+    x[torch.from_numpy(padded)] = float("nan")
+    weights[(ids < 0) | (ids > 4)] = np.nan
+    y = dq4.dq4_moe_fused(*layer.device(), 5, n_ff, n_in, 32, x.cuda(), torch.from_numpy(ids).cuda(),
+                          torch.from_numpy(weights).cuda(), residual=residual.cuda())
+    check(y, want, bound, f"padded {m}")
+    assert torch.equal(y.cpu()[torch.from_numpy(padded)], residual[torch.from_numpy(padded)])
+
+
+def test_route_infinite_logits():
+    """The softmax of an infinite logit is NaN, and masked experts stay out."""
+    x, router = torch.ones((3, 8), dtype=torch.float16, device="cuda"), torch.ones((70, 8), dtype=torch.float16, device="cuda")
+    bias = torch.zeros(70, device="cuda")
+    bias[66], bias[2], bias[3] = float("inf"), float("-inf"), 1.0
+    ids, weights = dq4.dq4_moe_route(x, router, 3, bias=bias)
+    assert ids.cpu().tolist() == [[66, 3, 0]] * 3 and bool(torch.isnan(weights).all())
+    bias[66] = -0.0  # as large as 0: the lower index first
+    ids, weights = dq4.dq4_moe_route(x * 0, router, 4, bias=bias)
+    assert ids.cpu().tolist() == [[3, 0, 1, 4]] * 3
+    bias[:], bias[5], bias[66] = -1.0, -0.0, 0.0
+    ids, weights = dq4.dq4_moe_route(x * 0, router, 2, bias=bias)
+    assert ids.cpu().tolist() == [[5, 66]] * 3 and weights.cpu().tolist() == [[0.5, 0.5]] * 3
+
+
 class Stacked:
     """The experts `of` of a stack that is drawn on the GPU, renumbered from 0."""
 
