@@ -15,6 +15,7 @@ A flag for speed only:
 """
 from __future__ import annotations
 
+import concurrent.futures
 import hashlib
 import json
 import os
@@ -55,11 +56,11 @@ def hipcc() -> str:
 def build(out: str = LIBRARY, extra_flags=()) -> str:
     """Compile the library; always recompiles.  Returns the .so path."""
     tmp = out + ".tmp%d" % os.getpid()
-    cmd = [hipcc(), *HIPCC_FLAGS, *extra_flags, "-shared", "-I", INCLUDE, "-o", tmp, *SOURCES,
-           *LIBS]
-    subprocess.run(cmd, check=True)
-    os.replace(tmp, out)
     with tempfile.TemporaryDirectory() as d:
+        objects = _compile_each(d, ".o", ["-c", *extra_flags])
+        subprocess.run([hipcc(), f"--offload-arch={ARCH}", *extra_flags, "-shared", "-fPIC", "-o", tmp, *objects, *LIBS],
+                       check=True)
+        os.replace(tmp, out)
         digests = kernel_digests(device_assembly(d))
     with open(KERNEL_DIGESTS, "w") as fh:
         json.dump(digests, fh, indent=1, sort_keys=True)
@@ -68,15 +69,22 @@ def build(out: str = LIBRARY, extra_flags=()) -> str:
 
 def device_assembly(workdir: str) -> str:
     """gfx950 assembly of the library's kernels (for instruction checks)."""
-    workdir = os.path.abspath(workdir)
     parts = []
-    for src in SOURCES:
-        out = os.path.join(workdir, os.path.basename(src) + "-gfx950.s")
-        cmd = [hipcc(), *HIPCC_FLAGS, "--cuda-device-only", "-S", "-I", INCLUDE, "-o", out, src]
-        subprocess.run(cmd, check=True, cwd=workdir)
+    for out in _compile_each(os.path.abspath(workdir), "-gfx950.s", ["--cuda-device-only", "-S"]):
         with open(out) as fh:
             parts.append(fh.read())
     return "\n".join(parts)
+
+
+def _compile_each(workdir: str, suffix: str, flags) -> list:
+    """One output in workdir per source, in their order; several compilers at a time."""
+    def one(src):
+        out = os.path.join(workdir, os.path.basename(src) + suffix)
+        subprocess.run([hipcc(), *HIPCC_FLAGS, *flags, "-I", INCLUDE, "-o", out, src], check=True, cwd=workdir)
+        return out
+
+    with concurrent.futures.ThreadPoolExecutor(min(len(SOURCES), os.cpu_count() or 1, 8)) as pool:
+        return list(pool.map(one, SOURCES))
 
 
 def kernel_bodies(asm: str) -> dict:
