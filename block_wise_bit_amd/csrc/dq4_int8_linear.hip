@@ -1295,6 +1295,13 @@ bool takes_rows(int64_t m, int64_t k, bool aligned)
     return m <= kRowsMost && (m <= 32 || k <= 4096 || !aligned);
 }
 
+// Tiles of 16 tokens that a row kernel works on.  It reads the outlier operands of all
+// of them, also of those behind the last token, so the workspace holds as many.
+int row_kernel_tiles(int64_t m)
+{
+    return m <= 16 ? 1 : m <= 32 ? 2 : 4;
+}
+
 constexpr int kTileCols[3] = {256, 128, 128}, kTileRows[3] = {256, 128, 64};
 constexpr int kTileResident[3] = {1, 2, 2};  // workgroups per CU (LDS)
 // Microseconds of one step of 64 k with every CU full, as measured at 8192^3 (438,
@@ -1363,7 +1370,7 @@ Layout layout_of(const void *codes, int64_t m, int64_t ld_codes, const void *w, 
     }
     if (outliers && k > 0 && m > kGatheredMost) {
         l.w_frags = l.rows ? ceil_div(n, 16) : ceil_div(n, kGroup) * kGroupFrags;
-        l.x_frags = ceil_div(m, 16);
+        l.x_frags = l.rows ? row_kernel_tiles(m) : ceil_div(m, 16);
     }
     return l;
 }
@@ -1396,9 +1403,10 @@ dq4_status_t launch_rows(const Int8Args &a, int cus, hipStream_t s)
 {
     const bool aligned = byte_rows_aligned(a.codes, a.ld_codes, a.m, a.k) && byte_rows_aligned(a.w, a.ld_w, a.n, a.k);
     const bool two = a.n > static_cast<int64_t>(16) * cus;  // more than 16 rows a workgroup
-    if (a.m <= 16)
+    const int tiles = row_kernel_tiles(a.m);
+    if (tiles == 1)
         return two ? launch_rows_tile<OUT, 1, 2>(a, aligned, cus, s) : launch_rows_tile<OUT, 1, 1>(a, aligned, cus, s);
-    if (a.m <= 32)
+    if (tiles == 2)
         return two ? launch_rows_tile<OUT, 2, 2>(a, aligned, cus, s) : launch_rows_tile<OUT, 2, 1>(a, aligned, cus, s);
     return two ? launch_rows_tile<OUT, 4, 2>(a, aligned, cus, s) : launch_rows_tile<OUT, 4, 1>(a, aligned, cus, s);
 }
