@@ -1269,8 +1269,8 @@ def dq4_moe_route(x, router, top_k: int, bias=None, renormalize: bool = True, id
     (m, top_k) int32 are those of the largest, in falling order, ties to the
     lower index; weights (m, top_k) float32 are their softmax, over the chosen
     experts or, with renormalize False, over all.  An expert with a bias of minus
-    infinity is not chosen: where fewer than top_k are left, the id is -1 and
-    the weight 0."""
+    infinity is not chosen, whatever its row of the router and the token hold:
+    where fewer than top_k are left, the id is -1 and the weight 0."""
     torch = _torch()
     code = _half_code(x.dtype, "x")
     device = x.device

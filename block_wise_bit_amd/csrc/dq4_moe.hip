@@ -115,8 +115,12 @@ __global__ __launch_bounds__(256) void moe_logits_kernel(RouteArgs a)
                 sum[q] = part[0] + part[1] + part[2] + part[3];
                 __syncthreads();
             }
-            if (lane == 0 && wave % kWaves == 0 && e0 + q < E)
-                a.logits[t * E + e0 + q] = a.bias ? sum[q] + static_cast<double>(a.bias[e0 + q]) : sum[q];
+            if (lane == 0 && wave % kWaves == 0 && e0 + q < E) {
+                const float bias = a.bias ? a.bias[e0 + q] : 0.0f;
+                // (a masked expert's sum may be an infinity or NaN: it is not looked at)
+                a.logits[t * E + e0 + q] = bias == -__builtin_inff() ? static_cast<double>(bias)
+                                                                     : sum[q] + static_cast<double>(bias);
+            }
         }
     }
 }

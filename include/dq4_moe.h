@@ -65,10 +65,11 @@ extern "C" {
  * x: m x n_in, T.  router: n_experts x n_in, T, dense.  bias: n_experts FP32
  * values, or NULL.  ids: m x top_k, weights: m x top_k, dense, in order of
  * falling logits.
- * An expert whose logit is minus infinity (a bias that masks it) is not chosen;
- * places that no expert is left for get id -1 and weight 0.  A NaN logit ranks
- * below every number; a token with one, or with a logit of plus infinity, gets
- * NaN for its weights.
+ * A bias of minus infinity masks its expert, whose logit is then minus infinity
+ * whatever its row of the router and the token hold.  An expert whose logit is
+ * minus infinity is not chosen; places that no expert is left for get id -1 and
+ * weight 0.  A NaN logit ranks below every number; a token with one, or with a
+ * logit of plus infinity, gets NaN for its weights.
  */
 dq4_status_t dq4_moe_route(const void *x, int64_t m, int64_t n_in, int64_t ld_x, int32_t dtype,
                            const void *router, const float *bias, int32_t n_experts, int32_t top_k,
