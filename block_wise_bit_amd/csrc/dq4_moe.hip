@@ -67,12 +67,14 @@ struct RouteArgs {
 
 // Logits.  kExperts = 1: a workgroup for one token and expert, its waves share k.
 // kExperts = 4: a wave for one token and four experts, so that x is read less often
-// (with router and choice, from Python, us, one expert | four: 64 tokens, 64 experts x
-// 2048 13.9 | 13.7, 128 tokens 16.5 | 13.4, 2048 tokens 157 | 101; up to 16 tokens and
-// 8 experts x 4096 14.0 | 14.9).
-// The products are exact in FP32 and their sums run in 64 bits, since the choice
-// between two experts hangs on the last place.  (One workgroup per token for
-// everything took 16.6 us for 64 experts x 2048: the conversions to 64 bits on one CU.)
+// (with router and choice, from Python, BF16, us, one expert | four: 128 tokens, 64
+// experts x 2048 17.0 | 13.4, 512 tokens 45 | 30, 2048 tokens 168 | 106; 16 tokens and 8
+// experts x 4096 13.9 | 14.7).
+// The sums run in 64 bits, since the choice between two experts hangs on the last
+// place.  The products are exact: of FP16 values in FP32, of BF16 values, whose
+// products leave FP32's range at both ends, in FP64 (2048 tokens, 64 experts x 2048:
+// FP16 103, BF16 106).  (One workgroup per token for everything took 16.6 us for 64
+// experts x 2048: the conversions to 64 bits on one CU.)
 template <int OUT, int kExperts>
 __global__ __launch_bounds__(256) void moe_logits_kernel(RouteArgs a)
 {
@@ -99,8 +101,12 @@ __global__ __launch_bounds__(256) void moe_logits_kernel(RouteArgs a)
                 float r[8];
                 load_values<OUT, 8>(a.router + static_cast<int64_t>(e) * k + c, a.vec, valid, r);
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    sum[q] = sum[q] + static_cast<double>(xv[j] * r[j]);
+                for (int j = 0; j < 8; ++j) {
+                    if constexpr (OUT == DQ4_F16)
+                        sum[q] = sum[q] + static_cast<double>(xv[j] * r[j]);
+                    else
+                        sum[q] = sum[q] + static_cast<double>(xv[j]) * static_cast<double>(r[j]);
+                }
             }
         }
 #pragma unroll

@@ -2,7 +2,7 @@
  * dq4_moe.h -- C ABI of a mixture-of-experts layer for a few tokens: the router,
  * and the chosen experts' gated feed-forward blocks over nested 4-bit weights.
  *
- *     router   l_e = sum_k x_k r_ek + bias_e             (64-bit sums)
+ *     router   l_e = sum_k x_k r_ek + bias_e             (64-bit sums of exact products)
  *              ids = the top_k experts of largest l, ties to the lower index
  *              weights = exp(l_id) / sum of exp(l) over the chosen experts
  *                        (renormalize != 0) or over all of them      (FP32)
