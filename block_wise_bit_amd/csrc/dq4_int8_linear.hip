@@ -1399,19 +1399,21 @@ dq4_status_t launch_rows_tile(Int8Args a, bool aligned, int cus, hipStream_t s)
     const int64_t grid = ceil_div(a.n, 16) < cus ? ceil_div(a.n, 16) : cus;
     a.rows_per = static_cast<int32_t>(a.n / grid);
     a.rows_extra = static_cast<int32_t>(a.n % grid);
+    const void *kernel = aligned ? reinterpret_cast<const void *>(&int8_rows_kernel<OUT, TF, R, 0>)
+                                 : reinterpret_cast<const void *>(&int8_any_rows_kernel<OUT, TF, R>);
     // codes are kept where there is more than one row block to keep them for (16
-    // tokens, 4096 x 14336, one row block: 16.4 us kept, 13.3 not)
-    const bool keep = a.n > grid * (16 * R);
-    const int64_t steps = ceil_div(ceil_div(a.k, kStep), 8);  // of a wave
-    const void *kernel = reinterpret_cast<const void *>(&int8_rows_kernel<OUT, TF, R, 0>);
-    if (!aligned)
-        kernel = reinterpret_cast<const void *>(&int8_any_rows_kernel<OUT, TF, R>);
-    else if (keep && steps <= 8)
-        kernel = reinterpret_cast<const void *>(&int8_rows_kernel<OUT, TF, R, 8>);
-    else if (keep && steps <= 16 && TF <= 2)
-        kernel = reinterpret_cast<const void *>(&int8_rows_kernel<OUT, TF, R, TF <= 2 ? 16 : 8>);
-    else if (keep && steps <= 32 && TF == 1)
-        kernel = reinterpret_cast<const void *>(&int8_rows_kernel<OUT, TF, R, TF == 1 ? 32 : 8>);
+    // tokens, 4096 x 14336, one row block: 16.4 us kept, 13.3 not); with R = 1 there is one
+    if constexpr (R == 2) {
+        const int64_t steps = ceil_div(ceil_div(a.k, kStep), 8);  // of a wave
+        if (aligned && a.n > grid * (16 * R)) {
+            if (steps <= 8)
+                kernel = reinterpret_cast<const void *>(&int8_rows_kernel<OUT, TF, R, 8>);
+            else if (steps <= 16 && TF <= 2)
+                kernel = reinterpret_cast<const void *>(&int8_rows_kernel<OUT, TF, R, TF <= 2 ? 16 : 8>);
+            else if (steps <= 32 && TF == 1)
+                kernel = reinterpret_cast<const void *>(&int8_rows_kernel<OUT, TF, R, TF == 1 ? 32 : 8>);
+        }
+    }
     void *params[] = {&a};
     return launch(kernel, grid, 1, 512, params, s);
 }
