@@ -37,9 +37,9 @@
  * are deterministic for a given device, shape, and alignment of x and the
  * packed codes; for another number of tokens the sums may run in another order.
  *   DQ4_EINVAL       negative size, row stride below the row length, missing
- *                    pointer, unknown type or activation, top_k below 1 or
- *                    above n_experts, workspace too small or not 256-byte
- *                    aligned
+ *                    pointer, unknown type or activation, top_k below 1, or
+ *                    above n_experts (dq4_moe_route alone), workspace too small
+ *                    or not 256-byte aligned
  *   DQ4_EUNSUPPORTED n_experts above 512, top_k above 16, more than 64 tokens
  *                    (dq4_moe_fused; 2^21 for the router), n_ff or n_in above
  *                    2^17, n_experts n_ff n_in above 2^40, block layout that
@@ -83,8 +83,8 @@ int64_t dq4_moe_route_workspace_bytes(int64_t m, int32_t n_experts);
  * x: m x n_in.  ids, weights: m x top_k, dense, as dq4_moe_route writes them or
  * from any other router.  An id outside 0 .. n_experts - 1 stands for no expert
  * (a padded token has only those); one that occurs twice in a row counts with
- * the sum of its weights.  activation: any but DQ4_ACT_NONE.  residual: m x
- * n_in, or NULL.  y: m x n_in.
+ * the sum of its weights, and top_k may exceed n_experts.  activation: any but
+ * DQ4_ACT_NONE.  residual: m x n_in, or NULL.  y: m x n_in.
  * m == 0 or n_in == 0 is a no-op; n_ff == 0 is an empty sum (down's codebooks are
  * asked for all the same).
  */
