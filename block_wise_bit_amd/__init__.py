@@ -1319,7 +1319,8 @@ def dq4_moe_fused(gate, up, down, n_experts: int, n_ff: int, n_in: int, blocksiz
     (to_device's) and offset.  x: (m, n_in) float16 or bfloat16; ids (m, top_k)
     int32 and weights (m, top_k) float32: dq4_moe_route's, or another router's.
     An id outside 0 .. n_experts - 1 stands for no expert; a row of those gives
-    residual, or zeros.  Longer prompts: dq4_gated_fused and dq4_linear_fused,
+    residual, or zeros.  The product of act and up is rounded to x's dtype: in
+    float16 one beyond 65504 is an infinity.  Longer prompts: dq4_gated_fused and dq4_linear_fused,
     expert by expert.  y may be residual itself.  Returns y (m, n_in)."""
     torch = _torch()
     n_ff, n_in, blocksize = _sizes(n_ff, n_in, blocksize)

@@ -14,7 +14,9 @@
  * dq4_linear.h) of (n_experts n_ff) x n_in elements, down one of (n_experts
  * n_in) x n_ff.  Their elements enter the products as exactly the values
  * dq4_nested_dequant writes for T; products are summed in FP32, h and y are
- * rounded once.
+ * rounded once.  h is an operand of the down product and has T's range: in FP16
+ * an h beyond 65504 is an infinity, as it is in dq4_gated_fused's output, and its
+ * token's y infinities and NaN.
  *
  * Matrices are row-major with unit stride along a row and the row stride (in
  * elements) given as ld_*; a single row's stride is not looked at.  Only the m
