@@ -1311,7 +1311,7 @@ def dq4_moe_fused(gate, up, down, n_experts: int, n_ff: int, n_in: int, blocksiz
                   nested_blocksize: int = NESTED_BLOCKSIZE, stream=None):
     """y = sum over the chosen experts e of w_e (act(x Wg_e^T) * (x Wu_e^T)) Wd_e^T
     + residual: a mixture-of-experts feed-forward layer for up to 64 tokens, each
-    chosen expert's 4-bit matrices read once.
+    chosen expert's 4-bit matrices read once for 16 or 32 of its tokens.
 
     gate, up: the experts' matrices stacked by rows, one nested 4-bit weight of
     (n_experts n_ff, n_in) each, down: (n_experts n_in, n_ff), as mappings with the

@@ -1,7 +1,8 @@
 // dq4_int8_linear.hip -- the LLM.int8 linear layer (include/dq4_int8.h): tokens
 // quantized to 8-bit codes, and the product of the codes with a scale for each
-// token and channel, the outlier columns in 16 bits.  (Its gradient is a product
-// over a 16-bit copy of the weight, in dq4_linear_fused.hip.)
+// token and channel, the outlier columns in 16 bits.  (Its gradient is in
+// dq4_linear_fused.hip: up to 128 tokens the weight's columns are multiplied as they
+// are decoded, beyond it is a product over a 16-bit copy of the weight.)
 //
 // The sum of a product is one of 8-bit integers in 32 bits, exact in any order,
 // on v_mfma_i32_16x16x64_i8: D (16 x 16) += A (16 x 64) B (64 x 16).  Lane l
@@ -82,8 +83,10 @@ __device__ __forceinline__ int code_of(float x, float up, float s, float inv)
 
 // A row of x per workgroup and turn: its scale, then its codes.  A thread holds up
 // to kHeld pieces of 8 elements between the two, the rest is read again.  Bound by
-// memory's latency: 2 bytes read and 1 written per element, 4096 x 4096 18 us (2.8
-// TB/s); a wave per row took 21.
+// memory's latency, which a workgroup waits for twice a row with nothing else in flight:
+// 2 bytes read and 1 written per element, 4096 x 4096 18 us (2.8 TB/s); a wave per row
+// took 21.  (kHeld is one for all widths, 8192 elements: 5 waves a SIMD; with two pieces,
+// enough for 4096, the registers would allow 8.)
 // kOne: the only row, by one workgroup, which also makes the list of outliers.
 constexpr int kHeld = 4;
 

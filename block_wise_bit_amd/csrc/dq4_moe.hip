@@ -2,8 +2,9 @@
 // the router, and the chosen experts' gated feed-forward blocks over nested 4-bit
 // weights.
 //
-// Few tokens choose few experts, and each chosen expert's matrices are read once:
-// the layer is bound by that and by the decode.  Two launches route (the logits, the
+// Few tokens choose few experts, and each chosen expert's matrices are read once for
+// 16 of its tokens (32 where tiles_per_pass says two): the layer is bound by that and by
+// the decode.  Two launches route (the logits, the
 // choice), three multiply: a plan (which experts, which tokens each, and x in operand
 // fragments; a single token's kernels plan for themselves), the gate and up products
 // of every chosen expert, and the down products of all of them with the weighted sum
@@ -1114,7 +1115,9 @@ bool one_token(const MoeArgs &a)
 // One token, up to a tile a pass, more.
 template <int OUT, class Rows>
 struct Kernels {
-    // (two tiles' sums and operands do not leave registers for 16 waves)
+    // (Two tiles' sums and operands do not leave EvenRows the registers for 16 waves: 9
+    // and 11 spill in gate and up, 2 and 5 in down.  AnyRows would fit and has the same
+    // number.)
     static constexpr int kWaves = 16, kWavesOfTwo = 8;
 
     static dq4_status_t gate_up(const MoeArgs &a, int cus, hipStream_t s)

@@ -16,7 +16,8 @@
  *     W             T(fl32(fl32(CB SCB) R127)), R127 the FP32 value nearest
  *                   1/127: the elements that dq4_int8_prep writes
  *
- * The sum over j is exact, in 32-bit integers; the other sums are FP32, and
+ * The sum over j is exact, in 32-bit integers, and scales may have any size: no
+ * step leaves FP32's range where its value does not.  The other sums are FP32, and
  * every output is rounded once.  Columns c_l are the outliers, those in which
  * some element's magnitude reaches the threshold: their codes are 0, and they
  * enter in 16 bits.  Their list stays on the device, as the quantization
