@@ -809,10 +809,11 @@ __device__ __forceinline__ void fill_pairs(uint8_t *table, const float (&cb4)[kW
 // in a fixed order, and h goes out in the down product's operand order.  The next
 // chunk's weight, also that of the next item, is in flight while one is multiplied.
 // h is rounded to T, the width of the matrix instruction's operands in the down product
-// (kept in two parts, it would take twice the instructions and the reads of h).  Against
-// 64 bits, y's error (norm) is then 1.8e-3 in BF16 for 1.65e-3 with FP32 h (one token, 8
-// of 64 experts of 1024 x 2048), 2.9e-4 in FP16 for 2.1e-4 (16 tokens, 8 of 14336 x 4096);
-// an FP16 h beyond 65504 is an infinity.
+// (kept in two parts, it would take twice the instructions and the reads of h).  This
+// rounding and y's own are as large, so y's error is up to sqrt 2 times that with FP32 h:
+// against 64 bits (norm) 1.8e-3 for 1.65e-3 in BF16 (one token, 8 of 64 experts of 1024 x
+// 2048), 2.9e-4 for 2.1e-4 in FP16 (16 tokens, 8 of 14336 x 4096).  An FP16 h beyond
+// 65504 is an infinity.
 // (A wave for each matrix: 16 waves hold one matrix's chunk and the next, and with
 // four waves a SIMD lookups, vector instructions and loads overlap; a wave for both
 // left room for 8 waves.)
